@@ -26,6 +26,7 @@ DLRM_FLAG_POOLED_F16 = 2
 DLRM_FLAG_GRAD_F16 = 4
 DLRM_F32 = 0
 DLRM_F16 = 1
+DLRM_BF16 = 2
 DLRM_FLAG_HASH_INDICES = 1
 DLRM_STATUS_OOB_INDEX = 1
 DLRM_STATUS_TIMEOUT = 2
@@ -91,6 +92,9 @@ def load(path: str | None = None) -> ctypes.CDLL:
     for f in ("dlrm_emb_fwd", "dlrm_interact_fwd", "dlrm_interact_fwd_cuda_core", "dlrm_emb_interact_fwd",
               "dlrm_emb_interact_fwd_train", "dlrm_emb_interact_bwd", "dlrm_interact_bwd", "dlrm_emb_bwd_sgd", "dlrm_emb_bwd_sgd_noalloc", "dlrm_synth_fill_uniform"):
         getattr(L, f).restype = _I
+    if hasattr(L, "dlrm_linear_fwd"):   # a library built before the dense network has none of it
+        from . import dense
+        dense.declare(L)
     if path is None:
         _lib = L
     return L
@@ -286,3 +290,20 @@ def dlrm_bottom_mlp_fwd(x, dims, weights, biases, out, workspace, status=None, s
                                     _ptr(biases), _ptr(out), _ptr(workspace), ws_bytes, _ptr(status),
                                     _stream(stream))
     _check("dlrm_bottom_mlp_fwd", rc)
+
+
+# ---------------------------------------------------------------- dense network
+_DENSE = frozenset((
+    "DLRM_ACT_NONE", "DLRM_ACT_RELU", "DLRM_ACT_GELU", "DLRM_ACT_SILU", "DLRM_MOE_MAX_TOKENS", "DLRM_MOE_MAX_EXPERTS",
+    "DLRM_MOE_MAX_TOP_K", "dlrm_dropout_fwd", "dlrm_dropout_bwd", "dlrm_linear_fwd", "dlrm_linear_fwd_workspace_size",
+    "dlrm_linear_bwd", "dlrm_linear_bwd_workspace_size", "dlrm_moe_fwd", "dlrm_moe_fwd_workspace_size"))
+
+
+def __getattr__(name):
+    """The names of ``dense.py``, imported (with torch) when the first of them is used."""
+    if name in _DENSE:
+        from . import dense
+        for n in _DENSE:
+            globals()[n] = getattr(dense, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

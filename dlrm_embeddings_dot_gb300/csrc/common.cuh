@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <cstdarg>
+#include <cstring>
 #include <type_traits>
 #include <utility>
 #include <cstdio>

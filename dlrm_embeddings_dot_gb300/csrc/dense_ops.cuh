@@ -1,0 +1,241 @@
+// dense_ops.cuh -- what the kernels of the dense network share: element types,
+// activations and their slopes, the counter-based generator, and access to
+// runs of eight columns of a row (the unit of the generator).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "dlrm_dense.h"
+
+namespace dlrm {
+
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v)
+{
+    if constexpr (std::is_same_v<T, float>) return v;
+    else if constexpr (std::is_same_v<T, __half>) return __float2half_rn(v);
+    else return __float2bfloat16_rn(v);
+}
+
+// Eight consecutive elements at a 16-byte aligned address.
+template <typename T>
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8])
+{
+    static_assert(sizeof(T) == 2);
+    if constexpr (std::is_same_v<T, __half>) {
+        h8_to_f8(v, f);
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8])
+{
+    static_assert(sizeof(T) == 2);
+    if constexpr (std::is_same_v<T, __half>) {
+        return f8_to_h8(f);
+    } else {
+        uint4 v;
+        __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        return v;
+    }
+}
+
+// Eight columns of a row as raw words, so that a load can be issued long before
+// its values are used: one 16-byte word for 2-byte types, two for fp32.
+template <typename T>
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+};
+
+// Columns [0, n) of the run at p (n <= 8; the others read as zero).  VEC: the
+// run is 16-byte aligned and has all eight columns.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw8<T> load8(const T* p, int n)
+{
+    Raw8<T> r;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = ldg_nc_v4(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = i < n ? __ldg(p + i) : from_f32<T>(0.f);
+        memcpy(&r, e, sizeof(r));
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&f)[8])
+{
+    if constexpr (std::is_same_v<T, float>) {
+        const float4 a = u4_as_f4(r.w[0]), b = u4_as_f4(r.w[1]);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+        unpack8<T>(r.w[0], f);
+    }
+}
+
+// Stores columns [0, n) of the run at p, rounding each once.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* p, int n, const float (&f)[8])
+{
+    if constexpr (VEC) {
+        if constexpr (std::is_same_v<T, float>) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            *reinterpret_cast<uint4*>(p) = pack8<T>(f);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = from_f32<T>(f[i]);
+    }
+}
+
+// -------------------------------------------------------------- activations
+// The functions of the header's definitions.  NaN passes through each (RELU
+// compares with z < 0, which is false for NaN).
+__device__ __forceinline__ float act_f(float z, int act)
+{
+    switch (act) {
+    case DLRM_ACT_RELU: return z < 0.f ? 0.f : z;
+    case DLRM_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678f));
+    case DLRM_ACT_SILU: return z / (1.f + expf(-z));
+    default: return z;
+    }
+}
+
+// a'(z)
+__device__ __forceinline__ float act_slope(float z, int act)
+{
+    switch (act) {
+    case DLRM_ACT_RELU: return z <= 0.f ? 0.f : 1.f;
+    case DLRM_ACT_GELU: return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z);
+    case DLRM_ACT_SILU: {
+        const float s = 1.f / (1.f + expf(-z));
+        return s * (1.f + z * (1.f - s));
+    }
+    default: return 1.f;
+    }
+}
+
+// ------------------------------------------------------------------ dropout
+// Philox4x32-10 (Salmon et al., SC 2011): ten rounds of two 32 x 32 -> 64 bit
+// products on a 128-bit counter, the key stepping by two Weyl constants.
+__device__ __forceinline__ uint4 philox4x32(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
+                                            uint32_t k1)
+{
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)b;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+
+// What a kernel needs to drop elements.  thr == 0: no dropout, rng unread.
+struct Drop {
+    const uint64_t* rng;
+    uint32_t thr;    // floor(65536 p + 0.5), below 65536
+    float scale;     // 65536 / (65536 - thr)
+};
+
+struct DropKey {
+    uint32_t k0, k1, o0, o1;
+};
+
+__device__ __forceinline__ DropKey drop_key(const Drop& d)
+{
+    DropKey k = {0, 0, 0, 0};
+    if (d.thr) {
+        const uint64_t a = __ldg(d.rng), b = __ldg(d.rng + 1);
+        k = {(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+    }
+    return k;
+}
+
+// Drops and scales the eight columns 8 * group .. 8 * group + 7 of a row.  A
+// number has 16 bits: one Philox call (about 60 instructions) serves eight
+// columns, where 32-bit numbers take two calls for them; the rate in force is
+// the multiple of 2^-16 nearest to p and the scale goes by it.
+__device__ __forceinline__ void drop8(float (&f)[8], const Drop& d, const DropKey& k, uint32_t row, uint32_t group)
+{
+    const uint4 u = philox4x32(group, row, k.o0, k.o1, k.k0, k.k1);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = (w[i] & 0xffffu) >= d.thr ? f[2 * i] * d.scale : 0.f;
+        f[2 * i + 1] = (w[i] >> 16) >= d.thr ? f[2 * i + 1] * d.scale : 0.f;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+inline bool dense_dtype_ok(dlrm_dtype dt) { return dt == DLRM_F32 || dt == DLRM_F16 || dt == DLRM_BF16; }
+inline int dense_dtype_size(dlrm_dtype dt) { return dt == DLRM_F32 ? 4 : 2; }
+
+// Whether a matrix's rows of `width` elements all start on 16-byte boundaries.
+inline bool rows_aligned16(const void* p, int64_t ld, int rows, int es)
+{
+    return aligned16(p) && (rows <= 1 || ld * es % 16 == 0);
+}
+
+// fn(T()) for the element type of dt.
+template <typename Fn>
+auto with_type(dlrm_dtype dt, Fn&& fn)
+{
+    if (dt == DLRM_F32) return fn(float());
+    if (dt == DLRM_F16) return fn(__half());
+    return fn(bf16());
+}
+
+// Checks p and rng; fills *d.
+inline dlrm_status make_drop(const char* fn, double p, const uint64_t* rng, Drop* d)
+{
+    if (!(p >= 0.0 && p * 65536.0 < 65535.5))
+        return fail(DLRM_ERR_INVALID_ARG, "%s: p must be in [0, 1) with 65536 p below 65535.5 (got %g)", fn, p);
+    d->thr = (uint32_t)(p * 65536.0 + 0.5);
+    d->scale = (float)(65536.0 / (65536.0 - d->thr));
+    d->rng = rng;
+    if (p > 0.0 && !rng) return fail(DLRM_ERR_INVALID_ARG, "%s: p > 0 needs d_rng", fn);
+    if (p > 0.0 && (reinterpret_cast<uintptr_t>(rng) & 7u))
+        return fail(DLRM_ERR_INVALID_ARG, "%s: d_rng must be 8-byte aligned", fn);
+    return DLRM_OK;
+}
+
+// Checks one matrix argument of a call (rows > 0).
+inline dlrm_status check_matrix(const char* fn, const char* name, const void* p, int64_t ld, int rows, int cols, int es)
+{
+    if (!p) return fail(DLRM_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+    if (reinterpret_cast<uintptr_t>(p) % es)
+        return fail(DLRM_ERR_INVALID_ARG, "%s: %s is not aligned to its element size", fn, name);
+    if (rows > 1 && (ld < cols || ld > (INT64_C(1) << 40)))
+        return fail(DLRM_ERR_INVALID_ARG, "%s: row distance of %s (%lld) must be in [%d, 2^40]", fn, name,
+                    (long long)ld, cols);
+    return DLRM_OK;
+}
+
+}  // namespace dlrm

@@ -56,7 +56,11 @@ typedef enum {
     DLRM_ERR_NO_FIT = 5         /* table placement: a table does not fit on its GPU */
 } dlrm_status;
 
-typedef enum { DLRM_F32 = 0, DLRM_F16 = 1 } dlrm_dtype;
+typedef enum {
+    DLRM_F32 = 0,
+    DLRM_F16 = 1,
+    DLRM_BF16 = 2   /* the dense network of dlrm_dense.h only */
+} dlrm_dtype;
 
 /* flags */
 #define DLRM_FLAG_HASH_INDICES 1u  /* fold every index into its table: idx := ((idx % N_t) + N_t) % N_t
