@@ -111,6 +111,20 @@ __device__ __forceinline__ void store8(T* p, int n, const float (&f)[8])
     }
 }
 
+// Three bf16 parts of a float: hi and mid as the upper halves of words, lo as a
+// float that has at most eight bits left.  hi and mid are cut, not rounded, so
+// none overflows, and lo holds the rest exactly.  An infinity or NaN goes whole
+// into lo, which meets only the other side's hi: no 0 * inf turns an infinity
+// into a NaN.
+__device__ __forceinline__ void split1(float v, uint32_t& hi, uint32_t& mid, float& lo)
+{
+    const bool wild = (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u;
+    hi = wild ? 0u : __float_as_uint(v) & 0xffff0000u;
+    const float r = v - __uint_as_float(hi);
+    mid = wild ? 0u : __float_as_uint(r) & 0xffff0000u;
+    lo = r - __uint_as_float(mid);
+}
+
 // -------------------------------------------------------------- activations
 // The functions of the header's definitions.  NaN passes through each (RELU
 // compares with z < 0, which is false for NaN).

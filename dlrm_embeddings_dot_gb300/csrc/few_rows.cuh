@@ -57,22 +57,10 @@ __device__ __forceinline__ uint4 load_lane(const T* p, int n)
     return v;
 }
 
-// Three bf16 parts of each of four floats, two values to a word.  The first two
-// parts are cut, not rounded (so none overflows), and the third holds the rest
-// exactly.  An infinity or NaN goes whole into the third part, which meets only
-// the other side's first one: no 0 * inf turns an infinity into a NaN.
+// Three bf16 parts of each of four floats (split1), two values to a word.
 struct Parts {
     uint32_t hi[2], mid[2], lo[2];
 };
-
-__device__ __forceinline__ void split1(float v, uint32_t& hi, uint32_t& mid, float& lo)
-{
-    const bool wild = (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u;
-    hi = wild ? 0u : __float_as_uint(v) & 0xffff0000u;
-    const float r = v - __uint_as_float(hi);
-    mid = wild ? 0u : __float_as_uint(r) & 0xffff0000u;
-    lo = r - __uint_as_float(mid);
-}
 
 __device__ __forceinline__ Parts split4(uint4 v)
 {
@@ -112,10 +100,11 @@ __device__ __forceinline__ void mac(float (&acc)[4], uint4 a, uint4 b, uint4 x)
 
 // acc[i][j] += tile i of 16 weight rows times tile j of 8 tokens over [k0, k1) of K
 // (k0 a multiple of kStep).  w[i][0] / w[i][1]: rows g and g + 8 of tile i;
-// x[j]: token g of tile j; NULL reads as zeros.
-template <typename T, int WT, int NT, bool VEC>
+// x[j]: token g of tile j; NULL reads as zeros.  XP: terms each token is the
+// sum of, term i at x[j] + i * xplane.
+template <typename T, int WT, int NT, bool VEC, int XP = 1>
 __device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* const (&w)[WT][2], const T* const (&x)[NT],
-                                         int k0, int k1)
+                                         int k0, int k1, int64_t xplane = 0)
 {
     constexpr int U = WT == 1 ? 4 : 2;   // steps whose weight loads are in flight together
     const int t = (threadIdx.x % kWarp) % 4;
@@ -134,11 +123,13 @@ __device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* const
         for (int u = 0; u < U; ++u) {
             const int at = k + u * kStep<T> + t * kLane<T>, n = k1 - at;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const uint4 b = x[j] && n > 0 ? load_lane<T, VEC, true>(x[j] + at, n) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int i = 0; i < WT; ++i) mac<T>(acc[i][j], a[u][i][0], a[u][i][1], b);
-            }
+                for (int q = 0; q < XP; ++q) {
+                    const uint4 b = x[j] && n > 0 ? load_lane<T, VEC, true>(x[j] + q * xplane + at, n) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < WT; ++i) mac<T>(acc[i][j], a[u][i][0], a[u][i][1], b);
+                }
         }
     }
 }

@@ -1,123 +1,283 @@
-// linear.cu -- the dense layer and its gradient: argument checks, workspaces
-// and the launches.
+// linear.cu -- the dense layer and its gradient: argument checks, workspaces,
+// and the kernels around the products.
 //
 //   forward   z = x W^T + b;  y = residual + drop(a(z))
 //   backward  dZ = a'(z) drop(dY);  dX = dZ W;  dW = dZ^T x;  db = sum dZ
-#include "dense_ops.cuh"
+//
+// Up to kFewRows rows the forward streams the weights into matrix fragments
+// (linear_few_kernel); the other products run on tcgen05 (gemm_tc.cuh), which
+// wants 2-byte operands with rows on the 16-byte grid.  pack_kernel lays out
+// again what is not like that: misaligned rows, and fp32 as three bf16 planes.
+#include "few_rows.cuh"
+#include "gemm_tc.cuh"
 
 namespace dlrm {
 namespace {
 
-// What follows a product: bias, activation, dropout and residual, with the
-// pre-activation kept where it is asked for.
-struct Epilogue {
-    const float* bias;
-    const void* res;
-    int64_t ldr;
-    void* pre;
-    int64_t ldp;
-    int act;
-    Drop drop;
+using gemm::Operand;
+using gemm::padded;
+using gemm::Shape;
+
+constexpr int kFewRows = few::kMaxTokens;
+
+// ------------------------------------------------------------------ packing
+// Stores eight columns as a 2-byte operand; fp32 as three planes.
+template <typename T>
+__device__ __forceinline__ void store_operand8(void* dst, int64_t at, int64_t plane, const float (&f)[8])
+{
+    if constexpr (std::is_same_v<T, float>) {
+        uint32_t hi[8], mid[8];
+        float lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split1(f[i], hi[i], mid[i], lo[i]);
+        uint4 h, m;
+        uint32_t *hw = &h.x, *mw = &m.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            hw[i] = __byte_perm(hi[2 * i], hi[2 * i + 1], 0x7632);
+            mw[i] = __byte_perm(mid[2 * i], mid[2 * i + 1], 0x7632);
+        }
+        bf16* p = (bf16*)dst + at;
+        *reinterpret_cast<uint4*>(p) = h;
+        *reinterpret_cast<uint4*>(p + plane) = m;
+        *reinterpret_cast<uint4*>(p + 2 * plane) = pack8<bf16>(lo);
+    } else {
+        *reinterpret_cast<uint4*>((T*)dst + at) = pack8<T>(f);
+    }
+}
+
+struct PackJob {
+    const void* src;
+    int64_t ld;
+    int rows, cols, vec;
+    void* dst;          // [planes][rows][padded(cols)]
 };
 
-constexpr int kTile = 64, kStepK = 16;
-
-// C[m][n] = sum_k A[m * sam + k * sak] * B[n * sbn + k * sbk], then the epilogue.
+// Up to two matrices laid out as operands, runs of eight columns a thread.
 template <typename T>
-__global__ void __launch_bounds__(256)
-product_kernel(const T* __restrict__ A, int64_t sam, int64_t sak, const T* __restrict__ B, int64_t sbn, int64_t sbk,
-               int M, int N, int K, Epilogue e, T* __restrict__ C, int64_t ldc)
+__global__ void __launch_bounds__(256) pack_kernel(PackJob j0, PackJob j1)
 {
     pdl_wait();
-    __shared__ float as[kStepK][kTile + 1], bs[kStepK][kTile + 1];
-    const int n_tiles = (N + kTile - 1) / kTile;
-    const int m0 = blockIdx.x / n_tiles * kTile, n0 = blockIdx.x % n_tiles * kTile;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += kStepK) {
-        for (int i = threadIdx.x; i < kTile * kStepK; i += 256) {
-            const int k = sak == 1 ? i % kStepK : i / kTile, r = sak == 1 ? i / kStepK : i % kTile;
-            as[k][r] = m0 + r < M && k0 + k < K ? to_f32(A[(m0 + r) * sam + (k0 + k) * sak]) : 0.f;
-        }
-        for (int i = threadIdx.x; i < kTile * kStepK; i += 256) {
-            const int k = sbk == 1 ? i % kStepK : i / kTile, r = sbk == 1 ? i / kStepK : i % kTile;
-            bs[k][r] = n0 + r < N && k0 + k < K ? to_f32(B[(n0 + r) * sbn + (k0 + k) * sbk]) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kStepK; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][ty * 4 + i], bs[k][tx * 4 + j], acc[i][j]);
-        __syncthreads();
+    const int64_t n0 = (int64_t)j0.rows * ((j0.cols + 7) / 8), n1 = (int64_t)j1.rows * ((j1.cols + 7) / 8);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n0 + n1; i += (int64_t)gridDim.x * 256) {
+        const PackJob& j = i < n0 ? j0 : j1;
+        const int64_t k = i < n0 ? i : i - n0;
+        const int groups = (j.cols + 7) / 8;
+        const int64_t row = k / groups;
+        const int col = (int)(k - row * groups) * 8, n = j.cols - col;
+        const T* p = (const T*)j.src + row * j.ld + col;
+        float f[8];
+        if (j.vec && n >= 8) widen8<T>(load8<T, true>(p, 8), f);
+        else widen8<T>(load8<T, false>(p, n), f);
+        store_operand8<T>(j.dst, k * 8, j.rows * (int64_t)groups * 8, f);
     }
+}
+
+template <typename T>
+dlrm_status launch_pack(const PackJob& a, const PackJob& b, cudaStream_t st)
+{
+    const int64_t runs = (int64_t)a.rows * ((a.cols + 7) / 8) + (int64_t)b.rows * ((b.cols + 7) / 8);
+    if (runs == 0) return DLRM_OK;
+    const int64_t want = (runs + 255) / 256, most = (int64_t)num_sms() * 8;
+    return check_launch_pdl(launch_pdl(pack_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, a, b),
+                            "pack_kernel");
+}
+
+// A matrix argument as an operand: itself, or its copy at ws.
+template <typename T>
+Operand operand(const void* p, int64_t ld, int rows, int cols, void* ws, bool mn)
+{
+    if (!ws) return {p, ld, 0, 1, mn};
+    return {ws, padded(cols), rows * padded(cols), std::is_same_v<T, float> ? 3 : 1, mn};
+}
+
+bool needs_pack(const void* p, int64_t ld, int rows, dlrm_dtype dt)
+{
+    return dt == DLRM_F32 || !rows_aligned16(p, ld, rows, 2);
+}
+
+size_t operand_bytes(int rows, int cols, dlrm_dtype dt)
+{
+    return dlrm_ws_align((size_t)(dt == DLRM_F32 ? 3 : 1) * rows * padded(cols) * 2);
+}
+
+// --------------------------------------------------------------- few rows
+// The forward of up to 64 rows: a cluster owns 16 output columns (weight rows),
+// its warps share out K, and their partial tiles are added in a fixed order.
+template <typename T, int NT, bool VEC>
+__global__ void __launch_bounds__(256, 2)
+linear_few_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ w, int64_t ldw, int M, int N, int K,
+                  const __grid_constant__ Epilogue e)
+{
+    using namespace few;
+    pdl_wait();
+    constexpr int kWarps = 8;
+    __shared__ __align__(16) float red[kWarps * NT * 8 * kPitch];
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4;
+    const int S = (int)cluster_size(), rank = (int)cluster_rank();
+    const int row0 = (int)(blockIdx.x / S) * kRows;
+    const int steps = (K + kStep<T> - 1) / kStep<T>, parts = S * kWarps, part = rank * kWarps + warp;
+    const int per = (steps + parts - 1) / parts * kStep<T>;
+    {
+        const T* wp[1][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) wp[0][b] = row0 + g + 8 * b < N ? w + (row0 + g + 8 * b) * ldw : nullptr;
+        const T* xp[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) xp[j] = j * 8 + g < M ? x + (j * 8 + g) * ldx : nullptr;
+        float acc[1][NT][4] = {};
+        rows_mac<T, 1, NT, VEC>(acc, wp, xp, part * per, min(K, (part + 1) * per));
+        put_partial(red + warp * NT * 8 * kPitch, acc[0]);
+    }
+    __syncthreads();
+    constexpr int kMine = (NT * 8 * kRows + 255) / 256;
+    float sum[kMine];
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+        const int i = threadIdx.x + m * 256;
+        sum[m] = 0.f;
+        if (i < NT * 8 * kRows)
+#pragma unroll
+            for (int q = 0; q < kWarps; ++q) sum[m] += red[(q * NT * 8 + i / kRows) * kPitch + i % kRows];
+    }
+    __syncthreads();
+    float* tot = red;    // [token][kRows], over the partial tiles
+#pragma unroll
+    for (int m = 0; m < kMine; ++m)
+        if (threadIdx.x + m * 256 < NT * 8 * kRows) tot[threadIdx.x + m * 256] = sum[m];
+    if (S > 1) cluster_sync();
+    else __syncthreads();
     const DropKey key = drop_key(e.drop);
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= M || n >= N) continue;
-            const float z = acc[i][j] + (e.bias ? e.bias[n] : 0.f);
-            if (e.pre) ((T*)e.pre)[m * e.ldp + n] = from_f32<T>(z);
-            float f[8] = {};
-            f[n & 7] = act_f(z, e.act);
-            if (e.drop.thr) drop8(f, e.drop, key, (uint32_t)m, (uint32_t)n >> 3);
-            const float y = f[n & 7] + (e.res ? to_f32(((const T*)e.res)[m * e.ldr + n]) : 0.f);
-            C[m * ldc + n] = from_f32<T>(y);
+    for (int i = threadIdx.x * S + rank; i < M * (kRows / 8); i += 256 * S) {
+        const int t = i / 2, col = row0 + i % 2 * 8, n = N - col;
+        if (n <= 0) continue;
+        float f[8] = {}, b[8];
+        for (int q = 0; q < S; ++q) {
+            const uint32_t at = cluster_map(tot + t * kRows + i % 2 * 8, q);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) f[c] += cluster_ld(at + 4 * c);
         }
+        bias8(e.bias, col, N, b);
+        finish8_any<T>(e, key, t, col, n, f, b);
+    }
+    if (S > 1) cluster_sync();   // no block leaves while another reads its sums
 }
 
-// dZ = a'(pre) drop(dY) for a chunk of rows, and that chunk's column sums.
+template <typename T>
+dlrm_status launch_few(const void* x, int64_t ldx, const void* w, int64_t ldw, int M, int N, int K, const Epilogue& e,
+                       cudaStream_t st)
+{
+    const int row_tiles = (N + few::kRows - 1) / few::kRows, steps = (K + few::kStep<T> - 1) / few::kStep<T>;
+    // a cluster splits K further while blocks are few and every warp keeps four steps
+    int S = 1;
+    while (S < 8 && row_tiles * S < num_sms() && steps >= S * 8 * 8) S *= 2;
+    const bool vec = rows_aligned16(x, ldx, M, sizeof(T)) && rows_aligned16(w, ldw, N, sizeof(T));
+    auto go = [&](auto n) {
+        constexpr int NT = decltype(n)::value;
+        auto kern = vec ? linear_few_kernel<T, NT, true> : linear_few_kernel<T, NT, false>;
+        return check_launch_pdl(few::launch_cluster(kern, dim3((unsigned)row_tiles * S), dim3(256), 0, st, S,
+                                                    (const T*)x, ldx, (const T*)w, ldw, M, N, K, e),
+                                "linear_few_kernel");
+    };
+    if (M <= 8) return go(std::integral_constant<int, 1>{});
+    if (M <= 16) return go(std::integral_constant<int, 2>{});
+    if (M <= 32) return go(std::integral_constant<int, 4>{});
+    return go(std::integral_constant<int, 8>{});
+}
+
+// ------------------------------------------------------- gradient of z and b
+// dZ = a'(pre) drop(dY) as an operand of the products (dz, may be NULL), and
+// column sums of it (partial [gridDim.y][N], may be NULL).  A block covers
+// cg * 8 columns and `rows` rows: a thread owns eight columns of every
+// (256 / cg)-th row and adds them up in registers, then the block adds its
+// threads' sums in shared memory.
 template <typename T>
 __global__ void __launch_bounds__(256)
-grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, int64_t ldp, int act, Drop drop, int M,
-              int N, int rows, T* __restrict__ dz, float* __restrict__ partial)
+grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, int64_t ldp, int act, int vec,
+              Drop drop, int M, int N, int cg, int rows, void* __restrict__ dz, float* __restrict__ partial)
 {
     pdl_wait();
+    __shared__ float red[256][8 + 1];
     const DropKey key = drop_key(drop);
-    const int g = blockIdx.x * 256 + threadIdx.x, col = g * 8, n = N - col;
-    if (n <= 0) return;
+    const int tx = threadIdx.x % cg, ty = threadIdx.x / cg, step = 256 / cg;
+    const int g = blockIdx.x * cg + tx, col = g * 8, n = N - col;
+    const int64_t Np = padded(N);
     float sum[8] = {};
-    const int r0 = blockIdx.y * rows, r1 = min(M, r0 + rows);
-    for (int r = r0; r < r1; ++r) {
-        float f[8], z[8];
-        widen8<T>(load8<T, false>(dy + r * ldg + col, n), f);
-        if (drop.thr) drop8(f, drop, key, (uint32_t)r, (uint32_t)g);
-        if (act != DLRM_ACT_NONE) {
-            widen8<T>(load8<T, false>(pre + r * ldp + col, n), z);
-            for (int j = 0; j < 8; ++j) f[j] *= act_slope(z[j], act);
+    if (n > 0) {
+        const int r0 = blockIdx.y * rows, r1 = min(M, r0 + rows);
+        const bool v = vec && n >= 8;
+#pragma unroll 2
+        for (int r = r0 + ty; r < r1; r += step) {
+            const T* gp = dy + r * ldg + col;
+            const T* pp = pre + r * ldp + col;
+            const Raw8<T> a = v ? load8<T, true>(gp, 8) : load8<T, false>(gp, n);
+            float f[8];
+            widen8<T>(a, f);
+            if (act != DLRM_ACT_NONE) {
+                const Raw8<T> b = v ? load8<T, true>(pp, 8) : load8<T, false>(pp, n);
+                float z[8];
+                widen8<T>(b, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] *= act_slope(z[i], act);
+            }
+            if (drop.thr) drop8(f, drop, key, (uint32_t)r, (uint32_t)g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += f[i];
+            if (dz) store_operand8<T>(dz, r * Np + col, M * Np, f);
         }
-        for (int j = 0; j < 8; ++j) sum[j] += f[j];
-        store8<T, false>(dz + (int64_t)r * N + col, n, f);
     }
-    if (partial)
-        for (int j = 0; j < 8; ++j)
-            if (j < n) partial[(int64_t)blockIdx.y * N + col + j] = sum[j];
+    if (!partial) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[threadIdx.x][i] = sum[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < cg * 8; i += 256) {
+        float s = 0.f;
+        for (int y = 0; y < step; ++y) s += red[y * cg + i / 8][i % 8];
+        const int c = blockIdx.x * cg * 8 + i;
+        if (c < N) partial[(int64_t)blockIdx.y * N + c] = s;
+    }
 }
 
-__global__ void sum_rows_kernel(const float* __restrict__ partial, int rows, int N, float* __restrict__ out)
+struct GradZ {
+    int cg, blocks_x, chunks, rows;
+};
+
+GradZ grad_z_shape(int M, int N)
+{
+    const int groups = (N + 7) / 8;
+    GradZ s = {1, 0, 0, 0};
+    while (s.cg < 32 && s.cg < groups) s.cg *= 2;
+    s.blocks_x = (groups + s.cg - 1) / s.cg;
+    const int step = 256 / s.cg;
+    int64_t chunks = (int64_t)num_sms() * 8 / s.blocks_x, most = ((int64_t)M + 4 * step - 1) / (4 * step);
+    if (chunks > most) chunks = most;
+    if (chunks < 1) chunks = 1;
+    s.rows = (int)((M + chunks - 1) / chunks);
+    s.chunks = (M + s.rows - 1) / s.rows;
+    return s;
+}
+
+// out[n] = the sum of partial's rows: 32 columns a block, 16 threads a column.
+__global__ void __launch_bounds__(512)
+sum_rows_kernel(const float* __restrict__ partial, int rows, int N, float* __restrict__ out)
 {
     pdl_wait();
-    const int n = blockIdx.x * blockDim.x + threadIdx.x;
-    if (n >= N) return;
+    __shared__ float red[16][33];
+    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, n = blockIdx.x * 32 + tx;
     float s = 0.f;
-    for (int r = 0; r < rows; ++r) s += partial[(int64_t)r * N + n];
-    out[n] = s;
+    if (n < N)
+#pragma unroll 4
+        for (int r = ty; r < rows; r += 16) s += partial[(int64_t)r * N + n];
+    red[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && n < N) {
+#pragma unroll
+        for (int y = 1; y < 16; ++y) s += red[y][tx];
+        out[n] = s;
+    }
 }
 
-template <typename T>
-dlrm_status launch_product(const T* A, int64_t sam, int64_t sak, const T* B, int64_t sbn, int64_t sbk, int M, int N,
-                           int K, const Epilogue& e, T* C, int64_t ldc, cudaStream_t st)
-{
-    const int64_t tiles = (int64_t)((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-    if (tiles > INT32_MAX) return fail(DLRM_ERR_UNSUPPORTED, "dense layer: %lld output tiles", (long long)tiles);
-    return check_launch_pdl(launch_pdl(product_kernel<T>, dim3((unsigned)tiles), dim3(256), 0, st, A, sam, sak, B, sbn,
-                                       sbk, M, N, K, e, C, ldc),
-                            "product_kernel");
-}
-
-constexpr int kChunkRows = 64;
-
+// ------------------------------------------------------------------- checks
 dlrm_status check_sizes(const char* fn, dlrm_dtype dtype, int M, int N, int K, dlrm_act act)
 {
     if (!dense_dtype_ok(dtype)) return fail(DLRM_ERR_INVALID_ARG, "%s: bad dtype", fn);
@@ -135,6 +295,43 @@ dlrm_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t
     return DLRM_OK;
 }
 
+bool sizes_ok(dlrm_dtype dtype, int M, int N, int K) { return dense_dtype_ok(dtype) && M >= 1 && N >= 1 && K >= 1; }
+
+// The workspaces' pieces, one after another.
+struct FwdLayout {
+    size_t x, w, partial, total;   // x, w: bytes of the operands' copies (0: used as they are)
+};
+
+FwdLayout fwd_layout(const void* x, int64_t ldx, const void* w, int64_t ldw, dlrm_dtype dt, int M, int N, int K)
+{
+    FwdLayout l = {};
+    if (M <= kFewRows) return l;
+    l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, dt) : 0;
+    l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
+    l.partial = gemm::partial_bytes({M, N, K, dt == DLRM_F32 ? 6 : 1});
+    l.total = l.x + l.w + l.partial;
+    return l;
+}
+
+struct BwdLayout {
+    size_t dz, x, w, sums, partial, total;
+};
+
+BwdLayout bwd_layout(const void* dy, int64_t ldg, const void* x, int64_t ldx, const void* w, int64_t ldw, dlrm_dtype dt,
+                     int M, int N, int K, dlrm_act act, double p)
+{
+    BwdLayout l = {};
+    const int pairs = dt == DLRM_F32 ? 6 : 1;
+    l.dz = act != DLRM_ACT_NONE || p > 0 || needs_pack(dy, ldg, M, dt) ? operand_bytes(M, N, dt) : 0;
+    l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, dt) : 0;
+    l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
+    l.sums = dlrm_ws_align((size_t)grad_z_shape(M, N).chunks * N * 4);
+    const size_t a = gemm::partial_bytes({M, K, N, pairs}), b = gemm::partial_bytes({N, K, M, pairs});
+    l.partial = a > b ? a : b;
+    l.total = l.dz + l.x + l.w + l.sums + l.partial;
+    return l;
+}
+
 }  // namespace
 }  // namespace dlrm
 
@@ -143,7 +340,7 @@ using namespace dlrm;
 extern "C" size_t dlrm_linear_fwd_workspace_size(const void* d_x, int64_t ldx, const void* d_w, int64_t ldw,
                                                  dlrm_dtype dtype, int M, int N, int K)
 {
-    return 0;
+    return sizes_ok(dtype, M, N, K) ? fwd_layout(d_x, ldx, d_w, ldw, dtype, M, N, K).total : 0;
 }
 
 extern "C" dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void* d_w, int64_t ldw, const float* d_bias,
@@ -157,7 +354,7 @@ extern "C" dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void*
     const char* fn = "dlrm_linear_fwd";
     dlrm_status s = check_sizes(fn, dtype, M, N, K, act);
     if (s != DLRM_OK) return s;
-    Epilogue e = {d_bias, d_residual, ldr, d_pre, ldp, act, {}};
+    Epilogue e = {d_bias, d_residual, ldr, d_pre, ldp, d_y, ldy, act, 0, {}};
     if ((s = make_drop(fn, p, d_rng, &e.drop)) != DLRM_OK) return s;
     if (M == 0) return DLRM_OK;
     const int es = dense_dtype_size(dtype);
@@ -167,13 +364,24 @@ extern "C" dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void*
     if (d_residual && (s = check_matrix(fn, "d_residual", d_residual, ldr, M, N, es)) != DLRM_OK) return s;
     if (d_pre && (s = check_matrix(fn, "d_pre", d_pre, ldp, M, N, es)) != DLRM_OK) return s;
     if ((s = check_matrix(fn, "d_y", d_y, ldy, M, N, es)) != DLRM_OK) return s;
-    s = check_workspace(fn, d_workspace, workspace_bytes,
-                        dlrm_linear_fwd_workspace_size(d_x, ldx, d_w, ldw, dtype, M, N, K));
-    if (s != DLRM_OK) return s;
-    return with_type(dtype, [&](auto t) {
+    const FwdLayout l = fwd_layout(d_x, ldx, d_w, ldw, dtype, M, N, K);
+    if ((s = check_workspace(fn, d_workspace, workspace_bytes, l.total)) != DLRM_OK) return s;
+    e.vec = epilogue_vec(e, M, es);
+    const cudaStream_t st = as_stream(stream);
+    return with_type(dtype, [&](auto t) -> dlrm_status {
         using T = decltype(t);
-        return launch_product<T>((const T*)d_x, ldx, 1, (const T*)d_w, ldw, 1, M, N, K, e, (T*)d_y, ldy,
-                                 as_stream(stream));
+        if (M <= kFewRows) return launch_few<T>(d_x, ldx, d_w, ldw, M, N, K, e, st);
+        uint8_t* ws = (uint8_t*)d_workspace;
+        void *xs = l.x ? ws : nullptr, *wsp = l.w ? ws + l.x : nullptr;
+        float* partial = (float*)(ws + l.x + l.w);
+        PackJob jx = {}, jw = {};
+        if (xs) jx = {d_x, ldx, M, K, rows_aligned16(d_x, ldx, M, es), xs};
+        if (wsp) jw = {d_w, ldw, N, K, rows_aligned16(d_w, ldw, N, es), wsp};
+        const dlrm_status r = launch_pack<T>(jx, jw, st);
+        if (r != DLRM_OK) return r;
+        return gemm::run<T, false, false>(fn, {M, N, K, dtype == DLRM_F32 ? 6 : 1}, operand<T>(d_x, ldx, M, K, xs, false),
+                                          operand<T>(d_w, ldw, N, K, wsp, false), dtype != DLRM_F16, e, partial,
+                                          d_status, st);
     });
 }
 
@@ -181,9 +389,8 @@ extern "C" size_t dlrm_linear_bwd_workspace_size(const void* d_grad_y, int64_t l
                                                  const void* d_w, int64_t ldw, dlrm_dtype dtype, int M, int N, int K,
                                                  dlrm_act act, double p)
 {
-    if (check_sizes("", dtype, M, N, K, act) != DLRM_OK || M == 0) return 0;
-    return dlrm_ws_align((size_t)M * N * dense_dtype_size(dtype)) +
-           dlrm_ws_align((size_t)((M + kChunkRows - 1) / kChunkRows) * N * 4);
+    if (!sizes_ok(dtype, M, N, K)) return 0;
+    return bwd_layout(d_grad_y, ldg, d_x, ldx, d_w, ldw, dtype, M, N, K, act, p).total;
 }
 
 extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const void* d_x, int64_t ldx,
@@ -216,27 +423,51 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
     if (d_grad_w && (s = check_matrix(fn, "d_x", d_x, ldx, M, K, es)) != DLRM_OK) return s;
     if (d_grad_x && (s = check_matrix(fn, "d_w", d_w, ldw, N, K, es)) != DLRM_OK) return s;
     if (d_grad_x && (s = check_matrix(fn, "d_grad_x", d_grad_x, lddx, M, K, es)) != DLRM_OK) return s;
-    s = check_workspace(fn, d_workspace, workspace_bytes,
-                        dlrm_linear_bwd_workspace_size(d_grad_y, ldg, d_x, ldx, d_w, ldw, dtype, M, N, K, act, p));
-    if (s != DLRM_OK) return s;
-    const int chunks = (M + kChunkRows - 1) / kChunkRows;
+    const BwdLayout l = bwd_layout(d_grad_y, ldg, d_x, ldx, d_w, ldw, dtype, M, N, K, act, p);
+    if ((s = check_workspace(fn, d_workspace, workspace_bytes, l.total)) != DLRM_OK) return s;
     return with_type(dtype, [&](auto t) -> dlrm_status {
         using T = decltype(t);
-        T* dz = (T*)d_workspace;
-        float* partial = (float*)((uint8_t*)d_workspace + dlrm_ws_align((size_t)M * N * sizeof(T)));
-        dlrm_status r = check_launch_pdl(
-            launch_pdl(grad_z_kernel<T>, dim3(((N + 7) / 8 + 255) / 256, chunks), dim3(256), 0, st, (const T*)d_grad_y,
-                       ldg, (const T*)d_pre, ldp, (int)act, drop, M, N, kChunkRows, dz, d_grad_bias ? partial : nullptr),
-            "grad_z_kernel");
-        if (r == DLRM_OK && d_grad_bias)
-            r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 255) / 256), dim3(256), 0, st, partial, chunks, N,
-                                            d_grad_bias),
-                                 "sum_rows_kernel");
-        const Epilogue none = {};
-        if (r == DLRM_OK && d_grad_x)
-            r = launch_product<T>(dz, N, 1, (const T*)d_w, 1, ldw, M, K, N, none, (T*)d_grad_x, lddx, st);
-        if (r == DLRM_OK && d_grad_w)
-            r = launch_product<T>(dz, 1, N, (const T*)d_x, 1, ldx, N, K, M, none, (T*)d_grad_w, lddw, st);
+        const int pairs = dtype == DLRM_F32 ? 6 : 1;
+        const bool bf = dtype != DLRM_F16;
+        uint8_t* ws = (uint8_t*)d_workspace;
+        void *dz = l.dz ? ws : nullptr, *xs = l.x ? ws + l.dz : nullptr, *wsp = l.w ? ws + l.dz + l.x : nullptr;
+        float* sums = (float*)(ws + l.dz + l.x + l.w);
+        float* partial = (float*)(ws + l.dz + l.x + l.w + l.sums);
+        const bool products = d_grad_x || d_grad_w;
+        dlrm_status r = DLRM_OK;
+        if ((dz && products) || d_grad_bias) {
+            const GradZ g = grad_z_shape(M, N);
+            const int vec = rows_aligned16(d_grad_y, ldg, M, es) && (act == DLRM_ACT_NONE || rows_aligned16(d_pre, ldp, M, es));
+            r = check_launch_pdl(launch_pdl(grad_z_kernel<T>, dim3(g.blocks_x, g.chunks), dim3(256), 0, st,
+                                            (const T*)d_grad_y, ldg, (const T*)d_pre, ldp, (int)act, vec, drop, M, N,
+                                            g.cg, g.rows, products ? dz : nullptr, d_grad_bias ? sums : nullptr),
+                                 "grad_z_kernel");
+            if (r == DLRM_OK && d_grad_bias)
+                r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 31) / 32), dim3(512), 0, st,
+                                                (const float*)sums, g.chunks, N, d_grad_bias),
+                                     "sum_rows_kernel");
+        }
+        if (r == DLRM_OK) {
+            PackJob jx = {}, jw = {};
+            if (xs && d_grad_w) jx = {d_x, ldx, M, K, rows_aligned16(d_x, ldx, M, es), xs};
+            if (wsp && d_grad_x) jw = {d_w, ldw, N, K, rows_aligned16(d_w, ldw, N, es), wsp};
+            r = launch_pack<T>(jx, jw, st);
+        }
+        Epilogue e = {};
+        if (r == DLRM_OK && d_grad_x) {
+            e.out = d_grad_x;
+            e.ldo = lddx;
+            e.vec = epilogue_vec(e, M, es);
+            r = gemm::run<T, false, true>(fn, {M, K, N, pairs}, operand<T>(d_grad_y, ldg, M, N, dz, false),
+                                          operand<T>(d_w, ldw, N, K, wsp, true), bf, e, partial, d_status, st);
+        }
+        if (r == DLRM_OK && d_grad_w) {
+            e.out = d_grad_w;
+            e.ldo = lddw;
+            e.vec = epilogue_vec(e, N, es);
+            r = gemm::run<T, true, true>(fn, {N, K, M, pairs}, operand<T>(d_grad_y, ldg, M, N, dz, true),
+                                         operand<T>(d_x, ldx, M, K, xs, true), bf, e, partial, d_status, st);
+        }
         return r;
     });
 }

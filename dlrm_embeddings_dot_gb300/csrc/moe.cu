@@ -38,8 +38,15 @@ struct MoeArgs {
     void* y;
     int32_t* ids;
     float* probs;
-    void* h;                                // [T][k][I]
+    void* h;                                // [kTerms][T][k][I]
 };
+
+// probs * h enters the second product as the sum of two values of a 2-byte type
+// (the rounded value and the rounded rest): the product of the weights with a
+// second fragment is free beside the weights' traffic, and y then has one
+// rounding, its own.
+template <typename T>
+constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
 
 // Which tokens chose which expert, in shared memory.
 struct Lists {
@@ -254,8 +261,16 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeArgs a)
             const int slot = entry[tok];
             float v = act_f(z, a.act);
             if (a.gated) v *= up;
-            if (row0 + r < a.I)
-                h[((int64_t)(slot / kMaxK) * a.k + slot % kMaxK) * a.I + row0 + r] = from_f32<T>(v * probs_s[slot]);
+            if (row0 + r < a.I) {
+                T* dst = h + ((int64_t)(slot / kMaxK) * a.k + slot % kMaxK) * a.I + row0 + r;
+                v *= probs_s[slot];
+                const T top = from_f32<T>(v);
+                *dst = top;
+                if constexpr (kTerms<T> == 2) {
+                    const float rest = v - to_f32(top);   // NaN for an infinite v: its rest is zero
+                    dst[(int64_t)a.T * a.k * a.I] = from_f32<T>(fabsf(to_f32(top)) <= 3.4e38f ? rest : 0.f);
+                }
+            }
         }
         group_sync(1 + mine, G * kWarp);
     }
@@ -296,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(MoeArgs a)
             }
         }
         float item[1][NT][4] = {};
-        rows_mac<T, 1, NT, VEC>(item, w, hp, k0, min(a.I, k0 + a.chunk));
+        rows_mac<T, 1, NT, VEC, kTerms<T>>(item, w, hp, k0, min(a.I, k0 + a.chunk), (int64_t)a.T * a.k * a.I);
         // only into the tokens that chose the expert: a zero fragment times an infinite weight is a NaN
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -413,7 +428,7 @@ using namespace dlrm;
 extern "C" size_t dlrm_moe_fwd_workspace_size(dlrm_dtype dtype, int T, int H, int I, int E, int k)
 {
     if (!moe_sizes_ok(dtype, T, H, I, E, k)) return 0;
-    return dlrm_ws_align((size_t)T * k * I * dense_dtype_size(dtype));
+    return dlrm_ws_align((size_t)T * k * I * 4);   // one fp32 term, or two of 2 bytes
 }
 
 extern "C" dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_w_router, const void* d_w1,
@@ -449,6 +464,7 @@ extern "C" dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_
         return fail(DLRM_ERR_INVALID_ARG, "%s: the workspace must be 256-byte aligned", fn);
     MoeArgs a = {d_x, d_w_router, d_w1, d_w2, d_residual, ldx, ldr, ldy, T,     H,       I,          E, k, (int)act,
                  gated != 0, 0, 0, d_y, d_ids, d_probs, d_workspace};
+    // the workspace's planes start on the grid where I keeps its rows there
     const bool vec = rows_aligned16(d_x, ldx, T, es) && rows_aligned16(d_w_router, H, E, es) &&
                      rows_aligned16(d_w1, H, 2, es) && rows_aligned16(d_w2, I, 2, es);
     return with_type(dtype, [&](auto t) {

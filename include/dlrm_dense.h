@@ -139,7 +139,8 @@ size_t dlrm_linear_bwd_workspace_size(const void* d_grad_y, int64_t ldg, const v
  *   last three contiguous;  d_residual [T][H] or NULL;  d_y [T][H] (output)
  *   d_ids int32 [T][k] (output);  d_probs fp32 [T][k] (output)
  *   d_workspace: dlrm_moe_fwd_workspace_size bytes, 256-byte aligned
- * probs * h is rounded once to dtype before the second product (2-byte types).
+ * probs * h enters the second product as two values of a 2-byte dtype (rounded
+ * and the rounded rest), or in fp32.
  * Experts that no token chose are not read.  Requires H, I >= 1, 0 <= T <=
  * DLRM_MOE_MAX_TOKENS, 1 <= E <= DLRM_MOE_MAX_EXPERTS and 1 <= k <=
  * min(E, DLRM_MOE_MAX_TOP_K); larger T, E or k is DLRM_ERR_UNSUPPORTED.
