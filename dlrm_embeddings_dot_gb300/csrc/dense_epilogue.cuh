@@ -39,6 +39,21 @@ __device__ __forceinline__ void act8(float (&f)[8], int act)
     }
 }
 
+// f *= a'(z)
+__device__ __forceinline__ void slope8(float (&f)[8], const float (&z)[8], int act)
+{
+    if (act == DLRM_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = z[i] <= 0.f ? 0.f : f[i];
+    } else if (act == DLRM_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= act_slope(z[i], DLRM_ACT_GELU);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= act_slope(z[i], DLRM_ACT_SILU);
+    }
+}
+
 // The bias of columns col .. col + 7 (zeros past N or without a bias).
 __device__ __forceinline__ void bias8(const float* bias, int col, int N, float (&b)[8])
 {

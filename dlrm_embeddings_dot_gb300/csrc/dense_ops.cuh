@@ -126,12 +126,15 @@ __device__ __forceinline__ void split1(float v, uint32_t& hi, uint32_t& mid, flo
 }
 
 // -------------------------------------------------------------- activations
-// The functions of the header's definitions.  NaN passes through each (RELU
-// compares with z < 0, which is false for NaN).
+// The functions of the header's definitions.  NaN passes through each.
 __device__ __forceinline__ float act_f(float z, int act)
 {
     switch (act) {
-    case DLRM_ACT_RELU: return z < 0.f ? 0.f : z;
+    case DLRM_ACT_RELU: {
+        float r;
+        asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(z));
+        return r;
+    }
     case DLRM_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678f));
     case DLRM_ACT_SILU: return z / (1.f + expf(-z));
     default: return z;
@@ -199,11 +202,11 @@ __device__ __forceinline__ DropKey drop_key(const Drop& d)
 __device__ __forceinline__ void drop8(float (&f)[8], const Drop& d, const DropKey& k, uint32_t row, uint32_t group)
 {
     const uint4 u = philox4x32(group, row, k.o0, k.o1, k.k0, k.k1);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w}, t = d.thr << 16;   // numbers compared in the upper half
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        f[2 * i] = (w[i] & 0xffffu) >= d.thr ? f[2 * i] * d.scale : 0.f;
-        f[2 * i + 1] = (w[i] >> 16) >= d.thr ? f[2 * i + 1] * d.scale : 0.f;
+        f[2 * i] = (w[i] << 16) >= t ? f[2 * i] * d.scale : 0.f;
+        f[2 * i + 1] = w[i] >= t ? f[2 * i + 1] * d.scale : 0.f;
     }
 }
 

@@ -12,6 +12,7 @@ namespace dlrm {
 namespace {
 
 constexpr int kDropThreads = 256;
+constexpr int kAhead = 2;
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kDropThreads)
@@ -25,28 +26,46 @@ dropout_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ res, 
     int64_t i = (int64_t)blockIdx.x * kDropThreads + threadIdx.x;
     int64_t row = i / groups, g = i - row * groups;
     const int64_t drow = stride / groups, dg = stride - drow * groups;
-    for (; i < runs; i += stride) {
-        const int col = (int)g * 8, n = N - col;
-        const Raw8<T> rx = load8<T, VEC>(x + row * ldx + col, n);
-        float f[8];
-        if (res) {
-            const Raw8<T> rr = load8<T, VEC>(res + row * ldr + col, n);
-            float r[8];
-            widen8<T>(rx, f);
-            if (drop.thr) drop8(f, drop, key, (uint32_t)row, (uint32_t)g);
-            widen8<T>(rr, r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] += r[j];
-        } else {
-            widen8<T>(rx, f);
-            if (drop.thr) drop8(f, drop, key, (uint32_t)row, (uint32_t)g);
-        }
-        store8<T, VEC>(y + row * ldy + col, n, f);
+    // two runs a turn, so that twice the loads are in flight
+    auto next = [&] {
+        i += stride;
         row += drow;
         g += dg;
         if (g >= groups) {
             g -= groups;
             ++row;
+        }
+    };
+    while (i < runs) {
+        Raw8<T> rx[kAhead], rr[kAhead];
+        int64_t at[kAhead], gs[kAhead];
+        int live = 0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (i < runs) {
+                const int col = (int)g * 8;
+                at[k] = row;
+                gs[k] = g;
+                rx[k] = load8<T, VEC>(x + row * ldx + col, N - col);
+                if (res) rr[k] = load8<T, VEC>(res + row * ldr + col, N - col);
+                live = k + 1;
+                next();
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (k >= live) break;
+            const int col = (int)gs[k] * 8;
+            float f[8];
+            widen8<T>(rx[k], f);
+            if (drop.thr) drop8(f, drop, key, (uint32_t)at[k], (uint32_t)gs[k]);
+            if (res) {
+                float r[8];
+                widen8<T>(rr[k], r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] += r[j];
+            }
+            store8<T, VEC>(y + at[k] * ldy + col, N - col, f);
         }
     }
 }

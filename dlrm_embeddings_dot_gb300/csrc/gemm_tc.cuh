@@ -3,15 +3,19 @@
 // contiguous: x and W of the forward, dZ of dX) or MN-major (the output's row
 // or column index contiguous: W of dX, dZ and x of dW).
 //
-// A persistent block per SM walks 128 x BN output tiles (BN = 256, 128 or 64):
+// A persistent block per SM, or pair of blocks (PAIR), walks output tiles of 128
+// (256) x BN rows and columns, BN = 256, 128 or 64:
 //   warp 0      TMA producer: per 64 of K a 128 x 64 tile of A and a BN x 64
-//               tile of B, 128-byte swizzle, into an NS-stage ring
-//   warp 1      TMEM allocation and MMA issue (M = 128, N = BN, K = 16 steps)
-//   warps 2..9  epilogue: TMEM lane quarter q = warp % 4, alternate 32-column
-//               slices.  A slice goes through 4 KB of shared memory, so that a
-//               lane then holds eight consecutive columns of a row: one Philox
-//               call, 16-byte loads and stores, and 64 contiguous bytes of a
-//               row for every four lanes
+//               tile of B, 128-byte swizzle, into an NS-stage ring; in a pair
+//               each block loads its own 128 rows of A and half of B's rows
+//   warp 1      TMEM allocation and MMA issue (M = 128 or 256, N = BN, K = 16
+//               steps; the pair's leader issues for both blocks, whose tensor
+//               cores read both halves of B)
+//   warps 2..17 epilogue: TMEM lane quarter q = warp % 4, every fourth
+//               32-column slice.  A slice goes through 4 KB of shared memory,
+//               so that a lane then holds eight consecutive columns of a row:
+//               one Philox call, 16-byte loads and stores, and 64 contiguous
+//               bytes of a row for every four lanes
 // Two TMEM accumulators let the products of the next tile run under the
 // epilogue of this one.
 //
@@ -31,8 +35,9 @@ using namespace tc;
 
 constexpr int kBM = 128;            // output rows of a tile
 constexpr int kKB = 64;             // K elements of a stage (128-byte rows)
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kSliceStep = kEpiWarps / 4 * 32;   // columns between a warp's slices
 constexpr int kMaxStages = 8;
 constexpr int kSmemLimit = 232448;  // 227 KB opt-in per block
 constexpr int kScratch = kEpiWarps * 32 * 128;
@@ -59,15 +64,15 @@ __device__ __forceinline__ int plane_pair(int pairs, int p)
     return pairs == 1 ? 0 : (int)(order >> (4 * p)) & 15;
 }
 
-inline size_t smem_bytes(int BN, int ns)
+inline size_t smem_bytes(int b_rows, int ns)
 {
-    return 1024 + (size_t)ns * (kBM * 128 + BN * 128) + kScratch + (size_t)(2 * ns + 4) * 8 + 16;
+    return 1024 + (size_t)ns * (kBM * 128 + b_rows * 128) + kScratch + (size_t)(2 * ns + 4) * 8 + 16;
 }
 
 // The warp's 32 x 32 slice of the accumulator at taddr to rows of eight columns
-// a lane, then fn(pass, row within the slice, f).
-template <typename Fn>
-__device__ __forceinline__ void transpose_slice(uint32_t taddr, uint8_t* scratch, Fn&& fn)
+// a lane, then fn(row within the slice, f); loaded() once TMEM has been read.
+template <typename Loaded, typename Fn>
+__device__ __forceinline__ void transpose_slice(uint32_t taddr, uint8_t* scratch, Loaded&& loaded, Fn&& fn)
 {
     const int lane = threadIdx.x % kWarp;
     uint32_t v[32];
@@ -78,36 +83,39 @@ __device__ __forceinline__ void transpose_slice(uint32_t taddr, uint8_t* scratch
     for (int c = 0; c < 8; ++c)
         *reinterpret_cast<uint4*>(scratch + lane * 128 + ((c ^ (lane & 7)) << 4)) =
             make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    loaded();
     __syncwarp();
-#pragma unroll
+#pragma unroll 1   // unrolled, four passes' registers are live at once and spill
     for (int pass = 0; pass < 4; ++pass) {
         const int r = pass * 8 + lane / 4, c = 2 * (lane % 4);
         const float4 lo = *reinterpret_cast<const float4*>(scratch + r * 128 + ((c ^ (r & 7)) << 4));
         const float4 hi = *reinterpret_cast<const float4*>(scratch + r * 128 + (((c + 1) ^ (r & 7)) << 4));
         float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        fn(pass, r, f);
+        fn(r, f);
     }
 }
 
-template <typename T, bool A_MN, bool B_MN>
+template <typename T, bool A_MN, bool B_MN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ Args a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    constexpr int CG = PAIR ? 2 : 1;
     const int BN = a.BN, NS = a.NS;
     constexpr int a_bytes = kBM * 128;
-    const int stage_bytes = a_bytes + BN * 128;
+    const int b_rows = BN / CG, stage_bytes = a_bytes + b_rows * 128;
     uint8_t* scratch = smem + (size_t)NS * stage_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kScratch);
+    uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kScratch);   // in a pair the leader's count both blocks' bytes
     uint64_t* empty = full + NS;
     uint64_t* tfull = empty + NS;
-    uint64_t* tempty = tfull + 2;
+    uint64_t* tempty = tfull + 2;                                       // in a pair the leader's count both epilogues
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tempty + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    const int rank = PAIR ? (int)(blockIdx.x & 1) : 0, first = (int)blockIdx.x / CG, stride = (int)gridDim.x / CG;
     const int per_split = a.tiles_m * a.tiles_n, tiles = per_split * a.splits;
 
     if (threadIdx.x == 0) {
@@ -117,119 +125,193 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], kEpiWarps);
+            mbar_init(&tempty[i], CG * kEpiWarps);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
-                     "r"(a.tmem_cols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_holder)),
+                         "r"(a.tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                             smem_u32(tmem_holder)),
+                         "r"(a.tmem_cols)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if constexpr (PAIR) cluster_barrier();   // the other block's barriers are set up too
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
     pdl_wait();
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ---------------------------------------------------- TMA producer
-            int q = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const int split = t / per_split, tt = t - split * per_split;
-                const int m0 = tt / a.tiles_n * kBM, n0 = tt % a.tiles_n * BN;
-                const int b0 = (int)((int64_t)a.kb * split / a.splits), b1 = (int)((int64_t)a.kb * (split + 1) / a.splits);
-                for (int p = 0; ok && p < a.pairs; ++p) {
-                    const int pp = plane_pair(a.pairs, p), pa = pp >> 2, pb = pp & 3;
-                    for (int kb = b0; kb < b1; ++kb, ++q) {
-                        const int stage = q % NS;
-                        if (!mbar_wait(&empty[stage], ((uint32_t)(q / NS) & 1u) ^ 1u, abort_flag, a.wait_cycles)) {
-                            ok = false;
-                            break;
-                        }
-                        uint8_t* sa = smem + (size_t)stage * stage_bytes;
-                        mbar_expect_tx(&full[stage], (uint32_t)stage_bytes);
+        // -------------------------------------------------------- TMA producer
+        int stage = 0, q = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = first; ok && t < tiles; t += stride) {
+            const int split = t / per_split, tt = t - split * per_split;
+            const int m0 = (tt / a.tiles_n * CG + rank) * kBM, n0 = tt % a.tiles_n * BN + rank * b_rows;
+            const int b0 = (int)((int64_t)a.kb * split / a.splits), b1 = (int)((int64_t)a.kb * (split + 1) / a.splits);
+            for (int p = 0; ok && p < a.pairs; ++p) {
+                const int pp = plane_pair(a.pairs, p), pa = pp >> 2, pb = pp & 3;
+                for (int kb = b0; kb < b1; ++kb) {
+                    ok = __all_sync(~0u, mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.wait_cycles));
+                    if (!ok) break;
+                    uint8_t* sa = smem + (size_t)stage * stage_bytes;
+                    if (elect_one()) {
+                        // the other block's bytes can only be those of this phase: it too waits for the stage
+                        if (rank == 0) mbar_expect_tx(&full[stage], (uint32_t)(CG * stage_bytes));
+                        const uint32_t bar = PAIR ? peer_u32(&full[stage], 0) : 0;
+                        auto load = [&](void* dst, const CUtensorMap* map, int c0, int c1, int c2) {
+                            if constexpr (PAIR) tma_load_3d_pair(dst, map, c0, c1, c2, bar);
+                            else tma_load_3d(dst, map, c0, c1, c2, &full[stage]);
+                        };
                         if constexpr (A_MN) {
 #pragma unroll
-                            for (int i = 0; i < kBM / 64; ++i)
-                                tma_load_3d(sa + i * 8192, &map_a, m0 + i * 64, kb * kKB, pa, &full[stage]);
+                            for (int i = 0; i < kBM / 64; ++i) load(sa + i * 8192, &map_a, m0 + i * 64, kb * kKB, pa);
                         } else {
-                            tma_load_3d(sa, &map_a, kb * kKB, m0, pa, &full[stage]);
+                            load(sa, &map_a, kb * kKB, m0, pa);
                         }
                         if constexpr (B_MN) {
-                            for (int i = 0; i < BN / 64; ++i)
-                                tma_load_3d(sa + a_bytes + i * 8192, &map_b, n0 + i * 64, kb * kKB, pb, &full[stage]);
+                            for (int i = 0; i < b_rows / 64; ++i)
+                                load(sa + a_bytes + i * 8192, &map_b, n0 + i * 64, kb * kKB, pb);
                         } else {
-                            tma_load_3d(sa + a_bytes, &map_b, kb * kKB, n0, pb, &full[stage]);
+                            load(sa + a_bytes, &map_b, kb * kKB, n0, pb);
                         }
+                    }
+                    __syncwarp();
+                    ++q;
+                    if (++stage == NS) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
-            if (*abort_flag)   // the copies already issued must land before the block exits
-                for (int j = (q > NS ? q - NS : 0); j < q; ++j) mbar_drain(&full[j % NS], (uint32_t)(j / NS) & 1u);
+        }
+        if (lane == 0) {
+            // every copy has been multiplied before the block exits
+            for (int j = (q > NS ? q - NS : 0); ok && j < q; ++j)
+                ok = mbar_wait(&empty[j % NS], (uint32_t)(j / NS) & 1u, abort_flag, a.wait_cycles);
+            if (*abort_flag) {   // the copies already issued must land before the block exits
+                if (rank == 0) {
+                    for (int j = (q > NS ? q - NS : 0); j < q; ++j) mbar_drain(&full[j % NS], (uint32_t)(j / NS) & 1u);
+                } else {         // counted in the leader's memory, which waits for them; its abort may have
+                                 // come first, so leave them a thousand times a copy's latency
+                    const long long t0 = clock64();
+                    while (clock64() - t0 < 2000000) {
+                    }
+                }
+            }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (rank == 0) {
             // ---------------------------------------------------- MMA issuer
-            int q = 0, it = 0;
+            auto commit = [&](uint64_t* bar) {
+                if constexpr (PAIR) tc_commit_pair(bar);
+                else tc_commit(bar);
+            };
+            auto mma = [&](uint32_t d, uint64_t ad, uint64_t bd, uint32_t accumulate) {
+                if constexpr (PAIR) tc_mma_f16_pair(d, ad, bd, a.idesc, accumulate);
+                else tc_mma_f16(d, ad, bd, a.idesc, accumulate);
+            };
+            // descriptors of stage 0, and what a K step adds to their address field (16-byte units)
+            const uint32_t sa = smem_u32(smem), sb = sa + a_bytes;
+            const uint64_t ad0 = A_MN ? sw128_desc_mn(sa, 8192, 1024) : sw128_desc(sa);
+            const uint64_t bd0 = B_MN ? sw128_desc_mn(sb, 8192, 1024) : sw128_desc(sb);
+            constexpr uint32_t da = A_MN ? 2048 / 16 : 32 / 16, db = B_MN ? 2048 / 16 : 32 / 16;
+            int stage = 0, it = 0;
+            uint32_t phase = 0;
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++it) {
+            for (int t = first; ok && t < tiles; t += stride, ++it) {
                 const int split = t / per_split;
                 const int b0 = (int)((int64_t)a.kb * split / a.splits), b1 = (int)((int64_t)a.kb * (split + 1) / a.splits);
                 const int buf = it & 1;
-                if (!mbar_wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.wait_cycles)) break;
+                ok = __all_sync(~0u, mbar_wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.wait_cycles));
+                if (!ok) break;
+                if constexpr (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(buf * BN);
                 uint32_t accumulate = 0;
                 for (int p = 0; ok && p < a.pairs; ++p) {
-                    for (int kb = b0; kb < b1; ++kb, ++q) {
-                        const int stage = q % NS;
-                        if (!mbar_wait(&full[stage], (uint32_t)(q / NS) & 1u, abort_flag, a.wait_cycles)) {
-                            ok = false;
-                            break;
-                        }
+                    for (int kb = b0; kb < b1; ++kb) {
+                        ok = __all_sync(~0u, mbar_wait(&full[stage], phase, abort_flag, a.wait_cycles));
+                        if (!ok) break;
                         tc_fence_after();
-                        const uint32_t sa = smem_u32(smem + (size_t)stage * stage_bytes), sb = sa + a_bytes;
-                        const int steps = kb == a.kb - 1 ? a.last_steps : kKB / 16;
-                        for (int kk = 0; kk < steps; ++kk) {
-                            const uint64_t ad = A_MN ? sw128_desc_mn(sa + kk * 2048, 8192, 1024) : sw128_desc(sa + kk * 32);
-                            const uint64_t bd = B_MN ? sw128_desc_mn(sb + kk * 2048, 8192, 1024) : sw128_desc(sb + kk * 32);
-                            tc_mma_f16(d, ad, bd, a.idesc, accumulate);
-                            accumulate = 1;
+                        const uint64_t ad = ad0 + (uint32_t)(stage * (stage_bytes / 16));
+                        const uint64_t bd = bd0 + (uint32_t)(stage * (stage_bytes / 16));
+                        if (kb != a.kb - 1 || a.last_steps == 4) {
+                            if (elect_one()) {
+                                mma(d, ad, bd, accumulate);
+                                mma(d, ad + da, bd + db, 1);
+                                mma(d, ad + 2 * da, bd + 2 * db, 1);
+                                mma(d, ad + 3 * da, bd + 3 * db, 1);
+                                commit(&empty[stage]);
+                            }
+                        } else {   // the rest of K holds zeros past last_steps
+                            if (elect_one()) {
+                                for (int kk = 0; kk < a.last_steps; ++kk)
+                                    mma(d, ad + kk * da, bd + kk * db, kk ? 1 : accumulate);
+                                commit(&empty[stage]);
+                            }
                         }
-                        tc_commit(&empty[stage]);
+                        __syncwarp();
+                        accumulate = 1;
+                        if (++stage == NS) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
-                if (ok) tc_commit(&tfull[buf]);
+                if (ok && elect_one()) commit(&tfull[buf]);
+                __syncwarp();
             }
-            if (*abort_flag) {   // MMAs already issued must finish before TMEM is freed
-                tc_commit(&tfull[it & 1]);
+            // MMAs already issued must finish before TMEM is freed
+            if (__any_sync(~0u, *abort_flag != 0) && elect_one()) {
+                commit(&tfull[it & 1]);
                 mbar_drain(&tfull[it & 1], (uint32_t)(it >> 1) & 1u);
             }
         }
     } else {
         // ------------------------------------------------------------ epilogue
-        const int quarter = warp & 3, half = (warp - 2) / 4;
+        const int quarter = warp & 3, part = (warp - 2) / 4;
         uint8_t* mine = scratch + (warp - 2) * (32 * 128);
         const DropKey key = drop_key(a.e.drop);
         int it = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++it) {
+        for (int t = first; t < tiles; t += stride, ++it) {
             const int buf = it & 1;
             if (!mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, a.wait_cycles)) break;
             __syncwarp();
             tc_fence_after();
             const int split = t / per_split, tt = t - split * per_split;
-            const int row0 = tt / a.tiles_n * kBM + 32 * quarter, n0 = tt % a.tiles_n * BN;
+            const int row0 = (tt / a.tiles_n * CG + rank) * kBM + 32 * quarter, n0 = tt % a.tiles_n * BN;
             const uint32_t taddr = tmem_base + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(buf * BN);
-            for (int c0 = 32 * half; c0 < BN; c0 += 64) {
-                if (n0 + c0 >= a.N) break;
+            const int cols = min(BN, a.N - n0);
+            auto release = [&] {   // the accumulator has been read: the tile after next may overwrite it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster(peer_u32(&tempty[buf], 0));
+                    else mbar_arrive(&tempty[buf]);
+                }
+            };
+            if (32 * part >= cols) release();
+            for (int c0 = 32 * part; c0 < cols; c0 += kSliceStep) {
                 const int col = n0 + c0 + 8 * (lane % 4), n = a.N - col;
+                auto loaded = [&] {
+                    if (c0 + kSliceStep >= cols) release();
+                };
                 if (a.splits > 1) {
-                    transpose_slice(taddr + c0, mine, [&](int, int r, float (&f)[8]) {
+                    transpose_slice(taddr + c0, mine, loaded, [&](int r, float (&f)[8]) {
                         const int row = row0 + r;
                         if (row < a.M && n > 0) {
                             float4* p = reinterpret_cast<float4*>(a.partial + ((int64_t)split * a.M + row) * a.Np + col);
@@ -249,29 +331,33 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                                 if (row < a.M) res[i] = load8<T, true>((const T*)a.e.res + row * a.e.ldr + col, 8);
                             }
                         }
-                        transpose_slice(taddr + c0, mine, [&](int pass, int r, float (&f)[8]) {
-                            if (row0 + r < a.M) finish8<T, true>(a.e, key, row0 + r, col, 8, f, b, res[pass]);
+                        transpose_slice(taddr + c0, mine, loaded, [&](int r, float (&f)[8]) {
+                            if (row0 + r < a.M) finish8<T, true>(a.e, key, row0 + r, col, 8, f, b, res[0]);
+                            res[0] = res[1], res[1] = res[2], res[2] = res[3];
                         });
                     } else {   // a ragged slice, or rows off the 16-byte grid
-                        transpose_slice(taddr + c0, mine, [&](int, int r, float (&f)[8]) {
+                        transpose_slice(taddr + c0, mine, loaded, [&](int r, float (&f)[8]) {
                             if (row0 + r < a.M && n > 0) finish8_any<T>(a.e, key, row0 + r, col, n, f, b);
                         });
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty[buf]);
         }
     }
 
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    if constexpr (PAIR) cluster_barrier();   // neither block leaves while the other still reads its memory
+    else __syncthreads();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(a.tmem_cols)
-                     : "memory");
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(a.tmem_cols)
+                         : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(a.tmem_cols)
+                         : "memory");
     }
     if (threadIdx.x == 0 && *abort_flag) set_status(a.status, DLRM_STATUS_TIMEOUT);
 }
@@ -315,29 +401,34 @@ struct Shape {
 
 struct Plan {
     int BN, splits;
+    bool pair;
 };
 
-// How a product is cut: the plan with the least estimated time.  The unit is
-// one 16-wide MMA step of a 128 x 64 tile.
+// How a product is cut: the plan with the least estimated time, in cycles.
 inline Plan plan(const Shape& s)
 {
+    struct Tile {
+        int BN;
+        bool pair;
+        double block;   // cycles of a 64-wide block of K
+    };
+    constexpr Tile tiles_of[] = {{256, true, 540}, {256, false, 640}, {128, true, 300}, {128, false, 340}, {64, false, 220}};
     const int sms = num_sms();
     const int64_t kb = (s.K + kKB - 1) / kKB;
-    Plan best = {256, 1};
+    Plan best = {};
     double least = 0;
-    for (int BN = 256; BN >= 64; BN /= 2) {
-        if (BN > 64 && BN / 2 >= s.N) continue;
-        const int64_t tiles = (int64_t)((s.M + kBM - 1) / kBM) * ((s.N + BN - 1) / BN);
+    for (const Tile& t : tiles_of) {
+        const int rows = kBM * (t.pair ? 2 : 1), units = t.pair ? sms / 2 : sms;
+        const int64_t tiles = (int64_t)((s.M + rows - 1) / rows) * ((s.N + t.BN - 1) / t.BN);
         for (int S = 1; S <= 32 && S <= kb; ++S) {
-            if (S > 1 && tiles * S > 4 * (int64_t)sms) break;
-            const int64_t waves = (tiles * S + sms - 1) / sms;
-            const int64_t blocks = (kb + S - 1) / S * s.pairs;
-            // a stage's products (a narrow tile is bound by its operands' arrival), a tile's epilogue, the finish pass
-            double cost = (double)waves * blocks * (BN == 256 ? 16.0 : BN == 128 ? 9.0 : 6.0) + waves * BN * 0.25 + 40;
-            if (S > 1) cost += 80 + (double)s.M * s.N * S / sms / 1200.0;
+            if (S > 1 && tiles * S > 4 * (int64_t)units) break;
+            const int64_t waves = (tiles * S + units - 1) / units;
+            const double products = (double)((kb + S - 1) / S) * s.pairs * t.block, epilogue = 12.0 * t.BN;
+            double cost = waves * (products > epilogue ? products : epilogue) + epilogue;
+            if (S > 1) cost += 4000 + (double)s.M * s.N * S * 8 / 4000;   // another launch, and the partial tiles' way
             if (least == 0 || cost < least) {
                 least = cost;
-                best = {BN, S};
+                best = {t.BN, S, t.pair};
             }
         }
     }
@@ -379,7 +470,7 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     const Plan p = plan(s);
     CUtensorMap ma, mb;
     dlrm_status r = make_map(fn, &ma, A, bf, s.M, s.K, kBM);
-    if (r == DLRM_OK) r = make_map(fn, &mb, B, bf, s.N, s.K, p.BN);
+    if (r == DLRM_OK) r = make_map(fn, &mb, B, bf, s.N, s.K, p.pair ? p.BN / 2 : p.BN);
     if (r != DLRM_OK) return r;
     Args a = {};
     a.M = s.M;
@@ -389,26 +480,29 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     a.pairs = s.pairs;
     a.splits = p.splits;
     a.BN = p.BN;
-    const int64_t tm = (s.M + kBM - 1) / kBM, tn = (s.N + p.BN - 1) / p.BN;
+    const int CG = p.pair ? 2 : 1, b_rows = p.BN / CG;
+    const int64_t tm = (s.M + CG * kBM - 1) / (CG * kBM), tn = (s.N + p.BN - 1) / p.BN;
     if (tm * tn > INT32_MAX / 64) return fail(DLRM_ERR_UNSUPPORTED, "%s: %lld output tiles", fn, (long long)(tm * tn));
     a.tiles_m = (int)tm;
     a.tiles_n = (int)tn;
     a.NS = kMaxStages;
-    while (smem_bytes(p.BN, a.NS) > (size_t)kSmemLimit) --a.NS;
-    a.idesc = idesc_f16(kBM, p.BN) | (bf ? 1u << 7 | 1u << 10 : 0u) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+    while (smem_bytes(b_rows, a.NS) > (size_t)kSmemLimit) --a.NS;
+    a.idesc = idesc_f16(CG * kBM, p.BN) | (bf ? 1u << 7 | 1u << 10 : 0u) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
     a.tmem_cols = 2 * p.BN;
     a.partial = partial;
     a.Np = padded(s.N);
     a.e = e;
     a.status = status;
     a.wait_cycles = wait_limit_cycles();
-    const int64_t tiles = tm * tn * p.splits;
-    const int grid = (int)(tiles < num_sms() ? tiles : num_sms());
-    const size_t smem = smem_bytes(p.BN, a.NS);
-    auto kern = gemm_kernel<T, A_MN, B_MN>;
+    const int64_t tiles = tm * tn * p.splits, units = num_sms() / CG;
+    const int grid = (int)(tiles < units ? tiles : units) * CG;
+    const size_t smem = smem_bytes(b_rows, a.NS);
+    auto kern = p.pair ? gemm_kernel<T, A_MN, B_MN, true> : gemm_kernel<T, A_MN, B_MN, false>;
     cudaError_t ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (ce != cudaSuccess) return fail(DLRM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
-    r = check_launch_pdl(launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, ma, mb, a), "gemm_kernel");
+    r = check_launch_pdl(p.pair ? launch_cluster(kern, dim3(grid), dim3(kThreads), smem, st, 2, ma, mb, a)
+                                : launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, ma, mb, a),
+                         "gemm_kernel");
     if (r != DLRM_OK || p.splits == 1) return r;
     const int64_t runs = a.Np / 8 * s.M, want = (runs + 255) / 256, most = (int64_t)num_sms() * 8;
     return check_launch_pdl(launch_pdl(finish_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,

@@ -175,7 +175,7 @@ dlrm_status launch_few(const void* x, int64_t ldx, const void* w, int64_t ldw, i
     auto go = [&](auto n) {
         constexpr int NT = decltype(n)::value;
         auto kern = vec ? linear_few_kernel<T, NT, true> : linear_few_kernel<T, NT, false>;
-        return check_launch_pdl(few::launch_cluster(kern, dim3((unsigned)row_tiles * S), dim3(256), 0, st, S,
+        return check_launch_pdl(launch_cluster(kern, dim3((unsigned)row_tiles * S), dim3(256), 0, st, S,
                                                     (const T*)x, ldx, (const T*)w, ldw, M, N, K, e),
                                 "linear_few_kernel");
     };
@@ -204,26 +204,37 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, 
     const int64_t Np = padded(N);
     float sum[8] = {};
     if (n > 0) {
-        const int r0 = blockIdx.y * rows, r1 = min(M, r0 + rows);
+        constexpr int kAhead = 8 / sizeof(T);   // rows whose loads are in flight together
+        const int r0 = blockIdx.y * rows + ty, r1 = min(M, (int)(blockIdx.y + 1) * rows);
         const bool v = vec && n >= 8;
-#pragma unroll 2
-        for (int r = r0 + ty; r < r1; r += step) {
-            const T* gp = dy + r * ldg + col;
-            const T* pp = pre + r * ldp + col;
-            const Raw8<T> a = v ? load8<T, true>(gp, 8) : load8<T, false>(gp, n);
-            float f[8];
-            widen8<T>(a, f);
-            if (act != DLRM_ACT_NONE) {
-                const Raw8<T> b = v ? load8<T, true>(pp, 8) : load8<T, false>(pp, n);
-                float z[8];
-                widen8<T>(b, z);
+        for (int r = r0; r < r1; r += step * kAhead) {
+            Raw8<T> a[kAhead], b[kAhead];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] *= act_slope(z[i], act);
+            for (int k = 0; k < kAhead; ++k) {
+                const int rr = r + k * step;
+                if (rr < r1) {
+                    const T* gp = dy + rr * ldg + col;
+                    const T* pp = pre + rr * ldp + col;
+                    a[k] = v ? load8<T, true>(gp, 8) : load8<T, false>(gp, n);
+                    if (act != DLRM_ACT_NONE) b[k] = v ? load8<T, true>(pp, 8) : load8<T, false>(pp, n);
+                }
             }
-            if (drop.thr) drop8(f, drop, key, (uint32_t)r, (uint32_t)g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += f[i];
-            if (dz) store_operand8<T>(dz, r * Np + col, M * Np, f);
+            for (int k = 0; k < kAhead; ++k) {
+                const int rr = r + k * step;
+                if (rr >= r1) break;
+                float f[8];
+                widen8<T>(a[k], f);
+                if (act != DLRM_ACT_NONE) {
+                    float z[8];
+                    widen8<T>(b[k], z);
+                    slope8(f, z, act);
+                }
+                if (drop.thr) drop8(f, drop, key, (uint32_t)rr, (uint32_t)g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] += f[i];
+                if (dz) store_operand8<T>(dz, rr * Np + col, M * Np, f);
+            }
         }
     }
     if (!partial) return;
@@ -257,22 +268,22 @@ GradZ grad_z_shape(int M, int N)
     return s;
 }
 
-// out[n] = the sum of partial's rows: 32 columns a block, 16 threads a column.
-__global__ void __launch_bounds__(512)
+// out[n] = the sum of partial's rows: 32 columns a block, 32 threads a column.
+__global__ void __launch_bounds__(1024)
 sum_rows_kernel(const float* __restrict__ partial, int rows, int N, float* __restrict__ out)
 {
     pdl_wait();
-    __shared__ float red[16][33];
+    __shared__ float red[32][33];
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, n = blockIdx.x * 32 + tx;
     float s = 0.f;
     if (n < N)
-#pragma unroll 4
-        for (int r = ty; r < rows; r += 16) s += partial[(int64_t)r * N + n];
+#pragma unroll 8
+        for (int r = ty; r < rows; r += 32) s += partial[(int64_t)r * N + n];
     red[ty][tx] = s;
     __syncthreads();
     if (ty == 0 && n < N) {
 #pragma unroll
-        for (int y = 1; y < 16; ++y) s += red[y][tx];
+        for (int y = 1; y < 32; ++y) s += red[y][tx];
         out[n] = s;
     }
 }
@@ -443,7 +454,7 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
                                             g.cg, g.rows, products ? dz : nullptr, d_grad_bias ? sums : nullptr),
                                  "grad_z_kernel");
             if (r == DLRM_OK && d_grad_bias)
-                r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 31) / 32), dim3(512), 0, st,
+                r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 31) / 32), dim3(1024), 0, st,
                                                 (const float*)sums, g.chunks, N, d_grad_bias),
                                      "sum_rows_kernel");
         }
