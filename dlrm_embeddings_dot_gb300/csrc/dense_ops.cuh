@@ -210,6 +210,17 @@ __device__ __forceinline__ void drop8(float (&f)[8], const Drop& d, const DropKe
     }
 }
 
+// The eight columns of a group that are kept, a bit each.
+__device__ __forceinline__ uint32_t keep8(const Drop& d, const DropKey& k, uint32_t row, uint32_t group)
+{
+    const uint4 u = philox4x32(group, row, k.o0, k.o1, k.k0, k.k1);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w}, t = d.thr << 16;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bits |= ((w[i] << 16) >= t ? 1u << 2 * i : 0u) | (w[i] >= t ? 2u << 2 * i : 0u);
+    return bits;
+}
+
 // ---------------------------------------------------------------- host side
 inline bool dense_dtype_ok(dlrm_dtype dt) { return dt == DLRM_F32 || dt == DLRM_F16 || dt == DLRM_BF16; }
 inline int dense_dtype_size(dlrm_dtype dt) { return dt == DLRM_F32 ? 4 : 2; }

@@ -44,17 +44,25 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // The lane's 16 bytes of a row: values [0, n) of the kLane at p, zeros behind.
-// KEEP: allocate in L1 (tokens, read by every warp); weights pass through once.
-template <typename T, bool VEC, bool KEEP>
-__device__ __forceinline__ uint4 load_lane(const T* p, int n)
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load_part(const T* p, int n)
 {
-    if (VEC && n >= kLane<T>) return KEEP ? ldg_nc_l1_v4(p) : ldg_nc_v4(p);
+    if (VEC && n >= kLane<T>) return ldg_nc_l1_v4(p);
     T e[kLane<T>];
 #pragma unroll
-    for (int i = 0; i < kLane<T>; ++i) e[i] = p && i < n ? __ldg(p + i) : from_f32<T>(0.f);
+    for (int i = 0; i < kLane<T>; ++i) e[i] = i < n ? __ldg(p + i) : from_f32<T>(0.f);
     uint4 v;
     memcpy(&v, e, 16);
     return v;
+}
+
+// All kLane values.  KEEP: allocate in L1 (tokens, read by every warp); weights
+// pass through once.
+template <typename T, bool VEC, bool KEEP>
+__device__ __forceinline__ uint4 load_lane(const T* p)
+{
+    if constexpr (!VEC) return load_part<T, false>(p, kLane<T>);
+    else return KEEP ? ldg_nc_l1_v4(p) : ldg_nc_v4(p);
 }
 
 // Three bf16 parts of each of four floats (split1), two values to a word.
@@ -100,37 +108,97 @@ __device__ __forceinline__ void mac(float (&acc)[4], uint4 a, uint4 b, uint4 x)
 
 // acc[i][j] += tile i of 16 weight rows times tile j of 8 tokens over [k0, k1) of K
 // (k0 a multiple of kStep).  w[i][0] / w[i][1]: rows g and g + 8 of tile i;
-// x[j]: token g of tile j; NULL reads as zeros.  XP: terms each token is the
-// sum of, term i at x[j] + i * xplane.
+// x[j]: token g of tile j.  Every pointer is a readable row: where a tile has no
+// such row or token any other does, as rows and tokens meet only in results
+// that the caller then leaves alone.  XP: terms each token is the sum of, term i
+// at x[j] + i * xplane.
 template <typename T, int WT, int NT, bool VEC, int XP = 1>
-__device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* const (&w)[WT][2], const T* const (&x)[NT],
-                                         int k0, int k1, int64_t xplane = 0)
+__device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* (&w)[WT][2], const T* (&x)[NT], int k0, int k1,
+                                         int64_t xplane = 0)
 {
-    constexpr int U = WT == 1 ? 4 : 2;   // steps whose weight loads are in flight together
+    constexpr int U = WT == 1 ? 4 : 2;   // steps whose weight loads are issued together
+    constexpr int kBlock = U * kStep<T>;
     const int t = (threadIdx.x % kWarp) % 4;
-    for (int k = k0; k < k1; k += U * kStep<T>) {
-        uint4 a[U][WT][2];
+    if (k0 >= k1) return;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int at = k + u * kStep<T> + t * kLane<T>, n = k1 - at;
+    for (int i = 0; i < WT; ++i) {
+        w[i][0] += k0 + t * kLane<T>;
+        w[i][1] += k0 + t * kLane<T>;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) x[j] += k0 + t * kLane<T>;
+    int left = k1 - k0;
+    auto load = [&](uint4 (&a)[U][WT][2], int at) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < WT; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    a[u][i][h] = w[i][h] && n > 0 ? load_lane<T, VEC, false>(w[i][h] + at, n) : make_uint4(0, 0, 0, 0);
-        }
+                for (int h = 0; h < 2; ++h) a[u][i][h] = load_lane<T, VEC, false>(w[i][h] + at + u * kStep<T>);
+    };
+    auto multiply = [&](const uint4 (&a)[U][WT][2], int at) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int at = k + u * kStep<T> + t * kLane<T>, n = k1 - at;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int q = 0; q < XP; ++q) {
-                    const uint4 b = x[j] && n > 0 ? load_lane<T, VEC, true>(x[j] + q * xplane + at, n) : make_uint4(0, 0, 0, 0);
+                    const uint4 b = load_lane<T, VEC, true>(x[j] + q * xplane + at + u * kStep<T>);
 #pragma unroll
                     for (int i = 0; i < WT; ++i) mac<T>(acc[i][j], a[u][i][0], a[u][i][1], b);
                 }
+    };
+    auto advance = [&](int by) {
+#pragma unroll
+        for (int i = 0; i < WT; ++i) {
+            w[i][0] += by;
+            w[i][1] += by;
         }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) x[j] += by;
+        left -= by;
+    };
+    if constexpr (NT <= 2 && VEC) {   // the next block's weights are on their way while one is multiplied
+        uint4 a[U][WT][2], b[U][WT][2];
+        if (left >= kBlock) load(a, 0);
+#pragma unroll 1
+        while (left >= 2 * kBlock) {
+            load(b, kBlock);
+            multiply(a, 0);
+            if (left >= 3 * kBlock) load(a, 2 * kBlock);
+            multiply(b, kBlock);
+            advance(2 * kBlock);
+        }
+        if (left >= kBlock) {
+            multiply(a, 0);
+            advance(kBlock);
+        }
+    } else {
+#pragma unroll 1
+        while (left >= kBlock) {
+            uint4 a[U][WT][2];
+            load(a, 0);
+            multiply(a, 0);
+            advance(kBlock);
+        }
+    }
+#pragma unroll 1
+    while (left > 0) {   // the last steps, one at a time; past K both sides are zero
+        const int n = left - t * kLane<T>;
+        uint4 a[WT][2];
+#pragma unroll
+        for (int i = 0; i < WT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) a[i][h] = load_part<T, VEC>(w[i][h], n);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int q = 0; q < XP; ++q) {
+                const uint4 b = load_part<T, VEC>(x[j] + q * xplane, n);
+#pragma unroll
+                for (int i = 0; i < WT; ++i) mac<T>(acc[i][j], a[i][0], a[i][1], b);
+            }
+        advance(kStep<T>);
     }
 }
 

@@ -121,10 +121,10 @@ linear_few_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ w,
     {
         const T* wp[1][2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) wp[0][b] = row0 + g + 8 * b < N ? w + (row0 + g + 8 * b) * ldw : nullptr;
+        for (int b = 0; b < 2; ++b) wp[0][b] = w + min(row0 + g + 8 * b, N - 1) * ldw;
         const T* xp[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) xp[j] = j * 8 + g < M ? x + (j * 8 + g) * ldx : nullptr;
+        for (int j = 0; j < NT; ++j) xp[j] = x + min(j * 8 + g, M - 1) * ldx;
         float acc[1][NT][4] = {};
         rows_mac<T, 1, NT, VEC>(acc, wp, xp, part * per, min(K, (part + 1) * per));
         put_partial(red + warp * NT * 8 * kPitch, acc[0]);

@@ -27,7 +27,7 @@ namespace {
 using namespace few;
 
 constexpr int kThreads = 256, kWarps = kThreads / kWarp;
-constexpr int kUpCluster = 8;
+constexpr int kUpCluster = 8, kMaxSplit = 8;   // blocks of a cluster in moe_up, at most in moe_down
 constexpr int kMaxE = DLRM_MOE_MAX_EXPERTS, kMaxK = DLRM_MOE_MAX_TOP_K;
 
 struct MoeArgs {
@@ -135,13 +135,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeArgs a)
             const int tile = i % e_tiles, s = i / e_tiles;
             const int k0 = ((int)rank * sub + s) * per, k1 = min(a.H, k0 + per);
             const int e0 = tile * kRows + g;
-            const T* w[1][2] = {{e0 < a.E ? wr + (int64_t)e0 * a.H : nullptr,
-                                 e0 + 8 < a.E ? wr + (int64_t)(e0 + 8) * a.H : nullptr}};
+            const T* w[1][2] = {{wr + (int64_t)min(e0, a.E - 1) * a.H, wr + (int64_t)min(e0 + 8, a.E - 1) * a.H}};
             with_token_tiles(a.T, [&](auto nt) {
                 constexpr int NT = decltype(nt)::value;
                 const T* xp[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) xp[j] = j * 8 + g < a.T ? x + (j * 8 + g) * a.ldx : nullptr;
+                for (int j = 0; j < NT; ++j) xp[j] = x + min(j * 8 + g, a.T - 1) * a.ldx;
                 float acc[1][NT][4] = {};
                 rows_mac<T, 1, NT, VEC>(acc, w, xp, k0, k1);
 #pragma unroll
@@ -153,13 +152,24 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeArgs a)
                     }
             });
         }
+        if (sub > 1) {   // the block's own sums first: what is read across the cluster is read once
+            __syncthreads();
+            for (int i = threadIdx.x; i < a.T * E16; i += kThreads) {
+                float v = lp[i];
+                for (int s = 1; s < sub; ++s) v += lp[s * a.T * E16 + i];
+                lp[i] = v;
+            }
+        }
         cluster_sync();
         // block r adds up every eighth logit and hands it to all
         for (int i = threadIdx.x * kUpCluster + rank; i < a.T * E16; i += kThreads * kUpCluster) {
-            float v = 0.f;
-            for (int r = 0; r < kUpCluster; ++r)
-                for (int s = 0; s < sub; ++s) v += cluster_ld(cluster_map(lp + s * a.T * E16 + i, r));
-            for (int r = 0; r < kUpCluster; ++r) cluster_st(cluster_map(lg + i, r), v);
+            float v[kUpCluster];
+#pragma unroll
+            for (int r = 0; r < kUpCluster; ++r) v[r] = cluster_ld(cluster_map(lp + i, r));
+#pragma unroll
+            for (int r = 1; r < kUpCluster; ++r) v[0] += v[r];
+#pragma unroll
+            for (int r = 0; r < kUpCluster; ++r) cluster_st(cluster_map(lg + i, r), v[0]);
         }
         cluster_sync();
     }
@@ -227,23 +237,21 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeArgs a)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int r = row0 + g + 8 * b;
-                w[i][b] = r < a.I ? w1 + (base + (int64_t)i * a.I + r) * a.H : nullptr;
-            }
+            for (int b = 0; b < 2; ++b)
+                w[i][b] = w1 + (base + (int64_t)(a.gated ? i : 0) * a.I + min(row0 + g + 8 * b, a.I - 1)) * a.H;
         with_token_tiles(n, [&](auto nt) {
             constexpr int NT = decltype(nt)::value;
             const T* xp[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                xp[j] = j * 8 + g < n ? x + (int64_t)(entry[j * 8 + g] / kMaxK) * a.ldx : nullptr;
+                xp[j] = x + (int64_t)(entry[min(j * 8 + g, n - 1)] / kMaxK) * a.ldx;
             if (a.gated) {
                 float acc[2][NT][4] = {};
                 rows_mac<T, 2, NT, VEC>(acc, w, xp, k0, k1);
                 put_partial(red + (warp * 2) * tile_floats, acc[0]);
                 put_partial(red + (warp * 2 + 1) * tile_floats, acc[1]);
             } else {
-                const T* const w0[1][2] = {{w[0][0], w[0][1]}};
+                const T* w0[1][2] = {{w[0][0], w[0][1]}};
                 float acc[1][NT][4] = {};
                 rows_mac<T, 1, NT, VEC>(acc, w0, xp, k0, k1);
                 put_partial(red + (warp * 2) * tile_floats, acc[0]);
@@ -276,74 +284,67 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeArgs a)
     }
 }
 
-template <typename T, int NT, bool VEC>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(MoeArgs a)
 {
     pdl_wait();
+    extern __shared__ float smem[];   // [warp][token][kPitch]: each warp's sums over its items
     __shared__ Lists lists;
-    __shared__ float red[kWarps * NT * 8 * kPitch];
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4;
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4, t4 = lane % 4;
     const int S = (int)cluster_size(), rank = (int)cluster_rank();
     const int row0 = (int)(blockIdx.x / S) * kRows;
+    float* mine = smem + warp * a.T * kPitch;
+    for (int i = lane; i < a.T * kPitch; i += kWarp) mine[i] = 0.f;
     build_lists(lists, a.T, a.k, a.E, [&](int t, int j) { return a.ids[t * a.k + j]; });
 
     const int chunks = (a.I + a.chunk - 1) / a.chunk, items = lists.n_active * chunks;
     const T *w2 = (const T*)a.w2, *h = (const T*)a.h;
-    float acc[NT][4] = {};
     for (int it = rank * kWarps + warp; it < items; it += S * kWarps) {
-        const int e = lists.active[it / chunks], k0 = it % chunks * a.chunk;
-        const unsigned long long mask = lists.mask[e];
+        const int e = lists.active[it / chunks], k0 = it % chunks * a.chunk, n = __popcll(lists.mask[e]);
         const uint16_t* entry = lists.entry + lists.first[e];
         const T* w[1][2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int r = row0 + g + 8 * b;
-            w[0][b] = r < a.H ? w2 + ((int64_t)e * a.H + r) * a.I : nullptr;
-        }
-        const T* hp[NT];
+        for (int b = 0; b < 2; ++b) w[0][b] = w2 + ((int64_t)e * a.H + min(row0 + g + 8 * b, a.H - 1)) * a.I;
+        with_token_tiles(n, [&](auto nt) {
+            constexpr int NT = decltype(nt)::value;
+            const T* hp[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int t = j * 8 + g;
-            hp[j] = nullptr;
-            if (mask >> t & 1) {
-                const int slot = entry[__popcll(mask & ((1ull << t) - 1))] % kMaxK;
-                hp[j] = h + ((int64_t)t * a.k + slot) * a.I;
+            for (int j = 0; j < NT; ++j) {
+                const int slot = entry[min(j * 8 + g, n - 1)];
+                hp[j] = h + ((int64_t)(slot / kMaxK) * a.k + slot % kMaxK) * a.I;
             }
-        }
-        float item[1][NT][4] = {};
-        rows_mac<T, 1, NT, VEC, kTerms<T>>(item, w, hp, k0, min(a.I, k0 + a.chunk), (int64_t)a.T * a.k * a.I);
-        // only into the tokens that chose the expert: a zero fragment times an infinite weight is a NaN
+            float acc[1][NT][4] = {};
+            rows_mac<T, 1, NT, VEC, kTerms<T>>(acc, w, hp, k0, min(a.I, k0 + a.chunk), (int64_t)a.T * a.k * a.I);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (mask >> (j * 8 + 2 * (lane % 4) + (c & 1)) & 1) acc[j][c] += item[0][j][c];
-    }
-    put_partial(red + warp * NT * 8 * kPitch, acc);
-    __syncthreads();
-    constexpr int kMine = (NT * 8 * kRows + kThreads - 1) / kThreads;
-    float sum[kMine];
-#pragma unroll
-    for (int m = 0; m < kMine; ++m) {
-        const int i = threadIdx.x + m * kThreads;
-        sum[m] = 0.f;
-        if (i < NT * 8 * kRows)
-#pragma unroll
-            for (int q = 0; q < kWarps; ++q) sum[m] += red[(q * NT * 8 + i / kRows) * kPitch + i % kRows];
+                for (int c = 0; c < 4; ++c) {
+                    const int i = j * 8 + 2 * t4 + (c & 1);
+                    if (i < n) mine[entry[i] / kMaxK * kPitch + g + (c >> 1) * 8] += acc[0][j][c];
+                }
+        });
+        __syncwarp();   // another item's token may be another lane's
     }
     __syncthreads();
-    float* tot = red;    // [token][kRows], over the partial tiles
+    // the warps' sums into the first one's place, then the blocks' into the output
+    for (int i = threadIdx.x; i < a.T * kRows; i += kThreads) {
+        const int at = i / kRows * kPitch + i % kRows;
+        float v = smem[at];
 #pragma unroll
-    for (int m = 0; m < kMine; ++m)
-        if (threadIdx.x + m * kThreads < NT * 8 * kRows) tot[threadIdx.x + m * kThreads] = sum[m];
+        for (int q = 1; q < kWarps; ++q) v += smem[q * a.T * kPitch + at];
+        smem[at] = v;
+    }
     cluster_sync();
     for (int i = threadIdx.x * S + rank; i < a.T * kRows; i += kThreads * S) {
         const int t = i / kRows, r = row0 + i % kRows;
-        float v = 0.f;
-        for (int q = 0; q < S; ++q) v += cluster_ld(cluster_map(tot + i, q));
+        float v[kMaxSplit];
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q) v[q] = q < S ? cluster_ld(cluster_map(smem + t * kPitch + i % kRows, q)) : 0.f;
+#pragma unroll
+        for (int q = 1; q < kMaxSplit; ++q) v[0] += v[q];
         if (r < a.H) {
-            if (a.res) v += to_f32(((const T*)a.res)[t * a.ldr + r]);
-            ((T*)a.y)[t * a.ldy + r] = from_f32<T>(v);
+            if (a.res) v[0] += to_f32(((const T*)a.res)[t * a.ldr + r]);
+            ((T*)a.y)[t * a.ldy + r] = from_f32<T>(v[0]);
         }
     }
     cluster_sync();   // no block leaves while another reads its sums
@@ -389,7 +390,17 @@ dlrm_status launch_moe(MoeArgs a, cudaStream_t st)
     const int most = resident_blocks(up, smem);
     const int chosen = a.E < a.T * a.k ? a.E : a.T * a.k;            // experts at most
     const int64_t units = (int64_t)chosen * ((a.I + kRows - 1) / kRows);
-    a.group = units <= most ? 8 : 4;
+    // warps of a unit: as many as leave every group of warps one unit, else the
+    // number whose rounds of units cost least (a step of K against a unit's ten steps of overhead)
+    const int64_t steps = (a.H + kStep<T> - 1) / kStep<T>;
+    int64_t least = 0;
+    for (int G = kWarps; G >= 1; G /= 2) {
+        const int64_t groups = (int64_t)most * kWarps / G, cost = (units + groups - 1) / groups * ((steps + G - 1) / G + 10);
+        if (least == 0 || cost < least) {
+            least = cost;
+            a.group = G;
+        }
+    }
     int64_t blocks = (units * a.group + kWarps - 1) / kWarps;
     if (blocks > most) blocks = most;
     blocks = (blocks + kUpCluster - 1) / kUpCluster * kUpCluster;
@@ -398,21 +409,14 @@ dlrm_status launch_moe(MoeArgs a, cudaStream_t st)
     if (s != DLRM_OK) return s;
 
     const int row_tiles = (a.H + kRows - 1) / kRows;
-    int S = 8;
+    int S = kMaxSplit;
     while (S > 1 && row_tiles * S > 4 * num_sms()) S /= 2;
-    int64_t share = (int64_t)chosen * a.I / (S * kWarps * 2);        // two items a warp where there is that much
-    int chunk = (int)(share < 512 ? share : 512) / kStep<T> * kStep<T>;
+    const int64_t share = (int64_t)chosen * a.I / (S * kWarps * 2);   // two items a warp where there is that much
+    const int chunk = (int)(share < 2048 ? share : 2048) / kStep<T> * kStep<T>;
     a.chunk = chunk < kStep<T> ? kStep<T> : chunk;
-    auto go = [&](auto n) {
-        constexpr int NT = decltype(n)::value;
-        return check_launch_pdl(launch_cluster(moe_down_kernel<T, NT, VEC>, dim3(row_tiles * S), dim3(kThreads), 0, st,
-                                               S, a),
-                                "moe_down_kernel");
-    };
-    if (nt == 1) return go(std::integral_constant<int, 1>{});
-    if (nt == 2) return go(std::integral_constant<int, 2>{});
-    if (nt == 4) return go(std::integral_constant<int, 4>{});
-    return go(std::integral_constant<int, 8>{});
+    return check_launch_pdl(launch_cluster(moe_down_kernel<T, VEC>, dim3(row_tiles * S), dim3(kThreads),
+                                           (size_t)kWarps * a.T * kPitch * 4, st, S, a),
+                            "moe_down_kernel");
 }
 
 bool moe_sizes_ok(dlrm_dtype dtype, int T, int H, int I, int E, int k)
