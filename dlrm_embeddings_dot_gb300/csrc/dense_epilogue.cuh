@@ -25,17 +25,19 @@ inline int epilogue_vec(const Epilogue& e, int M, int es)
            (!e.pre || rows_aligned16(e.pre, e.ldp, M, es));
 }
 
-__device__ __forceinline__ void act8(float (&f)[8], int act)
+// a(.) of n values: one branch for all of them.
+template <int n>
+__device__ __forceinline__ void act_n(float (&f)[n], int act)
 {
     if (act == DLRM_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = act_f(f[i], DLRM_ACT_RELU);
+        for (int i = 0; i < n; ++i) f[i] = act_f(f[i], DLRM_ACT_RELU);
     } else if (act == DLRM_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = act_f(f[i], DLRM_ACT_GELU);
+        for (int i = 0; i < n; ++i) f[i] = act_f(f[i], DLRM_ACT_GELU);
     } else if (act == DLRM_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = act_f(f[i], DLRM_ACT_SILU);
+        for (int i = 0; i < n; ++i) f[i] = act_f(f[i], DLRM_ACT_SILU);
     }
 }
 
@@ -77,7 +79,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, const DropKey& key, i
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] += b[i];
     if (e.pre) store8<T, VEC>((T*)e.pre + row * e.ldp + col, n, f);
-    act8(f, e.act);
+    act_n(f, e.act);
     if (e.drop.thr) drop8(f, e.drop, key, (uint32_t)row, (uint32_t)col >> 3);
     if (e.res) {
         float g[8];

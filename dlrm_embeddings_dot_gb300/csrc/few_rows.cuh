@@ -116,7 +116,8 @@ template <typename T, int WT, int NT, bool VEC, int XP = 1>
 __device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* (&w)[WT][2], const T* (&x)[NT], int k0, int k1,
                                          int64_t xplane = 0)
 {
-    constexpr int U = WT == 1 ? 4 : 2;   // steps whose weight loads are issued together
+    // steps whose weight loads are issued together: what the registers beside the accumulators hold
+    constexpr int U = (NT == 8 ? 2 : 4) / WT;
     constexpr int kBlock = U * kStep<T>;
     const int t = (threadIdx.x % kWarp) % 4;
     if (k0 >= k1) return;

@@ -11,11 +11,12 @@
 //   warp 1      TMEM allocation and MMA issue (M = 128 or 256, N = BN, K = 16
 //               steps; the pair's leader issues for both blocks, whose tensor
 //               cores read both halves of B)
-//   warps 2..17 epilogue: TMEM lane quarter q = warp % 4, every fourth
-//               32-column slice.  A slice goes through 4 KB of shared memory,
-//               so that a lane then holds eight consecutive columns of a row:
-//               one Philox call, 16-byte loads and stores, and 64 contiguous
-//               bytes of a row for every four lanes
+//   warps 2..9  epilogue: TMEM lane quarter q = warp % 4, every second 64-column
+//               slice; a lane has 64 columns of a row, i.e. eight runs of the
+//               generator.  Results leave as boxes of 32 rows by 128 bytes by
+//               TMA stores from swizzled shared memory, and the residual comes
+//               in the same way.  A slice costs about @SLICE@ cycles of latencies
+//               (TMEM, barriers, fence, store) whatever its width, so it is wide
 // Two TMEM accumulators let the products of the next tile run under the
 // epilogue of this one.
 //
@@ -35,13 +36,13 @@ using namespace tc;
 
 constexpr int kBM = 128;            // output rows of a tile
 constexpr int kKB = 64;             // K elements of a stage (128-byte rows)
-constexpr int kEpiWarps = 16;
+constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
-constexpr int kSliceStep = kEpiWarps / 4 * 32;   // columns between a warp's slices
+constexpr int kSlice = 64;          // columns of an epilogue slice
+constexpr int kSliceStep = kEpiWarps / 4 * kSlice;
 constexpr int kMaxStages = 8;
 constexpr int kSmemLimit = 232448;  // 227 KB opt-in per block
-constexpr int kScratch = kEpiWarps * 32 * 128;
-constexpr int kMaxPairs = 6;
+constexpr int kBoxRows = 32, kBoxBytes = kBoxRows * 128;
 
 struct Args {
     int M, N;
@@ -49,6 +50,9 @@ struct Args {
     int pairs;                      // plane pairs: 1, or 6 for fp32
     int splits;                     // parts of K; above 1 the tiles go to `partial`
     int tiles_m, tiles_n, BN, NS;
+    int tma;                        // out, pre and residual take TMA boxes (rows start and end on the 16-byte grid)
+    int bias_vec;                   // the bias starts on a 16-byte boundary
+    int warp_bytes;                 // an epilogue warp's shared memory
     uint32_t idesc, tmem_cols;
     float* partial;                 // [splits][M][Np]
     int64_t Np;
@@ -64,15 +68,68 @@ __device__ __forceinline__ int plane_pair(int pairs, int p)
     return pairs == 1 ? 0 : (int)(order >> (4 * p)) & 15;
 }
 
-inline size_t smem_bytes(int b_rows, int ns)
+// A slice as boxes of 32 rows by 128 bytes (128-byte swizzle): one of a 2-byte
+// type, two of fp32.  An epilogue warp holds one slice of each tensor.
+template <typename T>
+constexpr int kBoxCols = 128 / (int)sizeof(T);
+template <typename T>
+constexpr int kSliceBytes = kSlice / kBoxCols<T> * kBoxBytes;
+
+inline size_t smem_bytes(int b_rows, int ns, int warp_bytes)
 {
-    return 1024 + (size_t)ns * (kBM * 128 + b_rows * 128) + kScratch + (size_t)(2 * ns + 4) * 8 + 16;
+    return 1024 + (size_t)ns * (kBM * 128 + b_rows * 128) + (size_t)kEpiWarps * warp_bytes +
+           (size_t)(2 * ns + 4 + kEpiWarps) * 8 + 16;
 }
 
-// The warp's 32 x 32 slice of the accumulator at taddr to rows of eight columns
-// a lane, then fn(row within the slice, f); loaded() once TMEM has been read.
-template <typename Loaded, typename Fn>
-__device__ __forceinline__ void transpose_slice(uint32_t taddr, uint8_t* scratch, Loaded&& loaded, Fn&& fn)
+// 16-byte chunk c of the lane's row of a slice.
+__device__ __forceinline__ uint4* slice_at(uint8_t* slice, int c)
+{
+    const int lane = threadIdx.x % kWarp;
+    return reinterpret_cast<uint4*>(slice + c / 8 * kBoxBytes + lane * 128 + (((c ^ lane) & 7) << 4));
+}
+
+// f += the lane's row of a slice
+template <typename T>
+__device__ __forceinline__ void add_slice_row(uint8_t* slice, float (&f)[kSlice])
+{
+#pragma unroll
+    for (int q = 0; q < kSlice / 8; ++q) {
+        Raw8<T> r;
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = *slice_at(slice, q * (int)(sizeof(T) / 2) + i);
+        float g[8];
+        widen8<T>(r, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[8 * q + i] += g[i];
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void write_slice_row(uint8_t* slice, const float (&f)[kSlice])
+{
+#pragma unroll
+    for (int c = 0; c < kSliceBytes<T> / kBoxBytes * 8; ++c) {
+        if constexpr (std::is_same_v<T, float>)
+            *slice_at(slice, c) = f4_as_u4(make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]));
+        else
+            *slice_at(slice, c) = pack8<T>(reinterpret_cast<const float(&)[8]>(f[8 * c]));
+    }
+}
+
+// K blocks [b0, b1) of part `split`.
+struct Range {
+    int b0, b1;
+};
+__device__ __forceinline__ Range k_range(const Args& a, int split)
+{
+    if (a.splits == 1) return {0, a.kb};   // a 64-bit division takes as long as a K block's products
+    return {(int)((int64_t)a.kb * split / a.splits), (int)((int64_t)a.kb * (split + 1) / a.splits)};
+}
+
+// The warp's 32 x 32 slice of the accumulator at taddr into its scratch, a row
+// as eight swizzled 16-byte chunks; loaded() once TMEM has been read.
+template <typename Loaded>
+__device__ __forceinline__ void stage_slice(uint32_t taddr, uint8_t* scratch, Loaded&& loaded)
 {
     const int lane = threadIdx.x % kWarp;
     uint32_t v[32];
@@ -85,13 +142,19 @@ __device__ __forceinline__ void transpose_slice(uint32_t taddr, uint8_t* scratch
             make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
     loaded();
     __syncwarp();
-#pragma unroll 1   // unrolled, four passes' registers are live at once and spill
-    for (int pass = 0; pass < 4; ++pass) {
-        const int r = pass * 8 + lane / 4, c = 2 * (lane % 4);
+}
+
+// Columns 8 (lane % 4) and on of rows lane / 4, lane / 4 + 8, ... of the staged slice.
+__device__ __forceinline__ void take_rows(const uint8_t* scratch, float (&f)[4][8])
+{
+    const int lane = threadIdx.x % kWarp, c = 2 * (lane % 4);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int r = p * 8 + lane / 4;
         const float4 lo = *reinterpret_cast<const float4*>(scratch + r * 128 + ((c ^ (r & 7)) << 4));
         const float4 hi = *reinterpret_cast<const float4*>(scratch + r * 128 + (((c + 1) ^ (r & 7)) << 4));
-        float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-        fn(r, f);
+        f[p][0] = lo.x, f[p][1] = lo.y, f[p][2] = lo.z, f[p][3] = lo.w;
+        f[p][4] = hi.x, f[p][5] = hi.y, f[p][6] = hi.z, f[p][7] = hi.w;
     }
 }
 
@@ -109,18 +172,7 @@ __device__ __forceinline__ void ragged_slice(const Epilogue& e, const DropKey& k
 #pragma unroll
         for (int p = 0; p < 4; ++p)
             keep |= keep8(e.drop, key, (uint32_t)(row0 + 8 * p + lane / 4), (uint32_t)c0 / 8 + lane % 4) << 8 * p;
-    {
-        uint32_t v[32];
-        tmem_ld_x32(taddr, v);
-        tmem_wait_ld(v);
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4*>(scratch + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-                make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-    }
-    loaded();
-    __syncwarp();
+    stage_slice(taddr, scratch, loaded);
     const bool in = col < N;
     const float bias = e.bias && in ? __ldg(e.bias + col) : 0.f;
     const int rows = min(32, M - row0);
@@ -144,7 +196,8 @@ __device__ __forceinline__ void ragged_slice(const Epilogue& e, const DropKey& k
 template <typename T, bool A_MN, bool B_MN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-            const __grid_constant__ Args a)
+            const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
+            const __grid_constant__ CUtensorMap map_res, const __grid_constant__ Args a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -153,11 +206,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     constexpr int a_bytes = kBM * 128;
     const int b_rows = BN / CG, stage_bytes = a_bytes + b_rows * 128;
     uint8_t* scratch = smem + (size_t)NS * stage_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kScratch);   // in a pair the leader's count both blocks' bytes
+    uint64_t* full = reinterpret_cast<uint64_t*>(scratch + kEpiWarps * a.warp_bytes);   // in a pair the leader's count both blocks' bytes
     uint64_t* empty = full + NS;
     uint64_t* tfull = empty + NS;
     uint64_t* tempty = tfull + 2;                                       // in a pair the leader's count both epilogues
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tempty + 2);
+    uint64_t* rfull = tempty + 2;                                       // an epilogue warp's residual slice
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(rfull + kEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
@@ -173,6 +227,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], CG * kEpiWarps);
         }
+        for (int i = 0; i < kEpiWarps; ++i) mbar_init(&rfull[i], 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -205,9 +260,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         uint32_t phase = 0;
         bool ok = true;
         for (int t = first; ok && t < tiles; t += stride) {
-            const int split = t / per_split, tt = t - split * per_split;
+            const int split = a.splits == 1 ? 0 : t / per_split, tt = t - split * per_split;
             const int m0 = (tt / a.tiles_n * CG + rank) * kBM, n0 = tt % a.tiles_n * BN + rank * b_rows;
-            const int b0 = (int)((int64_t)a.kb * split / a.splits), b1 = (int)((int64_t)a.kb * (split + 1) / a.splits);
+            const auto [b0, b1] = k_range(a, split);
             for (int p = 0; ok && p < a.pairs; ++p) {
                 const int pp = plane_pair(a.pairs, p), pa = pp >> 2, pb = pp & 3;
                 for (int kb = b0; kb < b1; ++kb) {
@@ -279,12 +334,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             uint32_t phase = 0;
             bool ok = true;
             for (int t = first; ok && t < tiles; t += stride, ++it) {
-                const int split = t / per_split;
-                const int b0 = (int)((int64_t)a.kb * split / a.splits), b1 = (int)((int64_t)a.kb * (split + 1) / a.splits);
+                const int split = a.splits == 1 ? 0 : t / per_split;
+                const auto [b0, b1] = k_range(a, split);
                 const int buf = it & 1;
                 ok = __all_sync(~0u, mbar_wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.wait_cycles));
                 if (!ok) break;
-                if constexpr (PAIR) asm volatile("fence.acq_rel.cluster;" ::: "memory");
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(buf * BN);
                 uint32_t accumulate = 0;
@@ -330,18 +384,32 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     } else {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3, part = (warp - 2) / 4;
-        uint8_t* mine = scratch + (warp - 2) * (32 * 128);
+        uint8_t* mine = scratch + (warp - 2) * a.warp_bytes;   // a slice of out, of pre, of the residual
+        uint8_t* pre_slice = mine + kSliceBytes<T>;
+        uint8_t* res_slice = pre_slice + (a.e.pre ? kSliceBytes<T> : 0);
+        uint64_t* rbar = rfull + (warp - 2);
         const DropKey key = drop_key(a.e.drop);
+        const bool boxes = a.splits == 1 && a.tma;             // leaves by TMA
         int it = 0;
+        uint32_t asked = 0, used = 0;                          // residual slices asked for, and added
         for (int t = first; t < tiles; t += stride, ++it) {
             const int buf = it & 1;
-            if (!mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, a.wait_cycles)) break;
-            __syncwarp();
-            tc_fence_after();
-            const int split = t / per_split, tt = t - split * per_split;
+            const int split = a.splits == 1 ? 0 : t / per_split, tt = t - split * per_split;
             const int row0 = (tt / a.tiles_n * CG + rank) * kBM + 32 * quarter, n0 = tt % a.tiles_n * BN;
             const uint32_t taddr = tmem_base + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(buf * BN);
-            const int cols = min(BN, a.N - n0);
+            const int cols = row0 < a.M ? min(BN, a.N - n0) : 0;   // none of the warp's rows may lie inside
+            auto ask = [&](int c0) {   // the residual's slice at c0, ahead of its use
+                if (lane == 0) {
+                    const int most = min(kSlice, a.N - n0 - c0), n = (most + kBoxCols<T> - 1) / kBoxCols<T>;
+                    mbar_expect_tx(rbar, (uint32_t)(n * kBoxBytes));
+                    for (int i = 0; i < n; ++i)
+                        tma_load_2d(res_slice + i * kBoxBytes, &map_res, n0 + c0 + i * kBoxCols<T>, row0, rbar);
+                }
+                ++asked;
+            };
+            if (boxes && a.e.res && kSlice * part < cols) ask(kSlice * part);
+            if (!__all_sync(~0u, mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, a.wait_cycles))) break;
+            tc_fence_after();
             auto release = [&] {   // the accumulator has been read: the tile after next may overwrite it
                 tc_fence_before();
                 __syncwarp();
@@ -350,43 +418,101 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     else mbar_arrive(&tempty[buf]);
                 }
             };
-            if (32 * part >= cols) release();
-            for (int c0 = 32 * part; c0 < cols; c0 += kSliceStep) {
-                const int col = n0 + c0 + 8 * (lane % 4), n = a.N - col;
-                auto loaded = [&] {
-                    if (c0 + kSliceStep >= cols) release();
-                };
-                if (a.splits > 1) {
-                    transpose_slice(taddr + c0, mine, loaded, [&](int r, float (&f)[8]) {
-                        const int row = row0 + r;
-                        if (row < a.M && n > 0) {
-                            float4* p = reinterpret_cast<float4*>(a.partial + ((int64_t)split * a.M + row) * a.Np + col);
-                            p[0] = make_float4(f[0], f[1], f[2], f[3]);
-                            p[1] = make_float4(f[4], f[5], f[6], f[7]);
-                        }
-                    });
-                } else {
-                    if (a.e.vec && n0 + c0 + 32 <= a.N) {
-                        float b[8];
-                        bias8(a.e.bias, col, a.N, b);
-                        Raw8<T> res[4];
-                        if (a.e.res) {
+            if (kSlice * part >= cols) {
+                release();
+                continue;
+            }
+            bool ok = true;
+            for (int c0 = kSlice * part; c0 < cols; c0 += kSliceStep) {
+                const bool last = c0 + kSliceStep >= cols;
+                if (boxes) {
+                    float f[kSlice];
+                    {
+                        uint32_t v[32], u[32];
+                        tmem_ld_x32(taddr + c0, v);
+                        tmem_ld_x32(taddr + c0 + 32, u);
+                        tmem_wait_ld2(v, u);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int row = row0 + i * 8 + lane / 4;
-                                if (row < a.M) res[i] = load8<T, true>((const T*)a.e.res + row * a.e.ldr + col, 8);
-                            }
+                        for (int i = 0; i < 32; ++i) {
+                            f[i] = __uint_as_float(v[i]);
+                            f[32 + i] = __uint_as_float(u[i]);
                         }
-                        transpose_slice(taddr + c0, mine, loaded, [&](int r, float (&f)[8]) {
-                            if (row0 + r < a.M) finish8<T, true>(a.e, key, row0 + r, col, 8, f, b, res[0]);
-                            res[0] = res[1], res[1] = res[2], res[2] = res[3];
-                        });
-                    } else {
-                        ragged_slice<T>(a.e, key, taddr + c0, mine, row0, a.M, n0 + c0, a.N, loaded);
+                    }
+                    if (last) release();
+                    if (lane == 0) bulk_wait_read<0>();   // the previous slice's stores have read theirs
+                    if (a.e.bias) {                        // the same columns for every lane
+                        const float* bias = a.e.bias + n0 + c0;
+                        if (a.bias_vec && c0 + kSlice <= cols) {
+#pragma unroll
+                            for (int i = 0; i < kSlice / 4; ++i) {
+                                const float4 b = __ldg(reinterpret_cast<const float4*>(bias) + i);
+                                f[4 * i] += b.x, f[4 * i + 1] += b.y, f[4 * i + 2] += b.z, f[4 * i + 3] += b.w;
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kSlice; ++i) f[i] += c0 + i < cols ? __ldg(bias + i) : 0.f;
+                        }
+                    }
+                    __syncwarp();
+                    if (a.e.pre) write_slice_row<T>(pre_slice, f);
+                    act_n(f, a.e.act);
+                    if (a.e.drop.thr)
+#pragma unroll
+                        for (int q = 0; q < kSlice / 8; ++q)
+                            drop8(reinterpret_cast<float(&)[8]>(f[8 * q]), a.e.drop, key, (uint32_t)(row0 + lane),
+                                  (uint32_t)(n0 + c0) / 8 + q);
+                    if (a.e.res) {
+                        ok = __all_sync(~0u, mbar_wait(rbar, used & 1u, abort_flag, a.wait_cycles));
+                        if (!ok) break;
+                        ++used;
+                        add_slice_row<T>(res_slice, f);
+                        __syncwarp();
+                        if (!last) ask(c0 + kSliceStep);
+                    }
+                    write_slice_row<T>(mine, f);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {   // rows and columns past the tensor are clipped
+#pragma unroll
+                        for (int i = 0; i < kSlice / kBoxCols<T>; ++i) {
+                            const int at = c0 + i * kBoxCols<T>;
+                            if (at >= cols) break;
+                            tma_store_2d(&map_out, n0 + at, row0, mine + i * kBoxBytes);
+                            if (a.e.pre) tma_store_2d(&map_pre, n0 + at, row0, pre_slice + i * kBoxBytes);
+                        }
+                        bulk_commit();
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c1 = c0; c1 < min(c0 + kSlice, cols); c1 += 32) {   // 32 columns at a time
+                        auto loaded = [&] {
+                            if (last && c1 + 32 >= min(c0 + kSlice, cols)) release();
+                        };
+                        if (a.splits > 1) {
+                            stage_slice(taddr + c1, mine, loaded);
+                            float f[4][8];
+                            take_rows(mine, f);
+                            const int row = row0 + lane / 4, col = n0 + c1 + 8 * (lane % 4);
+                            float4* p = reinterpret_cast<float4*>(a.partial + ((int64_t)split * a.M + row) * a.Np + col);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (row + 8 * i < a.M && col < a.N) {
+                                    p[2 * i * a.Np] = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+                                    p[2 * i * a.Np + 1] = make_float4(f[i][4], f[i][5], f[i][6], f[i][7]);
+                                }
+                        } else {
+                            ragged_slice<T>(a.e, key, taddr + c1, mine, row0, a.M, n0 + c1, a.N, loaded);
+                        }
                     }
                 }
             }
+            if (!ok) break;
         }
+        if (lane == 0) {
+            bulk_wait_all();   // the stores are complete, and a slice asked for has landed, before the block exits
+            if (used < asked) mbar_drain(rbar, used & 1u);
+        }
+        __syncwarp();
     }
 
     tc_fence_before();
@@ -505,6 +631,25 @@ inline dlrm_status make_map(const char* fn, CUtensorMap* m, const Operand& o, bo
     return DLRM_OK;
 }
 
+// A box map of an output or of the residual.
+template <typename T>
+dlrm_status make_box_map(const char* fn, CUtensorMap* m, const void* p, int64_t ld, int M, int N)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return fail(DLRM_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", fn);
+    const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
+    const cuuint64_t str[1] = {(cuuint64_t)(M > 1 ? ld : padded(N)) * sizeof(T)};
+    const cuuint32_t box[2] = {kBoxCols<T>, kBoxRows}, ones[2] = {1, 1};
+    const CUtensorMapDataType type = std::is_same_v<T, float>    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : std::is_same_v<T, __half> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = enc(m, type, 2, const_cast<void*>(p), dims, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(DLRM_ERR_CUDA, "%s: tensor map (%d)", fn, (int)r);
+    return DLRM_OK;
+}
+
 // out = A B^T and the epilogue; T the type of the epilogue's tensors, bf
 // whether the operands are bf16 (fp16 otherwise).  partial: partial_bytes(s).
 template <typename T, bool A_MN, bool B_MN>
@@ -512,7 +657,7 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
                 float* partial, uint32_t* status, cudaStream_t st)
 {
     const Plan p = plan(s);
-    CUtensorMap ma, mb;
+    CUtensorMap ma, mb, mo = {}, mp = {}, mr = {};
     dlrm_status r = make_map(fn, &ma, A, bf, s.M, s.K, kBM);
     if (r == DLRM_OK) r = make_map(fn, &mb, B, bf, s.N, s.K, p.pair ? p.BN / 2 : p.BN);
     if (r != DLRM_OK) return r;
@@ -529,8 +674,19 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     if (tm * tn > INT32_MAX / 64) return fail(DLRM_ERR_UNSUPPORTED, "%s: %lld output tiles", fn, (long long)(tm * tn));
     a.tiles_m = (int)tm;
     a.tiles_n = (int)tn;
+    // a TMA store clips at 16 bytes: the last columns of another width would spill past N
+    a.tma = e.vec && s.N * (int64_t)sizeof(T) % 16 == 0;
+    a.bias_vec = aligned16(e.bias);
+    a.warp_bytes = kBoxBytes;   // a split's or a ragged slice's fp32 rows
+    if (p.splits == 1 && a.tma) {
+        a.warp_bytes = kSliceBytes<T> * (1 + (e.pre != nullptr) + (e.res != nullptr));
+        r = make_box_map<T>(fn, &mo, e.out, e.ldo, s.M, s.N);
+        if (r == DLRM_OK && e.pre) r = make_box_map<T>(fn, &mp, e.pre, e.ldp, s.M, s.N);
+        if (r == DLRM_OK && e.res) r = make_box_map<T>(fn, &mr, e.res, e.ldr, s.M, s.N);
+        if (r != DLRM_OK) return r;
+    }
     a.NS = kMaxStages;
-    while (smem_bytes(b_rows, a.NS) > (size_t)kSmemLimit) --a.NS;
+    while (smem_bytes(b_rows, a.NS, a.warp_bytes) > (size_t)kSmemLimit) --a.NS;
     a.idesc = idesc_f16(CG * kBM, p.BN) | (bf ? 1u << 7 | 1u << 10 : 0u) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
     a.tmem_cols = 2 * p.BN;
     a.partial = partial;
@@ -540,12 +696,12 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     a.wait_cycles = wait_limit_cycles();
     const int64_t tiles = tm * tn * p.splits, units = num_sms() / CG;
     const int grid = (int)(tiles < units ? tiles : units) * CG;
-    const size_t smem = smem_bytes(b_rows, a.NS);
+    const size_t smem = smem_bytes(b_rows, a.NS, a.warp_bytes);
     auto kern = p.pair ? gemm_kernel<T, A_MN, B_MN, true> : gemm_kernel<T, A_MN, B_MN, false>;
     cudaError_t ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (ce != cudaSuccess) return fail(DLRM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
-    r = check_launch_pdl(p.pair ? launch_cluster(kern, dim3(grid), dim3(kThreads), smem, st, 2, ma, mb, a)
-                                : launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, ma, mb, a),
+    r = check_launch_pdl(p.pair ? launch_cluster(kern, dim3(grid), dim3(kThreads), smem, st, 2, ma, mb, mo, mp, mr, a)
+                                : launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, ma, mb, mo, mp, mr, a),
                          "gemm_kernel");
     if (r != DLRM_OK || p.splits == 1) return r;
     const int64_t runs = a.Np / 8 * s.M, want = (runs + 255) / 256, most = (int64_t)num_sms() * 8;
