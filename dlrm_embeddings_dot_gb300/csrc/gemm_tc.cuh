@@ -11,12 +11,12 @@
 //   warp 1      TMEM allocation and MMA issue (M = 128 or 256, N = BN, K = 16
 //               steps; the pair's leader issues for both blocks, whose tensor
 //               cores read both halves of B)
-//   warps 2..9  epilogue: TMEM lane quarter q = warp % 4, every second 64-column
-//               slice; a lane has 64 columns of a row, i.e. eight runs of the
-//               generator.  Results leave as boxes of 32 rows by 128 bytes by
+//   warps 2..17 epilogue: TMEM lane quarter q = warp % 4, every fourth 32-column
+//               slice; a lane has 32 columns of a row, i.e. four runs of the
+//               generator.  Results leave as boxes of 32 rows and columns by
 //               TMA stores from swizzled shared memory, and the residual comes
-//               in the same way.  A slice costs about @SLICE@ cycles of latencies
-//               (TMEM, barriers, fence, store) whatever its width, so it is wide
+//               in the same way.  A slice is a chain of latencies (TMEM,
+//               barriers, fence, store), which is why there are many warps
 // Two TMEM accumulators let the products of the next tile run under the
 // epilogue of this one.
 //
@@ -36,13 +36,12 @@ using namespace tc;
 
 constexpr int kBM = 128;            // output rows of a tile
 constexpr int kKB = 64;             // K elements of a stage (128-byte rows)
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
-constexpr int kSlice = 64;          // columns of an epilogue slice
+constexpr int kSlice = 32;          // columns of an epilogue slice
 constexpr int kSliceStep = kEpiWarps / 4 * kSlice;
 constexpr int kMaxStages = 8;
 constexpr int kSmemLimit = 232448;  // 227 KB opt-in per block
-constexpr int kBoxRows = 32, kBoxBytes = kBoxRows * 128;
 
 struct Args {
     int M, N;
@@ -68,12 +67,11 @@ __device__ __forceinline__ int plane_pair(int pairs, int p)
     return pairs == 1 ? 0 : (int)(order >> (4 * p)) & 15;
 }
 
-// A slice as boxes of 32 rows by 128 bytes (128-byte swizzle): one of a 2-byte
-// type, two of fp32.  An epilogue warp holds one slice of each tensor.
+// A slice of 32 rows as a TMA box: rows of 64 bytes with the 64-byte swizzle
+// (2-byte types) or of 128 bytes with the 128-byte one (fp32).  An epilogue warp
+// holds one box of each tensor.
 template <typename T>
-constexpr int kBoxCols = 128 / (int)sizeof(T);
-template <typename T>
-constexpr int kSliceBytes = kSlice / kBoxCols<T> * kBoxBytes;
+constexpr int kBoxBytes = 32 * kSlice * (int)sizeof(T);
 
 inline size_t smem_bytes(int b_rows, int ns, int warp_bytes)
 {
@@ -81,22 +79,24 @@ inline size_t smem_bytes(int b_rows, int ns, int warp_bytes)
            (size_t)(2 * ns + 4 + kEpiWarps) * 8 + 16;
 }
 
-// 16-byte chunk c of the lane's row of a slice.
-__device__ __forceinline__ uint4* slice_at(uint8_t* slice, int c)
+// 16-byte chunk c of the lane's row of a box.
+template <typename T>
+__device__ __forceinline__ uint4* box_at(uint8_t* box, int c)
 {
     const int lane = threadIdx.x % kWarp;
-    return reinterpret_cast<uint4*>(slice + c / 8 * kBoxBytes + lane * 128 + (((c ^ lane) & 7) << 4));
+    const int at = sizeof(T) == 2 ? lane * 64 + ((c ^ (lane >> 1 & 3)) << 4) : lane * 128 + (((c ^ lane) & 7) << 4);
+    return reinterpret_cast<uint4*>(box + at);
 }
 
-// f += the lane's row of a slice
+// f += the lane's row of a box
 template <typename T>
-__device__ __forceinline__ void add_slice_row(uint8_t* slice, float (&f)[kSlice])
+__device__ __forceinline__ void add_box_row(uint8_t* box, float (&f)[kSlice])
 {
 #pragma unroll
     for (int q = 0; q < kSlice / 8; ++q) {
         Raw8<T> r;
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = *slice_at(slice, q * (int)(sizeof(T) / 2) + i);
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = *box_at<T>(box, q * (int)(sizeof(T) / 2) + i);
         float g[8];
         widen8<T>(r, g);
 #pragma unroll
@@ -105,14 +105,14 @@ __device__ __forceinline__ void add_slice_row(uint8_t* slice, float (&f)[kSlice]
 }
 
 template <typename T>
-__device__ __forceinline__ void write_slice_row(uint8_t* slice, const float (&f)[kSlice])
+__device__ __forceinline__ void write_box_row(uint8_t* box, const float (&f)[kSlice])
 {
 #pragma unroll
-    for (int c = 0; c < kSliceBytes<T> / kBoxBytes * 8; ++c) {
+    for (int c = 0; c < kSlice * (int)sizeof(T) / 16; ++c) {
         if constexpr (std::is_same_v<T, float>)
-            *slice_at(slice, c) = f4_as_u4(make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]));
+            *box_at<T>(box, c) = f4_as_u4(make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]));
         else
-            *slice_at(slice, c) = pack8<T>(reinterpret_cast<const float(&)[8]>(f[8 * c]));
+            *box_at<T>(box, c) = pack8<T>(reinterpret_cast<const float(&)[8]>(f[8 * c]));
     }
 }
 
@@ -330,41 +330,38 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const uint64_t ad0 = A_MN ? sw128_desc_mn(sa, 8192, 1024) : sw128_desc(sa);
             const uint64_t bd0 = B_MN ? sw128_desc_mn(sb, 8192, 1024) : sw128_desc(sb);
             constexpr uint32_t da = A_MN ? 2048 / 16 : 32 / 16, db = B_MN ? 2048 / 16 : 32 / 16;
+            // A wait that gives up raises the abort flag, after which every wait returns
+            // at once: the flag is looked at once a tile, and until then products of
+            // whatever the ring holds are harmless.
             int stage = 0, it = 0;
             uint32_t phase = 0;
-            bool ok = true;
-            for (int t = first; ok && t < tiles; t += stride, ++it) {
-                const int split = a.splits == 1 ? 0 : t / per_split;
-                const auto [b0, b1] = k_range(a, split);
+            for (int t = first; t < tiles; t += stride, ++it) {
+                const auto [b0, b1] = k_range(a, a.splits == 1 ? 0 : t / per_split);
                 const int buf = it & 1;
-                ok = __all_sync(~0u, mbar_wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.wait_cycles));
-                if (!ok) break;
+                mbar_wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.wait_cycles);
+                if (__any_sync(~0u, *abort_flag != 0)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)(buf * BN);
                 uint32_t accumulate = 0;
-                for (int p = 0; ok && p < a.pairs; ++p) {
+                for (int p = 0; p < a.pairs; ++p) {
                     for (int kb = b0; kb < b1; ++kb) {
-                        ok = __all_sync(~0u, mbar_wait(&full[stage], phase, abort_flag, a.wait_cycles));
-                        if (!ok) break;
+                        mbar_wait(&full[stage], phase, abort_flag, a.wait_cycles);
+                        __syncwarp();
                         tc_fence_after();
                         const uint64_t ad = ad0 + (uint32_t)(stage * (stage_bytes / 16));
                         const uint64_t bd = bd0 + (uint32_t)(stage * (stage_bytes / 16));
-                        if (kb != a.kb - 1 || a.last_steps == 4) {
-                            if (elect_one()) {
+                        if (elect_one()) {
+                            if (kb != a.kb - 1 || a.last_steps == 4) {
                                 mma(d, ad, bd, accumulate);
                                 mma(d, ad + da, bd + db, 1);
                                 mma(d, ad + 2 * da, bd + 2 * db, 1);
                                 mma(d, ad + 3 * da, bd + 3 * db, 1);
-                                commit(&empty[stage]);
-                            }
-                        } else {   // the rest of K holds zeros past last_steps
-                            if (elect_one()) {
+                            } else {   // the rest of K holds zeros past last_steps
                                 for (int kk = 0; kk < a.last_steps; ++kk)
                                     mma(d, ad + kk * da, bd + kk * db, kk ? 1 : accumulate);
-                                commit(&empty[stage]);
                             }
+                            commit(&empty[stage]);
                         }
-                        __syncwarp();
                         accumulate = 1;
                         if (++stage == NS) {
                             stage = 0;
@@ -372,7 +369,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         }
                     }
                 }
-                if (ok && elect_one()) commit(&tfull[buf]);
+                __syncwarp();
+                if (elect_one()) commit(&tfull[buf]);
                 __syncwarp();
             }
             // MMAs already issued must finish before TMEM is freed
@@ -384,9 +382,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     } else {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3, part = (warp - 2) / 4;
-        uint8_t* mine = scratch + (warp - 2) * a.warp_bytes;   // a slice of out, of pre, of the residual
-        uint8_t* pre_slice = mine + kSliceBytes<T>;
-        uint8_t* res_slice = pre_slice + (a.e.pre ? kSliceBytes<T> : 0);
+        uint8_t* mine = scratch + (warp - 2) * a.warp_bytes;   // a box of out, of pre, of the residual
+        uint8_t* pre_box = mine + kBoxBytes<T>;
+        uint8_t* res_box = pre_box + (a.e.pre ? kBoxBytes<T> : 0);
         uint64_t* rbar = rfull + (warp - 2);
         const DropKey key = drop_key(a.e.drop);
         const bool boxes = a.splits == 1 && a.tma;             // leaves by TMA
@@ -400,10 +398,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const int cols = row0 < a.M ? min(BN, a.N - n0) : 0;   // none of the warp's rows may lie inside
             auto ask = [&](int c0) {   // the residual's slice at c0, ahead of its use
                 if (lane == 0) {
-                    const int most = min(kSlice, a.N - n0 - c0), n = (most + kBoxCols<T> - 1) / kBoxCols<T>;
-                    mbar_expect_tx(rbar, (uint32_t)(n * kBoxBytes));
-                    for (int i = 0; i < n; ++i)
-                        tma_load_2d(res_slice + i * kBoxBytes, &map_res, n0 + c0 + i * kBoxCols<T>, row0, rbar);
+                    mbar_expect_tx(rbar, kBoxBytes<T>);
+                    tma_load_2d(res_box, &map_res, n0 + c0, row0, rbar);
                 }
                 ++asked;
             };
@@ -428,15 +424,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 if (boxes) {
                     float f[kSlice];
                     {
-                        uint32_t v[32], u[32];
+                        uint32_t v[32];
                         tmem_ld_x32(taddr + c0, v);
-                        tmem_ld_x32(taddr + c0 + 32, u);
-                        tmem_wait_ld2(v, u);
+                        tmem_wait_ld(v);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            f[i] = __uint_as_float(v[i]);
-                            f[32 + i] = __uint_as_float(u[i]);
-                        }
+                        for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
                     }
                     if (last) release();
                     if (lane == 0) bulk_wait_read<0>();   // the previous slice's stores have read theirs
@@ -454,7 +446,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         }
                     }
                     __syncwarp();
-                    if (a.e.pre) write_slice_row<T>(pre_slice, f);
+                    if (a.e.pre) write_box_row<T>(pre_box, f);
                     act_n(f, a.e.act);
                     if (a.e.drop.thr)
 #pragma unroll
@@ -465,44 +457,36 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         ok = __all_sync(~0u, mbar_wait(rbar, used & 1u, abort_flag, a.wait_cycles));
                         if (!ok) break;
                         ++used;
-                        add_slice_row<T>(res_slice, f);
+                        add_box_row<T>(res_box, f);
                         __syncwarp();
                         if (!last) ask(c0 + kSliceStep);
                     }
-                    write_slice_row<T>(mine, f);
+                    write_box_row<T>(mine, f);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {   // rows and columns past the tensor are clipped
-#pragma unroll
-                        for (int i = 0; i < kSlice / kBoxCols<T>; ++i) {
-                            const int at = c0 + i * kBoxCols<T>;
-                            if (at >= cols) break;
-                            tma_store_2d(&map_out, n0 + at, row0, mine + i * kBoxBytes);
-                            if (a.e.pre) tma_store_2d(&map_pre, n0 + at, row0, pre_slice + i * kBoxBytes);
-                        }
+                        tma_store_2d(&map_out, n0 + c0, row0, mine);
+                        if (a.e.pre) tma_store_2d(&map_pre, n0 + c0, row0, pre_box);
                         bulk_commit();
                     }
                 } else {
-#pragma unroll 1
-                    for (int c1 = c0; c1 < min(c0 + kSlice, cols); c1 += 32) {   // 32 columns at a time
-                        auto loaded = [&] {
-                            if (last && c1 + 32 >= min(c0 + kSlice, cols)) release();
-                        };
-                        if (a.splits > 1) {
-                            stage_slice(taddr + c1, mine, loaded);
-                            float f[4][8];
-                            take_rows(mine, f);
-                            const int row = row0 + lane / 4, col = n0 + c1 + 8 * (lane % 4);
-                            float4* p = reinterpret_cast<float4*>(a.partial + ((int64_t)split * a.M + row) * a.Np + col);
+                    auto loaded = [&] {
+                        if (last) release();
+                    };
+                    if (a.splits > 1) {
+                        stage_slice(taddr + c0, mine, loaded);
+                        float f[4][8];
+                        take_rows(mine, f);
+                        const int row = row0 + lane / 4, col = n0 + c0 + 8 * (lane % 4);
+                        float4* p = reinterpret_cast<float4*>(a.partial + ((int64_t)split * a.M + row) * a.Np + col);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (row + 8 * i < a.M && col < a.N) {
-                                    p[2 * i * a.Np] = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
-                                    p[2 * i * a.Np + 1] = make_float4(f[i][4], f[i][5], f[i][6], f[i][7]);
-                                }
-                        } else {
-                            ragged_slice<T>(a.e, key, taddr + c1, mine, row0, a.M, n0 + c1, a.N, loaded);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            if (row + 8 * i < a.M && col < a.N) {
+                                p[2 * i * a.Np] = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+                                p[2 * i * a.Np + 1] = make_float4(f[i][4], f[i][5], f[i][6], f[i][7]);
+                            }
+                    } else {
+                        ragged_slice<T>(a.e, key, taddr + c0, mine, row0, a.M, n0 + c0, a.N, loaded);
                     }
                 }
             }
@@ -639,12 +623,12 @@ dlrm_status make_box_map(const char* fn, CUtensorMap* m, const void* p, int64_t 
     if (!enc) return fail(DLRM_ERR_CUDA, "%s: cuTensorMapEncodeTiled unavailable", fn);
     const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
     const cuuint64_t str[1] = {(cuuint64_t)(M > 1 ? ld : padded(N)) * sizeof(T)};
-    const cuuint32_t box[2] = {kBoxCols<T>, kBoxRows}, ones[2] = {1, 1};
+    const cuuint32_t box[2] = {kSlice, 32}, ones[2] = {1, 1};
     const CUtensorMapDataType type = std::is_same_v<T, float>    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : std::is_same_v<T, __half> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                                  : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUresult r = enc(m, type, 2, const_cast<void*>(p), dims, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B,
+                           sizeof(T) == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(DLRM_ERR_CUDA, "%s: tensor map (%d)", fn, (int)r);
     return DLRM_OK;
@@ -677,9 +661,9 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     // a TMA store clips at 16 bytes: the last columns of another width would spill past N
     a.tma = e.vec && s.N * (int64_t)sizeof(T) % 16 == 0;
     a.bias_vec = aligned16(e.bias);
-    a.warp_bytes = kBoxBytes;   // a split's or a ragged slice's fp32 rows
+    a.warp_bytes = 32 * 128;   // a split's or a ragged slice's fp32 rows
     if (p.splits == 1 && a.tma) {
-        a.warp_bytes = kSliceBytes<T> * (1 + (e.pre != nullptr) + (e.res != nullptr));
+        a.warp_bytes = kBoxBytes<T> * (1 + (e.pre != nullptr) + (e.res != nullptr));
         r = make_box_map<T>(fn, &mo, e.out, e.ldo, s.M, s.N);
         if (r == DLRM_OK && e.pre) r = make_box_map<T>(fn, &mp, e.pre, e.ldp, s.M, s.N);
         if (r == DLRM_OK && e.res) r = make_box_map<T>(fn, &mr, e.res, e.ldr, s.M, s.N);
