@@ -2,16 +2,19 @@
 // where the weights are the traffic: every weight goes from HBM straight into
 // the registers of one warp as a matrix fragment.
 //
-// A warp multiplies WT tiles of 16 weight rows with NT tiles of 8 tokens over a
-// range of K (mma.sync m16n8k16: at these shapes the tensor pipe idles, and
-// unlike tcgen05 it takes both operands from registers, so nothing passes
-// through shared memory).  The order of K inside a step is free as long as both
-// operands use the same one: lane (g, t) = (lane / 4, lane % 4) takes the
-// 16 consecutive bytes at 16 t of rows g and g + 8 and of token g, so every
-// load is 16 bytes wide and four lanes cover 64 contiguous bytes of a row.
-//   2-byte types: 8 values, the fragments of two k16 steps (32 of K)
-//   fp32: 4 values, each split into three bf16 parts (8 + 8 + 8 bits); six
-//   products of the parts, the smallest first, give the fp32 product (16 of K)
+// A warp multiplies WT tiles of 16 weight rows with tokens over a range of K.
+// The order of K inside a step is free as long as both sides use the same one:
+// lane (g, t) = (lane / 4, lane % 4) takes the 32 consecutive bytes at 32 t of
+// rows g and g + 8 and of its token, so a load is up to 32 bytes wide and four
+// lanes cover 128 contiguous bytes of a row (with 16-byte loads L1's tag stage
+// alone held the weights to half of HBM's rate).
+//   2-byte types: 16 values, the fragments of four mma.sync m16n8k16 (64 of K)
+//     against NT tiles of 8 tokens.  At these shapes the tensor pipe idles, and
+//     unlike tcgen05 it takes both operands from registers
+//   fp32, up to 8 tokens: 8 values (32 of K), multiplied and added in fp32;
+//     the four lanes of a row add up their shares at the end
+//   fp32, more tokens: the same values as three bf16 parts each (8 + 8 + 8
+//     bits), whose six products, the smallest first, give the fp32 product
 #pragma once
 
 #include "dense_ops.cuh"
@@ -21,11 +24,11 @@ namespace few {
 
 constexpr int kRows = 16;         // weight rows of a tile
 constexpr int kMaxTokens = 64;
-constexpr int kPitch = 20;        // floats between tokens of a partial tile in shared memory: the fragment
-                                  // stores of a warp (tokens 2t, rows g) then hit 32 different banks
+constexpr int kPitch = 20;         // floats between tokens of a partial tile in shared memory: the fragment
+                                   // stores of a warp (tokens 2t, rows g) then hit 32 different banks
 
 template <typename T>
-constexpr int kLane = 16 / (int)sizeof(T);   // values of K a lane loads at once
+constexpr int kLane = 32 / (int)sizeof(T);   // values of K a lane loads at once
 template <typename T>
 constexpr int kStep = 4 * kLane<T>;          // values of K a warp covers at once
 
@@ -43,26 +46,46 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The lane's 16 bytes of a row: values [0, n) of the kLane at p, zeros behind.
-template <typename T, bool VEC>
-__device__ __forceinline__ uint4 load_part(const T* p, int n)
+struct Chunk {
+    uint4 v[2];
+};
+
+// The lane's 32 bytes of a row: values [0, n) of the kLane at p, zeros behind.
+template <typename T>
+__device__ __forceinline__ Chunk load_part(const T* p, int n)
 {
-    if (VEC && n >= kLane<T>) return ldg_nc_l1_v4(p);
     T e[kLane<T>];
 #pragma unroll
     for (int i = 0; i < kLane<T>; ++i) e[i] = i < n ? __ldg(p + i) : from_f32<T>(0.f);
-    uint4 v;
-    memcpy(&v, e, 16);
-    return v;
+    Chunk c;
+    memcpy(&c, e, 32);
+    return c;
 }
 
-// All kLane values.  KEEP: allocate in L1 (tokens, read by every warp); weights
-// pass through once.
-template <typename T, bool VEC, bool KEEP>
-__device__ __forceinline__ uint4 load_lane(const T* p)
+// All kLane values; VEC: 2 on the 32-byte grid, 1 on the 16-byte grid, 0 off it.
+// KEEP: allocate in L1 (tokens, read by every warp); weights pass through once.
+template <typename T, int VEC, bool KEEP>
+__device__ __forceinline__ Chunk load_lane(const T* p)
 {
-    if constexpr (!VEC) return load_part<T, false>(p, kLane<T>);
-    else return KEEP ? ldg_nc_l1_v4(p) : ldg_nc_v4(p);
+    Chunk c;
+    if constexpr (VEC == 2 && !KEEP) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(c.v[0].x), "=r"(c.v[0].y), "=r"(c.v[0].z), "=r"(c.v[0].w), "=r"(c.v[1].x), "=r"(c.v[1].y),
+                       "=r"(c.v[1].z), "=r"(c.v[1].w)
+                     : "l"(p));
+    } else if constexpr (VEC == 2) {
+        asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(c.v[0].x), "=r"(c.v[0].y), "=r"(c.v[0].z), "=r"(c.v[0].w), "=r"(c.v[1].x), "=r"(c.v[1].y),
+                       "=r"(c.v[1].z), "=r"(c.v[1].w)
+                     : "l"(p));
+    } else if constexpr (VEC == 1) {
+        const uint4* q = reinterpret_cast<const uint4*>(p);
+        c.v[0] = KEEP ? ldg_nc_l1_v4(q) : ldg_nc_v4(q);
+        c.v[1] = KEEP ? ldg_nc_l1_v4(q + 1) : ldg_nc_v4(q + 1);
+    } else {
+        c = load_part<T>(p, kLane<T>);
+    }
+    return c;
 }
 
 // Three bf16 parts of each of four floats (split1), two values to a word.
@@ -88,9 +111,9 @@ __device__ __forceinline__ Parts split4(uint4 v)
     return p;
 }
 
-// acc += the 16 rows (lane's bytes a of row g, b of row g + 8) times 8 tokens (x of token g).
+// acc += the 16 rows (lane's bytes a of row g, b of row g + 8) times 8 tokens (x of token g), 16 bytes each.
 template <typename T>
-__device__ __forceinline__ void mac(float (&acc)[4], uint4 a, uint4 b, uint4 x)
+__device__ __forceinline__ void mac16(float (&acc)[4], uint4 a, uint4 b, uint4 x)
 {
     if constexpr (std::is_same_v<T, float>) {
         const Parts p = split4(a), q = split4(b), y = split4(x);
@@ -106,19 +129,36 @@ __device__ __forceinline__ void mac(float (&acc)[4], uint4 a, uint4 b, uint4 x)
     }
 }
 
-// acc[i][j] += tile i of 16 weight rows times tile j of 8 tokens over [k0, k1) of K
-// (k0 a multiple of kStep).  w[i][0] / w[i][1]: rows g and g + 8 of tile i;
-// x[j]: token g of tile j.  Every pointer is a readable row: where a tile has no
-// such row or token any other does, as rows and tokens meet only in results
-// that the caller then leaves alone.  XP: terms each token is the sum of, term i
-// at x[j] + i * xplane.
-template <typename T, int WT, int NT, bool VEC, int XP = 1>
-__device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* (&w)[WT][2], const T* (&x)[NT], int k0, int k1,
-                                         int64_t xplane = 0)
+template <typename T>
+__device__ __forceinline__ void mac(float (&acc)[4], const Chunk& a, const Chunk& b, const Chunk& x)
 {
-    // steps whose weight loads are issued together: what the registers beside the accumulators hold
-    constexpr int U = (NT == 8 ? 2 : 4) / WT;
-    constexpr int kBlock = U * kStep<T>;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) mac16<T>(acc, a.v[h], b.v[h], x.v[h]);
+}
+
+// s += the eight products of two chunks of floats
+__device__ __forceinline__ void dot8(float& s, const Chunk& a, const Chunk& x)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 u = u4_as_f4(a.v[h]), v = u4_as_f4(x.v[h]);
+        s = fmaf(u.x, v.x, s);
+        s = fmaf(u.y, v.y, s);
+        s = fmaf(u.z, v.z, s);
+        s = fmaf(u.w, v.w, s);
+    }
+}
+
+// Visits [k0, k1) of K (k0 a multiple of kStep) for WT tiles of 16 weight rows and
+// NX tokens of this lane: mul(i, j, a, b, x) gets the lane's chunks of rows g and
+// g + 8 of tile i and of its token j.  w[i][0] / w[i][1]: rows g and g + 8 of tile
+// i.  Every pointer is a readable row: where a tile has no such row or token any
+// other does, as rows and tokens meet only in results that the caller then leaves
+// alone.  XP: terms each token is the sum of, term q at x[j] + q * xplane.
+template <typename T, int WT, int NX, int VEC, int XP, int U, bool AHEAD, typename Mul>
+__device__ __forceinline__ void visit_k(const T* (&w)[WT][2], const T* (&x)[NX], int k0, int k1, int64_t xplane, Mul&& mul)
+{
+    constexpr int kBlock = U * kStep<T>;   // K whose weight loads are issued together
     const int t = (threadIdx.x % kWarp) % 4;
     if (k0 >= k1) return;
 #pragma unroll
@@ -127,9 +167,9 @@ __device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* (&w)[
         w[i][1] += k0 + t * kLane<T>;
     }
 #pragma unroll
-    for (int j = 0; j < NT; ++j) x[j] += k0 + t * kLane<T>;
+    for (int j = 0; j < NX; ++j) x[j] += k0 + t * kLane<T>;
     int left = k1 - k0;
-    auto load = [&](uint4 (&a)[U][WT][2], int at) {
+    auto load = [&](Chunk (&a)[U][WT][2], int at) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -137,16 +177,16 @@ __device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* (&w)[
 #pragma unroll
                 for (int h = 0; h < 2; ++h) a[u][i][h] = load_lane<T, VEC, false>(w[i][h] + at + u * kStep<T>);
     };
-    auto multiply = [&](const uint4 (&a)[U][WT][2], int at) {
+    auto multiply = [&](const Chunk (&a)[U][WT][2], int at) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NX; ++j)
 #pragma unroll
                 for (int q = 0; q < XP; ++q) {
-                    const uint4 b = load_lane<T, VEC, true>(x[j] + q * xplane + at + u * kStep<T>);
+                    const Chunk b = load_lane<T, VEC, true>(x[j] + q * xplane + at + u * kStep<T>);
 #pragma unroll
-                    for (int i = 0; i < WT; ++i) mac<T>(acc[i][j], a[u][i][0], a[u][i][1], b);
+                    for (int i = 0; i < WT; ++i) mul(i, j, a[u][i][0], a[u][i][1], b);
                 }
     };
     auto advance = [&](int by) {
@@ -156,11 +196,11 @@ __device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* (&w)[
             w[i][1] += by;
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) x[j] += by;
+        for (int j = 0; j < NX; ++j) x[j] += by;
         left -= by;
     };
-    if constexpr (NT <= 2 && VEC) {   // the next block's weights are on their way while one is multiplied
-        uint4 a[U][WT][2], b[U][WT][2];
+    if constexpr (AHEAD && VEC > 0) {   // the next block's weights are on their way while one is multiplied
+        Chunk a[U][WT][2], b[U][WT][2];
         if (left >= kBlock) load(a, 0);
 #pragma unroll 1
         while (left >= 2 * kBlock) {
@@ -177,7 +217,7 @@ __device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* (&w)[
     } else {
 #pragma unroll 1
         while (left >= kBlock) {
-            uint4 a[U][WT][2];
+            Chunk a[U][WT][2];
             load(a, 0);
             multiply(a, 0);
             advance(kBlock);
@@ -186,36 +226,102 @@ __device__ __forceinline__ void rows_mac(float (&acc)[WT][NT][4], const T* (&w)[
 #pragma unroll 1
     while (left > 0) {   // the last steps, one at a time; past K both sides are zero
         const int n = left - t * kLane<T>;
-        uint4 a[WT][2];
+        Chunk a[WT][2];
+        if (VEC > 0 && left >= kStep<T>) {
 #pragma unroll
-        for (int i = 0; i < WT; ++i)
+            for (int i = 0; i < WT; ++i)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) a[i][h] = load_part<T, VEC>(w[i][h], n);
+                for (int h = 0; h < 2; ++h) a[i][h] = load_lane<T, VEC, false>(w[i][h]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+            for (int j = 0; j < NX; ++j)
 #pragma unroll
-            for (int q = 0; q < XP; ++q) {
-                const uint4 b = load_part<T, VEC>(x[j] + q * xplane, n);
+                for (int q = 0; q < XP; ++q) {
+                    const Chunk b = load_lane<T, VEC, true>(x[j] + q * xplane);
 #pragma unroll
-                for (int i = 0; i < WT; ++i) mac<T>(acc[i][j], a[i][0], a[i][1], b);
-            }
+                    for (int i = 0; i < WT; ++i) mul(i, j, a[i][0], a[i][1], b);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < WT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) a[i][h] = load_part<T>(w[i][h], n);
+#pragma unroll
+            for (int j = 0; j < NX; ++j)
+#pragma unroll
+                for (int q = 0; q < XP; ++q) {
+                    const Chunk b = load_part<T>(x[j] + q * xplane, n);
+#pragma unroll
+                    for (int i = 0; i < WT; ++i) mul(i, j, a[i][0], a[i][1], b);
+                }
+        }
         advance(kStep<T>);
     }
 }
 
-// The warp's partial tile to shared memory: part[token * kPitch + row].
-template <int NT>
-__device__ __forceinline__ void put_partial(float* part, const float (&acc)[NT][4])
+// out(i, token, row, value) for every sum of the warp's WT tiles of 16 weight rows
+// (pointers as for visit_k) with tokens [0, n), n <= 8 NT, over [k0, k1) of K.
+// token(j) gives the row of token j (j < n).
+template <typename T, int WT, int NT, int VEC, int XP = 1, typename Token, typename Out>
+__device__ __forceinline__ void rows_times_tokens(const T* (&w)[WT][2], Token&& token, int n, int k0, int k1,
+                                                  int64_t xplane, Out&& out)
 {
     const int lane = threadIdx.x % kWarp, g = lane / 4, t = lane % 4;
+    if constexpr (std::is_same_v<T, float> && NT == 1) {
+        // every lane has all the tokens, for its share of K
+        auto with = [&](auto nn) {
+            constexpr int NX = decltype(nn)::value;
+            const T* x[NX];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        float* p = part + (j * 8 + 2 * t) * kPitch + g;
-        p[0] = acc[j][0];
-        p[kPitch] = acc[j][1];
-        p[8] = acc[j][2];
-        p[kPitch + 8] = acc[j][3];
+            for (int j = 0; j < NX; ++j) x[j] = token(min(j, n - 1));
+            float acc[WT][NX][2] = {};
+            visit_k<T, WT, NX, VEC, XP, 2 / WT, (NX <= 2)>(w, x, k0, k1, xplane,
+                                                            [&](int i, int j, const Chunk& a, const Chunk& b, const Chunk& c) {
+                                                                dot8(acc[i][j][0], a, c);
+                                                                dot8(acc[i][j][1], b, c);
+                                                            });
+#pragma unroll
+            for (int i = 0; i < WT; ++i)
+#pragma unroll
+                for (int j = 0; j < NX; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v = acc[i][j][h];
+                        v += __shfl_xor_sync(~0u, v, 1);
+                        v += __shfl_xor_sync(~0u, v, 2);
+                        if (t == 0 && j < n) out(i, j, g + 8 * h, v);
+                    }
+        };
+        if (n == 1) with(std::integral_constant<int, 1>{});
+        else if (n == 2) with(std::integral_constant<int, 2>{});
+        else if (n <= 4) with(std::integral_constant<int, 4>{});
+        else with(std::integral_constant<int, 8>{});
+    } else {
+        const T* x[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) x[j] = token(min(j * 8 + g, n - 1));
+        float acc[WT][NT][4] = {};
+        constexpr int U = WT == 1 && NT < 8 ? 2 : 1;
+        visit_k<T, WT, NT, VEC, XP, U, (NT == 1)>(w, x, k0, k1, xplane,
+                                                  [&](int i, int j, const Chunk& a, const Chunk& b, const Chunk& c) {
+                                                      mac<T>(acc[i][j], a, b, c);
+                                                  });
+#pragma unroll
+        for (int i = 0; i < WT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int tok = j * 8 + 2 * t + (c & 1);
+                    if (tok < n) out(i, tok, g + 8 * (c >> 1), acc[i][j][c]);
+                }
     }
+}
+
+// 2, 1 or 0: whether rows of `width` elements lie on the 32-byte grid, on the 16-byte grid, or off both.
+inline int row_grid(const void* p, int64_t ld, int rows, int es)
+{
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0 && (rows <= 1 || ld * es % 32 == 0)) return 2;
+    return rows_aligned16(p, ld, rows, es) ? 1 : 0;
 }
 
 // Calls fn(std::integral_constant<int, NT>) with the least NT of 1, 2, 4, 8 that covers n tokens.

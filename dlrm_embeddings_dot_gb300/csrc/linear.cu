@@ -104,7 +104,7 @@ size_t operand_bytes(int rows, int cols, dlrm_dtype dt)
 // --------------------------------------------------------------- few rows
 // The forward of up to 64 rows: a cluster owns 16 output columns (weight rows),
 // its warps share out K, and their partial tiles are added in a fixed order.
-template <typename T, int NT, bool VEC>
+template <typename T, int NT, int VEC>
 __global__ void __launch_bounds__(256, 2)
 linear_few_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ w, int64_t ldw, int M, int N, int K,
                   const __grid_constant__ Epilogue e)
@@ -122,12 +122,10 @@ linear_few_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ w,
         const T* wp[1][2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) wp[0][b] = w + min(row0 + g + 8 * b, N - 1) * ldw;
-        const T* xp[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) xp[j] = x + min(j * 8 + g, M - 1) * ldx;
-        float acc[1][NT][4] = {};
-        rows_mac<T, 1, NT, VEC>(acc, wp, xp, part * per, min(K, (part + 1) * per));
-        put_partial(red + warp * NT * 8 * kPitch, acc[0]);
+        float* mine = red + warp * NT * 8 * kPitch;
+        rows_times_tokens<T, 1, NT, VEC>(
+            wp, [&](int t) { return x + t * ldx; }, M, part * per, min(K, (part + 1) * per), 0,
+            [&](int, int t, int r, float v) { mine[t * kPitch + r] = v; });
     }
     __syncthreads();
     constexpr int kMine = (NT * 8 * kRows + 255) / 256;
@@ -136,7 +134,7 @@ linear_few_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ w,
     for (int m = 0; m < kMine; ++m) {
         const int i = threadIdx.x + m * 256;
         sum[m] = 0.f;
-        if (i < NT * 8 * kRows)
+        if (i < M * kRows)
 #pragma unroll
             for (int q = 0; q < kWarps; ++q) sum[m] += red[(q * NT * 8 + i / kRows) * kPitch + i % kRows];
     }
@@ -168,13 +166,13 @@ dlrm_status launch_few(const void* x, int64_t ldx, const void* w, int64_t ldw, i
                        cudaStream_t st)
 {
     const int row_tiles = (N + few::kRows - 1) / few::kRows, steps = (K + few::kStep<T> - 1) / few::kStep<T>;
-    // a cluster splits K further while blocks are few and every warp keeps four steps
+    // a cluster splits K further while blocks are few and every warp keeps two steps
     int S = 1;
-    while (S < 8 && row_tiles * S < num_sms() && steps >= S * 8 * 8) S *= 2;
-    const bool vec = rows_aligned16(x, ldx, M, sizeof(T)) && rows_aligned16(w, ldw, N, sizeof(T));
+    while (S < 8 && row_tiles * S < num_sms() && steps >= S * 8 * 4) S *= 2;
+    const int gx = few::row_grid(x, ldx, M, sizeof(T)), gw = few::row_grid(w, ldw, N, sizeof(T)), grid = gx < gw ? gx : gw;
     auto go = [&](auto n) {
         constexpr int NT = decltype(n)::value;
-        auto kern = vec ? linear_few_kernel<T, NT, true> : linear_few_kernel<T, NT, false>;
+        auto kern = grid == 2 ? linear_few_kernel<T, NT, 2> : grid == 1 ? linear_few_kernel<T, NT, 1> : linear_few_kernel<T, NT, 0>;
         return check_launch_pdl(launch_cluster(kern, dim3((unsigned)row_tiles * S), dim3(256), 0, st, S,
                                                     (const T*)x, ldx, (const T*)w, ldw, M, N, K, e),
                                 "linear_few_kernel");

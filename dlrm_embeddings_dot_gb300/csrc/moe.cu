@@ -1,25 +1,33 @@
 // moe.cu -- a mixture-of-experts layer for a few tokens in two kernels.
 //
-// Bound by the touched experts' weights, each read once from HBM into matrix
-// fragments (few_rows.cuh).
+// Bound by the touched experts' weights, each read once from HBM.  A weight goes
+// by TMA into shared memory and from there into the fragments of one warp: each
+// of 8 warps has a ring of two stages of 8 KB that it asks for itself, on into its
+// next units, so that 128 KB an SM are on the way without a register (weights
+// loaded straight into registers, two blocks of 8 warps with 128 of them, reached
+// 3.2 TB/s).  A box is 16 rows by 256 or 512 bytes (TMA takes rows at a fixed
+// rate: rows of 64 bytes brought 3.2 TB/s at most); lane (g, t) = (lane / 4,
+// lane % 4) reads chunk t of row g of a 64-byte step, a two-way bank conflict that
+// is hidden behind HBM, and takes the same 16 bytes of its token.
 //
-//   moe_up    routing and the first product.  Every cluster of eight blocks
-//             computes the router's logits for itself (each block an eighth
+//   moe_up    routing and the first product.  Every cluster of four blocks
+//             computes the router's logits for itself (each block a quarter
 //             of H, the partial sums exchanged through distributed shared
 //             memory), so no block waits for another cluster; each block
 //             then picks the top k, lists the tokens of each chosen expert and
 //             takes its share of the (expert, 16 rows) units.  A unit's K is
 //             split over G warps, whose partial tiles meet in shared memory;
-//             probs * a(.) goes to the workspace in the tensors' type.
+//             probs * a(.) goes to the workspace.
 //   moe_down  a cluster owns 16 rows of the output: its warps share out the
 //             (expert, run of I) items of all chosen experts, each warp adding
-//             all its items into one set of accumulators (an absent token's
-//             fragment is zero), and the warps' and blocks' sums are added in a
-//             fixed order.  No atomics on floats, no partial outputs in HBM.
+//             its items into its own per-token sums in shared memory, and the
+//             warps' and blocks' sums are added in a fixed order.  No atomics on
+//             floats, no partial outputs in HBM.
 #include <map>
 #include <mutex>
 
 #include "few_rows.cuh"
+#include "tcgen05.cuh"
 
 namespace dlrm {
 namespace {
@@ -27,8 +35,25 @@ namespace {
 using namespace few;
 
 constexpr int kThreads = 256, kWarps = kThreads / kWarp;
-constexpr int kUpCluster = 8, kMaxSplit = 8;   // blocks of a cluster in moe_up, at most in moe_down
+constexpr int kUpCluster = 4, kMaxSplit = 8;   // blocks of a cluster in moe_up, at most in moe_down
+constexpr int64_t kOwnRouter = 32 << 10;
 constexpr int kMaxE = DLRM_MOE_MAX_EXPERTS, kMaxK = DLRM_MOE_MAX_TOP_K;
+constexpr int kGroup = 32;                     // tokens of an expert that are multiplied together
+constexpr int kMaxGroups = kMaxTokens * kMaxK / kGroup + kMaxE;
+constexpr int kStages = 2, kSteps = 8, kStage = kSteps * 1024;   // a step: 16 rows by 64 bytes
+constexpr int kRing = kWarps * kStages * kStage;
+
+template <typename T>
+constexpr int kQ = 16 / (int)sizeof(T);        // values of a lane's chunk
+template <typename T>
+constexpr int kStepK = 4 * kQ<T>;              // K of a step
+
+// probs * h enters the second product as the sum of two values of a 2-byte type
+// (the rounded value and the rounded rest): the product of the weights with a
+// second fragment is free beside the weights' traffic, and y then has one
+// rounding, its own.
+template <typename T>
+constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
 
 struct MoeArgs {
     const void *x, *wr, *w1, *w2, *res;
@@ -39,38 +64,46 @@ struct MoeArgs {
     int32_t* ids;
     float* probs;
     void* h;                                // [kTerms][T][k][I]
+    uint32_t* status;
+    long long wait_cycles;
 };
-
-// probs * h enters the second product as the sum of two values of a 2-byte type
-// (the rounded value and the rounded rest): the product of the weights with a
-// second fragment is free beside the weights' traffic, and y then has one
-// rounding, its own.
-template <typename T>
-constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
 
 // Which tokens chose which expert, in shared memory.
 struct Lists {
     unsigned long long mask[kMaxE];        // bit t: token t chose the expert
     uint16_t entry[kMaxTokens * kMaxK];    // per expert, its tokens ascending: token * kMaxK + slot
     uint16_t first[kMaxE];                 // an expert's first entry
-    uint16_t active[kMaxE];                // the chosen experts, ascending
+    uint16_t active[kMaxGroups];           // the chosen experts, ascending: expert + kMaxE * (group of tokens)
     int n_active;
 };
 
-// Builds the lists from id(t, j) (all threads of the block).
+// One entry of `active`.
+struct Choice {
+    int e, n;                // the expert, and how many tokens
+    const uint16_t* entry;   // theirs
+};
+
+__device__ __forceinline__ Choice choice(const Lists& l, int i)
+{
+    const int e = l.active[i] % kMaxE, grp = l.active[i] / kMaxE;
+    return {e, min(kGroup, __popcll(l.mask[e]) - grp * kGroup), l.entry + l.first[e] + grp * kGroup};
+}
+
+// Builds the lists from id(t, j) (all threads of the block; the masks are zero).
+// The last entries are in place after the caller's next __syncthreads.
 template <typename Id>
 __device__ __forceinline__ void build_lists(Lists& l, int T, int k, int E, Id&& id)
 {
-    for (int e = threadIdx.x; e < E; e += kThreads) l.mask[e] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < T * k; i += kThreads) atomicOr(&l.mask[id(i / k, i % k)], 1ull << (i / k));
+    for (int i = threadIdx.x; i < T * kMaxK; i += kThreads)
+        if (i % kMaxK < k) atomicOr(&l.mask[id(i / kMaxK, i % kMaxK)], 1ull << (i / kMaxK));
     __syncthreads();
     if (threadIdx.x < kWarp) {
-        const int lane = threadIdx.x;
+        const int lane = threadIdx.x, per = (E + kWarp - 1) / kWarp, e0 = lane * per, e1 = min(E, e0 + per);
         int n = 0, used = 0;
-        for (int e = lane * 8; e < min(E, lane * 8 + 8); ++e) {
-            n += __popcll(l.mask[e]);
-            used += l.mask[e] != 0;
+        for (int e = e0; e < e1; ++e) {
+            const int c = __popcll(l.mask[e]);
+            n += c;
+            used += (c + kGroup - 1) / kGroup;
         }
         int n0 = n, u0 = used;
 #pragma unroll
@@ -84,18 +117,20 @@ __device__ __forceinline__ void build_lists(Lists& l, int T, int k, int E, Id&& 
         if (lane == kWarp - 1) l.n_active = u0;
         n0 -= n;
         u0 -= used;
-        for (int e = lane * 8; e < min(E, lane * 8 + 8); ++e) {
+        for (int e = e0; e < e1; ++e) {
+            const int c = __popcll(l.mask[e]);
             l.first[e] = (uint16_t)n0;
-            if (l.mask[e]) l.active[u0++] = (uint16_t)e;
-            n0 += __popcll(l.mask[e]);
+            for (int grp = 0; grp * kGroup < c; ++grp) l.active[u0++] = (uint16_t)(e + kMaxE * grp);
+            n0 += c;
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < T * k; i += kThreads) {
-        const int t = i / k, j = i % k, e = id(t, j);
+    for (int i = threadIdx.x; i < T * kMaxK; i += kThreads) {
+        const int t = i / kMaxK, j = i % kMaxK;
+        if (j >= k) continue;
+        const int e = id(t, j);
         l.entry[l.first[e] + __popcll(l.mask[e] & ((1ull << t) - 1))] = (uint16_t)(t * kMaxK + j);
     }
-    __syncthreads();
 }
 
 // Order of the logits as integers: NaN above all, -0 equal to 0.
@@ -111,92 +146,321 @@ __device__ __forceinline__ void group_sync(int id, int threads)
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeArgs a)
+struct Rings {
+    uint64_t full[kWarps * kStages];
+    int abort_flag;
+};
+
+// Sets up the barriers; the caller synchronises.
+__device__ __forceinline__ void init_rings(Rings& r)
 {
-    pdl_wait();
-    extern __shared__ float smem[];
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps * kStages; ++i) tc::mbar_init(&r.full[i], 1);
+        r.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+}
+
+// What a warp asks for: of items first, first + stride, ... below `items`, K from
+// k0(item) to k1(item) of the WT tiles of 16 rows at row(item) and tile_rows
+// further; a stage holds WT boxes of 16 rows by 512 / WT bytes.
+template <typename T, int WT, typename Row, typename K0, typename K1>
+struct Ring {
+    const CUtensorMap* map;
+    uint8_t* mem;
+    uint64_t* full;
+    volatile int* abort_flag;
+    long long wait_cycles;
+    int item, stride, items, tile_rows;
+    Row row;
+    K0 k0;
+    K1 k1;
+    int k, end, at;
+    uint32_t asked, taken;
+
+    __device__ __forceinline__ void start()
+    {
+        asked = taken = 0;
+        if (item < items) enter();
+        for (int i = 0; i < kStages; ++i) ask();
+    }
+    __device__ __forceinline__ void enter()
+    {
+        k = k0(item);
+        end = k1(item);
+        at = row(item);
+        if (k >= end) items = 0;   // the warp's share of K is empty
+    }
+    __device__ __forceinline__ void ask()
+    {
+        if (item >= items) return;
+        const uint32_t s = asked++ % kStages;
+        if (threadIdx.x % kWarp == 0) {
+            tc::mbar_expect_tx(&full[s], kStage);
+#pragma unroll
+            for (int i = 0; i < WT; ++i)
+                tc::tma_load_2d(mem + s * kStage + i * (kStage / WT), map, k, at + i * tile_rows, &full[s]);
+        }
+        k += kSteps / WT * kStepK<T>;
+        if (k >= end) {
+            item += stride;
+            if (item < items) enter();
+        }
+    }
+    __device__ __forceinline__ const uint8_t* take()
+    {
+        const uint32_t s = taken % kStages;
+        tc::mbar_wait(&full[s], (taken / kStages) & 1u, abort_flag, wait_cycles);
+        __syncwarp();
+        return mem + s * kStage;
+    }
+    // The taken stage has been read: ask for another in its place.
+    __device__ __forceinline__ void give_back()
+    {
+        __syncwarp();
+        ++taken;
+        ask();
+    }
+    // Reports a wait that gave up; every copy has then landed (or was waited for).
+    __device__ __forceinline__ void finish(uint32_t* status)
+    {
+        if (threadIdx.x % kWarp == 0 && *abort_flag) {
+            for (uint32_t i = asked > kStages ? asked - kStages : 0; i < asked; ++i)
+                tc::mbar_drain(&full[i % kStages], (i / kStages) & 1u);
+            set_status(status, DLRM_STATUS_TIMEOUT);
+        }
+        __syncwarp();
+    }
+};
+
+template <typename T, int WT, typename Row, typename K0, typename K1>
+__device__ __forceinline__ Ring<T, WT, Row, K0, K1> make_ring(Rings& r, uint8_t* rings, const CUtensorMap* map,
+                                                              long long wait_cycles, int first, int stride, int items,
+                                                              int tile_rows, Row row, K0 k0, K1 k1)
+{
+    const int warp = threadIdx.x / kWarp;
+    return {map,  rings + warp * kStages * kStage, r.full + warp * kStages, &r.abort_flag, wait_cycles, first, stride, items,
+            tile_rows, row, k0, k1, 0, 0, 0, 0, 0};
+}
+
+__device__ __forceinline__ uint8_t* aligned128(uint8_t* p)
+{
+    return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 127) & ~(uintptr_t)127);
+}
+
+__device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// The sums of WT tiles of 16 weight rows with tokens [0, n) over [k0, k1) of K
+// (k0 a multiple of a stage's), the weights taken from the ring stage by stage.
+// out(i, token, row, value) gets every sum (zero for an empty range).  token(j):
+// the row of token j; its values past K are not read, and the boxes hold zeros
+// there.
+template <typename T, int WT, int XP, typename R, typename Token, typename Out>
+__device__ __forceinline__ void ring_times_tokens(R& ring, Token&& token, int n, int k0, int k1, int K, int64_t xplane,
+                                                  Out&& out)
+{
+    constexpr int ST = kSteps / WT, kRow = ST * 64;   // steps in a stage, bytes of a row in a box
+    const int lane = threadIdx.x % kWarp, g = lane / 4, t = lane % 4;
+    // mul(x, w): the products of one step of each tile (row g at w) with the tokens'
+    // chunks x[N]; at(j): where token chunk j begins.  The chunks of the next D
+    // steps are on their way while one step is multiplied; no more than D steps are
+    // unrolled, because a block runs this code for a few units only and has to
+    // fetch every instruction of it.
+    auto run = [&](auto nn, auto&& at, auto&& mul) {
+        constexpr int N = decltype(nn)::value, D = N <= 2 ? 4 : 2;
+        const T* x[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = at(j) + k0 + t * kQ<T>;
+        int left = K - k0 - t * kQ<T>;   // of the token's row, from this step's chunk on
+        uint4 b[D][N];
+        auto fetch = [&](uint4 (&c)[N], int ahead) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                c[j] = left > ahead * kStepK<T> ? ldg_nc_l1_v4(x[j] + ahead * kStepK<T>) : make_uint4(0, 0, 0, 0);
+        };
+#pragma unroll
+        for (int d = 0; d < D; ++d) fetch(b[d], d);
+        const uint8_t* w = nullptr;
+        int in = 0;   // steps left in the stage
+#pragma unroll 1
+        for (int k = k0; k < k1; k += D * kStepK<T>) {
+            if (in == 0) {
+                w = ring.take() + g * kRow + t * 16;
+                in = ST;
+            }
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                mul(b[d], w + d * 64);
+                fetch(b[d], D + d);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[j] += D * kStepK<T>;
+            left -= D * kStepK<T>;
+            w += D * 64;
+            in -= D;
+            if (in == 0 || k + D * kStepK<T> >= k1) {
+                in = 0;
+                ring.give_back();
+            }
+        }
+    };
+    if (std::is_same_v<T, float> && n <= 8) {
+        // fp32, few tokens: fp32 products; a lane has all the tokens for its share of K
+        auto with = [&](auto nn) {
+            constexpr int NX = decltype(nn)::value;
+            float acc[WT][NX][2] = {};
+            run(nn, [&](int j) { return token(min(j, n - 1)); },
+                [&](const uint4 (&x)[NX], const uint8_t* w) {
+#pragma unroll
+                    for (int i = 0; i < WT; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 a = u4_as_f4(lds16(w + i * (kStage / WT) + h * (8 * kRow)));
+#pragma unroll
+                            for (int j = 0; j < NX; ++j) {
+                                const float4 v = u4_as_f4(x[j]);
+                                float& d = acc[i][j][h];
+                                d = fmaf(a.x, v.x, d);
+                                d = fmaf(a.y, v.y, d);
+                                d = fmaf(a.z, v.z, d);
+                                d = fmaf(a.w, v.w, d);
+                            }
+                        }
+                });
+#pragma unroll
+            for (int i = 0; i < WT; ++i)
+#pragma unroll
+                for (int j = 0; j < NX; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v = acc[i][j][h];   // the four lanes of a row add up their shares
+                        v += __shfl_xor_sync(~0u, v, 1);
+                        v += __shfl_xor_sync(~0u, v, 2);
+                        if (t == 0 && j < n) out(i, j, g + 8 * h, v);
+                    }
+        };
+        if (n <= 2) with(std::integral_constant<int, 2>{});
+        else if (n <= 4) with(std::integral_constant<int, 4>{});
+        else with(std::integral_constant<int, 8>{});
+    } else {
+        auto with = [&](auto nn) {
+            constexpr int NT = decltype(nn)::value;
+            float acc[WT][NT][4] = {};
+            run(std::integral_constant<int, NT * XP>{},
+                [&](int j) { return token(min(j / XP * 8 + g, n - 1)) + j % XP * xplane; },
+                [&](const uint4 (&x)[NT * XP], const uint8_t* w) {
+#pragma unroll
+                    for (int i = 0; i < WT; ++i) {
+                        const uint4 lo = lds16(w + i * (kStage / WT)), hi = lds16(w + i * (kStage / WT) + 8 * kRow);
+#pragma unroll
+                        for (int j = 0; j < NT * XP; ++j) mac16<T>(acc[i][j / XP], lo, hi, x[j]);
+                    }
+                });
+#pragma unroll
+            for (int i = 0; i < WT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int tok = j * 8 + 2 * t + (d & 1);
+                        if (tok < n) out(i, tok, g + 8 * (d >> 1), acc[i][j][d]);
+                    }
+        };
+        if (n <= 8) with(std::integral_constant<int, 1>{});
+        else if (n <= 16) with(std::integral_constant<int, 2>{});
+        else with(std::integral_constant<int, 4>{});
+    }
+}
+
+// Dynamic shared memory of moe_up: the rings, which the logits use first (they fit:
+// 2 x 64 x 256 floats at most), then the partial tiles.  Without rings the
+// partial tiles are over the logits.
+inline size_t up_bytes(int T, int E, int nt, bool rings)
+{
+    const int e_tiles = (E + kRows - 1) / kRows, sub = e_tiles < kWarps ? kWarps / e_tiles : 1;
+    const size_t logits = (size_t)(sub + 1) * T * e_tiles * kRows * 4, red = (size_t)kWarps * 2 * nt * 8 * kPitch * 4;
+    return rings ? kRing + red + 128 : logits > red ? logits : red;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_constant__ CUtensorMap map, MoeArgs a)
+{
+    extern __shared__ uint8_t raw[];
+    uint8_t* rings = aligned128(raw);
+    float* smem = reinterpret_cast<float*>(rings);
     __shared__ Lists lists;
     __shared__ uint8_t ids_s[kMaxTokens * kMaxK];
+    __shared__ uint32_t keys_s[kWarps][kMaxE];
     __shared__ float probs_s[kMaxTokens * kMaxK];
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4, t4 = lane % 4;
+    __shared__ Rings sync;
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4;
     const T *x = (const T*)a.x, *wr = (const T*)a.wr, *w1 = (const T*)a.w1;
+    init_rings(sync);
+    for (int e = threadIdx.x; e < a.E; e += kThreads) lists.mask[e] = 0;
+    pdl_wait();
 
-    // ---- the router's logits: this block's eighth of H
+    // ---- the router's logits: this block's share of H
     const int e_tiles = (a.E + kRows - 1) / kRows, E16 = e_tiles * kRows;
     const int sub = e_tiles < kWarps ? kWarps / e_tiles : 1;     // warps that split an expert tile's K
-    const uint32_t rank = cluster_rank();
+    const int C = (int)cluster_size(), rank = (int)cluster_rank();
     float* lp = smem;                        // [sub][T][E16]: partial logits
     float* lg = smem + sub * a.T * E16;      // [T][E16]: logits
     {
         const int steps = (a.H + kStep<T> - 1) / kStep<T>;
-        const int per = (steps + kUpCluster * sub - 1) / (kUpCluster * sub) * kStep<T>;
+        const int per = (steps + C * sub - 1) / (C * sub) * kStep<T>;
         for (int i = warp; i < e_tiles * sub; i += kWarps) {
             const int tile = i % e_tiles, s = i / e_tiles;
-            const int k0 = ((int)rank * sub + s) * per, k1 = min(a.H, k0 + per);
+            const int k0 = (rank * sub + s) * per, k1 = min(a.H, k0 + per);
             const int e0 = tile * kRows + g;
-            const T* w[1][2] = {{wr + (int64_t)min(e0, a.E - 1) * a.H, wr + (int64_t)min(e0 + 8, a.E - 1) * a.H}};
-            with_token_tiles(a.T, [&](auto nt) {
-                constexpr int NT = decltype(nt)::value;
-                const T* xp[NT];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) xp[j] = x + min(j * 8 + g, a.T - 1) * a.ldx;
-                float acc[1][NT][4] = {};
-                rows_mac<T, 1, NT, VEC>(acc, w, xp, k0, k1);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int tok = j * 8 + 2 * t4 + (c & 1);
-                        if (tok < a.T) lp[(s * a.T + tok) * E16 + tile * kRows + g + (c >> 1) * 8] = acc[0][j][c];
-                    }
-            });
-        }
-        if (sub > 1) {   // the block's own sums first: what is read across the cluster is read once
-            __syncthreads();
-            for (int i = threadIdx.x; i < a.T * E16; i += kThreads) {
-                float v = lp[i];
-                for (int s = 1; s < sub; ++s) v += lp[s * a.T * E16 + i];
-                lp[i] = v;
+            for (int t0 = 0; t0 < a.T; t0 += kGroup) {
+                const T* w[1][2] = {{wr + (int64_t)min(e0, a.E - 1) * a.H, wr + (int64_t)min(e0 + 8, a.E - 1) * a.H}};
+                with_token_tiles(min(kGroup, a.T - t0), [&](auto nt) {
+                    rows_times_tokens<T, 1, decltype(nt)::value, VEC ? 1 : 0>(
+                        w, [&](int t) { return x + (t0 + t) * a.ldx; }, min(kGroup, a.T - t0), k0, k1, 0,
+                        [&](int, int t, int r, float v) { lp[(s * a.T + t0 + t) * E16 + tile * kRows + r] = v; });
+                });
             }
         }
-        cluster_sync();
-        // block r adds up every eighth logit and hands it to all
-        for (int i = threadIdx.x * kUpCluster + rank; i < a.T * E16; i += kThreads * kUpCluster) {
-            float v[kUpCluster];
-#pragma unroll
-            for (int r = 0; r < kUpCluster; ++r) v[r] = cluster_ld(cluster_map(lp + i, r));
-#pragma unroll
-            for (int r = 1; r < kUpCluster; ++r) v[0] += v[r];
-#pragma unroll
-            for (int r = 0; r < kUpCluster; ++r) cluster_st(cluster_map(lg + i, r), v[0]);
+        __syncthreads();
+        float* own = C > 1 ? lp : lg;   // the block's own sums first: what is read across the cluster is read once
+        for (int i = threadIdx.x; i < a.T * E16; i += kThreads) {
+            float v = lp[i];
+            for (int s = 1; s < sub; ++s) v += lp[s * a.T * E16 + i];
+            own[i] = v;
         }
-        cluster_sync();
+        if (C > 1) {
+            cluster_sync();
+            // block r adds up every C-th logit and hands it to all
+            for (int i = threadIdx.x * C + rank; i < a.T * E16; i += kThreads * C) {
+                float v[kUpCluster];
+#pragma unroll
+                for (int r = 0; r < kUpCluster; ++r) v[r] = cluster_ld(cluster_map(lp + i, r));
+#pragma unroll
+                for (int r = 1; r < kUpCluster; ++r) v[0] += v[r];
+#pragma unroll
+                for (int r = 0; r < kUpCluster; ++r) cluster_st(cluster_map(lg + i, r), v[0]);
+            }
+            cluster_sync();
+        } else {
+            __syncthreads();
+        }
     }
 
     // ---- top k and its softmax, a warp per token
+    uint32_t* keys = keys_s[warp];
     for (int t = warp; t < a.T; t += kWarps) {
-        unsigned long long key[kMaxE / kWarp];
-#pragma unroll
-        for (int i = 0; i < kMaxE / kWarp; ++i) {
-            const int e = i * kWarp + lane;
-            key[i] = e < a.E ? (unsigned long long)logit_key(lg[t * E16 + e]) << 32 | (uint32_t)(kMaxE - e) : 0;
-        }
+        for (int e = lane; e < a.E; e += kWarp) keys[e] = logit_key(lg[t * E16 + e]);
         float top = 0.f, mine = 0.f;
         int best = 0;
+#pragma unroll 1
         for (int j = 0; j < a.k; ++j) {
-            unsigned long long m = 0;
-#pragma unroll
-            for (int i = 0; i < kMaxE / kWarp; ++i) m = key[i] > m ? key[i] : m;
-#pragma unroll
-            for (int d = 16; d; d /= 2) {
-                const unsigned long long o = __shfl_xor_sync(~0u, m, d);
-                m = o > m ? o : m;
-            }
-            const int e = kMaxE - (int)(uint32_t)m;
-#pragma unroll
-            for (int i = 0; i < kMaxE / kWarp; ++i)
-                if (key[i] == m) key[i] = 0;
+            uint32_t m = 0, at = kMaxE;    // a lane's largest key and its lowest expert (no logit's key is 0)
+#pragma unroll 1
+            for (int e = lane; e < a.E; e += kWarp)
+                if (keys[e] > m) m = keys[e], at = e;
+            const uint32_t most = __reduce_max_sync(~0u, m);
+            const int e = (int)__reduce_min_sync(~0u, m == most ? at : kMaxE);
+            if (e % kWarp == lane) keys[e] = 0;
             const float v = lg[t * E16 + e];
             if (j == 0) top = v;
             if (lane == j) {
@@ -221,44 +485,21 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeArgs a)
 
     // ---- the first product: units of 16 rows of one chosen expert, G warps each
     const int G = a.group, groups = kWarps / G, mine = warp / G, wg = warp % G;
-    const int tiles = (a.I + kRows - 1) / kRows, units = lists.n_active * tiles;
-    const int steps = (a.H + kStep<T> - 1) / kStep<T>, per = (steps + G - 1) / G * kStep<T>;
+    const int tiles = (a.I + kRows - 1) / kRows, units = lists.n_active * tiles, stride = gridDim.x * groups;
+    const int WT = a.gated ? 2 : 1, stage_k = kSteps / WT * kStepK<T>;
+    const int per = ((a.H + stage_k - 1) / stage_k + G - 1) / G * stage_k;
     const int k0 = wg * per, k1 = min(a.H, k0 + per);
-    const int nt_max = a.T <= 8 ? 1 : a.T <= 16 ? 2 : a.T <= 32 ? 4 : 8;
+    const int nt_max = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
     const int tile_floats = nt_max * 8 * kPitch;
-    float* red = smem;    // [warp][2][token][kPitch], over the logits
+    float* red = reinterpret_cast<float*>(rings + (VEC ? kRing : 0));   // [warp][2][token][kPitch]
     T* h = (T*)a.h;
-    for (int u = blockIdx.x * groups + mine; u < units; u += gridDim.x * groups) {
-        const int e = lists.active[u / tiles], row0 = u % tiles * kRows;
-        const int n = __popcll(lists.mask[e]);
-        const uint16_t* entry = lists.entry + lists.first[e];
-        const int64_t base = (int64_t)e * (a.gated ? 2 : 1) * a.I;
-        const T* w[2][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                w[i][b] = w1 + (base + (int64_t)(a.gated ? i : 0) * a.I + min(row0 + g + 8 * b, a.I - 1)) * a.H;
-        with_token_tiles(n, [&](auto nt) {
-            constexpr int NT = decltype(nt)::value;
-            const T* xp[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                xp[j] = x + (int64_t)(entry[min(j * 8 + g, n - 1)] / kMaxK) * a.ldx;
-            if (a.gated) {
-                float acc[2][NT][4] = {};
-                rows_mac<T, 2, NT, VEC>(acc, w, xp, k0, k1);
-                put_partial(red + (warp * 2) * tile_floats, acc[0]);
-                put_partial(red + (warp * 2 + 1) * tile_floats, acc[1]);
-            } else {
-                const T* w0[1][2] = {{w[0][0], w[0][1]}};
-                float acc[1][NT][4] = {};
-                rows_mac<T, 1, NT, VEC>(acc, w0, xp, k0, k1);
-                put_partial(red + (warp * 2) * tile_floats, acc[0]);
-            }
-        });
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the rings were the logits' memory
+    __syncthreads();
+    // One unit: products(put) brings the warp's partial sums, which meet in shared memory.
+    auto unit = [&](const Choice& c, int row0, auto&& products) {
+        products([&](int i, int tok, int r, float v) { red[(warp * 2 + i) * tile_floats + tok * kPitch + r] = v; });
         group_sync(1 + mine, G * kWarp);
-        for (int i = wg * kWarp + lane; i < n * kRows; i += G * kWarp) {
+        for (int i = wg * kWarp + lane; i < c.n * kRows; i += G * kWarp) {
             const int tok = i / kRows, r = i % kRows;
             const float* p = red + (mine * G * 2) * tile_floats + tok * kPitch + r;
             float z = 0.f, up = 0.f;
@@ -266,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeArgs a)
                 z += p[q * 2 * tile_floats];
                 if (a.gated) up += p[(q * 2 + 1) * tile_floats];
             }
-            const int slot = entry[tok];
+            const int slot = c.entry[tok];
             float v = act_f(z, a.act);
             if (a.gated) v *= up;
             if (row0 + r < a.I) {
@@ -281,49 +522,98 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(MoeArgs a)
             }
         }
         group_sync(1 + mine, G * kWarp);
+    };
+    const int first = blockIdx.x * groups + mine;
+    if constexpr (VEC) {
+        auto all = [&](auto wt) {
+            constexpr int W = decltype(wt)::value;
+            auto ring = make_ring<T, W>(
+                sync, rings, &map, a.wait_cycles, first, stride, units, a.I,
+                [&](int u) { return (lists.active[u / tiles] % kMaxE) * W * a.I + u % tiles * kRows; }, [&](int) { return k0; },
+                [&](int) { return k1; });
+            ring.start();
+            for (int u = first; u < units; u += stride) {
+                const Choice c = choice(lists, u / tiles);
+                unit(c, u % tiles * kRows, [&](auto&& put) {
+                    ring_times_tokens<T, W, 1>(
+                        ring, [&](int i) { return x + (int64_t)(c.entry[i] / kMaxK) * a.ldx; }, c.n, k0, k1, a.H, 0, put);
+                });
+            }
+            ring.finish(a.status);
+        };
+        if (a.gated) all(std::integral_constant<int, 2>{});
+        else all(std::integral_constant<int, 1>{});
+    } else {
+        for (int u = first; u < units; u += stride) {
+            const Choice c = choice(lists, u / tiles);
+            const int row0 = u % tiles * kRows;
+            unit(c, row0, [&](auto&& put) {
+                for (int i = 0; i < WT; ++i) {
+                    const T* base = w1 + ((int64_t)c.e * WT * a.I + (int64_t)i * a.I) * a.H;
+                    const T* w[1][2] = {{base + (int64_t)min(row0 + g, a.I - 1) * a.H,
+                                         base + (int64_t)min(row0 + g + 8, a.I - 1) * a.H}};
+                    with_token_tiles(c.n, [&](auto nt) {
+                        rows_times_tokens<T, 1, decltype(nt)::value, 0>(
+                            w, [&](int t) { return x + (int64_t)(c.entry[t] / kMaxK) * a.ldx; }, c.n, k0, k1, 0,
+                            [&](int, int tok, int r, float v) { put(i, tok, r, v); });
+                    });
+                }
+            });
+        }
     }
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(MoeArgs a)
+__global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_constant__ CUtensorMap map, MoeArgs a)
 {
-    pdl_wait();
-    extern __shared__ float smem[];   // [warp][token][kPitch]: each warp's sums over its items
+    extern __shared__ uint8_t raw[];
+    uint8_t* rings = aligned128(raw);
+    float* smem = reinterpret_cast<float*>(rings + (VEC ? kRing : 0));   // [warp][token][kPitch]: each warp's sums
     __shared__ Lists lists;
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4, t4 = lane % 4;
+    __shared__ Rings sync;
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4;
     const int S = (int)cluster_size(), rank = (int)cluster_rank();
     const int row0 = (int)(blockIdx.x / S) * kRows;
-    float* mine = smem + warp * a.T * kPitch;
-    for (int i = lane; i < a.T * kPitch; i += kWarp) mine[i] = 0.f;
+    init_rings(sync);
+    for (int e = threadIdx.x; e < a.E; e += kThreads) lists.mask[e] = 0;
+    for (int i = threadIdx.x; i < kWarps * a.T * kPitch; i += kThreads) smem[i] = 0.f;
+    __syncthreads();
+    pdl_wait();
     build_lists(lists, a.T, a.k, a.E, [&](int t, int j) { return a.ids[t * a.k + j]; });
+    __syncthreads();
 
-    const int chunks = (a.I + a.chunk - 1) / a.chunk, items = lists.n_active * chunks;
+    const int chunks = (a.I + a.chunk - 1) / a.chunk, items = lists.n_active * chunks, stride = S * kWarps;
     const T *w2 = (const T*)a.w2, *h = (const T*)a.h;
-    for (int it = rank * kWarps + warp; it < items; it += S * kWarps) {
-        const int e = lists.active[it / chunks], k0 = it % chunks * a.chunk, n = __popcll(lists.mask[e]);
-        const uint16_t* entry = lists.entry + lists.first[e];
-        const T* w[1][2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) w[0][b] = w2 + ((int64_t)e * a.H + min(row0 + g + 8 * b, a.H - 1)) * a.I;
-        with_token_tiles(n, [&](auto nt) {
-            constexpr int NT = decltype(nt)::value;
-            const T* hp[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int slot = entry[min(j * 8 + g, n - 1)];
-                hp[j] = h + ((int64_t)(slot / kMaxK) * a.k + slot % kMaxK) * a.I;
-            }
-            float acc[1][NT][4] = {};
-            rows_mac<T, 1, NT, VEC, kTerms<T>>(acc, w, hp, k0, min(a.I, k0 + a.chunk), (int64_t)a.T * a.k * a.I);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int i = j * 8 + 2 * t4 + (c & 1);
-                    if (i < n) mine[entry[i] / kMaxK * kPitch + g + (c >> 1) * 8] += acc[0][j][c];
-                }
+    const int first = rank * kWarps + warp;
+    float* mine = smem + warp * a.T * kPitch;
+    const int64_t plane = (int64_t)a.T * a.k * a.I;
+    auto k0 = [&](int i) { return i % chunks * a.chunk; };
+    auto k1 = [&](int i) { return min(a.I, i % chunks * a.chunk + a.chunk); };
+    auto all = [&](auto&& products) {
+        for (int it = first; it < items; it += stride) {
+            const Choice c = choice(lists, it / chunks);
+            products(c, it, [&](int i) { return h + ((int64_t)(c.entry[i] / kMaxK) * a.k + c.entry[i] % kMaxK) * a.I; },
+                     [&](int, int i, int r, float v) { mine[c.entry[i] / kMaxK * kPitch + r] += v; });
+            __syncwarp();   // another item's token may be another lane's
+        }
+    };
+    if constexpr (VEC) {
+        auto ring = make_ring<T, 1>(sync, rings, &map, a.wait_cycles, first, stride, items, 0,
+                                    [&](int i) { return (lists.active[i / chunks] % kMaxE) * a.H + row0; }, k0, k1);
+        ring.start();
+        all([&](const Choice& c, int it, auto&& token, auto&& add) {
+            ring_times_tokens<T, 1, kTerms<T>>(ring, token, c.n, k0(it), k1(it), a.I, plane, add);
         });
-        __syncwarp();   // another item's token may be another lane's
+        ring.finish(a.status);
+    } else {
+        all([&](const Choice& c, int it, auto&& token, auto&& add) {
+            const T* base = w2 + (int64_t)c.e * a.H * a.I;
+            const T* w[1][2] = {{base + (int64_t)min(row0 + g, a.H - 1) * a.I,
+                                 base + (int64_t)min(row0 + g + 8, a.H - 1) * a.I}};
+            with_token_tiles(c.n, [&](auto nt) {
+                rows_times_tokens<T, 1, decltype(nt)::value, 0, kTerms<T>>(w, token, c.n, k0(it), k1(it), plane, add);
+            });
+        });
     }
     __syncthreads();
     // the warps' sums into the first one's place, then the blocks' into the output
@@ -350,72 +640,104 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(MoeArgs a)
     cluster_sync();   // no block leaves while another reads its sums
 }
 
-// Blocks of moe_up that run at the same time (a multiple of the cluster).
+// Blocks of a kernel that run at the same time in clusters of `cluster`.
 template <typename K>
-int resident_blocks(K kern, size_t smem)
+int resident_blocks(K kern, size_t smem, int cluster)
 {
     static std::mutex mu;
     static std::map<std::pair<int, size_t>, int> known;
     int dev = 0;
     cudaGetDevice(&dev);
     std::lock_guard<std::mutex> lock(mu);
-    auto [it, fresh] = known.try_emplace({dev, smem}, kUpCluster);
-    if (fresh) {
+    auto [it, fresh] = known.try_emplace({dev * 16 + cluster, smem}, num_sms() / cluster * cluster);
+    if (fresh && cluster > 1) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = kUpCluster;
+        cfg.gridDim = cluster;
         cfg.blockDim = kThreads;
         cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim = {kUpCluster, 1, 1};
+        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) it->second = n * kUpCluster;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) it->second = n * cluster;
         else cudaGetLastError();
     }
     return it->second;
 }
 
+// Boxes of 16 rows by `steps` steps of a [rows][cols] matrix of weights.
+template <typename T>
+dlrm_status weight_map(CUtensorMap* m, const void* p, int64_t rows, int cols, int steps)
+{
+    tc::EncodeTiledFn enc = tc::encode_fn();
+    if (!enc) return fail(DLRM_ERR_CUDA, "dlrm_moe_fwd: cuTensorMapEncodeTiled unavailable");
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, str[1] = {(cuuint64_t)cols * sizeof(T)};
+    const cuuint32_t box[2] = {(cuuint32_t)(steps * kStepK<T>), kRows}, ones[2] = {1, 1};
+    const CUtensorMapDataType type = std::is_same_v<T, float>    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : std::is_same_v<T, __half> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = enc(m, type, 2, const_cast<void*>(p), dims, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(DLRM_ERR_CUDA, "dlrm_moe_fwd: tensor map (%d)", (int)r);
+    return DLRM_OK;
+}
+
 template <typename T, bool VEC>
 dlrm_status launch_moe(MoeArgs a, cudaStream_t st)
 {
-    const int nt = a.T <= 8 ? 1 : a.T <= 16 ? 2 : a.T <= 32 ? 4 : 8;
-    const int e_tiles = (a.E + kRows - 1) / kRows, E16 = e_tiles * kRows, sub = e_tiles < kWarps ? kWarps / e_tiles : 1;
-    const size_t logits = (size_t)(sub + 1) * a.T * E16 * 4, red = (size_t)kWarps * 2 * nt * 8 * kPitch * 4;
-    const size_t smem = logits > red ? logits : red;
+    CUtensorMap m1 = {}, m2 = {};
+    dlrm_status s;
+    if (VEC) {
+        s = weight_map<T>(&m1, a.w1, (int64_t)a.E * (a.gated ? 2 : 1) * a.I, a.H, kSteps / (a.gated ? 2 : 1));
+        if (s == DLRM_OK) s = weight_map<T>(&m2, a.w2, (int64_t)a.E * a.H, a.I, kSteps);
+        if (s != DLRM_OK) return s;
+    }
+    const int nt = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
+    const size_t smem = up_bytes(a.T, a.E, nt, VEC);
     auto up = moe_up_kernel<T, VEC>;
     cudaError_t e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return fail(DLRM_ERR_CUDA, "dlrm_moe_fwd: %s", cudaGetErrorString(e));
-    const int most = resident_blocks(up, smem);
+    // a cluster shares the router's product out; a router of a few kilobytes is read sooner by every block for itself
+    const int C = (int64_t)a.E * a.H * (int64_t)sizeof(T) <= kOwnRouter ? 1 : kUpCluster;
+    const int most = resident_blocks(up, smem, C);
     const int chosen = a.E < a.T * a.k ? a.E : a.T * a.k;            // experts at most
     const int64_t units = (int64_t)chosen * ((a.I + kRows - 1) / kRows);
-    // warps of a unit: as many as leave every group of warps one unit, else the
-    // number whose rounds of units cost least (a step of K against a unit's ten steps of overhead)
-    const int64_t steps = (a.H + kStep<T> - 1) / kStep<T>;
-    int64_t least = 0;
-    for (int G = kWarps; G >= 1; G /= 2) {
-        const int64_t groups = (int64_t)most * kWarps / G, cost = (units + groups - 1) / groups * ((steps + G - 1) / G + 10);
-        if (least == 0 || cost < least) {
-            least = cost;
-            a.group = G;
-        }
-    }
+    a.group = kWarps;
+    while (a.group > 1 && units * a.group > 16 * (int64_t)most * kWarps) a.group /= 2;   // many units: fewer meetings
     int64_t blocks = (units * a.group + kWarps - 1) / kWarps;
     if (blocks > most) blocks = most;
-    blocks = (blocks + kUpCluster - 1) / kUpCluster * kUpCluster;
-    e = launch_cluster(up, dim3((unsigned)blocks), dim3(kThreads), smem, st, kUpCluster, a);
-    dlrm_status s = check_launch_pdl(e, "moe_up_kernel");
+    blocks = (blocks + C - 1) / C * C;
+    e = launch_cluster(up, dim3((unsigned)blocks), dim3(kThreads), smem, st, C, m1, a);
+    s = check_launch_pdl(e, "moe_up_kernel");
     if (s != DLRM_OK) return s;
 
     const int row_tiles = (a.H + kRows - 1) / kRows;
-    int S = kMaxSplit;
-    while (S > 1 && row_tiles * S > 4 * num_sms()) S /= 2;
-    const int64_t share = (int64_t)chosen * a.I / (S * kWarps * 2);   // two items a warp where there is that much
-    const int chunk = (int)(share < 2048 ? share : 2048) / kStep<T> * kStep<T>;
-    a.chunk = chunk < kStep<T> ? kStep<T> : chunk;
-    return check_launch_pdl(launch_cluster(moe_down_kernel<T, VEC>, dim3(row_tiles * S), dim3(kThreads),
-                                           (size_t)kWarps * a.T * kPitch * 4, st, S, a),
+    const size_t down = (VEC ? kRing + 128 : 0) + (size_t)kWarps * a.T * kPitch * 4;
+    auto kern = moe_down_kernel<T, VEC>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)down);
+    if (e != cudaSuccess) return fail(DLRM_ERR_CUDA, "dlrm_moe_fwd: %s", cudaGetErrorString(e));
+    // blocks that share 16 rows of the output: the number with the least time, in
+    // nanoseconds (an SM's share of HBM is 45 bytes each; 2 us for a round of blocks)
+    int S = 1;
+    double best = 0;
+    for (int c = 1; c <= kMaxSplit; c *= 2) {
+        const int at_once = resident_blocks(kern, down, c);
+        const double rounds = ((int64_t)row_tiles * c + at_once - 1) / at_once;
+        const double cost = rounds * ((double)chosen * kRows * a.I * sizeof(T) / c / 45 + 2000) + (c > 1 ? 500 : 0);
+        if (best == 0 || cost < best) {
+            best = cost;
+            S = c;
+        }
+    }
+    // an item: as long as leaves every warp four
+    const int down_k = kSteps * kStepK<T>;
+    const int64_t share = (int64_t)chosen * a.I / (S * kWarps * 4) / down_k * down_k;
+    a.chunk = share < down_k ? down_k : share > 8 * down_k ? 8 * down_k : (int)share;
+    return check_launch_pdl(launch_cluster(kern, dim3(row_tiles * S), dim3(kThreads), down, st, S, m2, a),
                             "moe_down_kernel");
 }
 
@@ -439,7 +761,7 @@ extern "C" dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_
                                     const void* d_w2, const void* d_residual, int64_t ldr, dlrm_dtype dtype, int T,
                                     int H, int I, int E, int k, dlrm_act act, int gated, void* d_y, int64_t ldy,
                                     int32_t* d_ids, float* d_probs, void* d_workspace, size_t workspace_bytes,
-                                    void* stream)
+                                    uint32_t* d_status, void* stream)
 {
     DLRM_API_RANGE("dlrm_moe_fwd");
     clear_error();
@@ -466,11 +788,17 @@ extern "C" dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_
         return fail(DLRM_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu", fn, d_workspace ? workspace_bytes : 0, need);
     if (reinterpret_cast<uintptr_t>(d_workspace) & 255u)
         return fail(DLRM_ERR_INVALID_ARG, "%s: the workspace must be 256-byte aligned", fn);
-    MoeArgs a = {d_x, d_w_router, d_w1, d_w2, d_residual, ldx, ldr, ldy, T,     H,       I,          E, k, (int)act,
-                 gated != 0, 0, 0, d_y, d_ids, d_probs, d_workspace};
-    // the workspace's planes start on the grid where I keeps its rows there
+    if ((int64_t)E * 2 * I > INT32_MAX || (int64_t)E * H > INT32_MAX)
+        return fail(DLRM_ERR_UNSUPPORTED, "%s: more than 2^31 weight rows", fn);
+    MoeArgs a = {};
+    a.x = d_x, a.wr = d_w_router, a.w1 = d_w1, a.w2 = d_w2, a.res = d_residual;
+    a.ldx = ldx, a.ldr = ldr, a.ldy = ldy;
+    a.T = T, a.H = H, a.I = I, a.E = E, a.k = k, a.act = act, a.gated = gated != 0;
+    a.y = d_y, a.ids = d_ids, a.probs = d_probs, a.h = d_workspace;
+    a.status = d_status, a.wait_cycles = wait_limit_cycles();
+    // TMA and 16-byte loads where every row is on the grid (the workspace's are where I's are)
     const bool vec = rows_aligned16(d_x, ldx, T, es) && rows_aligned16(d_w_router, H, E, es) &&
-                     rows_aligned16(d_w1, H, 2, es) && rows_aligned16(d_w2, I, 2, es);
+                     rows_aligned16(d_w1, H, 2, es) && rows_aligned16(d_w2, I, 2, es) && H * es % 16 == 0 && I * es % 16 == 0;
     return with_type(dtype, [&](auto t) {
         using T_ = decltype(t);
         return vec ? launch_moe<T_, true>(a, as_stream(stream)) : launch_moe<T_, false>(a, as_stream(stream));

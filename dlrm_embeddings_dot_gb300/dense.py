@@ -36,7 +36,7 @@ _SIGNATURES = {
     "dlrm_linear_bwd": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _I, _D, _P, _P, _L, _P, _L, _P, _P, _Z,
                              _P, _P]),
     "dlrm_linear_bwd_workspace_size": (_Z, [_P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _I, _D]),
-    "dlrm_moe_fwd": (_I, [_P, _L, _P, _P, _P, _P, _L, _I, _I, _I, _I, _I, _I, _I, _I, _P, _L, _P, _P, _P, _Z, _P]),
+    "dlrm_moe_fwd": (_I, [_P, _L, _P, _P, _P, _P, _L, _I, _I, _I, _I, _I, _I, _I, _I, _P, _L, _P, _P, _P, _Z, _P, _P]),
     "dlrm_moe_fwd_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
 }
 
@@ -177,7 +177,7 @@ def dlrm_moe_fwd_workspace_size(x, w_router, w1, w2, top_k) -> int:
 
 
 def dlrm_moe_fwd(x, w_router, w1, w2, residual, y, ids, probs, act=DLRM_ACT_SILU, gated=True, workspace=None,
-                 stream=None):
+                 status=None, stream=None):
     """Mixture-of-experts layer for a few tokens: y = residual + sum of probs * expert(x) over the
     top-k experts (k from ids [T][k]); residual may be None.  See ``include/dlrm_dense.h``."""
     T, H, I, E = _moe_sizes(x, w_router, w1, w2)
@@ -186,4 +186,4 @@ def dlrm_moe_fwd(x, w_router, w1, w2, residual, y, ids, probs, act=DLRM_ACT_SILU
           _dense("w1", w1, (E, 2 * I if gated else I, H), dt), _dense("w2", w2, (E, H, I), dt),
           *_mat("residual", residual, (T, H), dt), _code(x.dtype), T, H, I, E, k, act, bool(gated),
           *_mat("y", y, (T, H), dt), _dense("ids", ids, (T, k), torch.int32),
-          _dense("probs", probs, (T, k), torch.float32), *_ws(workspace), _stream(stream))
+          _dense("probs", probs, (T, k), torch.float32), *_ws(workspace), _dl._ptr(status), _stream(stream))

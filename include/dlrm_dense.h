@@ -139,6 +139,7 @@ size_t dlrm_linear_bwd_workspace_size(const void* d_grad_y, int64_t ldg, const v
  *   last three contiguous;  d_residual [T][H] or NULL;  d_y [T][H] (output)
  *   d_ids int32 [T][k] (output);  d_probs fp32 [T][k] (output)
  *   d_workspace: dlrm_moe_fwd_workspace_size bytes, 256-byte aligned
+ *   d_status may be NULL; gets DLRM_STATUS_TIMEOUT if a bounded wait gave up.
  * probs * h enters the second product as two values of a 2-byte dtype (rounded
  * and the rounded rest), or in fp32.
  * Experts that no token chose are not read.  Requires H, I >= 1, 0 <= T <=
@@ -148,7 +149,7 @@ size_t dlrm_linear_bwd_workspace_size(const void* d_grad_y, int64_t ldg, const v
 dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_w_router, const void* d_w1, const void* d_w2,
                          const void* d_residual, int64_t ldr, dlrm_dtype dtype, int T, int H, int I, int E, int k,
                          dlrm_act act, int gated, void* d_y, int64_t ldy, int32_t* d_ids, float* d_probs,
-                         void* d_workspace, size_t workspace_bytes, void* stream);
+                         void* d_workspace, size_t workspace_bytes, uint32_t* d_status, void* stream);
 
 /* Workspace bytes of dlrm_moe_fwd (0 for invalid sizes and for T = 0). */
 size_t dlrm_moe_fwd_workspace_size(dlrm_dtype dtype, int T, int H, int I, int E, int k);

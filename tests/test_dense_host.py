@@ -107,7 +107,7 @@ def test_linear_bwd_refusals(L):
 
 def _moe(L, x=FAKE, ldx=16, wr=FAKE, w1=FAKE, w2=FAKE, r=None, ldr=0, dt=1, T=4, H=16, I=8, E=4, k=2, act=3, gated=1,
          y=FAKE, ldy=16, ids=FAKE, probs=FAKE, ws=FAKE, wsb=1 << 40):
-    return L.dlrm_moe_fwd(x, ldx, wr, w1, w2, r, ldr, dt, T, H, I, E, k, act, gated, y, ldy, ids, probs, ws, wsb, None)
+    return L.dlrm_moe_fwd(x, ldx, wr, w1, w2, r, ldr, dt, T, H, I, E, k, act, gated, y, ldy, ids, probs, ws, wsb, None, None)
 
 
 def test_moe_refusals(L):
