@@ -41,13 +41,6 @@ __device__ __forceinline__ void act_n(float (&f)[n], int act)
     }
 }
 
-__device__ __forceinline__ float act_any(float z, int act)
-{
-    if (act == DLRM_ACT_RELU) return act_f(z, DLRM_ACT_RELU);
-    if (act == DLRM_ACT_GELU) return act_f(z, DLRM_ACT_GELU);
-    return act == DLRM_ACT_SILU ? act_f(z, DLRM_ACT_SILU) : z;
-}
-
 // f *= a'(z)
 __device__ __forceinline__ void slope8(float (&f)[8], const float (&z)[8], int act)
 {
@@ -88,17 +81,6 @@ __device__ __forceinline__ void finish8(const Epilogue& e, const DropKey& key, i
         for (int i = 0; i < 8; ++i) f[i] += g[i];
     }
     store8<T, VEC>((T*)e.out + row * e.ldo + col, n, f);
-}
-
-// A value of column `col` after the product: the scalar form of finish8.
-template <typename T>
-__device__ __forceinline__ void finish1(const Epilogue& e, int64_t row, int col, float v, float bias, bool kept, float res)
-{
-    v += bias;
-    if (e.pre) ((T*)e.pre)[row * e.ldp + col] = from_f32<T>(v);
-    v = act_any(v, e.act);
-    if (e.drop.thr) v = kept ? v * e.drop.scale : 0.f;
-    ((T*)e.out)[row * e.ldo + col] = from_f32<T>(e.res ? v + res : v);
 }
 
 // finish8 for a run that may be short or off the 16-byte grid.

@@ -41,6 +41,7 @@ constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kSlice = 32;          // columns of an epilogue slice
 constexpr int kSliceStep = kEpiWarps / 4 * kSlice;
 constexpr int kMaxStages = 8;
+constexpr int kMaxPairs = 6;         // products of two operands of three planes each
 constexpr int kSmemLimit = 232448;  // 227 KB opt-in per block
 
 struct Args {
@@ -49,7 +50,7 @@ struct Args {
     int pairs;                      // plane pairs: 1, or 6 for fp32
     int splits;                     // parts of K; above 1 the tiles go to `partial`
     int tiles_m, tiles_n, BN, NS;
-    int tma;                        // out, pre and residual take TMA boxes (rows start and end on the 16-byte grid)
+    int a_mn, b_mn;                 // operand layouts
     int bias_vec;                   // the bias starts on a 16-byte boundary
     int warp_bytes;                 // an epilogue warp's shared memory
     uint32_t idesc, tmem_cols;
@@ -158,42 +159,71 @@ __device__ __forceinline__ void take_rows(const uint8_t* scratch, float (&f)[4][
     }
 }
 
-// The epilogue of a ragged slice, or of rows off the 16-byte grid: a lane takes
+// The epilogue of rows that do not start and end on the 16-byte grid: a lane takes
 // one column of each row, so that a warp's loads and stores are contiguous
-// whatever the alignment (eight scalar accesses a lane spread over 32 sectors
-// instead: 48 us against @RAGGED@ us at 5003 x 515 x 367 fp32).
+// whatever the alignment, eight rows a turn, each step over all of them.
 template <typename T, typename Loaded>
 __device__ __forceinline__ void ragged_slice(const Epilogue& e, const DropKey& key, uint32_t taddr, uint8_t* scratch,
                                              int row0, int M, int c0, int N, Loaded&& loaded)
 {
-    const int lane = threadIdx.x % kWarp, col = c0 + lane;
+    constexpr int kTurn = 8;
+    const int lane = threadIdx.x % kWarp, col = c0 + lane, rows = min(32, M - row0);
+    const bool in = col < N;
+    const float bias = e.bias && in ? __ldg(e.bias + col) : 0.f;
+    const T* rp = (const T*)e.res + (int64_t)row0 * e.ldr + col;
+    float res[kTurn], ahead[kTurn];   // the residual of this turn and of the next
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i) ahead[i] = in && r0 + i < rows ? to_f32(__ldg(rp + (r0 + i) * e.ldr)) : 0.f;
+    };
+    if (e.res) fetch(0);
     uint32_t keep = 0;   // byte p: row 8 p + lane / 4, columns 8 (lane % 4) and on
     if (e.drop.thr)
 #pragma unroll
         for (int p = 0; p < 4; ++p)
             keep |= keep8(e.drop, key, (uint32_t)(row0 + 8 * p + lane / 4), (uint32_t)c0 / 8 + lane % 4) << 8 * p;
     stage_slice(taddr, scratch, loaded);
-    const bool in = col < N;
-    const float bias = e.bias && in ? __ldg(e.bias + col) : 0.f;
-    const int rows = min(32, M - row0);
-    constexpr int kTurn = 8;   // rows whose residual is on its way together
+#pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += kTurn) {
-        float res[kTurn];
-        if (e.res)
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i)
-                if (in && r0 + i < rows) res[i] = to_f32(__ldg((const T*)e.res + (int64_t)(row0 + r0 + i) * e.ldr + col));
+        float f[kTurn];
 #pragma unroll
         for (int i = 0; i < kTurn; ++i) {
             const int r = r0 + i;
-            const uint32_t bits = e.drop.thr ? __shfl_sync(~0u, keep, (r % 8) * 4 + lane / 8) >> (r / 8 * 8 + lane % 8) : 0;
-            const float v = *reinterpret_cast<const float*>(scratch + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4);
-            if (in && r < rows) finish1<T>(e, row0 + r, col, v, bias, bits & 1, e.res ? res[i] : 0.f);
+            f[i] = bias + *reinterpret_cast<const float*>(scratch + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4);
         }
+        if (e.res) {
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) res[i] = ahead[i];
+            if (r0 + kTurn < rows) fetch(r0 + kTurn);
+        }
+        if (e.pre) {
+            T* at = (T*)e.pre + (int64_t)(row0 + r0) * e.ldp + col;
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i)
+                if (in && r0 + i < rows) at[i * e.ldp] = from_f32<T>(f[i]);
+        }
+        act_n(f, e.act);
+        if (e.drop.thr) {
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) {
+                const uint32_t bits = __shfl_sync(~0u, keep, i * 4 + lane / 8) >> (r0 + lane % 8);
+                f[i] = bits & 1 ? f[i] * e.drop.scale : 0.f;
+            }
+        }
+        if (e.res) {
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) f[i] += res[i];
+        }
+        T* at = (T*)e.out + (int64_t)(row0 + r0) * e.ldo + col;
+#pragma unroll
+        for (int i = 0; i < kTurn; ++i)
+            if (in && r0 + i < rows) at[i * e.ldo] = from_f32<T>(f[i]);
     }
 }
 
-template <typename T, bool A_MN, bool B_MN, bool PAIR>
+// BOXES: results leave as TMA boxes; otherwise as a split's partial tiles, or by
+// ragged_slice.
+template <typename T, bool PAIR, bool BOXES>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
@@ -277,13 +307,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             if constexpr (PAIR) tma_load_3d_pair(dst, map, c0, c1, c2, bar);
                             else tma_load_3d(dst, map, c0, c1, c2, &full[stage]);
                         };
-                        if constexpr (A_MN) {
+                        if (a.a_mn) {
 #pragma unroll
                             for (int i = 0; i < kBM / 64; ++i) load(sa + i * 8192, &map_a, m0 + i * 64, kb * kKB, pa);
                         } else {
                             load(sa, &map_a, kb * kKB, m0, pa);
                         }
-                        if constexpr (B_MN) {
+                        if (a.b_mn) {
                             for (int i = 0; i < b_rows / 64; ++i)
                                 load(sa + a_bytes + i * 8192, &map_b, n0 + i * 64, kb * kKB, pb);
                         } else {
@@ -327,9 +357,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             };
             // descriptors of stage 0, and what a K step adds to their address field (16-byte units)
             const uint32_t sa = smem_u32(smem), sb = sa + a_bytes;
-            const uint64_t ad0 = A_MN ? sw128_desc_mn(sa, 8192, 1024) : sw128_desc(sa);
-            const uint64_t bd0 = B_MN ? sw128_desc_mn(sb, 8192, 1024) : sw128_desc(sb);
-            constexpr uint32_t da = A_MN ? 2048 / 16 : 32 / 16, db = B_MN ? 2048 / 16 : 32 / 16;
+            const uint64_t ad0 = a.a_mn ? sw128_desc_mn(sa, 8192, 1024) : sw128_desc(sa);
+            const uint64_t bd0 = a.b_mn ? sw128_desc_mn(sb, 8192, 1024) : sw128_desc(sb);
+            const uint32_t da = a.a_mn ? 2048 / 16 : 32 / 16, db = a.b_mn ? 2048 / 16 : 32 / 16;
             // A wait that gives up raises the abort flag, after which every wait returns
             // at once: the flag is looked at once a tile, and until then products of
             // whatever the ring holds are harmless.
@@ -387,7 +417,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         uint8_t* res_box = pre_box + (a.e.pre ? kBoxBytes<T> : 0);
         uint64_t* rbar = rfull + (warp - 2);
         const DropKey key = drop_key(a.e.drop);
-        const bool boxes = a.splits == 1 && a.tma;             // leaves by TMA
         int it = 0;
         uint32_t asked = 0, used = 0;                          // residual slices asked for, and added
         for (int t = first; t < tiles; t += stride, ++it) {
@@ -403,7 +432,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 }
                 ++asked;
             };
-            if (boxes && a.e.res && kSlice * part < cols) ask(kSlice * part);
+            if (BOXES && a.e.res && kSlice * part < cols) ask(kSlice * part);
             if (!__all_sync(~0u, mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, a.wait_cycles))) break;
             tc_fence_after();
             auto release = [&] {   // the accumulator has been read: the tile after next may overwrite it
@@ -421,7 +450,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             bool ok = true;
             for (int c0 = kSlice * part; c0 < cols; c0 += kSliceStep) {
                 const bool last = c0 + kSliceStep >= cols;
-                if (boxes) {
+                if constexpr (BOXES) {
                     float f[kSlice];
                     {
                         uint32_t v[32];
@@ -551,7 +580,16 @@ struct Operand {
 
 struct Shape {
     int M, N, K, pairs;
+    int column;   // cycles an epilogue takes for a tile's column
 };
+
+// What the plan takes for it (64K x 1024 outputs: 14 cycles a column of a 128-row
+// tile for the stores alone, 14 for dropout, 16 for GELU, 12 for the residual;
+// ragged rows 40).  It goes by the sizes alone, which the workspace query has too.
+inline int column_cycles(int N, int es, bool layer) { return (N * (int64_t)es % 16 ? 40 : 14) + (layer ? 14 : 0); }
+
+// A TMA store clips at 16 bytes: the last columns of another width would spill past N.
+inline bool takes_boxes(const Epilogue& e, int N, int es) { return e.vec && (int64_t)N * es % 16 == 0; }
 
 struct Plan {
     int BN, splits;
@@ -564,9 +602,10 @@ inline Plan plan(const Shape& s)
     struct Tile {
         int BN;
         bool pair;
-        double block;   // cycles of a 64-wide block of K
+        double block;   // cycles of a 64-wide block of K, measured: bound by the products for the
+                        // widest, by the operands' way from L2 for the narrow ones
     };
-    constexpr Tile tiles_of[] = {{256, true, 540}, {256, false, 640}, {128, true, 300}, {128, false, 340}, {64, false, 220}};
+    constexpr Tile tiles_of[] = {{256, true, 700}, {256, false, 800}, {128, true, 600}, {128, false, 650}, {64, false, 500}};
     const int sms = num_sms();
     const int64_t kb = (s.K + kKB - 1) / kKB;
     Plan best = {};
@@ -577,9 +616,11 @@ inline Plan plan(const Shape& s)
         for (int S = 1; S <= 32 && S <= kb; ++S) {
             if (S > 1 && tiles * S > 4 * (int64_t)units) break;
             const int64_t waves = (tiles * S + units - 1) / units;
-            const double products = (double)((kb + S - 1) / S) * s.pairs * t.block, epilogue = 12.0 * t.BN;
+            const double products = (double)((kb + S - 1) / S) * s.pairs * t.block;
+            const double epilogue = 1500 + (S > 1 ? 20.0 : s.column) * (s.N < t.BN ? s.N : t.BN);
             double cost = waves * (products > epilogue ? products : epilogue) + epilogue;
-            if (S > 1) cost += 4000 + (double)s.M * s.N * S * 8 / 4000;   // another launch, and the partial tiles' way
+            // another launch, and the partial tiles' way to memory and back
+            if (S > 1) cost += 4000 + (double)s.M * s.N * S * 8 / 4000 + (double)s.M * s.N * s.column / 128 / sms;
             if (least == 0 || cost < least) {
                 least = cost;
                 best = {t.BN, S, t.pair};
@@ -636,7 +677,7 @@ dlrm_status make_box_map(const char* fn, CUtensorMap* m, const void* p, int64_t 
 
 // out = A B^T and the epilogue; T the type of the epilogue's tensors, bf
 // whether the operands are bf16 (fp16 otherwise).  partial: partial_bytes(s).
-template <typename T, bool A_MN, bool B_MN>
+template <typename T>
 dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand& B, bool bf, const Epilogue& e,
                 float* partial, uint32_t* status, cudaStream_t st)
 {
@@ -658,11 +699,12 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     if (tm * tn > INT32_MAX / 64) return fail(DLRM_ERR_UNSUPPORTED, "%s: %lld output tiles", fn, (long long)(tm * tn));
     a.tiles_m = (int)tm;
     a.tiles_n = (int)tn;
-    // a TMA store clips at 16 bytes: the last columns of another width would spill past N
-    a.tma = e.vec && s.N * (int64_t)sizeof(T) % 16 == 0;
+    a.a_mn = A.mn;
+    a.b_mn = B.mn;
+    const bool boxes = p.splits == 1 && takes_boxes(e, s.N, sizeof(T));
     a.bias_vec = aligned16(e.bias);
     a.warp_bytes = 32 * 128;   // a split's or a ragged slice's fp32 rows
-    if (p.splits == 1 && a.tma) {
+    if (boxes) {
         a.warp_bytes = kBoxBytes<T> * (1 + (e.pre != nullptr) + (e.res != nullptr));
         r = make_box_map<T>(fn, &mo, e.out, e.ldo, s.M, s.N);
         if (r == DLRM_OK && e.pre) r = make_box_map<T>(fn, &mp, e.pre, e.ldp, s.M, s.N);
@@ -671,7 +713,7 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     }
     a.NS = kMaxStages;
     while (smem_bytes(b_rows, a.NS, a.warp_bytes) > (size_t)kSmemLimit) --a.NS;
-    a.idesc = idesc_f16(CG * kBM, p.BN) | (bf ? 1u << 7 | 1u << 10 : 0u) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+    a.idesc = idesc_f16(CG * kBM, p.BN) | (bf ? 1u << 7 | 1u << 10 : 0u) | (A.mn ? 1u << 15 : 0u) | (B.mn ? 1u << 16 : 0u);
     a.tmem_cols = 2 * p.BN;
     a.partial = partial;
     a.Np = padded(s.N);
@@ -681,7 +723,8 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     const int64_t tiles = tm * tn * p.splits, units = num_sms() / CG;
     const int grid = (int)(tiles < units ? tiles : units) * CG;
     const size_t smem = smem_bytes(b_rows, a.NS, a.warp_bytes);
-    auto kern = p.pair ? gemm_kernel<T, A_MN, B_MN, true> : gemm_kernel<T, A_MN, B_MN, false>;
+    auto kern = p.pair ? (boxes ? gemm_kernel<T, true, true> : gemm_kernel<T, true, false>)
+                       : (boxes ? gemm_kernel<T, false, true> : gemm_kernel<T, false, false>);
     cudaError_t ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (ce != cudaSuccess) return fail(DLRM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
     r = check_launch_pdl(p.pair ? launch_cluster(kern, dim3(grid), dim3(kThreads), smem, st, 2, ma, mb, mo, mp, mr, a)

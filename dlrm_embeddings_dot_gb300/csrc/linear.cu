@@ -19,6 +19,7 @@ using gemm::padded;
 using gemm::Shape;
 
 constexpr int kFewRows = few::kMaxTokens;
+constexpr int kOneChunk = 1024;   // rows that grad_z_kernel takes as one chunk
 
 // ------------------------------------------------------------------ packing
 // Stores eight columns as a 2-byte operand; fp32 as three planes.
@@ -190,7 +191,7 @@ dlrm_status launch_few(const void* x, int64_t ldx, const void* w, int64_t ldw, i
 // (256 / cg)-th row and adds them up in registers, then the block adds its
 // threads' sums in shared memory.
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
 grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, int64_t ldp, int act, int vec,
               Drop drop, int M, int N, int cg, int rows, void* __restrict__ dz, float* __restrict__ partial)
 {
@@ -202,7 +203,7 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, 
     const int64_t Np = padded(N);
     float sum[8] = {};
     if (n > 0) {
-        constexpr int kAhead = 8 / sizeof(T);   // rows whose loads are in flight together
+        constexpr int kAhead = 4 / sizeof(T);   // rows whose loads are in flight together
         const int r0 = blockIdx.y * rows + ty, r1 = min(M, (int)(blockIdx.y + 1) * rows);
         const bool v = vec && n >= 8;
         for (int r = r0; r < r1; r += step * kAhead) {
@@ -251,10 +252,17 @@ struct GradZ {
     int cg, blocks_x, chunks, rows;
 };
 
+// Few rows: one chunk of narrow blocks, whose sums are the bias gradient itself.
+// Otherwise chunks of rows for eight blocks an SM, and sum_rows_kernel behind.
 GradZ grad_z_shape(int M, int N)
 {
     const int groups = (N + 7) / 8;
-    GradZ s = {1, 0, 0, 0};
+    GradZ s = {1, 0, 1, M};
+    if (M <= kOneChunk) {
+        while (s.cg < 32 && s.cg < groups && 256 / (2 * s.cg) * 4 >= M) s.cg *= 2;   // four rows a thread
+        s.blocks_x = (groups + s.cg - 1) / s.cg;
+        return s;
+    }
     while (s.cg < 32 && s.cg < groups) s.cg *= 2;
     s.blocks_x = (groups + s.cg - 1) / s.cg;
     const int step = 256 / s.cg;
@@ -306,6 +314,17 @@ dlrm_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t
 
 bool sizes_ok(dlrm_dtype dtype, int M, int N, int K) { return dense_dtype_ok(dtype) && M >= 1 && N >= 1 && K >= 1; }
 
+// The products as shapes: output rows, output columns, summed index.
+Shape fwd_shape(dlrm_dtype dt, int M, int N, int K)
+{
+    return {M, N, K, dt == DLRM_F32 ? gemm::kMaxPairs : 1, gemm::column_cycles(N, dense_dtype_size(dt), true)};
+}
+
+Shape grad_shape(dlrm_dtype dt, int M, int N, int K)
+{
+    return {M, N, K, dt == DLRM_F32 ? gemm::kMaxPairs : 1, gemm::column_cycles(N, dense_dtype_size(dt), false)};
+}
+
 // The workspaces' pieces, one after another.
 struct FwdLayout {
     size_t x, w, partial, total;   // x, w: bytes of the operands' copies (0: used as they are)
@@ -317,7 +336,7 @@ FwdLayout fwd_layout(const void* x, int64_t ldx, const void* w, int64_t ldw, dlr
     if (M <= kFewRows) return l;
     l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, dt) : 0;
     l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
-    l.partial = gemm::partial_bytes({M, N, K, dt == DLRM_F32 ? 6 : 1});
+    l.partial = gemm::partial_bytes(fwd_shape(dt, M, N, K));
     l.total = l.x + l.w + l.partial;
     return l;
 }
@@ -330,12 +349,12 @@ BwdLayout bwd_layout(const void* dy, int64_t ldg, const void* x, int64_t ldx, co
                      int M, int N, int K, dlrm_act act, double p)
 {
     BwdLayout l = {};
-    const int pairs = dt == DLRM_F32 ? 6 : 1;
     l.dz = act != DLRM_ACT_NONE || p > 0 || needs_pack(dy, ldg, M, dt) ? operand_bytes(M, N, dt) : 0;
     l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, dt) : 0;
     l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
-    l.sums = dlrm_ws_align((size_t)grad_z_shape(M, N).chunks * N * 4);
-    const size_t a = gemm::partial_bytes({M, K, N, pairs}), b = gemm::partial_bytes({N, K, M, pairs});
+    const GradZ g = grad_z_shape(M, N);
+    l.sums = g.chunks > 1 ? dlrm_ws_align((size_t)g.chunks * N * 4) : 0;
+    const size_t a = gemm::partial_bytes(grad_shape(dt, M, K, N)), b = gemm::partial_bytes(grad_shape(dt, N, K, M));
     l.partial = a > b ? a : b;
     l.total = l.dz + l.x + l.w + l.sums + l.partial;
     return l;
@@ -388,7 +407,7 @@ extern "C" dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void*
         if (wsp) jw = {d_w, ldw, N, K, rows_aligned16(d_w, ldw, N, es), wsp};
         const dlrm_status r = launch_pack<T>(jx, jw, st);
         if (r != DLRM_OK) return r;
-        return gemm::run<T, false, false>(fn, {M, N, K, dtype == DLRM_F32 ? 6 : 1}, operand<T>(d_x, ldx, M, K, xs, false),
+        return gemm::run<T>(fn, fwd_shape(dtype, M, N, K), operand<T>(d_x, ldx, M, K, xs, false),
                                           operand<T>(d_w, ldw, N, K, wsp, false), dtype != DLRM_F16, e, partial,
                                           d_status, st);
     });
@@ -436,7 +455,6 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
     if ((s = check_workspace(fn, d_workspace, workspace_bytes, l.total)) != DLRM_OK) return s;
     return with_type(dtype, [&](auto t) -> dlrm_status {
         using T = decltype(t);
-        const int pairs = dtype == DLRM_F32 ? 6 : 1;
         const bool bf = dtype != DLRM_F16;
         uint8_t* ws = (uint8_t*)d_workspace;
         void *dz = l.dz ? ws : nullptr, *xs = l.x ? ws + l.dz : nullptr, *wsp = l.w ? ws + l.dz + l.x : nullptr;
@@ -449,9 +467,9 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
             const int vec = rows_aligned16(d_grad_y, ldg, M, es) && (act == DLRM_ACT_NONE || rows_aligned16(d_pre, ldp, M, es));
             r = check_launch_pdl(launch_pdl(grad_z_kernel<T>, dim3(g.blocks_x, g.chunks), dim3(256), 0, st,
                                             (const T*)d_grad_y, ldg, (const T*)d_pre, ldp, (int)act, vec, drop, M, N,
-                                            g.cg, g.rows, products ? dz : nullptr, d_grad_bias ? sums : nullptr),
+                                            g.cg, g.rows, products ? dz : nullptr, d_grad_bias ? (g.chunks > 1 ? sums : d_grad_bias) : nullptr),
                                  "grad_z_kernel");
-            if (r == DLRM_OK && d_grad_bias)
+            if (r == DLRM_OK && d_grad_bias && g.chunks > 1)
                 r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 31) / 32), dim3(1024), 0, st,
                                                 (const float*)sums, g.chunks, N, d_grad_bias),
                                      "sum_rows_kernel");
@@ -467,14 +485,14 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
             e.out = d_grad_x;
             e.ldo = lddx;
             e.vec = epilogue_vec(e, M, es);
-            r = gemm::run<T, false, true>(fn, {M, K, N, pairs}, operand<T>(d_grad_y, ldg, M, N, dz, false),
+            r = gemm::run<T>(fn, grad_shape(dtype, M, K, N), operand<T>(d_grad_y, ldg, M, N, dz, false),
                                           operand<T>(d_w, ldw, N, K, wsp, true), bf, e, partial, d_status, st);
         }
         if (r == DLRM_OK && d_grad_w) {
             e.out = d_grad_w;
             e.ldo = lddw;
             e.vec = epilogue_vec(e, N, es);
-            r = gemm::run<T, true, true>(fn, {N, K, M, pairs}, operand<T>(d_grad_y, ldg, M, N, dz, true),
+            r = gemm::run<T>(fn, grad_shape(dtype, N, K, M), operand<T>(d_grad_y, ldg, M, N, dz, true),
                                          operand<T>(d_x, ldx, M, K, xs, true), bf, e, partial, d_status, st);
         }
         return r;
