@@ -359,12 +359,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const uint32_t sa = smem_u32(smem), sb = sa + a_bytes;
             const uint64_t ad0 = a.a_mn ? sw128_desc_mn(sa, 8192, 1024) : sw128_desc(sa);
             const uint64_t bd0 = a.b_mn ? sw128_desc_mn(sb, 8192, 1024) : sw128_desc(sb);
-            const uint32_t da = a.a_mn ? 2048 / 16 : 32 / 16, db = a.b_mn ? 2048 / 16 : 32 / 16;
+            constexpr uint32_t kMajor = 32 / 16, mnMajor = 2048 / 16;
             // A wait that gives up raises the abort flag, after which every wait returns
             // at once: the flag is looked at once a tile, and until then products of
             // whatever the ring holds are harmless.
             int stage = 0, it = 0;
             uint32_t phase = 0;
+            auto issue = [&](auto step_a, auto step_b) {   // the descriptors' steps as constants
+            constexpr uint32_t da = decltype(step_a)::value, db = decltype(step_b)::value;
             for (int t = first; t < tiles; t += stride, ++it) {
                 const auto [b0, b1] = k_range(a, a.splits == 1 ? 0 : t / per_split);
                 const int buf = it & 1;
@@ -403,6 +405,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 if (elect_one()) commit(&tfull[buf]);
                 __syncwarp();
             }
+            };
+            using K = std::integral_constant<uint32_t, kMajor>;
+            using MN = std::integral_constant<uint32_t, mnMajor>;
+            if (a.a_mn) issue(MN{}, MN{});
+            else if (a.b_mn) issue(K{}, MN{});
+            else issue(K{}, K{});
             // MMAs already issued must finish before TMEM is freed
             if (__any_sync(~0u, *abort_flag != 0) && elect_one()) {
                 commit(&tfull[it & 1]);

@@ -4,7 +4,7 @@
 //   forward   z = x W^T + b;  y = residual + drop(a(z))
 //   backward  dZ = a'(z) drop(dY);  dX = dZ W;  dW = dZ^T x;  db = sum dZ
 //
-// Up to kFewRows rows the forward streams the weights into matrix fragments
+// Few rows (few_rows): the forward streams the weights into matrix fragments
 // (linear_few_kernel); the other products run on tcgen05 (gemm_tc.cuh), which
 // wants 2-byte operands with rows on the 16-byte grid.  pack_kernel lays out
 // again what is not like that: misaligned rows, and fp32 as three bf16 planes.
@@ -18,7 +18,13 @@ using gemm::Operand;
 using gemm::padded;
 using gemm::Shape;
 
-constexpr int kFewRows = few::kMaxTokens;
+// Whether the forward streams the weights (linear_few_kernel) instead of running on
+// tcgen05 tiles.  Measured, us, streamed / tiles: 1024 x 480 bf16 2.5 / 5.9 at 16 rows,
+// 4.0 / 5.9 at 64; 4096 x 1024 5.1 / 8.1 at 48 rows (fp32 20.3 / 19.1); 4096 x 4096
+// 10.0 / 14.1 at 32 rows (fp32 40.0 / 53.0), but 14.4 / 13.0 at 48 (fp32 70.3 / 53.6): there
+// a block's 16 weight rows come with more token bytes from L2 than weight bytes.
+inline bool few_rows(int M, int N, int K) { return M <= 32 || (M <= few::kMaxTokens && (int64_t)N * K <= 1 << 23); }
+
 constexpr int kOneChunk = 1024;   // rows that grad_z_kernel takes as one chunk
 
 // ------------------------------------------------------------------ packing
@@ -333,7 +339,7 @@ struct FwdLayout {
 FwdLayout fwd_layout(const void* x, int64_t ldx, const void* w, int64_t ldw, dlrm_dtype dt, int M, int N, int K)
 {
     FwdLayout l = {};
-    if (M <= kFewRows) return l;
+    if (few_rows(M, N, K)) return l;
     l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, dt) : 0;
     l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
     l.partial = gemm::partial_bytes(fwd_shape(dt, M, N, K));
@@ -398,7 +404,7 @@ extern "C" dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void*
     const cudaStream_t st = as_stream(stream);
     return with_type(dtype, [&](auto t) -> dlrm_status {
         using T = decltype(t);
-        if (M <= kFewRows) return launch_few<T>(d_x, ldx, d_w, ldw, M, N, K, e, st);
+        if (few_rows(M, N, K)) return launch_few<T>(d_x, ldx, d_w, ldw, M, N, K, e, st);
         uint8_t* ws = (uint8_t*)d_workspace;
         void *xs = l.x ? ws : nullptr, *wsp = l.w ? ws + l.x : nullptr;
         float* partial = (float*)(ws + l.x + l.w);

@@ -193,7 +193,8 @@ struct Ring {
     }
     __device__ __forceinline__ void ask()
     {
-        if (item >= items) return;
+        // after a wait gave up a stage may be asked for already: no barrier takes two requests
+        if (item >= items || *abort_flag) return;
         const uint32_t s = asked++ % kStages;
         if (threadIdx.x % kWarp == 0) {
             tc::mbar_expect_tx(&full[s], kStage);
