@@ -3,7 +3,8 @@
 Each ``csrc/*.cu`` (and host-only ``csrc/*.cpp``) file is compiled by nvcc
 in parallel and linked into one shared object exporting the C ABI of
 ``include/*.h``.  The CUDA runtime is linked statically, so the
-library needs only the driver at run time.
+library needs only the driver at run time.  ``csrc/marshal.c`` becomes the
+small CPython extension ``_marshal.so`` beside it.
 """
 
 from __future__ import annotations
@@ -15,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -22,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdlrm_gb300.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.c")
+MARSHAL = os.path.join(HERE, "_marshal.so")     # the dense network's argument checks (a CPython extension)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -42,7 +46,7 @@ def _sources() -> list[str]:
 def _digest() -> str:
     h = hashlib.sha256()
     files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)]
+        sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [MARSHAL_SRC, os.path.abspath(__file__)]
     for f in files:
         h.update(f.encode())
         with open(f, "rb") as fh:
@@ -55,7 +59,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link the library unless an up-to-date build exists."""
     stamp = os.path.join(BUILD, "stamp")
     digest = _digest()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == digest:
+    if not force and os.path.exists(LIB) and os.path.exists(MARSHAL) and os.path.exists(stamp) and \
+            open(stamp).read() == digest:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -81,6 +86,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = MARSHAL + f".{os.getpid()}.tmp"
+    r = subprocess.run([shutil.which("gcc") or "cc", "-O2", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+                        "-I", INCLUDE, "-o", tmp, MARSHAL_SRC], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {MARSHAL_SRC} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
     with open(stamp, "w") as f:
         f.write(digest)
     return LIB
