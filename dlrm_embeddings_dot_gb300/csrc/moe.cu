@@ -37,6 +37,10 @@ using namespace few;
 constexpr int kThreads = 256, kWarps = kThreads / kWarp;
 constexpr int kUpCluster = 4, kMaxSplit = 8;   // blocks of a cluster in moe_up, at most in moe_down
 constexpr int64_t kOwnRouter = 32 << 10;
+// Weights past this leave L2 first (half of L2: less may stay there from call to
+// call).  Streaming 805 MB so took 160 us instead of 181: the tokens, the
+// intermediate rows and the code itself stay in L2.
+constexpr int64_t kOnce = 64 << 20;
 constexpr int kMaxE = DLRM_MOE_MAX_EXPERTS, kMaxK = DLRM_MOE_MAX_TOP_K;
 constexpr int kGroup = 32;                     // tokens of an expert that are multiplied together
 constexpr int kMaxGroups = kMaxTokens * kMaxK / kGroup + kMaxE;
@@ -66,6 +70,7 @@ struct MoeArgs {
     void* h;                                // [kTerms][T][k][I]
     uint32_t* status;
     long long wait_cycles;
+    int once;                               // the weights are more than L2 keeps from call to call
 };
 
 // Which tokens chose which expert, in shared memory.
@@ -177,6 +182,7 @@ struct Ring {
     K1 k1;
     int k, end, at;
     uint32_t asked, taken;
+    uint64_t policy;   // 0: none
 
     __device__ __forceinline__ void start()
     {
@@ -199,8 +205,11 @@ struct Ring {
         if (threadIdx.x % kWarp == 0) {
             tc::mbar_expect_tx(&full[s], kStage);
 #pragma unroll
-            for (int i = 0; i < WT; ++i)
-                tc::tma_load_2d(mem + s * kStage + i * (kStage / WT), map, k, at + i * tile_rows, &full[s]);
+            for (int i = 0; i < WT; ++i) {
+                uint8_t* dst = mem + s * kStage + i * (kStage / WT);
+                if (policy) tc::tma_load_2d_hint(dst, map, k, at + i * tile_rows, &full[s], policy);
+                else tc::tma_load_2d(dst, map, k, at + i * tile_rows, &full[s]);
+            }
         }
         k += kSteps / WT * kStepK<T>;
         if (k >= end) {
@@ -236,12 +245,12 @@ struct Ring {
 
 template <typename T, int WT, typename Row, typename K0, typename K1>
 __device__ __forceinline__ Ring<T, WT, Row, K0, K1> make_ring(Rings& r, uint8_t* rings, const CUtensorMap* map,
-                                                              long long wait_cycles, int first, int stride, int items,
+                                                              const MoeArgs& a, int first, int stride, int items,
                                                               int tile_rows, Row row, K0 k0, K1 k1)
 {
     const int warp = threadIdx.x / kWarp;
-    return {map,  rings + warp * kStages * kStage, r.full + warp * kStages, &r.abort_flag, wait_cycles, first, stride, items,
-            tile_rows, row, k0, k1, 0, 0, 0, 0, 0};
+    return {map,  rings + warp * kStages * kStage, r.full + warp * kStages, &r.abort_flag, a.wait_cycles, first, stride, items,
+            tile_rows, row, k0, k1, 0, 0, 0, 0, 0, a.once ? tc::l2_evict_first() : 0};
 }
 
 __device__ __forceinline__ uint8_t* aligned128(uint8_t* p)
@@ -529,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
         auto all = [&](auto wt) {
             constexpr int W = decltype(wt)::value;
             auto ring = make_ring<T, W>(
-                sync, rings, &map, a.wait_cycles, first, stride, units, a.I,
+                sync, rings, &map, a, first, stride, units, a.I,
                 [&](int u) { return (lists.active[u / tiles] % kMaxE) * W * a.I + u % tiles * kRows; }, [&](int) { return k0; },
                 [&](int) { return k1; });
             ring.start();
@@ -599,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
         }
     };
     if constexpr (VEC) {
-        auto ring = make_ring<T, 1>(sync, rings, &map, a.wait_cycles, first, stride, items, 0,
+        auto ring = make_ring<T, 1>(sync, rings, &map, a, first, stride, items, 0,
                                     [&](int i) { return (lists.active[i / chunks] % kMaxE) * a.H + row0; }, k0, k1);
         ring.start();
         all([&](const Choice& c, int it, auto&& token, auto&& add) {
@@ -707,8 +716,18 @@ dlrm_status launch_moe(MoeArgs a, cudaStream_t st)
     const int most = resident_blocks(up, smem, C);
     const int chosen = a.E < a.T * a.k ? a.E : a.T * a.k;            // experts at most
     const int64_t units = (int64_t)chosen * ((a.I + kRows - 1) / kRows);
-    a.group = kWarps;
-    while (a.group > 1 && units * a.group > 16 * (int64_t)most * kWarps) a.group /= 2;   // many units: fewer meetings
+    // warps of a unit: the number with the least time in stages, a unit's overhead
+    // (its meeting in shared memory) being one
+    const int stage_k = kSteps / (a.gated ? 2 : 1) * kStepK<T>;
+    const int64_t stages = (a.H + stage_k - 1) / stage_k;
+    int64_t least = 0;
+    for (int G = kWarps; G >= 1; G /= 2) {
+        const int64_t groups = (int64_t)most * kWarps / G, cost = (units + groups - 1) / groups * ((stages + G - 1) / G + 1);
+        if (least == 0 || cost < least) {
+            least = cost;
+            a.group = G;
+        }
+    }
     int64_t blocks = (units * a.group + kWarps - 1) / kWarps;
     if (blocks > most) blocks = most;
     blocks = (blocks + C - 1) / C * C;
@@ -797,6 +816,7 @@ extern "C" dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_
     a.T = T, a.H = H, a.I = I, a.E = E, a.k = k, a.act = act, a.gated = gated != 0;
     a.y = d_y, a.ids = d_ids, a.probs = d_probs, a.h = d_workspace;
     a.status = d_status, a.wait_cycles = wait_limit_cycles();
+    a.once = (int64_t)E * (gated ? 3 : 2) * I * H * es > kOnce;
     // TMA and 16-byte loads where every row is on the grid (the workspace's are where I's are)
     const bool vec = rows_aligned16(d_x, ldx, T, es) && rows_aligned16(d_w_router, H, E, es) &&
                      rows_aligned16(d_w1, H, 2, es) && rows_aligned16(d_w2, I, 2, es) && H * es % 16 == 0 && I * es % 16 == 0;
