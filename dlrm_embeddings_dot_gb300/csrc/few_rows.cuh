@@ -324,16 +324,6 @@ inline int row_grid(const void* p, int64_t ld, int rows, int es)
     return rows_aligned16(p, ld, rows, es) ? 1 : 0;
 }
 
-// Calls fn(std::integral_constant<int, NT>) with the least NT of 1, 2, 4, 8 that covers n tokens.
-template <typename Fn>
-__device__ __forceinline__ void with_token_tiles(int n, Fn&& fn)
-{
-    if (n <= 8) fn(std::integral_constant<int, 1>{});
-    else if (n <= 16) fn(std::integral_constant<int, 2>{});
-    else if (n <= 32) fn(std::integral_constant<int, 4>{});
-    else fn(std::integral_constant<int, 8>{});
-}
-
 // ------------------------------------------------------- thread-block cluster
 __device__ __forceinline__ uint32_t cluster_rank()
 {

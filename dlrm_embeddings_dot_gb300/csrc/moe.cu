@@ -146,6 +146,15 @@ __device__ __forceinline__ uint32_t logit_key(float v)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// fn(std::integral_constant<int, NT>) with the least NT of 1, 2, 4 that covers n <= 32 tokens.
+template <typename Fn>
+__device__ __forceinline__ void with_group_tiles(int n, Fn&& fn)
+{
+    if (n <= 8) fn(std::integral_constant<int, 1>{});
+    else if (n <= 16) fn(std::integral_constant<int, 2>{});
+    else fn(std::integral_constant<int, 4>{});
+}
+
 __device__ __forceinline__ void group_sync(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -376,10 +385,53 @@ __device__ __forceinline__ void ring_times_tokens(R& ring, Token&& token, int n,
                         if (tok < n) out(i, tok, g + 8 * (d >> 1), acc[i][j][d]);
                     }
         };
-        if (n <= 8) with(std::integral_constant<int, 1>{});
-        else if (n <= 16) with(std::integral_constant<int, 2>{});
-        else with(std::integral_constant<int, 4>{});
+        if constexpr (std::is_same_v<T, float>) {
+            if (n <= 16) with(std::integral_constant<int, 2>{});
+            else with(std::integral_constant<int, 4>{});
+        } else {
+            with_group_tiles(n, with);
+        }
     }
+}
+
+// 16 experts' logits of n <= 8 NT tokens over [k0, k1) of H.  Short loops: a block
+// runs this once, and what takes its time is fetching the code.
+template <typename T, int NT, bool VEC, typename Token, typename Out>
+__device__ __forceinline__ void router_tile(const T* w0, const T* w8, Token&& token, int n, int k0, int k1, Out&& out)
+{
+    const int lane = threadIdx.x % kWarp, g = lane / 4, t = lane % 4;
+    const T* x[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) x[j] = token(min(j * 8 + g, n - 1));
+    auto chunk = [&](const T* p, int at) {
+        if constexpr (VEC) {
+            return at < k1 ? ldg_nc_l1_v4(p + at) : make_uint4(0, 0, 0, 0);
+        } else {
+            T e[kQ<T>];
+#pragma unroll
+            for (int i = 0; i < kQ<T>; ++i) e[i] = at + i < k1 ? __ldg(p + at + i) : from_f32<T>(0.f);
+            uint4 v;
+            memcpy(&v, e, 16);
+            return v;
+        }
+    };
+    float acc[NT][4] = {};
+#pragma unroll 1
+    for (int at = k0 + t * kQ<T>; at - t * kQ<T> < k1; at += kStepK<T>) {
+        const uint4 lo = chunk(w0, at), hi = chunk(w8, at);
+        uint4 b[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) b[j] = chunk(x[j], at);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mac16<T>(acc[j], lo, hi, b[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const int tok = j * 8 + 2 * t + (d & 1);
+            if (tok < n) out(tok, g + 8 * (d >> 1), acc[j][d]);
+        }
 }
 
 // Dynamic shared memory of moe_up: the rings, which the logits use first (they fit:
@@ -416,18 +468,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
     float* lp = smem;                        // [sub][T][E16]: partial logits
     float* lg = smem + sub * a.T * E16;      // [T][E16]: logits
     {
-        const int steps = (a.H + kStep<T> - 1) / kStep<T>;
-        const int per = (steps + C * sub - 1) / (C * sub) * kStep<T>;
+        const int steps = (a.H + kStepK<T> - 1) / kStepK<T>;
+        const int per = (steps + C * sub - 1) / (C * sub) * kStepK<T>;
         for (int i = warp; i < e_tiles * sub; i += kWarps) {
             const int tile = i % e_tiles, s = i / e_tiles;
             const int k0 = (rank * sub + s) * per, k1 = min(a.H, k0 + per);
-            const int e0 = tile * kRows + g;
+            const T* w0 = wr + (int64_t)min(tile * kRows + g, a.E - 1) * a.H;
+            const T* w8 = wr + (int64_t)min(tile * kRows + g + 8, a.E - 1) * a.H;
             for (int t0 = 0; t0 < a.T; t0 += kGroup) {
-                const T* w[1][2] = {{wr + (int64_t)min(e0, a.E - 1) * a.H, wr + (int64_t)min(e0 + 8, a.E - 1) * a.H}};
-                with_token_tiles(min(kGroup, a.T - t0), [&](auto nt) {
-                    rows_times_tokens<T, 1, decltype(nt)::value, VEC ? 1 : 0>(
-                        w, [&](int t) { return x + (t0 + t) * a.ldx; }, min(kGroup, a.T - t0), k0, k1, 0,
-                        [&](int, int t, int r, float v) { lp[(s * a.T + t0 + t) * E16 + tile * kRows + r] = v; });
+                const int n = min(kGroup, a.T - t0);
+                with_group_tiles(n, [&](auto nt) {
+                    router_tile<T, decltype(nt)::value, VEC>(
+                        w0, w8, [&](int t) { return x + (t0 + t) * a.ldx; }, n, k0, k1,
+                        [&](int t, int r, float v) { lp[(s * a.T + t0 + t) * E16 + tile * kRows + r] = v; });
                 });
             }
         }
@@ -562,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
                     const T* base = w1 + ((int64_t)c.e * WT * a.I + (int64_t)i * a.I) * a.H;
                     const T* w[1][2] = {{base + (int64_t)min(row0 + g, a.I - 1) * a.H,
                                          base + (int64_t)min(row0 + g + 8, a.I - 1) * a.H}};
-                    with_token_tiles(c.n, [&](auto nt) {
+                    with_group_tiles(c.n, [&](auto nt) {
                         rows_times_tokens<T, 1, decltype(nt)::value, 0>(
                             w, [&](int t) { return x + (int64_t)(c.entry[t] / kMaxK) * a.ldx; }, c.n, k0, k1, 0,
                             [&](int, int tok, int r, float v) { put(i, tok, r, v); });
@@ -620,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
             const T* base = w2 + (int64_t)c.e * a.H * a.I;
             const T* w[1][2] = {{base + (int64_t)min(row0 + g, a.H - 1) * a.I,
                                  base + (int64_t)min(row0 + g + 8, a.H - 1) * a.I}};
-            with_token_tiles(c.n, [&](auto nt) {
+            with_group_tiles(c.n, [&](auto nt) {
                 rows_times_tokens<T, 1, decltype(nt)::value, 0, kTerms<T>>(w, token, c.n, k0(it), k1(it), plane, add);
             });
         });
