@@ -5,7 +5,8 @@
 //   backward  dZ = a'(z) drop(dY);  dX = dZ W;  dW = dZ^T x;  db = sum dZ
 //
 // Few rows (few_rows): the forward streams the weights into matrix fragments
-// (linear_few_kernel); the other products run on tcgen05 (gemm_tc.cuh), which
+// (linear_few_kernel).  Few outputs (few_columns): it streams the rows of x so
+// (linear_thin_kernel).  The other products run on tcgen05 (gemm_tc.cuh), which
 // wants 2-byte operands with rows on the 16-byte grid.  pack_kernel lays out
 // again what is not like that: misaligned rows, and fp32 as three bf16 planes.
 #include "few_rows.cuh"
@@ -25,6 +26,13 @@ using gemm::Shape;
 // a block's 16 weight rows come with more token bytes from L2 than weight bytes.
 inline bool few_rows(int M, int N, int K) { return M <= 32 || (M <= few::kMaxTokens && (int64_t)N * K <= 1 << 23); }
 
+// Whether the forward streams the rows of x (linear_thin_kernel).  Measured, us,
+// streamed / tiles (whose 64 columns are mostly waste): 65536 x 256 fp16 5.6 / 16.8 for 1
+// output, 8.4 / 9.9 for 16 (fp32 13 / 71, 37 / 59); 300 x 64 1.8 / 6.1; but 1711 x 1285
+// 20.8 / 10.0 (fp32 35.1 / 17.6 for 16): a warp walks K alone, and there too few warps do.
+inline bool few_columns(int M, int N, int K) { return N <= 16 && (K <= 512 || M >= 1 << 14); }
+
+constexpr int kMaxSize = INT32_MAX - (1 << 20);   // tiles and chunks that start below it end below 2^31
 constexpr int kOneChunk = 1024;   // rows that grad_z_kernel takes as one chunk
 
 // ------------------------------------------------------------------ packing
@@ -190,6 +198,57 @@ dlrm_status launch_few(const void* x, int64_t ldx, const void* w, int64_t ldw, i
     return go(std::integral_constant<int, 8>{});
 }
 
+// ------------------------------------------------------------- few columns
+// The forward of up to 16 outputs (the logit layer): the rows of x are the stream
+// and the weights' rows the tokens.  A warp takes 16 rows of x at a time, the whole
+// of K, and 32 lanes finish its 16 x 16 outputs.
+template <typename T, int NT, int VEC>
+__global__ void __launch_bounds__(256, 2)
+linear_thin_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ w, int64_t ldw, int M, int N, int K,
+                   const __grid_constant__ Epilogue e)
+{
+    using namespace few;
+    pdl_wait();
+    __shared__ float tile[8][kRows][kPitch];
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, g = lane / 4;
+    const int tiles = (M + kRows - 1) / kRows;
+    const DropKey key = drop_key(e.drop);
+    for (int i = blockIdx.x * 8 + warp; i < tiles; i += gridDim.x * 8) {
+        const int m0 = i * kRows;
+        const T* rows[1][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) rows[0][b] = x + min(m0 + g + 8 * b, M - 1) * ldx;
+        rows_times_tokens<T, 1, NT, VEC>(rows, [&](int n) { return w + n * ldw; }, N, 0, K, 0,
+                                         [&](int, int n, int r, float v) { tile[warp][r][n] = v; });
+        __syncwarp();
+        const int row = m0 + lane / 2, col = lane % 2 * 8, n = N - col;
+        if (row < M && n > 0) {
+            float f[8], b[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) f[c] = c < n ? tile[warp][lane / 2][col + c] : 0.f;
+            bias8(e.bias, col, N, b);
+            finish8_any<T>(e, key, row, col, n, f, b);
+        }
+        __syncwarp();
+    }
+}
+
+template <typename T>
+dlrm_status launch_thin(const void* x, int64_t ldx, const void* w, int64_t ldw, int M, int N, int K, const Epilogue& e,
+                        cudaStream_t st)
+{
+    const int64_t want = (M + few::kRows * 8 - 1) / (few::kRows * 8), most = (int64_t)num_sms() * 2;
+    const int gx = few::row_grid(x, ldx, M, sizeof(T)), gw = few::row_grid(w, ldw, N, sizeof(T)), grid = gx < gw ? gx : gw;
+    auto go = [&](auto n) {
+        constexpr int NT = decltype(n)::value;
+        auto kern = grid == 2 ? linear_thin_kernel<T, NT, 2> : grid == 1 ? linear_thin_kernel<T, NT, 1> : linear_thin_kernel<T, NT, 0>;
+        return check_launch_pdl(launch_pdl(kern, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, (const T*)x,
+                                           ldx, (const T*)w, ldw, M, N, K, e),
+                                "linear_thin_kernel");
+    };
+    return N <= 8 ? go(std::integral_constant<int, 1>{}) : go(std::integral_constant<int, 2>{});
+}
+
 // ------------------------------------------------------- gradient of z and b
 // dZ = a'(pre) drop(dY) as an operand of the products (dz, may be NULL), and
 // column sums of it (partial [gridDim.y][N], may be NULL).  A block covers
@@ -305,6 +364,8 @@ dlrm_status check_sizes(const char* fn, dlrm_dtype dtype, int M, int N, int K, d
 {
     if (!dense_dtype_ok(dtype)) return fail(DLRM_ERR_INVALID_ARG, "%s: bad dtype", fn);
     if (M < 0 || N < 1 || K < 1) return fail(DLRM_ERR_INVALID_ARG, "%s: need M >= 0, N >= 1 and K >= 1", fn);
+    if (M > kMaxSize || N > kMaxSize || K > kMaxSize)
+        return fail(DLRM_ERR_UNSUPPORTED, "%s: sizes up to %d", fn, kMaxSize);
     if (act < DLRM_ACT_NONE || act > DLRM_ACT_SILU) return fail(DLRM_ERR_INVALID_ARG, "%s: bad activation", fn);
     return DLRM_OK;
 }
@@ -318,7 +379,10 @@ dlrm_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t
     return DLRM_OK;
 }
 
-bool sizes_ok(dlrm_dtype dtype, int M, int N, int K) { return dense_dtype_ok(dtype) && M >= 1 && N >= 1 && K >= 1; }
+bool sizes_ok(dlrm_dtype dtype, int M, int N, int K)
+{
+    return dense_dtype_ok(dtype) && M >= 1 && N >= 1 && K >= 1 && M <= kMaxSize && N <= kMaxSize && K <= kMaxSize;
+}
 
 // The products as shapes: output rows, output columns, summed index.
 Shape fwd_shape(dlrm_dtype dt, int M, int N, int K)
@@ -339,7 +403,7 @@ struct FwdLayout {
 FwdLayout fwd_layout(const void* x, int64_t ldx, const void* w, int64_t ldw, dlrm_dtype dt, int M, int N, int K)
 {
     FwdLayout l = {};
-    if (few_rows(M, N, K)) return l;
+    if (few_rows(M, N, K) || few_columns(M, N, K)) return l;
     l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, dt) : 0;
     l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
     l.partial = gemm::partial_bytes(fwd_shape(dt, M, N, K));
@@ -405,6 +469,7 @@ extern "C" dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void*
     return with_type(dtype, [&](auto t) -> dlrm_status {
         using T = decltype(t);
         if (few_rows(M, N, K)) return launch_few<T>(d_x, ldx, d_w, ldw, M, N, K, e, st);
+        if (few_columns(M, N, K)) return launch_thin<T>(d_x, ldx, d_w, ldw, M, N, K, e, st);
         uint8_t* ws = (uint8_t*)d_workspace;
         void *xs = l.x ? ws : nullptr, *wsp = l.w ? ws + l.x : nullptr;
         float* partial = (float*)(ws + l.x + l.w);

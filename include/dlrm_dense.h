@@ -81,7 +81,8 @@ dlrm_status dlrm_dropout_bwd(const void* d_grad_y, int64_t ldg, dlrm_dtype dtype
  * fp32 operands are split into three bf16 parts each, whose six products of
  * weight 2^-16 and more are summed on the tensor cores: the error stays at that
  * of an fp32 sum.  A product of two infinities is a NaN there, and infinite or
- * NaN operands otherwise give what fp32 gives.  Requires N >= 1, K >= 1.
+ * NaN operands otherwise give what fp32 gives.  Requires N >= 1, K >= 1 and sizes up to
+ * 2^31 - 2^20 - 1 (DLRM_ERR_UNSUPPORTED).
  */
 dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void* d_w, int64_t ldw, const float* d_bias,
                             const void* d_residual, int64_t ldr, dlrm_dtype dtype, int M, int N, int K, dlrm_act act,

@@ -68,6 +68,8 @@ def test_linear_fwd_refusals(L):
                dict(pre=ODD, ldp=8)):
         assert _fwd(L, **kw) == INVALID, kw
         assert "dlrm_linear_fwd" in dl.dlrm_last_error()
+    for big in (dict(M=2**31 - 1), dict(N=2**31 - 1, ldy=2**31), dict(K=2**31 - 1, ldx=2**31, ldw=2**31)):
+        assert _fwd(L, **big) == UNSUPPORTED, big
     assert _fwd(L, M=0) == OK and _fwd(L, M=0, x=None, y=None, w=None) == OK
 
 

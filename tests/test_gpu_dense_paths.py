@@ -31,9 +31,10 @@ def _gpu64(bound_of, *args):
     return bound_of(*[a.double() if isinstance(a, torch.Tensor) and a.is_floating_point() else a for a in args])
 
 
-# block pairs of 256 x 256 and 256 x 128, single blocks, split K, ragged last tiles, several tiles a block
+# block pairs of 256 x 256 and 256 x 128, single blocks, split K, ragged last tiles, several tiles a block; few outputs
 LARGE = [(8192, 1024, 480, "f16"), (40000, 264, 72, "bf16"), (2048, 512, 4096, "f16"), (300, 1032, 2056, "bf16"),
-         (5003, 515, 367, "f32"), (1024, 2048, 264, "f32"), (20000, 40, 1024, "bf16"), (70000, 8, 24, "f16")]
+         (5003, 515, 367, "f32"), (1024, 2048, 264, "f32"), (20000, 40, 1024, "bf16"), (70000, 8, 24, "f16"),
+         (40000, 13, 600, "f32"), (40000, 1, 256, "f16"), (2000, 5, 1304, "bf16"), (2000, 16, 1300, "f32")]
 
 
 @pytest.mark.parametrize("M,N,K,dtype", LARGE)
