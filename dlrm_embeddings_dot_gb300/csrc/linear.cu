@@ -6,11 +6,12 @@
 //
 // Few rows (few_rows): the forward streams the weights into matrix fragments
 // (linear_few_kernel).  Few outputs (few_columns): it streams the rows of x so
-// (linear_thin_kernel).  The other products run on tcgen05 (gemm_tc.cuh), which
+// (linear_thin_kernel, and thin_grad.cuh backward).  The other products run on tcgen05 (gemm_tc.cuh), which
 // wants 2-byte operands with rows on the 16-byte grid.  pack_kernel lays out
 // again what is not like that: misaligned rows, and fp32 as three bf16 planes.
 #include "few_rows.cuh"
 #include "gemm_tc.cuh"
+#include "thin_grad.cuh"
 
 namespace dlrm {
 namespace {
@@ -31,6 +32,9 @@ inline bool few_rows(int M, int N, int K) { return M <= 32 || (M <= few::kMaxTok
 // output, 8.4 / 9.9 for 16 (fp32 13 / 71, 37 / 59); 300 x 64 1.8 / 6.1; but 1711 x 1285
 // 20.8 / 10.0 (fp32 35.1 / 17.6 for 16): a warp walks K alone, and there too few warps do.
 inline bool few_columns(int M, int N, int K) { return N <= 16 && (K <= 512 || M >= 1 << 14); }
+
+// Whether the backward is the one pass of thin_grad.cuh.
+inline bool few_outputs(int N) { return N <= thin::kMaxOutputs; }
 
 constexpr int kMaxSize = INT32_MAX - (1 << 20);   // tiles and chunks that start below it end below 2^31
 constexpr int kOneChunk = 1024;   // rows that grad_z_kernel takes as one chunk
@@ -419,6 +423,10 @@ BwdLayout bwd_layout(const void* dy, int64_t ldg, const void* x, int64_t ldx, co
                      int M, int N, int K, dlrm_act act, double p)
 {
     BwdLayout l = {};
+    if (few_outputs(N)) {
+        l.total = l.sums = thin::workspace_bytes(dt, M, N, K);
+        return l;
+    }
     l.dz = act != DLRM_ACT_NONE || p > 0 || needs_pack(dy, ldg, M, dt) ? operand_bytes(M, N, dt) : 0;
     l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, dt) : 0;
     l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
@@ -526,6 +534,16 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
     if ((s = check_workspace(fn, d_workspace, workspace_bytes, l.total)) != DLRM_OK) return s;
     return with_type(dtype, [&](auto t) -> dlrm_status {
         using T = decltype(t);
+        if (few_outputs(N)) {
+            if (!d_grad_x && !d_grad_w && !d_grad_bias) return DLRM_OK;
+            thin::Grad a = {d_grad_y, d_pre, d_x, d_w, ldg, ldp, ldx, ldw, M, N, K, (int)act, drop};
+            a.dx = d_grad_x;
+            a.dw = d_grad_w;
+            a.lddx = lddx;
+            a.lddw = lddw;
+            a.db = d_grad_bias;
+            return thin::run<T>(dtype, a, (float*)d_workspace, st);
+        }
         const bool bf = dtype != DLRM_F16;
         uint8_t* ws = (uint8_t*)d_workspace;
         void *dz = l.dz ? ws : nullptr, *xs = l.x ? ws + l.dz : nullptr, *wsp = l.w ? ws + l.dz + l.x : nullptr;

@@ -75,6 +75,31 @@ def test_large_backward(cuda_lib, M, N, K, dtype, name, p):
     assert int(status.item()) == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N", [1, 2, 3, 4, 5, 8, 9, 13, 16])
+@pytest.mark.parametrize("M,K,pad", [(1, 1, 0), (5, 8, 0), (40, 520, 0), (31, 1027, 3), (513, 64, 8), (9001, 250, 0),
+                                     (66000, 16, 0)])
+def test_few_outputs_backward(cuda_lib, dtype, N, M, K, pad):
+    """One row chunk and many, rows on and off the 16-byte grid, several column blocks, every count of
+    outputs a kernel is made for and those between; each gradient alone has the same bits."""
+    g = torch.Generator().manual_seed(M + N)
+    x, w = (_rand(g, r, K + pad, dtype=dtype)[:, :K] for r in (M, N))
+    dy, z = _rand(g, M, N + pad, std=0.1, dtype=dtype)[:, :N], _rand(g, M, N, dtype=dtype)
+    dx, dw, db = torch.zeros_like(x), torch.zeros_like(w), torch.zeros(N, device=dev())
+    code, p = ref.ACT["gelu"], 0.2
+    ws = _ws(cuda_lib.dlrm_linear_bwd_workspace_size(dy, x, w, act=code, p=p))
+    cuda_lib.dlrm_linear_bwd(dy, x, w, z, dx, dw, db, act=code, p=p, rng=_rng(8, 9), workspace=ws)
+    kept, scale = ref.keep_scale(8, 9, M, N, p)
+    want = _gpu64(ref.linear_bwd, dy, x, w, z, "gelu", ref.U[dtype], kept.to(dev()), scale)
+    ref.assert_close(dx, *want["dx"], dtype, "dx")
+    ref.assert_close(dw, *want["dw"], dtype, "dw")
+    ref.assert_close(db, *want["db"], "f32", "db")
+    for only in range(3):
+        o = [torch.empty_like(t) if i == only else None for i, t in enumerate((dx, dw, db))]
+        cuda_lib.dlrm_linear_bwd(dy, x, w, z, *o, act=code, p=p, rng=_rng(8, 9), workspace=ws)
+        assert torch.equal(o[only], (dx, dw, db)[only])
+
+
 @pytest.fixture
 def wait_limit(cuda_lib):
     """Restores the wait limit whatever the test does."""
