@@ -81,6 +81,40 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int n)
     return r;
 }
 
+// The same for a run that starts anywhere: the 16-byte words that it lies in, shifted into
+// place, where those are inside the matrix [lo, hi) (nearly everywhere), else element by
+// element.  Columns from n on hold anything.  n >= 1.  A third of the instructions of
+// eight single loads, and each reads whole sectors.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8_shifted(const T* p, int n, const T* lo, const T* hi)
+{
+    constexpr int kWords = 2 * sizeof(T), kLoads = kWords / 4 + 1;   // 32-bit words of a run; 16-byte words it can touch
+    const uint32_t off = (uint32_t)(uintptr_t)p & 15u;
+    const uint4* base = reinterpret_cast<const uint4*>((const char*)p - off);
+    const int last = (int)(off + min(n, 8) * (int)sizeof(T) - 1) / 16;   // the last word with a column of the run
+    if ((uintptr_t)base < (uintptr_t)lo || (uintptr_t)(base + last + 1) > (uintptr_t)hi) return load8<T, false>(p, n);
+    uint32_t w[4 * kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const uint4 v = ldg_nc_v4(base + min(i, last));
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+    }
+    if (off & 8u)
+#pragma unroll
+        for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
+    if (off & 4u)
+#pragma unroll
+        for (int i = 0; i < kWords + 1; ++i) w[i] = w[i + 1];
+    Raw8<T> r;
+    uint32_t* out = &r.w[0].x;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) out[i] = sizeof(T) == 2 ? __funnelshift_r(w[i], w[i + 1], (off & 2u) * 8) : w[i];
+    return r;
+}
+
 template <typename T>
 __device__ __forceinline__ void widen8(const Raw8<T>& r, float (&f)[8])
 {

@@ -125,15 +125,17 @@ __device__ __forceinline__ uint32_t pack2(T lo, T hi)
 }
 
 // VEC: rows of x and dX are on the 16-byte grid and K is a multiple of eight.  Lane 4 g + q, step j
-// of a warp's eight products of each kind: for dW (column i of a product is lane group i's) column
-// 8 g + j of x, or j * 8 + g; for dX column 2 q + b of a product is 16 q + 2 j + b, or j * 8 + 2 q + b.
-// Measured at 65536 x 256 fp16, us, multiply-adds / products: MEASURED_MMA
+// of a warp's eight products of each kind: for dW column g of a product is column 8 g + j of x; for
+// dX column 2 q + b of a product is 16 q + 2 j + b (j * 8 + 2 q + b where rows go by shared memory).
+// Measured, us, products / multiply-adds as in fp32: 65536 x 256 fp16 22 / 22 for 1 output, 24 / 39
+// for 8, 30 / 70 for 16.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_constant__ Grad a)
 {
     pdl_wait();
     __shared__ __align__(16) T dzs[kTile * kPitch];
     __shared__ float red[8 * 8 * 64];
+    __shared__ __align__(16) T stage[VEC ? 1 : 8][16][72];   // a warp's 16 x 64 of dX where rows are off the 16-byte grid
     const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, q = lane % 4;
     const int cw = tid / 32 % a.cg, rw = tid / 32 / a.cg, step = 8 / a.cg;   // a.cg warps side by side
     const int64_t c0 = ((int64_t)blockIdx.x * a.cg + cw) * 64;
@@ -164,6 +166,7 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
     uint4* const mine = reinterpret_cast<uint4*>(dzs + tid * kPitch);
     mine[0] = mine[1] = make_uint4(0, 0, 0, 0);   // outputs past N stay zero
 
+    const T* const xend = (const T*)a.x + (a.M - 1) * a.ldx + a.K;
     // rows s + 2 q, + 1, + 8, + 9 of a tile; element j of a row is step j's
     auto fetch = [&](int t0, int rows, int s, uint4 (&v)[4]) {
 #pragma unroll
@@ -171,13 +174,9 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
             const int r = s + 2 * q + i % 2 + i / 2 * 8;
             const T* p = (const T*)a.x + (t0 + r) * a.ldx + c0;
             v[i] = make_uint4(0, 0, 0, 0);
-            if constexpr (VEC) {
-                if (r < rows && g * 8 < left) v[i] = ldg_nc_v4(reinterpret_cast<const uint4*>(p) + g);
-            } else {
-                T e[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) e[j] = r < rows && j * 8 + g < left ? __ldg(p + j * 8 + g) : zero;
-                memcpy(&v[i], e, 16);
+            if (r < rows && g * 8 < left) {
+                if constexpr (VEC) v[i] = ldg_nc_v4(reinterpret_cast<const uint4*>(p) + g);
+                else v[i] = load8_shifted<T>(p + g * 8, (int)min((int64_t)8, left - g * 8), (const T*)a.x, xend).w[0];
             }
         }
     };
@@ -203,6 +202,7 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
                 uint32_t d[4];
                 ldmatrix4<false>(d, at + (lane % 16 * kPitch + lane / 16 * 8) * 2);
                 uint32_t out[2][8];
+                if constexpr (!VEC) __syncwarp();   // the last rows have left the stage
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float o[4] = {};
@@ -213,21 +213,40 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int r = s + g + 8 * h;
-                    if (r >= rows) break;
                     T* p = (T*)a.dx + (t0 + r) * a.lddx + c0;
                     if constexpr (VEC) {
                         uint4* v = reinterpret_cast<uint4*>(p + q * 16);
-                        if (q * 16 < left) v[0] = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
-                        if (q * 16 + 8 < left) v[1] = make_uint4(out[h][4], out[h][5], out[h][6], out[h][7]);
+                        if (r < rows && q * 16 < left) v[0] = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
+                        if (r < rows && q * 16 + 8 < left) v[1] = make_uint4(out[h][4], out[h][5], out[h][6], out[h][7]);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            T e[2];
-                            memcpy(e, &out[h][j], 4);
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint32_t*>(&stage[tid / 32][g + 8 * h][j * 8 + 2 * q]) = out[h][j];
+                    }
+                }
+                if constexpr (!VEC) {
+                    // four rows at a time from shared memory, eight lanes a row: its whole 16-byte words, then the
+                    // elements before and behind them
+                    __syncwarp();
+                    const int lim = (int)min((int64_t)64, left), k = lane % 8;
 #pragma unroll
-                            for (int b = 0; b < 2; ++b)
-                                if (j * 8 + 2 * q + b < left) p[j * 8 + 2 * q + b] = e[b];
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 4 + lane / 8;
+                        if (s + r >= rows) break;
+                        const T* from = stage[tid / 32][r];
+                        T* p = (T*)a.dx + (t0 + s + r) * a.lddx + c0;
+                        const int off = (int)((uintptr_t)p >> 1 & 7), head = off ? 8 - off : 0, e = head + 8 * k;
+                        if (e + 8 <= lim) {
+                            const uint32_t* w = reinterpret_cast<const uint32_t*>(from) + e / 2;
+                            const uint32_t u[5] = {w[0], w[1], w[2], w[3], w[4]};
+                            const int sh = (e & 1) * 16;
+                            *reinterpret_cast<uint4*>(p + e) =
+                                make_uint4(__funnelshift_r(u[0], u[1], sh), __funnelshift_r(u[1], u[2], sh),
+                                           __funnelshift_r(u[2], u[3], sh), __funnelshift_r(u[3], u[4], sh));
                         }
+                        const int tail = lim > head ? head + (lim - head) / 8 * 8 + k : lim;
+                        if (k < min(head, lim)) p[k] = from[k];
+                        if (tail < lim) p[tail] = from[tail];
                     }
                 }
             }
@@ -259,7 +278,7 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
             for (int j = 0; j < 8; ++j)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
-                    red[(rw * 8 + g) * width + cw * 64 + (VEC ? 8 * (2 * q + b) + j : j * 8 + 2 * q + b)] = acc[j][2 * h + b];
+                    red[(rw * 8 + g) * width + cw * 64 + 8 * (2 * q + b) + j] = acc[j][2 * h + b];
             __syncthreads();
             for (int i = tid; i < 8 * width; i += 256) {
                 const int n = h * 8 + i / width;
@@ -462,8 +481,9 @@ inline Shape shape(dlrm_dtype dt, int M, int N, int K)
     const bool f32 = dt == DLRM_F32;
     const int unit = f32 ? columns(N) : 64, most_cg = f32 ? 64 : 8;
     const int units = (int)(((int64_t)K + unit - 1) / unit);
-    Shape s = {1, 0, 1, M};
-    while (s.cg < most_cg && s.cg < units) s.cg *= 2;
+    Shape s = {most_cg, 0, 1, M};
+    // as wide as leaves no more than an eighth of the columns idle, fp32 not under a warp's 256 bytes
+    while (s.cg > (f32 ? 8 : 1) && ((int64_t)units + s.cg - 1) / s.cg * s.cg * 8 > (int64_t)units * 9) s.cg /= 2;
     s.blocks_x = (units + s.cg - 1) / s.cg;
     const int least = f32 ? 4 * 256 / s.cg : 16 * 8 / s.cg;   // rows
     int64_t chunks = (int64_t)num_sms() * 2 / s.blocks_x, most = ((int64_t)M + least - 1) / least;
