@@ -76,7 +76,7 @@ def test_linear_fwd_refusals(L):
 def test_linear_workspace_refusals(L):
     sizes = {}
     for dt in (0, 1, 2):
-        for M, N, K in ((4, 8, 16), (1000, 40, 13), (5000, 520, 264)):
+        for M, N, K in ((4, 8, 16), (4, 24, 16), (1000, 40, 13), (5000, 520, 264), (5000, 8, 16)):
             need = L.dlrm_linear_fwd_workspace_size(FAKE, K, FAKE, K, dt, M, N, K)
             sizes[dt, M, K] = need
             if need:
@@ -84,9 +84,10 @@ def test_linear_workspace_refusals(L):
                 assert _fwd(L, dt=dt, M=M, N=N, K=K, ldx=K, ldw=K, ldy=N, ws=FAKE, wsb=need - 1) == WORKSPACE
                 assert _fwd(L, dt=dt, M=M, N=N, K=K, ldx=K, ldw=K, ldy=N, ws=FAKE + 16, wsb=need) == INVALID
             need = L.dlrm_linear_bwd_workspace_size(FAKE, N, FAKE, K, FAKE, K, dt, M, N, K, 1, 0.1)
-            assert need > 0
-            assert _bwd(L, dt=dt, M=M, N=N, K=K, ws=FAKE, wsb=need - 1) == WORKSPACE
-            assert _bwd(L, dt=dt, M=M, N=N, K=K, ws=None, wsb=need) == WORKSPACE
+            assert need > 0 or (M, N) == (4, 8)   # a few rows of few outputs are one chunk
+            if need:
+                assert _bwd(L, dt=dt, M=M, N=N, K=K, ws=FAKE, wsb=need - 1) == WORKSPACE
+                assert _bwd(L, dt=dt, M=M, N=N, K=K, ws=None, wsb=need) == WORKSPACE
     for bad in ((3, 4, 8, 16), (1, -1, 8, 16), (1, 4, 0, 16), (1, 4, 8, 0), (1, 0, 8, 16)):
         assert L.dlrm_linear_fwd_workspace_size(FAKE, 16, FAKE, 16, *bad) == 0
         assert L.dlrm_linear_bwd_workspace_size(FAKE, 16, FAKE, 16, FAKE, 16, *bad, 1, 0.1) == 0
@@ -102,7 +103,7 @@ def test_linear_bwd_refusals(L):
     for kw in (dict(g=None), dict(x=None), dict(w=None), dict(pre=None), dict(dt=3), dict(M=-1), dict(N=0), dict(K=0),
                dict(act=4), dict(p=1.5), dict(rng=None), dict(g=ODD), dict(x=ODD), dict(w=ODD), dict(pre=ODD),
                dict(dx=ODD), dict(dw=ODD), dict(db=0x10002), dict(ldg=7), dict(ldx=15), dict(ldw=15), dict(ldp=7),
-               dict(lddx=15), dict(lddw=15), dict(ws=FAKE + 8)):
+               dict(lddx=15), dict(lddw=15), dict(ws=FAKE + 8, N=24)):
         assert _bwd(L, **kw) == INVALID, kw
     assert _bwd(L, M=0, dw=None, db=None) == OK       # nothing to write
 
