@@ -40,7 +40,7 @@ inline dlrm_status check_launch(const char* what)
 
 // Launch with programmatic stream serialization: the launch is processed
 // while the previous kernel on the stream runs.  Every kernel launched this
-// way calls pdl_wait() before touching global memory, so it still sees all of
+// way calls pdl_wait() before touching global memory (but for Overlap's), so it still sees all of
 // the previous kernel's writes and makes none the previous kernel could see.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
@@ -122,7 +122,7 @@ constexpr int kWarp = 32;
 // attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// No kernel triggers its dependents early (griddepcontrol.launch_dependents):
+// Outside the dense gradient no kernel triggers its dependents early (griddepcontrol.launch_dependents):
 // the next grid is then scheduled only when this one completes, and the
 // attribute still hides its launch processing.  With an early trigger the
 // next grid's blocks took registers and shared memory on SMs as this grid's
@@ -130,6 +130,26 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // forward after the sparse update, the backward after the forward) started
 // with fewer blocks on those SMs: 0.851 ms per 64K fp32 training step with the
 // trigger, 0.808 ms without, 0.839 ms with plain launches.
+
+// Kernels of one call that do not read each other's results, run together.  The first
+// triggers its dependents once it has waited itself; the next, late, starts at once: what
+// came before the first is complete and visible, as no block of the first triggers sooner.
+// It waits for the first before it ends, so its own end still means that all before it is done.
+// Its blocks find room: the first's are all running by then.  The layer's gradient, us, in
+// turn / together: 256 x 512 x 1024 bf16 14.5 / 11.0, 4099 x 771 x 513 fp32 98 / 92, 65536 x
+// 1024 x 1024 fp16 267 / 264, 170 x 892 x 218 fp16 20 / 15.
+struct Overlap {
+    int late, trigger;
+};
+__device__ __forceinline__ void pdl_begin(const Overlap& o)
+{
+    if (!o.late) pdl_wait();
+    if (o.trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_end(const Overlap& o)
+{
+    if (o.late) pdl_wait();
+}
 
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t bit)
 {

@@ -59,6 +59,7 @@ struct Args {
     Epilogue e;
     uint32_t* status;
     long long wait_cycles;
+    Overlap overlap;
 };
 
 // Plane pair p of the fp32 products, (A plane << 2) | B plane: hi = 0, mid = 1, lo = 2.
@@ -282,7 +283,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
-    pdl_wait();
+    pdl_begin(a.overlap);
 
     if (warp == 0) {
         // -------------------------------------------------------- TMA producer
@@ -551,6 +552,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                          : "memory");
     }
     if (threadIdx.x == 0 && *abort_flag) set_status(a.status, DLRM_STATUS_TIMEOUT);
+    pdl_end(a.overlap);
 }
 
 // The partial tiles of a split product added in order, then the epilogue.
@@ -684,10 +686,11 @@ dlrm_status make_box_map(const char* fn, CUtensorMap* m, const void* p, int64_t 
 }
 
 // out = A B^T and the epilogue; T the type of the epilogue's tensors, bf
-// whether the operands are bf16 (fp16 otherwise).  partial: partial_bytes(s).
+// whether the operands are bf16 (fp16 otherwise).  partial: partial_bytes(s);
+// finish() has to follow.
 template <typename T>
 dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand& B, bool bf, const Epilogue& e,
-                float* partial, uint32_t* status, cudaStream_t st)
+                float* partial, uint32_t* status, cudaStream_t st, Overlap overlap = {})
 {
     const Plan p = plan(s);
     CUtensorMap ma, mb, mo = {}, mp = {}, mr = {};
@@ -728,6 +731,7 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     a.e = e;
     a.status = status;
     a.wait_cycles = wait_limit_cycles();
+    a.overlap = overlap;
     const int64_t tiles = tm * tn * p.splits, units = num_sms() / CG;
     const int grid = (int)(tiles < units ? tiles : units) * CG;
     const size_t smem = smem_bytes(b_rows, a.NS, a.warp_bytes);
@@ -735,13 +739,20 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
                        : (boxes ? gemm_kernel<T, false, true> : gemm_kernel<T, false, false>);
     cudaError_t ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (ce != cudaSuccess) return fail(DLRM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
-    r = check_launch_pdl(p.pair ? launch_cluster(kern, dim3(grid), dim3(kThreads), smem, st, 2, ma, mb, mo, mp, mr, a)
-                                : launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, ma, mb, mo, mp, mr, a),
-                         "gemm_kernel");
-    if (r != DLRM_OK || p.splits == 1) return r;
-    const int64_t runs = a.Np / 8 * s.M, want = (runs + 255) / 256, most = (int64_t)num_sms() * 8;
+    return check_launch_pdl(p.pair ? launch_cluster(kern, dim3(grid), dim3(kThreads), smem, st, 2, ma, mb, mo, mp, mr, a)
+                                   : launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, ma, mb, mo, mp, mr, a),
+                            "gemm_kernel");
+}
+
+// Adds up a split product's partial tiles.
+template <typename T>
+dlrm_status finish(const Shape& s, const Epilogue& e, const float* partial, cudaStream_t st)
+{
+    const Plan p = plan(s);
+    if (p.splits == 1) return DLRM_OK;
+    const int64_t Np = padded(s.N), runs = Np / 8 * s.M, want = (runs + 255) / 256, most = (int64_t)num_sms() * 8;
     return check_launch_pdl(launch_pdl(finish_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,
-                                       (const float*)partial, p.splits, a.Np, s.M, s.N, e),
+                                       partial, p.splits, Np, s.M, s.N, e),
                             "finish_kernel");
 }
 

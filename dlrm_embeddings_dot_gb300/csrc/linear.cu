@@ -78,9 +78,9 @@ struct PackJob {
 
 // Up to two matrices laid out as operands, runs of eight columns a thread.
 template <typename T>
-__global__ void __launch_bounds__(256) pack_kernel(PackJob j0, PackJob j1)
+__global__ void __launch_bounds__(256) pack_kernel(PackJob j0, PackJob j1, Overlap overlap)
 {
-    pdl_wait();
+    pdl_begin(overlap);
     const int64_t n0 = (int64_t)j0.rows * ((j0.cols + 7) / 8), n1 = (int64_t)j1.rows * ((j1.cols + 7) / 8);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n0 + n1; i += (int64_t)gridDim.x * 256) {
         const PackJob& j = i < n0 ? j0 : j1;
@@ -97,12 +97,13 @@ __global__ void __launch_bounds__(256) pack_kernel(PackJob j0, PackJob j1)
 }
 
 template <typename T>
-dlrm_status launch_pack(const PackJob& a, const PackJob& b, cudaStream_t st)
+dlrm_status launch_pack(const PackJob& a, const PackJob& b, cudaStream_t st, Overlap overlap = {})
 {
     const int64_t runs = (int64_t)a.rows * ((a.cols + 7) / 8) + (int64_t)b.rows * ((b.cols + 7) / 8);
     if (runs == 0) return DLRM_OK;
     const int64_t want = (runs + 255) / 256, most = (int64_t)num_sms() * 8;
-    return check_launch_pdl(launch_pdl(pack_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, a, b),
+    return check_launch_pdl(launch_pdl(pack_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, a, b,
+                                       overlap),
                             "pack_kernel");
 }
 
@@ -266,9 +267,9 @@ dlrm_status launch_thin(const void* x, int64_t ldx, const void* w, int64_t ldw, 
 template <typename T>
 __global__ void __launch_bounds__(256, 3)
 grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, int64_t ldp, int act, int vec,
-              Drop drop, int M, int N, int cg, int rows, void* __restrict__ dz, float* __restrict__ partial)
+              Drop drop, int M, int N, int cg, int rows, void* __restrict__ dz, float* __restrict__ partial, Overlap overlap)
 {
-    pdl_wait();
+    pdl_begin(overlap);
     __shared__ float red[256][8 + 1];
     const DropKey key = drop_key(drop);
     const int tx = threadIdx.x % cg, ty = threadIdx.x / cg, step = 256 / cg;
@@ -309,7 +310,7 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, 
             }
         }
     }
-    if (!partial) return;
+    if (!partial) return pdl_end(overlap);
 #pragma unroll
     for (int i = 0; i < 8; ++i) red[threadIdx.x][i] = sum[i];
     __syncthreads();
@@ -319,6 +320,7 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, 
         const int c = blockIdx.x * cg * 8 + i;
         if (c < N) partial[(int64_t)blockIdx.y * N + c] = s;
     }
+    pdl_end(overlap);
 }
 
 struct GradZ {
@@ -349,9 +351,9 @@ GradZ grad_z_shape(int M, int N)
 
 // out[n] = the sum of partial's rows: 32 columns a block, 32 threads a column.
 __global__ void __launch_bounds__(1024)
-sum_rows_kernel(const float* __restrict__ partial, int rows, int N, float* __restrict__ out)
+sum_rows_kernel(const float* __restrict__ partial, int rows, int N, float* __restrict__ out, Overlap overlap)
 {
-    pdl_wait();
+    pdl_begin(overlap);
     __shared__ float red[32][33];
     const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, n = blockIdx.x * 32 + tx;
     float s = 0.f;
@@ -365,6 +367,7 @@ sum_rows_kernel(const float* __restrict__ partial, int rows, int N, float* __res
         for (int y = 1; y < 32; ++y) s += red[y][tx];
         out[n] = s;
     }
+    pdl_end(overlap);
 }
 
 // ------------------------------------------------------------------- checks
@@ -420,7 +423,7 @@ FwdLayout fwd_layout(const void* x, int64_t ldx, const void* w, int64_t ldw, dlr
 }
 
 struct BwdLayout {
-    size_t dz, x, w, sums, partial, total;
+    size_t dz, x, w, sums, partial_x, partial_w, total;
 };
 
 BwdLayout bwd_layout(const void* dy, int64_t ldg, const void* x, int64_t ldx, const void* w, int64_t ldw, dlrm_dtype dt,
@@ -436,9 +439,9 @@ BwdLayout bwd_layout(const void* dy, int64_t ldg, const void* x, int64_t ldx, co
     l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
     const GradZ g = grad_z_shape(M, N);
     l.sums = g.chunks > 1 ? dlrm_ws_align((size_t)g.chunks * N * 4) : 0;
-    const size_t a = gemm::partial_bytes(grad_shape(dt, M, K, N)), b = gemm::partial_bytes(grad_shape(dt, N, K, M));
-    l.partial = a > b ? a : b;
-    l.total = l.dz + l.x + l.w + l.sums + l.partial;
+    l.partial_x = gemm::partial_bytes(grad_shape(dt, M, K, N));
+    l.partial_w = gemm::partial_bytes(grad_shape(dt, N, K, M));
+    l.total = l.dz + l.x + l.w + l.sums + l.partial_x + l.partial_w;
     return l;
 }
 
@@ -490,9 +493,10 @@ extern "C" dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void*
         if (wsp) jw = {d_w, ldw, N, K, rows_aligned16(d_w, ldw, N, es), wsp};
         const dlrm_status r = launch_pack<T>(jx, jw, st);
         if (r != DLRM_OK) return r;
-        return gemm::run<T>(fn, fwd_shape(dtype, M, N, K), operand<T>(d_x, ldx, M, K, xs, false),
-                                          operand<T>(d_w, ldw, N, K, wsp, false), dtype != DLRM_F16, e, partial,
-                                          d_status, st);
+        const Shape z = fwd_shape(dtype, M, N, K);
+        const dlrm_status q = gemm::run<T>(fn, z, operand<T>(d_x, ldx, M, K, xs, false), operand<T>(d_w, ldw, N, K, wsp, false),
+                                           dtype != DLRM_F16, e, partial, d_status, st);
+        return q == DLRM_OK ? gemm::finish<T>(z, e, partial, st) : q;
     });
 }
 
@@ -552,42 +556,47 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
         uint8_t* ws = (uint8_t*)d_workspace;
         void *dz = l.dz ? ws : nullptr, *xs = l.x ? ws + l.dz : nullptr, *wsp = l.w ? ws + l.dz + l.x : nullptr;
         float* sums = (float*)(ws + l.dz + l.x + l.w);
-        float* partial = (float*)(ws + l.dz + l.x + l.w + l.sums);
+        float* px = (float*)(ws + l.dz + l.x + l.w + l.sums);
+        float* pw = (float*)(ws + l.dz + l.x + l.w + l.sums + l.partial_x);
+        // the copies and dZ run together, then dX, dW and the sum of the bias gradient
         const bool products = d_grad_x || d_grad_w;
-        dlrm_status r = DLRM_OK;
-        if ((dz && products) || d_grad_bias) {
-            const GradZ g = grad_z_shape(M, N);
+        const GradZ g = grad_z_shape(M, N);
+        const bool make_z = (dz && products) || d_grad_bias, sum = d_grad_bias && g.chunks > 1;
+        PackJob jx = {}, jw = {};
+        if (xs && d_grad_w) jx = {d_x, ldx, M, K, rows_aligned16(d_x, ldx, M, es), xs};
+        if (wsp && d_grad_x) jw = {d_w, ldw, N, K, rows_aligned16(d_w, ldw, N, es), wsp};
+        const bool packs = jx.src || jw.src;
+        dlrm_status r = launch_pack<T>(jx, jw, st, {0, make_z});
+        if (r == DLRM_OK && make_z) {
             const int vec = rows_aligned16(d_grad_y, ldg, M, es) && (act == DLRM_ACT_NONE || rows_aligned16(d_pre, ldp, M, es));
             r = check_launch_pdl(launch_pdl(grad_z_kernel<T>, dim3(g.blocks_x, g.chunks), dim3(256), 0, st,
                                             (const T*)d_grad_y, ldg, (const T*)d_pre, ldp, (int)act, vec, drop, M, N,
-                                            g.cg, g.rows, products ? dz : nullptr, d_grad_bias ? (g.chunks > 1 ? sums : d_grad_bias) : nullptr),
+                                            g.cg, g.rows, products ? dz : nullptr,
+                                            d_grad_bias ? (sum ? sums : d_grad_bias) : nullptr, Overlap{packs, 0}),
                                  "grad_z_kernel");
-            if (r == DLRM_OK && d_grad_bias && g.chunks > 1)
-                r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 31) / 32), dim3(1024), 0, st,
-                                                (const float*)sums, g.chunks, N, d_grad_bias),
-                                     "sum_rows_kernel");
         }
-        if (r == DLRM_OK) {
-            PackJob jx = {}, jw = {};
-            if (xs && d_grad_w) jx = {d_x, ldx, M, K, rows_aligned16(d_x, ldx, M, es), xs};
-            if (wsp && d_grad_x) jw = {d_w, ldw, N, K, rows_aligned16(d_w, ldw, N, es), wsp};
-            r = launch_pack<T>(jx, jw, st);
-        }
-        Epilogue e = {};
+        Epilogue ex = {}, ew = {};
+        const Shape sx = grad_shape(dtype, M, K, N), sw = grad_shape(dtype, N, K, M);
         if (r == DLRM_OK && d_grad_x) {
-            e.out = d_grad_x;
-            e.ldo = lddx;
-            e.vec = epilogue_vec(e, M, es);
-            r = gemm::run<T>(fn, grad_shape(dtype, M, K, N), operand<T>(d_grad_y, ldg, M, N, dz, false),
-                                          operand<T>(d_w, ldw, N, K, wsp, true), bf, e, partial, d_status, st);
+            ex.out = d_grad_x;
+            ex.ldo = lddx;
+            ex.vec = epilogue_vec(ex, M, es);
+            r = gemm::run<T>(fn, sx, operand<T>(d_grad_y, ldg, M, N, dz, false), operand<T>(d_w, ldw, N, K, wsp, true), bf, ex,
+                             px, d_status, st, {0, d_grad_w || sum});
         }
         if (r == DLRM_OK && d_grad_w) {
-            e.out = d_grad_w;
-            e.ldo = lddw;
-            e.vec = epilogue_vec(e, N, es);
-            r = gemm::run<T>(fn, grad_shape(dtype, N, K, M), operand<T>(d_grad_y, ldg, M, N, dz, true),
-                                         operand<T>(d_x, ldx, M, K, xs, true), bf, e, partial, d_status, st);
+            ew.out = d_grad_w;
+            ew.ldo = lddw;
+            ew.vec = epilogue_vec(ew, N, es);
+            r = gemm::run<T>(fn, sw, operand<T>(d_grad_y, ldg, M, N, dz, true), operand<T>(d_x, ldx, M, K, xs, true), bf, ew,
+                             pw, d_status, st, {d_grad_x != nullptr, sum});
         }
+        if (r == DLRM_OK && sum)
+            r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 31) / 32), dim3(1024), 0, st, (const float*)sums,
+                                            g.chunks, N, d_grad_bias, Overlap{products, 0}),
+                                 "sum_rows_kernel");
+        if (r == DLRM_OK && d_grad_x) r = gemm::finish<T>(sx, ex, px, st);
+        if (r == DLRM_OK && d_grad_w) r = gemm::finish<T>(sw, ew, pw, st);
         return r;
     });
 }

@@ -100,6 +100,43 @@ def test_few_outputs_backward(cuda_lib, dtype, N, M, K, pad):
         assert torch.equal(o[only], (dx, dw, db)[only])
 
 
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("M,N,K,dtype", [(256, 512, 1024, "bf16"), (3000, 515, 130, "f32"), (5000, 64, 2056, "f16"),
+                                         (200, 100, 13, "f16"), (3000, 8, 130, "bf16")])
+def test_gradients_back_to_back(cuda_lib, M, N, K, dtype, graph):
+    """A call's kernels overlap one another, never those of the call before or after: gradients in one
+    workspace, each fed by the last one's dX, have the bits of calls with a synchronize between."""
+    g = torch.Generator().manual_seed(K)
+    w, z, dy = _rand(g, N, K, std=K**-0.5, dtype=dtype), _rand(g, M, N, dtype=dtype), _rand(g, M, N, dtype=dtype)
+    x0 = _rand(g, M, K, dtype=dtype)
+    ws = _ws(cuda_lib.dlrm_linear_bwd_workspace_size(dy, x0, w, act=3, p=0.1))
+    steps = 8
+    dx = [torch.zeros_like(x0) for _ in range(steps)]
+    dw, db = [torch.zeros_like(w) for _ in range(steps)], [torch.zeros(N, device=dev()) for _ in range(steps)]
+    rng = _rng(2, 3)
+
+    def run(sync):
+        for i in range(steps):
+            cuda_lib.dlrm_linear_bwd(dy, dx[i - 1] if i else x0, w, z, dx[i], dw[i], db[i], act=3, p=0.1, rng=rng, workspace=ws)
+            dy.mul_(-1)
+            if sync:
+                torch.cuda.synchronize()
+
+    run(True)
+    want = [t.clone() for t in dx + dw + db]
+    for t in dx + dw + db:
+        t.zero_()
+    if graph:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run(False)
+        graph.replay()
+    else:
+        run(False)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(dx + dw + db, want))
+
+
 @pytest.fixture
 def wait_limit(cuda_lib):
     """Restores the wait limit whatever the test does."""
