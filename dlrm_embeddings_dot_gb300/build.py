@@ -45,7 +45,7 @@ def _sources() -> list[str]:
 
 def _digest() -> str:
     h = hashlib.sha256()
-    files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
+    files = _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))) + \
         sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [MARSHAL_SRC, os.path.abspath(__file__)]
     for f in files:
         h.update(f.encode())

@@ -27,14 +27,16 @@
 #include <mutex>
 
 #include "few_rows.cuh"
+#include "moe_layout.h"
 #include "tcgen05.cuh"
 
 namespace dlrm {
 namespace {
 
 using namespace few;
+using moe::kRing, moe::kStage, moe::kStages, moe::kSteps, moe::kThreads, moe::kWarps;
+static_assert(moe::kRows == few::kRows && moe::kPitch == few::kPitch);
 
-constexpr int kThreads = 256, kWarps = kThreads / kWarp;
 constexpr int kUpCluster = 4, kMaxSplit = 8;   // blocks of a cluster in moe_up, at most in moe_down
 constexpr int64_t kOwnRouter = 32 << 10;
 // Weights past this leave L2 first (half of L2: less may stay there from call to
@@ -44,8 +46,6 @@ constexpr int64_t kOnce = 64 << 20;
 constexpr int kMaxE = DLRM_MOE_MAX_EXPERTS, kMaxK = DLRM_MOE_MAX_TOP_K;
 constexpr int kGroup = 32;                     // tokens of an expert that are multiplied together
 constexpr int kMaxGroups = kMaxTokens * kMaxK / kGroup + kMaxE;
-constexpr int kStages = 2, kSteps = 8, kStage = kSteps * 1024;   // a step: 16 rows by 64 bytes
-constexpr int kRing = kWarps * kStages * kStage;
 
 template <typename T>
 constexpr int kQ = 16 / (int)sizeof(T);        // values of a lane's chunk
@@ -262,9 +262,9 @@ __device__ __forceinline__ Ring<T, WT, Row, K0, K1> make_ring(Rings& r, uint8_t*
             tile_rows, row, k0, k1, 0, 0, 0, 0, 0, a.once ? tc::l2_evict_first() : 0};
 }
 
-__device__ __forceinline__ uint8_t* aligned128(uint8_t* p)
+__device__ __forceinline__ uint8_t* shared_area(uint8_t* raw)
 {
-    return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 127) & ~(uintptr_t)127);
+    return reinterpret_cast<uint8_t*>(moe::area(reinterpret_cast<uintptr_t>(raw)));
 }
 
 __device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
@@ -434,21 +434,11 @@ __device__ __forceinline__ void router_tile(const T* w0, const T* w8, Token&& to
         }
 }
 
-// Dynamic shared memory of moe_up: the rings, which the logits use first (they fit:
-// 2 x 64 x 256 floats at most), then the partial tiles.  Without rings the
-// partial tiles are over the logits.
-inline size_t up_bytes(int T, int E, int nt, bool rings)
-{
-    const int e_tiles = (E + kRows - 1) / kRows, sub = e_tiles < kWarps ? kWarps / e_tiles : 1;
-    const size_t logits = (size_t)(sub + 1) * T * e_tiles * kRows * 4, red = (size_t)kWarps * 2 * nt * 8 * kPitch * 4;
-    return rings ? kRing + red + 128 : logits > red ? logits : red;
-}
-
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_constant__ CUtensorMap map, MoeArgs a)
 {
     extern __shared__ uint8_t raw[];
-    uint8_t* rings = aligned128(raw);
+    uint8_t* rings = shared_area(raw);
     float* smem = reinterpret_cast<float*>(rings);
     __shared__ Lists lists;
     __shared__ uint8_t ids_s[kMaxTokens * kMaxK];
@@ -462,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
     pdl_wait();
 
     // ---- the router's logits: this block's share of H
-    const int e_tiles = (a.E + kRows - 1) / kRows, E16 = e_tiles * kRows;
-    const int sub = e_tiles < kWarps ? kWarps / e_tiles : 1;     // warps that split an expert tile's K
+    const int e_tiles = moe::expert_tiles(a.E), E16 = e_tiles * kRows;
+    const int sub = moe::router_split(a.E);
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
     float* lp = smem;                        // [sub][T][E16]: partial logits
     float* lg = smem + sub * a.T * E16;      // [T][E16]: logits
@@ -552,8 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
     const int WT = a.gated ? 2 : 1, stage_k = kSteps / WT * kStepK<T>;
     const int per = ((a.H + stage_k - 1) / stage_k + G - 1) / G * stage_k;
     const int k0 = wg * per, k1 = min(a.H, k0 + per);
-    const int nt_max = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
-    const int tile_floats = nt_max * 8 * kPitch;
+    const int tile_floats = moe::token_tiles(a.T) * 8 * kPitch;
     float* red = reinterpret_cast<float*>(rings + (VEC ? kRing : 0));   // [warp][2][token][kPitch]
     T* h = (T*)a.h;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the rings were the logits' memory
@@ -630,7 +619,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_constant__ CUtensorMap map, MoeArgs a)
 {
     extern __shared__ uint8_t raw[];
-    uint8_t* rings = aligned128(raw);
+    uint8_t* rings = shared_area(raw);
     float* smem = reinterpret_cast<float*>(rings + (VEC ? kRing : 0));   // [warp][token][kPitch]: each warp's sums
     __shared__ Lists lists;
     __shared__ Rings sync;
@@ -759,8 +748,7 @@ dlrm_status launch_moe(MoeArgs a, cudaStream_t st)
         if (s == DLRM_OK) s = weight_map<T>(&m2, a.w2, (int64_t)a.E * a.H, a.I, kSteps);
         if (s != DLRM_OK) return s;
     }
-    const int nt = a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
-    const size_t smem = up_bytes(a.T, a.E, nt, VEC);
+    const size_t smem = moe::asked(moe::up_used(a.T, a.E, VEC));
     auto up = moe_up_kernel<T, VEC>;
     cudaError_t e = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return fail(DLRM_ERR_CUDA, "dlrm_moe_fwd: %s", cudaGetErrorString(e));
@@ -789,7 +777,7 @@ dlrm_status launch_moe(MoeArgs a, cudaStream_t st)
     if (s != DLRM_OK) return s;
 
     const int row_tiles = (a.H + kRows - 1) / kRows;
-    const size_t down = (VEC ? kRing + 128 : 0) + (size_t)kWarps * a.T * kPitch * 4;
+    const size_t down = moe::asked(moe::down_used(a.T, VEC));
     auto kern = moe_down_kernel<T, VEC>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)down);
     if (e != cudaSuccess) return fail(DLRM_ERR_CUDA, "dlrm_moe_fwd: %s", cudaGetErrorString(e));
