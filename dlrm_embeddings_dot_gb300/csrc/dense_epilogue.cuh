@@ -17,6 +17,7 @@ struct Epilogue {
     int act;
     int vec;             // rows of res, pre and out all start on 16-byte boundaries
     Drop drop;
+    float scale = 1.f;   // of the product (1 where there is a bias)
 };
 
 inline int epilogue_vec(const Epilogue& e, int M, int es)
@@ -70,7 +71,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, const DropKey& key, i
                                         const float (&b)[8], const Raw8<T>& r)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] += b[i];
+    for (int i = 0; i < 8; ++i) f[i] = fmaf(f[i], e.scale, b[i]);   // zeros without a bias
     if (e.pre) store8<T, VEC>((T*)e.pre + row * e.ldp + col, n, f);
     act_n(f, e.act);
     if (e.drop.thr) drop8(f, e.drop, key, (uint32_t)row, (uint32_t)col >> 3);

@@ -159,6 +159,22 @@ __device__ __forceinline__ void split1(float v, uint32_t& hi, uint32_t& mid, flo
     lo = r - __uint_as_float(mid);
 }
 
+// A gradient as the sum of two values of a 2-byte type: hi rounded, kept finite, and the
+// rest.  An infinity or NaN goes whole into lo.  fp16 gets 7/8 of it: a slope of up to
+// 1.13 (GELU) times any fp16 number then is in range, and no more than a fifth of a
+// bit is lost at the range's other end.
+template <typename T>
+constexpr float kFit = std::is_same_v<T, __half> ? 0.875f : 1.f;
+
+template <typename T>
+__device__ __forceinline__ void split2(float v, float& hi, float& lo)
+{
+    constexpr float kMost = std::is_same_v<T, __half> ? 65504.f : 3.38953139e38f;
+    v *= kFit<T>;
+    hi = to_f32(from_f32<T>(fmaxf(fminf(v, kMost), -kMost)));
+    lo = v - hi;
+}
+
 // -------------------------------------------------------------- activations
 // The functions of the header's definitions.  NaN passes through each.  The
 // exponential and the reciprocal are the hardware's approximations (two units in

@@ -21,7 +21,8 @@
 // epilogue of this one.
 //
 // fp32 operands come as three bf16 planes (see split planes in linear.cu); the
-// K loop then runs over six plane pairs, the smallest products first.  Few
+// K loop then runs over six plane pairs, the smallest products first.  A gradient
+// that its 2-byte type does not hold comes as two planes of A.  Few
 // output tiles: K is split over blocks, each writing its fp32 partial tile, and
 // finish_kernel adds them in order and applies the epilogue.
 #pragma once
@@ -47,7 +48,7 @@ constexpr int kSmemLimit = 232448;  // 227 KB opt-in per block
 struct Args {
     int M, N;
     int kb, last_steps;             // 64-wide blocks of K, and 16-wide steps of the last one
-    int pairs;                      // plane pairs: 1, or 6 for fp32
+    int pairs;                      // plane pairs: 1, 2 (A has two planes), or 6 for fp32
     int splits;                     // parts of K; above 1 the tiles go to `partial`
     int tiles_m, tiles_n, BN, NS;
     int a_mn, b_mn;                 // operand layouts
@@ -62,11 +63,12 @@ struct Args {
     Overlap overlap;
 };
 
-// Plane pair p of the fp32 products, (A plane << 2) | B plane: hi = 0, mid = 1, lo = 2.
+// Plane pair p, (A plane << 2) | B plane, the small products first.  fp32: planes hi = 0,
+// mid = 1, lo = 2 of both; two pairs: planes hi = 0, lo = 1 of A.
 __device__ __forceinline__ int plane_pair(int pairs, int p)
 {
     constexpr uint32_t order = 0x2u | 0x8u << 4 | 0x5u << 8 | 0x1u << 12 | 0x4u << 16 | 0x0u << 20;
-    return pairs == 1 ? 0 : (int)(order >> (4 * p)) & 15;
+    return pairs == kMaxPairs ? (int)(order >> (4 * p)) & 15 : p + 1 < pairs ? 0x4 : 0;
 }
 
 // A slice of 32 rows as a TMA box: rows of 64 bytes with the 64-byte swizzle
@@ -190,7 +192,8 @@ __device__ __forceinline__ void ragged_slice(const Epilogue& e, const DropKey& k
 #pragma unroll
         for (int i = 0; i < kTurn; ++i) {
             const int r = r0 + i;
-            f[i] = bias + *reinterpret_cast<const float*>(scratch + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4);
+            const float v = *reinterpret_cast<const float*>(scratch + r * 128 + (((lane / 4) ^ (r & 7)) << 4) + lane % 4 * 4);
+            f[i] = fmaf(v, e.scale, bias);
         }
         if (e.res) {
 #pragma unroll
@@ -482,6 +485,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 #pragma unroll
                             for (int i = 0; i < kSlice; ++i) f[i] += c0 + i < cols ? __ldg(bias + i) : 0.f;
                         }
+                    } else if (a.e.scale != 1.f) {
+#pragma unroll
+                        for (int i = 0; i < kSlice; ++i) f[i] *= a.e.scale;
                     }
                     __syncwarp();
                     if (a.e.pre) write_box_row<T>(pre_box, f);

@@ -44,9 +44,9 @@ constexpr int kMaxSize = INT32_MAX - (1 << 20);   // tiles and chunks that start
 constexpr int kOneChunk = 1024;   // rows that grad_z_kernel takes as one chunk
 
 // ------------------------------------------------------------------ packing
-// Stores eight columns as a 2-byte operand; fp32 as three planes.
+// Stores eight columns as a 2-byte operand; fp32 as three planes, `two`: as two.
 template <typename T>
-__device__ __forceinline__ void store_operand8(void* dst, int64_t at, int64_t plane, const float (&f)[8])
+__device__ __forceinline__ void store_operand8(void* dst, int64_t at, int64_t plane, const float (&f)[8], bool two = false)
 {
     if constexpr (std::is_same_v<T, float>) {
         uint32_t hi[8], mid[8];
@@ -64,6 +64,12 @@ __device__ __forceinline__ void store_operand8(void* dst, int64_t at, int64_t pl
         *reinterpret_cast<uint4*>(p) = h;
         *reinterpret_cast<uint4*>(p + plane) = m;
         *reinterpret_cast<uint4*>(p + 2 * plane) = pack8<bf16>(lo);
+    } else if (two) {
+        float hi[8], lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split2<T>(f[i], hi[i], lo[i]);
+        *reinterpret_cast<uint4*>((T*)dst + at) = pack8<T>(hi);
+        *reinterpret_cast<uint4*>((T*)dst + at + plane) = pack8<T>(lo);
     } else {
         *reinterpret_cast<uint4*>((T*)dst + at) = pack8<T>(f);
     }
@@ -107,12 +113,24 @@ dlrm_status launch_pack(const PackJob& a, const PackJob& b, cudaStream_t st, Ove
                             "pack_kernel");
 }
 
-// A matrix argument as an operand: itself, or its copy at ws.
-template <typename T>
-Operand operand(const void* p, int64_t ld, int rows, int cols, void* ws, bool mn)
+// A matrix argument as an operand: itself, or its copy at ws of `planes` planes.
+Operand operand(const void* p, int64_t ld, int rows, int cols, void* ws, int planes, bool mn)
 {
     if (!ws) return {p, ld, 0, 1, mn};
-    return {ws, padded(cols), rows * padded(cols), std::is_same_v<T, float> ? 3 : 1, mn};
+    return {ws, padded(cols), rows * padded(cols), planes, mn};
+}
+
+int planes_of(dlrm_dtype dt) { return dt == DLRM_F32 ? 3 : 1; }
+
+// Planes of dZ, held without the dropout's scale (that goes to the products' sums): a'
+// of NONE and RELU is 0 or 1, so it is dY's own values and one plane of the type
+// holds it.  The other slopes need the digits behind: rounded to one plane the
+// gradients' error against 64 bits was 1.4 times that of their own last rounding
+// (256 x 512 x 1024 bf16: 2.3e-3, two planes 1.7e-3), and fp16 lost what dY / (1 - p)
+// takes past 65504.
+int z_planes(dlrm_dtype dt, dlrm_act act)
+{
+    return dt == DLRM_F32 ? 3 : act == DLRM_ACT_GELU || act == DLRM_ACT_SILU ? 2 : 1;
 }
 
 bool needs_pack(const void* p, int64_t ld, int rows, dlrm_dtype dt)
@@ -120,10 +138,7 @@ bool needs_pack(const void* p, int64_t ld, int rows, dlrm_dtype dt)
     return dt == DLRM_F32 || !rows_aligned16(p, ld, rows, 2);
 }
 
-size_t operand_bytes(int rows, int cols, dlrm_dtype dt)
-{
-    return dlrm_ws_align((size_t)(dt == DLRM_F32 ? 3 : 1) * rows * padded(cols) * 2);
-}
+size_t operand_bytes(int rows, int cols, int planes) { return dlrm_ws_align((size_t)planes * rows * padded(cols) * 2); }
 
 // --------------------------------------------------------------- few rows
 // The forward of up to 64 rows: a cluster owns 16 output columns (weight rows),
@@ -259,15 +274,16 @@ dlrm_status launch_thin(const void* x, int64_t ldx, const void* w, int64_t ldw, 
 }
 
 // ------------------------------------------------------- gradient of z and b
-// dZ = a'(pre) drop(dY) as an operand of the products (dz, may be NULL), and
-// column sums of it (partial [gridDim.y][N], may be NULL).  A block covers
+// dZ = a'(pre) drop(dY) as an operand of the products (dz, may be NULL; two: of two
+// planes), and column sums of it times scale (partial [gridDim.y][N], may be NULL).  A block covers
 // cg * 8 columns and `rows` rows: a thread owns eight columns of every
 // (256 / cg)-th row and adds them up in registers, then the block adds its
 // threads' sums in shared memory.
 template <typename T>
 __global__ void __launch_bounds__(256, 3)
 grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, int64_t ldp, int act, int vec,
-              Drop drop, int M, int N, int cg, int rows, void* __restrict__ dz, float* __restrict__ partial, Overlap overlap)
+              Drop drop, float scale, int M, int N, int cg, int rows, int two, void* __restrict__ dz,
+              float* __restrict__ partial, Overlap overlap)
 {
     pdl_begin(overlap);
     __shared__ float red[256][8 + 1];
@@ -306,7 +322,7 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, 
                 if (drop.thr) drop8(f, drop, key, (uint32_t)rr, (uint32_t)g);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum[i] += f[i];
-                if (dz) store_operand8<T>(dz, rr * Np + col, M * Np, f);
+                if (dz) store_operand8<T>(dz, rr * Np + col, M * Np, f, two);
             }
         }
     }
@@ -318,7 +334,7 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, 
         float s = 0.f;
         for (int y = 0; y < step; ++y) s += red[y * cg + i / 8][i % 8];
         const int c = blockIdx.x * cg * 8 + i;
-        if (c < N) partial[(int64_t)blockIdx.y * N + c] = s;
+        if (c < N) partial[(int64_t)blockIdx.y * N + c] = s * scale;
     }
     pdl_end(overlap);
 }
@@ -401,9 +417,10 @@ Shape fwd_shape(dlrm_dtype dt, int M, int N, int K)
     return {M, N, K, dt == DLRM_F32 ? gemm::kMaxPairs : 1, gemm::column_cycles(N, dense_dtype_size(dt), true)};
 }
 
-Shape grad_shape(dlrm_dtype dt, int M, int N, int K)
+Shape grad_shape(dlrm_dtype dt, dlrm_act act, int M, int N, int K)
 {
-    return {M, N, K, dt == DLRM_F32 ? gemm::kMaxPairs : 1, gemm::column_cycles(N, dense_dtype_size(dt), false)};
+    return {M, N, K, dt == DLRM_F32 ? gemm::kMaxPairs : z_planes(dt, act),
+            gemm::column_cycles(N, dense_dtype_size(dt), false)};
 }
 
 // The workspaces' pieces, one after another.
@@ -415,8 +432,8 @@ FwdLayout fwd_layout(const void* x, int64_t ldx, const void* w, int64_t ldw, dlr
 {
     FwdLayout l = {};
     if (few_rows(M, N, K) || few_columns(M, N, K)) return l;
-    l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, dt) : 0;
-    l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
+    l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, planes_of(dt)) : 0;
+    l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, planes_of(dt)) : 0;
     l.partial = gemm::partial_bytes(fwd_shape(dt, M, N, K));
     l.total = l.x + l.w + l.partial;
     return l;
@@ -434,13 +451,13 @@ BwdLayout bwd_layout(const void* dy, int64_t ldg, const void* x, int64_t ldx, co
         l.total = l.sums = thin::workspace_bytes(dt, M, N, K);
         return l;
     }
-    l.dz = act != DLRM_ACT_NONE || p > 0 || needs_pack(dy, ldg, M, dt) ? operand_bytes(M, N, dt) : 0;
-    l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, dt) : 0;
-    l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, dt) : 0;
+    l.dz = act != DLRM_ACT_NONE || p > 0 || needs_pack(dy, ldg, M, dt) ? operand_bytes(M, N, z_planes(dt, act)) : 0;
+    l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, planes_of(dt)) : 0;
+    l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, planes_of(dt)) : 0;
     const GradZ g = grad_z_shape(M, N);
     l.sums = g.chunks > 1 ? dlrm_ws_align((size_t)g.chunks * N * 4) : 0;
-    l.partial_x = gemm::partial_bytes(grad_shape(dt, M, K, N));
-    l.partial_w = gemm::partial_bytes(grad_shape(dt, N, K, M));
+    l.partial_x = gemm::partial_bytes(grad_shape(dt, act, M, K, N));
+    l.partial_w = gemm::partial_bytes(grad_shape(dt, act, N, K, M));
     l.total = l.dz + l.x + l.w + l.sums + l.partial_x + l.partial_w;
     return l;
 }
@@ -494,8 +511,9 @@ extern "C" dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void*
         const dlrm_status r = launch_pack<T>(jx, jw, st);
         if (r != DLRM_OK) return r;
         const Shape z = fwd_shape(dtype, M, N, K);
-        const dlrm_status q = gemm::run<T>(fn, z, operand<T>(d_x, ldx, M, K, xs, false), operand<T>(d_w, ldw, N, K, wsp, false),
-                                           dtype != DLRM_F16, e, partial, d_status, st);
+        const int planes = planes_of(dtype);
+        const dlrm_status q = gemm::run<T>(fn, z, operand(d_x, ldx, M, K, xs, planes, false),
+                                           operand(d_w, ldw, N, K, wsp, planes, false), dtype != DLRM_F16, e, partial, d_status, st);
         return q == DLRM_OK ? gemm::finish<T>(z, e, partial, st) : q;
     });
 }
@@ -540,11 +558,16 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
     if (d_grad_x && (s = check_matrix(fn, "d_grad_x", d_grad_x, lddx, M, K, es)) != DLRM_OK) return s;
     const BwdLayout l = bwd_layout(d_grad_y, ldg, d_x, ldx, d_w, ldw, dtype, M, N, K, act, p);
     if ((s = check_workspace(fn, d_workspace, workspace_bytes, l.total)) != DLRM_OK) return s;
+    // 2-byte types: dZ without the dropout's scale, the sums times it (fp32's planes hold the scaled values)
+    const float scale = dtype == DLRM_F32 ? 1.f : drop.scale;
+    if (dtype != DLRM_F32) drop.scale = 1.f;
+    const int zp = z_planes(dtype, act), planes = planes_of(dtype);
     return with_type(dtype, [&](auto t) -> dlrm_status {
         using T = decltype(t);
+        const float z_scale = zp == 2 ? scale / kFit<T> : scale;
         if (few_outputs(N)) {
             if (!d_grad_x && !d_grad_w && !d_grad_bias) return DLRM_OK;
-            thin::Grad a = {d_grad_y, d_pre, d_x, d_w, ldg, ldp, ldx, ldw, M, N, K, (int)act, drop};
+            thin::Grad a = {d_grad_y, d_pre, d_x, d_w, ldg, ldp, ldx, ldw, M, N, K, (int)act, drop, z_scale, scale};
             a.dx = d_grad_x;
             a.dw = d_grad_w;
             a.lddx = lddx;
@@ -570,26 +593,27 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
         if (r == DLRM_OK && make_z) {
             const int vec = rows_aligned16(d_grad_y, ldg, M, es) && (act == DLRM_ACT_NONE || rows_aligned16(d_pre, ldp, M, es));
             r = check_launch_pdl(launch_pdl(grad_z_kernel<T>, dim3(g.blocks_x, g.chunks), dim3(256), 0, st,
-                                            (const T*)d_grad_y, ldg, (const T*)d_pre, ldp, (int)act, vec, drop, M, N,
-                                            g.cg, g.rows, products ? dz : nullptr,
+                                            (const T*)d_grad_y, ldg, (const T*)d_pre, ldp, (int)act, vec, drop, scale,
+                                            M, N, g.cg, g.rows, (int)(zp == 2), products ? dz : nullptr,
                                             d_grad_bias ? (sum ? sums : d_grad_bias) : nullptr, Overlap{packs, 0}),
                                  "grad_z_kernel");
         }
         Epilogue ex = {}, ew = {};
-        const Shape sx = grad_shape(dtype, M, K, N), sw = grad_shape(dtype, N, K, M);
+        ex.scale = ew.scale = z_scale;
+        const Shape sx = grad_shape(dtype, act, M, K, N), sw = grad_shape(dtype, act, N, K, M);
         if (r == DLRM_OK && d_grad_x) {
             ex.out = d_grad_x;
             ex.ldo = lddx;
             ex.vec = epilogue_vec(ex, M, es);
-            r = gemm::run<T>(fn, sx, operand<T>(d_grad_y, ldg, M, N, dz, false), operand<T>(d_w, ldw, N, K, wsp, true), bf, ex,
-                             px, d_status, st, {0, d_grad_w || sum});
+            r = gemm::run<T>(fn, sx, operand(d_grad_y, ldg, M, N, dz, zp, false), operand(d_w, ldw, N, K, wsp, planes, true),
+                             bf, ex, px, d_status, st, {0, d_grad_w || sum});
         }
         if (r == DLRM_OK && d_grad_w) {
             ew.out = d_grad_w;
             ew.ldo = lddw;
             ew.vec = epilogue_vec(ew, N, es);
-            r = gemm::run<T>(fn, sw, operand<T>(d_grad_y, ldg, M, N, dz, true), operand<T>(d_x, ldx, M, K, xs, true), bf, ew,
-                             pw, d_status, st, {d_grad_x != nullptr, sum});
+            r = gemm::run<T>(fn, sw, operand(d_grad_y, ldg, M, N, dz, zp, true), operand(d_x, ldx, M, K, xs, planes, true),
+                             bf, ew, pw, d_status, st, {d_grad_x != nullptr, sum});
         }
         if (r == DLRM_OK && sum)
             r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 31) / 32), dim3(1024), 0, st, (const float*)sums,

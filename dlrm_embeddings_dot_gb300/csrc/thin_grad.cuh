@@ -5,9 +5,8 @@
 //
 // One pass: x is read once and dX written once, both products beside it; the
 // tcgen05 tiles' 64 columns would be mostly padding.  A block owns some columns of
-// x and a chunk of its rows.  dZ of 256 rows goes to shared memory, rounded to the
-// tensors' type as a layer below would get it; then the warps walk rows, the
-// columns' part of W and of dW in registers.  Chunks' sums are added in order by
+// x and a chunk of its rows.  dZ of 256 rows goes to shared memory; then the warps walk
+// rows, the columns' part of W and of dW in registers.  Chunks' sums are added in order by
 // thin_sum_kernel.
 //
 //   2-byte types: mma.sync m16n8k16.  A warp takes 16 rows x 64 columns at a time, a
@@ -34,6 +33,7 @@ struct Grad {
     int64_t ldg, ldp, ldx, ldw;
     int M, N, K, act;
     Drop drop;
+    float scale, bias_scale;   // of the products' and of the bias gradient's sums
     int cg, rows;       // threads along the columns; rows of a chunk
     void *dx, *dw;      // each may be NULL
     int64_t lddx, lddw;
@@ -85,6 +85,7 @@ struct Sums {
     }
     __device__ void weight(int n, int64_t k, float s)
     {
+        s *= a.scale;
         if (partial) partial[(int64_t)n * a.K + k] = s;
         else ((T*)a.dw)[n * a.lddw + k] = from_f32<T>(s);
     }
@@ -99,6 +100,7 @@ struct Sums {
         float s = red[tid];
 #pragma unroll
         for (int y = 1; y < 8; ++y) s += red[y * kMaxOutputs + tid];
+        s *= a.bias_scale;
         if (partial) partial[NK + tid] = s;
         else a.db[tid] = s;
     }
@@ -132,13 +134,18 @@ __device__ __forceinline__ uint32_t pack2(T lo, T hi)
 // dX column 2 q + b of a product is 16 q + 2 j + b (j * 8 + 2 q + b where rows go by shared memory).
 // Measured, us, products / multiply-adds as in fp32: 65536 x 256 fp16 22 / 22 for 1 output, 24 / 39
 // for 8, 30 / 70 for 16.
-template <typename T, bool VEC>
+// TERMS: dZ as one value of the type, or as the sum of two (GELU and SILU, whose slopes it does not
+// hold): the products of the second are added first.
+template <typename T, bool VEC, int TERMS>
 __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_constant__ Grad a)
 {
     pdl_wait();
-    __shared__ __align__(16) T dzs[kTile * kPitch];
-    __shared__ float red[8 * 8 * 64];
-    __shared__ __align__(16) T stage[VEC ? 1 : 8][16][72];   // a warp's 16 x 64 of dX where rows are off the 16-byte grid
+    __shared__ __align__(16) T dzs[TERMS][kTile * kPitch];
+    using Stage = T[8][16][72];                              // a warp's 16 x 64 of dX where rows are off the 16-byte grid
+    constexpr size_t kRed = 8 * 8 * 64 * 4;
+    __shared__ __align__(16) uint8_t pool[!VEC && sizeof(Stage) > kRed ? sizeof(Stage) : kRed];
+    float* const red = reinterpret_cast<float*>(pool);       // the block's sums, once all rows are through
+    Stage& stage = *reinterpret_cast<Stage*>(pool);
     const int tid = threadIdx.x, lane = tid % 32, g = lane / 4, q = lane % 4;
     const int cw = tid / 32 % a.cg, rw = tid / 32 / a.cg, step = 8 / a.cg;   // a.cg warps side by side
     const int64_t c0 = ((int64_t)blockIdx.x * a.cg + cw) * 64;
@@ -166,8 +173,12 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
     for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-    uint4* const mine = reinterpret_cast<uint4*>(dzs + tid * kPitch);
-    mine[0] = mine[1] = make_uint4(0, 0, 0, 0);   // outputs past N stay zero
+    uint4* mine[TERMS];
+#pragma unroll
+    for (int u = 0; u < TERMS; ++u) {
+        mine[u] = reinterpret_cast<uint4*>(dzs[u] + tid * kPitch);
+        mine[u][0] = mine[u][1] = make_uint4(0, 0, 0, 0);   // outputs past N stay zero
+    }
 
     const T* const xend = (const T*)a.x + (a.M - 1) * a.ldx + a.K;
     // rows s + 2 q, + 1, + 8, + 9 of a tile; element j of a row is step j's
@@ -190,7 +201,17 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
         uint4 xn[4];
         if (a.dw) fetch(t0, rows, rw * 16, xn);
         __syncthreads();
-        tile_of_dz<T>(a, key, t0, rows, bsum, [&](int h, const float (&f)[8]) { mine[h] = pack8<T>(f); });
+        tile_of_dz<T>(a, key, t0, rows, bsum, [&](int h, const float (&f)[8]) {
+            if constexpr (TERMS == 2) {
+                float hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split2<T>(f[i], hi[i], lo[i]);
+                mine[0][h] = pack8<T>(hi);
+                mine[1][h] = pack8<T>(lo);
+            } else {
+                mine[0][h] = pack8<T>(f);
+            }
+        });
         __syncthreads();
         if (left <= 0) continue;
         for (int s = rw * 16; s < rows; s += step * 16) {
@@ -200,18 +221,23 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
                 for (int i = 0; i < 4; ++i) xv[i] = xn[i];
                 fetch(t0, rows, s + step * 16, xn);
             }
-            const uint32_t at = (uint32_t)__cvta_generic_to_shared(dzs) + (s * kPitch) * 2;
+            const uint32_t at = (uint32_t)__cvta_generic_to_shared(dzs[0]) + (s * kPitch) * 2;
+            constexpr uint32_t kTerm = kTile * kPitch * 2;
             if (a.dx) {
-                uint32_t d[4];
-                ldmatrix4<false>(d, at + (lane % 16 * kPitch + lane / 16 * 8) * 2);
+                uint32_t d[TERMS][4];
+#pragma unroll
+                for (int u = 0; u < TERMS; ++u) ldmatrix4<false>(d[u], at + u * kTerm + (lane % 16 * kPitch + lane / 16 * 8) * 2);
                 uint32_t out[2][8];
                 if constexpr (!VEC) __syncwarp();   // the last rows have left the stage
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     float o[4] = {};
-                    few::mma16816<T>(o, d[0], d[1], d[2], d[3], wf[j][0], wf[j][1]);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) out[h][j] = pack2(from_f32<T>(o[2 * h]), from_f32<T>(o[2 * h + 1]));
+                    for (int u = TERMS - 1; u >= 0; --u)
+                        few::mma16816<T>(o, d[u][0], d[u][1], d[u][2], d[u][3], wf[j][0], wf[j][1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        out[h][j] = pack2(from_f32<T>(o[2 * h] * a.scale), from_f32<T>(o[2 * h + 1] * a.scale));
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -254,15 +280,19 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
                 }
             }
             if (a.dw) {
-                uint32_t d[4];
-                ldmatrix4<true>(d, at + ((lane % 8 + lane / 16 * 8) * kPitch + lane / 8 % 2 * 8) * 2);
+                uint32_t d[TERMS][4];
+#pragma unroll
+                for (int u = 0; u < TERMS; ++u)
+                    ldmatrix4<true>(d[u], at + u * kTerm + ((lane % 8 + lane / 16 * 8) * kPitch + lane / 8 % 2 * 8) * 2);
                 const uint32_t* x0 = &xv[0].x;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const uint32_t pick = j % 2 ? 0x7632 : 0x5410;
                     const uint32_t b0 = __byte_perm(x0[j / 2], x0[4 + j / 2], pick);
                     const uint32_t b1 = __byte_perm(x0[8 + j / 2], x0[12 + j / 2], pick);
-                    few::mma16816<T>(acc[j], d[0], d[1], d[2], d[3], b0, b1);
+#pragma unroll
+                    for (int u = TERMS - 1; u >= 0; --u)
+                        few::mma16816<T>(acc[j], d[u][0], d[u][1], d[u][2], d[u][3], b0, b1);
                 }
             }
         }
@@ -528,7 +558,9 @@ dlrm_status run(dlrm_dtype dt, Grad a, float* ws, cudaStream_t st)
             : a.N <= 8 ? go(std::integral_constant<int, 8>{})
                        : go(std::integral_constant<int, 16>{});
     } else {
-        auto kern = vec && a.K % 8 == 0 ? thin_grad_mma_kernel<T, true> : thin_grad_mma_kernel<T, false>;
+        const bool v = vec && a.K % 8 == 0, two = a.act == DLRM_ACT_GELU || a.act == DLRM_ACT_SILU;
+        auto kern = two ? (v ? thin_grad_mma_kernel<T, true, 2> : thin_grad_mma_kernel<T, false, 2>)
+                        : (v ? thin_grad_mma_kernel<T, true, 1> : thin_grad_mma_kernel<T, false, 1>);
         r = check_launch_pdl(launch_pdl(kern, grid, dim3(256), 0, st, a), "thin_grad_mma_kernel");
     }
     if (r != DLRM_OK || s.chunks == 1 || !(a.dw || a.db)) return r;

@@ -104,9 +104,12 @@ size_t dlrm_linear_fwd_workspace_size(const void* d_x, int64_t ldx, const void* 
  *   d_grad_y [M][N];  d_x, d_w as in the forward;  d_pre [M][N] (NULL for
  *   DLRM_ACT_NONE);  d_grad_x [M][K], d_grad_w [N][K], d_grad_bias fp32 [N]
  *   (outputs, each may be NULL: that gradient is not computed)
- * The residual's gradient is grad_y itself.  grad_bias is summed from dZ in
- * fp32; the two products take dZ rounded once to dtype (fp32: its three parts),
- * as if a layer below had handed it over.
+ * The residual's gradient is grad_y itself.  dZ is not rounded to dtype: for NONE
+ * and RELU it is grad_y's own values, the dropout's scale being applied to the
+ * sums; for GELU and SILU fp16 and bf16 hold it as the sum of two values, which
+ * doubles the products' work (an infinite weight or input can then give a NaN
+ * where it meets a second value of 0).  fp16: the second value lies on a grid of
+ * 2^-24, as grad_y's least values do.
  */
 dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const void* d_x, int64_t ldx, const void* d_w,
                             int64_t ldw, const void* d_pre, int64_t ldp, dlrm_dtype dtype, int M, int N, int K,

@@ -1,0 +1,115 @@
+"""What the dense layer's gradient holds between its two halves, against 64-bit forms: dZ is not
+rounded to a 2-byte type, and what dropout's scale or a slope takes past fp16's range is not lost.
+
+Bounds (u = half an ulp of the output type; A = the same expression on absolute values):
+  * a' of NONE and RELU is 0 or 1 and dropout's scale is applied to the sums: dZ is exact, and so is
+    its plane; the sums' error is (L + 8) 2^-23 A, the scale's and the last rounding's 2^-23 and u
+  * GELU and SILU: the slope is within 2^-20 of its largest size, 1.2; the value in two terms within
+    2^-16 (bf16) or 2^-20 (fp16) of itself, fp16's second term on a grid of 2^-24
+"""
+
+import pytest
+import torch
+
+import dense_ref as ref
+from gpu_util import dev
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+TERMS = {"f16": 2.0**-20, "bf16": 2.0**-16, "f32": 0.0}
+
+
+def _rand(g, *shape, std=1.0, dtype="f32"):
+    return (torch.randn(*shape, generator=g, dtype=torch.float64) * std).to(ref.TYPES[dtype]).to(dev())
+
+
+def _gradients(dl, dy, x, w, z, name, p=0.0, seed=(5, 6)):
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(w.shape[0], device=dev())
+    n = dl.dlrm_linear_bwd_workspace_size(dy, x, w, act=ref.ACT[name], p=p)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev()) if n else None
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    dl.dlrm_linear_bwd(dy, x, w, z, dx, dw, db, act=ref.ACT[name], p=p, workspace=ws, status=status,
+                       rng=torch.tensor(seed, dtype=torch.int64, device=dev()))
+    assert int(status.item()) == 0
+    return dx, dw, db
+
+
+def _want(dy, x, w, z, name, dtype, p=0.0, seed=(5, 6)):
+    """{gradient: (value, bound)} in 64 bits on the GPU."""
+    dy, x, w = dy.double(), x.double(), w.double()
+    (M, K), N = x.shape, w.shape[0]
+    scale = 1.0
+    g = dy
+    if p:
+        kept, scale = ref.keep_scale(*seed, M, N, p)
+        g = torch.where(kept.to(dev()), dy, torch.zeros_like(dy))
+    dz = g if name == "none" else g * ref.slope(z.double(), name)
+    if name in ("none", "relu"):
+        one = torch.zeros_like(dz)
+    else:
+        one = 2.0**-20 * 1.2 * g.abs() + TERMS[dtype] * dz.abs() + (2.0**-25 if dtype == "f16" else 0.0)
+    size = dz.abs() + one
+
+    def product(a, b, ea, L):
+        v, e = a @ b * scale, (ea @ b.abs() + (L + 8) * 2.0**-23 * (size_of(a) @ b.abs())) * scale
+        return v, e + 2.0**-22 * v.abs()
+
+    def size_of(a):
+        return size if a.shape == size.shape and a is dz else size.t()
+
+    return {"dx": product(dz, w, one, N), "dw": product(dz.t(), x, one.t(), M),
+            "db": (dz.sum(0) * scale, (one.sum(0) + (M + 16) * 2.0**-23 * size.sum(0)) * scale)}
+
+
+# tiles and few outputs, split K and not, aligned and ragged
+SIZES = [(256, 512, 1024), (700, 40, 264), (65, 48, 72), (130, 77, 129), (3000, 24, 40), (256, 16, 1024), (40, 5, 333),
+         (9000, 1, 72)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("name,p", [("none", 0.3), ("relu", 0.1), ("gelu", 0.0), ("silu", 0.2)])
+def test_gradient_has_one_rounding(cuda_lib, dtype, M, N, K, name, p):
+    g = torch.Generator().manual_seed(M + N + K)
+    x, w = _rand(g, M, K, dtype=dtype), _rand(g, N, K, std=K**-0.5, dtype=dtype)
+    dy, z = _rand(g, M, N, std=0.1, dtype=dtype), _rand(g, M, N, dtype=dtype)
+    got = _gradients(cuda_lib, dy, x, w, z, name, p)
+    want = _want(dy, x, w, z, name, dtype, p)
+    for t, k in zip(got, ("dx", "dw", "db")):
+        ref.assert_close(t, *want[k], "f32" if k == "db" else dtype, k)
+
+
+@pytest.mark.parametrize("M,N,K", [(130, 40, 72), (130, 40, 77), (130, 8, 72), (130, 8, 77)])
+@pytest.mark.parametrize("name,p", [("none", 0.5), ("relu", 0.75), ("gelu", 0.5), ("silu", 0.0)])
+def test_gradient_past_the_range_of_fp16(cuda_lib, M, N, K, name, p):
+    """|dY| up to 65,504 with a slope above 1 or a scale of 2 and 4: dZ does not fit fp16, the gradients do."""
+    g = torch.Generator().manual_seed(M + N)
+    x, w = _rand(g, M, K, std=2.0**-12, dtype="f16"), _rand(g, N, K, std=2.0**-12, dtype="f16")
+    dy = (torch.rand(M, N, generator=g, dtype=torch.float64) * 15504 + 50000).half().to(dev())
+    z = (torch.rand(M, N, generator=g, dtype=torch.float64) + 1.5).half().to(dev())   # slopes up to 1.13
+    got = _gradients(cuda_lib, dy, x, w, z, name, p)
+    want = _want(dy, x, w, z, name, "f16", p)
+    for t, k in zip(got, ("dx", "dw", "db")):
+        assert bool(torch.isfinite(t).all()), k
+        ref.assert_close(t, *want[k], "f32" if k == "db" else "f16", k)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("N", [40, 8])
+@pytest.mark.parametrize("name", ["none", "gelu", "silu"])
+def test_infinite_and_nan_gradients(cuda_lib, dtype, N, name):
+    """An infinity in dY reaches its row of dX and its column's row of dW with the sign 32 bits give, a
+    NaN as NaN, and nothing else."""
+    M, K = 130, 72
+    g = torch.Generator().manual_seed(N)
+    x, w = _rand(g, M, K, dtype=dtype), _rand(g, N, K, std=K**-0.5, dtype=dtype)
+    dy, z = _rand(g, M, N, std=0.1, dtype=dtype), _rand(g, M, N, dtype=dtype)
+    dy[3, 2], dy[9, 5] = -INF, NAN
+    dx, dw, db = _gradients(cuda_lib, dy, x, w, z, name)
+    dz = dy.double() if name == "none" else dy.double() * ref.slope(z.double(), name)
+    for got, want in ((dx, dz @ w.double()), (dw, dz.t() @ x.double()), (db, dz.sum(0))):
+        got = got.double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        inf = torch.isinf(want)
+        assert int(inf.sum()) > 0 and torch.equal(got[inf], want[inf])
+        assert bool(torch.isfinite(got[torch.isfinite(want)]).all())
