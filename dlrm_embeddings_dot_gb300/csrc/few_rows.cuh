@@ -154,9 +154,11 @@ __device__ __forceinline__ void dot8(float& s, const Chunk& a, const Chunk& x)
 // g + 8 of tile i and of its token j.  w[i][0] / w[i][1]: rows g and g + 8 of tile
 // i.  Every pointer is a readable row: where a tile has no such row or token any
 // other does, as rows and tokens meet only in results that the caller then leaves
-// alone.  XP: terms each token is the sum of, term q at x[j] + q * xplane.
-template <typename T, int WT, int NX, int VEC, int XP, int U, bool AHEAD, typename Mul>
-__device__ __forceinline__ void visit_k(const T* (&w)[WT][2], const T* (&x)[NX], int k0, int k1, int64_t xplane, Mul&& mul)
+// alone.  XP: terms each token is the sum of, term q at x[j] + q * xplane.  fix(j, k, x)
+// may change a chunk of token j, whose first value is k values behind k0, before use.
+template <typename T, int WT, int NX, int VEC, int XP, int U, bool AHEAD, typename Mul, typename Fix>
+__device__ __forceinline__ void visit_k(const T* (&w)[WT][2], const T* (&x)[NX], int k0, int k1, int64_t xplane, Mul&& mul,
+                                        Fix&& fix)
 {
     constexpr int kBlock = U * kStep<T>;   // K whose weight loads are issued together
     const int t = (threadIdx.x % kWarp) % 4;
@@ -184,7 +186,8 @@ __device__ __forceinline__ void visit_k(const T* (&w)[WT][2], const T* (&x)[NX],
             for (int j = 0; j < NX; ++j)
 #pragma unroll
                 for (int q = 0; q < XP; ++q) {
-                    const Chunk b = load_lane<T, VEC, true>(x[j] + q * xplane + at + u * kStep<T>);
+                    Chunk b = load_lane<T, VEC, true>(x[j] + q * xplane + at + u * kStep<T>);
+                    fix(j, k1 - k0 - left + at + u * kStep<T> + t * kLane<T>, b);
 #pragma unroll
                     for (int i = 0; i < WT; ++i) mul(i, j, a[u][i][0], a[u][i][1], b);
                 }
@@ -236,7 +239,8 @@ __device__ __forceinline__ void visit_k(const T* (&w)[WT][2], const T* (&x)[NX],
             for (int j = 0; j < NX; ++j)
 #pragma unroll
                 for (int q = 0; q < XP; ++q) {
-                    const Chunk b = load_lane<T, VEC, true>(x[j] + q * xplane);
+                    Chunk b = load_lane<T, VEC, true>(x[j] + q * xplane);
+                    fix(j, k1 - k0 - left + t * kLane<T>, b);
 #pragma unroll
                     for (int i = 0; i < WT; ++i) mul(i, j, a[i][0], a[i][1], b);
                 }
@@ -249,7 +253,8 @@ __device__ __forceinline__ void visit_k(const T* (&w)[WT][2], const T* (&x)[NX],
             for (int j = 0; j < NX; ++j)
 #pragma unroll
                 for (int q = 0; q < XP; ++q) {
-                    const Chunk b = load_part<T>(x[j] + q * xplane, n);
+                    Chunk b = load_part<T>(x[j] + q * xplane, n);
+                    fix(j, k1 - k0 - left + t * kLane<T>, b);
 #pragma unroll
                     for (int i = 0; i < WT; ++i) mul(i, j, a[i][0], a[i][1], b);
                 }
@@ -260,10 +265,14 @@ __device__ __forceinline__ void visit_k(const T* (&w)[WT][2], const T* (&x)[NX],
 
 // out(i, token, row, value) for every sum of the warp's WT tiles of 16 weight rows
 // (pointers as for visit_k) with tokens [0, n), n <= 8 NT, over [k0, k1) of K.
-// token(j) gives the row of token j (j < n).
-template <typename T, int WT, int NT, int VEC, int XP = 1, typename Token, typename Out>
+// token(j) gives the row of token j (j < n).  fix as for visit_k, j counting the lane's
+// tokens 8 j + g (2-byte types).
+struct Unchanged {
+    __device__ __forceinline__ void operator()(int, int, Chunk&) const {}
+};
+template <typename T, int WT, int NT, int VEC, int XP = 1, typename Token, typename Out, typename Fix = Unchanged>
 __device__ __forceinline__ void rows_times_tokens(const T* (&w)[WT][2], Token&& token, int n, int k0, int k1,
-                                                  int64_t xplane, Out&& out)
+                                                  int64_t xplane, Out&& out, Fix&& fix = Fix())
 {
     const int lane = threadIdx.x % kWarp, g = lane / 4, t = lane % 4;
     if constexpr (std::is_same_v<T, float> && NT == 1) {
@@ -278,7 +287,7 @@ __device__ __forceinline__ void rows_times_tokens(const T* (&w)[WT][2], Token&& 
                                                             [&](int i, int j, const Chunk& a, const Chunk& b, const Chunk& c) {
                                                                 dot8(acc[i][j][0], a, c);
                                                                 dot8(acc[i][j][1], b, c);
-                                                            });
+                                                            }, Unchanged());
 #pragma unroll
             for (int i = 0; i < WT; ++i)
 #pragma unroll
@@ -304,7 +313,7 @@ __device__ __forceinline__ void rows_times_tokens(const T* (&w)[WT][2], Token&& 
         visit_k<T, WT, NT, VEC, XP, U, (NT == 1)>(w, x, k0, k1, xplane,
                                                   [&](int i, int j, const Chunk& a, const Chunk& b, const Chunk& c) {
                                                       mac<T>(acc[i][j], a, b, c);
-                                                  });
+                                                  }, fix);
 #pragma unroll
         for (int i = 0; i < WT; ++i)
 #pragma unroll

@@ -52,12 +52,27 @@ constexpr int kQ = 16 / (int)sizeof(T);        // values of a lane's chunk
 template <typename T>
 constexpr int kStepK = 4 * kQ<T>;              // K of a step
 
-// probs * h enters the second product as the sum of two values of a 2-byte type
-// (the rounded value and the rounded rest): the product of the weights with a
-// second fragment is free beside the weights' traffic, and y then has one
-// rounding, its own.
+// probs * h enters the second product with 22 bits or more: the products of the
+// weights with further fragments are free beside the weights' traffic, and y then
+// has one rounding, its own.
+//   fp32  as it is
+//   bf16  as the sum of three values (split1)
+//   fp16  as the sum of two, divided by a power of two, so that none overflows and none
+//         is lost below 2^-14, whatever the size of the activations.  Each run of 16
+//         values of a token (a unit's rows) has its own: 2^kPower where the run's
+//         largest is in [2^kPowerLow, 2^kPowerHigh) (no fewer than 21 bits of it), as
+//         activations mostly are, else what brings that into [2^14, 2^15).  Where
+//         all are 2^kPower moe_down has no more to do than to multiply its sums.
+//         Otherwise it brings the runs of an item to the largest power among them
+//         (times 1 or less) before the products (48 tokens, 64 experts, 182 us where
+//         that took 172).
 template <typename T>
-constexpr int kTerms = sizeof(T) == 2 ? 2 : 1;
+constexpr int kTerms = std::is_same_v<T, float> ? 1 : std::is_same_v<T, bf16> ? 3 : 2;
+template <typename T>
+constexpr bool kScaled = std::is_same_v<T, __half>;
+constexpr int kPower = -11, kPowerLow = -15, kPowerHigh = 4;
+constexpr int kLeastPower = -80, kMostPower = 113;   // of the others (values below 2^-66 are nothing to any fp16 y)
+constexpr int kMaxUpBlocks = kThreads;               // blocks of moe_up: a thread of moe_down reads one's report
 
 struct MoeArgs {
     const void *x, *wr, *w1, *w2, *res;
@@ -68,6 +83,9 @@ struct MoeArgs {
     int32_t* ids;
     float* probs;
     void* h;                                // [kTerms][T][k][I]
+    uint8_t* other;                         // fp16: [up_blocks]: 1 where a block had runs of another power than kPower
+    int8_t* powers;                         // fp16: [T][k][runs of 16 in I]: what their values were divided by, log2
+    int up_blocks;
     uint32_t* status;
     long long wait_cycles;
     int once;                               // the weights are more than L2 keeps from call to call
@@ -267,26 +285,74 @@ __device__ __forceinline__ uint8_t* shared_area(uint8_t* raw)
     return reinterpret_cast<uint8_t*>(moe::area(reinterpret_cast<uintptr_t>(raw)));
 }
 
+// fp16's runs of one item where not all have the same power, for the lane's token 8 j + g of each j.
+template <int NT>
+struct RunScale {
+    const int8_t* at[NT];   // the runs' powers from the item's first value on
+    int top[NT];            // their largest
+
+    // powers(token): the powers of a token's row
+    template <typename Powers>
+    __device__ __forceinline__ void load(Powers&& powers, int n, int k0, int k1)
+    {
+        const int lane = threadIdx.x % kWarp, g = lane / 4, t = lane % 4;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            at[j] = powers(min(j * 8 + g, n - 1)) + k0 / kRows;
+            int m = kLeastPower;
+            for (int i = t; k0 + i * kRows < k1; i += 4) m = max(m, (int)__ldg(at[j] + i));
+            m = max(m, __shfl_xor_sync(~0u, m, 1));
+            top[j] = max(m, __shfl_xor_sync(~0u, m, 2));
+        }
+    }
+    // What a run is multiplied with, twice in a word: 2^(power - top).
+    __device__ __forceinline__ uint32_t factor(int j, int power) const
+    {
+        const int d = power - top[j];
+        return (d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u) * 0x10001u;
+    }
+    static __device__ __forceinline__ void apply(uint4& v, uint32_t f)
+    {
+        __half2 h[4], s;
+        memcpy(h, &v, 16);
+        memcpy(&s, &f, 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __hmul2(h[i], s);
+        memcpy(&v, h, 16);
+    }
+    // The sums of tokens 8 j + 2 t and 8 j + 2 t + 1 are to be multiplied with these (all lanes).
+    __device__ __forceinline__ float2 of_sums(int j) const
+    {
+        const int t = threadIdx.x % 4;
+        const int a = __shfl_sync(~0u, top[j], 8 * t), b = __shfl_sync(~0u, top[j], 8 * t + 4);
+        return make_float2(__int_as_float((a + 127) << 23), __int_as_float((b + 127) << 23));
+    }
+};
+
 __device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // The sums of WT tiles of 16 weight rows with tokens [0, n) over [k0, k1) of K
 // (k0 a multiple of a stage's), the weights taken from the ring stage by stage.
 // out(i, token, row, value) gets every sum (zero for an empty range).  token(j):
 // the row of token j; its values past K are not read, and the boxes hold zeros
-// there.
-template <typename T, int WT, int XP, typename R, typename Token, typename Out>
+// there.  SCALED: powers(j) has the powers of two of its runs.
+struct NoPowers {
+};
+template <typename T, int WT, int XP, typename R, typename Token, typename Out, typename Powers = NoPowers>
 __device__ __forceinline__ void ring_times_tokens(R& ring, Token&& token, int n, int k0, int k1, int K, int64_t xplane,
-                                                  Out&& out)
+                                                  Out&& out, Powers&& powers = Powers())
 {
+    constexpr bool SCALED = !std::is_same_v<std::decay_t<Powers>, NoPowers>;
     constexpr int ST = kSteps / WT, kRow = ST * 64;   // steps in a stage, bytes of a row in a box
     const int lane = threadIdx.x % kWarp, g = lane / 4, t = lane % 4;
-    // mul(x, w): the products of one step of each tile (row g at w) with the tokens'
-    // chunks x[N]; at(j): where token chunk j begins.  The chunks of the next D
+    // mul(x, w, ahead): the products of one step of each tile (row g at w) with the tokens'
+    // chunks x[N]; at(j): where token chunk j begins; also(d, k): anything else to load
+    // for the step that begins at k.  The chunks of the next D
     // steps are on their way while one step is multiplied; no more than D steps are
     // unrolled, because a block runs this code for a few units only and has to
     // fetch every instruction of it.
-    auto run = [&](auto nn, auto&& at, auto&& mul) {
-        constexpr int N = decltype(nn)::value, D = N <= 2 ? 4 : 2;
+    auto run = [&](auto nn, auto dd, auto&& at, auto&& also, auto&& mul) {
+        constexpr int N = decltype(nn)::value, D = decltype(dd)::value;
         const T* x[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) x[j] = at(j) + k0 + t * kQ<T>;
@@ -298,7 +364,10 @@ __device__ __forceinline__ void ring_times_tokens(R& ring, Token&& token, int n,
                 c[j] = left > ahead * kStepK<T> ? ldg_nc_l1_v4(x[j] + ahead * kStepK<T>) : make_uint4(0, 0, 0, 0);
         };
 #pragma unroll
-        for (int d = 0; d < D; ++d) fetch(b[d], d);
+        for (int d = 0; d < D; ++d) {
+            fetch(b[d], d);
+            also(d, k0 + d * kStepK<T>);
+        }
         const uint8_t* w = nullptr;
         int in = 0;   // steps left in the stage
 #pragma unroll 1
@@ -309,8 +378,9 @@ __device__ __forceinline__ void ring_times_tokens(R& ring, Token&& token, int n,
             }
 #pragma unroll
             for (int d = 0; d < D; ++d) {
-                mul(b[d], w + d * 64);
+                mul(b[d], w + d * 64, d);
                 fetch(b[d], D + d);
+                also(d, k + (D + d) * kStepK<T>);
             }
 #pragma unroll
             for (int j = 0; j < N; ++j) x[j] += D * kStepK<T>;
@@ -328,8 +398,9 @@ __device__ __forceinline__ void ring_times_tokens(R& ring, Token&& token, int n,
         auto with = [&](auto nn) {
             constexpr int NX = decltype(nn)::value;
             float acc[WT][NX][2] = {};
-            run(nn, [&](int j) { return token(min(j, n - 1)); },
-                [&](const uint4 (&x)[NX], const uint8_t* w) {
+            run(nn, std::integral_constant<int, NX <= 2 ? 4 : 2>{}, [&](int j) { return token(min(j, n - 1)); },
+                [](int, int) {},
+                [&](uint4 (&x)[NX], const uint8_t* w, int) {
 #pragma unroll
                     for (int i = 0; i < WT; ++i)
 #pragma unroll
@@ -363,11 +434,30 @@ __device__ __forceinline__ void ring_times_tokens(R& ring, Token&& token, int n,
         else with(std::integral_constant<int, 8>{});
     } else {
         auto with = [&](auto nn) {
-            constexpr int NT = decltype(nn)::value;
+            constexpr int NT = decltype(nn)::value, D = NT * XP <= 3 ? 4 : 2;
             float acc[WT][NT][4] = {};
-            run(std::integral_constant<int, NT * XP>{},
+            RunScale<NT> scale;
+            if constexpr (SCALED) scale.load(powers, n, k0, k1);
+            int power[D][NT];
+            run(std::integral_constant<int, NT * XP>{}, std::integral_constant<int, D>{},
                 [&](int j) { return token(min(j / XP * 8 + g, n - 1)) + j % XP * xplane; },
-                [&](const uint4 (&x)[NT * XP], const uint8_t* w) {
+                [&](int d, int k) {
+                    if constexpr (SCALED) {
+                        const int c = k + t * kQ<T>;   // the lane's chunk lies within one run
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+                            power[d][j] = c < k1 ? __ldg(scale.at[j] + (c - k0) / kRows) : kLeastPower;
+                    }
+                },
+                [&](uint4 (&x)[NT * XP], const uint8_t* w, int d) {
+                    if constexpr (SCALED) {
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const uint32_t f = scale.factor(j, power[d][j]);
+#pragma unroll
+                            for (int q = 0; q < XP; ++q) scale.apply(x[j * XP + q], f);
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < WT; ++i) {
                         const uint4 lo = lds16(w + i * (kStage / WT)), hi = lds16(w + i * (kStage / WT) + 8 * kRow);
@@ -376,14 +466,17 @@ __device__ __forceinline__ void ring_times_tokens(R& ring, Token&& token, int n,
                     }
                 });
 #pragma unroll
-            for (int i = 0; i < WT; ++i)
+            for (int j = 0; j < NT; ++j) {
+                float2 f = make_float2(1.f, 1.f);
+                if constexpr (SCALED) f = scale.of_sums(j);
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int i = 0; i < WT; ++i)
 #pragma unroll
                     for (int d = 0; d < 4; ++d) {
                         const int tok = j * 8 + 2 * t + (d & 1);
-                        if (tok < n) out(i, tok, g + 8 * (d >> 1), acc[i][j][d]);
+                        if (tok < n) out(i, tok, g + 8 * (d >> 1), acc[i][j][d] * (d & 1 ? f.y : f.x));
                     }
+            }
         };
         if constexpr (std::is_same_v<T, float>) {
             if (n <= 16) with(std::integral_constant<int, 2>{});
@@ -547,12 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
     T* h = (T*)a.h;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the rings were the logits' memory
     __syncthreads();
+    bool other = false;   // fp16: a run had another power than kPower
     // One unit: products(put) brings the warp's partial sums, which meet in shared memory.
     auto unit = [&](const Choice& c, int row0, auto&& products) {
         products([&](int i, int tok, int r, float v) { red[(warp * 2 + i) * tile_floats + tok * kPitch + r] = v; });
         group_sync(1 + mine, G * kWarp);
-        for (int i = wg * kWarp + lane; i < c.n * kRows; i += G * kWarp) {
-            const int tok = i / kRows, r = i % kRows;
+        for (int i0 = wg * kWarp; i0 < c.n * kRows; i0 += G * kWarp) {   // a token's 16 rows are 16 neighbouring lanes'
+            const int tok = min((i0 + lane) / kRows, c.n - 1), r = lane % kRows;
+            const bool token = i0 + lane < c.n * kRows, in = token && row0 + r < a.I;
             const float* p = red + (mine * G * 2) * tile_floats + tok * kPitch + r;
             float z = 0.f, up = 0.f;
             for (int q = 0; q < G; ++q) {
@@ -562,15 +657,36 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
             const int slot = c.entry[tok];
             float v = act_f(z, a.act);
             if (a.gated) v *= up;
-            if (row0 + r < a.I) {
-                T* dst = h + ((int64_t)(slot / kMaxK) * a.k + slot % kMaxK) * a.I + row0 + r;
-                v *= probs_s[slot];
+            v *= probs_s[slot];
+            const int64_t row = (int64_t)(slot / kMaxK) * a.k + slot % kMaxK, plane = (int64_t)a.T * a.k * a.I;
+            T* dst = h + row * a.I + row0 + r;
+            if constexpr (kScaled<T>) {
+                float m = in ? fabsf(v) : 0.f;   // a NaN stays one whatever the power
+#pragma unroll
+                for (int d = 8; d; d /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+                const int e = (int)(__float_as_uint(m) >> 23) - 127;
+                const bool usual = e >= kPowerLow && e < kPowerHigh;
+                const int power = usual ? kPower : min(max(e - 14, kLeastPower), kMostPower);
+                other |= token && !usual && m != 0.f;   // (a run of zeros goes with any power)
+                if (token && r == 0) a.powers[row * tiles + row0 / kRows] = (int8_t)power;
+                v *= __int_as_float((127 - power) << 23);
                 const T top = from_f32<T>(v);
-                *dst = top;
-                if constexpr (kTerms<T> == 2) {
-                    const float rest = v - to_f32(top);   // NaN for an infinite v: its rest is zero
-                    dst[(int64_t)a.T * a.k * a.I] = from_f32<T>(fabsf(to_f32(top)) <= 3.4e38f ? rest : 0.f);
+                const float rest = v - to_f32(top);   // NaN for an infinite v: its rest is zero
+                if (in) {
+                    dst[0] = top;
+                    dst[plane] = from_f32<T>(fabsf(to_f32(top)) <= 65504.f ? rest : 0.f);
                 }
+            } else if constexpr (kTerms<T> == 3) {
+                uint32_t hi, mid;
+                float lo;
+                split1(v, hi, mid, lo);
+                if (in) {
+                    dst[0] = from_f32<T>(__uint_as_float(hi));
+                    dst[plane] = from_f32<T>(__uint_as_float(mid));
+                    dst[2 * plane] = from_f32<T>(lo);
+                }
+            } else if (in) {
+                dst[0] = v;
             }
         }
         group_sync(1 + mine, G * kWarp);
@@ -613,6 +729,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
             });
         }
     }
+    if constexpr (kScaled<T>) {
+        other = __syncthreads_or(other);
+        if (threadIdx.x == 0) a.other[blockIdx.x] = other;
+    }
 }
 
 template <typename T, bool VEC>
@@ -631,8 +751,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     for (int i = threadIdx.x; i < kWarps * a.T * kPitch; i += kThreads) smem[i] = 0.f;
     __syncthreads();
     pdl_wait();
+    uint8_t other = 0;
+    if constexpr (kScaled<T>)
+        if (threadIdx.x < a.up_blocks) other = __ldg(a.other + threadIdx.x);
     build_lists(lists, a.T, a.k, a.E, [&](int t, int j) { return a.ids[t * a.k + j]; });
-    __syncthreads();
+    const bool scaled = __syncthreads_or(other != 0);   // fp16: the runs' powers differ
 
     const int chunks = (a.I + a.chunk - 1) / a.chunk, items = lists.n_active * chunks, stride = S * kWarps;
     const T *w2 = (const T*)a.w2, *h = (const T*)a.h;
@@ -641,11 +764,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     const int64_t plane = (int64_t)a.T * a.k * a.I;
     auto k0 = [&](int i) { return i % chunks * a.chunk; };
     auto k1 = [&](int i) { return min(a.I, i % chunks * a.chunk + a.chunk); };
+    const int runs = (a.I + kRows - 1) / kRows;
     auto all = [&](auto&& products) {
         for (int it = first; it < items; it += stride) {
             const Choice c = choice(lists, it / chunks);
-            products(c, it, [&](int i) { return h + ((int64_t)(c.entry[i] / kMaxK) * a.k + c.entry[i] % kMaxK) * a.I; },
-                     [&](int, int i, int r, float v) { mine[c.entry[i] / kMaxK * kPitch + r] += v; });
+            auto row = [&](int i) { return (int64_t)(c.entry[i] / kMaxK) * a.k + c.entry[i] % kMaxK; };
+            products(c, it, [&](int i) { return h + row(i) * a.I; }, [&](int i) { return a.powers + row(i) * runs; },
+                     [&](int, int i, int r, float v) {
+                         if constexpr (kScaled<T>) v = scaled ? v : v * (1.f / (1 << -kPower));
+                         mine[c.entry[i] / kMaxK * kPitch + r] += v;
+                     });
             __syncwarp();   // another item's token may be another lane's
         }
     };
@@ -653,17 +781,45 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
         auto ring = make_ring<T, 1>(sync, rings, &map, a, first, stride, items, 0,
                                     [&](int i) { return (lists.active[i / chunks] % kMaxE) * a.H + row0; }, k0, k1);
         ring.start();
-        all([&](const Choice& c, int it, auto&& token, auto&& add) {
-            ring_times_tokens<T, 1, kTerms<T>>(ring, token, c.n, k0(it), k1(it), a.I, plane, add);
-        });
+        if (kScaled<T> && scaled)
+            all([&](const Choice& c, int it, auto&& token, auto&& powers, auto&& add) {
+                ring_times_tokens<T, 1, kTerms<T>>(ring, token, c.n, k0(it), k1(it), a.I, plane, add, powers);
+            });
+        else
+            all([&](const Choice& c, int it, auto&& token, auto&& powers, auto&& add) {
+                ring_times_tokens<T, 1, kTerms<T>>(ring, token, c.n, k0(it), k1(it), a.I, plane, add);
+            });
         ring.finish(a.status);
     } else {
-        all([&](const Choice& c, int it, auto&& token, auto&& add) {
+        all([&](const Choice& c, int it, auto&& token, auto&& powers, auto&& add) {
             const T* base = w2 + (int64_t)c.e * a.H * a.I;
             const T* w[1][2] = {{base + (int64_t)min(row0 + g, a.H - 1) * a.I,
                                  base + (int64_t)min(row0 + g + 8, a.H - 1) * a.I}};
             with_group_tiles(c.n, [&](auto nt) {
-                rows_times_tokens<T, 1, decltype(nt)::value, 0, kTerms<T>>(w, token, c.n, k0(it), k1(it), plane, add);
+                constexpr int NT = decltype(nt)::value;
+                if (kScaled<T> && scaled) {
+                    RunScale<NT> scale;
+                    scale.load(powers, c.n, k0(it), k1(it));
+                    float2 f[NT];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) f[j] = scale.of_sums(j);
+                    rows_times_tokens<T, 1, NT, 0, kTerms<T>>(
+                        w, token, c.n, k0(it), k1(it), plane,
+                        [&](int i, int tok, int r, float v) {
+                            float2 s = f[0];
+#pragma unroll
+                            for (int j = 1; j < NT; ++j)
+                                if (tok / 8 == j) s = f[j];
+                            add(i, tok, r, v * (tok & 1 ? s.y : s.x));
+                        },
+                        [&](int j, int k, Chunk& x) {   // k: of the lane's 16 values, one run, from the item's first on
+                            const uint32_t s = scale.factor(j, k + k0(it) < k1(it) ? __ldg(scale.at[j] + k / kRows) : kLeastPower);
+                            scale.apply(x.v[0], s);
+                            scale.apply(x.v[1], s);
+                        });
+                } else {
+                    rows_times_tokens<T, 1, NT, 0, kTerms<T>>(w, token, c.n, k0(it), k1(it), plane, add);
+                }
             });
         });
     }
@@ -771,7 +927,9 @@ dlrm_status launch_moe(MoeArgs a, cudaStream_t st)
     }
     int64_t blocks = (units * a.group + kWarps - 1) / kWarps;
     if (blocks > most) blocks = most;
-    blocks = (blocks + C - 1) / C * C;
+    if (blocks > kMaxUpBlocks) blocks = kMaxUpBlocks;
+    blocks = (blocks + C - 1) / C * C;   // C divides kMaxUpBlocks
+    a.up_blocks = (int)blocks;
     e = launch_cluster(up, dim3((unsigned)blocks), dim3(kThreads), smem, st, C, m1, a);
     s = check_launch_pdl(e, "moe_up_kernel");
     if (s != DLRM_OK) return s;
@@ -815,7 +973,10 @@ using namespace dlrm;
 extern "C" size_t dlrm_moe_fwd_workspace_size(dlrm_dtype dtype, int T, int H, int I, int E, int k)
 {
     if (!moe_sizes_ok(dtype, T, H, I, E, k)) return 0;
-    return dlrm_ws_align((size_t)T * k * I * 4);   // one fp32 term, or two of 2 bytes
+    // the terms of probs * h, and fp16's reports and powers of two
+    const size_t bytes = dtype == DLRM_BF16 ? 6 : 4;
+    return dlrm_ws_align((size_t)T * k * I * bytes +
+                         (dtype == DLRM_F16 ? kMaxUpBlocks + (size_t)T * k * (((size_t)I + 15) / 16) : 0));
 }
 
 extern "C" dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_w_router, const void* d_w1,
@@ -856,6 +1017,8 @@ extern "C" dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_
     a.ldx = ldx, a.ldr = ldr, a.ldy = ldy;
     a.T = T, a.H = H, a.I = I, a.E = E, a.k = k, a.act = act, a.gated = gated != 0;
     a.y = d_y, a.ids = d_ids, a.probs = d_probs, a.h = d_workspace;
+    a.other = (uint8_t*)d_workspace + (size_t)T * k * I * 4;
+    a.powers = (int8_t*)a.other + kMaxUpBlocks;
     a.status = d_status, a.wait_cycles = wait_limit_cycles();
     a.once = (int64_t)E * (gated ? 3 : 2) * I * H * es > kOnce;
     // TMA and 16-byte loads where every row is on the grid (the workspace's are where I's are)

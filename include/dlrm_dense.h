@@ -144,8 +144,10 @@ size_t dlrm_linear_bwd_workspace_size(const void* d_grad_y, int64_t ldg, const v
  *   d_ids int32 [T][k] (output);  d_probs fp32 [T][k] (output)
  *   d_workspace: dlrm_moe_fwd_workspace_size bytes, 256-byte aligned
  *   d_status may be NULL; gets DLRM_STATUS_TIMEOUT if a bounded wait gave up.
- * probs * h enters the second product as two values of a 2-byte dtype (rounded
- * and the rounded rest), or in fp32.
+ * probs * h enters the second product with 21 bits or more: in fp32, as the sum
+ * of three bf16 values, or of two fp16 values times a power of two of their own,
+ * so its size is not bound by fp16's range.  (Where a second or third value is 0
+ * an infinite weight gives a NaN.)
  * Experts that no token chose are not read.  Requires H, I >= 1, 0 <= T <=
  * DLRM_MOE_MAX_TOKENS, 1 <= E <= DLRM_MOE_MAX_EXPERTS and 1 <= k <=
  * min(E, DLRM_MOE_MAX_TOP_K); larger T, E or k is DLRM_ERR_UNSUPPORTED.
