@@ -972,7 +972,7 @@ using namespace dlrm;
 
 extern "C" size_t dlrm_moe_fwd_workspace_size(dlrm_dtype dtype, int T, int H, int I, int E, int k)
 {
-    if (!moe_sizes_ok(dtype, T, H, I, E, k)) return 0;
+    if (!moe_sizes_ok(dtype, T, H, I, E, k) || T == 0) return 0;
     // the terms of probs * h, and fp16's reports and powers of two
     const size_t bytes = dtype == DLRM_BF16 ? 6 : 4;
     return dlrm_ws_align((size_t)T * k * I * bytes +
