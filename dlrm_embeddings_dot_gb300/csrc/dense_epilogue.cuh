@@ -27,22 +27,23 @@ inline int epilogue_vec(const Epilogue& e, int M, int es)
 }
 
 // a(.) of n values: one branch for all of them.
-template <int n>
+template <typename T, int n>
 __device__ __forceinline__ void act_n(float (&f)[n], int act)
 {
     if (act == DLRM_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < n; ++i) f[i] = act_f(f[i], DLRM_ACT_RELU);
+        for (int i = 0; i < n; ++i) f[i] = act_f<T>(f[i], DLRM_ACT_RELU);
     } else if (act == DLRM_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < n; ++i) f[i] = act_f(f[i], DLRM_ACT_GELU);
+        for (int i = 0; i < n; ++i) f[i] = act_f<T>(f[i], DLRM_ACT_GELU);
     } else if (act == DLRM_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < n; ++i) f[i] = act_f(f[i], DLRM_ACT_SILU);
+        for (int i = 0; i < n; ++i) f[i] = act_f<T>(f[i], DLRM_ACT_SILU);
     }
 }
 
 // f *= a'(z)
+template <typename T>
 __device__ __forceinline__ void slope8(float (&f)[8], const float (&z)[8], int act)
 {
     if (act == DLRM_ACT_RELU) {
@@ -50,10 +51,10 @@ __device__ __forceinline__ void slope8(float (&f)[8], const float (&z)[8], int a
         for (int i = 0; i < 8; ++i) f[i] = z[i] <= 0.f ? 0.f : f[i];
     } else if (act == DLRM_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= act_slope(z[i], DLRM_ACT_GELU);
+        for (int i = 0; i < 8; ++i) f[i] *= act_slope<T>(z[i], DLRM_ACT_GELU);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= act_slope(z[i], DLRM_ACT_SILU);
+        for (int i = 0; i < 8; ++i) f[i] *= act_slope<T>(z[i], DLRM_ACT_SILU);
     }
 }
 
@@ -73,7 +74,7 @@ __device__ __forceinline__ void finish8(const Epilogue& e, const DropKey& key, i
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = fmaf(f[i], e.scale, b[i]);   // zeros without a bias
     if (e.pre) store8<T, VEC>((T*)e.pre + row * e.ldp + col, n, f);
-    act_n(f, e.act);
+    act_n<T>(f, e.act);
     if (e.drop.thr) drop8(f, e.drop, key, (uint32_t)row, (uint32_t)col >> 3);
     if (e.res) {
         float g[8];

@@ -206,7 +206,7 @@ __device__ __forceinline__ void ragged_slice(const Epilogue& e, const DropKey& k
             for (int i = 0; i < kTurn; ++i)
                 if (in && r0 + i < rows) at[i * e.ldp] = from_f32<T>(f[i]);
         }
-        act_n(f, e.act);
+        act_n<T>(f, e.act);
         if (e.drop.thr) {
 #pragma unroll
             for (int i = 0; i < kTurn; ++i) {
@@ -491,7 +491,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     }
                     __syncwarp();
                     if (a.e.pre) write_box_row<T>(pre_box, f);
-                    act_n(f, a.e.act);
+                    act_n<T>(f, a.e.act);
                     if (a.e.drop.thr)
 #pragma unroll
                         for (int q = 0; q < kSlice / 8; ++q)

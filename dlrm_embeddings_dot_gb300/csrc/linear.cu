@@ -317,7 +317,7 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, 
                 if (act != DLRM_ACT_NONE) {
                     float z[8];
                     widen8<T>(b[k], z);
-                    slope8(f, z, act);
+                    slope8<T>(f, z, act);
                 }
                 if (drop.thr) drop8(f, drop, key, (uint32_t)rr, (uint32_t)g);
 #pragma unroll

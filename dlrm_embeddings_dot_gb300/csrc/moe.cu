@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
                 if (a.gated) up += p[(q * 2 + 1) * tile_floats];
             }
             const int slot = c.entry[tok];
-            float v = act_f(z, a.act);
+            float v = act_f<T>(z, a.act);
             if (a.gated) v *= up;
             v *= probs_s[slot];
             const int64_t row = (int64_t)(slot / kMaxK) * a.k + slot % kMaxK, plane = (int64_t)a.T * a.k * a.I;

@@ -57,7 +57,7 @@ __device__ __forceinline__ void tile_of_dz(const Grad& a, const DropKey& key, in
             if (a.act != DLRM_ACT_NONE) {
                 float z[8];
                 widen8<T>(load8<T, false>((const T*)a.pre + row * a.ldp + g * 8, n), z);
-                slope8(f, z, a.act);
+                slope8<T>(f, z, a.act);
             }
             if (a.drop.thr) drop8(f, a.drop, key, (uint32_t)row, (uint32_t)g);
         }

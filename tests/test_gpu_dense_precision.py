@@ -113,3 +113,35 @@ def test_infinite_and_nan_gradients(cuda_lib, dtype, N, name):
         inf = torch.isinf(want)
         assert int(inf.sum()) > 0 and torch.equal(got[inf], want[inf])
         assert bool(torch.isfinite(got[torch.isfinite(want)]).all())
+
+
+def _plain32(z, name, slope):
+    """The header's definition in 32 bits by torch."""
+    if name == "gelu":
+        cdf = 0.5 * (1 + torch.erf(z * 0.5**0.5))
+        return cdf + z * torch.exp(-0.5 * z * z) / (2 * torch.pi) ** 0.5 if slope else z * cdf
+    s = 1 / (1 + torch.exp(-z))
+    return s * (1 + z * (1 - s)) if slope else z / (1 + torch.exp(-z))
+
+
+@pytest.mark.parametrize("N", [1, 24])
+@pytest.mark.parametrize("name", ["gelu", "silu"])
+@pytest.mark.parametrize("span", [0.5, 3.0, 8.0])
+def test_fp32_activations_are_as_exact_as_their_definition_in_32_bits(cuda_lib, name, span, N):
+    """The same formula in the same arithmetic has the same error: the root mean square over a range is
+    that of torch's form to within a quarter.  (x is z, the weight 1: the sum before is exact.)"""
+    M = 1 << 16
+    z = torch.linspace(-span, span, M, device=dev())
+    x, w = z[:, None].contiguous(), torch.zeros(N, 1, device=dev())
+    w[0] = 1.0
+    y = torch.empty(M, N, device=dev())
+    n = cuda_lib.dlrm_linear_fwd_workspace_size(x, w)
+    cuda_lib.dlrm_linear_fwd(x, w, None, None, y, act=ref.ACT[name],
+                             workspace=torch.empty(n, dtype=torch.uint8, device=dev()) if n else None)
+    dy, pre = torch.zeros(M, N, device=dev()), torch.zeros(M, N, device=dev())
+    dy[:, 0], pre[:, 0] = 1.0, z
+    dx, _, _ = _gradients(cuda_lib, dy, x, w, pre, name)
+    for got, form, exact in ((y[:, 0], _plain32(z, name, False), ref.act(z.double(), name)),
+                             (dx[:, 0], _plain32(z, name, True), ref.slope(z.double(), name))):
+        own, plain = ((t.double() - exact).square().mean().sqrt().item() for t in (got, form))
+        assert own <= 1.25 * plain, (own, plain)
