@@ -13,6 +13,10 @@ from __future__ import annotations
 import ctypes
 import os
 
+from . import dense_abi
+from .dense_abi import (DLRM_ACT_GELU, DLRM_ACT_NONE, DLRM_ACT_RELU, DLRM_ACT_SILU, DLRM_MOE_MAX_EXPERTS,  # noqa: F401
+                        DLRM_MOE_MAX_TOKENS, DLRM_MOE_MAX_TOP_K)
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdlrm_gb300.so")
 
@@ -93,8 +97,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
               "dlrm_emb_interact_fwd_train", "dlrm_emb_interact_bwd", "dlrm_interact_bwd", "dlrm_emb_bwd_sgd", "dlrm_emb_bwd_sgd_noalloc", "dlrm_synth_fill_uniform"):
         getattr(L, f).restype = _I
     if hasattr(L, "dlrm_linear_fwd"):   # a library built before the dense network has none of it
-        from . import dense
-        dense.declare(L)
+        dense_abi.declare(L)
     if path is None:
         _lib = L
     return L
@@ -294,9 +297,8 @@ def dlrm_bottom_mlp_fwd(x, dims, weights, biases, out, workspace, status=None, s
 
 # ---------------------------------------------------------------- dense network
 _DENSE = frozenset((
-    "DLRM_ACT_NONE", "DLRM_ACT_RELU", "DLRM_ACT_GELU", "DLRM_ACT_SILU", "DLRM_MOE_MAX_TOKENS", "DLRM_MOE_MAX_EXPERTS",
-    "DLRM_MOE_MAX_TOP_K", "dlrm_dropout_fwd", "dlrm_dropout_bwd", "dlrm_linear_fwd", "dlrm_linear_fwd_workspace_size",
-    "dlrm_linear_bwd", "dlrm_linear_bwd_workspace_size", "dlrm_moe_fwd", "dlrm_moe_fwd_workspace_size"))
+    "dlrm_dropout_fwd", "dlrm_dropout_bwd", "dlrm_linear_fwd", "dlrm_linear_fwd_workspace_size", "dlrm_linear_bwd",
+    "dlrm_linear_bwd_workspace_size", "dlrm_moe_fwd", "dlrm_moe_fwd_workspace_size"))
 
 
 def __getattr__(name):

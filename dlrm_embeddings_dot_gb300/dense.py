@@ -16,36 +16,11 @@ import torch
 
 import dlrm_embeddings_dot_gb300 as _dl
 
-DLRM_ACT_NONE = 0
-DLRM_ACT_RELU = 1
-DLRM_ACT_GELU = 2
-DLRM_ACT_SILU = 3
-DLRM_MOE_MAX_TOKENS = 64
-DLRM_MOE_MAX_EXPERTS = 256
-DLRM_MOE_MAX_TOP_K = 8
+from .dense_abi import (DLRM_ACT_GELU, DLRM_ACT_NONE, DLRM_ACT_RELU, DLRM_ACT_SILU, DLRM_MOE_MAX_EXPERTS,  # noqa: F401
+                        DLRM_MOE_MAX_TOKENS, DLRM_MOE_MAX_TOP_K, declare)
 
-_P, _I, _L, _D, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_double, ctypes.c_size_t
 _TYPES = (torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.int64)
 _marshal = None
-
-_SIGNATURES = {
-    "dlrm_dropout_fwd": (_I, [_P, _L, _P, _L, _I, _I, _I, _D, _P, _P, _L, _P]),
-    "dlrm_dropout_bwd": (_I, [_P, _L, _I, _I, _I, _D, _P, _P, _L, _P]),
-    "dlrm_linear_fwd": (_I, [_P, _L, _P, _L, _P, _P, _L, _I, _I, _I, _I, _I, _D, _P, _P, _L, _P, _L, _P, _Z, _P, _P]),
-    "dlrm_linear_fwd_workspace_size": (_Z, [_P, _L, _P, _L, _I, _I, _I, _I]),
-    "dlrm_linear_bwd": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _I, _D, _P, _P, _L, _P, _L, _P, _P, _Z,
-                             _P, _P]),
-    "dlrm_linear_bwd_workspace_size": (_Z, [_P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _I, _D]),
-    "dlrm_moe_fwd": (_I, [_P, _L, _P, _P, _P, _P, _L, _I, _I, _I, _I, _I, _I, _I, _I, _P, _L, _P, _P, _P, _Z, _P, _P]),
-    "dlrm_moe_fwd_workspace_size": (_Z, [_I, _I, _I, _I, _I, _I]),
-}
-
-
-def declare(lib) -> None:
-    """Sets the C signatures of the entry points on a loaded library."""
-    for name, (res, args) in _SIGNATURES.items():
-        f = getattr(lib, name)
-        f.restype, f.argtypes = res, args
 
 
 def _load():
