@@ -31,8 +31,9 @@ def _load():
         try:
             from . import _marshal as m
         except ImportError as e:
-            raise RuntimeError("_marshal.so is missing: build the library first "
-                               "(python -c 'import __graft_entry__ as g; g.build()')") from e
+            raise RuntimeError("the _marshal extension is missing: build the library first "
+                               "(python -c 'import __graft_entry__ as g; g.build()'), with a C compiler and Python's "
+                               "headers") from e
         names = ("dlrm_dropout_fwd", "dlrm_dropout_bwd", "dlrm_linear_fwd", "dlrm_linear_bwd", "dlrm_moe_fwd")
         m.bind(_TYPES, torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device,
                torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream")
