@@ -23,10 +23,8 @@
 //             its items into its own per-token sums in shared memory, and the
 //             warps' and blocks' sums are added in a fixed order.  No atomics on
 //             floats, no partial outputs in HBM.
-#include <map>
-#include <mutex>
-
 #include "few_rows.cuh"
+#include "memo.h"
 #include "moe_layout.h"
 #include "tcgen05.cuh"
 
@@ -852,13 +850,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
 template <typename K>
 int resident_blocks(K kern, size_t smem, int cluster)
 {
-    static std::mutex mu;
-    static std::map<std::pair<int, size_t>, int> known;
+    const int one_each = num_sms() / cluster * cluster;
+    if (cluster == 1) return one_each;
     int dev = 0;
     cudaGetDevice(&dev);
-    std::lock_guard<std::mutex> lock(mu);
-    auto [it, fresh] = known.try_emplace({dev * 16 + cluster, smem}, num_sms() / cluster * cluster);
-    if (fresh && cluster > 1) {
+    static KernelMemo memo;   // one for all kernels of the type K: the key says which
+    return memo.get({reinterpret_cast<const void*>(kern), dev, cluster, smem}, [&] {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = cluster;
         cfg.blockDim = kThreads;
@@ -870,10 +867,10 @@ int resident_blocks(K kern, size_t smem, int cluster)
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) it->second = n * cluster;
-        else cudaGetLastError();
-    }
-    return it->second;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0) return n * cluster;
+        cudaGetLastError();
+        return one_each;
+    });
 }
 
 // Boxes of 16 rows by `steps` steps of a [rows][cols] matrix of weights.
