@@ -21,7 +21,7 @@ dropout_kernel(const T* __restrict__ x, int64_t ldx, const T* __restrict__ res, 
 {
     pdl_wait();
     const DropKey key = drop_key(drop);
-    const int64_t groups = (N + 7) / 8, runs = groups * M;
+    const int64_t groups = (N - 1) / 8 + 1, runs = groups * M;   // N + 7 may pass 2^31
     const int64_t stride = (int64_t)gridDim.x * kDropThreads;
     int64_t i = (int64_t)blockIdx.x * kDropThreads + threadIdx.x;
     int64_t row = i / groups, g = i - row * groups;
@@ -86,7 +86,7 @@ dlrm_status run_dropout(const char* fn, const void* x, int64_t ldx, const void* 
     if ((s = check_matrix(fn, "the output", y, ldy, M, N, es)) != DLRM_OK) return s;
     const bool vec = N % 8 == 0 && rows_aligned16(x, ldx, M, es) && rows_aligned16(y, ldy, M, es) &&
                      (!res || rows_aligned16(res, ldr, M, es));
-    const int64_t runs = (int64_t)((N + 7) / 8) * M;
+    const int64_t runs = (int64_t)((N - 1) / 8 + 1) * M;
     const int64_t want = (runs + kDropThreads - 1) / kDropThreads, most = (int64_t)num_sms() * 8;
     const int blocks = (int)(want < most ? want : most);
     return with_type(dtype, [&](auto t) {
