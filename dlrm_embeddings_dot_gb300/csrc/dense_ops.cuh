@@ -337,6 +337,8 @@ __device__ __forceinline__ uint32_t keep8(const Drop& d, const DropKey& k, uint3
 }
 
 // ---------------------------------------------------------------- host side
+constexpr int kMaxSize = INT32_MAX - (1 << 20);   // tiles and chunks that start below it end below 2^31
+
 inline bool dense_dtype_ok(dlrm_dtype dt) { return dt == DLRM_F32 || dt == DLRM_F16 || dt == DLRM_BF16; }
 inline int dense_dtype_size(dlrm_dtype dt) { return dt == DLRM_F32 ? 4 : 2; }
 

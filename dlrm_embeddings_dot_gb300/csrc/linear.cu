@@ -40,7 +40,6 @@ inline bool few_columns(int M, int N, int K) { return N <= 16 && (K <= 512 || M 
 // 6.4 / 13 and 9.2 / 13.  Its fragments hold 16 outputs.
 inline bool few_outputs(int N) { return N <= thin::kMaxOutputs; }
 
-constexpr int kMaxSize = INT32_MAX - (1 << 20);   // tiles and chunks that start below it end below 2^31
 constexpr int kOneChunk = 1024;   // rows that grad_z_kernel takes as one chunk
 
 // ------------------------------------------------------------------ packing

@@ -991,6 +991,7 @@ extern "C" dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_
     if (T > DLRM_MOE_MAX_TOKENS || E > kMaxE || k > kMaxK)
         return fail(DLRM_ERR_UNSUPPORTED, "%s: at most %d tokens, %d experts and %d experts a token", fn,
                     DLRM_MOE_MAX_TOKENS, kMaxE, kMaxK);
+    if (H > kMaxSize || I > kMaxSize) return fail(DLRM_ERR_UNSUPPORTED, "%s: sizes up to %d", fn, kMaxSize);
     if (T == 0) return DLRM_OK;
     const int es = dense_dtype_size(dtype);
     dlrm_status s;

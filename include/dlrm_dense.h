@@ -150,7 +150,8 @@ size_t dlrm_linear_bwd_workspace_size(const void* d_grad_y, int64_t ldg, const v
  * an infinite weight gives a NaN.)
  * Experts that no token chose are not read.  Requires H, I >= 1, 0 <= T <=
  * DLRM_MOE_MAX_TOKENS, 1 <= E <= DLRM_MOE_MAX_EXPERTS and 1 <= k <=
- * min(E, DLRM_MOE_MAX_TOP_K); larger T, E or k is DLRM_ERR_UNSUPPORTED.
+ * min(E, DLRM_MOE_MAX_TOP_K); larger T, E or k, H or I past 2^31 - 2^20 - 1, and
+ * 2^31 weight rows (E H, 2 E I) or more are DLRM_ERR_UNSUPPORTED.
  */
 dlrm_status dlrm_moe_fwd(const void* d_x, int64_t ldx, const void* d_w_router, const void* d_w1, const void* d_w2,
                          const void* d_residual, int64_t ldr, dlrm_dtype dtype, int T, int H, int I, int E, int k,

@@ -4,9 +4,26 @@ import pytest
 import torch
 
 import dense_ref as ref
+import dlrm_embeddings_dot_gb300 as dl
+from dlrm_embeddings_dot_gb300 import build as libbuild
 from gpu_util import dev
 
+FAKE = 0x10000      # never dereferenced
 MOST = 2**31 - 1
+
+
+def test_mixture_refuses_widths_near_2_31():
+    libbuild.build()
+    L = dl.load()
+
+    def call(H, I, T=1):
+        return L.dlrm_moe_fwd(FAKE, H, FAKE, FAKE, FAKE, None, 0, 1, T, H, I, 1, 1, 3, 0, FAKE, H, FAKE, FAKE, FAKE, 1 << 50,
+                              None, None)
+
+    for H, I in ((MOST, 1), (MOST - 6, 1), (1, MOST), (MOST - 2**20 + 1, 8)):
+        for T in (0, 1):
+            assert call(H, I, T) == dl.DLRM_ERR_UNSUPPORTED, (H, I, T)
+            assert "dlrm_moe_fwd" in dl.dlrm_last_error()
 
 
 @pytest.mark.gpu
