@@ -4,16 +4,16 @@
  * its checks and the ctypes call in Python the host needed 8 us for it.
  *
  * Each function takes the tensors and numbers of one entry point of
- * include/dlrm_dense.h, checks shapes, dtypes and strides (TypeError,
- * ValueError), calls the entry point through the address bind() was given and
- * returns its status.
+ * include/dlrm_dense.h, checks shapes, dtypes and strides, then that every tensor
+ * is on the current device (TypeError, ValueError), calls the entry point through
+ * the address bind() was given and returns its status.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include "dlrm_dense.h"
 
-static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_nbytes;
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_nbytes, *s_get_device;
 /* torch's dtypes: fp32, fp16, bf16 (their codes are the indices), int32, int64 */
 enum { F32, F16, BF16, I32, I64, N_TYPES };
 static PyObject* types[N_TYPES];
@@ -150,24 +150,62 @@ static int status_word(PyObject* t, void** p)
         *p = PyLong_AsVoidPtr(t);
         return !PyErr_Occurred();
     }
+    PyObject* n = PyObject_GetAttr(t, s_nbytes);
+    if (!n) return 0;
+    const size_t bytes = PyLong_AsSize_t(n);
+    Py_DECREF(n);
+    if (PyErr_Occurred()) return 0;
+    if (bytes < 4) {
+        PyErr_SetString(PyExc_ValueError, "status has fewer than 4 bytes");
+        return 0;
+    }
     return address(t, p);
 }
 
-/* A stream handle; None: torch's current stream on the current device. */
-static int stream(PyObject* t, void** p)
+/* The last of a call's checks: its tensors (the first n of t that are not None, nor
+   numbers: addresses) are on the current device.  Then the stream's handle; None: torch's
+   current stream on that device. */
+static int where(PyObject* const* t, const char* const* names, int n, PyObject* on, void** p)
 {
-    if (t != Py_None) {
-        *p = PyLong_AsVoidPtr(t);
+    PyObject* d = NULL;
+    long current = 0;
+    for (int i = 0; i < n; ++i) {
+        if (t[i] == Py_None || !names[i] || PyLong_Check(t[i])) continue;
+        PyObject* o = PyObject_CallMethodNoArgs(t[i], s_get_device);
+        if (!o) goto bad;
+        const long at = PyLong_AsLong(o);
+        Py_DECREF(o);
+        if (at == -1 && PyErr_Occurred()) goto bad;
+        if (at < 0) {
+            PyErr_Format(PyExc_ValueError, "%s is not on a CUDA device", names[i]);
+            goto bad;
+        }
+        if (!d) {
+            d = PyObject_CallNoArgs(get_device);
+            if (!d) return 0;
+            current = PyLong_AsLong(d);
+            if (current == -1 && PyErr_Occurred()) goto bad;
+        }
+        if (at != current) {
+            PyErr_Format(PyExc_ValueError, "%s is on device %ld, not on the current one (%ld)", names[i], at, current);
+            goto bad;
+        }
+    }
+    if (on != Py_None) {
+        Py_XDECREF(d);
+        *p = PyLong_AsVoidPtr(on);
         return !PyErr_Occurred();
     }
-    PyObject* d = PyObject_CallNoArgs(get_device);
-    if (!d) return 0;
+    if (!d && !(d = PyObject_CallNoArgs(get_device))) return 0;
     PyObject* s = PyObject_CallOneArg(get_raw_stream, d);
     Py_DECREF(d);
     if (!s) return 0;
     *p = PyLong_AsVoidPtr(s);
     Py_DECREF(s);
     return !PyErr_Occurred();
+bad:
+    Py_XDECREF(d);
+    return 0;
 }
 
 static int number(PyObject* t, int* v)
@@ -197,10 +235,11 @@ static PyObject* dropout_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *x, *r, *y, *rng, *st;
     double p;
     int c;
+    static const char* const names[] = {"x", "residual", "y", NULL, "rng"};
     if (!count(n, 6) || (c = type_code(a[0])) < 0 || !sizes(a[0], "x", 2, mn) ||
         !matrix(a[0], "x", types[c], mn[0], mn[1], &x, &ldx) || !matrix(a[1], "residual", types[c], mn[0], mn[1], &r, &ldr) ||
         !matrix(a[2], "y", types[c], mn[0], mn[1], &y, &ldy) || !real(a[3], &p) ||
-        !vector(a[4], "rng", types[I64], 2, &rng) || !stream(a[5], &st))
+        !vector(a[4], "rng", types[I64], 2, &rng) || !where(a, names, 5, a[5], &st))
         return NULL;
     return PyLong_FromLong(fn.dropout_fwd(x, ldx, r, ldr, (dlrm_dtype)c, (int)mn[0], (int)mn[1], p, rng, y, ldy, st));
 }
@@ -212,9 +251,10 @@ static PyObject* dropout_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *g, *x, *rng, *st;
     double p;
     int c;
+    static const char* const names[] = {"grad_y", "grad_x", NULL, "rng"};
     if (!count(n, 5) || (c = type_code(a[0])) < 0 || !sizes(a[0], "grad_y", 2, mn) ||
         !matrix(a[0], "grad_y", types[c], mn[0], mn[1], &g, &ldg) || !matrix(a[1], "grad_x", types[c], mn[0], mn[1], &x, &ldx) ||
-        !real(a[2], &p) || !vector(a[3], "rng", types[I64], 2, &rng) || !stream(a[4], &st))
+        !real(a[2], &p) || !vector(a[3], "rng", types[I64], 2, &rng) || !where(a, names, 4, a[4], &st))
         return NULL;
     return PyLong_FromLong(fn.dropout_bwd(g, ldg, (dlrm_dtype)c, (int)mn[0], (int)mn[1], p, rng, x, ldx, st));
 }
@@ -227,6 +267,7 @@ static PyObject* linear_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     size_t bytes;
     double p;
     int c, act;
+    static const char* const names[] = {"x", "w", "bias", "residual", "y", "pre", NULL, NULL, "rng", "workspace", "status"};
     if (!count(n, 12) || (c = type_code(a[0])) < 0 || !sizes(a[0], "x", 2, mk) || !sizes(a[1], "w", 2, nk)) return NULL;
     PyObject* t = types[c];
     const int64_t M = mk[0], K = mk[1], N = nk[0];
@@ -234,7 +275,7 @@ static PyObject* linear_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
         !vector(a[2], "bias", types[F32], N, &b) || !matrix(a[3], "residual", t, M, N, &r, &ldr) ||
         !matrix(a[4], "y", t, M, N, &y, &ldy) || !matrix(a[5], "pre", t, M, N, &z, &ldp) || !number(a[6], &act) ||
         !real(a[7], &p) || !vector(a[8], "rng", types[I64], 2, &rng) || !workspace(a[9], &ws, &bytes) ||
-        !status_word(a[10], &status) || !stream(a[11], &st))
+        !status_word(a[10], &status) || !where(a, names, 11, a[11], &st))
         return NULL;
     return PyLong_FromLong(fn.linear_fwd(x, ldx, w, ldw, b, r, ldr, (dlrm_dtype)c, (int)M, (int)N, (int)K, (dlrm_act)act, p,
                                          rng, y, ldy, z, ldp, ws, bytes, status, st));
@@ -248,6 +289,8 @@ static PyObject* linear_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     size_t bytes;
     double p;
     int c, act;
+    static const char* const names[] = {"grad_y", "x",  "w",  "pre", "grad_x",    "grad_w",
+                                        "grad_bias", NULL, NULL, "rng", "workspace", "status"};
     if (!count(n, 13) || (c = type_code(a[1])) < 0 || !sizes(a[1], "x", 2, mk) || !sizes(a[2], "w", 2, nk)) return NULL;
     PyObject* t = types[c];
     const int64_t M = mk[0], K = mk[1], N = nk[0];
@@ -256,7 +299,7 @@ static PyObject* linear_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
         !matrix(a[4], "grad_x", t, M, K, &dx, &lddx) || !matrix(a[5], "grad_w", t, N, K, &dw, &lddw) ||
         !vector(a[6], "grad_bias", types[F32], N, &db) || !number(a[7], &act) || !real(a[8], &p) ||
         !vector(a[9], "rng", types[I64], 2, &rng) || !workspace(a[10], &ws, &bytes) || !status_word(a[11], &status) ||
-        !stream(a[12], &st))
+        !where(a, names, 12, a[12], &st))
         return NULL;
     return PyLong_FromLong(fn.linear_bwd(g, ldg, x, ldx, w, ldw, z, ldp, (dlrm_dtype)c, (int)M, (int)N, (int)K,
                                          (dlrm_act)act, p, rng, dx, lddx, dw, lddw, db, ws, bytes, status, st));
@@ -269,6 +312,8 @@ static PyObject* moe_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *x, *wr, *w1, *w2, *r, *y, *ids, *probs, *ws, *status, *st;
     size_t bytes;
     int c, act, gated;
+    static const char* const names[] = {"x",   "w_router", "w1", "w2", "residual",  "y",
+                                        "ids", "probs",    NULL, NULL, "workspace", "status"};
     if (!count(n, 13) || (c = type_code(a[0])) < 0 || !sizes(a[0], "x", 2, th) || !sizes(a[1], "w_router", 2, eh) ||
         !sizes(a[3], "w2", 3, ehi) || !sizes(a[6], "ids", 2, tk) || (gated = PyObject_IsTrue(a[9])) < 0)
         return NULL;
@@ -280,7 +325,7 @@ static PyObject* moe_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
         !matrix(a[4], "residual", t, T, H, &r, &ldr) || !matrix(a[5], "y", t, T, H, &y, &ldy) ||
         !argument(a[6], "ids", types[I32], 2, choice, &ids, NULL) ||
         !argument(a[7], "probs", types[F32], 2, choice, &probs, NULL) || !number(a[8], &act) ||
-        !workspace(a[10], &ws, &bytes) || !status_word(a[11], &status) || !stream(a[12], &st))
+        !workspace(a[10], &ws, &bytes) || !status_word(a[11], &status) || !where(a, names, 12, a[12], &st))
         return NULL;
     return PyLong_FromLong(fn.moe_fwd(x, ldx, wr, w1, w2, r, ldr, (dlrm_dtype)c, (int)T, (int)H, (int)I, (int)E, (int)k,
                                       (dlrm_act)act, gated, y, ldy, ids, probs, ws, bytes, status, st));
@@ -328,6 +373,7 @@ PyMODINIT_FUNC PyInit__marshal(void)
     s_stride = PyUnicode_InternFromString("stride");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_nbytes = PyUnicode_InternFromString("nbytes");
-    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_nbytes) return NULL;
+    s_get_device = PyUnicode_InternFromString("get_device");
+    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_nbytes || !s_get_device) return NULL;
     return PyModule_Create(&module);
 }

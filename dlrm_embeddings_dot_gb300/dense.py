@@ -5,7 +5,8 @@ As in the package, every function has the name of the C entry point it calls and
 output tensors it is given.  Sizes and row distances come from the tensors: matrices are 2-D
 with unit column stride (rows may be further apart than their width), of one dtype (fp32,
 fp16 or bf16); biases and their gradients are fp32 vectors; ``rng`` is an int64 tensor of two
-elements (seed, offset) on the device.
+elements (seed, offset).  Every tensor is on the current device, ``rng``, ``workspace`` and
+``status`` too (ValueError otherwise).
 """
 
 from __future__ import annotations
