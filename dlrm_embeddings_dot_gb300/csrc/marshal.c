@@ -11,6 +11,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <limits.h>
+
 #include "dlrm_dense.h"
 
 static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_nbytes, *s_get_device;
@@ -210,8 +212,14 @@ bad:
 
 static int number(PyObject* t, int* v)
 {
-    *v = (int)PyLong_AsLong(t);
-    return !PyErr_Occurred();
+    const long long l = PyLong_AsLongLong(t);
+    if (l == -1 && PyErr_Occurred()) return 0;
+    if (l < INT_MIN || l > INT_MAX) {
+        PyErr_Format(PyExc_ValueError, "act is %lld", l);
+        return 0;
+    }
+    *v = (int)l;
+    return 1;
 }
 
 static int real(PyObject* t, double* v)

@@ -96,3 +96,11 @@ def test_short_status_is_refused():
     x, w, y = torch.zeros(4, 16), torch.zeros(8, 16), torch.zeros(4, 8)
     with pytest.raises(ValueError, match="status"):
         dl.dlrm_linear_fwd(x, w, None, None, y, status=torch.zeros(0, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("act", [2**32, 2**32 + 1, -2**31 - 1])
+def test_activations_past_32_bits_are_refused(act):
+    """2^32 + 1 is not RELU."""
+    x, w, y = (Elsewhere(torch.zeros(4, 16), 0), Elsewhere(torch.zeros(8, 16), 0), Elsewhere(torch.zeros(4, 8), 0))
+    with pytest.raises(ValueError, match="^act is"):
+        _on_device_0(dl.dlrm_linear_fwd, dict(x=x, w=w, bias=None, residual=None, y=y, act=act))
