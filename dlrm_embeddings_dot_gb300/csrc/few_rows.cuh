@@ -14,7 +14,11 @@
 //   fp32, up to 8 tokens: 8 values (32 of K), multiplied and added in fp32;
 //     the four lanes of a row add up their shares at the end
 //   fp32, more tokens: the same values as three bf16 parts each (8 + 8 + 8
-//     bits), whose six products, the smallest first, give the fp32 product
+//     bits), whose six products, the smallest first, give the fp32 product.  The
+//     tensor cores cut what they add to an accumulator instead of rounding it, so
+//     16 of K are summed from zero and added in fp32: in one accumulator through
+//     all of K the error was 3 to 7 times an fp32 product's (32 x 4096 x 4096:
+//     3.7e-6 against 1.2e-6, 32768 x 256 to 16: 1.9e-6 against 2.9e-7)
 #pragma once
 
 #include "dense_ops.cuh"
@@ -117,12 +121,15 @@ __device__ __forceinline__ void mac16(float (&acc)[4], uint4 a, uint4 b, uint4 x
 {
     if constexpr (std::is_same_v<T, float>) {
         const Parts p = split4(a), q = split4(b), y = split4(x);
-        mma16816<bf16>(acc, p.hi[0], q.hi[0], p.hi[1], q.hi[1], y.lo[0], y.lo[1]);
-        mma16816<bf16>(acc, p.lo[0], q.lo[0], p.lo[1], q.lo[1], y.hi[0], y.hi[1]);
-        mma16816<bf16>(acc, p.mid[0], q.mid[0], p.mid[1], q.mid[1], y.mid[0], y.mid[1]);
-        mma16816<bf16>(acc, p.hi[0], q.hi[0], p.hi[1], q.hi[1], y.mid[0], y.mid[1]);
-        mma16816<bf16>(acc, p.mid[0], q.mid[0], p.mid[1], q.mid[1], y.hi[0], y.hi[1]);
-        mma16816<bf16>(acc, p.hi[0], q.hi[0], p.hi[1], q.hi[1], y.hi[0], y.hi[1]);
+        float d[4] = {};
+        mma16816<bf16>(d, p.hi[0], q.hi[0], p.hi[1], q.hi[1], y.lo[0], y.lo[1]);
+        mma16816<bf16>(d, p.lo[0], q.lo[0], p.lo[1], q.lo[1], y.hi[0], y.hi[1]);
+        mma16816<bf16>(d, p.mid[0], q.mid[0], p.mid[1], q.mid[1], y.mid[0], y.mid[1]);
+        mma16816<bf16>(d, p.hi[0], q.hi[0], p.hi[1], q.hi[1], y.mid[0], y.mid[1]);
+        mma16816<bf16>(d, p.mid[0], q.mid[0], p.mid[1], q.mid[1], y.hi[0], y.hi[1]);
+        mma16816<bf16>(d, p.hi[0], q.hi[0], p.hi[1], q.hi[1], y.hi[0], y.hi[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += d[i];
     } else {
         mma16816<T>(acc, a.x, b.x, a.y, b.y, x.x, x.y);
         mma16816<T>(acc, a.z, b.z, a.w, b.w, x.z, x.w);

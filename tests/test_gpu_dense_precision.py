@@ -145,3 +145,34 @@ def test_fp32_activations_are_as_exact_as_their_definition_in_32_bits(cuda_lib, 
                              (dx[:, 0], _plain32(z, name, True), ref.slope(z.double(), name))):
         own, plain = ((t.double() - exact).square().mean().sqrt().item() for t in (got, form))
         assert own <= 1.25 * plain, (own, plain)
+
+
+def _rms_share(got, exact):
+    return ((got.double() - exact).norm() / exact.norm()).item()
+
+
+@pytest.mark.parametrize("M,N,K", [(32, 4096, 4096), (9, 1024, 480), (64, 512, 1000), (32768, 16, 256), (20000, 9, 300)])
+def test_fp32_sums_on_fragments_are_fp32_sums(cuda_lib, M, N, K):
+    """Few rows or few outputs, more than eight tokens: blocks of 16 of K, each within 2^-22 for the cuts of its
+    six sums, are added in fp32, a rounding of 2^-24 each; for terms of random sign they add like their
+    square root."""
+    g = torch.Generator().manual_seed(M)
+    x, w = _rand(g, M, K), _rand(g, N, K, std=K**-0.5)
+    y = torch.empty(M, N, device=dev())
+    n = cuda_lib.dlrm_linear_fwd_workspace_size(x, w)
+    cuda_lib.dlrm_linear_fwd(x, w, None, None, y, workspace=torch.empty(n, dtype=torch.uint8, device=dev()) if n else None)
+    assert _rms_share(y, x.double() @ w.double().t()) <= (K / 16) ** 0.5 * 2.0**-24 + 2.0**-22
+
+
+@pytest.mark.parametrize("H,I", [(2048, 1024), (1001, 515)])
+def test_fp32_mixture_sums_are_fp32_sums(cuda_lib, H, I):
+    """One expert with 32 tokens: both products within the same bound."""
+    T = 32
+    g = torch.Generator().manual_seed(H)
+    x, wr = _rand(g, T, H), torch.zeros(1, H, device=dev())
+    w1, w2 = _rand(g, 1, I, H, std=H**-0.5), _rand(g, 1, H, I, std=I**-0.5)
+    y, probs, ids = torch.empty_like(x), torch.empty(T, 1, device=dev()), torch.empty(T, 1, dtype=torch.int32, device=dev())
+    cuda_lib.dlrm_moe_fwd(x, wr, w1, w2, None, y, ids, probs, act=0, gated=False, workspace=torch.empty(
+        cuda_lib.dlrm_moe_fwd_workspace_size(x, wr, w1, w2, 1), dtype=torch.uint8, device=dev()))
+    exact = x.double() @ w1[0].double().t() @ w2[0].double().t()
+    assert _rms_share(y, exact) <= ((H / 16) ** 0.5 + (I / 16) ** 0.5) * 2.0**-24 + 2 * 2.0**-22
