@@ -21,7 +21,13 @@
 // epilogue of this one.
 //
 // fp32 operands come as three bf16 planes (see split planes in linear.cu); the
-// K loop then runs over six plane pairs, the smallest products first.  A gradient
+// K loop then runs over six plane pairs, the smallest products first.  The tensor
+// cores cut what they add to an accumulator instead of rounding it, which shrinks a
+// sum by 8e-10 of itself for each of K: past kChain blocks of K (LONG) the products of
+// the first planes go to the accumulators in segments, which the epilogue warps add up
+// in registers while the next one runs (16384 x 1024 outputs, error against 64 bits,
+// one accumulator / segments: K = 1024 9.7e-7 / 3.5e-7, 152 / 155 us; K = 4096 4.3e-6 / 4.0e-7;
+// the library's fp32 5.7e-7 and 1.2e-6).  A gradient
 // that its 2-byte type does not hold comes as two planes of A.  Few
 // output tiles: K is split over blocks, each writing its fp32 partial tile, and
 // finish_kernel adds them in order and applies the epilogue.
@@ -43,6 +49,7 @@ constexpr int kSlice = 32;          // columns of an epilogue slice
 constexpr int kSliceStep = kEpiWarps / 4 * kSlice;
 constexpr int kMaxStages = 8;
 constexpr int kMaxPairs = 6;         // products of two operands of three planes each
+constexpr int kChain = 6;           // 64-wide blocks of K that fp32's first planes add up in one accumulator
 constexpr int kSmemLimit = 232448;  // 227 KB opt-in per block
 
 struct Args {
@@ -128,6 +135,44 @@ __device__ __forceinline__ Range k_range(const Args& a, int split)
 {
     if (a.splits == 1) return {0, a.kb};   // a 64-bit division takes as long as a K block's products
     return {(int)((int64_t)a.kb * split / a.splits), (int)((int64_t)a.kb * (split + 1) / a.splits)};
+}
+
+// Segments of a range of K, and their length in blocks (the last may be shorter).
+struct Segments {
+    int n, len;
+};
+template <bool LONG>
+__device__ __forceinline__ Segments segments(const Range& r)
+{
+    const int blocks = r.b1 - r.b0;
+    if (!LONG || blocks <= kChain) return {1, blocks};
+    const int n = (blocks + kChain - 1) / kChain, len = (blocks + n - 1) / n;
+    return {(blocks + len - 1) / len, len};
+}
+
+// sum += the warp's 32 x 32 slice of the accumulator at taddr
+__device__ __forceinline__ void add_slice(uint32_t taddr, float (&sum)[kSlice])
+{
+#pragma unroll
+    for (int h = 0; h < kSlice; h += 16) {
+        uint32_t v[16];
+        tmem_ld_x16(taddr + h, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[h + i] += __uint_as_float(v[i]);
+    }
+}
+
+// The slice at taddr = sum
+__device__ __forceinline__ void put_slice(uint32_t taddr, const float (&sum)[kSlice])
+{
+#pragma unroll
+    for (int h = 0; h < kSlice; h += 16) {
+        uint32_t v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[h + i]);
+        tmem_st_x16(taddr + h, v);
+    }
 }
 
 // The warp's 32 x 32 slice of the accumulator at taddr into its scratch, a row
@@ -226,8 +271,8 @@ __device__ __forceinline__ void ragged_slice(const Epilogue& e, const DropKey& k
 }
 
 // BOXES: results leave as TMA boxes; otherwise as a split's partial tiles, or by
-// ragged_slice.
-template <typename T, bool PAIR, bool BOXES>
+// ragged_slice.  LONG: fp32 with more than kChain blocks of K.
+template <typename T, bool PAIR, bool BOXES, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_pre,
@@ -371,43 +416,52 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             uint32_t phase = 0;
             auto issue = [&](auto step_a, auto step_b) {   // the descriptors' steps as constants
             constexpr uint32_t da = decltype(step_a)::value, db = decltype(step_b)::value;
-            for (int t = first; t < tiles; t += stride, ++it) {
-                const auto [b0, b1] = k_range(a, a.splits == 1 ? 0 : t / per_split);
-                const int buf = it & 1;
-                mbar_wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.wait_cycles);
-                if (__any_sync(~0u, *abort_flag != 0)) break;
-                tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(buf * BN);
-                uint32_t accumulate = 0;
-                for (int p = 0; p < a.pairs; ++p) {
-                    for (int kb = b0; kb < b1; ++kb) {
-                        mbar_wait(&full[stage], phase, abort_flag, a.wait_cycles);
-                        __syncwarp();
-                        tc_fence_after();
-                        const uint64_t ad = ad0 + (uint32_t)(stage * (stage_bytes / 16));
-                        const uint64_t bd = bd0 + (uint32_t)(stage * (stage_bytes / 16));
-                        if (elect_one()) {
-                            if (kb != a.kb - 1 || a.last_steps == 4) {
-                                mma(d, ad, bd, accumulate);
-                                mma(d, ad + da, bd + db, 1);
-                                mma(d, ad + 2 * da, bd + 2 * db, 1);
-                                mma(d, ad + 3 * da, bd + 3 * db, 1);
-                            } else {   // the rest of K holds zeros past last_steps
-                                for (int kk = 0; kk < a.last_steps; ++kk)
-                                    mma(d, ad + kk * da, bd + kk * db, kk ? 1 : accumulate);
+            for (int t = first; t < tiles; t += stride) {
+                const Range r = k_range(a, a.splits == 1 ? 0 : t / per_split);
+                const Segments sg = segments<LONG>(r);
+                bool given_up = false;
+                for (int s = 0; s < sg.n; ++s, ++it) {
+                    const int buf = it & 1;
+                    mbar_wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.wait_cycles);
+                    given_up = __any_sync(~0u, *abort_flag != 0);
+                    if (given_up) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + (uint32_t)(buf * BN);
+                    uint32_t accumulate = 0;
+                    // the small products all in the first segment, then the first planes' share
+                    for (int p = s ? a.pairs - 1 : 0; p < a.pairs; ++p) {
+                        const bool last = p == a.pairs - 1;
+                        const int b0 = last ? r.b0 + s * sg.len : r.b0, b1 = last ? min(r.b1, b0 + sg.len) : r.b1;
+                        for (int kb = b0; kb < b1; ++kb) {
+                            mbar_wait(&full[stage], phase, abort_flag, a.wait_cycles);
+                            __syncwarp();
+                            tc_fence_after();
+                            const uint64_t ad = ad0 + (uint32_t)(stage * (stage_bytes / 16));
+                            const uint64_t bd = bd0 + (uint32_t)(stage * (stage_bytes / 16));
+                            if (elect_one()) {
+                                if (kb != a.kb - 1 || a.last_steps == 4) {
+                                    mma(d, ad, bd, accumulate);
+                                    mma(d, ad + da, bd + db, 1);
+                                    mma(d, ad + 2 * da, bd + 2 * db, 1);
+                                    mma(d, ad + 3 * da, bd + 3 * db, 1);
+                                } else {   // the rest of K holds zeros past last_steps
+                                    for (int kk = 0; kk < a.last_steps; ++kk)
+                                        mma(d, ad + kk * da, bd + kk * db, kk ? 1 : accumulate);
+                                }
+                                commit(&empty[stage]);
                             }
-                            commit(&empty[stage]);
-                        }
-                        accumulate = 1;
-                        if (++stage == NS) {
-                            stage = 0;
-                            phase ^= 1u;
+                            accumulate = 1;
+                            if (++stage == NS) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
                         }
                     }
+                    __syncwarp();
+                    if (elect_one()) commit(&tfull[buf]);
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (elect_one()) commit(&tfull[buf]);
-                __syncwarp();
+                if (given_up) break;
             }
             };
             using K = std::integral_constant<uint32_t, kMajor>;
@@ -432,10 +486,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         int it = 0;
         uint32_t asked = 0, used = 0;                          // residual slices asked for, and added
         for (int t = first; t < tiles; t += stride, ++it) {
-            const int buf = it & 1;
             const int split = a.splits == 1 ? 0 : t / per_split, tt = t - split * per_split;
             const int row0 = (tt / a.tiles_n * CG + rank) * kBM + 32 * quarter, n0 = tt % a.tiles_n * BN;
-            const uint32_t taddr = tmem_base + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(buf * BN);
+            const uint32_t lanes = tmem_base + ((uint32_t)(32 * quarter) << 16);
             const int cols = row0 < a.M ? min(BN, a.N - n0) : 0;   // none of the warp's rows may lie inside
             auto ask = [&](int c0) {   // the residual's slice at c0, ahead of its use
                 if (lane == 0) {
@@ -445,16 +498,49 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 ++asked;
             };
             if (BOXES && a.e.res && kSlice * part < cols) ask(kSlice * part);
-            if (!__all_sync(~0u, mbar_wait(&tfull[buf], (uint32_t)(it >> 1) & 1u, abort_flag, a.wait_cycles))) break;
-            tc_fence_after();
-            auto release = [&] {   // the accumulator has been read: the tile after next may overwrite it
+            auto arrived = [&] {   // the products of buffer it & 1
+                const bool in = __all_sync(~0u, mbar_wait(&tfull[it & 1], (uint32_t)(it >> 1) & 1u, abort_flag, a.wait_cycles));
+                tc_fence_after();
+                return in;
+            };
+            auto release = [&] {   // the accumulator has been read: the tile or segment after next may overwrite it
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (PAIR) mbar_arrive_cluster(peer_u32(&tempty[buf], 0));
-                    else mbar_arrive(&tempty[buf]);
+                    if constexpr (PAIR) mbar_arrive_cluster(peer_u32(&tempty[it & 1], 0));
+                    else mbar_arrive(&tempty[it & 1]);
                 }
             };
+            const Segments sg = segments<LONG>(k_range(a, split));
+            if (sg.n == 1) {
+                if (!arrived()) break;
+            } else {
+                // the segments' sums, then the whole in the last one's place, from where it goes on as any tile
+                constexpr int kSlices = 256 / kSliceStep;   // the most a warp has
+                float sum[kSlices][kSlice] = {};
+                bool in = true;
+                for (int s = 0; in && s < sg.n; ++s) {
+                    if (s) {
+                        release();
+                        ++it;
+                    }
+                    in = arrived();
+                    if (!in) break;
+#pragma unroll
+                    for (int j = 0; j < kSlices; ++j) {
+                        const int c0 = kSlice * part + kSliceStep * j;
+                        if (c0 < cols) add_slice(lanes + (uint32_t)((it & 1) * BN + c0), sum[j]);
+                    }
+                }
+                if (!in) break;
+#pragma unroll
+                for (int j = 0; j < kSlices; ++j) {
+                    const int c0 = kSlice * part + kSliceStep * j;
+                    if (c0 < cols) put_slice(lanes + (uint32_t)((it & 1) * BN + c0), sum[j]);
+                }
+                tmem_wait_st();
+            }
+            const uint32_t taddr = lanes + (uint32_t)((it & 1) * BN);
             if (kSlice * part >= cols) {
                 release();
                 continue;
@@ -741,8 +827,14 @@ dlrm_status run(const char* fn, const Shape& s, const Operand& A, const Operand&
     const int64_t tiles = tm * tn * p.splits, units = num_sms() / CG;
     const int grid = (int)(tiles < units ? tiles : units) * CG;
     const size_t smem = smem_bytes(b_rows, a.NS, a.warp_bytes);
-    auto kern = p.pair ? (boxes ? gemm_kernel<T, true, true> : gemm_kernel<T, true, false>)
-                       : (boxes ? gemm_kernel<T, false, true> : gemm_kernel<T, false, false>);
+    auto pick = [&](auto l) {
+        constexpr bool LONG = decltype(l)::value;
+        return p.pair ? (boxes ? gemm_kernel<T, true, true, LONG> : gemm_kernel<T, true, false, LONG>)
+                      : (boxes ? gemm_kernel<T, false, true, LONG> : gemm_kernel<T, false, false, LONG>);
+    };
+    auto kern = pick(std::false_type());
+    if constexpr (std::is_same_v<T, float>)
+        if ((a.kb + p.splits - 1) / p.splits > kChain) kern = pick(std::true_type());
     cudaError_t ce = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (ce != cudaSuccess) return fail(DLRM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
     return check_launch_pdl(p.pair ? launch_cluster(kern, dim3(grid), dim3(kThreads), smem, st, 2, ma, mb, mo, mp, mr, a)

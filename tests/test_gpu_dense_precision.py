@@ -176,3 +176,26 @@ def test_fp32_mixture_sums_are_fp32_sums(cuda_lib, H, I):
         cuda_lib.dlrm_moe_fwd_workspace_size(x, wr, w1, w2, 1), dtype=torch.uint8, device=dev()))
     exact = x.double() @ w1[0].double().t() @ w2[0].double().t()
     assert _rms_share(y, exact) <= ((H / 16) ** 0.5 + (I / 16) ** 0.5) * 2.0**-24 + 2 * 2.0**-22
+
+
+@pytest.mark.parametrize("M,N,K", [(8192, 1024, 512), (8192, 1024, 1024), (2000, 520, 2048), (8192, 512, 4096), (4099, 771, 771),
+                                   (300, 96, 1100), (20000, 40, 1048)])
+def test_fp32_sums_of_any_length_are_fp32_sums(cuda_lib, M, N, K):
+    """384 of K are added up on the tensor cores, 24 sums that are each cut by half of 2^-23 on average, at
+    sizes that grow like a square root (two thirds of the last): 24 / 2 * 2 / 3 * 2^-23 = 9.5e-7, less where the
+    accumulator keeps bits below; beyond, such blocks are added in fp32.  So no length has more than a
+    library's fp32 product of 2,048 of K, 8e-7."""
+    g = torch.Generator().manual_seed(K)
+    x, w = _rand(g, M, K), _rand(g, N, K, std=K**-0.5)
+    y = torch.empty(M, N, device=dev())
+    n = cuda_lib.dlrm_linear_fwd_workspace_size(x, w)
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    cuda_lib.dlrm_linear_fwd(x, w, None, None, y, status=status,
+                             workspace=torch.empty(n, dtype=torch.uint8, device=dev()) if n else None)
+    assert _rms_share(y, x.double() @ w.double().t()) <= 8e-7 and int(status.item()) == 0
+    # the gradients sum over N and over M
+    dy, dx, dw, db = _rand(g, M, N), torch.empty_like(x), torch.empty_like(w), torch.empty(N, device=dev())
+    n = cuda_lib.dlrm_linear_bwd_workspace_size(dy, x, w)
+    cuda_lib.dlrm_linear_bwd(dy, x, w, None, dx, dw, db, workspace=torch.empty(n, dtype=torch.uint8, device=dev()))
+    assert _rms_share(dx, dy.double() @ w.double()) <= 8e-7
+    assert _rms_share(dw, dy.double().t() @ x.double()) <= 8e-7
