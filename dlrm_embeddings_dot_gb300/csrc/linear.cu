@@ -21,15 +21,20 @@ using gemm::padded;
 using gemm::Shape;
 
 // Whether the forward streams the weights (linear_few_kernel) instead of running on
-// tcgen05 tiles.  Measured, us, streamed / tiles: 1024 x 480 bf16 2.5 / 5.9 at 16 rows,
-// 4.0 / 5.9 at 64; 4096 x 1024 5.1 / 8.1 at 48 rows (fp32 20.3 / 19.1); 4096 x 4096
-// 10.0 / 14.1 at 32 rows (fp32 40.0 / 53.0), but 14.4 / 13.0 at 48 (fp32 70.3 / 53.6): there
-// a block's 16 weight rows come with more token bytes from L2 than weight bytes.
-inline bool few_rows(int M, int N, int K) { return M <= 32 || (M <= few::kMaxTokens && (int64_t)N * K <= 1 << 23); }
+// tcgen05 tiles.  Measured, us, streamed / tiles.  bf16: 1024 x 480 2.6 / 6.0 at 16 rows, 4.0 /
+// 6.0 at 64; 4096 x 1024 5.2 / 8.2 at 48 rows; 1024 x 4096 8.9 / 8.9 at 48; 4096 x 4096 10.3 / 14.3 at 32
+// rows but 13.0 / 13.1 at 40 and 15 / 13 at 48: there a block's 16 weight rows come with more
+// token bytes from L2 than weight bytes.  fp32: 1024 x 480 3.5 / 10.3 at 16 rows, 8.1 / 10.7 at
+// 64; 4096 x 1024 13.1 / 19.0 at 32 rows but 20.6 / 19.5 at 48; 4096 x 4096 42 / 54 and 72 / 55.
+// So weights of 16 MB and more are streamed for up to 32 rows only.
+inline bool few_rows(int M, int N, int K, int es)
+{
+    return M <= 32 || (M <= few::kMaxTokens && (int64_t)N * K * es < 1 << 24);
+}
 
 // Whether the forward streams the rows of x (linear_thin_kernel).  Measured, us,
 // streamed / tiles (whose 64 columns are mostly waste): 65536 x 256 fp16 5.6 / 16.8 for 1
-// output, 8.4 / 9.9 for 16 (fp32 13 / 71, 37 / 59); 300 x 64 1.8 / 6.1; but 1711 x 1285
+// output, 8.4 / 9.9 for 16 (fp32 14 / 71, 40 / 59); 300 x 64 1.8 / 6.1; but 1711 x 1285
 // 20.8 / 10.0 (fp32 35.1 / 17.6 for 16): a warp walks K alone, and there too few warps do.
 inline bool few_columns(int M, int N, int K) { return N <= 16 && (K <= 512 || M >= 1 << 14); }
 
@@ -430,7 +435,7 @@ struct FwdLayout {
 FwdLayout fwd_layout(const void* x, int64_t ldx, const void* w, int64_t ldw, dlrm_dtype dt, int M, int N, int K)
 {
     FwdLayout l = {};
-    if (few_rows(M, N, K) || few_columns(M, N, K)) return l;
+    if (few_rows(M, N, K, dense_dtype_size(dt)) || few_columns(M, N, K)) return l;
     l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, planes_of(dt)) : 0;
     l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, planes_of(dt)) : 0;
     l.partial = gemm::partial_bytes(fwd_shape(dt, M, N, K));
@@ -499,7 +504,7 @@ extern "C" dlrm_status dlrm_linear_fwd(const void* d_x, int64_t ldx, const void*
     const cudaStream_t st = as_stream(stream);
     return with_type(dtype, [&](auto t) -> dlrm_status {
         using T = decltype(t);
-        if (few_rows(M, N, K)) return launch_few<T>(d_x, ldx, d_w, ldw, M, N, K, e, st);
+        if (few_rows(M, N, K, es)) return launch_few<T>(d_x, ldx, d_w, ldw, M, N, K, e, st);
         if (few_columns(M, N, K)) return launch_thin<T>(d_x, ldx, d_w, ldw, M, N, K, e, st);
         uint8_t* ws = (uint8_t*)d_workspace;
         void *xs = l.x ? ws : nullptr, *wsp = l.w ? ws + l.x : nullptr;
