@@ -25,7 +25,8 @@ using gemm::Shape;
 // 6.0 at 64; 4096 x 1024 5.2 / 8.2 at 48 rows; 1024 x 4096 8.9 / 8.9 at 48; 4096 x 4096 10.3 / 14.3 at 32
 // rows but 13.0 / 13.1 at 40 and 15 / 13 at 48: there a block's 16 weight rows come with more
 // token bytes from L2 than weight bytes.  fp32: 1024 x 480 3.5 / 10.3 at 16 rows, 8.1 / 10.7 at
-// 64; 4096 x 1024 13.1 / 19.0 at 32 rows but 20.6 / 19.5 at 48; 4096 x 4096 42 / 54 and 72 / 55.
+// 64; 4096 x 1024 13.1 / 19.0 at 32 rows but 20.4 / 19.6 at 48; 2048 x 4096 24.5 / 31.1 and 39.5 /
+// 32.0; 4096 x 4096 42 / 54 and 72 / 55.
 // So weights of 16 MB and more are streamed for up to 32 rows only.
 inline bool few_rows(int M, int N, int K, int es)
 {
