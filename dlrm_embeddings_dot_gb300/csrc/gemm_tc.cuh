@@ -383,13 +383,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             for (int j = (q > NS ? q - NS : 0); ok && j < q; ++j)
                 ok = mbar_wait(&empty[j % NS], (uint32_t)(j / NS) & 1u, abort_flag, a.wait_cycles);
             if (*abort_flag) {   // the copies already issued must land before the block exits
-                if (rank == 0) {
-                    for (int j = (q > NS ? q - NS : 0); j < q; ++j) mbar_drain(&full[j % NS], (uint32_t)(j / NS) & 1u);
-                } else {         // counted in the leader's memory, which waits for them; its abort may have
-                                 // come first, so leave them a thousand times a copy's latency
+                if constexpr (PAIR) {
+                    // counted together with the other block's, which may have given up before it asked
+                    // for them: leave them a thousand times a copy's latency
                     const long long t0 = clock64();
                     while (clock64() - t0 < 2000000) {
                     }
+                } else {
+                    for (int j = (q > NS ? q - NS : 0); j < q; ++j) mbar_drain(&full[j % NS], (uint32_t)(j / NS) & 1u);
                 }
             }
         }
@@ -409,9 +410,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const uint64_t ad0 = a.a_mn ? sw128_desc_mn(sa, 8192, 1024) : sw128_desc(sa);
             const uint64_t bd0 = a.b_mn ? sw128_desc_mn(sb, 8192, 1024) : sw128_desc(sb);
             constexpr uint32_t kMajor = 32 / 16, mnMajor = 2048 / 16;
-            // A wait that gives up raises the abort flag, after which every wait returns
-            // at once: the flag is looked at once a tile, and until then products of
-            // whatever the ring holds are harmless.
+            // A wait that gives up ends the issue at once: a stage whose copies have not
+            // landed must not be handed back, as its barrier takes no second request
+            // while one is open, and the other block would load on into its own.
             int stage = 0, it = 0;
             uint32_t phase = 0;
             auto issue = [&](auto step_a, auto step_b) {   // the descriptors' steps as constants
@@ -419,22 +420,21 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             for (int t = first; t < tiles; t += stride) {
                 const Range r = k_range(a, a.splits == 1 ? 0 : t / per_split);
                 const Segments sg = segments<LONG>(r);
-                bool given_up = false;
-                for (int s = 0; s < sg.n; ++s, ++it) {
+                bool ok = true;
+                for (int s = 0; ok && s < sg.n; ++s) {
                     const int buf = it & 1;
-                    mbar_wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.wait_cycles);
-                    given_up = __any_sync(~0u, *abort_flag != 0);
-                    if (given_up) break;
+                    ok = __all_sync(~0u, mbar_wait(&tempty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u, abort_flag, a.wait_cycles));
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem_base + (uint32_t)(buf * BN);
                     uint32_t accumulate = 0;
                     // the small products all in the first segment, then the first planes' share
-                    for (int p = s ? a.pairs - 1 : 0; p < a.pairs; ++p) {
+                    for (int p = s ? a.pairs - 1 : 0; ok && p < a.pairs; ++p) {
                         const bool last = p == a.pairs - 1;
                         const int b0 = last ? r.b0 + s * sg.len : r.b0, b1 = last ? min(r.b1, b0 + sg.len) : r.b1;
                         for (int kb = b0; kb < b1; ++kb) {
-                            mbar_wait(&full[stage], phase, abort_flag, a.wait_cycles);
-                            __syncwarp();
+                            ok = __all_sync(~0u, mbar_wait(&full[stage], phase, abort_flag, a.wait_cycles));
+                            if (!ok) break;
                             tc_fence_after();
                             const uint64_t ad = ad0 + (uint32_t)(stage * (stage_bytes / 16));
                             const uint64_t bd = bd0 + (uint32_t)(stage * (stage_bytes / 16));
@@ -457,11 +457,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                             }
                         }
                     }
+                    if (!ok) break;
                     __syncwarp();
                     if (elect_one()) commit(&tfull[buf]);
                     __syncwarp();
+                    ++it;
                 }
-                if (given_up) break;
+                if (!ok) break;
             }
             };
             using K = std::integral_constant<uint32_t, kMajor>;
@@ -469,7 +471,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             if (a.a_mn) issue(MN{}, MN{});
             else if (a.b_mn) issue(K{}, MN{});
             else issue(K{}, K{});
-            // MMAs already issued must finish before TMEM is freed
+            // MMAs already issued must finish before TMEM is freed; tfull[it & 1] has not been
+            // committed to for this segment
             if (__any_sync(~0u, *abort_flag != 0) && elect_one()) {
                 commit(&tfull[it & 1]);
                 mbar_drain(&tfull[it & 1], (uint32_t)(it >> 1) & 1u);

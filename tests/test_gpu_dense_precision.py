@@ -199,3 +199,60 @@ def test_fp32_sums_of_any_length_are_fp32_sums(cuda_lib, M, N, K):
     cuda_lib.dlrm_linear_bwd(dy, x, w, None, dx, dw, db, workspace=torch.empty(n, dtype=torch.uint8, device=dev()))
     assert _rms_share(dx, dy.double() @ w.double()) <= 8e-7
     assert _rms_share(dw, dy.double().t() @ x.double()) <= 8e-7
+
+
+@pytest.mark.parametrize("M,N,K", [(16384, 512, 1024), (9000, 515, 771)])
+def test_long_fp32_sums_repeat_and_give_up(cuda_lib, M, N, K):
+    """Sums in segments have the same bits in every call, and a wait that gives up among them ends the call
+    with DLRM_STATUS_TIMEOUT, the next one being right."""
+    g = torch.Generator().manual_seed(N)
+    x, w, r, b = _rand(g, M, K), _rand(g, N, K, std=K**-0.5), _rand(g, M, N), _rand(g, N)
+    n = cuda_lib.dlrm_linear_fwd_workspace_size(x, w)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev())
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+    outs = [torch.empty(M, N, device=dev()) for _ in range(4)]
+    for y in outs[:3]:
+        cuda_lib.dlrm_linear_fwd(x, w, b, r, y, act=2, workspace=ws, status=status)
+    assert int(status.item()) == 0 and torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    try:
+        cuda_lib.dlrm_set_wait_limit(0)
+        cuda_lib.dlrm_linear_fwd(x, w, b, r, outs[3], act=2, workspace=ws, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == cuda_lib.DLRM_STATUS_TIMEOUT
+    finally:
+        cuda_lib.dlrm_set_wait_limit(-1)
+    status.zero_()
+    cuda_lib.dlrm_linear_fwd(x, w, b, r, outs[3], act=2, workspace=ws, status=status)
+    assert int(status.item()) == 0 and torch.equal(outs[0], outs[3])
+
+
+@pytest.mark.parametrize("limit", [0, 300, 3000, 30000])
+@pytest.mark.parametrize("M,N,K,dtype", [(8192, 1024, 480, "f16"), (300, 200, 264, "bf16"), (9000, 515, 771, "f32"),
+                                         (16384, 512, 1024, "f32"), (2048, 512, 512, "bf16")])
+def test_a_layer_given_up_anywhere_leaves_the_next_one_right(cuda_lib, M, N, K, dtype, limit):
+    """Waits that give up at the start, or after some cycles in the middle of a tile: the call ends, says so if
+    it did, and the forward and the gradient after it have their bits."""
+    g = torch.Generator().manual_seed(limit)
+    x, w, dy = _rand(g, M, K, dtype=dtype), _rand(g, N, K, std=K**-0.5, dtype=dtype), _rand(g, M, N, dtype=dtype)
+    wf = torch.empty(max(1, cuda_lib.dlrm_linear_fwd_workspace_size(x, w)), dtype=torch.uint8, device=dev())
+    wb = torch.empty(max(1, cuda_lib.dlrm_linear_bwd_workspace_size(dy, x, w, act=2)), dtype=torch.uint8, device=dev())
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+
+    def run():
+        y, dx, dw, db = torch.empty_like(dy), torch.empty_like(x), torch.empty_like(w), torch.empty(N, device=dev())
+        cuda_lib.dlrm_linear_fwd(x, w, None, None, y, act=2, workspace=wf, status=status)
+        cuda_lib.dlrm_linear_bwd(dy, x, w, dy, dx, dw, db, act=2, workspace=wb, status=status)
+        torch.cuda.synchronize()
+        return y, dx, dw, db
+
+    want = run()
+    assert int(status.item()) == 0
+    for _ in range(4):
+        try:
+            cuda_lib.dlrm_set_wait_limit(limit)
+            run()
+        finally:
+            cuda_lib.dlrm_set_wait_limit(-1)
+        assert int(status.item()) in ((cuda_lib.DLRM_STATUS_TIMEOUT,) if limit == 0 else (0, cuda_lib.DLRM_STATUS_TIMEOUT))
+        status.zero_()
+        assert all(torch.equal(a, b) for a, b in zip(run(), want)) and int(status.item()) == 0
