@@ -169,3 +169,29 @@ def test_moe_infinite_and_nan_activations(cuda_lib, dtype):
     assert bool(torch.isnan(y[1]).all()) and bool(torch.isnan(y[4]).all())
     for t in (0, 2, 3, 5):
         assert torch.equal(got[0][t], clean[0][t])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("limit", [0, 300, 3000, 30000])
+def test_a_mixture_given_up_anywhere_leaves_the_next_one_right(cuda_lib, dtype, limit):
+    T, H, I, E, k = 12, 2048, 512, 16, 4
+    x, wr, w1, w2 = _case(T, H, I, E, dtype, True)
+    status = torch.zeros(1, dtype=torch.int32, device=dev())
+
+    def run():
+        y, ids, probs, ws = _buffers(cuda_lib, x, wr, w1, w2, k)
+        cuda_lib.dlrm_moe_fwd(x, wr, w1, w2, None, y, ids, probs, workspace=ws, status=status)
+        torch.cuda.synchronize()
+        return y, ids, probs
+
+    want = run()
+    assert int(status.item()) == 0
+    for _ in range(4):
+        try:
+            cuda_lib.dlrm_set_wait_limit(limit)
+            run()
+        finally:
+            cuda_lib.dlrm_set_wait_limit(-1)
+        assert int(status.item()) in (0, cuda_lib.DLRM_STATUS_TIMEOUT)
+        status.zero_()
+        assert all(torch.equal(a, b) for a, b in zip(run(), want)) and int(status.item()) == 0
