@@ -15,7 +15,7 @@
 
 #include "dlrm_dense.h"
 
-static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_nbytes, *s_get_device;
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_nbytes, *s_get_device, *s_is_contiguous;
 /* torch's dtypes: fp32, fp16, bf16 (their codes are the indices), int32, int64 */
 enum { F32, F16, BF16, I32, I64, N_TYPES };
 static PyObject* types[N_TYPES];
@@ -137,6 +137,15 @@ static int workspace(PyObject* t, void** p, size_t* bytes)
     *p = NULL;
     *bytes = 0;
     if (t == Py_None) return 1;
+    PyObject* c = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+    if (!c) return 0;
+    const int contiguous = PyObject_IsTrue(c);
+    Py_DECREF(c);
+    if (contiguous < 0) return 0;
+    if (!contiguous) {   /* an expanded tensor has fewer bytes than it says */
+        PyErr_SetString(PyExc_ValueError, "workspace must be contiguous");
+        return 0;
+    }
     PyObject* n = PyObject_GetAttr(t, s_nbytes);
     if (!n) return 0;
     *bytes = PyLong_AsSize_t(n);
@@ -382,6 +391,7 @@ PyMODINIT_FUNC PyInit__marshal(void)
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_nbytes = PyUnicode_InternFromString("nbytes");
     s_get_device = PyUnicode_InternFromString("get_device");
-    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_nbytes || !s_get_device) return NULL;
+    s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
+    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_nbytes || !s_get_device || !s_is_contiguous) return NULL;
     return PyModule_Create(&module);
 }

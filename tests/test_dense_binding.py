@@ -104,3 +104,11 @@ def test_activations_past_32_bits_are_refused(act):
     x, w, y = (Elsewhere(torch.zeros(4, 16), 0), Elsewhere(torch.zeros(8, 16), 0), Elsewhere(torch.zeros(4, 8), 0))
     with pytest.raises(ValueError, match="^act is"):
         _on_device_0(dl.dlrm_linear_fwd, dict(x=x, w=w, bias=None, residual=None, y=y, act=act))
+
+
+@pytest.mark.parametrize("ws", [torch.zeros(1, dtype=torch.uint8).expand(1 << 30), torch.zeros(64, dtype=torch.uint8)[::2]])
+def test_workspaces_that_are_not_contiguous_are_refused(ws):
+    """An expanded byte says it has a gigabyte."""
+    x, w, y = (Elsewhere(torch.zeros(4, 16), 0), Elsewhere(torch.zeros(8, 16), 0), Elsewhere(torch.zeros(4, 8), 0))
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        _on_device_0(dl.dlrm_linear_fwd, dict(x=x, w=w, bias=None, residual=None, y=y, workspace=Elsewhere(ws, 0)))
