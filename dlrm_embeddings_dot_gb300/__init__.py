@@ -13,7 +13,9 @@ from __future__ import annotations
 import ctypes
 import os
 
-from . import dense_abi
+from . import block_abi, dense_abi
+from .block_abi import (DLRM_BLOCK_MAX_WIDTH, DLRM_GATE_NONE, DLRM_GATE_SIGMOID, DLRM_GATE_SILU, DLRM_NORM_LAYER,  # noqa: F401
+                        DLRM_NORM_RMS, DLRM_ROUTE_MAX_EXPERTS, DLRM_ROUTE_MAX_TOP_K)
 from .dense_abi import (DLRM_ACT_GELU, DLRM_ACT_NONE, DLRM_ACT_RELU, DLRM_ACT_SILU, DLRM_MOE_MAX_EXPERTS,  # noqa: F401
                         DLRM_MOE_MAX_TOKENS, DLRM_MOE_MAX_TOP_K)
 
@@ -98,6 +100,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         getattr(L, f).restype = _I
     if hasattr(L, "dlrm_linear_fwd"):   # a library built before the dense network has none of it
         dense_abi.declare(L)
+    if hasattr(L, "dlrm_block_norm_fwd"):
+        block_abi.declare(L)
     if path is None:
         _lib = L
     return L
@@ -301,11 +305,15 @@ _DENSE = frozenset((
     "dlrm_linear_bwd_workspace_size", "dlrm_moe_fwd", "dlrm_moe_fwd_workspace_size"))
 
 
+_BLOCK = frozenset(block_abi.ENTRY_POINTS + block_abi.SIZES)
+
+
 def __getattr__(name):
-    """The names of ``dense.py``, imported (with torch) when the first of them is used."""
-    if name in _DENSE:
-        from . import dense
-        for n in _DENSE:
-            globals()[n] = getattr(dense, n)
+    """The names of ``dense.py`` and ``block.py``, imported (with torch) when the first of them is used."""
+    if name in _DENSE or name in _BLOCK:
+        from . import block, dense
+        for names, module in ((_DENSE, dense), (_BLOCK, block)):
+            for n in names:
+                globals()[n] = getattr(module, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

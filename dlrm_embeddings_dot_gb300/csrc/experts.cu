@@ -1,0 +1,686 @@
+// experts.cu -- a mixture of experts in training: the choice of experts and its
+// gradient, the order of the choices by expert, and the rows' way to their
+// experts and back.  Each is bound by memory, or by latency where there are few tokens.
+#include "dense_ops.cuh"
+#include "dlrm_block.h"
+
+namespace dlrm {
+namespace {
+
+// ------------------------------------------------------------ choice of experts
+// A float as an unsigned number in the same order, a NaN above all, -0 as 0.
+__device__ __forceinline__ uint32_t ordered(float v)
+{
+    const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
+    return v != v ? 0xffffffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+constexpr uint32_t kClosed = 0x007fffffu;   // ordered(-infinity); 0 stands for no logit
+
+// A warp takes a token, a lane the logits lane, lane + 32, ..: k rounds of the largest of the
+// lanes' largest and the least index that has it.
+template <typename T>
+__global__ void __launch_bounds__(256)
+route_fwd_kernel(const T* __restrict__ logits, int64_t ldl, int tokens, int E, int k, int32_t* __restrict__ ids,
+                 float* __restrict__ probs)
+{
+    pdl_wait();
+    constexpr int kMine = DLRM_ROUTE_MAX_EXPERTS / kWarp;
+    const int lane = threadIdx.x % kWarp;
+    for (int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / kWarp; t < tokens; t += (int64_t)gridDim.x * 8) {
+        const T* row = logits + t * ldl;
+        uint32_t key[kMine];
+        T raw[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i)
+            if (lane + 32 * i < E) raw[i] = __ldg(row + lane + 32 * i);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) key[i] = lane + 32 * i < E ? ordered(to_f32(raw[i])) : 0;
+        int id = -1;         // lane j: the j-th choice
+        float logit = 0.f;
+        for (int j = 0; j < k; ++j) {
+            uint32_t best = 0;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) best = max(best, key[i]);
+            best = __reduce_max_sync(~0u, best);
+            if (best <= kClosed) break;
+            uint32_t at = ~0u;
+#pragma unroll
+            for (int i = kMine - 1; i >= 0; --i)
+                if (key[i] == best) at = lane + 32 * i;
+            at = __reduce_min_sync(~0u, at);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                if (at == lane + 32 * i) key[i] = 0;
+            if (lane == j) {
+                id = (int)at;
+                logit = best == ~0u ? __uint_as_float(0x7fc00000u)
+                                    : __uint_as_float(best & 0x80000000u ? best ^ 0x80000000u : ~best);
+            }
+        }
+        const float top = __shfl_sync(~0u, logit, 0);
+        const float e = id >= 0 ? expf(logit - top) : 0.f;
+        float sum = 0.f;
+        for (int j = 0; j < k; ++j) sum += __shfl_sync(~0u, e, j);
+        if (lane < k) {
+            ids[t * k + lane] = id;
+            probs[t * k + lane] = id >= 0 ? e / sum : 0.f;
+        }
+    }
+}
+
+// A warp takes a token's row of grad_logits; lane j < k has choice j.
+template <typename T>
+__global__ void __launch_bounds__(256)
+route_bwd_kernel(const float* __restrict__ grad_probs, const int32_t* __restrict__ ids, const float* __restrict__ probs,
+                 int tokens, int E, int k, T* __restrict__ grad, int64_t ldgl)
+{
+    pdl_wait();
+    const int lane = threadIdx.x % kWarp;
+    for (int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / kWarp; t < tokens; t += (int64_t)gridDim.x * 8) {
+        int id = -1;
+        float p = 0.f, g = 0.f;
+        if (lane < k) {
+            id = __ldg(ids + t * k + lane);
+            p = __ldg(probs + t * k + lane);
+            g = __ldg(grad_probs + t * k + lane);
+        }
+        if (id < 0 || id >= E) {
+            id = -1;
+            p = g = 0.f;
+        }
+        float dot = 0.f;
+        for (int j = 0; j < k; ++j) dot = fmaf(__shfl_sync(~0u, g, j), __shfl_sync(~0u, p, j), dot);
+        const float d = p * (g - dot);
+        T* row = grad + t * ldgl;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            float v = 0.f;
+            for (int j = 0; j < k; ++j) {
+                const int at = __shfl_sync(~0u, id, j);
+                const float dj = __shfl_sync(~0u, d, j);
+                if (at == e0 + lane) v = dj;
+            }
+            if (e0 + lane < E) row[e0 + lane] = from_f32<T>(v);
+        }
+    }
+}
+
+// ------------------------------------------------------------- order by expert
+// A counting sort that keeps the order of equal experts.  A block takes a chunk of the choices,
+// its warps contiguous parts of it; a warp counts and places 32 choices at a time, those of
+// one expert found by match.any, in counters of its own in shared memory.  Choices without
+// expert count as expert E.  With one block that is all; with more, expert_count_kernel writes
+// the chunks' counts first, and a block adds up those of the blocks before it (and all of
+// them: where an expert begins).
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / kWarp;
+constexpr int kSortChunk = 4096;        // choices of a block, while there are no more than kSortBlocks blocks
+constexpr int kSortBlocks = 256;
+constexpr int kBins = DLRM_ROUTE_MAX_EXPERTS + 1;
+
+struct SortShape {
+    int blocks;
+    int64_t chunk;
+};
+
+inline SortShape sort_shape(int64_t n)
+{
+    int64_t chunk = kSortChunk;
+    if ((n + chunk - 1) / chunk > kSortBlocks)
+        chunk = ((n + kSortBlocks - 1) / kSortBlocks + kSortThreads - 1) / kSortThreads * kSortThreads;
+    return {n > 0 ? (int)((n + chunk - 1) / chunk) : 1, chunk};
+}
+
+// Choices [from, to) of a warp's part: each(choice, bin, rank among the 32 of its bin, how many of them)
+template <typename Each>
+__device__ __forceinline__ void walk(const int32_t* ids, int64_t from, int64_t to, int E, Each each)
+{
+    const int lane = threadIdx.x % kWarp;
+    for (int64_t c0 = from; c0 < to; c0 += kWarp) {
+        const int64_t c = c0 + lane;
+        int bin = kBins;       // past the part's end: a bin of its own, not counted
+        if (c < to) {
+            const int id = __ldg(ids + c);
+            bin = id >= 0 && id < E ? id : E;
+        }
+        const uint32_t same = __match_any_sync(~0u, bin);
+        each(c, bin, __popc(same & ((1u << lane) - 1)), __popc(same));
+        __syncwarp();
+    }
+}
+
+// Counts the warps' parts of the block's chunk into warps[warp][bin].
+__device__ __forceinline__ void count_parts(const int32_t* ids, int64_t n, int64_t chunk, int E, int (*warps)[kBins],
+                                            int64_t& from, int64_t& to)
+{
+    const int warp = threadIdx.x / kWarp;
+    for (int i = threadIdx.x; i < kSortWarps * kBins; i += kSortThreads) warps[i / kBins][i % kBins] = 0;
+    __syncthreads();
+    const int64_t part = chunk / kSortWarps, first = blockIdx.x * chunk;
+    from = min(n, first + warp * part);
+    to = min(n, from + part);
+    int* mine = warps[warp];
+    walk(ids, from, to, E, [&](int64_t, int bin, int rank, int many) {
+        if (rank == 0 && bin < kBins) mine[bin] += many;
+    });
+    __syncthreads();
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+expert_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int E, int32_t* __restrict__ counts)
+{
+    pdl_wait();
+    __shared__ int warps[kSortWarps][kBins];
+    int64_t from, to;
+    count_parts(ids, n, chunk, E, warps, from, to);
+    for (int e = threadIdx.x; e <= E; e += kSortThreads) {
+        int s = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) s += warps[w][e];
+        counts[blockIdx.x * kBins + e] = s;
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads)
+expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int E, const int32_t* __restrict__ counts,
+                    int32_t* __restrict__ offsets, int32_t* __restrict__ slots, int32_t* __restrict__ order,
+                    uint32_t* __restrict__ status)
+{
+    pdl_wait();
+    __shared__ int warps[kSortWarps][kBins];
+    __shared__ int total[kBins], before[kBins], scan[kSortWarps];
+    int64_t from, to;
+    count_parts(ids, n, chunk, E, warps, from, to);
+    for (int e = threadIdx.x; e <= E; e += kSortThreads) {
+        int all = 0, ahead = 0;
+        if (gridDim.x == 1) {
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) all += warps[w][e];
+        } else {
+#pragma unroll 16
+            for (int b = 0; b < (int)gridDim.x; ++b) {
+                const int v = __ldg(counts + b * kBins + e);
+                all += v;
+                ahead += b < (int)blockIdx.x ? v : 0;
+            }
+        }
+        total[e] = all;
+        before[e] = ahead;
+    }
+    __syncthreads();
+    // where each expert's places begin: an exclusive scan of total over the bins (kBins <= kSortThreads)
+    {
+        const int e = threadIdx.x, lane = e % kWarp, v = e <= E ? total[e] : 0;
+        int s = v;
+#pragma unroll
+        for (int m = 1; m < kWarp; m *= 2) {
+            const int o = __shfl_up_sync(~0u, s, m);
+            if (lane >= m) s += o;
+        }
+        if (lane == kWarp - 1) scan[e / kWarp] = s;
+        __syncthreads();
+        for (int w = 0; w < e / kWarp; ++w) s += scan[w];
+        if (e <= E) {
+            int at = s - v;
+            if (blockIdx.x == 0) offsets[e] = at;   // offsets[E]: how many have a place
+            at += before[e];
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) {
+                const int many = warps[w][e];
+                warps[w][e] = at;
+                at += many;
+            }
+        }
+    }
+    __syncthreads();
+    int* mine = warps[threadIdx.x / kWarp];
+    bool bad = false;
+    walk(ids, from, to, E, [&](int64_t c, int bin, int rank, int many) {
+        const int at = bin < kBins ? mine[bin] + rank : 0;
+        __syncwarp();
+        if (rank == 0 && bin < kBins) mine[bin] += many;
+        if (c < to) {
+            slots[c] = bin < E ? at : -1;
+            if (order) order[at] = bin < E ? (int32_t)c : -1;
+            if (bin == E && __ldg(ids + c) >= E) bad = true;
+        }
+    });
+    if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
+}
+static_assert(kBins <= kSortThreads, "a thread for each bin");
+
+// -------------------------------------------------- rows to their experts and back
+// Walks the runs of eight columns of `rows` rows, a run a thread at a time, stepping row and run
+// without a division.
+struct Runs {
+    int64_t i, end, stride, row, g, groups, drow, dg;
+    __device__ Runs(int64_t rows, int H)
+    {
+        groups = (H - 1) / 8 + 1;
+        end = groups * rows;
+        stride = (int64_t)gridDim.x * blockDim.x;
+        i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+        row = i / groups;
+        g = i - row * groups;
+        drow = stride / groups;
+        dg = stride - drow * groups;
+    }
+    __device__ bool more() const { return i < end; }
+    __device__ void next()
+    {
+        i += stride;
+        row += drow;
+        g += dg;
+        if (g >= groups) {
+            g -= groups;
+            ++row;
+        }
+    }
+};
+
+constexpr int kMaxK = DLRM_ROUTE_MAX_TOP_K;
+
+// The slots of a token; those without a row as -1.
+__device__ __forceinline__ void load_slots(const int32_t* slots, int64_t t, int k, int R, int (&s)[kMaxK], bool& bad)
+{
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) s[j] = j < k ? __ldg(slots + t * k + j) : -1;
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j)
+        if (s[j] >= R) {
+            bad = true;
+            s[j] = -1;
+        }
+}
+
+// xs[slots[t][j]] = x[t]: a row is read once and written k times.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slots, int tokens, int k, int H, int R,
+                T* __restrict__ xs, int64_t ldxs, uint32_t* __restrict__ status)
+{
+    pdl_wait();
+    bool bad = false;
+    for (Runs r(tokens, H); r.more(); r.next()) {
+        const int col = (int)r.g * 8, n = H - col;
+        int s[kMaxK];
+        const Raw8<T> v = load8<T, VEC>(x + r.row * ldx + col, n);
+        load_slots(slots, r.row, k, R, s, bad);
+        float f[8];
+        widen8<T>(v, f);
+#pragma unroll
+        for (int j = 0; j < kMaxK; ++j)
+            if (s[j] >= 0) store8<T, VEC>(xs + s[j] * ldxs + col, n, f);
+    }
+    if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
+}
+
+// y[t] = residual[t] + sum over j of probs[t][j] ys[slots[t][j]]; probs NULL: the plain sum.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256)
+combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict__ slots, const float* __restrict__ probs,
+               const T* __restrict__ res, int64_t ldres, int tokens, int k, int H, int R, T* __restrict__ y, int64_t ldy,
+               uint32_t* __restrict__ status)
+{
+    pdl_wait();
+    bool bad = false;
+    for (Runs r(tokens, H); r.more(); r.next()) {
+        const int col = (int)r.g * 8, n = H - col;
+        int s[kMaxK];
+        load_slots(slots, r.row, k, R, s, bad);
+        Raw8<T> v[kMaxK], vr;
+        float p[kMaxK];
+#pragma unroll
+        for (int j = 0; j < kMaxK; ++j)
+            if (s[j] >= 0) {
+                v[j] = load8<T, VEC>(ys + s[j] * ldys + col, n);
+                p[j] = probs ? __ldg(probs + r.row * k + j) : 1.f;
+            }
+        if (res) vr = load8<T, VEC>(res + r.row * ldres + col, n);
+        float f[8] = {};
+#pragma unroll
+        for (int j = 0; j < kMaxK; ++j)
+            if (s[j] >= 0) {
+                float w[8];
+                widen8<T>(v[j], w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = fmaf(p[j], w[i], f[i]);
+            }
+        if (res) {
+            float w[8];
+            widen8<T>(vr, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] += w[i];
+        }
+        store8<T, VEC>(y + r.row * ldy + col, n, f);
+    }
+    if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
+}
+
+struct CombineBwd {
+    const void *gy, *ys;
+    int64_t ldgy, ldys;
+    const int32_t* slots;
+    const float* probs;
+    int tokens, k, H, R;
+    void* gys;          // may be NULL
+    int64_t ldgys;
+    float* gp;          // may be NULL
+    uint32_t* status;
+};
+
+// W warps take a token: grad_y once, and for each choice its row of ys in and of grad_ys out.
+template <typename T, bool VEC, int W>
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant__ CombineBwd a)
+{
+    constexpr int G = 8 / W;
+    __shared__ float red[W > 1 ? 8 * kMaxK : 1];
+    pdl_wait();
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    bool bad = false;
+    for (int64_t t = (int64_t)blockIdx.x * G + warp / W; t < a.tokens; t += (int64_t)gridDim.x * G) {
+        int s[kMaxK];
+        load_slots(a.slots, t, a.k, a.R, s, bad);
+        float p[kMaxK], dot[kMaxK];
+#pragma unroll
+        for (int j = 0; j < kMaxK; ++j) {
+            p[j] = s[j] >= 0 && a.gys ? __ldg(a.probs + t * a.k + j) : 0.f;
+            dot[j] = 0.f;
+        }
+        for (int col = (warp % W * 32 + lane) * 8; col < a.H; col += W * 256) {
+            const int n = a.H - col;
+            const Raw8<T> vg = load8<T, VEC>((const T*)a.gy + t * a.ldgy + col, n);
+            Raw8<T> v[kMaxK];
+            if (a.gp)
+#pragma unroll
+                for (int j = 0; j < kMaxK; ++j)
+                    if (s[j] >= 0) v[j] = load8<T, VEC>((const T*)a.ys + s[j] * a.ldys + col, n);
+            float g[8];
+            widen8<T>(vg, g);
+#pragma unroll
+            for (int j = 0; j < kMaxK; ++j)
+                if (s[j] >= 0) {
+                    if (a.gp) {
+                        float w[8];
+                        widen8<T>(v[j], w);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], w[i], dot[j]);
+                    }
+                    if (a.gys) {
+                        float o[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = p[j] * g[i];
+                        store8<T, VEC>((T*)a.gys + s[j] * a.ldgys + col, n, o);
+                    }
+                }
+        }
+        if (!a.gp) continue;
+#pragma unroll
+        for (int j = 0; j < kMaxK; ++j)
+            if (j < a.k)
+#pragma unroll
+                for (int m = 16; m; m /= 2) dot[j] += __shfl_xor_sync(~0u, dot[j], m);
+        if constexpr (W > 1) {   // W == 8: the block has one token
+            static_assert(W == 8, "the block's barrier");
+            __syncthreads();
+            if (lane == 0)
+#pragma unroll
+                for (int j = 0; j < kMaxK; ++j) red[warp * kMaxK + j] = dot[j];
+            __syncthreads();
+            if (threadIdx.x < (unsigned)a.k) {
+                float sum = red[threadIdx.x];
+#pragma unroll
+                for (int w = 1; w < W; ++w) sum += red[w * kMaxK + threadIdx.x];
+                a.gp[t * a.k + threadIdx.x] = sum;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kMaxK; ++j)
+                if (lane == j && j < a.k) a.gp[t * a.k + j] = dot[j];
+        }
+    }
+    if (bad) set_status(a.status, DLRM_STATUS_OOB_INDEX);
+}
+
+// ------------------------------------------------------------------- checks
+dlrm_status check_route(const char* fn, dlrm_dtype dtype, int T, int E, int k)
+{
+    if (!dense_dtype_ok(dtype)) return fail(DLRM_ERR_INVALID_ARG, "%s: bad dtype", fn);
+    if (T < 0 || E < 1 || k < 1) return fail(DLRM_ERR_INVALID_ARG, "%s: need T >= 0, E >= 1 and k >= 1", fn);
+    if (k > E) return fail(DLRM_ERR_INVALID_ARG, "%s: k is more than E", fn);
+    if (E > DLRM_ROUTE_MAX_EXPERTS || k > DLRM_ROUTE_MAX_TOP_K || T > kMaxSize)
+        return fail(DLRM_ERR_UNSUPPORTED, "%s: up to %d tokens, %d experts and %d of them a token", fn, kMaxSize,
+                    DLRM_ROUTE_MAX_EXPERTS, DLRM_ROUTE_MAX_TOP_K);
+    return DLRM_OK;
+}
+
+// An array of 4-byte elements that has to be there.
+dlrm_status check_words(const char* fn, const char* name, const void* p)
+{
+    if (!p) return fail(DLRM_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+    if (reinterpret_cast<uintptr_t>(p) & 3u)
+        return fail(DLRM_ERR_INVALID_ARG, "%s: %s is not aligned to its element size", fn, name);
+    return DLRM_OK;
+}
+
+dlrm_status check_rows(const char* fn, dlrm_dtype dtype, int T, int k, int H, int R)
+{
+    if (!dense_dtype_ok(dtype)) return fail(DLRM_ERR_INVALID_ARG, "%s: bad dtype", fn);
+    if (T < 0 || k < 1 || H < 1 || R < 0)
+        return fail(DLRM_ERR_INVALID_ARG, "%s: need T >= 0, k >= 1, H >= 1 and R >= 0", fn);
+    if (k > DLRM_ROUTE_MAX_TOP_K || T > kMaxSize || H > kMaxSize || R > kMaxSize)
+        return fail(DLRM_ERR_UNSUPPORTED, "%s: sizes up to %d and %d places a token", fn, kMaxSize, DLRM_ROUTE_MAX_TOP_K);
+    return DLRM_OK;
+}
+
+inline unsigned run_blocks(int64_t rows, int H)
+{
+    const int64_t want = (((int64_t)H + 7) / 8 * rows + 255) / 256, most = (int64_t)num_sms() * 8;
+    return (unsigned)(want < most ? want : most);
+}
+
+inline unsigned warp_blocks(int64_t tokens)
+{
+    const int64_t want = (tokens + 7) / 8, most = (int64_t)num_sms() * 8;
+    return (unsigned)(want < most ? want : most);
+}
+
+dlrm_status run_combine(const char* fn, const void* ys, int64_t ldys, const int32_t* slots, const float* probs,
+                        const void* res, int64_t ldres, dlrm_dtype dtype, int T, int k, int H, int R, void* y, int64_t ldy,
+                        uint32_t* status, void* stream)
+{
+    const int es = dense_dtype_size(dtype);
+    const bool vec = H % 8 == 0 && rows_aligned16(ys, ldys, R, es) && (!res || rows_aligned16(res, ldres, T, es)) &&
+                     rows_aligned16(y, ldy, T, es);
+    return with_type(dtype, [&](auto t) {
+        using E = decltype(t);
+        auto kern = vec ? combine_kernel<E, true> : combine_kernel<E, false>;
+        return check_launch_pdl(launch_pdl(kern, dim3(run_blocks(T, H)), dim3(256), 0, as_stream(stream), (const E*)ys, ldys,
+                                           slots, probs, (const E*)res, ldres, T, k, H, R, (E*)y, ldy, status),
+                                fn);
+    });
+}
+
+}  // namespace
+}  // namespace dlrm
+
+using namespace dlrm;
+
+extern "C" dlrm_status dlrm_route_fwd(const void* d_logits, int64_t ldl, dlrm_dtype dtype, int T, int E, int k,
+                                      int32_t* d_ids, float* d_probs, void* stream)
+{
+    DLRM_API_RANGE("dlrm_route_fwd");
+    clear_error();
+    const char* fn = "dlrm_route_fwd";
+    dlrm_status s = check_route(fn, dtype, T, E, k);
+    if (s != DLRM_OK || T == 0) return s;
+    if ((s = check_matrix(fn, "d_logits", d_logits, ldl, T, E, dense_dtype_size(dtype))) != DLRM_OK) return s;
+    if ((s = check_words(fn, "d_ids", d_ids)) != DLRM_OK) return s;
+    if ((s = check_words(fn, "d_probs", d_probs)) != DLRM_OK) return s;
+    return with_type(dtype, [&](auto t) {
+        using X = decltype(t);
+        return check_launch_pdl(launch_pdl(route_fwd_kernel<X>, dim3(warp_blocks(T)), dim3(256), 0, as_stream(stream),
+                                           (const X*)d_logits, ldl, T, E, k, d_ids, d_probs),
+                                "route_fwd_kernel");
+    });
+}
+
+extern "C" dlrm_status dlrm_route_bwd(const float* d_grad_probs, const int32_t* d_ids, const float* d_probs,
+                                      dlrm_dtype dtype, int T, int E, int k, void* d_grad_logits, int64_t ldgl,
+                                      void* stream)
+{
+    DLRM_API_RANGE("dlrm_route_bwd");
+    clear_error();
+    const char* fn = "dlrm_route_bwd";
+    dlrm_status s = check_route(fn, dtype, T, E, k);
+    if (s != DLRM_OK || T == 0) return s;
+    if ((s = check_words(fn, "d_grad_probs", d_grad_probs)) != DLRM_OK) return s;
+    if ((s = check_words(fn, "d_ids", d_ids)) != DLRM_OK) return s;
+    if ((s = check_words(fn, "d_probs", d_probs)) != DLRM_OK) return s;
+    if ((s = check_matrix(fn, "d_grad_logits", d_grad_logits, ldgl, T, E, dense_dtype_size(dtype))) != DLRM_OK) return s;
+    return with_type(dtype, [&](auto t) {
+        using X = decltype(t);
+        return check_launch_pdl(launch_pdl(route_bwd_kernel<X>, dim3(warp_blocks(T)), dim3(256), 0, as_stream(stream),
+                                           d_grad_probs, d_ids, d_probs, T, E, k, (X*)d_grad_logits, ldgl),
+                                "route_bwd_kernel");
+    });
+}
+
+static bool sort_sizes_ok(int T, int k, int E)
+{
+    return T >= 0 && k >= 1 && k <= DLRM_ROUTE_MAX_TOP_K && E >= 1 && E <= DLRM_ROUTE_MAX_EXPERTS &&
+           (int64_t)T * k <= kMaxSize;
+}
+
+extern "C" size_t dlrm_expert_sort_workspace_size(int T, int k, int E)
+{
+    if (!sort_sizes_ok(T, k, E)) return 0;
+    const SortShape z = sort_shape((int64_t)T * k);
+    return z.blocks > 1 ? dlrm_ws_align((size_t)z.blocks * kBins * 4) : 0;
+}
+
+extern "C" dlrm_status dlrm_expert_sort(const int32_t* d_ids, int T, int k, int E, int32_t* d_offsets, int32_t* d_slots,
+                                        int32_t* d_order, void* d_workspace, size_t workspace_bytes, uint32_t* d_status,
+                                        void* stream)
+{
+    DLRM_API_RANGE("dlrm_expert_sort");
+    clear_error();
+    const char* fn = "dlrm_expert_sort";
+    if (T < 0 || k < 1 || E < 1) return fail(DLRM_ERR_INVALID_ARG, "%s: need T >= 0, k >= 1 and E >= 1", fn);
+    if (!sort_sizes_ok(T, k, E))
+        return fail(DLRM_ERR_UNSUPPORTED, "%s: up to %d choices, %d experts and %d of them a token", fn, kMaxSize,
+                    DLRM_ROUTE_MAX_EXPERTS, DLRM_ROUTE_MAX_TOP_K);
+    dlrm_status s = check_words(fn, "d_offsets", d_offsets);
+    if (s != DLRM_OK) return s;
+    if (T > 0 && (s = check_words(fn, "d_ids", d_ids)) != DLRM_OK) return s;
+    if (T > 0 && (s = check_words(fn, "d_slots", d_slots)) != DLRM_OK) return s;
+    if (d_order && (s = check_words(fn, "d_order", d_order)) != DLRM_OK) return s;
+    const size_t need = dlrm_expert_sort_workspace_size(T, k, E);
+    if (need && (!d_workspace || workspace_bytes < need))
+        return fail(DLRM_ERR_WORKSPACE, "%s: workspace %zu bytes < %zu", fn, d_workspace ? workspace_bytes : 0, need);
+    if (need && (reinterpret_cast<uintptr_t>(d_workspace) & 255u))
+        return fail(DLRM_ERR_INVALID_ARG, "%s: the workspace must be 256-byte aligned", fn);
+    const int64_t n = (int64_t)T * k;
+    const SortShape z = sort_shape(n);
+    const cudaStream_t st = as_stream(stream);
+    int32_t* counts = (int32_t*)d_workspace;
+    if (z.blocks > 1) {
+        s = check_launch_pdl(launch_pdl(expert_count_kernel, dim3(z.blocks), dim3(kSortThreads), 0, st, d_ids, n, z.chunk, E,
+                                        counts),
+                             "expert_count_kernel");
+        if (s != DLRM_OK) return s;
+    }
+    return check_launch_pdl(launch_pdl(expert_place_kernel, dim3(z.blocks), dim3(kSortThreads), 0, st, d_ids, n, z.chunk, E,
+                                       (const int32_t*)counts, d_offsets, d_slots, d_order, d_status),
+                            "expert_place_kernel");
+}
+
+extern "C" dlrm_status dlrm_dispatch_fwd(const void* d_x, int64_t ldx, const int32_t* d_slots, dlrm_dtype dtype, int T,
+                                         int k, int H, int R, void* d_xs, int64_t ldxs, uint32_t* d_status, void* stream)
+{
+    DLRM_API_RANGE("dlrm_dispatch_fwd");
+    clear_error();
+    const char* fn = "dlrm_dispatch_fwd";
+    dlrm_status s = check_rows(fn, dtype, T, k, H, R);
+    if (s != DLRM_OK || T == 0) return s;
+    const int es = dense_dtype_size(dtype);
+    if ((s = check_matrix(fn, "d_x", d_x, ldx, T, H, es)) != DLRM_OK) return s;
+    if ((s = check_words(fn, "d_slots", d_slots)) != DLRM_OK) return s;
+    if (R > 0 && (s = check_matrix(fn, "d_xs", d_xs, ldxs, R, H, es)) != DLRM_OK) return s;
+    const bool vec = H % 8 == 0 && rows_aligned16(d_x, ldx, T, es) && rows_aligned16(d_xs, ldxs, R, es);
+    return with_type(dtype, [&](auto t) {
+        using X = decltype(t);
+        auto kern = vec ? dispatch_kernel<X, true> : dispatch_kernel<X, false>;
+        return check_launch_pdl(launch_pdl(kern, dim3(run_blocks(T, H)), dim3(256), 0, as_stream(stream), (const X*)d_x, ldx,
+                                           d_slots, T, k, H, R, (X*)d_xs, ldxs, d_status),
+                                "dispatch_kernel");
+    });
+}
+
+extern "C" dlrm_status dlrm_dispatch_bwd(const void* d_grad_xs, int64_t ldgxs, const int32_t* d_slots, dlrm_dtype dtype,
+                                         int T, int k, int H, int R, void* d_grad_x, int64_t ldgx, uint32_t* d_status,
+                                         void* stream)
+{
+    DLRM_API_RANGE("dlrm_dispatch_bwd");
+    clear_error();
+    const char* fn = "dlrm_dispatch_bwd";
+    dlrm_status s = check_rows(fn, dtype, T, k, H, R);
+    if (s != DLRM_OK || T == 0) return s;
+    const int es = dense_dtype_size(dtype);
+    if (R > 0 && (s = check_matrix(fn, "d_grad_xs", d_grad_xs, ldgxs, R, H, es)) != DLRM_OK) return s;
+    if ((s = check_words(fn, "d_slots", d_slots)) != DLRM_OK) return s;
+    if ((s = check_matrix(fn, "d_grad_x", d_grad_x, ldgx, T, H, es)) != DLRM_OK) return s;
+    return run_combine("dispatch_bwd's combine_kernel", d_grad_xs, ldgxs, d_slots, nullptr, nullptr, 0, dtype, T, k, H, R,
+                       d_grad_x, ldgx, d_status, stream);
+}
+
+extern "C" dlrm_status dlrm_combine_fwd(const void* d_ys, int64_t ldys, const int32_t* d_slots, const float* d_probs,
+                                        const void* d_residual, int64_t ldres, dlrm_dtype dtype, int T, int k, int H,
+                                        int R, void* d_y, int64_t ldy, uint32_t* d_status, void* stream)
+{
+    DLRM_API_RANGE("dlrm_combine_fwd");
+    clear_error();
+    const char* fn = "dlrm_combine_fwd";
+    dlrm_status s = check_rows(fn, dtype, T, k, H, R);
+    if (s != DLRM_OK || T == 0) return s;
+    const int es = dense_dtype_size(dtype);
+    if (R > 0 && (s = check_matrix(fn, "d_ys", d_ys, ldys, R, H, es)) != DLRM_OK) return s;
+    if ((s = check_words(fn, "d_slots", d_slots)) != DLRM_OK) return s;
+    if ((s = check_words(fn, "d_probs", d_probs)) != DLRM_OK) return s;
+    if (d_residual && (s = check_matrix(fn, "d_residual", d_residual, ldres, T, H, es)) != DLRM_OK) return s;
+    if ((s = check_matrix(fn, "d_y", d_y, ldy, T, H, es)) != DLRM_OK) return s;
+    return run_combine("combine_kernel", d_ys, ldys, d_slots, d_probs, d_residual, ldres, dtype, T, k, H, R, d_y, ldy,
+                       d_status, stream);
+}
+
+extern "C" dlrm_status dlrm_combine_bwd(const void* d_grad_y, int64_t ldgy, const void* d_ys, int64_t ldys,
+                                        const int32_t* d_slots, const float* d_probs, dlrm_dtype dtype, int T, int k,
+                                        int H, int R, void* d_grad_ys, int64_t ldgys, float* d_grad_probs,
+                                        uint32_t* d_status, void* stream)
+{
+    DLRM_API_RANGE("dlrm_combine_bwd");
+    clear_error();
+    const char* fn = "dlrm_combine_bwd";
+    dlrm_status s = check_rows(fn, dtype, T, k, H, R);
+    if (s != DLRM_OK || T == 0) return s;
+    const int es = dense_dtype_size(dtype);
+    if (!d_grad_ys && !d_grad_probs && R > 0) return fail(DLRM_ERR_INVALID_ARG, "%s: neither d_grad_ys nor d_grad_probs", fn);
+    if ((s = check_matrix(fn, "d_grad_y", d_grad_y, ldgy, T, H, es)) != DLRM_OK) return s;
+    if ((s = check_words(fn, "d_slots", d_slots)) != DLRM_OK) return s;
+    if (R > 0 && d_grad_probs && (s = check_matrix(fn, "d_ys", d_ys, ldys, R, H, es)) != DLRM_OK) return s;
+    if (d_grad_ys && (s = check_words(fn, "d_probs", d_probs)) != DLRM_OK) return s;
+    if (R > 0 && d_grad_ys && (s = check_matrix(fn, "d_grad_ys", d_grad_ys, ldgys, R, H, es)) != DLRM_OK) return s;
+    if (d_grad_probs && (s = check_words(fn, "d_grad_probs", d_grad_probs)) != DLRM_OK) return s;
+    const bool vec = H % 8 == 0 && rows_aligned16(d_grad_y, ldgy, T, es) &&
+                     (!d_grad_probs || rows_aligned16(d_ys, ldys, R, es)) &&
+                     (!d_grad_ys || rows_aligned16(d_grad_ys, ldgys, R, es));
+    const CombineBwd a = {d_grad_y, d_ys, ldgy, ldys, d_slots, d_probs, T, k, H, R, d_grad_ys, ldgys, d_grad_probs, d_status};
+    const bool wide = T < num_sms() * 4 && H > 512;
+    const int64_t blocks = wide ? T : ((int64_t)T + 7) / 8, most = (int64_t)num_sms() * 8;
+    return with_type(dtype, [&](auto t) {
+        using X = decltype(t);
+        auto kern = wide ? (vec ? combine_bwd_kernel<X, true, 8> : combine_bwd_kernel<X, false, 8>)
+                         : (vec ? combine_bwd_kernel<X, true, 1> : combine_bwd_kernel<X, false, 1>);
+        return check_launch_pdl(launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
+                                           as_stream(stream), a),
+                                "combine_bwd_kernel");
+    });
+}

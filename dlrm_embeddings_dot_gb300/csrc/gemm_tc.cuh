@@ -55,7 +55,7 @@ constexpr int kSmemLimit = 232448;  // 227 KB opt-in per block
 struct Args {
     int M, N;
     int kb, last_steps;             // 64-wide blocks of K, and 16-wide steps of the last one
-    int pairs;                      // plane pairs: 1, 2 (A has two planes), or 6 for fp32
+    int pairs;                      // plane pairs: 1, 2 or 3 (of A alone), or 6 for fp32
     int splits;                     // parts of K; above 1 the tiles go to `partial`
     int tiles_m, tiles_n, BN, NS;
     int a_mn, b_mn;                 // operand layouts
@@ -71,11 +71,12 @@ struct Args {
 };
 
 // Plane pair p, (A plane << 2) | B plane, the small products first.  fp32: planes hi = 0,
-// mid = 1, lo = 2 of both; two pairs: planes hi = 0, lo = 1 of A.
+// mid = 1, lo = 2 of both; two and three pairs: planes hi = 0, lo = 1 and hi, mid, lo of A,
+// where one plane holds B.
 __device__ __forceinline__ int plane_pair(int pairs, int p)
 {
     constexpr uint32_t order = 0x2u | 0x8u << 4 | 0x5u << 8 | 0x1u << 12 | 0x4u << 16 | 0x0u << 20;
-    return pairs == kMaxPairs ? (int)(order >> (4 * p)) & 15 : p + 1 < pairs ? 0x4 : 0;
+    return pairs == kMaxPairs ? (int)(order >> (4 * p)) & 15 : (pairs - 1 - p) << 2;
 }
 
 // A slice of 32 rows as a TMA box: rows of 64 bytes with the 64-byte swizzle

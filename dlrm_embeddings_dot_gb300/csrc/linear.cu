@@ -9,8 +9,10 @@
 // (linear_thin_kernel, and thin_grad.cuh backward).  The other products run on tcgen05 (gemm_tc.cuh), which
 // wants 2-byte operands with rows on the 16-byte grid.  pack_kernel lays out
 // again what is not like that: misaligned rows, and fp32 as three bf16 planes.
+#include "dlrm_block.h"
 #include "few_rows.cuh"
 #include "gemm_tc.cuh"
+#include "packed8.cuh"
 #include "thin_grad.cuh"
 
 namespace dlrm {
@@ -116,6 +118,50 @@ dlrm_status launch_pack(const PackJob& a, const PackJob& b, cudaStream_t st, Ove
     return check_launch_pdl(launch_pdl(pack_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, a, b,
                                        overlap),
                             "pack_kernel");
+}
+
+struct Unpack8Job {
+    Packed8 src;
+    int rows, cols, vec;
+    void* dst;          // [rows][padded(cols)], T; for fp32 bf16, which holds every value of 8 bits
+};
+
+// The input in 8 bits read back as an operand, and beside it the weights' copy as in pack_kernel.
+template <typename T>
+__global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ Unpack8Job j0, const __grid_constant__ PackJob j1,
+                                                     Overlap overlap)
+{
+    using X = std::conditional_t<std::is_same_v<T, float>, bf16, T>;
+    pdl_begin(overlap);
+    const int64_t n0 = (int64_t)j0.rows * ((j0.cols + 7) / 8), n1 = (int64_t)j1.rows * ((j1.cols + 7) / 8);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n0 + n1; i += (int64_t)gridDim.x * 256) {
+        const bool first = i < n0;
+        const int64_t k = first ? i : i - n0;
+        const int cols = first ? j0.cols : j1.cols, groups = (cols + 7) / 8;
+        const int64_t row = k / groups;
+        const int col = (int)(k - row * groups) * 8, n = cols - col;
+        float f[8];
+        if (first) {
+            widen_run8<T>(j0.vec && n >= 8 ? load_run8<true>(j0.src, row, col, 8) : load_run8<false>(j0.src, row, col, n), f);
+            *reinterpret_cast<uint4*>((X*)j0.dst + k * 8) = pack8<X>(f);
+        } else {
+            const T* p = (const T*)j1.src + row * j1.ld + col;
+            if (j1.vec && n >= 8) widen8<T>(load8<T, true>(p, 8), f);
+            else widen8<T>(load8<T, false>(p, n), f);
+            store_operand8<T>(j1.dst, k * 8, j1.rows * (int64_t)groups * 8, f);
+        }
+    }
+}
+
+template <typename T>
+dlrm_status launch_unpack(const Unpack8Job& a, const PackJob& b, cudaStream_t st, Overlap overlap)
+{
+    const int64_t runs = (int64_t)a.rows * ((a.cols + 7) / 8) + (int64_t)b.rows * ((b.cols + 7) / 8);
+    if (runs == 0) return DLRM_OK;
+    const int64_t want = (runs + 255) / 256, most = (int64_t)num_sms() * 8;
+    return check_launch_pdl(launch_pdl(unpack_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, a, b,
+                                       overlap),
+                            "unpack_kernel");
 }
 
 // A matrix argument as an operand: itself, or its copy at ws of `planes` planes.
@@ -280,13 +326,37 @@ dlrm_status launch_thin(const void* x, int64_t ldx, const void* w, int64_t ldw, 
 
 // ------------------------------------------------------- gradient of z and b
 // dZ = a'(pre) drop(dY) as an operand of the products (dz, may be NULL; two: of two
-// planes), and column sums of it times scale (partial [gridDim.y][N], may be NULL).  A block covers
+// planes; pre of type T, or in 8 bits), and column sums of it times scale (partial [gridDim.y][N], may be NULL).  A block covers
 // cg * 8 columns and `rows` rows: a thread owns eight columns of every
 // (256 / cg)-th row and adds them up in registers, then the block adds its
 // threads' sums in shared memory.
 template <typename T>
+struct PreMatrix {
+    const T* p;
+    int64_t ld;
+    using Run = Raw8<T>;
+    __device__ Run load(int r, int col, int n, bool v) const
+    {
+        const T* q = p + r * ld + col;
+        return v ? load8<T, true>(q, 8) : load8<T, false>(q, n);
+    }
+    static __device__ void widen(const Run& r, float (&f)[8]) { widen8<T>(r, f); }
+};
+
+template <typename T>
+struct PreMatrix8 {
+    Packed8 m;
+    using Run = Run8;
+    __device__ Run load(int r, int col, int n, bool v) const
+    {
+        return v ? load_run8<true>(m, r, col, 8) : load_run8<false>(m, r, col, n);
+    }
+    static __device__ void widen(const Run& r, float (&f)[8]) { widen_run8<T>(r, f); }
+};
+
+template <typename T, typename Pre>
 __global__ void __launch_bounds__(256, 3)
-grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, int64_t ldp, int act, int vec,
+grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const Pre pre, int act, int vec,
               Drop drop, float scale, int M, int N, int cg, int rows, int two, void* __restrict__ dz,
               float* __restrict__ partial, Overlap overlap)
 {
@@ -302,15 +372,15 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, 
         const int r0 = blockIdx.y * rows + ty, r1 = min(M, (int)(blockIdx.y + 1) * rows);
         const bool v = vec && n >= 8;
         for (int r = r0; r < r1; r += step * kAhead) {
-            Raw8<T> a[kAhead], b[kAhead];
+            Raw8<T> a[kAhead];
+            typename Pre::Run b[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int rr = r + k * step;
                 if (rr < r1) {
                     const T* gp = dy + rr * ldg + col;
-                    const T* pp = pre + rr * ldp + col;
                     a[k] = v ? load8<T, true>(gp, 8) : load8<T, false>(gp, n);
-                    if (act != DLRM_ACT_NONE) b[k] = v ? load8<T, true>(pp, 8) : load8<T, false>(pp, n);
+                    if (act != DLRM_ACT_NONE) b[k] = pre.load(rr, col, n, v);
                 }
             }
 #pragma unroll
@@ -321,7 +391,7 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const T* __restrict__ pre, 
                 widen8<T>(a[k], f);
                 if (act != DLRM_ACT_NONE) {
                     float z[8];
-                    widen8<T>(b[k], z);
+                    Pre::widen(b[k], z);
                     slope8<T>(f, z, act);
                 }
                 if (drop.thr) drop8(f, drop, key, (uint32_t)rr, (uint32_t)g);
@@ -428,6 +498,12 @@ Shape grad_shape(dlrm_dtype dt, dlrm_act act, int M, int N, int K)
             gemm::column_cycles(N, dense_dtype_size(dt), false)};
 }
 
+// dW's shape where the input comes in 8 bits: one plane holds it, whatever the type.
+Shape grad_shape8(dlrm_dtype dt, dlrm_act act, int M, int N, int K)
+{
+    return {M, N, K, z_planes(dt, act), gemm::column_cycles(N, dense_dtype_size(dt), false)};
+}
+
 // The workspaces' pieces, one after another.
 struct FwdLayout {
     size_t x, w, partial, total;   // x, w: bytes of the operands' copies (0: used as they are)
@@ -448,23 +524,161 @@ struct BwdLayout {
     size_t dz, x, w, sums, partial_x, partial_w, total;
 };
 
-BwdLayout bwd_layout(const void* dy, int64_t ldg, const void* x, int64_t ldx, const void* w, int64_t ldw, dlrm_dtype dt,
-                     int M, int N, int K, dlrm_act act, double p)
+// The layer's input and pre-activation, of the call's type or in 8 bits (bits8).
+struct Kept {
+    bool bits8;
+    const void *x, *pre;
+    int64_t ldx, ldp;
+    Packed8 x8, pre8;
+};
+
+BwdLayout bwd_layout(const void* dy, int64_t ldg, const Kept& in, const void* w, int64_t ldw, dlrm_dtype dt, int M, int N,
+                     int K, dlrm_act act, double p)
 {
     BwdLayout l = {};
     if (few_outputs(N)) {
-        l.total = l.sums = thin::workspace_bytes(dt, M, N, K);
+        if (in.bits8) {   // read back first
+            const int es = dense_dtype_size(dt);
+            l.x = dlrm_ws_align((size_t)M * padded(K) * es);
+            l.dz = act != DLRM_ACT_NONE ? dlrm_ws_align((size_t)M * padded(N) * es) : 0;
+        }
+        l.sums = thin::workspace_bytes(dt, M, N, K);
+        l.total = l.dz + l.x + l.sums;
         return l;
     }
     l.dz = act != DLRM_ACT_NONE || p > 0 || needs_pack(dy, ldg, M, dt) ? operand_bytes(M, N, z_planes(dt, act)) : 0;
-    l.x = needs_pack(x, ldx, M, dt) ? operand_bytes(M, K, planes_of(dt)) : 0;
+    l.x = in.bits8 ? operand_bytes(M, K, 1) : needs_pack(in.x, in.ldx, M, dt) ? operand_bytes(M, K, planes_of(dt)) : 0;
     l.w = needs_pack(w, ldw, N, dt) ? operand_bytes(N, K, planes_of(dt)) : 0;
     const GradZ g = grad_z_shape(M, N);
     l.sums = g.chunks > 1 ? dlrm_ws_align((size_t)g.chunks * N * 4) : 0;
     l.partial_x = gemm::partial_bytes(grad_shape(dt, act, M, K, N));
-    l.partial_w = gemm::partial_bytes(grad_shape(dt, act, N, K, M));
+    l.partial_w = gemm::partial_bytes(in.bits8 ? grad_shape8(dt, act, N, K, M) : grad_shape(dt, act, N, K, M));
     l.total = l.dz + l.x + l.w + l.sums + l.partial_x + l.partial_w;
     return l;
+}
+
+// dlrm_linear_bwd, and dlrm_linear_bwd8: the same with the kept tensors in 8 bits.
+dlrm_status run_bwd(const char* fn, const void* d_grad_y, int64_t ldg, const Kept& in, const void* d_w, int64_t ldw,
+                    dlrm_dtype dtype, int M, int N, int K, dlrm_act act, double p, const uint64_t* d_rng, void* d_grad_x,
+                    int64_t lddx, void* d_grad_w, int64_t lddw, float* d_grad_bias, void* d_workspace,
+                    size_t workspace_bytes, uint32_t* d_status, void* stream)
+{
+    dlrm_status s = check_sizes(fn, dtype, M, N, K, act);
+    if (s != DLRM_OK) return s;
+    Drop drop;
+    if ((s = make_drop(fn, p, d_rng, &drop)) != DLRM_OK) return s;
+    const int es = dense_dtype_size(dtype);
+    if (d_grad_w && (s = check_matrix(fn, "d_grad_w", d_grad_w, lddw, N, K, es)) != DLRM_OK) return s;
+    if (d_grad_bias && (s = check_matrix(fn, "d_grad_bias", d_grad_bias, N, 1, N, 4)) != DLRM_OK) return s;
+    cudaStream_t st = as_stream(stream);
+    if (M == 0) {
+        // no rows: the gradients that sum over them are zero
+        cudaError_t ce = cudaSuccess;
+        if (d_grad_w)
+            ce = cudaMemset2DAsync(d_grad_w, (size_t)(N > 1 ? lddw : K) * es, 0, (size_t)K * es, (size_t)N, st);
+        if (ce == cudaSuccess && d_grad_bias) ce = cudaMemsetAsync(d_grad_bias, 0, (size_t)N * 4, st);
+        return ce == cudaSuccess ? DLRM_OK : fail(DLRM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
+    }
+    if ((s = check_matrix(fn, "d_grad_y", d_grad_y, ldg, M, N, es)) != DLRM_OK) return s;
+    if (in.bits8) {
+        if (act != DLRM_ACT_NONE && (s = check_packed(fn, "d_pre_q", in.pre8.q, in.pre8.ld, in.pre8.exps, M, N)) != DLRM_OK)
+            return s;
+        if (d_grad_w && (s = check_packed(fn, "d_x_q", in.x8.q, in.x8.ld, in.x8.exps, M, K)) != DLRM_OK) return s;
+    } else {
+        if (act != DLRM_ACT_NONE && (s = check_matrix(fn, "d_pre", in.pre, in.ldp, M, N, es)) != DLRM_OK) return s;
+        if (d_grad_w && (s = check_matrix(fn, "d_x", in.x, in.ldx, M, K, es)) != DLRM_OK) return s;
+    }
+    if (d_grad_x && (s = check_matrix(fn, "d_w", d_w, ldw, N, K, es)) != DLRM_OK) return s;
+    if (d_grad_x && (s = check_matrix(fn, "d_grad_x", d_grad_x, lddx, M, K, es)) != DLRM_OK) return s;
+    const BwdLayout l = bwd_layout(d_grad_y, ldg, in, d_w, ldw, dtype, M, N, K, act, p);
+    if ((s = check_workspace(fn, d_workspace, workspace_bytes, l.total)) != DLRM_OK) return s;
+    // 2-byte types: dZ without the dropout's scale, the sums times it (fp32's planes hold the scaled values)
+    const float scale = dtype == DLRM_F32 ? 1.f : drop.scale;
+    if (dtype != DLRM_F32) drop.scale = 1.f;
+    const int zp = z_planes(dtype, act), planes = planes_of(dtype);
+    return with_type(dtype, [&](auto t) -> dlrm_status {
+        using T = decltype(t);
+        const float z_scale = zp == 2 ? scale / kFit<T> : scale;
+        if (few_outputs(N)) {
+            if (!d_grad_x && !d_grad_w && !d_grad_bias) return DLRM_OK;
+            uint8_t* ws = (uint8_t*)d_workspace;
+            Kept at = in;
+            if (in.bits8) {
+                dlrm_status r = DLRM_OK;
+                at.pre = ws;
+                at.x = ws + l.dz;
+                at.ldp = padded(N);
+                at.ldx = padded(K);
+                if (act != DLRM_ACT_NONE)
+                    r = dlrm_unpack8(in.pre8.q, in.pre8.ld, in.pre8.exps, dtype, M, N, ws, at.ldp, st);
+                if (r == DLRM_OK && d_grad_w)
+                    r = dlrm_unpack8(in.x8.q, in.x8.ld, in.x8.exps, dtype, M, K, ws + l.dz, at.ldx, st);
+                if (r != DLRM_OK) return r;
+                ws += l.dz + l.x;
+            }
+            thin::Grad a = {d_grad_y, at.pre, at.x, d_w, ldg, at.ldp, at.ldx, ldw, M, N, K, (int)act, drop, z_scale, scale};
+            a.dx = d_grad_x;
+            a.dw = d_grad_w;
+            a.lddx = lddx;
+            a.lddw = lddw;
+            a.db = d_grad_bias;
+            return thin::run<T>(dtype, a, (float*)ws, st);
+        }
+        const bool bf = dtype != DLRM_F16;
+        uint8_t* ws = (uint8_t*)d_workspace;
+        void *dz = l.dz ? ws : nullptr, *xs = l.x ? ws + l.dz : nullptr, *wsp = l.w ? ws + l.dz + l.x : nullptr;
+        float* sums = (float*)(ws + l.dz + l.x + l.w);
+        float* px = (float*)(ws + l.dz + l.x + l.w + l.sums);
+        float* pw = (float*)(ws + l.dz + l.x + l.w + l.sums + l.partial_x);
+        // the copies and dZ run together, then dX, dW and the sum of the bias gradient
+        const bool products = d_grad_x || d_grad_w;
+        const GradZ g = grad_z_shape(M, N);
+        const bool make_z = (dz && products) || d_grad_bias, sum = d_grad_bias && g.chunks > 1;
+        PackJob jx = {}, jw = {};
+        Unpack8Job j8 = {};
+        if (in.bits8 && d_grad_w) j8 = {in.x8, M, K, rows_aligned8(in.x8.q, in.x8.ld, M), xs};
+        else if (xs && d_grad_w) jx = {in.x, in.ldx, M, K, rows_aligned16(in.x, in.ldx, M, es), xs};
+        if (wsp && d_grad_x) jw = {d_w, ldw, N, K, rows_aligned16(d_w, ldw, N, es), wsp};
+        const bool packs = jx.src || jw.src || j8.dst;
+        dlrm_status r = in.bits8 ? launch_unpack<T>(j8, jw, st, {0, make_z}) : launch_pack<T>(jx, jw, st, {0, make_z});
+        if (r == DLRM_OK && make_z) {
+            auto go = [&](auto pre, bool pre_vec) {
+                const int vec = rows_aligned16(d_grad_y, ldg, M, es) && (act == DLRM_ACT_NONE || pre_vec);
+                return check_launch_pdl(launch_pdl(grad_z_kernel<T, decltype(pre)>, dim3(g.blocks_x, g.chunks), dim3(256), 0,
+                                                   st, (const T*)d_grad_y, ldg, pre, (int)act, vec, drop, scale, M, N, g.cg,
+                                                   g.rows, (int)(zp == 2), products ? dz : nullptr,
+                                                   d_grad_bias ? (sum ? sums : d_grad_bias) : nullptr, Overlap{packs, 0}),
+                                        "grad_z_kernel");
+            };
+            r = in.bits8 ? go(PreMatrix8<T>{in.pre8}, rows_aligned8(in.pre8.q, in.pre8.ld, M))
+                         : go(PreMatrix<T>{(const T*)in.pre, in.ldp}, rows_aligned16(in.pre, in.ldp, M, es));
+        }
+        Epilogue ex = {}, ew = {};
+        ex.scale = ew.scale = z_scale;
+        const Shape sx = grad_shape(dtype, act, M, K, N), 
+                    sw = in.bits8 ? grad_shape8(dtype, act, N, K, M) : grad_shape(dtype, act, N, K, M);
+        if (r == DLRM_OK && d_grad_x) {
+            ex.out = d_grad_x;
+            ex.ldo = lddx;
+            ex.vec = epilogue_vec(ex, M, es);
+            r = gemm::run<T>(fn, sx, operand(d_grad_y, ldg, M, N, dz, zp, false), operand(d_w, ldw, N, K, wsp, planes, true),
+                             bf, ex, px, d_status, st, {0, d_grad_w || sum});
+        }
+        if (r == DLRM_OK && d_grad_w) {
+            ew.out = d_grad_w;
+            ew.ldo = lddw;
+            ew.vec = epilogue_vec(ew, N, es);
+            r = gemm::run<T>(fn, sw, operand(d_grad_y, ldg, M, N, dz, zp, true), operand(in.x, in.ldx, M, K, xs, in.bits8 ? 1 : planes, true),
+                             bf, ew, pw, d_status, st, {d_grad_x != nullptr, sum});
+        }
+        if (r == DLRM_OK && sum)
+            r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 31) / 32), dim3(1024), 0, st, (const float*)sums,
+                                            g.chunks, N, d_grad_bias, Overlap{products, 0}),
+                                 "sum_rows_kernel");
+        if (r == DLRM_OK && d_grad_x) r = gemm::finish<T>(sx, ex, px, st);
+        if (r == DLRM_OK && d_grad_w) r = gemm::finish<T>(sw, ew, pw, st);
+        return r;
+    });
 }
 
 }  // namespace
@@ -528,7 +742,10 @@ extern "C" size_t dlrm_linear_bwd_workspace_size(const void* d_grad_y, int64_t l
                                                  dlrm_act act, double p)
 {
     if (!sizes_ok(dtype, M, N, K)) return 0;
-    return bwd_layout(d_grad_y, ldg, d_x, ldx, d_w, ldw, dtype, M, N, K, act, p).total;
+    Kept in = {};
+    in.x = d_x;
+    in.ldx = ldx;
+    return bwd_layout(d_grad_y, ldg, in, d_w, ldw, dtype, M, N, K, act, p).total;
 }
 
 extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const void* d_x, int64_t ldx,
@@ -539,93 +756,37 @@ extern "C" dlrm_status dlrm_linear_bwd(const void* d_grad_y, int64_t ldg, const 
 {
     DLRM_API_RANGE("dlrm_linear_bwd");
     clear_error();
-    const char* fn = "dlrm_linear_bwd";
-    dlrm_status s = check_sizes(fn, dtype, M, N, K, act);
-    if (s != DLRM_OK) return s;
-    Drop drop;
-    if ((s = make_drop(fn, p, d_rng, &drop)) != DLRM_OK) return s;
-    const int es = dense_dtype_size(dtype);
-    if (d_grad_w && (s = check_matrix(fn, "d_grad_w", d_grad_w, lddw, N, K, es)) != DLRM_OK) return s;
-    if (d_grad_bias && (s = check_matrix(fn, "d_grad_bias", d_grad_bias, N, 1, N, 4)) != DLRM_OK) return s;
-    cudaStream_t st = as_stream(stream);
-    if (M == 0) {
-        // no rows: the gradients that sum over them are zero
-        cudaError_t ce = cudaSuccess;
-        if (d_grad_w)
-            ce = cudaMemset2DAsync(d_grad_w, (size_t)(N > 1 ? lddw : K) * es, 0, (size_t)K * es, (size_t)N, st);
-        if (ce == cudaSuccess && d_grad_bias) ce = cudaMemsetAsync(d_grad_bias, 0, (size_t)N * 4, st);
-        return ce == cudaSuccess ? DLRM_OK : fail(DLRM_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(ce));
-    }
-    if ((s = check_matrix(fn, "d_grad_y", d_grad_y, ldg, M, N, es)) != DLRM_OK) return s;
-    if (act != DLRM_ACT_NONE && (s = check_matrix(fn, "d_pre", d_pre, ldp, M, N, es)) != DLRM_OK) return s;
-    if (d_grad_w && (s = check_matrix(fn, "d_x", d_x, ldx, M, K, es)) != DLRM_OK) return s;
-    if (d_grad_x && (s = check_matrix(fn, "d_w", d_w, ldw, N, K, es)) != DLRM_OK) return s;
-    if (d_grad_x && (s = check_matrix(fn, "d_grad_x", d_grad_x, lddx, M, K, es)) != DLRM_OK) return s;
-    const BwdLayout l = bwd_layout(d_grad_y, ldg, d_x, ldx, d_w, ldw, dtype, M, N, K, act, p);
-    if ((s = check_workspace(fn, d_workspace, workspace_bytes, l.total)) != DLRM_OK) return s;
-    // 2-byte types: dZ without the dropout's scale, the sums times it (fp32's planes hold the scaled values)
-    const float scale = dtype == DLRM_F32 ? 1.f : drop.scale;
-    if (dtype != DLRM_F32) drop.scale = 1.f;
-    const int zp = z_planes(dtype, act), planes = planes_of(dtype);
-    return with_type(dtype, [&](auto t) -> dlrm_status {
-        using T = decltype(t);
-        const float z_scale = zp == 2 ? scale / kFit<T> : scale;
-        if (few_outputs(N)) {
-            if (!d_grad_x && !d_grad_w && !d_grad_bias) return DLRM_OK;
-            thin::Grad a = {d_grad_y, d_pre, d_x, d_w, ldg, ldp, ldx, ldw, M, N, K, (int)act, drop, z_scale, scale};
-            a.dx = d_grad_x;
-            a.dw = d_grad_w;
-            a.lddx = lddx;
-            a.lddw = lddw;
-            a.db = d_grad_bias;
-            return thin::run<T>(dtype, a, (float*)d_workspace, st);
-        }
-        const bool bf = dtype != DLRM_F16;
-        uint8_t* ws = (uint8_t*)d_workspace;
-        void *dz = l.dz ? ws : nullptr, *xs = l.x ? ws + l.dz : nullptr, *wsp = l.w ? ws + l.dz + l.x : nullptr;
-        float* sums = (float*)(ws + l.dz + l.x + l.w);
-        float* px = (float*)(ws + l.dz + l.x + l.w + l.sums);
-        float* pw = (float*)(ws + l.dz + l.x + l.w + l.sums + l.partial_x);
-        // the copies and dZ run together, then dX, dW and the sum of the bias gradient
-        const bool products = d_grad_x || d_grad_w;
-        const GradZ g = grad_z_shape(M, N);
-        const bool make_z = (dz && products) || d_grad_bias, sum = d_grad_bias && g.chunks > 1;
-        PackJob jx = {}, jw = {};
-        if (xs && d_grad_w) jx = {d_x, ldx, M, K, rows_aligned16(d_x, ldx, M, es), xs};
-        if (wsp && d_grad_x) jw = {d_w, ldw, N, K, rows_aligned16(d_w, ldw, N, es), wsp};
-        const bool packs = jx.src || jw.src;
-        dlrm_status r = launch_pack<T>(jx, jw, st, {0, make_z});
-        if (r == DLRM_OK && make_z) {
-            const int vec = rows_aligned16(d_grad_y, ldg, M, es) && (act == DLRM_ACT_NONE || rows_aligned16(d_pre, ldp, M, es));
-            r = check_launch_pdl(launch_pdl(grad_z_kernel<T>, dim3(g.blocks_x, g.chunks), dim3(256), 0, st,
-                                            (const T*)d_grad_y, ldg, (const T*)d_pre, ldp, (int)act, vec, drop, scale,
-                                            M, N, g.cg, g.rows, (int)(zp == 2), products ? dz : nullptr,
-                                            d_grad_bias ? (sum ? sums : d_grad_bias) : nullptr, Overlap{packs, 0}),
-                                 "grad_z_kernel");
-        }
-        Epilogue ex = {}, ew = {};
-        ex.scale = ew.scale = z_scale;
-        const Shape sx = grad_shape(dtype, act, M, K, N), sw = grad_shape(dtype, act, N, K, M);
-        if (r == DLRM_OK && d_grad_x) {
-            ex.out = d_grad_x;
-            ex.ldo = lddx;
-            ex.vec = epilogue_vec(ex, M, es);
-            r = gemm::run<T>(fn, sx, operand(d_grad_y, ldg, M, N, dz, zp, false), operand(d_w, ldw, N, K, wsp, planes, true),
-                             bf, ex, px, d_status, st, {0, d_grad_w || sum});
-        }
-        if (r == DLRM_OK && d_grad_w) {
-            ew.out = d_grad_w;
-            ew.ldo = lddw;
-            ew.vec = epilogue_vec(ew, N, es);
-            r = gemm::run<T>(fn, sw, operand(d_grad_y, ldg, M, N, dz, zp, true), operand(d_x, ldx, M, K, xs, planes, true),
-                             bf, ew, pw, d_status, st, {d_grad_x != nullptr, sum});
-        }
-        if (r == DLRM_OK && sum)
-            r = check_launch_pdl(launch_pdl(sum_rows_kernel, dim3((N + 31) / 32), dim3(1024), 0, st, (const float*)sums,
-                                            g.chunks, N, d_grad_bias, Overlap{products, 0}),
-                                 "sum_rows_kernel");
-        if (r == DLRM_OK && d_grad_x) r = gemm::finish<T>(sx, ex, px, st);
-        if (r == DLRM_OK && d_grad_w) r = gemm::finish<T>(sw, ew, pw, st);
-        return r;
-    });
+    Kept in = {};
+    in.x = d_x;
+    in.ldx = ldx;
+    in.pre = d_pre;
+    in.ldp = ldp;
+    return run_bwd("dlrm_linear_bwd", d_grad_y, ldg, in, d_w, ldw, dtype, M, N, K, act, p, d_rng, d_grad_x, lddx, d_grad_w,
+                   lddw, d_grad_bias, d_workspace, workspace_bytes, d_status, stream);
+}
+
+extern "C" size_t dlrm_linear_bwd8_workspace_size(const void* d_grad_y, int64_t ldg, const void* d_w, int64_t ldw,
+                                                  dlrm_dtype dtype, int M, int N, int K, dlrm_act act, double p)
+{
+    if (!sizes_ok(dtype, M, N, K)) return 0;
+    Kept in = {};
+    in.bits8 = true;
+    return bwd_layout(d_grad_y, ldg, in, d_w, ldw, dtype, M, N, K, act, p).total;
+}
+
+extern "C" dlrm_status dlrm_linear_bwd8(const void* d_grad_y, int64_t ldg, const uint8_t* d_x_q, int64_t ldx,
+                                        const uint8_t* d_x_exps, const void* d_w, int64_t ldw, const uint8_t* d_pre_q,
+                                        int64_t ldp, const uint8_t* d_pre_exps, dlrm_dtype dtype, int M, int N, int K,
+                                        dlrm_act act, double p, const uint64_t* d_rng, void* d_grad_x, int64_t lddx,
+                                        void* d_grad_w, int64_t lddw, float* d_grad_bias, void* d_workspace,
+                                        size_t workspace_bytes, uint32_t* d_status, void* stream)
+{
+    DLRM_API_RANGE("dlrm_linear_bwd8");
+    clear_error();
+    Kept in = {};
+    in.bits8 = true;
+    in.x8 = {d_x_q, ldx, d_x_exps, blocks8(K)};
+    in.pre8 = {d_pre_q, ldp, d_pre_exps, blocks8(N)};
+    return run_bwd("dlrm_linear_bwd8", d_grad_y, ldg, in, d_w, ldw, dtype, M, N, K, act, p, d_rng, d_grad_x, lddx, d_grad_w,
+                   lddw, d_grad_bias, d_workspace, workspace_bytes, d_status, stream);
 }

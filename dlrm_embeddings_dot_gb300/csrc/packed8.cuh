@@ -1,0 +1,84 @@
+// packed8.cuh -- matrices in 8 bits (include/dlrm_block.h): eight columns read back.
+#pragma once
+
+#include "dense_ops.cuh"
+
+namespace dlrm {
+
+constexpr int kBlock8 = 32;   // columns that share an exponent byte
+
+struct Packed8 {
+    const uint8_t* q;
+    int64_t ld;
+    const uint8_t* exps;      // [rows][blocks]
+    int blocks;
+};
+
+inline int blocks8(int cols) { return (cols - 1) / kBlock8 + 1; }
+
+// Eight columns as they lie in memory, and their block's exponent byte.
+struct Run8 {
+    uint2 q;
+    uint32_t e;
+};
+
+// VEC: the run starts on an 8-byte boundary and has all eight columns; the others read as 0.
+template <bool VEC>
+__device__ __forceinline__ Run8 load_run8(const Packed8& m, int64_t row, int col, int n)
+{
+    Run8 r;
+    const uint8_t* p = m.q + row * m.ld + col;
+    if constexpr (VEC) {
+        r.q = __ldg(reinterpret_cast<const uint2*>(p));
+    } else {
+        uint8_t b[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = i < n ? __ldg(p + i) : 0;
+        memcpy(&r.q, b, 8);
+    }
+    r.e = __ldg(m.exps + row * m.blocks + col / kBlock8);
+    return r;
+}
+
+// The largest size a value read back has as a T (fp32: bf16's).
+template <typename T>
+constexpr float kMost8 = std::is_same_v<T, __half> ? 65504.f : 3.3895313892515355e38f;
+
+// q 2^(e - 127), exact in fp32
+template <typename T>
+__device__ __forceinline__ void widen_run8(const Run8& r, float (&f)[8])
+{
+    const float scale = __uint_as_float(r.e ? r.e << 23 : 0x00400000u);
+    const uint32_t w[2] = {r.q.x, r.q.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i / 2] >> 16 * (i % 2))));
+        __half2 v;
+        memcpy(&v, &h, 4);
+        const float2 g = __half22float2(v);
+        f[2 * i] = g.x * scale;
+        f[2 * i + 1] = g.y * scale;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (fabsf(f[i]) > kMost8<T>) f[i] = copysignf(kMost8<T>, f[i]);
+}
+
+// Whether runs of eight columns start on 8-byte boundaries in every row.
+inline bool rows_aligned8(const void* p, int64_t ld, int rows)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 7u) == 0 && (rows <= 1 || ld % 8 == 0);
+}
+
+// Checks a matrix in 8 bits (rows > 0).
+inline dlrm_status check_packed(const char* fn, const char* name, const uint8_t* q, int64_t ld, const uint8_t* exps, int rows,
+                                int cols)
+{
+    const dlrm_status s = check_matrix(fn, name, q, ld, rows, cols, 1);
+    if (s != DLRM_OK) return s;
+    if (!exps) return fail(DLRM_ERR_INVALID_ARG, "%s: %s has no exponents", fn, name);
+    return DLRM_OK;
+}
+
+}  // namespace dlrm

@@ -17,6 +17,7 @@ import torch
 
 import dlrm_embeddings_dot_gb300 as _dl
 
+from . import block_abi
 from .dense_abi import (DLRM_ACT_GELU, DLRM_ACT_NONE, DLRM_ACT_RELU, DLRM_ACT_SILU, DLRM_MOE_MAX_EXPERTS,  # noqa: F401
                         DLRM_MOE_MAX_TOKENS, DLRM_MOE_MAX_TOP_K, declare)
 
@@ -40,6 +41,7 @@ def _load():
                torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream")
                else lambda d: torch.cuda.current_stream(d).cuda_stream,
                tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+        m.bind_block(torch.uint8, tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in block_abi.ENTRY_POINTS))
         _marshal = m
     return _marshal
 
