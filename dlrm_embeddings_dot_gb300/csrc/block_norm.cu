@@ -6,11 +6,14 @@
 // and its gradient.  Both are bound by memory: every matrix goes once, a row stays in
 // registers between its sums.
 //
-//   forward    a row by W warps of C runs of eight columns a lane; the statistics are
-//              taken in two passes over the registers (mean, then squares about it)
-//   backward   a row by W warps of one run a lane, which then holds the vectors' part
-//              and the sums over rows of its columns in registers, and the next row's
-//              loads are in flight while a row is computed.  Blocks' sums go to `partial`
+// A row is taken by W warps, eight columns a lane, which holds its part of the vectors in
+// registers.  The next rows are on their way meanwhile: a ring of rows in shared
+// memory, each thread copying its own columns (cp.async), so that no thread waits for
+// another's copies.  Sums of a row go by shuffles, then over its warps by shared memory.
+//
+//   forward    the statistics are taken in two passes over the registers (mean, then
+//              squares about it)
+//   backward   a lane also adds up its columns' sums over rows.  Blocks' sums go to `partial`
 //              and block_norm_sum_kernel adds them in order
 //
 // Nothing here depends on which column a lane has, so rows off the 16-byte grid give a
@@ -53,9 +56,72 @@ __device__ __forceinline__ Raw8<T> load_run(const T* row, int first, int N)
     return r;
 }
 
+// A thread's part of the rows to come: kAhead rows of NT tensors, three where the blocks that
+// share an SM (two of 256 threads, one of more) have the memory.  Where copies cannot be
+// asynchronous (2-byte elements off the grid) a row is loaded to registers and stored.
+template <typename T, bool VEC, int NT, int THREADS>
+struct Ring {
+    static constexpr int kWords = sizeof(T) / 2, kSlot = kWords * THREADS * 16, kStage = NT * kSlot;
+    static constexpr int kMost = (THREADS > 256 ? 224 << 10 : 110 << 10) / kStage, kAhead = kMost < 3 ? kMost : 3;
+    static_assert(kAhead >= 1, "a row fits");
+    static constexpr size_t kBytes = (size_t)kAhead * kStage;
+    uint8_t* mine;    // word 0 of slot 0 of stage 0
+    uint32_t at;      // its shared address
+    int N, first;
+
+    __device__ Ring(uint8_t* smem, int n, int f) : mine(smem + threadIdx.x * 16), N(n), first(f)
+    {
+        at = (uint32_t)__cvta_generic_to_shared(mine);
+        for (int i = 0; i < kAhead * NT * kWords; ++i)   // columns past the end stay 0
+            *reinterpret_cast<uint4*>(mine + i * THREADS * 16) = make_uint4(0, 0, 0, 0);
+    }
+    // Starts the copy of a row's run to a slot.
+    __device__ __forceinline__ void fetch(int stage, int slot, const T* row) const
+    {
+        const uint32_t to = at + stage * kStage + slot * kSlot;
+        if constexpr (VEC) {
+            if (first < N)
+#pragma unroll
+                for (int i = 0; i < kWords; ++i)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * THREADS * 16),
+                                 "l"(reinterpret_cast<const uint4*>(row + first) + i)
+                                 : "memory");
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (first + 32 * i < N)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + i / 4 * THREADS * 16 + i % 4 * 4),
+                                 "l"(row + first + 32 * i)
+                                 : "memory");
+        } else {
+            *reinterpret_cast<uint4*>(mine + stage * kStage + slot * kSlot) = load_run<T, VEC>(row, first, N).w[0];
+        }
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // The oldest row's copies are complete.
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
+    __device__ __forceinline__ void read(int stage, int slot, float2 (&f)[4]) const
+    {
+        Raw8<T> r;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            r.w[i] = *reinterpret_cast<const uint4*>(mine + stage * kStage + slot * kSlot + i * THREADS * 16);
+        float v[8];
+        widen8<T>(r, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+    }
+};
+
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_run(T* row, int first, int N, const float (&f)[8])
+__device__ __forceinline__ void store_run(T* row, int first, int N, const float2 (&v)[4])
 {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = v[i].x;
+        f[2 * i + 1] = v[i].y;
+    }
     if constexpr (VEC) {
         if (first < N) store8<T, true>(row + first, 8, f);
     } else {
@@ -65,74 +131,97 @@ __device__ __forceinline__ void store_run(T* row, int first, int N, const float 
     }
 }
 
-// The run's part of a vector, `fill` everywhere where there is none.
+// The run's part of a vector: `fill` everywhere where there is none, 0 past the row's end.
 template <bool VEC>
-__device__ __forceinline__ void load_vector(const float* p, int first, int N, float fill, float (&f)[8])
+__device__ __forceinline__ void load_vector(const float* p, int first, int N, float fill, float2 (&f)[4])
 {
-    if (!p) {
+    float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = fill;
-    } else if constexpr (VEC) {
-        float4 a = make_float4(0, 0, 0, 0), b = a;
-        if (first < N) {
-            a = __ldg(reinterpret_cast<const float4*>(p + first));
-            b = __ldg(reinterpret_cast<const float4*>(p + first) + 1);
-        }
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
+    for (int i = 0; i < 8; ++i)
+        v[i] = !run_has<VEC>(first, i, N) ? 0.f : p ? __ldg(p + first + (VEC ? i : 32 * i)) : fill;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = first + 32 * i < N ? __ldg(p + first + 32 * i) : 0.f;
-    }
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
 }
 
-// Sums of V values over the W warps of a row, the same in all of them.  red: two areas that
-// take turns, so that one barrier a sum is enough.
+// Sums of V (1 or 2) values over the W warps of a row, the same in all of them.  red: two areas
+// that take turns, so that one barrier a sum is enough.
 template <int W, int V>
 __device__ __forceinline__ void row_sum(float (&v)[V], float* red, int& turn, int warp)
 {
+    const int lane = threadIdx.x % kWarp;
+    float s = v[0];
+    if constexpr (V == 2) {   // each half of the warp goes on with one of the two
+        const bool up = lane & 16;
+        s = (up ? v[1] : v[0]) + __shfl_xor_sync(~0u, up ? v[0] : v[1], 16);
+    } else {
+        s += __shfl_xor_sync(~0u, s, 16);
+    }
 #pragma unroll
-    for (int m = 16; m; m /= 2)
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] += __shfl_xor_sync(~0u, v[i], m);
-    if constexpr (W > 1) {
+    for (int m = 8; m; m /= 2) s += __shfl_xor_sync(~0u, s, m);
+    if constexpr (W == 1) {
+        if constexpr (V == 2) {
+            const float o = __shfl_xor_sync(~0u, s, 16);
+            v[0] = lane & 16 ? o : s;
+            v[1] = lane & 16 ? s : o;
+        } else {
+            v[0] = s;
+        }
+    } else {
         constexpr int kWarps = W > 8 ? W : 8;
-        float* area = red + turn * kWarps * 4;
+        float* area = red + turn * kWarps * 2;   // [row][value][warp]
         turn ^= 1;
-        if (threadIdx.x % kWarp == 0)
-#pragma unroll
-            for (int i = 0; i < V; ++i) area[warp * 4 + i] = v[i];
+        if (V == 2 ? lane % 16 == 0 : lane == 0) area[(warp / W * V + lane / 16) * W + warp % W] = s;
         if constexpr (W >= 8) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "r"(W * 32) : "memory");
-        const float* row = area + warp / W * W * 4;
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = row[i];
+        for (int i = 0; i < V; ++i) {
+            const float* p = area + (warp / W * V + i) * W;
+            if constexpr (W == 2) {
+                const float2 q = *reinterpret_cast<const float2*>(p);
+                v[i] = q.x + q.y;
+            } else {
+                v[i] = 0.f;
 #pragma unroll
-        for (int w = 1; w < W; ++w)
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] += row[w * 4 + i];
+                for (int w = 0; w < W; w += 4) {
+                    const float4 q = *reinterpret_cast<const float4*>(p + w);
+                    v[i] += (q.x + q.y) + (q.z + q.w);
+                }
+            }
+        }
     }
 }
 
+// (s, s) and sums of pairs
+__device__ __forceinline__ float2 both(float s) { return make_float2(s, s); }
+__device__ __forceinline__ float add_up(const float2 (&v)[4])
+{
+    const float2 a = __fadd2_rn(__fadd2_rn(v[0], v[1]), __fadd2_rn(v[2], v[3]));
+    return a.x + a.y;
+}
+
+// gate(g), and gate'(g): with s the sigmoid, SIGMOID s and s (1 - s), SILU s g and s (1 + g (1 - s)).
 template <typename T>
 __device__ __forceinline__ float gate_f(float g, int act)
 {
     if (act == DLRM_GATE_NONE) return g;
-    const float s = sigmoid<T>(g);
-    return act == DLRM_GATE_SIGMOID ? s : g * s;
+    return sigmoid<T>(g) * (act == DLRM_GATE_SIGMOID ? 1.f : g);
 }
 
-// gate(g) and gate'(g)
 template <typename T>
-__device__ __forceinline__ void gate_both(float g, int act, float& v, float& slope)
+__device__ __forceinline__ void gate_both(float& g, int act, float& slope)
 {
-    v = g;
     slope = 1.f;
     if (act == DLRM_GATE_NONE) return;
-    const float s = sigmoid<T>(g);
-    v = act == DLRM_GATE_SIGMOID ? s : g * s;
-    slope = act == DLRM_GATE_SIGMOID ? s * (1.f - s) : s * fmaf(g, 1.f - s, 1.f);
+    const float s = sigmoid<T>(g), m = act == DLRM_GATE_SIGMOID ? 1.f : g;
+    g = s * m;
+    slope = s * fmaf(m, 1.f - s, act == DLRM_GATE_SIGMOID ? 0.f : 1.f);
 }
+
+// Blocks of at least 256 threads, G rows at a time.
+template <int W>
+struct Group {
+    static constexpr int kWarps = W > 8 ? W : 8, kThreads = kWarps * 32, kRows = kWarps / W;
+};
 
 // ------------------------------------------------------------------- forward
 struct NormFwd {
@@ -147,130 +236,158 @@ struct NormFwd {
     float4* stats;
 };
 
-// (mean, 1 / sqrt(mean square + eps)) of a row
-template <bool VEC, int C, int W>
-__device__ __forceinline__ float2 row_stats(const float (&f)[C][8], const int (&first)[C], const NormFwd& a, float* red,
-                                            int& turn, int warp)
+// (mean, 1 / sqrt(mean square + eps)) of a row; f becomes what is left without the mean, 0 past the end
+template <bool VEC, int W>
+__device__ __forceinline__ float2 centre(float2 (&f)[4], int first, const NormFwd& a, float* red, int& turn, int warp)
 {
-    float mean = 0.f, s[1] = {0.f};
+    float s[1], mean = 0.f;
     if (a.layer) {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[0] += f[c][i];
+        s[0] = add_up(f);
         row_sum<W>(s, red, turn, warp);
         mean = s[0] * a.inv_n;
-        s[0] = 0.f;
-    }
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = run_has<VEC>(first[c], i, a.N) ? f[c][i] - mean : 0.f;
-            s[0] = fmaf(d, d, s[0]);
+        for (int i = 0; i < 4; ++i) {
+            f[i].x = run_has<VEC>(first, 2 * i, a.N) ? f[i].x - mean : 0.f;
+            f[i].y = run_has<VEC>(first, 2 * i + 1, a.N) ? f[i].y - mean : 0.f;
         }
+    }
+    float2 q = __fmul2_rn(f[0], f[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) q = __ffma2_rn(f[i], f[i], q);
+    s[0] = q.x + q.y;
     row_sum<W>(s, red, turn, warp);
     return make_float2(mean, 1.f / sqrtf(fmaf(s[0], a.inv_n, a.eps)));
 }
 
-template <typename T, bool VEC, int C, int W>
-__global__ void __launch_bounds__(W > 8 ? W * 32 : 256)
+template <typename T, bool VEC, int W>
+__global__ void __launch_bounds__(Group<W>::kThreads, W > 8 ? 1 : 2)
 block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
 {
-    constexpr int kWarps = W > 8 ? W : 8, G = kWarps / W;   // G rows of a block at a time
-    __shared__ float red[W > 1 ? 2 * kWarps * 4 : 1];
+    constexpr int kWarps = Group<W>::kWarps, G = Group<W>::kRows;
+    using R = Ring<T, VEC, 3, Group<W>::kThreads>;
+    constexpr int kAhead = R::kAhead;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
     pdl_wait();
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-    int turn = 0, first[C];
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, N = a.N;
+    const int first = run_first<VEC>(warp % W, lane);
+    int turn = 0;
+    const R ring(smem, N, first);
+    float2 aw[4], ab[4], wp[4], bp[4];   // scale w_post, scale b_post, w_pre, b_pre
+    load_vector<VEC>(a.scale, first, N, 1.f, wp);
+    load_vector<VEC>(a.w_post, first, N, 1.f, aw);
+    load_vector<VEC>(a.b_post, first, N, 0.f, ab);
 #pragma unroll
-    for (int c = 0; c < C; ++c) first[c] = run_first<VEC>(warp % W + W * c, lane);
-    for (int64_t row = (int64_t)blockIdx.x * G + warp / W; row < a.M; row += (int64_t)gridDim.x * G) {
-        Raw8<T> ry[C], rg[C], rr[C];
-        float g1 = 1.f;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (a.y) ry[c] = load_run<T, VEC>((const T*)a.y + row * a.ldy, first[c], a.N);
-            if (a.gate_cols > 1) rg[c] = load_run<T, VEC>((const T*)a.gate + row * a.ldg, first[c], a.N);
-            if (a.res) rr[c] = load_run<T, VEC>((const T*)a.res + row * a.ldres, first[c], a.N);
+    for (int i = 0; i < 4; ++i) {
+        aw[i] = __fmul2_rn(aw[i], wp[i]);
+        ab[i] = __fmul2_rn(ab[i], wp[i]);
+    }
+    load_vector<VEC>(a.w_pre, first, N, 1.f, wp);
+    load_vector<VEC>(a.b_pre, first, N, 0.f, bp);
+    const int64_t step = (int64_t)gridDim.x * G;
+    const int64_t row0 = (int64_t)blockIdx.x * G + warp / W;
+    auto fetch = [&](int stage, int64_t row) {
+        if (row < a.M) {
+            if (a.y) ring.fetch(stage, 0, (const T*)a.y + row * a.ldy);
+            if (a.gate_cols > 1) ring.fetch(stage, 1, (const T*)a.gate + row * a.ldg);
+            if (a.res) ring.fetch(stage, 2, (const T*)a.res + row * a.ldres);
         }
-        if (a.gate_cols == 1) g1 = gate_f<T>(to_f32(__ldg((const T*)a.gate + row * a.ldg)), a.gate_act);
-        float r[C][8];
+        R::commit();
+    };
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (a.res) widen8<T>(rr[c], r[c]);
-            else
-#pragma unroll
-                for (int i = 0; i < 8; ++i) r[c][i] = 0.f;
-        }
+    for (int k = 0; k < kAhead - 1; ++k) fetch(k, row0 + k * step);
+    int stage = 0;
+    for (int64_t row = row0; row < a.M; row += step) {
+        fetch(stage == 0 ? kAhead - 1 : stage - 1, row + (kAhead - 1) * step);
+        R::wait();
         float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 r[4];
+        ring.read(stage, 2, r);
         if (a.y) {
-            float f[C][8];
+            float2 f[4], g[4];
+            ring.read(stage, 0, f);
+            if (a.gate_cols > 1) {
+                ring.read(stage, 1, g);
+                if (a.gate_act != DLRM_GATE_NONE)
 #pragma unroll
-            for (int c = 0; c < C; ++c) widen8<T>(ry[c], f[c]);
-            const float2 s = row_stats<VEC, C, W>(f, first, a, red, turn, warp);
+                    for (int i = 0; i < 4; ++i) {
+                        g[i].x = gate_f<T>(g[i].x, a.gate_act);
+                        g[i].y = gate_f<T>(g[i].y, a.gate_act);
+                    }
+            } else {
+                const float g1 = a.gate_cols == 1 ? gate_f<T>(to_f32(__ldg((const T*)a.gate + row * a.ldg)), a.gate_act) : 1.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) g[i] = both(g1);
+            }
+            const float2 s = centre<VEC, W>(f, first, a, red, turn, warp);
             st.x = s.x;
             st.y = s.y;
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float w[8], b[8], sc[8], g[8];
-                load_vector<VEC>(a.w_post, first[c], a.N, 1.f, w);
-                load_vector<VEC>(a.b_post, first[c], a.N, 0.f, b);
-                load_vector<VEC>(a.scale, first[c], a.N, 1.f, sc);
-                if (a.gate_cols > 1) widen8<T>(rg[c], g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float u = fmaf((f[c][i] - s.x) * s.y, w[i], b[i]);
-                    u *= a.gate_cols > 1 ? gate_f<T>(g[i], a.gate_act) : g1;
-                    r[c][i] = fmaf(sc[i], u, r[c][i]);
-                }
-                store_run<T, VEC>((T*)a.r + row * a.ldr, first[c], a.N, r[c]);
+            for (int i = 0; i < 4; ++i) {
+                const float2 u = __ffma2_rn(__fmul2_rn(f[i], both(s.y)), aw[i], ab[i]);   // scale u
+                r[i] = __ffma2_rn(u, g[i], r[i]);
             }
+            store_run<T, VEC>((T*)a.r + row * a.ldr, first, N, r);
         }
         if (a.h) {
-            if (a.y)   // columns past the row's end hold what the vectors' fill made of them
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (!run_has<VEC>(first[c], i, a.N)) r[c][i] = 0.f;
-            const float2 s = row_stats<VEC, C, W>(r, first, a, red, turn, warp);
+            const float2 s = centre<VEC, W>(r, first, a, red, turn, warp);
             st.z = s.x;
             st.w = s.y;
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float w[8], b[8], o[8];
-                load_vector<VEC>(a.w_pre, first[c], a.N, 1.f, w);
-                load_vector<VEC>(a.b_pre, first[c], a.N, 0.f, b);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = fmaf((r[c][i] - s.x) * s.y, w[i], b[i]);
-                store_run<T, VEC>((T*)a.h + row * a.ldh, first[c], a.N, o);
-            }
+            for (int i = 0; i < 4; ++i) r[i] = __ffma2_rn(__fmul2_rn(r[i], both(s.y)), wp[i], bp[i]);
+            store_run<T, VEC>((T*)a.h + row * a.ldh, first, N, r);
         }
         if (a.stats && warp % W == 0 && lane == 0) a.stats[row] = st;
+        stage = stage == kAhead - 1 ? 0 : stage + 1;
     }
+}
+
+// Warps of a row, a power of two, and the blocks of a call.
+int norm_warps(int N)
+{
+    int w = 1;
+    while (w * 256 < N) w *= 2;
+    return w;
+}
+
+int norm_blocks(int M, int N)
+{
+    const int w = norm_warps(N), rows = w > 8 ? 1 : 8 / w;
+    const int64_t want = ((int64_t)M + rows - 1) / rows, most = (int64_t)num_sms() * (w > 8 ? 1 : 2);
+    return (int)(want < most ? want : most);
+}
+
+// fn(the warps of a row as a constant)
+template <typename Fn>
+dlrm_status with_warps(int N, Fn&& fn)
+{
+    using std::integral_constant;
+    switch (norm_warps(N)) {
+    case 1: return fn(integral_constant<int, 1>());
+    case 2: return fn(integral_constant<int, 2>());
+    case 4: return fn(integral_constant<int, 4>());
+    case 8: return fn(integral_constant<int, 8>());
+    case 16: return fn(integral_constant<int, 16>());
+    default: return fn(integral_constant<int, 32>());
+    }
+}
+
+template <typename K, typename A>
+dlrm_status launch_norm(const char* what, K kern, const A& a, int threads, size_t smem, cudaStream_t st)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return fail(DLRM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+    return check_launch_pdl(launch_pdl(kern, dim3(norm_blocks(a.M, a.N)), dim3(threads), smem, st, a), what);
 }
 
 template <typename T, bool VEC>
 dlrm_status launch_fwd(const NormFwd& a, cudaStream_t st)
 {
-    auto go = [&](auto c, auto w) {
-        constexpr int C = decltype(c)::value, W = decltype(w)::value, kWarps = W > 8 ? W : 8;
-        const int64_t want = ((int64_t)a.M + kWarps / W - 1) / (kWarps / W), most = (int64_t)num_sms() * 8;
-        return check_launch_pdl(launch_pdl(block_norm_fwd_kernel<T, VEC, C, W>, dim3((unsigned)(want < most ? want : most)),
-                                           dim3(kWarps * 32), 0, st, a),
-                                "block_norm_fwd_kernel");
-    };
-    using std::integral_constant;
-    constexpr int L = sizeof(T) == 4 ? 2 : 4;   // runs a lane: what three tensors' words leave registers for
-    constexpr integral_constant<int, 1> one;
-    constexpr integral_constant<int, 2> two;
-    constexpr integral_constant<int, L> most;
-    if (a.N <= 256) return go(one, one);
-    if (a.N <= 512) return go(two, one);
-    if (a.N <= 1024) return go(most, integral_constant<int, 4 / L>());
-    if (a.N <= 2048) return go(most, integral_constant<int, 8 / L>());
-    if (a.N <= 4096) return go(most, integral_constant<int, 16 / L>());
-    return go(most, integral_constant<int, 32 / L>());
+    return with_warps(a.N, [&](auto w) {
+        constexpr int W = decltype(w)::value, kThreads = Group<W>::kThreads;
+        return launch_norm("block_norm_fwd_kernel", block_norm_fwd_kernel<T, VEC, W>, a, kThreads,
+                           Ring<T, VEC, 3, kThreads>::kBytes, st);
+    });
 }
 
 // ------------------------------------------------------------------ backward
@@ -288,137 +405,171 @@ struct NormBwd {
     int64_t Np;
 };
 
-template <typename T>
-struct BwdRow {
-    Raw8<T> gr, gh, y, gate, r;
-    float4 st;
-    float g1;
-};
-
-template <typename T, bool VEC, bool POST, bool PRE>
-__device__ __forceinline__ void load_bwd(BwdRow<T>& q, const NormBwd& a, int64_t row, int first)
-{
-    if (PRE) {
-        q.gh = load_run<T, VEC>((const T*)a.gh + row * a.ldgh, first, a.N);
-        q.r = load_run<T, VEC>((const T*)a.r + row * a.ldr, first, a.N);
-    }
-    if (a.gr) q.gr = load_run<T, VEC>((const T*)a.gr + row * a.ldgr, first, a.N);
-    if (POST) {
-        q.y = load_run<T, VEC>((const T*)a.y + row * a.ldy, first, a.N);
-        if (a.gate_cols > 1) q.gate = load_run<T, VEC>((const T*)a.gate + row * a.ldg, first, a.N);
-        q.g1 = a.gate_cols == 1 ? to_f32(__ldg((const T*)a.gate + row * a.ldg)) : 1.f;
-    }
-    q.st = __ldg(a.stats + row);
-}
-
 template <typename T, bool VEC, int W, bool POST, bool PRE>
-__global__ void __launch_bounds__(W > 8 ? W * 32 : 256, W > 8 ? 1 : 2)
+__global__ void __launch_bounds__(Group<W>::kThreads, W > 8 ? 1 : 2)
 block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
 {
-    constexpr int kWarps = W > 8 ? W : 8, G = kWarps / W;
-    __shared__ float red[W > 1 ? 2 * kWarps * 4 : 1];
-    __shared__ float tile[G > 1 ? 8 * 256 : 1];
+    constexpr int kWarps = Group<W>::kWarps, G = Group<W>::kRows;
+    constexpr int kGr = 0, kGh = 1, kR = 2, kY = PRE ? 3 : 1, kGate = kY + 1;   // slots
+    using Rg = Ring<T, VEC, POST && PRE ? 5 : 3, Group<W>::kThreads>;
+    constexpr int kAhead = Rg::kAhead;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
     pdl_wait();
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-    const int first = run_first<VEC>(warp % W, lane), N = a.N;
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, N = a.N;
+    const int first = run_first<VEC>(warp % W, lane);
     int turn = 0;
-    // scale w_post, scale b_post, w_pre; 0 past the row's end
-    float aw[8], ab[8], wp[8];
-    {
-        float sc[8];
-        load_vector<VEC>(a.w_post, first, N, 1.f, aw);
-        load_vector<VEC>(a.b_post, first, N, 0.f, ab);
-        load_vector<VEC>(a.scale, first, N, 1.f, sc);
-        load_vector<VEC>(a.w_pre, first, N, 1.f, wp);
+    const Rg ring(smem, N, first);
+    float2 aw[4], ab[4], wp[4];   // scale w_post, scale b_post, w_pre; 0 past the row's end
+    load_vector<VEC>(a.scale, first, N, 1.f, wp);
+    load_vector<VEC>(a.w_post, first, N, 1.f, aw);
+    load_vector<VEC>(a.b_post, first, N, 0.f, ab);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool in = run_has<VEC>(first, i, N);
-            aw[i] = in ? aw[i] * sc[i] : 0.f;
-            ab[i] = in ? ab[i] * sc[i] : 0.f;
-            wp[i] = in ? wp[i] : 0.f;
-        }
+    for (int i = 0; i < 4; ++i) {
+        aw[i] = __fmul2_rn(aw[i], wp[i]);
+        ab[i] = __fmul2_rn(ab[i], wp[i]);
     }
-    float sum[4][8] = {};
-    const int64_t step = (int64_t)gridDim.x * G;
-    int64_t row = (int64_t)blockIdx.x * G + warp / W;
-    BwdRow<T> q;
-    if (row < a.M) load_bwd<T, VEC, POST, PRE>(q, a, row, first);
-    for (; row < a.M; row += step) {
-        BwdRow<T> next;
-        if (row + step < a.M) load_bwd<T, VEC, POST, PRE>(next, a, row + step, first);
-        float dr[8];
-        if (a.gr) widen8<T>(q.gr, dr);
-        else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dr[i] = 0.f;
-        if (PRE) {
-            float d[8], x[8], c[2] = {0.f, 0.f};
-            widen8<T>(q.gh, d);
-            widen8<T>(q.r, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = (x[i] - q.st.z) * q.st.w;
-                sum[2][i] = fmaf(d[i], x[i], sum[2][i]);
-                sum[3][i] += d[i];
-                d[i] *= wp[i];
-                c[0] = fmaf(d[i], x[i], c[0]);
-                c[1] += d[i];
+    load_vector<VEC>(a.w_pre, first, N, 1.f, wp);
+    float2 sum[4][4] = {};
+    const int64_t step = (int64_t)gridDim.x * G, row0 = (int64_t)blockIdx.x * G + warp / W;
+    auto fetch = [&](int stage, int64_t row) {
+        if (row < a.M) {
+            if (a.gr) ring.fetch(stage, kGr, (const T*)a.gr + row * a.ldgr);
+            if (PRE) {
+                ring.fetch(stage, kGh, (const T*)a.gh + row * a.ldgh);
+                ring.fetch(stage, kR, (const T*)a.r + row * a.ldr);
             }
-            row_sum<W>(c, red, turn, warp);
-            c[0] *= a.inv_n;
-            c[1] = a.layer ? c[1] * a.inv_n : 0.f;
+            if (POST) {
+                ring.fetch(stage, kY, (const T*)a.y + row * a.ldy);
+                if (a.gate_cols > 1) ring.fetch(stage, kGate, (const T*)a.gate + row * a.ldg);
+            }
+        }
+        Rg::commit();
+    };
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dr[i] = fmaf(d[i] - c[1] - x[i] * c[0], q.st.w, dr[i]);
+    for (int k = 0; k < kAhead - 1; ++k) fetch(k, row0 + k * step);
+    // what a row has one of is loaded a row ahead
+    float4 st_next = row0 < a.M ? __ldg(a.stats + row0) : make_float4(0, 0, 0, 0);
+    float g_next = a.gate_cols == 1 && row0 < a.M ? to_f32(__ldg((const T*)a.gate + row0 * a.ldg)) : 1.f;
+    int stage = 0;
+    for (int64_t row = row0; row < a.M; row += step) {
+        fetch(stage == 0 ? kAhead - 1 : stage - 1, row + (kAhead - 1) * step);
+        const float4 st = st_next;
+        float g1 = g_next, slope1 = 1.f;
+        if (row + step < a.M) {
+            st_next = __ldg(a.stats + row + step);
+            if (a.gate_cols == 1) g_next = to_f32(__ldg((const T*)a.gate + (row + step) * a.ldg));
+        }
+        Rg::wait();
+        float2 dr[4];
+        ring.read(stage, kGr, dr);
+        if (PRE) {
+            float2 d[4], x[4], p, q;
+            ring.read(stage, kGh, d);
+            ring.read(stage, kR, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = __fmul2_rn(__fadd2_rn(x[i], both(-st.z)), both(st.w));
+                sum[2][i] = __ffma2_rn(d[i], x[i], sum[2][i]);
+                sum[3][i] = __fadd2_rn(sum[3][i], d[i]);
+                d[i] = __fmul2_rn(d[i], wp[i]);
+                p = i ? __ffma2_rn(d[i], x[i], p) : __fmul2_rn(d[i], x[i]);
+                q = i ? __fadd2_rn(d[i], q) : d[i];
+            }
+            float c0, c1 = 0.f;
+            if (a.layer) {
+                float c[2] = {p.x + p.y, q.x + q.y};
+                row_sum<W>(c, red, turn, warp);
+                c0 = c[0] * -a.inv_n;
+                c1 = c[1] * -a.inv_n;
+            } else {
+                float c[1] = {p.x + p.y};
+                row_sum<W>(c, red, turn, warp);
+                c0 = c[0] * -a.inv_n;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dr[i] = __ffma2_rn(__ffma2_rn(x[i], both(c0), __fadd2_rn(d[i], both(c1))), both(st.w), dr[i]);
         }
         if (a.gres) store_run<T, VEC>((T*)a.gres + row * a.ldgres, first, N, dr);
         if (POST) {
-            float x[8], c[3] = {0.f, 0.f, 0.f}, dg[8], g1 = q.g1, slope1 = 1.f;
-            widen8<T>(q.y, x);
-            if (a.gate_cols > 1) widen8<T>(q.gate, dg);
-            else if (a.gate_cols == 1) gate_both<T>(q.g1, a.gate_act, g1, slope1);
+            float2 x[4], g[4], k[4], p, q, t = both(0.f);
+            ring.read(stage, kY, x);
+            if (a.gate_cols > 1) {
+                ring.read(stage, kGate, g);
+                if (a.gate_act != DLRM_GATE_NONE)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = (x[i] - q.st.x) * q.st.y;
-                float g = g1, slope = 1.f;
-                if (a.gate_cols > 1) gate_both<T>(dg[i], a.gate_act, g, slope);
-                const float du = dr[i] * g, su = fmaf(x[i], aw[i], ab[i]);   // su: scale u
-                dg[i] = dr[i] * su * slope;
-                c[2] = fmaf(dr[i], su, c[2]);
-                sum[0][i] = fmaf(du, x[i], sum[0][i]);
-                sum[1][i] += du;
-                dr[i] = du * aw[i];
-                c[0] = fmaf(dr[i], x[i], c[0]);
-                c[1] += dr[i];
+                    for (int i = 0; i < 4; ++i) {
+                        gate_both<T>(g[i].x, a.gate_act, k[i].x);
+                        gate_both<T>(g[i].y, a.gate_act, k[i].y);
+                    }
+                else
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) k[i] = both(1.f);
+            } else {
+                if (a.gate_cols == 1) gate_both<T>(g1, a.gate_act, slope1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    g[i] = both(g1);
+                    k[i] = both(1.f);
+                }
             }
-            row_sum<W>(c, red, turn, warp);
-            if (a.gg) {
-                if (a.gate_cols > 1) store_run<T, VEC>((T*)a.gg + row * a.ldgg, first, N, dg);
-                else if (warp % W == 0 && lane == 0) ((T*)a.gg)[row * a.ldgg] = from_f32<T>(c[2] * slope1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = __fmul2_rn(__fadd2_rn(x[i], both(-st.x)), both(st.y));
+                const float2 su = __ffma2_rn(x[i], aw[i], ab[i]);   // scale u
+                t = __ffma2_rn(dr[i], su, t);
+                k[i] = __fmul2_rn(__fmul2_rn(dr[i], su), k[i]);
+                dr[i] = __fmul2_rn(dr[i], g[i]);
+                sum[0][i] = __ffma2_rn(dr[i], x[i], sum[0][i]);
+                sum[1][i] = __fadd2_rn(sum[1][i], dr[i]);
+                dr[i] = __fmul2_rn(dr[i], aw[i]);
+                p = i ? __ffma2_rn(dr[i], x[i], p) : __fmul2_rn(dr[i], x[i]);
+                q = i ? __fadd2_rn(dr[i], q) : dr[i];
+            }
+            if (a.gg && a.gate_cols > 1) store_run<T, VEC>((T*)a.gg + row * a.ldgg, first, N, k);
+            float c0, c1 = 0.f;
+            if (a.layer) {
+                float c[2] = {p.x + p.y, q.x + q.y};
+                row_sum<W>(c, red, turn, warp);
+                c0 = c[0] * -a.inv_n;
+                c1 = c[1] * -a.inv_n;
+            } else {
+                float c[1] = {p.x + p.y};
+                row_sum<W>(c, red, turn, warp);
+                c0 = c[0] * -a.inv_n;
+            }
+            if (a.gg && a.gate_cols == 1) {
+                float c[1] = {t.x + t.y};
+                row_sum<W>(c, red, turn, warp);
+                if (warp % W == 0 && lane == 0) ((T*)a.gg)[row * a.ldgg] = from_f32<T>(c[0] * slope1);
             }
             if (a.gy) {
-                c[0] *= a.inv_n;
-                c[1] = a.layer ? c[1] * a.inv_n : 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dr[i] = (dr[i] - c[1] - x[i] * c[0]) * q.st.y;
+                for (int i = 0; i < 4; ++i)
+                    dr[i] = __fmul2_rn(__ffma2_rn(x[i], both(c0), __fadd2_rn(dr[i], both(c1))), both(st.y));
                 store_run<T, VEC>((T*)a.gy + row * a.ldgy, first, N, dr);
             }
         }
-        q = next;
+        stage = stage == kAhead - 1 ? 0 : stage + 1;
     }
     if (!a.partial) return;
+    // the rows' sums of a block: its groups one after another, by way of the ring's memory
+    float2* const tile = reinterpret_cast<float2*>(smem);
+    asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         if (s < 2 ? !POST : !PRE) continue;
         if constexpr (G > 1) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) tile[i * 256 + threadIdx.x] = sum[s][i];
+            for (int i = 0; i < 4; ++i) tile[i * 256 + threadIdx.x] = sum[s][i];
             __syncthreads();
             if (warp < W) {
 #pragma unroll
                 for (int g = 1; g < G; ++g)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) sum[s][i] += tile[i * 256 + g * W * 32 + threadIdx.x];
+                    for (int i = 0; i < 4; ++i) sum[s][i] = __fadd2_rn(sum[s][i], tile[i * 256 + g * W * 32 + threadIdx.x]);
             }
         }
         if (warp < W) store_run<float, VEC>(a.partial + ((int64_t)blockIdx.x * 4 + s) * a.Np, first, N, sum[s]);
@@ -471,39 +622,14 @@ __global__ void __launch_bounds__(1024) block_norm_sum_kernel(const __grid_const
     }
 }
 
-// Warps of a row, a power of two, and the blocks of the backward.
-int bwd_warps(int N)
-{
-    int w = 1;
-    while (w * 256 < N) w *= 2;
-    return w;
-}
-
-int bwd_blocks(int M, int N)
-{
-    const int w = bwd_warps(N), rows = w > 8 ? 1 : 8 / w;
-    const int64_t want = ((int64_t)M + rows - 1) / rows, most = (int64_t)num_sms() * (w > 8 ? 1 : 2);
-    return (int)(want < most ? want : most);
-}
-
 template <typename T, bool VEC, bool POST, bool PRE>
 dlrm_status launch_bwd(const NormBwd& a, cudaStream_t st)
 {
-    auto go = [&](auto w) {
-        constexpr int W = decltype(w)::value;
-        return check_launch_pdl(launch_pdl(block_norm_bwd_kernel<T, VEC, W, POST, PRE>, dim3(bwd_blocks(a.M, a.N)),
-                                           dim3(W > 8 ? W * 32 : 256), 0, st, a),
-                                "block_norm_bwd_kernel");
-    };
-    using std::integral_constant;
-    switch (bwd_warps(a.N)) {
-    case 1: return go(integral_constant<int, 1>());
-    case 2: return go(integral_constant<int, 2>());
-    case 4: return go(integral_constant<int, 4>());
-    case 8: return go(integral_constant<int, 8>());
-    case 16: return go(integral_constant<int, 16>());
-    default: return go(integral_constant<int, 32>());
-    }
+    return with_warps(a.N, [&](auto w) {
+        constexpr int W = decltype(w)::value, kThreads = Group<W>::kThreads;
+        return launch_norm("block_norm_bwd_kernel", block_norm_bwd_kernel<T, VEC, W, POST, PRE>, a, kThreads,
+                           Ring<T, VEC, POST && PRE ? 5 : 3, kThreads>::kBytes, st);
+    });
 }
 
 // ------------------------------------------------------------------- checks
@@ -583,7 +709,7 @@ extern "C" dlrm_status dlrm_block_norm_fwd(const void* d_y, int64_t ldy, const v
 extern "C" size_t dlrm_block_norm_bwd_workspace_size(int M, int N)
 {
     if (M < 1 || N < 1 || M > kMaxSize || N > DLRM_BLOCK_MAX_WIDTH) return 0;
-    return dlrm_ws_align((size_t)bwd_blocks(M, N) * 4 * ((N + 7) / 8 * 8) * 4);
+    return dlrm_ws_align((size_t)norm_blocks(M, N) * 4 * ((N + 7) / 8 * 8) * 4);
 }
 
 extern "C" dlrm_status dlrm_block_norm_bwd(
@@ -662,7 +788,7 @@ extern "C" dlrm_status dlrm_block_norm_bwd(
         return vec ? go(std::true_type()) : go(std::false_type());
     });
     if (s != DLRM_OK || !sums) return s;
-    const NormSum q = {a.partial, Np, bwd_blocks(M, N), N, d_w_post, d_b_post, d_scale,
+    const NormSum q = {a.partial, Np, norm_blocks(M, N), N, d_w_post, d_b_post, d_scale,
                        d_grad_w_post, d_grad_b_post, d_grad_scale, d_grad_w_pre, d_grad_b_pre};
     return check_launch_pdl(launch_pdl(block_norm_sum_kernel, dim3((N + 31) / 32, 2), dim3(1024), 0, st, q),
                             "block_norm_sum_kernel");
