@@ -16,8 +16,9 @@
 //   backward   a lane also adds up its columns' sums over rows.  Blocks' sums go to `partial`
 //              and block_norm_sum_kernel adds them in order
 //
-// Nothing here depends on which column a lane has, so rows off the 16-byte grid give a
-// lane every 32nd column instead of eight in a row: whole sectors a load, whatever the base.
+// Nothing here depends on which columns a lane has.  On the 16-byte grid they are eight
+// neighbours.  Off it a warp copies the aligned 16-byte words that hold its 256 columns and a
+// lane has every 32nd column, or pair of them, which shared memory gives without conflicts.
 #include "dense_ops.cuh"
 #include "dlrm_block.h"
 
@@ -25,44 +26,34 @@ namespace dlrm {
 namespace {
 
 // ------------------------------------------------------------- runs of a row
-// A lane's run c of a row: columns first .. first + 7, or first, first + 32, ..
-template <bool VEC>
-__device__ __forceinline__ int run_first(int chunk, int lane)
+// A lane's run of a row: its first column and the others, ES the element's size.
+template <bool VEC, int ES>
+__device__ __forceinline__ int run_first(int warp, int lane)
 {
-    return chunk * 256 + (VEC ? lane * 8 : lane);
+    return warp * 256 + lane * (VEC ? 8 : ES == 2 ? 2 : 1);
 }
 
-template <bool VEC>
-__device__ __forceinline__ bool run_has(int first, int i, int N)
+template <bool VEC, int ES>
+__device__ __forceinline__ int run_col(int first, int i)
 {
-    return VEC ? first < N : first + 32 * i < N;
+    return first + (VEC ? i : ES == 2 ? i / 2 * 64 + i % 2 : i * 32);
 }
 
-// The run's columns of a row, 0 past its end.
-template <typename T, bool VEC>
-__device__ __forceinline__ Raw8<T> load_run(const T* row, int first, int N)
+// The rows to come: kAhead rows of NT tensors, three where the blocks that share an SM (two of
+// 256 threads, one of more) have the memory.  Columns past the row's end are 0.
+template <int STAGE, int THREADS>
+constexpr int kRowsAhead = (THREADS > 256 ? 224 << 10 : 110 << 10) / STAGE < 3 ? (THREADS > 256 ? 224 << 10 : 110 << 10) / STAGE : 3;
+
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, uint32_t bytes)   // the rest of the word becomes 0
 {
-    Raw8<T> r;
-    if constexpr (VEC) {
-        if (first < N) return load8<T, true>(row + first, 8);
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.w[i] = make_uint4(0, 0, 0, 0);
-    } else {
-        T e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = first + 32 * i < N ? __ldg(row + first + 32 * i) : from_f32<T>(0.f);
-        memcpy(&r, e, sizeof(r));
-    }
-    return r;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 
-// A thread's part of the rows to come: kAhead rows of NT tensors, three where the blocks that
-// share an SM (two of 256 threads, one of more) have the memory.  Where copies cannot be
-// asynchronous (2-byte elements off the grid) a row is loaded to registers and stored.
+// On the grid: each thread copies and reads its own eight columns.
 template <typename T, bool VEC, int NT, int THREADS>
 struct Ring {
     static constexpr int kWords = sizeof(T) / 2, kSlot = kWords * THREADS * 16, kStage = NT * kSlot;
-    static constexpr int kMost = (THREADS > 256 ? 224 << 10 : 110 << 10) / kStage, kAhead = kMost < 3 ? kMost : 3;
+    static constexpr int kAhead = kRowsAhead<kStage, THREADS>;
     static_assert(kAhead >= 1, "a row fits");
     static constexpr size_t kBytes = (size_t)kAhead * kStage;
     uint8_t* mine;    // word 0 of slot 0 of stage 0
@@ -72,35 +63,24 @@ struct Ring {
     __device__ Ring(uint8_t* smem, int n, int f) : mine(smem + threadIdx.x * 16), N(n), first(f)
     {
         at = (uint32_t)__cvta_generic_to_shared(mine);
-        for (int i = 0; i < kAhead * NT * kWords; ++i)   // columns past the end stay 0
+        for (int i = 0; i < kAhead * NT * kWords; ++i)
             *reinterpret_cast<uint4*>(mine + i * THREADS * 16) = make_uint4(0, 0, 0, 0);
     }
-    // Starts the copy of a row's run to a slot.
-    __device__ __forceinline__ void fetch(int stage, int slot, const T* row) const
+    // Starts the copy of the row at m + off to a slot.
+    __device__ __forceinline__ void fetch(int stage, int slot, const T* m, int64_t off) const
     {
+        const T* row = m + off;
         const uint32_t to = at + stage * kStage + slot * kSlot;
-        if constexpr (VEC) {
-            if (first < N)
+        if (first < N)
 #pragma unroll
-                for (int i = 0; i < kWords; ++i)
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * THREADS * 16),
-                                 "l"(reinterpret_cast<const uint4*>(row + first) + i)
-                                 : "memory");
-        } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (first + 32 * i < N)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + i / 4 * THREADS * 16 + i % 4 * 4),
-                                 "l"(row + first + 32 * i)
-                                 : "memory");
-        } else {
-            *reinterpret_cast<uint4*>(mine + stage * kStage + slot * kSlot) = load_run<T, VEC>(row, first, N).w[0];
-        }
+            for (int i = 0; i < kWords; ++i)
+                copy16(to + i * THREADS * 16, reinterpret_cast<const uint4*>(row + first) + i, 16);
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     // The oldest row's copies are complete.
     static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory"); }
-    __device__ __forceinline__ void read(int stage, int slot, float2 (&f)[4]) const
+    static __device__ __forceinline__ void done() {}
+    __device__ __forceinline__ void read(int stage, int slot, const T*, float2 (&f)[4]) const
     {
         Raw8<T> r;
 #pragma unroll
@@ -113,34 +93,144 @@ struct Ring {
     }
 };
 
+// Off the grid: a warp's 256 columns lie in 16 ES + 1 aligned words at most, which its lanes copy.
+// The last word ends with the row; one that begins before the matrix is put together from its elements.
+template <typename T, int NT, int THREADS>
+struct Ring<T, false, NT, THREADS> {
+    static constexpr int kWords = 16 * sizeof(T) + 1, kSlot = THREADS / kWarp * kWords * 16, kStage = NT * kSlot;
+    static constexpr int kAhead = kRowsAhead<kStage, THREADS>;
+    static_assert(kAhead >= 1, "a row fits");
+    static constexpr size_t kBytes = (size_t)kAhead * kStage;
+    uint8_t* mine;    // the warp's word 0
+    uint32_t at;
+    int N, first, from, bytes;   // from: the warp's first column; bytes of its columns, 0 or less: none
+
+    __device__ Ring(uint8_t* smem, int n, int f) : mine(smem + threadIdx.x / kWarp * kWords * 16), N(n), first(f)
+    {
+        at = (uint32_t)__cvta_generic_to_shared(mine);
+        from = first / 256 * 256;
+        bytes = min(256, N - from) * (int)sizeof(T);
+        // columns past the end: what lies behind the last word, and all of a warp without columns
+        const int lane = threadIdx.x % kWarp;
+        for (int s = 0; s < kAhead * NT; ++s)
+            for (int w = lane; w < kWords; w += kWarp)
+                *reinterpret_cast<uint4*>(mine + s * kSlot + w * 16) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+    }
+    __device__ __forceinline__ void fetch(int stage, int slot, const T* m, int64_t at_row) const
+    {
+        if (bytes <= 0) return;
+        const T* row = m + at_row;
+        const uint32_t to = at + stage * kStage + slot * kSlot;
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(row + from);
+        const int off = (int)((uintptr_t)p & 15), end = off + bytes;
+        const int lane = threadIdx.x % kWarp;
+#pragma unroll
+        for (int i = 0; i < (kWords + kWarp - 1) / kWarp; ++i) {
+            const int w = lane + kWarp * i;
+            if (w < kWords && w * 16 < end) {
+                if (w > 0 || (at_row + from) * (int)sizeof(T) >= off) {
+                    copy16(to + w * 16, p - off + w * 16, min(16, end - w * 16));
+                } else {
+                    T* word = reinterpret_cast<T*>(mine + stage * kStage + slot * kSlot);
+                    for (int e = off / (int)sizeof(T); e < min(16, end) / (int)sizeof(T); ++e)
+                        word[e] = __ldg(row + e - off / (int)sizeof(T));
+                }
+            }
+        }
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    static __device__ __forceinline__ void wait()
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        __syncwarp();   // the other lanes' copies too
+    }
+    static __device__ __forceinline__ void done() { __syncwarp(); }   // all lanes have read the row
+    __device__ __forceinline__ void read(int stage, int slot, const T* row, float2 (&f)[4]) const
+    {
+        const uint8_t* p = mine + stage * kStage + slot * kSlot + ((uintptr_t)(row + from) & 15) +
+                           (first - from) * (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                f[i] = make_float2(*reinterpret_cast<const float*>(p + 256 * i), *reinterpret_cast<const float*>(p + 256 * i + 128));
+            } else {
+                f[i] = make_float2(to_f32(*reinterpret_cast<const T*>(p + 128 * i)), to_f32(*reinterpret_cast<const T*>(p + 128 * i + 2)));
+            }
+        }
+        // what lies behind the row in its last word is 0; a stage's later words may be an earlier row's
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (run_col<false, sizeof(T)>(first, 2 * i) >= N) f[i].x = 0.f;
+            if (run_col<false, sizeof(T)>(first, 2 * i + 1) >= N) f[i].y = 0.f;
+        }
+    }
+};
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void store_run(T* row, int first, int N, const float2 (&v)[4])
 {
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = v[i].x;
-        f[2 * i + 1] = v[i].y;
-    }
     if constexpr (VEC) {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = v[i].x;
+            f[2 * i + 1] = v[i].y;
+        }
         if (first < N) store8<T, true>(row + first, 8, f);
+    } else if constexpr (sizeof(T) == 2) {
+        const bool words = ((uintptr_t)row & 3) == 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = run_col<false, 2>(first, 2 * i);
+            const T a = from_f32<T>(v[i].x), b = from_f32<T>(v[i].y);
+            if (words && c + 1 < N) {
+                uint16_t x, y;
+                memcpy(&x, &a, 2);
+                memcpy(&y, &b, 2);
+                *reinterpret_cast<uint32_t*>(row + c) = (uint32_t)y << 16 | x;
+            } else {
+                if (c < N) row[c] = a;
+                if (c + 1 < N) row[c + 1] = b;
+            }
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (first + 32 * i < N) row[first + 32 * i] = from_f32<T>(f[i]);
+        for (int i = 0; i < 4; ++i) {
+            const int c = run_col<false, 4>(first, 2 * i), d = run_col<false, 4>(first, 2 * i + 1);
+            if (c < N) row[c] = v[i].x;
+            if (d < N) row[d] = v[i].y;
+        }
     }
 }
 
-// The run's part of a vector: `fill` everywhere where there is none, 0 past the row's end.
-template <bool VEC>
+// The run's part of a vector: `fill` everywhere where there is none, 0 past the row's end; and of an fp32 output.
+template <bool VEC, int ES>
 __device__ __forceinline__ void load_vector(const float* p, int first, int N, float fill, float2 (&f)[4])
 {
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = !run_has<VEC>(first, i, N) ? 0.f : p ? __ldg(p + first + (VEC ? i : 32 * i)) : fill;
+    for (int i = 0; i < 8; ++i) {
+        const int c = run_col<VEC, ES>(first, i);
+        v[i] = c >= N ? 0.f : p ? __ldg(p + c) : fill;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[i] = make_float2(v[2 * i], v[2 * i + 1]);
+}
+
+template <bool VEC, int ES>
+__device__ __forceinline__ void store_vector(float* p, int first, int N, const float2 (&v)[4])
+{
+    if constexpr (VEC) {
+        store_run<float, true>(p, first, N, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = run_col<VEC, ES>(first, 2 * i), d = run_col<VEC, ES>(first, 2 * i + 1);
+            if (c < N) p[c] = v[i].x;
+            if (d < N) p[d] = v[i].y;
+        }
+    }
 }
 
 // Sums of V (1 or 2) values over the W warps of a row, the same in all of them.  red: two areas
@@ -237,7 +327,7 @@ struct NormFwd {
 };
 
 // (mean, 1 / sqrt(mean square + eps)) of a row; f becomes what is left without the mean, 0 past the end
-template <bool VEC, int W>
+template <bool VEC, int ES, int W>
 __device__ __forceinline__ float2 centre(float2 (&f)[4], int first, const NormFwd& a, float* red, int& turn, int warp)
 {
     float s[1], mean = 0.f;
@@ -247,8 +337,8 @@ __device__ __forceinline__ float2 centre(float2 (&f)[4], int first, const NormFw
         mean = s[0] * a.inv_n;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f[i].x = run_has<VEC>(first, 2 * i, a.N) ? f[i].x - mean : 0.f;
-            f[i].y = run_has<VEC>(first, 2 * i + 1, a.N) ? f[i].y - mean : 0.f;
+            f[i].x = run_col<VEC, ES>(first, 2 * i) < a.N ? f[i].x - mean : 0.f;
+            f[i].y = run_col<VEC, ES>(first, 2 * i + 1) < a.N ? f[i].y - mean : 0.f;
         }
     }
     float2 q = __fmul2_rn(f[0], f[0]);
@@ -270,27 +360,27 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
     __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
     pdl_wait();
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, N = a.N;
-    const int first = run_first<VEC>(warp % W, lane);
+    const int first = run_first<VEC, sizeof(T)>(warp % W, lane);
     int turn = 0;
     const R ring(smem, N, first);
     float2 aw[4], ab[4], wp[4], bp[4];   // scale w_post, scale b_post, w_pre, b_pre
-    load_vector<VEC>(a.scale, first, N, 1.f, wp);
-    load_vector<VEC>(a.w_post, first, N, 1.f, aw);
-    load_vector<VEC>(a.b_post, first, N, 0.f, ab);
+    load_vector<VEC, sizeof(T)>(a.scale, first, N, 1.f, wp);
+    load_vector<VEC, sizeof(T)>(a.w_post, first, N, 1.f, aw);
+    load_vector<VEC, sizeof(T)>(a.b_post, first, N, 0.f, ab);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         aw[i] = __fmul2_rn(aw[i], wp[i]);
         ab[i] = __fmul2_rn(ab[i], wp[i]);
     }
-    load_vector<VEC>(a.w_pre, first, N, 1.f, wp);
-    load_vector<VEC>(a.b_pre, first, N, 0.f, bp);
+    load_vector<VEC, sizeof(T)>(a.w_pre, first, N, 1.f, wp);
+    load_vector<VEC, sizeof(T)>(a.b_pre, first, N, 0.f, bp);
     const int64_t step = (int64_t)gridDim.x * G;
     const int64_t row0 = (int64_t)blockIdx.x * G + warp / W;
     auto fetch = [&](int stage, int64_t row) {
         if (row < a.M) {
-            if (a.y) ring.fetch(stage, 0, (const T*)a.y + row * a.ldy);
-            if (a.gate_cols > 1) ring.fetch(stage, 1, (const T*)a.gate + row * a.ldg);
-            if (a.res) ring.fetch(stage, 2, (const T*)a.res + row * a.ldres);
+            if (a.y) ring.fetch(stage, 0, (const T*)a.y, row * a.ldy);
+            if (a.gate_cols > 1) ring.fetch(stage, 1, (const T*)a.gate, row * a.ldg);
+            if (a.res) ring.fetch(stage, 2, (const T*)a.res, row * a.ldres);
         }
         R::commit();
     };
@@ -302,12 +392,15 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
         R::wait();
         float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
         float2 r[4];
-        ring.read(stage, 2, r);
+        if (a.res) ring.read(stage, 2, (const T*)a.res + row * a.ldres, r);
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = both(0.f);
         if (a.y) {
             float2 f[4], g[4];
-            ring.read(stage, 0, f);
+            ring.read(stage, 0, (const T*)a.y + row * a.ldy, f);
             if (a.gate_cols > 1) {
-                ring.read(stage, 1, g);
+                ring.read(stage, 1, (const T*)a.gate + row * a.ldg, g);
                 if (a.gate_act != DLRM_GATE_NONE)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -319,7 +412,7 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) g[i] = both(g1);
             }
-            const float2 s = centre<VEC, W>(f, first, a, red, turn, warp);
+            const float2 s = centre<VEC, sizeof(T), W>(f, first, a, red, turn, warp);
             st.x = s.x;
             st.y = s.y;
 #pragma unroll
@@ -330,7 +423,7 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
             store_run<T, VEC>((T*)a.r + row * a.ldr, first, N, r);
         }
         if (a.h) {
-            const float2 s = centre<VEC, W>(r, first, a, red, turn, warp);
+            const float2 s = centre<VEC, sizeof(T), W>(r, first, a, red, turn, warp);
             st.z = s.x;
             st.w = s.y;
 #pragma unroll
@@ -338,6 +431,7 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
             store_run<T, VEC>((T*)a.h + row * a.ldh, first, N, r);
         }
         if (a.stats && warp % W == 0 && lane == 0) a.stats[row] = st;
+        R::done();
         stage = stage == kAhead - 1 ? 0 : stage + 1;
     }
 }
@@ -417,31 +511,31 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
     __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
     pdl_wait();
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, N = a.N;
-    const int first = run_first<VEC>(warp % W, lane);
+    const int first = run_first<VEC, sizeof(T)>(warp % W, lane);
     int turn = 0;
     const Rg ring(smem, N, first);
     float2 aw[4], ab[4], wp[4];   // scale w_post, scale b_post, w_pre; 0 past the row's end
-    load_vector<VEC>(a.scale, first, N, 1.f, wp);
-    load_vector<VEC>(a.w_post, first, N, 1.f, aw);
-    load_vector<VEC>(a.b_post, first, N, 0.f, ab);
+    load_vector<VEC, sizeof(T)>(a.scale, first, N, 1.f, wp);
+    load_vector<VEC, sizeof(T)>(a.w_post, first, N, 1.f, aw);
+    load_vector<VEC, sizeof(T)>(a.b_post, first, N, 0.f, ab);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         aw[i] = __fmul2_rn(aw[i], wp[i]);
         ab[i] = __fmul2_rn(ab[i], wp[i]);
     }
-    load_vector<VEC>(a.w_pre, first, N, 1.f, wp);
+    load_vector<VEC, sizeof(T)>(a.w_pre, first, N, 1.f, wp);
     float2 sum[4][4] = {};
     const int64_t step = (int64_t)gridDim.x * G, row0 = (int64_t)blockIdx.x * G + warp / W;
     auto fetch = [&](int stage, int64_t row) {
         if (row < a.M) {
-            if (a.gr) ring.fetch(stage, kGr, (const T*)a.gr + row * a.ldgr);
+            if (a.gr) ring.fetch(stage, kGr, (const T*)a.gr, row * a.ldgr);
             if (PRE) {
-                ring.fetch(stage, kGh, (const T*)a.gh + row * a.ldgh);
-                ring.fetch(stage, kR, (const T*)a.r + row * a.ldr);
+                ring.fetch(stage, kGh, (const T*)a.gh, row * a.ldgh);
+                ring.fetch(stage, kR, (const T*)a.r, row * a.ldr);
             }
             if (POST) {
-                ring.fetch(stage, kY, (const T*)a.y + row * a.ldy);
-                if (a.gate_cols > 1) ring.fetch(stage, kGate, (const T*)a.gate + row * a.ldg);
+                ring.fetch(stage, kY, (const T*)a.y, row * a.ldy);
+                if (a.gate_cols > 1) ring.fetch(stage, kGate, (const T*)a.gate, row * a.ldg);
             }
         }
         Rg::commit();
@@ -462,11 +556,14 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
         }
         Rg::wait();
         float2 dr[4];
-        ring.read(stage, kGr, dr);
+        if (a.gr) ring.read(stage, kGr, (const T*)a.gr + row * a.ldgr, dr);
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dr[i] = both(0.f);
         if (PRE) {
             float2 d[4], x[4], p, q;
-            ring.read(stage, kGh, d);
-            ring.read(stage, kR, x);
+            ring.read(stage, kGh, (const T*)a.gh + row * a.ldgh, d);
+            ring.read(stage, kR, (const T*)a.r + row * a.ldr, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[i] = __fmul2_rn(__fadd2_rn(x[i], both(-st.z)), both(st.w));
@@ -494,9 +591,9 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
         if (a.gres) store_run<T, VEC>((T*)a.gres + row * a.ldgres, first, N, dr);
         if (POST) {
             float2 x[4], g[4], k[4], p, q, t = both(0.f);
-            ring.read(stage, kY, x);
+            ring.read(stage, kY, (const T*)a.y + row * a.ldy, x);
             if (a.gate_cols > 1) {
-                ring.read(stage, kGate, g);
+                ring.read(stage, kGate, (const T*)a.gate + row * a.ldg, g);
                 if (a.gate_act != DLRM_GATE_NONE)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -551,6 +648,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
                 store_run<T, VEC>((T*)a.gy + row * a.ldgy, first, N, dr);
             }
         }
+        Rg::done();
         stage = stage == kAhead - 1 ? 0 : stage + 1;
     }
     if (!a.partial) return;
@@ -572,7 +670,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
                     for (int i = 0; i < 4; ++i) sum[s][i] = __fadd2_rn(sum[s][i], tile[i * 256 + g * W * 32 + threadIdx.x]);
             }
         }
-        if (warp < W) store_run<float, VEC>(a.partial + ((int64_t)blockIdx.x * 4 + s) * a.Np, first, N, sum[s]);
+        if (warp < W) store_vector<VEC, sizeof(T)>(a.partial + ((int64_t)blockIdx.x * 4 + s) * a.Np, first, N, sum[s]);
     }
 }
 
