@@ -8,100 +8,148 @@ namespace dlrm {
 namespace {
 
 // ------------------------------------------------------------ choice of experts
-// A float as an unsigned number in the same order, a NaN above all, -0 as 0.
-__device__ __forceinline__ uint32_t ordered(float v)
-{
-    const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
-    return v != v ? 0xffffffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-constexpr uint32_t kClosed = 0x007fffffu;   // ordered(-infinity); 0 stands for no logit
-
-// A warp takes a token, a lane the logits lane, lane + 32, ..: k rounds of the largest of the
-// lanes' largest and the least index that has it.
+// A logit and its expert as one unsigned number, so that the largest is the choice: the value's
+// bits made to order as numbers do (a NaN above all, -0 as 0), below them 255 - e, so that equal
+// ones go by lower index.  2-byte types fit 32 bits.  0 stands for no logit; expert() and
+// value() give the parts back.
 template <typename T>
+struct Key {
+    using Word = uint32_t;
+    static constexpr uint32_t kInf = std::is_same_v<T, __half> ? 0x7c00u : 0x7f80u;
+    static constexpr Word kClosed = (Word)(0xffffu & ~(0x8000u | kInf)) << 16 | 0xffffu;   // -infinity, whichever expert
+    static __device__ __forceinline__ Word make(T v, int e)
+    {
+        uint16_t h;
+        memcpy(&h, &v, 2);
+        const uint32_t b = h == 0x8000u ? 0u : h;
+        const uint32_t o = (b & 0x7fffu) > kInf ? 0xffffu : b & 0x8000u ? ~b & 0xffffu : b | 0x8000u;
+        return o << 16 | (255 - e);
+    }
+    static __device__ __forceinline__ float value(Word k)
+    {
+        const uint32_t o = k >> 16;
+        const uint16_t h = (uint16_t)(o == 0xffffu ? 0x7fffu : o & 0x8000u ? o ^ 0x8000u : ~o);
+        T v;
+        memcpy(&v, &h, 2);
+        return to_f32(v);
+    }
+    static __device__ __forceinline__ int expert(Word k) { return 255 - (int)(k & 0xffu); }
+};
+
+template <>
+struct Key<float> {
+    using Word = unsigned long long;
+    static constexpr Word kClosed = (Word)0x007fffffu << 32 | 0xffffffffu;
+    static __device__ __forceinline__ Word make(float v, int e)
+    {
+        const uint32_t b = v == 0.f ? 0u : __float_as_uint(v);
+        const uint32_t o = v != v ? 0xffffffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
+        return (Word)o << 32 | (uint32_t)(255 - e);
+    }
+    static __device__ __forceinline__ float value(Word k)
+    {
+        const uint32_t o = (uint32_t)(k >> 32);
+        return __uint_as_float(o == 0xffffffffu ? 0x7fffffffu : o & 0x80000000u ? o ^ 0x80000000u : ~o);
+    }
+    static __device__ __forceinline__ int expert(Word k) { return 255 - (int)((uint32_t)k & 0xffu); }
+};
+
+// L lanes take a token, eight logits each: k rounds of the largest key left.  Its whole cost is
+// instructions and their latency, so a warp takes 32 / L tokens (65536 of 64 experts, 4 of them, bf16:
+// a warp a token 33 us).
+template <typename T, bool VEC, int L>
 __global__ void __launch_bounds__(256)
 route_fwd_kernel(const T* __restrict__ logits, int64_t ldl, int tokens, int E, int k, int32_t* __restrict__ ids,
                  float* __restrict__ probs)
 {
+    using K = Key<T>;
+    using Word = typename K::Word;
     pdl_wait();
-    constexpr int kMine = DLRM_ROUTE_MAX_EXPERTS / kWarp;
-    const int lane = threadIdx.x % kWarp;
-    for (int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / kWarp; t < tokens; t += (int64_t)gridDim.x * 8) {
-        const T* row = logits + t * ldl;
-        uint32_t key[kMine];
-        T raw[kMine];
-#pragma unroll
-        for (int i = 0; i < kMine; ++i)
-            if (lane + 32 * i < E) raw[i] = __ldg(row + lane + 32 * i);
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) key[i] = lane + 32 * i < E ? ordered(to_f32(raw[i])) : 0;
-        int id = -1;         // lane j: the j-th choice
-        float logit = 0.f;
-        for (int j = 0; j < k; ++j) {
-            uint32_t best = 0;
-#pragma unroll
-            for (int i = 0; i < kMine; ++i) best = max(best, key[i]);
-            best = __reduce_max_sync(~0u, best);
-            if (best <= kClosed) break;
-            uint32_t at = ~0u;
-#pragma unroll
-            for (int i = kMine - 1; i >= 0; --i)
-                if (key[i] == best) at = lane + 32 * i;
-            at = __reduce_min_sync(~0u, at);
-#pragma unroll
-            for (int i = 0; i < kMine; ++i)
-                if (at == lane + 32 * i) key[i] = 0;
-            if (lane == j) {
-                id = (int)at;
-                logit = best == ~0u ? __uint_as_float(0x7fc00000u)
-                                    : __uint_as_float(best & 0x80000000u ? best ^ 0x80000000u : ~best);
+    const int lane = threadIdx.x % kWarp, l = lane % L, n = E - l * 8;
+    const int64_t step = (int64_t)gridDim.x * (256 / L);
+    for (int64_t t0 = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / kWarp * (kWarp / L); t0 < tokens; t0 += step) {
+        const int64_t t = t0 + lane / L;
+        const bool here = t < tokens;
+        Word key[8];
+        {
+            T v[8];
+            if (here && n > 0) {
+                const Raw8<T> raw = load8<T, VEC>(logits + t * ldl + l * 8, n);
+                memcpy(v, &raw, sizeof(raw));
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) key[i] = here && i < n ? K::make(v[i], l * 8 + i) : 0;
         }
-        const float top = __shfl_sync(~0u, logit, 0);
-        const float e = id >= 0 ? expf(logit - top) : 0.f;
-        float sum = 0.f;
-        for (int j = 0; j < k; ++j) sum += __shfl_sync(~0u, e, j);
-        if (lane < k) {
-            ids[t * k + lane] = id;
-            probs[t * k + lane] = id >= 0 ? e / sum : 0.f;
+        Word mine = 0;       // lane j of the token's: choice j
+        for (int j = 0; j < k; ++j) {
+            Word best = key[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) best = max(best, key[i]);
+#pragma unroll
+            for (int m = L / 2; m; m /= 2) best = max(best, __shfl_xor_sync(~0u, best, m));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (key[i] == best) key[i] = 0;
+            if (l == j) mine = best;
+        }
+        const bool open = mine > K::kClosed;
+        const float logit = K::value(mine), top = __shfl_sync(~0u, logit, 0, L);
+        const float e = open ? expf(logit - top) : 0.f;
+        float sum = e;
+#pragma unroll
+        for (int m = 4; m; m /= 2) sum += __shfl_xor_sync(~0u, sum, m);   // the first eight lanes have the choices
+        if (here && l < k) {
+            ids[t * k + l] = open ? K::expert(mine) : -1;
+            probs[t * k + l] = open ? e / sum : 0.f;
         }
     }
 }
 
-// A warp takes a token's row of grad_logits; lane j < k has choice j.
-template <typename T>
+// L lanes take a token's row of grad_logits, eight columns each; lane j < k has choice j.
+template <typename T, bool VEC, int L>
 __global__ void __launch_bounds__(256)
 route_bwd_kernel(const float* __restrict__ grad_probs, const int32_t* __restrict__ ids, const float* __restrict__ probs,
                  int tokens, int E, int k, T* __restrict__ grad, int64_t ldgl)
 {
     pdl_wait();
-    const int lane = threadIdx.x % kWarp;
-    for (int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / kWarp; t < tokens; t += (int64_t)gridDim.x * 8) {
+    const int lane = threadIdx.x % kWarp, l = lane % L, n = E - l * 8;
+    const int64_t step = (int64_t)gridDim.x * (256 / L);
+    for (int64_t t0 = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / kWarp * (kWarp / L); t0 < tokens; t0 += step) {
+        const int64_t t = t0 + lane / L;
         int id = -1;
         float p = 0.f, g = 0.f;
-        if (lane < k) {
-            id = __ldg(ids + t * k + lane);
-            p = __ldg(probs + t * k + lane);
-            g = __ldg(grad_probs + t * k + lane);
-        }
-        if (id < 0 || id >= E) {
-            id = -1;
-            p = g = 0.f;
-        }
-        float dot = 0.f;
-        for (int j = 0; j < k; ++j) dot = fmaf(__shfl_sync(~0u, g, j), __shfl_sync(~0u, p, j), dot);
-        const float d = p * (g - dot);
-        T* row = grad + t * ldgl;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            float v = 0.f;
-            for (int j = 0; j < k; ++j) {
-                const int at = __shfl_sync(~0u, id, j);
-                const float dj = __shfl_sync(~0u, d, j);
-                if (at == e0 + lane) v = dj;
+        if (t < tokens && l < k) {
+            id = __ldg(ids + t * k + l);
+            if (id >= 0 && id < E) {
+                p = __ldg(probs + t * k + l);
+                g = __ldg(grad_probs + t * k + l);
+            } else {
+                id = -1;
             }
-            if (e0 + lane < E) row[e0 + lane] = from_f32<T>(v);
         }
+        float dot = g * p;
+#pragma unroll
+        for (int m = 4; m; m /= 2) dot += __shfl_xor_sync(~0u, dot, m);
+        const float d = p * (g - __shfl_sync(~0u, dot, 0, L));
+        float f[8] = {};
+        for (int j = 0; j < k; ++j) {
+            const int at = __shfl_sync(~0u, id, j, L) - l * 8;
+            const float dj = __shfl_sync(~0u, d, j, L);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (at == i) f[i] = dj;
+        }
+        if (t < tokens && n > 0) store8<T, VEC>(grad + t * ldgl + l * 8, n, f);
     }
+}
+
+// fn(the lanes of a token as a constant)
+template <typename Fn>
+dlrm_status with_lanes(int E, Fn&& fn)
+{
+    if (E <= 64) return fn(std::integral_constant<int, 8>());
+    if (E <= 128) return fn(std::integral_constant<int, 16>());
+    return fn(std::integral_constant<int, 32>());
 }
 
 // ------------------------------------------------------------- order by expert
@@ -110,11 +158,15 @@ route_bwd_kernel(const float* __restrict__ grad_probs, const int32_t* __restrict
 // one expert found by match.any, in counters of its own in shared memory.  Choices without
 // expert count as expert E.  With one block that is all; with more, expert_count_kernel writes
 // the chunks' counts first, and a block adds up those of the blocks before it (and all of
-// them: where an expert begins).
+// them: where an expert begins).  The steps are chains of latencies: a warp's choices are
+// loaded kBatch rounds at a time, and the counts' sums are shared out over all threads.
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / kWarp;
-constexpr int kSortChunk = 4096;        // choices of a block, while there are no more than kSortBlocks blocks
+constexpr int kSortChunk = 2048;        // choices of a block, while there are no more than kSortBlocks blocks
+constexpr int kSortOne = 4096;          // so many choices are one block's
 constexpr int kSortBlocks = 256;
+constexpr int kBatch = 8;
 constexpr int kBins = DLRM_ROUTE_MAX_EXPERTS + 1;
+static_assert(kBins <= kSortThreads, "a thread for each bin");
 
 struct SortShape {
     int blocks;
@@ -123,27 +175,35 @@ struct SortShape {
 
 inline SortShape sort_shape(int64_t n)
 {
+    if (n <= kSortOne) return {1, (n + kSortThreads - 1) / kSortThreads * kSortThreads};
     int64_t chunk = kSortChunk;
     if ((n + chunk - 1) / chunk > kSortBlocks)
         chunk = ((n + kSortBlocks - 1) / kSortBlocks + kSortThreads - 1) / kSortThreads * kSortThreads;
-    return {n > 0 ? (int)((n + chunk - 1) / chunk) : 1, chunk};
+    return {(int)((n + chunk - 1) / chunk), chunk};
 }
 
-// Choices [from, to) of a warp's part: each(choice, bin, rank among the 32 of its bin, how many of them)
+// Choices [from, to) of a warp's part: each(choice, id, bin, rank among the 32 of its bin, how many of them).
+// Bin kBins: past the part's end.
 template <typename Each>
 __device__ __forceinline__ void walk(const int32_t* ids, int64_t from, int64_t to, int E, Each each)
 {
     const int lane = threadIdx.x % kWarp;
-    for (int64_t c0 = from; c0 < to; c0 += kWarp) {
-        const int64_t c = c0 + lane;
-        int bin = kBins;       // past the part's end: a bin of its own, not counted
-        if (c < to) {
-            const int id = __ldg(ids + c);
-            bin = id >= 0 && id < E ? id : E;
+    for (int64_t c0 = from; c0 < to; c0 += kBatch * kWarp) {
+        int id[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t c = c0 + b * kWarp + lane;
+            id[b] = c < to ? __ldg(ids + c) : 0;
         }
-        const uint32_t same = __match_any_sync(~0u, bin);
-        each(c, bin, __popc(same & ((1u << lane) - 1)), __popc(same));
-        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t c = c0 + b * kWarp + lane;
+            if (c0 + b * kWarp >= to) break;
+            const int bin = c >= to ? kBins : id[b] >= 0 && id[b] < E ? id[b] : E;
+            const uint32_t same = __match_any_sync(~0u, bin);
+            each(c, id[b], bin, __popc(same & ((1u << lane) - 1)), __popc(same));
+            __syncwarp();
+        }
     }
 }
 
@@ -152,13 +212,13 @@ __device__ __forceinline__ void count_parts(const int32_t* ids, int64_t n, int64
                                             int64_t& from, int64_t& to)
 {
     const int warp = threadIdx.x / kWarp;
-    for (int i = threadIdx.x; i < kSortWarps * kBins; i += kSortThreads) warps[i / kBins][i % kBins] = 0;
-    __syncthreads();
+    int* mine = warps[warp];
+    for (int e = threadIdx.x % kWarp; e <= E; e += kWarp) mine[e] = 0;
+    __syncwarp();
     const int64_t part = chunk / kSortWarps, first = blockIdx.x * chunk;
     from = min(n, first + warp * part);
     to = min(n, from + part);
-    int* mine = warps[warp];
-    walk(ids, from, to, E, [&](int64_t, int bin, int rank, int many) {
+    walk(ids, from, to, E, [&](int64_t, int, int bin, int rank, int many) {
         if (rank == 0 && bin < kBins) mine[bin] += many;
     });
     __syncthreads();
@@ -175,7 +235,7 @@ expert_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
         int s = 0;
 #pragma unroll
         for (int w = 0; w < kSortWarps; ++w) s += warps[w][e];
-        counts[blockIdx.x * kBins + e] = s;
+        counts[blockIdx.x * (E + 1) + e] = s;
     }
 }
 
@@ -187,28 +247,40 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
     pdl_wait();
     __shared__ int warps[kSortWarps][kBins];
     __shared__ int total[kBins], before[kBins], scan[kSortWarps];
-    int64_t from, to;
-    count_parts(ids, n, chunk, E, warps, from, to);
-    for (int e = threadIdx.x; e <= E; e += kSortThreads) {
-        int all = 0, ahead = 0;
-        if (gridDim.x == 1) {
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) all += warps[w][e];
-        } else {
-#pragma unroll 16
-            for (int b = 0; b < (int)gridDim.x; ++b) {
-                const int v = __ldg(counts + b * kBins + e);
+    const int bins = E + 1, tid = threadIdx.x;
+    if (gridDim.x > 1) {
+        for (int e = tid; e < bins; e += kSortThreads) total[e] = before[e] = 0;
+        __syncthreads();
+        // a thread has one bin of every (kSortThreads / bins)-th block
+        const int parts = kSortThreads / bins, e = tid % bins, p = tid / bins;
+        if (p < parts) {
+            int all = 0, ahead = 0;
+#pragma unroll 8
+            for (int b = p; b < (int)gridDim.x; b += parts) {
+                const int v = __ldg(counts + b * bins + e);
                 all += v;
                 ahead += b < (int)blockIdx.x ? v : 0;
             }
+            atomicAdd(&total[e], all);      // whole numbers: the same in any order
+            atomicAdd(&before[e], ahead);
         }
-        total[e] = all;
-        before[e] = ahead;
     }
-    __syncthreads();
-    // where each expert's places begin: an exclusive scan of total over the bins (kBins <= kSortThreads)
+    int64_t from, to;
+    count_parts(ids, n, chunk, E, warps, from, to);
+    // where each expert's places begin: an exclusive scan of the totals over the bins
     {
-        const int e = threadIdx.x, lane = e % kWarp, v = e <= E ? total[e] : 0;
+        const int e = tid, lane = e % kWarp;
+        int mine[kSortWarps], v = 0;
+        if (e < bins) {
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) mine[w] = warps[w][e];
+            if (gridDim.x > 1) {
+                v = total[e];
+            } else {
+#pragma unroll
+                for (int w = 0; w < kSortWarps; ++w) v += mine[w];
+            }
+        }
         int s = v;
 #pragma unroll
         for (int m = 1; m < kWarp; m *= 2) {
@@ -217,35 +289,33 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
         }
         if (lane == kWarp - 1) scan[e / kWarp] = s;
         __syncthreads();
-        for (int w = 0; w < e / kWarp; ++w) s += scan[w];
-        if (e <= E) {
+        if (e < bins) {
+            for (int w = 0; w < e / kWarp; ++w) s += scan[w];
             int at = s - v;
             if (blockIdx.x == 0) offsets[e] = at;   // offsets[E]: how many have a place
-            at += before[e];
+            if (gridDim.x > 1) at += before[e];
 #pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
-                const int many = warps[w][e];
                 warps[w][e] = at;
-                at += many;
+                at += mine[w];
             }
         }
     }
     __syncthreads();
-    int* mine = warps[threadIdx.x / kWarp];
+    int* mine = warps[tid / kWarp];
     bool bad = false;
-    walk(ids, from, to, E, [&](int64_t c, int bin, int rank, int many) {
+    walk(ids, from, to, E, [&](int64_t c, int id, int bin, int rank, int many) {
         const int at = bin < kBins ? mine[bin] + rank : 0;
         __syncwarp();
         if (rank == 0 && bin < kBins) mine[bin] += many;
         if (c < to) {
             slots[c] = bin < E ? at : -1;
             if (order) order[at] = bin < E ? (int32_t)c : -1;
-            if (bin == E && __ldg(ids + c) >= E) bad = true;
+            bad = bad || id >= E;
         }
     });
     if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
 }
-static_assert(kBins <= kSortThreads, "a thread for each bin");
 
 // -------------------------------------------------- rows to their experts and back
 // Walks the runs of eight columns of `rows` rows, a run a thread at a time, stepping row and run
@@ -477,9 +547,10 @@ inline unsigned run_blocks(int64_t rows, int H)
     return (unsigned)(want < most ? want : most);
 }
 
-inline unsigned warp_blocks(int64_t tokens)
+// Blocks of 256 threads where `lanes` take a token.
+inline unsigned token_blocks(int64_t tokens, int lanes)
 {
-    const int64_t want = (tokens + 7) / 8, most = (int64_t)num_sms() * 8;
+    const int64_t want = (tokens * lanes + 255) / 256, most = (int64_t)num_sms() * 8;
     return (unsigned)(want < most ? want : most);
 }
 
@@ -517,9 +588,14 @@ extern "C" dlrm_status dlrm_route_fwd(const void* d_logits, int64_t ldl, dlrm_dt
     if ((s = check_words(fn, "d_probs", d_probs)) != DLRM_OK) return s;
     return with_type(dtype, [&](auto t) {
         using X = decltype(t);
-        return check_launch_pdl(launch_pdl(route_fwd_kernel<X>, dim3(warp_blocks(T)), dim3(256), 0, as_stream(stream),
-                                           (const X*)d_logits, ldl, T, E, k, d_ids, d_probs),
-                                "route_fwd_kernel");
+        return with_lanes(E, [&](auto l) {
+            constexpr int L = decltype(l)::value;
+            auto kern = E % 8 == 0 && rows_aligned16(d_logits, ldl, T, sizeof(X)) ? route_fwd_kernel<X, true, L>
+                                                                                  : route_fwd_kernel<X, false, L>;
+            return check_launch_pdl(launch_pdl(kern, dim3(token_blocks(T, L)), dim3(256), 0, as_stream(stream),
+                                               (const X*)d_logits, ldl, T, E, k, d_ids, d_probs),
+                                    "route_fwd_kernel");
+        });
     });
 }
 
@@ -538,9 +614,14 @@ extern "C" dlrm_status dlrm_route_bwd(const float* d_grad_probs, const int32_t* 
     if ((s = check_matrix(fn, "d_grad_logits", d_grad_logits, ldgl, T, E, dense_dtype_size(dtype))) != DLRM_OK) return s;
     return with_type(dtype, [&](auto t) {
         using X = decltype(t);
-        return check_launch_pdl(launch_pdl(route_bwd_kernel<X>, dim3(warp_blocks(T)), dim3(256), 0, as_stream(stream),
-                                           d_grad_probs, d_ids, d_probs, T, E, k, (X*)d_grad_logits, ldgl),
-                                "route_bwd_kernel");
+        return with_lanes(E, [&](auto l) {
+            constexpr int L = decltype(l)::value;
+            auto kern = E % 8 == 0 && rows_aligned16(d_grad_logits, ldgl, T, sizeof(X)) ? route_bwd_kernel<X, true, L>
+                                                                                        : route_bwd_kernel<X, false, L>;
+            return check_launch_pdl(launch_pdl(kern, dim3(token_blocks(T, L)), dim3(256), 0, as_stream(stream), d_grad_probs,
+                                               d_ids, d_probs, T, E, k, (X*)d_grad_logits, ldgl),
+                                    "route_bwd_kernel");
+        });
     });
 }
 
@@ -554,7 +635,7 @@ extern "C" size_t dlrm_expert_sort_workspace_size(int T, int k, int E)
 {
     if (!sort_sizes_ok(T, k, E)) return 0;
     const SortShape z = sort_shape((int64_t)T * k);
-    return z.blocks > 1 ? dlrm_ws_align((size_t)z.blocks * kBins * 4) : 0;
+    return z.blocks > 1 ? dlrm_ws_align((size_t)z.blocks * (E + 1) * 4) : 0;
 }
 
 extern "C" dlrm_status dlrm_expert_sort(const int32_t* d_ids, int T, int k, int E, int32_t* d_offsets, int32_t* d_slots,
