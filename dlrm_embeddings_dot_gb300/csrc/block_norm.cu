@@ -19,24 +19,18 @@
 // Nothing here depends on which columns a lane has.  On the 16-byte grid they are eight
 // neighbours.  Off it a warp copies the aligned 16-byte words that hold its 256 columns and a
 // lane has every 32nd column, or pair of them, which shared memory gives without conflicts.
-#include "dense_ops.cuh"
 #include "dlrm_block.h"
+#include "row_units.cuh"
 
 namespace dlrm {
 namespace {
 
 // ------------------------------------------------------------- runs of a row
-// A lane's run of a row: its first column and the others, ES the element's size.
+// The first column of a lane's run where a warp has 256 columns of a row; run_col has the others.
 template <bool VEC, int ES>
 __device__ __forceinline__ int run_first(int warp, int lane)
 {
     return warp * 256 + lane * (VEC ? 8 : ES == 2 ? 2 : 1);
-}
-
-template <bool VEC, int ES>
-__device__ __forceinline__ int run_col(int first, int i)
-{
-    return first + (VEC ? i : ES == 2 ? i / 2 * 64 + i % 2 : i * 32);
 }
 
 // The rows to come: kAhead rows of NT tensors, three where the blocks that share an SM (two of
@@ -128,9 +122,9 @@ struct Ring<T, false, NT, THREADS> {
 #pragma unroll
         for (int i = 0; i < (kWords + kWarp - 1) / kWarp; ++i) {
             const int w = lane + kWarp * i;
-            if (w < kWords && w * 16 < end) {
+            if (w < kWords) {   // words behind the row become 0
                 if (w > 0 || (at_row + from) * (int)sizeof(T) >= off) {
-                    copy16(to + w * 16, p - off + w * 16, min(16, end - w * 16));
+                    copy16(to + w * 16, w * 16 < end ? p - off + w * 16 : p - off, max(0, min(16, end - w * 16)));
                 } else {
                     T* word = reinterpret_cast<T*>(mine + stage * kStage + slot * kSlot);
                     for (int e = off / (int)sizeof(T); e < min(16, end) / (int)sizeof(T); ++e)
@@ -154,15 +148,14 @@ struct Ring<T, false, NT, THREADS> {
         for (int i = 0; i < 4; ++i) {
             if constexpr (sizeof(T) == 4) {
                 f[i] = make_float2(*reinterpret_cast<const float*>(p + 256 * i), *reinterpret_cast<const float*>(p + 256 * i + 128));
+            } else if (((uintptr_t)row & 3) == 0) {
+                const uint32_t w = *reinterpret_cast<const uint32_t*>(p + 128 * i);
+                T e[2];
+                memcpy(e, &w, 4);
+                f[i] = make_float2(to_f32(e[0]), to_f32(e[1]));
             } else {
                 f[i] = make_float2(to_f32(*reinterpret_cast<const T*>(p + 128 * i)), to_f32(*reinterpret_cast<const T*>(p + 128 * i + 2)));
             }
-        }
-        // what lies behind the row in its last word is 0; a stage's later words may be an earlier row's
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (run_col<false, sizeof(T)>(first, 2 * i) >= N) f[i].x = 0.f;
-            if (run_col<false, sizeof(T)>(first, 2 * i + 1) >= N) f[i].y = 0.f;
         }
     }
 };

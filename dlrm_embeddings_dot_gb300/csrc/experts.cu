@@ -1,8 +1,8 @@
 // experts.cu -- a mixture of experts in training: the choice of experts and its
 // gradient, the order of the choices by expert, and the rows' way to their
 // experts and back.  Each is bound by memory, or by latency where there are few tokens.
-#include "dense_ops.cuh"
 #include "dlrm_block.h"
+#include "row_units.cuh"
 
 namespace dlrm {
 namespace {
@@ -54,6 +54,22 @@ struct Key<float> {
     static __device__ __forceinline__ int expert(Word k) { return 255 - (int)((uint32_t)k & 0xffu); }
 };
 
+// The largest of L lanes' keys, in all of them.
+template <int L, typename Word>
+__device__ __forceinline__ Word largest(Word k)
+{
+    if constexpr (L == kWarp && sizeof(Word) == 4) {
+        return __reduce_max_sync(~0u, k);
+    } else if constexpr (L == kWarp) {
+        const uint32_t hi = __reduce_max_sync(~0u, (uint32_t)(k >> 32));
+        return (Word)hi << 32 | __reduce_max_sync(~0u, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+    } else {
+#pragma unroll
+        for (int m = L / 2; m; m /= 2) k = max(k, __shfl_xor_sync(~0u, k, m));
+        return k;
+    }
+}
+
 // L lanes take a token, eight logits each: k rounds of the largest key left.  Its whole cost is
 // instructions and their latency, so a warp takes 32 / L tokens (65536 of 64 experts, 4 of them, bf16:
 // a warp a token 33 us).
@@ -85,8 +101,7 @@ route_fwd_kernel(const T* __restrict__ logits, int64_t ldl, int tokens, int E, i
             Word best = key[0];
 #pragma unroll
             for (int i = 1; i < 8; ++i) best = max(best, key[i]);
-#pragma unroll
-            for (int m = L / 2; m; m /= 2) best = max(best, __shfl_xor_sync(~0u, best, m));
+            best = largest<L>(best);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (key[i] == best) key[i] = 0;
@@ -120,12 +135,12 @@ route_bwd_kernel(const float* __restrict__ grad_probs, const int32_t* __restrict
         float p = 0.f, g = 0.f;
         if (t < tokens && l < k) {
             id = __ldg(ids + t * k + l);
-            if (id >= 0 && id < E) {
-                p = __ldg(probs + t * k + l);
-                g = __ldg(grad_probs + t * k + l);
-            } else {
-                id = -1;
-            }
+            p = __ldg(probs + t * k + l);
+            g = __ldg(grad_probs + t * k + l);
+        }
+        if (id < 0 || id >= E) {
+            id = -1;
+            p = g = 0.f;
         }
         float dot = g * p;
 #pragma unroll
@@ -160,10 +175,10 @@ dlrm_status with_lanes(int E, Fn&& fn)
 // the chunks' counts first, and a block adds up those of the blocks before it (and all of
 // them: where an expert begins).  The steps are chains of latencies: a warp's choices are
 // loaded kBatch rounds at a time, and the counts' sums are shared out over all threads.
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / kWarp;
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / kWarp;
 constexpr int kSortChunk = 2048;        // choices of a block, while there are no more than kSortBlocks blocks
 constexpr int kSortOne = 4096;          // so many choices are one block's
-constexpr int kSortBlocks = 256;
+constexpr int kSortBlocks = 128;    // each of which reads all counts
 constexpr int kBatch = 8;
 constexpr int kBins = DLRM_ROUTE_MAX_EXPERTS + 1;
 static_assert(kBins <= kSortThreads, "a thread for each bin");
@@ -318,43 +333,16 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
 }
 
 // -------------------------------------------------- rows to their experts and back
-// Walks the runs of eight columns of `rows` rows, a run a thread at a time, stepping row and run
-// without a division.
-struct Runs {
-    int64_t i, end, stride, row, g, groups, drow, dg;
-    __device__ Runs(int64_t rows, int H)
-    {
-        groups = (H - 1) / 8 + 1;
-        end = groups * rows;
-        stride = (int64_t)gridDim.x * blockDim.x;
-        i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-        row = i / groups;
-        g = i - row * groups;
-        drow = stride / groups;
-        dg = stride - drow * groups;
-    }
-    __device__ bool more() const { return i < end; }
-    __device__ void next()
-    {
-        i += stride;
-        row += drow;
-        g += dg;
-        if (g >= groups) {
-            g -= groups;
-            ++row;
-        }
-    }
-};
-
 constexpr int kMaxK = DLRM_ROUTE_MAX_TOP_K;
 
 // The slots of a token; those without a row as -1.
-__device__ __forceinline__ void load_slots(const int32_t* slots, int64_t t, int k, int R, int (&s)[kMaxK], bool& bad)
+template <int K>
+__device__ __forceinline__ void load_slots(const int32_t* slots, int64_t t, int k, int R, int (&s)[K], bool& bad)
 {
 #pragma unroll
-    for (int j = 0; j < kMaxK; ++j) s[j] = j < k ? __ldg(slots + t * k + j) : -1;
+    for (int j = 0; j < K; ++j) s[j] = j < k ? __ldg(slots + t * k + j) : -1;
 #pragma unroll
-    for (int j = 0; j < kMaxK; ++j)
+    for (int j = 0; j < K; ++j)
         if (s[j] >= R) {
             bad = true;
             s[j] = -1;
@@ -365,62 +353,76 @@ __device__ __forceinline__ void load_slots(const int32_t* slots, int64_t t, int 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
 dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slots, int tokens, int k, int H, int R,
-                T* __restrict__ xs, int64_t ldxs, uint32_t* __restrict__ status)
+                int lanes, T* __restrict__ xs, int64_t ldxs, uint32_t* __restrict__ status)
 {
+    constexpr int U = kRuns<T, VEC, 2>;
     pdl_wait();
     bool bad = false;
-    for (Runs r(tokens, H); r.more(); r.next()) {
-        const int col = (int)r.g * 8, n = H - col;
+    const Unit unit(lanes);
+    for (Items it(unit, (H + lanes * 8 * U - 1) / (lanes * 8 * U)); it.row < tokens; it.next()) {
         int s[kMaxK];
-        const Raw8<T> v = load8<T, VEC>(x + r.row * ldx + col, n);
-        load_slots(slots, r.row, k, R, s, bad);
-        float f[8];
-        widen8<T>(v, f);
+        Raw8<T> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (unit.has<VEC>((int)it.part * U + u, H))
+                v[u] = load_cols<T, VEC>(x + it.row * ldx, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H);
+        load_slots(slots, it.row, k, R, s, bad);
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j)
-            if (s[j] >= 0) store8<T, VEC>(xs + s[j] * ldxs + col, n, f);
+            if (s[j] >= 0)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (unit.has<VEC>((int)it.part * U + u, H))
+                        store_raw<T, VEC>(xs + s[j] * ldxs, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, v[u]);
     }
     if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
 }
 
-// y[t] = residual[t] + sum over j of probs[t][j] ys[slots[t][j]]; probs NULL: the plain sum.
-template <typename T, bool VEC>
+// y[t] = residual[t] + sum over j of probs[t][j] ys[slots[t][j]]; probs NULL: the plain sum.  k <= K.
+template <typename T, bool VEC, int K>
 __global__ void __launch_bounds__(256)
 combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict__ slots, const float* __restrict__ probs,
-               const T* __restrict__ res, int64_t ldres, int tokens, int k, int H, int R, T* __restrict__ y, int64_t ldy,
-               uint32_t* __restrict__ status)
+               const T* __restrict__ res, int64_t ldres, int tokens, int k, int H, int R, int lanes, T* __restrict__ y,
+               int64_t ldy, uint32_t* __restrict__ status)
 {
+    constexpr int U = kRuns<T, VEC, K>;
     pdl_wait();
     bool bad = false;
-    for (Runs r(tokens, H); r.more(); r.next()) {
-        const int col = (int)r.g * 8, n = H - col;
-        int s[kMaxK];
-        load_slots(slots, r.row, k, R, s, bad);
-        Raw8<T> v[kMaxK], vr;
-        float p[kMaxK];
+    const Unit unit(lanes);
+    for (Items it(unit, (H + lanes * 8 * U - 1) / (lanes * 8 * U)); it.row < tokens; it.next()) {
+        int s[K];
+        float p[K];
+        load_slots(slots, it.row, k, R, s, bad);
 #pragma unroll
-        for (int j = 0; j < kMaxK; ++j)
-            if (s[j] >= 0) {
-                v[j] = load8<T, VEC>(ys + s[j] * ldys + col, n);
-                p[j] = probs ? __ldg(probs + r.row * k + j) : 1.f;
-            }
-        if (res) vr = load8<T, VEC>(res + r.row * ldres + col, n);
-        float f[8] = {};
+        for (int j = 0; j < K; ++j) p[j] = probs && j < k ? __ldg(probs + it.row * k + j) : 1.f;
+        Raw8<T> v[U][K], vr[U];
 #pragma unroll
-        for (int j = 0; j < kMaxK; ++j)
-            if (s[j] >= 0) {
-                float w[8];
-                widen8<T>(v[j], w);
+        for (int u = 0; u < U; ++u) {
+            if (!unit.has<VEC>((int)it.part * U + u, H)) break;
+            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = fmaf(p[j], w[i], f[i]);
-            }
-        if (res) {
-            float w[8];
-            widen8<T>(vr, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] += w[i];
+            for (int j = 0; j < K; ++j)
+                if (s[j] >= 0) v[u][j] = load_cols<T, VEC>(ys + s[j] * ldys, c, H);
+            if (res) vr[u] = load_cols<T, VEC>(res + it.row * ldres, c, H);
         }
-        store8<T, VEC>(y + r.row * ldy + col, n, f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!unit.has<VEC>((int)it.part * U + u, H)) break;
+            float f[8] = {}, w[8];
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                if (s[j] >= 0) {
+                    widen8<T>(v[u][j], w);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = fmaf(p[j], w[i], f[i]);
+                }
+            if (res) {
+                widen8<T>(vr[u], w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] += w[i];
+            }
+            store_cols<T, VEC>(y + it.row * ldy, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, f);
+        }
     }
     if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
 }
@@ -430,81 +432,96 @@ struct CombineBwd {
     int64_t ldgy, ldys;
     const int32_t* slots;
     const float* probs;
-    int tokens, k, H, R;
+    int tokens, k, H, R, lanes;
     void* gys;          // may be NULL
     int64_t ldgys;
     float* gp;          // may be NULL
     uint32_t* status;
 };
 
-// W warps take a token: grad_y once, and for each choice its row of ys in and of grad_ys out.
-template <typename T, bool VEC, int W>
+// A unit takes a token, or with W = 8 warps a whole block does: grad_y once, and for each choice its
+// row of ys in and of grad_ys out.  k <= K.
+template <typename T, bool VEC, int K, int W>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant__ CombineBwd a)
 {
-    constexpr int G = 8 / W;
-    __shared__ float red[W > 1 ? 8 * kMaxK : 1];
+    constexpr int U = kRuns<T, VEC, K>;
+    __shared__ float red[W > 1 ? 8 * K : 1];
     pdl_wait();
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, H = a.H;
+    const Unit unit(W > 1 ? kWarp : a.lanes);
+    const int lanes = unit.lanes;
     bool bad = false;
-    for (int64_t t = (int64_t)blockIdx.x * G + warp / W; t < a.tokens; t += (int64_t)gridDim.x * G) {
-        int s[kMaxK];
-        load_slots(a.slots, t, a.k, a.R, s, bad);
-        float p[kMaxK], dot[kMaxK];
+    // all units of a warp go through the loop together
+    for (int64_t t0 = W > 1 ? blockIdx.x : unit.unit - lane / lanes; t0 < a.tokens; t0 += W > 1 ? gridDim.x : unit.units) {
+        const int64_t t = W > 1 ? t0 : t0 + lane / lanes;
+        const bool here = t < a.tokens;
+        int s[K];
+        float p[K], dot[K];
+        if (here) load_slots(a.slots, t, a.k, a.R, s, bad);
 #pragma unroll
-        for (int j = 0; j < kMaxK; ++j) {
+        for (int j = 0; j < K; ++j) {
+            if (!here) s[j] = -1;
             p[j] = s[j] >= 0 && a.gys ? __ldg(a.probs + t * a.k + j) : 0.f;
             dot[j] = 0.f;
         }
-        for (int col = (warp % W * 32 + lane) * 8; col < a.H; col += W * 256) {
-            const int n = a.H - col;
-            const Raw8<T> vg = load8<T, VEC>((const T*)a.gy + t * a.ldgy + col, n);
-            Raw8<T> v[kMaxK];
-            if (a.gp)
+        for (int run = W > 1 ? warp * U : 0; here && run * lanes * 8 < H; run += W * U) {
+            Raw8<T> vg[U], v[U][K];
 #pragma unroll
-                for (int j = 0; j < kMaxK; ++j)
-                    if (s[j] >= 0) v[j] = load8<T, VEC>((const T*)a.ys + s[j] * a.ldys + col, n);
-            float g[8];
-            widen8<T>(vg, g);
+            for (int u = 0; u < U; ++u) {
+                if (!unit.has<VEC>(run + u, H)) break;
+                const int c = unit.first<VEC, sizeof(T)>(run + u);
+                vg[u] = load_cols<T, VEC>((const T*)a.gy + t * a.ldgy, c, H);
+                if (a.gp)
 #pragma unroll
-            for (int j = 0; j < kMaxK; ++j)
-                if (s[j] >= 0) {
-                    if (a.gp) {
-                        float w[8];
-                        widen8<T>(v[j], w);
+                    for (int j = 0; j < K; ++j)
+                        if (s[j] >= 0) v[u][j] = load_cols<T, VEC>((const T*)a.ys + s[j] * a.ldys, c, H);
+            }
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], w[i], dot[j]);
+            for (int u = 0; u < U; ++u) {
+                if (!unit.has<VEC>(run + u, H)) break;
+                const int c = unit.first<VEC, sizeof(T)>(run + u);
+                float g[8];
+                widen8<T>(vg[u], g);
+#pragma unroll
+                for (int j = 0; j < K; ++j)
+                    if (s[j] >= 0) {
+                        if (a.gp) {
+                            float w[8];
+                            widen8<T>(v[u][j], w);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dot[j] = fmaf(g[i], w[i], dot[j]);
+                        }
+                        if (a.gys) {
+                            float o[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = p[j] * g[i];
+                            store_cols<T, VEC>((T*)a.gys + s[j] * a.ldgys, c, H, o);
+                        }
                     }
-                    if (a.gys) {
-                        float o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = p[j] * g[i];
-                        store8<T, VEC>((T*)a.gys + s[j] * a.ldgys + col, n, o);
-                    }
-                }
+            }
         }
         if (!a.gp) continue;
 #pragma unroll
-        for (int j = 0; j < kMaxK; ++j)
+        for (int j = 0; j < K; ++j)
             if (j < a.k)
-#pragma unroll
-                for (int m = 16; m; m /= 2) dot[j] += __shfl_xor_sync(~0u, dot[j], m);
-        if constexpr (W > 1) {   // W == 8: the block has one token
+                for (int m = lanes / 2; m; m /= 2) dot[j] += __shfl_xor_sync(~0u, dot[j], m);
+        if constexpr (W > 1) {
             static_assert(W == 8, "the block's barrier");
             __syncthreads();
             if (lane == 0)
 #pragma unroll
-                for (int j = 0; j < kMaxK; ++j) red[warp * kMaxK + j] = dot[j];
+                for (int j = 0; j < K; ++j) red[warp * K + j] = dot[j];
             __syncthreads();
             if (threadIdx.x < (unsigned)a.k) {
                 float sum = red[threadIdx.x];
 #pragma unroll
-                for (int w = 1; w < W; ++w) sum += red[w * kMaxK + threadIdx.x];
+                for (int w = 1; w < W; ++w) sum += red[w * K + threadIdx.x];
                 a.gp[t * a.k + threadIdx.x] = sum;
             }
-        } else {
+        } else if (here && unit.l == 0) {
 #pragma unroll
-            for (int j = 0; j < kMaxK; ++j)
-                if (lane == j && j < a.k) a.gp[t * a.k + j] = dot[j];
+            for (int j = 0; j < K; ++j)
+                if (j < a.k) a.gp[t * a.k + j] = dot[j];
         }
     }
     if (bad) set_status(a.status, DLRM_STATUS_OOB_INDEX);
@@ -541,10 +558,13 @@ dlrm_status check_rows(const char* fn, dlrm_dtype dtype, int T, int k, int H, in
     return DLRM_OK;
 }
 
-inline unsigned run_blocks(int64_t rows, int H)
+// fn(k rounded up to 2, 4 or 8 as a constant)
+template <typename Fn>
+dlrm_status with_choices(int k, Fn&& fn)
 {
-    const int64_t want = (((int64_t)H + 7) / 8 * rows + 255) / 256, most = (int64_t)num_sms() * 8;
-    return (unsigned)(want < most ? want : most);
+    if (k <= 2) return fn(std::integral_constant<int, 2>());
+    if (k <= 4) return fn(std::integral_constant<int, 4>());
+    return fn(std::integral_constant<int, 8>());
 }
 
 // Blocks of 256 threads where `lanes` take a token.
@@ -563,10 +583,15 @@ dlrm_status run_combine(const char* fn, const void* ys, int64_t ldys, const int3
                      rows_aligned16(y, ldy, T, es);
     return with_type(dtype, [&](auto t) {
         using E = decltype(t);
-        auto kern = vec ? combine_kernel<E, true> : combine_kernel<E, false>;
-        return check_launch_pdl(launch_pdl(kern, dim3(run_blocks(T, H)), dim3(256), 0, as_stream(stream), (const E*)ys, ldys,
-                                           slots, probs, (const E*)res, ldres, T, k, H, R, (E*)y, ldy, status),
-                                fn);
+        return with_choices(k, [&](auto kk) {
+            constexpr int K = decltype(kk)::value;
+            auto kern = vec ? combine_kernel<E, true, K> : combine_kernel<E, false, K>;
+            const int lanes = unit_lanes(H, vec);
+            return check_launch_pdl(launch_pdl(kern, dim3(item_blocks(T, H, lanes, vec ? kRuns<E, true, K> : kRuns<E, false, K>)), dim3(256), 0,
+                                               as_stream(stream), (const E*)ys, ldys, slots, probs, (const E*)res, ldres, T, k,
+                                               H, R, lanes, (E*)y, ldy, status),
+                                    fn);
+        });
     });
 }
 
@@ -690,8 +715,9 @@ extern "C" dlrm_status dlrm_dispatch_fwd(const void* d_x, int64_t ldx, const int
     return with_type(dtype, [&](auto t) {
         using X = decltype(t);
         auto kern = vec ? dispatch_kernel<X, true> : dispatch_kernel<X, false>;
-        return check_launch_pdl(launch_pdl(kern, dim3(run_blocks(T, H)), dim3(256), 0, as_stream(stream), (const X*)d_x, ldx,
-                                           d_slots, T, k, H, R, (X*)d_xs, ldxs, d_status),
+        const int lanes = unit_lanes(H, vec);
+        return check_launch_pdl(launch_pdl(kern, dim3(item_blocks(T, H, lanes, vec ? kRuns<X, true, 2> : kRuns<X, false, 2>)), dim3(256), 0, as_stream(stream),
+                                           (const X*)d_x, ldx, d_slots, T, k, H, R, lanes, (X*)d_xs, ldxs, d_status),
                                 "dispatch_kernel");
     });
 }
@@ -753,15 +779,21 @@ extern "C" dlrm_status dlrm_combine_bwd(const void* d_grad_y, int64_t ldgy, cons
     const bool vec = H % 8 == 0 && rows_aligned16(d_grad_y, ldgy, T, es) &&
                      (!d_grad_probs || rows_aligned16(d_ys, ldys, R, es)) &&
                      (!d_grad_ys || rows_aligned16(d_grad_ys, ldgys, R, es));
-    const CombineBwd a = {d_grad_y, d_ys, ldgy, ldys, d_slots, d_probs, T, k, H, R, d_grad_ys, ldgys, d_grad_probs, d_status};
+    // a block a token where those would leave SMs idle (16 tokens of 4096 columns, 4 each, fp16)
     const bool wide = T < num_sms() * 4 && H > 512;
-    const int64_t blocks = wide ? T : ((int64_t)T + 7) / 8, most = (int64_t)num_sms() * 8;
+    const int lanes = unit_lanes(H, vec);
+    const CombineBwd a = {d_grad_y, d_ys, ldgy, ldys, d_slots, d_probs, T, k, H, R, lanes, d_grad_ys, ldgys, d_grad_probs,
+                          d_status};
+    const int64_t blocks = wide ? T : ((int64_t)T * lanes + 255) / 256, most = (int64_t)num_sms() * 8;
     return with_type(dtype, [&](auto t) {
         using X = decltype(t);
-        auto kern = wide ? (vec ? combine_bwd_kernel<X, true, 8> : combine_bwd_kernel<X, false, 8>)
-                         : (vec ? combine_bwd_kernel<X, true, 1> : combine_bwd_kernel<X, false, 1>);
-        return check_launch_pdl(launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
-                                           as_stream(stream), a),
-                                "combine_bwd_kernel");
+        return with_choices(k, [&](auto kk) {
+            constexpr int K = decltype(kk)::value;
+            auto kern = wide ? (vec ? combine_bwd_kernel<X, true, K, 8> : combine_bwd_kernel<X, false, K, 8>)
+                             : (vec ? combine_bwd_kernel<X, true, K, 1> : combine_bwd_kernel<X, false, K, 1>);
+            return check_launch_pdl(launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
+                                               as_stream(stream), a),
+                                    "combine_bwd_kernel");
+        });
     });
 }

@@ -124,44 +124,76 @@ struct Unpack8Job {
     Packed8 src;
     int rows, cols, vec;
     void* dst;          // [rows][padded(cols)], T; for fp32 bf16, which holds every value of 8 bits
+    int blocks;
 };
 
-// The input in 8 bits read back as an operand, and beside it the weights' copy as in pack_kernel.
+// The input in 8 bits read back as an operand, and beside it the weights' copy as in pack_kernel: blocks from
+// j0.blocks on.
 template <typename T>
 __global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ Unpack8Job j0, const __grid_constant__ PackJob j1,
                                                      Overlap overlap)
 {
     using X = std::conditional_t<std::is_same_v<T, float>, bf16, T>;
     pdl_begin(overlap);
-    const int64_t n0 = (int64_t)j0.rows * ((j0.cols + 7) / 8), n1 = (int64_t)j1.rows * ((j1.cols + 7) / 8);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n0 + n1; i += (int64_t)gridDim.x * 256) {
-        const bool first = i < n0;
-        const int64_t k = first ? i : i - n0;
-        const int cols = first ? j0.cols : j1.cols, groups = (cols + 7) / 8;
-        const int64_t row = k / groups;
-        const int col = (int)(k - row * groups) * 8, n = cols - col;
-        float f[8];
-        if (first) {
-            widen_run8<T>(j0.vec && n >= 8 ? load_run8<true>(j0.src, row, col, 8) : load_run8<false>(j0.src, row, col, n), f);
-            *reinterpret_cast<uint4*>((X*)j0.dst + k * 8) = pack8<X>(f);
-        } else {
-            const T* p = (const T*)j1.src + row * j1.ld + col;
-            if (j1.vec && n >= 8) widen8<T>(load8<T, true>(p, 8), f);
-            else widen8<T>(load8<T, false>(p, n), f);
-            store_operand8<T>(j1.dst, k * 8, j1.rows * (int64_t)groups * 8, f);
+    if ((int)blockIdx.x < j0.blocks) {
+        const int64_t groups = (j0.cols + 7) / 8, n = groups * j0.rows, stride = (int64_t)j0.blocks * 256;
+        const int64_t drow = stride / groups, dg = stride - drow * groups;
+        int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / groups, g = i - row * groups;
+        while (i < n) {   // kUnpack runs at a time, whose loads are in flight together
+            constexpr int kUnpack = 4;
+            Run8 r[kUnpack];
+            int64_t at[kUnpack];
+#pragma unroll
+            for (int k = 0; k < kUnpack; ++k) {
+                at[k] = i;
+                if (i < n) {
+                    const int col = (int)g * 8, left = j0.cols - col;
+                    r[k] = j0.vec && left >= 8 ? load_run8<true>(j0.src, row, col, 8) : load_run8<false>(j0.src, row, col, left);
+                    i += stride;
+                    row += drow;
+                    g += dg;
+                    if (g >= groups) {
+                        g -= groups;
+                        ++row;
+                    }
+                } else {
+                    at[k] = n;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kUnpack; ++k)
+                if (at[k] < n) {
+                    float f[8];
+                    widen_run8<T>(r[k], f);
+                    *reinterpret_cast<uint4*>((X*)j0.dst + at[k] * 8) = pack8<X>(f);
+                }
         }
+        return;
+    }
+    const int64_t n1 = (int64_t)j1.rows * ((j1.cols + 7) / 8), stride = (int64_t)(gridDim.x - j0.blocks) * 256;
+    for (int64_t k = (int64_t)(blockIdx.x - j0.blocks) * 256 + threadIdx.x; k < n1; k += stride) {
+        const int groups = (j1.cols + 7) / 8;
+        const int64_t row = k / groups;
+        const int col = (int)(k - row * groups) * 8, n = j1.cols - col;
+        const T* p = (const T*)j1.src + row * j1.ld + col;
+        float f[8];
+        if (j1.vec && n >= 8) widen8<T>(load8<T, true>(p, 8), f);
+        else widen8<T>(load8<T, false>(p, n), f);
+        store_operand8<T>(j1.dst, k * 8, j1.rows * (int64_t)groups * 8, f);
     }
 }
 
 template <typename T>
-dlrm_status launch_unpack(const Unpack8Job& a, const PackJob& b, cudaStream_t st, Overlap overlap)
+dlrm_status launch_unpack(Unpack8Job a, const PackJob& b, cudaStream_t st, Overlap overlap)
 {
-    const int64_t runs = (int64_t)a.rows * ((a.cols + 7) / 8) + (int64_t)b.rows * ((b.cols + 7) / 8);
-    if (runs == 0) return DLRM_OK;
-    const int64_t want = (runs + 255) / 256, most = (int64_t)num_sms() * 8;
-    return check_launch_pdl(launch_pdl(unpack_kernel<T>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, a, b,
-                                       overlap),
-                            "unpack_kernel");
+    auto blocks = [](int64_t runs, int each) {
+        const int64_t want = (runs + each - 1) / each, most = (int64_t)num_sms() * 8;
+        return (int)(want < most ? want : most);
+    };
+    a.blocks = blocks((int64_t)a.rows * ((a.cols + 7) / 8), 1024);
+    const int more = blocks((int64_t)b.rows * ((b.cols + 7) / 8), 256);
+    if (a.blocks + more == 0) return DLRM_OK;
+    return check_launch_pdl(launch_pdl(unpack_kernel<T>, dim3(a.blocks + more), dim3(256), 0, st, a, b, overlap), "unpack_kernel");
 }
 
 // A matrix argument as an operand: itself, or its copy at ws of `planes` planes.
@@ -335,23 +367,44 @@ struct PreMatrix {
     const T* p;
     int64_t ld;
     using Run = Raw8<T>;
-    __device__ Run load(int r, int col, int n, bool v) const
+    __device__ Run load(int r, int col, int n, bool v, int) const
     {
         const T* q = p + r * ld + col;
         return v ? load8<T, true>(q, 8) : load8<T, false>(q, n);
     }
-    static __device__ void widen(const Run& r, float (&f)[8]) { widen8<T>(r, f); }
+    static __device__ void slope(float (&f)[8], const Run& r, int act)   // f times a'(the run)
+    {
+        float z[8];
+        widen8<T>(r, z);
+        slope8<T>(f, z, act);
+    }
 };
 
 template <typename T>
 struct PreMatrix8 {
     Packed8 m;
     using Run = Run8;
-    __device__ Run load(int r, int col, int n, bool v) const
+    // RELU asks for the sign alone, which the bytes have without their exponent
+    __device__ Run load(int r, int col, int n, bool v, int act) const
     {
-        return v ? load_run8<true>(m, r, col, 8) : load_run8<false>(m, r, col, n);
+        const bool scaled = act != DLRM_ACT_RELU;
+        return v ? load_run8<true>(m, r, col, 8, scaled) : load_run8<false>(m, r, col, n, scaled);
     }
-    static __device__ void widen(const Run& r, float (&f)[8]) { widen_run8<T>(r, f); }
+    static __device__ void slope(float (&f)[8], const Run& r, int act)
+    {
+        if (act == DLRM_ACT_RELU) {
+            const uint32_t w[2] = {r.q.x, r.q.y};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t b = w[i / 4] >> 8 * (i % 4) & 0xffu;
+                if (b - 1u >= 0x7fu && b != 0xffu) f[i] = 0.f;    // 0 or the sign bit, but for a NaN
+            }
+            return;
+        }
+        float z[8];
+        widen_run8<T>(r, z);
+        slope8<T>(f, z, act);
+    }
 };
 
 template <typename T, typename Pre>
@@ -380,7 +433,7 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const Pre pre, int act, int
                 if (rr < r1) {
                     const T* gp = dy + rr * ldg + col;
                     a[k] = v ? load8<T, true>(gp, 8) : load8<T, false>(gp, n);
-                    if (act != DLRM_ACT_NONE) b[k] = pre.load(rr, col, n, v);
+                    if (act != DLRM_ACT_NONE) b[k] = pre.load(rr, col, n, v, act);
                 }
             }
 #pragma unroll
@@ -389,11 +442,7 @@ grad_z_kernel(const T* __restrict__ dy, int64_t ldg, const Pre pre, int act, int
                 if (rr >= r1) break;
                 float f[8];
                 widen8<T>(a[k], f);
-                if (act != DLRM_ACT_NONE) {
-                    float z[8];
-                    Pre::widen(b[k], z);
-                    slope8<T>(f, z, act);
-                }
+                if (act != DLRM_ACT_NONE) Pre::slope(f, b[k], act);
                 if (drop.thr) drop8(f, drop, key, (uint32_t)rr, (uint32_t)g);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum[i] += f[i];

@@ -1,92 +1,184 @@
 // packed8.cu -- matrices to 8 bits and back: 8-bit floats with a power of two for
 // every 32 columns, so that scaling is exact and the only rounding is the one to four bits.
-// Bound by memory.  A lane has eight columns, four lanes a block of 32, whose largest
-// size they find by two shuffles.
+// Bound by memory: rows by units of lanes (row_units.cuh), several runs' loads in flight.  Four
+// lanes have a block of 32 columns, eight neighbours each.
 #include "packed8.cuh"
 #include "dlrm_block.h"
+#include "row_units.cuh"
 
 namespace dlrm {
 namespace {
 
 constexpr int kThreads8 = 256;
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads8)
-pack8_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, uint8_t* __restrict__ q, int64_t ldq,
-             uint8_t* __restrict__ exps)
+template <typename T>
+constexpr int kRuns8 = kRuns<T, true, 2>;
+
+// A value's size as it counts for its block: infinities and NaN, which become NaN, do not.
+__device__ __forceinline__ uint32_t size_bits(float& f)
 {
-    pdl_wait();
-    const int64_t groups = ((int64_t)N + kBlock8 - 1) / kBlock8 * 4, runs = groups * M;   // four a block, some past the row's end
-    const int64_t stride = (int64_t)gridDim.x * kThreads8;
+    const uint32_t b = __float_as_uint(f) & 0x7fffffffu;
+    if (b < 0x7f800000u) return b;
+    f = __uint_as_float(0x7fc00000u);
+    return 0;
+}
+
+// The exponent byte for the largest size 1.m 2^(E - 127): that is at most 448 2^(e - 127) from
+// e = E - 8 on, or E - 7 where 1.m > 1.75.
+__device__ __forceinline__ int exponent8(uint32_t top)
+{
+    return max(0, (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u));
+}
+
+__device__ __forceinline__ float scale_up(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }   // 2^(127 - e)
+
+__device__ __forceinline__ uint16_t round8(float lo, float hi)
+{
+    uint16_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+    return h;
+}
+
+// The exponent of a quad's block, and the lane's values in its scale as bytes.
+__device__ __forceinline__ int quad8(float (&f)[8], uint32_t (&w)[2])
+{
     const uint32_t quad = 0xfu << (threadIdx.x % kWarp & ~3);
-    int64_t i = (int64_t)blockIdx.x * kThreads8 + threadIdx.x;
-    int64_t row = i / groups, g = i - row * groups;
-    const int64_t drow = stride / groups, dg = stride - drow * groups;
-    while (i < runs) {   // a quad's lanes leave together: runs and stride are multiples of four
-        const int64_t col = g * 8;
-        const int n = (int)min((int64_t)8, N - col);   // 0 or less: past the row's end
-        float f[8] = {};
-        if (n > 0) widen8<T>(load8<T, VEC>(x + row * ldx + col, n), f);
-        uint32_t top = 0;
+    uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = __float_as_uint(f[j]) & 0x7fffffffu;
-            if (b >= 0x7f800000u) f[j] = __uint_as_float(0x7fc00000u);
-            else top = max(top, b);
-        }
-        top = max(top, __shfl_xor_sync(quad, top, 1));
-        top = max(top, __shfl_xor_sync(quad, top, 2));
-        // top = 1.m 2^(E - 127) is at most 448 2^(e - 127) from e = E - 8 on, or E - 7 where 1.m > 1.75
-        const int e = max(0, (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u));
-        const float up = __uint_as_float((uint32_t)(254 - e) << 23);   // 2^(127 - e)
-        if (n > 0) {
-            uint16_t h[4];
+    for (int i = 0; i < 8; ++i) top = max(top, size_bits(f[i]));
+    top = max(top, __shfl_xor_sync(quad, top, 1));
+    top = max(top, __shfl_xor_sync(quad, top, 2));
+    const int e = exponent8(top);
+    const float up = scale_up(e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[j]) : "f"(f[2 * j + 1] * up), "f"(f[2 * j] * up));
-            uint8_t* p = q + row * ldq + col;
-            if constexpr (VEC) {
-                uint2 v;
-                memcpy(&v, h, 8);
-                *reinterpret_cast<uint2*>(p) = v;
-            } else {
+    for (int i = 0; i < 2; ++i)
+        w[i] = round8(f[4 * i] * up, f[4 * i + 1] * up) | (uint32_t)round8(f[4 * i + 2] * up, f[4 * i + 3] * up) << 16;
+    return e;
+}
+
+// blocks: exponent bytes of a row
+template <typename T>
+__global__ void __launch_bounds__(kThreads8)
+pack8_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, int lanes, uint8_t* __restrict__ q, int64_t ldq,
+             uint8_t* __restrict__ exps, int blocks)
+{
+    constexpr int U = kRuns8<T>;
+    pdl_wait();
+    const Unit unit(lanes);
+    for (Items it(unit, (N + lanes * 8 * U - 1) / (lanes * 8 * U)); it.row < M; it.next()) {
+        Raw8<T> v[U];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < n) p[j] = (uint8_t)(h[j / 2] >> 8 * (j % 2));
+        for (int u = 0; u < U; ++u)
+            v[u] = load_cols<T, true>(x + it.row * ldx, unit.first<true, sizeof(T)>((int)it.part * U + u), N);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = unit.first<true, sizeof(T)>((int)it.part * U + u);
+            float f[8];
+            uint32_t w[2];
+            widen8<T>(v[u], f);
+            const int e = quad8(f, w);
+            if (c < N) {
+                *reinterpret_cast<uint2*>(q + it.row * ldq + c) = make_uint2(w[0], w[1]);
+                if (unit.l % 4 == 0) exps[it.row * blocks + c / kBlock8] = (uint8_t)e;
             }
         }
-        if (g % 4 == 0) exps[row * (groups / 4) + g / 4] = (uint8_t)e;
-        i += stride;
-        row += drow;
-        g += dg;
-        if (g >= groups) {
-            g -= groups;
-            ++row;
+    }
+}
+
+// Off the grid: the runs of all rows are one sequence, four a block; a run is read as the 16-byte words
+// that it lies in and leaves in the widest pieces that its address allows.  (Every 32nd column a lane
+// instead: 60000 x 515 bf16 62 us, where single loads of neighbours took 35.)
+template <typename T>
+__global__ void __launch_bounds__(kThreads8)
+pack8_any_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, uint8_t* __restrict__ q, int64_t ldq,
+                 uint8_t* __restrict__ exps, int blocks)
+{
+    pdl_wait();
+    const T* const end = x + (M - 1) * ldx + N;
+    const Unit unit(1);
+    for (Items it(unit, (int64_t)blocks * 4); it.row < M; it.next()) {   // a quad's lanes leave together
+        const int64_t c = it.part * 8;
+        const int n = (int)min((int64_t)8, N - c);    // 0 or less: past the row's end
+        float f[8] = {};
+        if (n > 0) {
+            widen8<T>(load8_shifted<T>(x + it.row * ldx + c, n, x, end), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i >= n) f[i] = 0.f;
         }
+        uint32_t w[2];
+        const int e = quad8(f, w);
+        uint8_t* p = q + it.row * ldq + c;
+        const uint32_t off = (uint32_t)(uintptr_t)p & 7u;
+        if (n == 8 && off == 0) {
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        } else if (n == 8 && off == 4) {
+            reinterpret_cast<uint32_t*>(p)[0] = w[0];
+            reinterpret_cast<uint32_t*>(p)[1] = w[1];
+        } else if (n == 8 && off % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i / 2] >> 16 * (i % 2));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) p[i] = (uint8_t)(w[i / 4] >> 8 * (i % 4));
+        }
+        if (it.part % 4 == 0) exps[it.row * blocks + it.part / 4] = (uint8_t)e;
     }
 }
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads8)
-unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, T* __restrict__ y, int64_t ldy)
+unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __restrict__ y, int64_t ldy)
 {
+    constexpr int U = VEC ? 4 : 1;
     pdl_wait();
-    const int64_t groups = (N - 1) / 8 + 1, runs = groups * M;
-    const int64_t stride = (int64_t)gridDim.x * kThreads8;
-    int64_t i = (int64_t)blockIdx.x * kThreads8 + threadIdx.x;
-    int64_t row = i / groups, g = i - row * groups;
-    const int64_t drow = stride / groups, dg = stride - drow * groups;
-    while (i < runs) {
-        const int col = (int)g * 8, n = N - col;
-        float f[8];
-        widen_run8<T>(load_run8<VEC>(m, row, col, n), f);
-        store8<T, VEC>(y + row * ldy + col, n, f);
-        i += stride;
-        row += drow;
-        g += dg;
-        if (g >= groups) {
-            g -= groups;
-            ++row;
+    const Unit unit(lanes);
+    const int lane = threadIdx.x % kWarp;
+    for (Items it(unit, (N + lanes * 8 * U - 1) / (lanes * 8 * U)); it.row < M; it.next()) {
+        Run8 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!unit.has<VEC>((int)it.part * U + u, N)) break;
+            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
+            if constexpr (VEC) {
+                if (c < N) v[u] = load_run8<true>(m, it.row, c, 8);
+            } else {
+                const uint8_t* row = m.q + it.row * m.ld;
+                const bool words = sizeof(T) == 2 && ((uintptr_t)row & 1u) == 0;
+                uint32_t w[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int x = run_col<VEC, sizeof(T)>(c, 2 * i), z = run_col<VEC, sizeof(T)>(c, 2 * i + 1);
+                    uint32_t h = 0;
+                    if (words && z < N) {
+                        h = __ldg(reinterpret_cast<const uint16_t*>(row + x));
+                    } else {
+                        if (x < N) h = __ldg(row + x);
+                        if (z < N) h |= (uint32_t)__ldg(row + z) << 8;
+                    }
+                    w[i / 2] |= h << 16 * (i % 2);
+                }
+                v[u].q = make_uint2(w[0], w[1]);
+                const int64_t b = (it.part * U + u) * 8 + lane;   // lane i has the run's i-th block's exponent
+                v[u].e = lane < 8 && b < m.blocks ? __ldg(m.exps + it.row * m.blocks + b) : 0;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!unit.has<VEC>((int)it.part * U + u, N)) break;
+            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
+            float f[8];
+            if constexpr (VEC) {
+                widen_run8<T>(v[u], f);
+            } else {
+                float scale[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    scale[i] = scale8(__shfl_sync(~0u, v[u].e, sizeof(T) == 4 ? i : i / 2 * 2 + lane / 16));
+                widen_codes8<T>(v[u].q, scale, f);
+            }
+            store_cols<T, VEC>(y + it.row * ldy, c, N, f);
         }
     }
 }
@@ -97,12 +189,6 @@ dlrm_status check_sizes8(const char* fn, dlrm_dtype dtype, int M, int N)
     if (M < 0 || N < 1) return fail(DLRM_ERR_INVALID_ARG, "%s: need M >= 0 and N >= 1", fn);
     if (M > kMaxSize || N > kMaxSize) return fail(DLRM_ERR_UNSUPPORTED, "%s: sizes up to %d", fn, kMaxSize);
     return DLRM_OK;
-}
-
-inline unsigned blocks_for(int64_t runs)
-{
-    const int64_t want = (runs + kThreads8 - 1) / kThreads8, most = (int64_t)num_sms() * 8;
-    return (unsigned)(want < most ? want : most);
 }
 
 }  // namespace
@@ -124,10 +210,14 @@ extern "C" dlrm_status dlrm_pack8(const void* d_x, int64_t ldx, dlrm_dtype dtype
     const bool vec = N % 8 == 0 && rows_aligned16(d_x, ldx, M, es) && rows_aligned8(d_q, ldq, M);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        auto kern = vec ? pack8_kernel<T, true> : pack8_kernel<T, false>;
-        return check_launch_pdl(launch_pdl(kern, dim3(blocks_for((int64_t)M * blocks8(N) * 4)), dim3(kThreads8), 0,
-                                           as_stream(stream), (const T*)d_x, ldx, M, N, d_q, ldq, d_exps),
-                                "pack8_kernel");
+        const int lanes = unit_lanes(N, true, 4), blocks = blocks8(N);   // a block's four lanes at least
+        if (vec)
+            return check_launch_pdl(launch_pdl(pack8_kernel<T>, dim3(item_blocks(M, N, lanes, kRuns8<T>)), dim3(kThreads8), 0,
+                                               as_stream(stream), (const T*)d_x, ldx, M, N, lanes, d_q, ldq, d_exps, blocks),
+                                    "pack8_kernel");
+        return check_launch_pdl(launch_pdl(pack8_any_kernel<T>, dim3(item_blocks(M, blocks * kBlock8, 1, 1)), dim3(kThreads8),
+                                           0, as_stream(stream), (const T*)d_x, ldx, M, N, d_q, ldq, d_exps, blocks),
+                                "pack8_any_kernel");
     });
 }
 
@@ -147,8 +237,9 @@ extern "C" dlrm_status dlrm_unpack8(const uint8_t* d_q, int64_t ldq, const uint8
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
         auto kern = vec ? unpack8_kernel<T, true> : unpack8_kernel<T, false>;
-        return check_launch_pdl(launch_pdl(kern, dim3(blocks_for((int64_t)M * ((N - 1) / 8 + 1))), dim3(kThreads8), 0,
-                                           as_stream(stream), m, M, N, (T*)d_y, ldy),
+        const int lanes = unit_lanes(N, vec);
+        return check_launch_pdl(launch_pdl(kern, dim3(item_blocks(M, N, lanes, vec ? 4 : 1)), dim3(kThreads8), 0, as_stream(stream), m, M,
+                                           N, lanes, (T*)d_y, ldy),
                                 "unpack8_kernel");
     });
 }

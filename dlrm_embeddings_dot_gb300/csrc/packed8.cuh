@@ -23,8 +23,9 @@ struct Run8 {
 };
 
 // VEC: the run starts on an 8-byte boundary and has all eight columns; the others read as 0.
+// scaled: with the exponent.
 template <bool VEC>
-__device__ __forceinline__ Run8 load_run8(const Packed8& m, int64_t row, int col, int n)
+__device__ __forceinline__ Run8 load_run8(const Packed8& m, int64_t row, int col, int n, bool scaled = true)
 {
     Run8 r;
     const uint8_t* p = m.q + row * m.ld + col;
@@ -36,7 +37,7 @@ __device__ __forceinline__ Run8 load_run8(const Packed8& m, int64_t row, int col
         for (int i = 0; i < 8; ++i) b[i] = i < n ? __ldg(p + i) : 0;
         memcpy(&r.q, b, 8);
     }
-    r.e = __ldg(m.exps + row * m.blocks + col / kBlock8);
+    r.e = scaled ? __ldg(m.exps + row * m.blocks + col / kBlock8) : 0;
     return r;
 }
 
@@ -44,12 +45,14 @@ __device__ __forceinline__ Run8 load_run8(const Packed8& m, int64_t row, int col
 template <typename T>
 constexpr float kMost8 = std::is_same_v<T, __half> ? 65504.f : 3.3895313892515355e38f;
 
-// q 2^(e - 127), exact in fp32
+// 2^(e - 127), below fp32's normal numbers too
+__device__ __forceinline__ float scale8(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x00400000u); }
+
+// q scale, exact in fp32, a scale for each column
 template <typename T>
-__device__ __forceinline__ void widen_run8(const Run8& r, float (&f)[8])
+__device__ __forceinline__ void widen_codes8(const uint2& q, const float (&scale)[8], float (&f)[8])
 {
-    const float scale = __uint_as_float(r.e ? r.e << 23 : 0x00400000u);
-    const uint32_t w[2] = {r.q.x, r.q.y};
+    const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t h;
@@ -57,12 +60,21 @@ __device__ __forceinline__ void widen_run8(const Run8& r, float (&f)[8])
         __half2 v;
         memcpy(&v, &h, 4);
         const float2 g = __half22float2(v);
-        f[2 * i] = g.x * scale;
-        f[2 * i + 1] = g.y * scale;
+        f[2 * i] = g.x * scale[2 * i];
+        f[2 * i + 1] = g.y * scale[2 * i + 1];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (fabsf(f[i]) > kMost8<T>) f[i] = copysignf(kMost8<T>, f[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ void widen_run8(const Run8& r, float (&f)[8])
+{
+    float scale[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) scale[i] = scale8(r.e);
+    widen_codes8<T>(r.q, scale, f);
 }
 
 // Whether runs of eight columns start on 8-byte boundaries in every row.

@@ -1,0 +1,155 @@
+// row_units.cuh -- how kernels that pass over rows once share them out: a unit of threads takes part
+// of a row, several runs of eight columns a lane.
+#pragma once
+
+#include "dense_ops.cuh"
+
+namespace dlrm {
+
+// A lane's run of eight columns of a row, ES the element's size: on the 16-byte grid (VEC) eight
+// neighbours, off it every 32nd column of 256, or pair of them, so that a warp's accesses stay whole.
+template <bool VEC, int ES>
+__device__ __forceinline__ int run_col(int first, int i)
+{
+    return first + (VEC ? i : ES == 2 ? i / 2 * 64 + i % 2 : i * 32);
+}
+
+// A unit of `lanes` threads (on the grid a power of two up to a warp, as many as a row has runs; else
+// a warp) takes U runs a lane of one row at a time, whose loads are in flight together.
+struct Unit {
+    int lanes, l;                 // the unit's threads, and which of them this is
+    int64_t units, unit;          // in the grid
+    __device__ explicit Unit(int n) : lanes(n), l((int)threadIdx.x % n)
+    {
+        const int per = blockDim.x / n;
+        units = (int64_t)gridDim.x * per;
+        unit = (int64_t)blockIdx.x * per + threadIdx.x / n;
+    }
+    // the first column of the lane's run-th run of a row
+    template <bool VEC, int ES>
+    __device__ __forceinline__ int first(int run) const
+    {
+        return VEC ? (run * lanes + l) * 8 : run * 256 + l * (ES == 2 ? 2 : 1);
+    }
+    // whether the run-th run of any of the unit's lanes has columns of a row
+    template <bool VEC>
+    __device__ __forceinline__ bool has(int run, int H) const { return VEC || run * 256 < H; }
+};
+
+// Runs a lane takes at once: as many as eight 16-byte words hold for K rows; off the grid one, whose
+// single loads are as many (sums of two rows 40000 x 515 fp16: one run 41 us, four 62).
+template <typename T, bool VEC, int K>
+constexpr int kRuns = VEC && 16 / (K * (int)sizeof(T)) > 1 ? 16 / (K * (int)sizeof(T)) : 1;
+
+// Whether two neighbouring 2-byte elements of a row are one 4-byte word.
+__device__ __forceinline__ bool row_of_words(const void* row) { return ((uintptr_t)row & 3u) == 0; }
+
+// The run's columns of a row; columns past its end read as 0 and are not stored.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw8<T> load_cols(const T* row, int first, int H)
+{
+    Raw8<T> r = {};
+    if constexpr (VEC) {
+        if (first < H) r = load8<T, true>(row + first, 8);
+    } else if constexpr (sizeof(T) == 2) {
+        uint32_t* const w = &r.w[0].x;
+        const T* p = row + first;
+        if (row_of_words(row)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (first + 64 * i + 1 < H) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + 32 * i);
+                else if (first + 64 * i < H) w[i] = __ldg(reinterpret_cast<const uint16_t*>(p) + 64 * i);
+            }
+        } else {
+            uint16_t e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                e[i] = run_col<false, 2>(first, i) < H ? __ldg(reinterpret_cast<const uint16_t*>(p) + run_col<false, 2>(0, i)) : 0;
+            memcpy(w, e, 16);
+        }
+    } else {
+        float e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = first + 32 * i < H ? __ldg(row + first + 32 * i) : 0.f;
+        memcpy(&r, e, 32);
+    }
+    return r;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_raw(T* row, int first, int H, const Raw8<T>& r)
+{
+    T* p = row + first;
+    if constexpr (VEC) {
+        if (first < H)
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+    } else if constexpr (sizeof(T) == 2) {
+        uint32_t w[4];
+        memcpy(w, &r, 16);
+        const bool words = row_of_words(row);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (words && first + 64 * i + 1 < H) {
+                reinterpret_cast<uint32_t*>(p)[32 * i] = w[i];
+            } else {
+                if (first + 64 * i < H) reinterpret_cast<uint16_t*>(p)[64 * i] = (uint16_t)w[i];
+                if (first + 64 * i + 1 < H) reinterpret_cast<uint16_t*>(p)[64 * i + 1] = (uint16_t)(w[i] >> 16);
+            }
+        }
+    } else {
+        float e[8];
+        memcpy(e, &r, 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (first + 32 * i < H) p[32 * i] = e[i];
+    }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_cols(T* row, int first, int H, const float (&f)[8])
+{
+    Raw8<T> r;
+    if constexpr (sizeof(T) == 2) r.w[0] = pack8<T>(f);
+    else memcpy(&r, f, 32);
+    store_raw<T, VEC>(row, first, H, r);
+}
+
+// Walks (row, part of the row) pairs, a unit at a time, without a division after the first.
+struct Items {
+    int64_t row, part, parts, drow, dpart;
+    __device__ Items(const Unit& u, int64_t p) : parts(p)
+    {
+        row = u.unit / p;
+        part = u.unit - row * p;
+        drow = u.units / p;
+        dpart = u.units - drow * p;
+    }
+    __device__ void next()
+    {
+        row += drow;
+        part += dpart;
+        if (part >= parts) {
+            part -= parts;
+            ++row;
+        }
+    }
+};
+
+// ---------------------------------------------------------------- host side
+// The lanes of a unit, and the blocks of 256 threads for rows taken in parts of `runs` runs a lane.
+inline int unit_lanes(int H, bool vec, int least = 1)
+{
+    int n = vec ? least : kWarp;
+    while (n < kWarp && n * 8 < H) n *= 2;
+    return n;
+}
+
+inline unsigned item_blocks(int64_t rows, int H, int lanes, int runs)
+{
+    const int64_t part = (int64_t)lanes * 8 * runs, want = (rows * ((H + part - 1) / part) * lanes + 255) / 256;
+    const int64_t most = (int64_t)num_sms() * 8;
+    return (unsigned)(want < most ? want : most);
+}
+
+}  // namespace dlrm
