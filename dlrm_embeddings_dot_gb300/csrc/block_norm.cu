@@ -54,7 +54,7 @@ struct Ring {
     uint32_t at;      // its shared address
     int N, first;
 
-    __device__ Ring(uint8_t* smem, int n, int f) : mine(smem + threadIdx.x * 16), N(n), first(f)
+    __device__ Ring(uint8_t* smem, int n, int f, int) : mine(smem + threadIdx.x * 16), N(n), first(f)
     {
         at = (uint32_t)__cvta_generic_to_shared(mine);
         for (int i = 0; i < kAhead * NT * kWords; ++i)
@@ -99,10 +99,11 @@ struct Ring<T, false, NT, THREADS> {
     uint32_t at;
     int N, first, from, bytes;   // from: the warp's first column; bytes of its columns, 0 or less: none
 
-    __device__ Ring(uint8_t* smem, int n, int f) : mine(smem + threadIdx.x / kWarp * kWords * 16), N(n), first(f)
+    // f0: the row's warp's number times 256
+    __device__ Ring(uint8_t* smem, int n, int f, int f0) : N(n), first(f), from(f0)
     {
+        mine = smem + __shfl_sync(~0u, (int)threadIdx.x / kWarp, 0) * kWords * 16;
         at = (uint32_t)__cvta_generic_to_shared(mine);
-        from = first / 256 * 256;
         bytes = min(256, N - from) * (int)sizeof(T);
         // columns past the end: what lies behind the last word, and all of a warp without columns
         const int lane = threadIdx.x % kWarp;
@@ -119,6 +120,12 @@ struct Ring<T, false, NT, THREADS> {
         const uint8_t* p = reinterpret_cast<const uint8_t*>(row + from);
         const int off = (int)((uintptr_t)p & 15), end = off + bytes;
         const int lane = threadIdx.x % kWarp;
+        if (bytes == 256 * (int)sizeof(T) && (at_row + from) * (int)sizeof(T) >= off) {   // as nearly always
+#pragma unroll
+            for (int i = 0; i < kWords / kWarp; ++i) copy16(to + (lane + kWarp * i) * 16, p - off + (lane + kWarp * i) * 16, 16);
+            if (lane == 0 && off) copy16(to + (kWords - 1) * 16, p - off + (kWords - 1) * 16, off);
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < (kWords + kWarp - 1) / kWarp; ++i) {
             const int w = lane + kWarp * i;
@@ -161,7 +168,7 @@ struct Ring<T, false, NT, THREADS> {
 };
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_run(T* row, int first, int N, const float2 (&v)[4])
+__device__ __forceinline__ void store_run(T* row, int first, int N, bool full, const float2 (&v)[4])
 {
     if constexpr (VEC) {
         float f[8];
@@ -172,27 +179,39 @@ __device__ __forceinline__ void store_run(T* row, int first, int N, const float2
         }
         if (first < N) store8<T, true>(row + first, 8, f);
     } else if constexpr (sizeof(T) == 2) {
-        const bool words = ((uintptr_t)row & 3) == 0;
+        T* const p = row + first;
+        if (full && row_of_words(row)) {
+            float f[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = run_col<false, 2>(first, 2 * i);
-            const T a = from_f32<T>(v[i].x), b = from_f32<T>(v[i].y);
-            if (words && c + 1 < N) {
-                uint16_t x, y;
-                memcpy(&x, &a, 2);
-                memcpy(&y, &b, 2);
-                *reinterpret_cast<uint32_t*>(row + c) = (uint32_t)y << 16 | x;
-            } else {
-                if (c < N) row[c] = a;
-                if (c + 1 < N) row[c + 1] = b;
+            for (int i = 0; i < 4; ++i) {
+                f[2 * i] = v[i].x;
+                f[2 * i + 1] = v[i].y;
+            }
+            const uint4 w = pack8<T>(f);
+            uint32_t* const q = reinterpret_cast<uint32_t*>(p);
+            q[0] = w.x;
+            q[32] = w.y;
+            q[64] = w.z;
+            q[96] = w.w;
+        } else if (full) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p[64 * i] = from_f32<T>(v[i].x);
+                p[64 * i + 1] = from_f32<T>(v[i].y);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (first + 64 * i < N) p[64 * i] = from_f32<T>(v[i].x);
+                if (first + 64 * i + 1 < N) p[64 * i + 1] = from_f32<T>(v[i].y);
             }
         }
     } else {
+        T* const p = row + first;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = run_col<false, 4>(first, 2 * i), d = run_col<false, 4>(first, 2 * i + 1);
-            if (c < N) row[c] = v[i].x;
-            if (d < N) row[d] = v[i].y;
+            if (full || first + 64 * i < N) p[64 * i] = v[i].x;
+            if (full || first + 64 * i + 32 < N) p[64 * i + 32] = v[i].y;
         }
     }
 }
@@ -215,7 +234,7 @@ template <bool VEC, int ES>
 __device__ __forceinline__ void store_vector(float* p, int first, int N, const float2 (&v)[4])
 {
     if constexpr (VEC) {
-        store_run<float, true>(p, first, N, v);
+        store_run<float, true>(p, first, N, false, v);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -321,17 +340,22 @@ struct NormFwd {
 
 // (mean, 1 / sqrt(mean square + eps)) of a row; f becomes what is left without the mean, 0 past the end
 template <bool VEC, int ES, int W>
-__device__ __forceinline__ float2 centre(float2 (&f)[4], int first, const NormFwd& a, float* red, int& turn, int warp)
+__device__ __forceinline__ float2 centre(float2 (&f)[4], int first, bool full, const NormFwd& a, float* red, int& turn, int warp)
 {
     float s[1], mean = 0.f;
     if (a.layer) {
         s[0] = add_up(f);
         row_sum<W>(s, red, turn, warp);
         mean = s[0] * a.inv_n;
+        if (full) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i].x = run_col<VEC, ES>(first, 2 * i) < a.N ? f[i].x - mean : 0.f;
-            f[i].y = run_col<VEC, ES>(first, 2 * i + 1) < a.N ? f[i].y - mean : 0.f;
+            for (int i = 0; i < 4; ++i) f[i] = __fadd2_rn(f[i], both(-mean));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[i].x = run_col<VEC, ES>(first, 2 * i) < a.N ? f[i].x - mean : 0.f;
+                f[i].y = run_col<VEC, ES>(first, 2 * i + 1) < a.N ? f[i].y - mean : 0.f;
+            }
         }
     }
     float2 q = __fmul2_rn(f[0], f[0]);
@@ -352,10 +376,12 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
     pdl_wait();
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, N = a.N;
+    // the same in all lanes, so that what depends on the row alone takes the uniform datapath
+    const int warp = __shfl_sync(~0u, (int)threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp, N = a.N;
+    const bool full = warp % W * 256 + 256 <= N;   // all columns of the warp are in the row
     const int first = run_first<VEC, sizeof(T)>(warp % W, lane);
     int turn = 0;
-    const R ring(smem, N, first);
+    const R ring(smem, N, first, warp % W * 256);
     float2 aw[4], ab[4], wp[4], bp[4];   // scale w_post, scale b_post, w_pre, b_pre
     load_vector<VEC, sizeof(T)>(a.scale, first, N, 1.f, wp);
     load_vector<VEC, sizeof(T)>(a.w_post, first, N, 1.f, aw);
@@ -405,7 +431,7 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) g[i] = both(g1);
             }
-            const float2 s = centre<VEC, sizeof(T), W>(f, first, a, red, turn, warp);
+            const float2 s = centre<VEC, sizeof(T), W>(f, first, full, a, red, turn, warp);
             st.x = s.x;
             st.y = s.y;
 #pragma unroll
@@ -413,15 +439,15 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
                 const float2 u = __ffma2_rn(__fmul2_rn(f[i], both(s.y)), aw[i], ab[i]);   // scale u
                 r[i] = __ffma2_rn(u, g[i], r[i]);
             }
-            store_run<T, VEC>((T*)a.r + row * a.ldr, first, N, r);
+            store_run<T, VEC>((T*)a.r + row * a.ldr, first, N, full, r);
         }
         if (a.h) {
-            const float2 s = centre<VEC, sizeof(T), W>(r, first, a, red, turn, warp);
+            const float2 s = centre<VEC, sizeof(T), W>(r, first, full, a, red, turn, warp);
             st.z = s.x;
             st.w = s.y;
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] = __ffma2_rn(__fmul2_rn(r[i], both(s.y)), wp[i], bp[i]);
-            store_run<T, VEC>((T*)a.h + row * a.ldh, first, N, r);
+            store_run<T, VEC>((T*)a.h + row * a.ldh, first, N, full, r);
         }
         if (a.stats && warp % W == 0 && lane == 0) a.stats[row] = st;
         R::done();
@@ -503,10 +529,12 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
     pdl_wait();
-    const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, N = a.N;
+    // the same in all lanes, so that what depends on the row alone takes the uniform datapath
+    const int warp = __shfl_sync(~0u, (int)threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp, N = a.N;
+    const bool full = warp % W * 256 + 256 <= N;   // all columns of the warp are in the row
     const int first = run_first<VEC, sizeof(T)>(warp % W, lane);
     int turn = 0;
-    const Rg ring(smem, N, first);
+    const Rg ring(smem, N, first, warp % W * 256);
     float2 aw[4], ab[4], wp[4];   // scale w_post, scale b_post, w_pre; 0 past the row's end
     load_vector<VEC, sizeof(T)>(a.scale, first, N, 1.f, wp);
     load_vector<VEC, sizeof(T)>(a.w_post, first, N, 1.f, aw);
@@ -581,7 +609,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
             for (int i = 0; i < 4; ++i)
                 dr[i] = __ffma2_rn(__ffma2_rn(x[i], both(c0), __fadd2_rn(d[i], both(c1))), both(st.w), dr[i]);
         }
-        if (a.gres) store_run<T, VEC>((T*)a.gres + row * a.ldgres, first, N, dr);
+        if (a.gres) store_run<T, VEC>((T*)a.gres + row * a.ldgres, first, N, full, dr);
         if (POST) {
             float2 x[4], g[4], k[4], p, q, t = both(0.f);
             ring.read(stage, kY, (const T*)a.y + row * a.ldy, x);
@@ -617,7 +645,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
                 p = i ? __ffma2_rn(dr[i], x[i], p) : __fmul2_rn(dr[i], x[i]);
                 q = i ? __fadd2_rn(dr[i], q) : dr[i];
             }
-            if (a.gg && a.gate_cols > 1) store_run<T, VEC>((T*)a.gg + row * a.ldgg, first, N, k);
+            if (a.gg && a.gate_cols > 1) store_run<T, VEC>((T*)a.gg + row * a.ldgg, first, N, full, k);
             float c0, c1 = 0.f;
             if (a.layer) {
                 float c[2] = {p.x + p.y, q.x + q.y};
@@ -638,7 +666,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     dr[i] = __fmul2_rn(__ffma2_rn(x[i], both(c0), __fadd2_rn(dr[i], both(c1))), both(st.y));
-                store_run<T, VEC>((T*)a.gy + row * a.ldgy, first, N, dr);
+                store_run<T, VEC>((T*)a.gy + row * a.ldgy, first, N, full, dr);
             }
         }
         Rg::done();

@@ -172,11 +172,21 @@ unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __
             if constexpr (VEC) {
                 widen_run8<T>(v[u], f);
             } else {
-                float scale[8];
+                const float own = scale8(v[u].e);
+                if constexpr (sizeof(T) == 2) {
+                    float scale[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    scale[i] = scale8(__shfl_sync(~0u, v[u].e, sizeof(T) == 4 ? i : i / 2 * 2 + lane / 16));
-                widen_codes8<T>(v[u].q, scale, f);
+                    for (int i = 0; i < 4; ++i) scale[i] = __shfl_sync(~0u, own, 2 * i + lane / 16);
+                    widen_codes8<T>(v[u].q, scale, f);
+                } else {   // a scale each: the values without it, then it
+                    const float one[4] = {1.f, 1.f, 1.f, 1.f};
+                    widen_codes8<T>(v[u].q, one, f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        f[i] *= __shfl_sync(~0u, own, i);
+                        if (fabsf(f[i]) > kMost8<T>) f[i] = copysignf(kMost8<T>, f[i]);
+                    }
+                }
             }
             store_cols<T, VEC>(y + it.row * ldy, c, N, f);
         }

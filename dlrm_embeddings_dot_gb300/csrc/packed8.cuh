@@ -48,9 +48,13 @@ constexpr float kMost8 = std::is_same_v<T, __half> ? 65504.f : 3.389531389251535
 // 2^(e - 127), below fp32's normal numbers too
 __device__ __forceinline__ float scale8(uint32_t e) { return __uint_as_float(e ? e << 23 : 0x00400000u); }
 
-// q scale, exact in fp32, a scale for each column
+// The largest scale under which no value passes kMost8: 448 2^7, or 448 2^119.
 template <typename T>
-__device__ __forceinline__ void widen_codes8(const uint2& q, const float (&scale)[8], float (&f)[8])
+constexpr float kSafe8 = std::is_same_v<T, __half> ? 128.f : 0x1p119f;
+
+// q scale, exact in fp32, a scale for each pair of columns
+template <typename T>
+__device__ __forceinline__ void widen_codes8(const uint2& q, const float (&scale)[4], float (&f)[8])
 {
     const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
@@ -60,20 +64,19 @@ __device__ __forceinline__ void widen_codes8(const uint2& q, const float (&scale
         __half2 v;
         memcpy(&v, &h, 4);
         const float2 g = __half22float2(v);
-        f[2 * i] = g.x * scale[2 * i];
-        f[2 * i + 1] = g.y * scale[2 * i + 1];
+        f[2 * i] = g.x * scale[i];
+        f[2 * i + 1] = g.y * scale[i];
     }
+    if (fmaxf(fmaxf(scale[0], scale[1]), fmaxf(scale[2], scale[3])) > kSafe8<T>)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (fabsf(f[i]) > kMost8<T>) f[i] = copysignf(kMost8<T>, f[i]);
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(f[i]) > kMost8<T>) f[i] = copysignf(kMost8<T>, f[i]);
 }
 
 template <typename T>
 __device__ __forceinline__ void widen_run8(const Run8& r, float (&f)[8])
 {
-    float scale[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) scale[i] = scale8(r.e);
+    const float s = scale8(r.e), scale[4] = {s, s, s, s};
     widen_codes8<T>(r.q, scale, f);
 }
 
