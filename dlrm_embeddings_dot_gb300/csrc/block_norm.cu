@@ -33,6 +33,20 @@ __device__ __forceinline__ int run_first(int warp, int lane)
     return warp * 256 + lane * (VEC ? 8 : ES == 2 ? 2 : 1);
 }
 
+// A tensor's row that a group of warps is at, stepped from one of its rows to the next.
+template <typename T>
+struct Cursor {
+    const T *base, *row;
+    int64_t inc;
+    __device__ Cursor(const void* p, int64_t ld, int64_t row0, int64_t step)
+        : base((const T*)p), row((const T*)p + row0 * ld), inc(step * ld)
+    {
+    }
+    __device__ __forceinline__ const T* ahead(int rows) const { return row + rows * inc; }
+    __device__ __forceinline__ T* out() const { return const_cast<T*>(row); }
+    __device__ __forceinline__ void next() { row += inc; }
+};
+
 // The rows to come: kAhead rows of NT tensors, three where the blocks that share an SM (two of
 // 256 threads, one of more) have the memory.  Columns past the row's end are 0.
 template <int STAGE, int THREADS>
@@ -60,10 +74,11 @@ struct Ring {
         for (int i = 0; i < kAhead * NT * kWords; ++i)
             *reinterpret_cast<uint4*>(mine + i * THREADS * 16) = make_uint4(0, 0, 0, 0);
     }
-    // Starts the copy of the row at m + off to a slot.
-    __device__ __forceinline__ void fetch(int stage, int slot, const T* m, int64_t off) const
+    // Starts the copy of a tensor's row `rows` ahead to a slot.  inner: words that hold a part of the
+    // row are in the matrix as a whole.
+    __device__ __forceinline__ void fetch(int stage, int slot, const Cursor<T>& c, int rows, bool) const
     {
-        const T* row = m + off;
+        const T* row = c.ahead(rows);
         const uint32_t to = at + stage * kStage + slot * kSlot;
         if (first < N)
 #pragma unroll
@@ -88,10 +103,11 @@ struct Ring {
 };
 
 // Off the grid: a warp's 256 columns lie in 16 ES + 1 aligned words at most, which its lanes copy.
-// The last word ends with the row; one that begins before the matrix is put together from its elements.
+// Near the matrix's ends the last word is cut there, and one that begins before the matrix is put
+// together from its elements.
 template <typename T, int NT, int THREADS>
 struct Ring<T, false, NT, THREADS> {
-    static constexpr int kWords = 16 * sizeof(T) + 1, kSlot = THREADS / kWarp * kWords * 16, kStage = NT * kSlot;
+    static constexpr int kES = sizeof(T), kWords = 16 * kES + 1, kSlot = THREADS / kWarp * kWords * 16, kStage = NT * kSlot;
     static constexpr int kAhead = kRowsAhead<kStage, THREADS>;
     static_assert(kAhead >= 1, "a row fits");
     static constexpr size_t kBytes = (size_t)kAhead * kStage;
@@ -104,40 +120,25 @@ struct Ring<T, false, NT, THREADS> {
     {
         mine = smem + __shfl_sync(~0u, (int)threadIdx.x / kWarp, 0) * kWords * 16;
         at = (uint32_t)__cvta_generic_to_shared(mine);
-        bytes = min(256, N - from) * (int)sizeof(T);
-        // columns past the end: what lies behind the last word, and all of a warp without columns
-        const int lane = threadIdx.x % kWarp;
-        for (int s = 0; s < kAhead * NT; ++s)
-            for (int w = lane; w < kWords; w += kWarp)
-                *reinterpret_cast<uint4*>(mine + s * kSlot + w * 16) = make_uint4(0, 0, 0, 0);
-        __syncwarp();
+        bytes = min(256, N - from) * kES;
     }
-    __device__ __forceinline__ void fetch(int stage, int slot, const T* m, int64_t at_row) const
+    __device__ __forceinline__ void fetch(int stage, int slot, const Cursor<T>& c, int rows, bool inner) const
     {
-        if (bytes <= 0) return;
-        const T* row = m + at_row;
-        const uint32_t to = at + stage * kStage + slot * kSlot;
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(row + from);
-        const int off = (int)((uintptr_t)p & 15), end = off + bytes;
         const int lane = threadIdx.x % kWarp;
-        if (bytes == 256 * (int)sizeof(T) && (at_row + from) * (int)sizeof(T) >= off) {   // as nearly always
+        const uint32_t to = at + stage * kStage + slot * kSlot + lane * 16;
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(c.ahead(rows) + from);
+        const int off = (int)((uintptr_t)p & 15), end = off + bytes;
+        const uint8_t* word = p - off + lane * 16;
+        if (inner) {
 #pragma unroll
-            for (int i = 0; i < kWords / kWarp; ++i) copy16(to + (lane + kWarp * i) * 16, p - off + (lane + kWarp * i) * 16, 16);
-            if (lane == 0 && off) copy16(to + (kWords - 1) * 16, p - off + (kWords - 1) * 16, off);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < (kWords + kWarp - 1) / kWarp; ++i) {
-            const int w = lane + kWarp * i;
-            if (w < kWords) {   // words behind the row become 0
-                if (w > 0 || (at_row + from) * (int)sizeof(T) >= off) {
-                    copy16(to + w * 16, w * 16 < end ? p - off + w * 16 : p - off, max(0, min(16, end - w * 16)));
-                } else {
-                    T* word = reinterpret_cast<T*>(mine + stage * kStage + slot * kSlot);
-                    for (int e = off / (int)sizeof(T); e < min(16, end) / (int)sizeof(T); ++e)
-                        word[e] = __ldg(row + e - off / (int)sizeof(T));
-                }
-            }
+            for (int i = 0; i < (kWords + kWarp - 1) / kWarp; ++i)
+                if ((lane + kWarp * i) * 16 < end) copy16(to + kWarp * 16 * i, word + kWarp * 16 * i, 16);
+        } else if (bytes > 0) {
+            const bool cut = (uintptr_t)(p - off) < (uintptr_t)c.base;
+            for (int w = lane; w * 16 < end; w += kWarp)
+                if (w > 0 || !cut) copy16(to + (w - lane) * 16, p - off + w * 16, min(16, end - w * 16));
+            if (cut && lane >= off / kES && lane < min(16, end) / kES)
+                reinterpret_cast<T*>(mine + stage * kStage + slot * kSlot)[lane] = __ldg(reinterpret_cast<const T*>(p) + lane - off / kES);
         }
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -149,19 +150,16 @@ struct Ring<T, false, NT, THREADS> {
     static __device__ __forceinline__ void done() { __syncwarp(); }   // all lanes have read the row
     __device__ __forceinline__ void read(int stage, int slot, const T* row, float2 (&f)[4]) const
     {
-        const uint8_t* p = mine + stage * kStage + slot * kSlot + ((uintptr_t)(row + from) & 15) +
-                           (first - from) * (int)sizeof(T);
+        const uint8_t* p = mine + stage * kStage + slot * kSlot + ((uintptr_t)(row + from) & 15) + (first - from) * kES;
+        const T* e = reinterpret_cast<const T*>(p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                f[i] = make_float2(*reinterpret_cast<const float*>(p + 256 * i), *reinterpret_cast<const float*>(p + 256 * i + 128));
-            } else if (((uintptr_t)row & 3) == 0) {
-                const uint32_t w = *reinterpret_cast<const uint32_t*>(p + 128 * i);
-                T e[2];
-                memcpy(e, &w, 4);
-                f[i] = make_float2(to_f32(e[0]), to_f32(e[1]));
-            } else {
-                f[i] = make_float2(to_f32(*reinterpret_cast<const T*>(p + 128 * i)), to_f32(*reinterpret_cast<const T*>(p + 128 * i + 2)));
+        for (int i = 0; i < 4; ++i)
+            f[i] = make_float2(to_f32(e[run_col<false, kES>(0, 2 * i)]), to_f32(e[run_col<false, kES>(0, 2 * i + 1)]));
+        if (bytes < 256 * kES) {   // what is left there from other rows
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[i].x = run_col<false, kES>(first, 2 * i) < N ? f[i].x : 0.f;
+                f[i].y = run_col<false, kES>(first, 2 * i + 1) < N ? f[i].y : 0.f;
             }
         }
     }
@@ -331,7 +329,7 @@ struct NormFwd {
     int64_t ldy, ldg, ldres;
     int gate_cols;                   // 0: no gate
     const float *w_post, *b_post, *scale, *w_pre, *b_pre;
-    int M, N, layer, gate_act;
+    int M, N, margin, layer, gate_act;   // margin: rows at the matrices' ends that do not have 16 bytes of them beyond
     float eps, inv_n;
     void *r, *h;
     int64_t ldr, ldh;
@@ -395,31 +393,35 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
     load_vector<VEC, sizeof(T)>(a.b_pre, first, N, 0.f, bp);
     const int64_t step = (int64_t)gridDim.x * G;
     const int64_t row0 = (int64_t)blockIdx.x * G + warp / W;
-    auto fetch = [&](int stage, int64_t row) {
-        if (row < a.M) {
-            if (a.y) ring.fetch(stage, 0, (const T*)a.y, row * a.ldy);
-            if (a.gate_cols > 1) ring.fetch(stage, 1, (const T*)a.gate, row * a.ldg);
-            if (a.res) ring.fetch(stage, 2, (const T*)a.res, row * a.ldres);
+    Cursor<T> cy(a.y, a.ldy, row0, step), cg(a.gate, a.ldg, row0, step), cres(a.res, a.ldres, row0, step),
+        cr(a.r, a.ldr, row0, step), ch(a.h, a.ldh, row0, step);
+    auto fetch = [&](int stage, int64_t row, int rows) {
+        const int64_t at = row + rows * step;
+        if (at < a.M) {
+            const bool inner = at >= a.margin && at < a.M - a.margin;
+            if (a.y) ring.fetch(stage, 0, cy, rows, inner);
+            if (a.gate_cols > 1) ring.fetch(stage, 1, cg, rows, inner);
+            if (a.res) ring.fetch(stage, 2, cres, rows, inner);
         }
         R::commit();
     };
 #pragma unroll
-    for (int k = 0; k < kAhead - 1; ++k) fetch(k, row0 + k * step);
+    for (int k = 0; k < kAhead - 1; ++k) fetch(k, row0, k);
     int stage = 0;
     for (int64_t row = row0; row < a.M; row += step) {
-        fetch(stage == 0 ? kAhead - 1 : stage - 1, row + (kAhead - 1) * step);
+        fetch(stage == 0 ? kAhead - 1 : stage - 1, row, kAhead - 1);
         R::wait();
         float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
         float2 r[4];
-        if (a.res) ring.read(stage, 2, (const T*)a.res + row * a.ldres, r);
+        if (a.res) ring.read(stage, 2, cres.row, r);
         else
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] = both(0.f);
         if (a.y) {
             float2 f[4], g[4];
-            ring.read(stage, 0, (const T*)a.y + row * a.ldy, f);
+            ring.read(stage, 0, cy.row, f);
             if (a.gate_cols > 1) {
-                ring.read(stage, 1, (const T*)a.gate + row * a.ldg, g);
+                ring.read(stage, 1, cg.row, g);
                 if (a.gate_act != DLRM_GATE_NONE)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -427,7 +429,7 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
                         g[i].y = gate_f<T>(g[i].y, a.gate_act);
                     }
             } else {
-                const float g1 = a.gate_cols == 1 ? gate_f<T>(to_f32(__ldg((const T*)a.gate + row * a.ldg)), a.gate_act) : 1.f;
+                const float g1 = a.gate_cols == 1 ? gate_f<T>(to_f32(__ldg(cg.row)), a.gate_act) : 1.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) g[i] = both(g1);
             }
@@ -439,7 +441,7 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
                 const float2 u = __ffma2_rn(__fmul2_rn(f[i], both(s.y)), aw[i], ab[i]);   // scale u
                 r[i] = __ffma2_rn(u, g[i], r[i]);
             }
-            store_run<T, VEC>((T*)a.r + row * a.ldr, first, N, full, r);
+            store_run<T, VEC>(cr.out(), first, N, full, r);
         }
         if (a.h) {
             const float2 s = centre<VEC, sizeof(T), W>(r, first, full, a, red, turn, warp);
@@ -447,10 +449,15 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
             st.w = s.y;
 #pragma unroll
             for (int i = 0; i < 4; ++i) r[i] = __ffma2_rn(__fmul2_rn(r[i], both(s.y)), wp[i], bp[i]);
-            store_run<T, VEC>((T*)a.h + row * a.ldh, first, N, full, r);
+            store_run<T, VEC>(ch.out(), first, N, full, r);
         }
         if (a.stats && warp % W == 0 && lane == 0) a.stats[row] = st;
         R::done();
+        cy.next();
+        cg.next();
+        cres.next();
+        cr.next();
+        ch.next();
         stage = stage == kAhead - 1 ? 0 : stage + 1;
     }
 }
@@ -510,7 +517,7 @@ struct NormBwd {
     int gate_cols;
     const float4* stats;
     const float *w_post, *b_post, *scale, *w_pre;
-    int M, N, layer, gate_act;
+    int M, N, margin, layer, gate_act;
     float inv_n;
     void *gy, *gg, *gres;
     int64_t ldgy, ldgg, ldgres;
@@ -547,44 +554,49 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
     load_vector<VEC, sizeof(T)>(a.w_pre, first, N, 1.f, wp);
     float2 sum[4][4] = {};
     const int64_t step = (int64_t)gridDim.x * G, row0 = (int64_t)blockIdx.x * G + warp / W;
-    auto fetch = [&](int stage, int64_t row) {
-        if (row < a.M) {
-            if (a.gr) ring.fetch(stage, kGr, (const T*)a.gr, row * a.ldgr);
+    Cursor<T> cgr(a.gr, a.ldgr, row0, step), cgh(a.gh, a.ldgh, row0, step), cr(a.r, a.ldr, row0, step),
+        cy(a.y, a.ldy, row0, step), cg(a.gate, a.ldg, row0, step), cgy(a.gy, a.ldgy, row0, step), cgg(a.gg, a.ldgg, row0, step),
+        cgres(a.gres, a.ldgres, row0, step);
+    auto fetch = [&](int stage, int64_t row, int rows) {
+        const int64_t at = row + rows * step;
+        if (at < a.M) {
+            const bool inner = at >= a.margin && at < a.M - a.margin;
+            if (a.gr) ring.fetch(stage, kGr, cgr, rows, inner);
             if (PRE) {
-                ring.fetch(stage, kGh, (const T*)a.gh, row * a.ldgh);
-                ring.fetch(stage, kR, (const T*)a.r, row * a.ldr);
+                ring.fetch(stage, kGh, cgh, rows, inner);
+                ring.fetch(stage, kR, cr, rows, inner);
             }
             if (POST) {
-                ring.fetch(stage, kY, (const T*)a.y, row * a.ldy);
-                if (a.gate_cols > 1) ring.fetch(stage, kGate, (const T*)a.gate, row * a.ldg);
+                ring.fetch(stage, kY, cy, rows, inner);
+                if (a.gate_cols > 1) ring.fetch(stage, kGate, cg, rows, inner);
             }
         }
         Rg::commit();
     };
 #pragma unroll
-    for (int k = 0; k < kAhead - 1; ++k) fetch(k, row0 + k * step);
+    for (int k = 0; k < kAhead - 1; ++k) fetch(k, row0, k);
     // what a row has one of is loaded a row ahead
     float4 st_next = row0 < a.M ? __ldg(a.stats + row0) : make_float4(0, 0, 0, 0);
-    float g_next = a.gate_cols == 1 && row0 < a.M ? to_f32(__ldg((const T*)a.gate + row0 * a.ldg)) : 1.f;
+    float g_next = a.gate_cols == 1 && row0 < a.M ? to_f32(__ldg(cg.row)) : 1.f;
     int stage = 0;
     for (int64_t row = row0; row < a.M; row += step) {
-        fetch(stage == 0 ? kAhead - 1 : stage - 1, row + (kAhead - 1) * step);
+        fetch(stage == 0 ? kAhead - 1 : stage - 1, row, kAhead - 1);
         const float4 st = st_next;
         float g1 = g_next, slope1 = 1.f;
         if (row + step < a.M) {
             st_next = __ldg(a.stats + row + step);
-            if (a.gate_cols == 1) g_next = to_f32(__ldg((const T*)a.gate + (row + step) * a.ldg));
+            if (a.gate_cols == 1) g_next = to_f32(__ldg(cg.ahead(1)));
         }
         Rg::wait();
         float2 dr[4];
-        if (a.gr) ring.read(stage, kGr, (const T*)a.gr + row * a.ldgr, dr);
+        if (a.gr) ring.read(stage, kGr, cgr.row, dr);
         else
 #pragma unroll
             for (int i = 0; i < 4; ++i) dr[i] = both(0.f);
         if (PRE) {
             float2 d[4], x[4], p, q;
-            ring.read(stage, kGh, (const T*)a.gh + row * a.ldgh, d);
-            ring.read(stage, kR, (const T*)a.r + row * a.ldr, x);
+            ring.read(stage, kGh, cgh.row, d);
+            ring.read(stage, kR, cr.row, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[i] = __fmul2_rn(__fadd2_rn(x[i], both(-st.z)), both(st.w));
@@ -609,12 +621,12 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
             for (int i = 0; i < 4; ++i)
                 dr[i] = __ffma2_rn(__ffma2_rn(x[i], both(c0), __fadd2_rn(d[i], both(c1))), both(st.w), dr[i]);
         }
-        if (a.gres) store_run<T, VEC>((T*)a.gres + row * a.ldgres, first, N, full, dr);
+        if (a.gres) store_run<T, VEC>(cgres.out(), first, N, full, dr);
         if (POST) {
             float2 x[4], g[4], k[4], p, q, t = both(0.f);
-            ring.read(stage, kY, (const T*)a.y + row * a.ldy, x);
+            ring.read(stage, kY, cy.row, x);
             if (a.gate_cols > 1) {
-                ring.read(stage, kGate, (const T*)a.gate + row * a.ldg, g);
+                ring.read(stage, kGate, cg.row, g);
                 if (a.gate_act != DLRM_GATE_NONE)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -645,7 +657,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
                 p = i ? __ffma2_rn(dr[i], x[i], p) : __fmul2_rn(dr[i], x[i]);
                 q = i ? __fadd2_rn(dr[i], q) : dr[i];
             }
-            if (a.gg && a.gate_cols > 1) store_run<T, VEC>((T*)a.gg + row * a.ldgg, first, N, full, k);
+            if (a.gg && a.gate_cols > 1) store_run<T, VEC>(cgg.out(), first, N, full, k);
             float c0, c1 = 0.f;
             if (a.layer) {
                 float c[2] = {p.x + p.y, q.x + q.y};
@@ -660,16 +672,24 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
             if (a.gg && a.gate_cols == 1) {
                 float c[1] = {t.x + t.y};
                 row_sum<W>(c, red, turn, warp);
-                if (warp % W == 0 && lane == 0) ((T*)a.gg)[row * a.ldgg] = from_f32<T>(c[0] * slope1);
+                if (warp % W == 0 && lane == 0) *cgg.out() = from_f32<T>(c[0] * slope1);
             }
             if (a.gy) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     dr[i] = __fmul2_rn(__ffma2_rn(x[i], both(c0), __fadd2_rn(dr[i], both(c1))), both(st.y));
-                store_run<T, VEC>((T*)a.gy + row * a.ldgy, first, N, full, dr);
+                store_run<T, VEC>(cgy.out(), first, N, full, dr);
             }
         }
         Rg::done();
+        cgr.next();
+        cgh.next();
+        cr.next();
+        cy.next();
+        cg.next();
+        cgy.next();
+        cgg.next();
+        cgres.next();
         stage = stage == kAhead - 1 ? 0 : stage + 1;
     }
     if (!a.partial) return;
@@ -774,6 +794,9 @@ dlrm_status check_vectors(const char* fn, std::initializer_list<const void*> v, 
     return DLRM_OK;
 }
 
+// The rows at the ends of matrices of N columns or more whose neighbours' bytes may be fewer than 16.
+int end_rows(int N, int es) { return 16 / (N * es) + 1; }
+
 dlrm_status check_gate(const char* fn, const void* gate, int64_t ldg, int gate_cols, int M, int N, int es)
 {
     if (gate_cols != 1 && gate_cols != N) return fail(DLRM_ERR_INVALID_ARG, "%s: gate_cols is neither 1 nor N", fn);
@@ -817,7 +840,7 @@ extern "C" dlrm_status dlrm_block_norm_fwd(const void* d_y, int64_t ldy, const v
           (!wide_gate || rows_aligned16(d_gate, ldg, M, es)) && (!d_residual || rows_aligned16(d_residual, ldres, M, es)) &&
           (!d_h || rows_aligned16(d_h, ldh, M, es));
     const NormFwd a = {d_y, d_gate, d_residual, ldy, ldg, ldres, !d_gate ? 0 : wide_gate ? N : 1, d_w_post, d_b_post,
-                       d_scale, d_w_pre, d_b_pre, M, N, norm == DLRM_NORM_LAYER, (int)gate_act, (float)eps,
+                       d_scale, d_w_pre, d_b_pre, M, N, end_rows(N, es), norm == DLRM_NORM_LAYER, (int)gate_act, (float)eps,
                        (float)(1.0 / N), d_r, d_h, ldr, ldh, (float4*)d_stats};
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
@@ -894,7 +917,7 @@ extern "C" dlrm_status dlrm_block_norm_bwd(
           (!d_grad_residual || rows_aligned16(d_grad_residual, ldgres, M, es));
     const int64_t Np = (N + 7) / 8 * 8;
     const NormBwd a = {d_grad_r, d_grad_h, d_y, d_gate, d_r, ldgr, ldgh, ldy, ldg, ldr, !d_gate ? 0 : wide_gate ? N : 1,
-                       (const float4*)d_stats, d_w_post, d_b_post, d_scale, d_w_pre, M, N, norm == DLRM_NORM_LAYER,
+                       (const float4*)d_stats, d_w_post, d_b_post, d_scale, d_w_pre, M, N, end_rows(N, es), norm == DLRM_NORM_LAYER,
                        (int)gate_act, (float)(1.0 / N), d_grad_y, d_grad_gate, d_grad_residual, ldgy, ldgg, ldgres,
                        sums ? (float*)d_workspace : nullptr, Np};
     s = with_type(dtype, [&](auto t) {
