@@ -30,7 +30,7 @@ namespace {
 template <bool VEC, int ES>
 __device__ __forceinline__ int run_first(int warp, int lane)
 {
-    return warp * 256 + lane * (VEC ? 8 : ES == 2 ? 2 : 1);
+    return warp * 256 + lane * (VEC ? 16 / ES : ES == 2 ? 2 : 1);
 }
 
 // A tensor's row that a group of warps is at, stepped from one of its rows to the next.
@@ -80,10 +80,9 @@ struct Ring {
     {
         const T* row = c.ahead(rows);
         const uint32_t to = at + stage * kStage + slot * kSlot;
-        if (first < N)
 #pragma unroll
-            for (int i = 0; i < kWords; ++i)
-                copy16(to + i * THREADS * 16, reinterpret_cast<const uint4*>(row + first) + i, 16);
+        for (int i = 0; i < kWords; ++i)
+            if (first + i * 128 < N) copy16(to + i * THREADS * 16, row + first + i * 128, 16);
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
     // The oldest row's copies are complete.
@@ -175,7 +174,14 @@ __device__ __forceinline__ void store_run(T* row, int first, int N, bool full, c
             f[2 * i] = v[i].x;
             f[2 * i + 1] = v[i].y;
         }
-        if (first < N) store8<T, true>(row + first, 8, f);
+        if constexpr (sizeof(T) == 2) {
+            if (first < N) store8<T, true>(row + first, 8, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (first + i * 128 < N)
+                    *reinterpret_cast<float4*>(row + first + i * 128) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        }
     } else if constexpr (sizeof(T) == 2) {
         T* const p = row + first;
         if (full && row_of_words(row)) {
@@ -231,8 +237,11 @@ __device__ __forceinline__ void load_vector(const float* p, int first, int N, fl
 template <bool VEC, int ES>
 __device__ __forceinline__ void store_vector(float* p, int first, int N, const float2 (&v)[4])
 {
-    if constexpr (VEC) {
-        store_run<float, true>(p, first, N, false, v);
+    if constexpr (VEC) {   // N is a multiple of eight
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (run_col<VEC, ES>(first, 4 * i) < N)
+                *reinterpret_cast<float4*>(p + run_col<VEC, ES>(first, 4 * i)) = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -365,7 +365,7 @@ dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict_
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (unit.has<VEC>((int)it.part * U + u, H))
-                v[u] = load_cols<T, VEC>(x + it.row * ldx, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H);
+                v[u] = load_cols<T, VEC>(x + it.row * ldx, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, lanes);
         load_slots(slots, it.row, k, R, s, bad);
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j)
@@ -373,7 +373,7 @@ dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict_
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (unit.has<VEC>((int)it.part * U + u, H))
-                        store_raw<T, VEC>(xs + s[j] * ldxs, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, v[u]);
+                        store_raw<T, VEC>(xs + s[j] * ldxs, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, lanes, v[u]);
     }
     if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
 }
@@ -402,8 +402,8 @@ combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict
             const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
 #pragma unroll
             for (int j = 0; j < K; ++j)
-                if (s[j] >= 0) v[u][j] = load_cols<T, VEC>(ys + s[j] * ldys, c, H);
-            if (res) vr[u] = load_cols<T, VEC>(res + it.row * ldres, c, H);
+                if (s[j] >= 0) v[u][j] = load_cols<T, VEC>(ys + s[j] * ldys, c, H, lanes);
+            if (res) vr[u] = load_cols<T, VEC>(res + it.row * ldres, c, H, lanes);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -421,7 +421,7 @@ combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] += w[i];
             }
-            store_cols<T, VEC>(y + it.row * ldy, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, f);
+            store_cols<T, VEC>(y + it.row * ldy, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, lanes, f);
         }
     }
     if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
@@ -470,11 +470,11 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant_
             for (int u = 0; u < U; ++u) {
                 if (!unit.has<VEC>(run + u, H)) break;
                 const int c = unit.first<VEC, sizeof(T)>(run + u);
-                vg[u] = load_cols<T, VEC>((const T*)a.gy + t * a.ldgy, c, H);
+                vg[u] = load_cols<T, VEC>((const T*)a.gy + t * a.ldgy, c, H, lanes);
                 if (a.gp)
 #pragma unroll
                     for (int j = 0; j < K; ++j)
-                        if (s[j] >= 0) v[u][j] = load_cols<T, VEC>((const T*)a.ys + s[j] * a.ldys, c, H);
+                        if (s[j] >= 0) v[u][j] = load_cols<T, VEC>((const T*)a.ys + s[j] * a.ldys, c, H, lanes);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant_
                             float o[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) o[i] = p[j] * g[i];
-                            store_cols<T, VEC>((T*)a.gys + s[j] * a.ldgys, c, H, o);
+                            store_cols<T, VEC>((T*)a.gys + s[j] * a.ldgys, c, H, lanes, o);
                         }
                     }
             }

@@ -69,10 +69,11 @@ pack8_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, int lanes, uint
         Raw8<T> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            v[u] = load_cols<T, true>(x + it.row * ldx, unit.first<true, sizeof(T)>((int)it.part * U + u), N);
+            if (const int c = unit.eight((int)it.part * U + u); c < N) v[u] = load8<T, true>(x + it.row * ldx + c, 8);
+            else v[u] = Raw8<T>{};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = unit.first<true, sizeof(T)>((int)it.part * U + u);
+            const int c = unit.eight((int)it.part * U + u);
             float f[8];
             uint32_t w[2];
             widen8<T>(v[u], f);
@@ -140,7 +141,7 @@ unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!unit.has<VEC>((int)it.part * U + u, N)) break;
-            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
+            const int c = VEC ? unit.eight((int)it.part * U + u) : unit.first<VEC, sizeof(T)>((int)it.part * U + u);
             if constexpr (VEC) {
                 if (c < N) v[u] = load_run8<true>(m, it.row, c, 8);
             } else {
@@ -167,7 +168,7 @@ unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!unit.has<VEC>((int)it.part * U + u, N)) break;
-            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
+            const int c = VEC ? unit.eight((int)it.part * U + u) : unit.first<VEC, sizeof(T)>((int)it.part * U + u);
             float f[8];
             if constexpr (VEC) {
                 widen_run8<T>(v[u], f);
@@ -188,7 +189,8 @@ unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __
                     }
                 }
             }
-            store_cols<T, VEC>(y + it.row * ldy, c, N, f);
+            if constexpr (!VEC) store_cols<T, VEC>(y + it.row * ldy, c, N, lanes, f);
+            else if (c < N) store8<T, true>(y + it.row * ldy + c, 8, f);
         }
     }
 }

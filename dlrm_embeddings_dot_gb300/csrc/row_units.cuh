@@ -6,12 +6,14 @@
 
 namespace dlrm {
 
-// A lane's run of eight columns of a row, ES the element's size: on the 16-byte grid (VEC) eight
-// neighbours, off it every 32nd column of 256, or pair of them, so that a warp's accesses stay whole.
+// A lane's run of eight columns of a row, ES the element's size: on the 16-byte grid (VEC) 16-byte
+// words, a warp's words one after another so that each access is of whole sectors (two words side by side
+// in a lane cost fp32 every sector twice: norms 16384 x 1024 75 us, 64 so); off it every 32nd column
+// of 256, or pair of them.
 template <bool VEC, int ES>
 __device__ __forceinline__ int run_col(int first, int i)
 {
-    return first + (VEC ? i : ES == 2 ? i / 2 * 64 + i % 2 : i * 32);
+    return first + (VEC ? ES == 2 ? i : i / 4 * 128 + i % 4 : ES == 2 ? i / 2 * 64 + i % 2 : i * 32);
 }
 
 // A unit of `lanes` threads (on the grid a power of two up to a warp, as many as a row has runs; else
@@ -29,8 +31,10 @@ struct Unit {
     template <bool VEC, int ES>
     __device__ __forceinline__ int first(int run) const
     {
-        return VEC ? (run * lanes + l) * 8 : run * 256 + l * (ES == 2 ? 2 : 1);
+        return VEC ? run * lanes * 8 + l * (ES == 2 ? 8 : 4) : run * 256 + l * (ES == 2 ? 2 : 1);
     }
+    // the first of eight neighbouring columns
+    __device__ __forceinline__ int eight(int run) const { return (run * lanes + l) * 8; }
     // whether the run-th run of any of the unit's lanes has columns of a row
     template <bool VEC>
     __device__ __forceinline__ bool has(int run, int H) const { return VEC || run * 256 < H; }
@@ -44,13 +48,16 @@ constexpr int kRuns = VEC && 16 / (K * (int)sizeof(T)) > 1 ? 16 / (K * (int)size
 // Whether two neighbouring 2-byte elements of a row are one 4-byte word.
 __device__ __forceinline__ bool row_of_words(const void* row) { return ((uintptr_t)row & 3u) == 0; }
 
-// The run's columns of a row; columns past its end read as 0 and are not stored.
+// The run's columns of a row; columns past its end read as 0 and are not stored.  VEC: a lane's second
+// 16-byte word is `lanes` words behind its first.
 template <typename T, bool VEC>
-__device__ __forceinline__ Raw8<T> load_cols(const T* row, int first, int H)
+__device__ __forceinline__ Raw8<T> load_cols(const T* row, int first, int H, int lanes)
 {
     Raw8<T> r = {};
     if constexpr (VEC) {
-        if (first < H) r = load8<T, true>(row + first, 8);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+            if (first + i * 4 * lanes < H) r.w[i] = ldg_nc_v4(row + first + i * 4 * lanes);
     } else if constexpr (sizeof(T) == 2) {
         uint32_t* const w = &r.w[0].x;
         const T* p = row + first;
@@ -77,13 +84,13 @@ __device__ __forceinline__ Raw8<T> load_cols(const T* row, int first, int H)
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_raw(T* row, int first, int H, const Raw8<T>& r)
+__device__ __forceinline__ void store_raw(T* row, int first, int H, int lanes, const Raw8<T>& r)
 {
     T* p = row + first;
     if constexpr (VEC) {
-        if (first < H)
 #pragma unroll
-            for (int i = 0; i < (int)(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = r.w[i];
+        for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+            if (first + i * 4 * lanes < H) *reinterpret_cast<uint4*>(p + i * 4 * lanes) = r.w[i];
     } else if constexpr (sizeof(T) == 2) {
         uint32_t w[4];
         memcpy(w, &r, 16);
@@ -107,12 +114,12 @@ __device__ __forceinline__ void store_raw(T* row, int first, int H, const Raw8<T
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_cols(T* row, int first, int H, const float (&f)[8])
+__device__ __forceinline__ void store_cols(T* row, int first, int H, int lanes, const float (&f)[8])
 {
     Raw8<T> r;
     if constexpr (sizeof(T) == 2) r.w[0] = pack8<T>(f);
     else memcpy(&r, f, 32);
-    store_raw<T, VEC>(row, first, H, r);
+    store_raw<T, VEC>(row, first, H, lanes, r);
 }
 
 // Walks (row, part of the row) pairs, a unit at a time, without a division after the first.
