@@ -277,14 +277,14 @@ __device__ __forceinline__ void row_sum(float (&v)[V], float* red, int& turn, in
         }
     } else {
         constexpr int kWarps = W > 8 ? W : 8;
-        float* area = red + turn * kWarps * 2;   // [row][value][warp]
+        float* area = red + turn * kWarps * 2;   // [row][2 values][warp]: rows' sums of one and two values may meet
         turn ^= 1;
-        if (V == 2 ? lane % 16 == 0 : lane == 0) area[(warp / W * V + lane / 16) * W + warp % W] = s;
+        if (V == 2 ? lane % 16 == 0 : lane == 0) area[(warp / W * 2 + lane / 16) * W + warp % W] = s;
         if constexpr (W >= 8) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "r"(W * 32) : "memory");
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float* p = area + (warp / W * V + i) * W;
+            const float* p = area + (warp / W * 2 + i) * W;
             if constexpr (W == 2) {
                 const float2 q = *reinterpret_cast<const float2*>(p);
                 v[i] = q.x + q.y;
@@ -382,24 +382,13 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
     constexpr int kAhead = R::kAhead;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
-    pdl_wait();
     // the same in all lanes, so that what depends on the row alone takes the uniform datapath
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp, N = a.N;
     const bool full = warp % W * 256 + 256 <= N;   // all columns of the warp are in the row
     const int first = run_first<VEC, sizeof(T)>(warp % W, lane);
     int turn = 0;
     const R ring(smem, N, first, warp % W * 256);
-    float2 aw[4], ab[4], wp[4], bp[4];   // scale w_post, scale b_post, w_pre, b_pre
-    load_vector<VEC, sizeof(T)>(a.scale, first, N, 1.f, wp);
-    load_vector<VEC, sizeof(T)>(a.w_post, first, N, 1.f, aw);
-    load_vector<VEC, sizeof(T)>(a.b_post, first, N, 0.f, ab);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        aw[i] = __fmul2_rn(aw[i], wp[i]);
-        ab[i] = __fmul2_rn(ab[i], wp[i]);
-    }
-    load_vector<VEC, sizeof(T)>(a.w_pre, first, N, 1.f, wp);
-    load_vector<VEC, sizeof(T)>(a.b_pre, first, N, 0.f, bp);
+    pdl_wait();
     const int64_t step = (int64_t)gridDim.x * G;
     const int64_t row0 = (int64_t)blockIdx.x * G + warp / W;
     Cursor<T> cy(a.y, a.ldy, row0, step), cg(a.gate, a.ldg, row0, step), cres(a.res, a.ldres, row0, step),
@@ -416,6 +405,17 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
     };
 #pragma unroll
     for (int k = 0; k < kAhead - 1; ++k) fetch(k, row0, k);
+    float2 aw[4], ab[4], wp[4], bp[4];   // scale w_post, scale b_post, w_pre, b_pre
+    load_vector<VEC, sizeof(T)>(a.scale, first, N, 1.f, wp);
+    load_vector<VEC, sizeof(T)>(a.w_post, first, N, 1.f, aw);
+    load_vector<VEC, sizeof(T)>(a.b_post, first, N, 0.f, ab);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        aw[i] = __fmul2_rn(aw[i], wp[i]);
+        ab[i] = __fmul2_rn(ab[i], wp[i]);
+    }
+    load_vector<VEC, sizeof(T)>(a.w_pre, first, N, 1.f, wp);
+    load_vector<VEC, sizeof(T)>(a.b_pre, first, N, 0.f, bp);
     int stage = 0;
     for (int64_t row = row0; row < a.M; row += step) {
         fetch(stage == 0 ? kAhead - 1 : stage - 1, row, kAhead - 1);
@@ -504,7 +504,8 @@ dlrm_status with_warps(int N, Fn&& fn)
 template <typename K, typename A>
 dlrm_status launch_norm(const char* what, K kern, const A& a, int threads, size_t smem, cudaStream_t st)
 {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e =   // the first 48 KB need no leave
+        smem > 46 << 10 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
     if (e != cudaSuccess) return fail(DLRM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     return check_launch_pdl(launch_pdl(kern, dim3(norm_blocks(a.M, a.N)), dim3(threads), smem, st, a), what);
 }
@@ -544,24 +545,13 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
     constexpr int kAhead = Rg::kAhead;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
-    pdl_wait();
     // the same in all lanes, so that what depends on the row alone takes the uniform datapath
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp, N = a.N;
     const bool full = warp % W * 256 + 256 <= N;   // all columns of the warp are in the row
     const int first = run_first<VEC, sizeof(T)>(warp % W, lane);
     int turn = 0;
     const Rg ring(smem, N, first, warp % W * 256);
-    float2 aw[4], ab[4], wp[4];   // scale w_post, scale b_post, w_pre; 0 past the row's end
-    load_vector<VEC, sizeof(T)>(a.scale, first, N, 1.f, wp);
-    load_vector<VEC, sizeof(T)>(a.w_post, first, N, 1.f, aw);
-    load_vector<VEC, sizeof(T)>(a.b_post, first, N, 0.f, ab);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        aw[i] = __fmul2_rn(aw[i], wp[i]);
-        ab[i] = __fmul2_rn(ab[i], wp[i]);
-    }
-    load_vector<VEC, sizeof(T)>(a.w_pre, first, N, 1.f, wp);
-    float2 sum[4][4] = {};
+    pdl_wait();
     const int64_t step = (int64_t)gridDim.x * G, row0 = (int64_t)blockIdx.x * G + warp / W;
     Cursor<T> cgr(a.gr, a.ldgr, row0, step), cgh(a.gh, a.ldgh, row0, step), cr(a.r, a.ldr, row0, step),
         cy(a.y, a.ldy, row0, step), cg(a.gate, a.ldg, row0, step), cgy(a.gy, a.ldgy, row0, step), cgg(a.gg, a.ldgg, row0, step),
@@ -584,6 +574,17 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
     };
 #pragma unroll
     for (int k = 0; k < kAhead - 1; ++k) fetch(k, row0, k);
+    float2 aw[4], ab[4], wp[4];   // scale w_post, scale b_post, w_pre; 0 past the row's end
+    load_vector<VEC, sizeof(T)>(a.scale, first, N, 1.f, wp);
+    load_vector<VEC, sizeof(T)>(a.w_post, first, N, 1.f, aw);
+    load_vector<VEC, sizeof(T)>(a.b_post, first, N, 0.f, ab);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        aw[i] = __fmul2_rn(aw[i], wp[i]);
+        ab[i] = __fmul2_rn(ab[i], wp[i]);
+    }
+    load_vector<VEC, sizeof(T)>(a.w_pre, first, N, 1.f, wp);
+    float2 sum[4][4] = {};
     // what a row has one of is loaded a row ahead
     float4 st_next = row0 < a.M ? __ldg(a.stats + row0) : make_float4(0, 0, 0, 0);
     float g_next = a.gate_cols == 1 && row0 < a.M ? to_f32(__ldg(cg.row)) : 1.f;
@@ -732,30 +733,39 @@ struct NormSum {
     float *gw_post, *gb_post, *gscale, *gw_pre, *gb_pre;
 };
 
-// The vectors' gradients: 32 columns a block, 32 threads a column; blockIdx.y 0 the side of the
-// norm after the block, 1 that of the norm before the next.
-__global__ void __launch_bounds__(1024) block_norm_sum_kernel(const __grid_constant__ NormSum a)
+// The vectors' gradients: kSumCols columns a block, a sector of each block's sums, 128 threads a column;
+// blockIdx.y 0 the side of the norm after the block, 1 that of the norm before the next.
+constexpr int kSumCols = 8, kSumRows = 128;
+
+__global__ void __launch_bounds__(kSumCols * kSumRows) block_norm_sum_kernel(const __grid_constant__ NormSum a)
 {
     pdl_wait();
-    __shared__ float red[2][32][33];
-    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32, n = blockIdx.x * 32 + tx;
+    __shared__ float red[2][kSumRows / 4][kSumCols];
+    const int tx = threadIdx.x % kSumCols, ty = threadIdx.x / kSumCols, n = blockIdx.x * kSumCols + tx;
     const bool pre = blockIdx.y == 1;
     if (pre ? !a.gw_pre && !a.gb_pre : !a.gw_post && !a.gb_post && !a.gscale) return;
     float s = 0.f, t = 0.f;
     if (n < a.N) {
         const float* p = a.partial + (pre ? 2 * a.Np : 0) + n;
 #pragma unroll 4
-        for (int b = ty; b < a.blocks; b += 32) {
+        for (int b = ty; b < a.blocks; b += kSumRows) {
             s += p[(int64_t)b * 4 * a.Np];
             t += p[(int64_t)b * 4 * a.Np + a.Np];
         }
     }
-    red[0][ty][tx] = s;
-    red[1][ty][tx] = t;
+#pragma unroll
+    for (int m = 16; m >= kSumCols; m /= 2) {   // a warp's four rows
+        s += __shfl_xor_sync(~0u, s, m);
+        t += __shfl_xor_sync(~0u, t, m);
+    }
+    if (ty % 4 == 0) {
+        red[0][ty / 4][tx] = s;
+        red[1][ty / 4][tx] = t;
+    }
     __syncthreads();
     if (ty || n >= a.N) return;
 #pragma unroll
-    for (int y = 1; y < 32; ++y) {
+    for (int y = 1; y < kSumRows / 4; ++y) {
         s += red[0][y][tx];
         t += red[1][y][tx];
     }
@@ -941,6 +951,6 @@ extern "C" dlrm_status dlrm_block_norm_bwd(
     if (s != DLRM_OK || !sums) return s;
     const NormSum q = {a.partial, Np, norm_blocks(M, N), N, d_w_post, d_b_post, d_scale,
                        d_grad_w_post, d_grad_b_post, d_grad_scale, d_grad_w_pre, d_grad_b_pre};
-    return check_launch_pdl(launch_pdl(block_norm_sum_kernel, dim3((N + 31) / 32, 2), dim3(1024), 0, st, q),
+    return check_launch_pdl(launch_pdl(block_norm_sum_kernel, dim3((N + kSumCols - 1) / kSumCols, 2), dim3(kSumCols * kSumRows), 0, st, q),
                             "block_norm_sum_kernel");
 }

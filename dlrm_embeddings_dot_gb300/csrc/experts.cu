@@ -70,9 +70,27 @@ __device__ __forceinline__ Word largest(Word k)
     }
 }
 
-// L lanes take a token, eight logits each: k rounds of the largest key left.  Its whole cost is
-// instructions and their latency, so a warp takes 32 / L tokens (65536 of 64 experts, 4 of them, bf16:
-// a warp a token 33 us).
+// Eight keys in descending order (a network of 19 exchanges, the fewest there are).
+template <typename Word>
+__device__ __forceinline__ void sort8(Word (&k)[8])
+{
+    auto order = [&](int i, int j) {
+        const Word a = k[i], b = k[j];
+        k[i] = max(a, b);
+        k[j] = min(a, b);
+    };
+    order(0, 2); order(1, 3); order(4, 6); order(5, 7);
+    order(0, 4); order(1, 5); order(2, 6); order(3, 7);
+    order(0, 1); order(2, 3); order(4, 5); order(6, 7);
+    order(2, 4); order(3, 5);
+    order(1, 4); order(3, 6);
+    order(1, 2); order(3, 4); order(5, 6);
+}
+
+// L lanes take a token, eight logits each, which they sort; k rounds of the largest of the lanes'
+// first keys, whose lane drops it.  Its whole cost is instructions and their latency, so a warp
+// takes 32 / L tokens (65536 of 64 experts, 4 of them, bf16: a warp a token and searched anew each
+// round 33 us, sorted 9; of 256 experts, 8 of them, fp32: searched anew 77 us).
 template <typename T, bool VEC, int L>
 __global__ void __launch_bounds__(256)
 route_fwd_kernel(const T* __restrict__ logits, int64_t ldl, int tokens, int E, int k, int32_t* __restrict__ ids,
@@ -96,15 +114,15 @@ route_fwd_kernel(const T* __restrict__ logits, int64_t ldl, int tokens, int E, i
 #pragma unroll
             for (int i = 0; i < 8; ++i) key[i] = here && i < n ? K::make(v[i], l * 8 + i) : 0;
         }
+        sort8(key);
         Word mine = 0;       // lane j of the token's: choice j
         for (int j = 0; j < k; ++j) {
-            Word best = key[0];
+            const Word best = largest<L>(key[0]);
+            if (key[0] == best) {
 #pragma unroll
-            for (int i = 1; i < 8; ++i) best = max(best, key[i]);
-            best = largest<L>(best);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (key[i] == best) key[i] = 0;
+                for (int i = 0; i < 7; ++i) key[i] = key[i + 1];
+                key[7] = 0;
+            }
             if (l == j) mine = best;
         }
         const bool open = mine > K::kClosed;
@@ -120,23 +138,32 @@ route_fwd_kernel(const T* __restrict__ logits, int64_t ldl, int tokens, int E, i
     }
 }
 
-// L lanes take a token's row of grad_logits, eight columns each; lane j < k has choice j.
+// L lanes take a token's row of grad_logits: zeros, eight columns each, then lane j < k writes choice j.
 template <typename T, bool VEC, int L>
 __global__ void __launch_bounds__(256)
 route_bwd_kernel(const float* __restrict__ grad_probs, const int32_t* __restrict__ ids, const float* __restrict__ probs,
                  int tokens, int E, int k, T* __restrict__ grad, int64_t ldgl)
 {
     pdl_wait();
-    const int lane = threadIdx.x % kWarp, l = lane % L, n = E - l * 8;
+    const int lane = threadIdx.x % kWarp, l = lane % L;
     const int64_t step = (int64_t)gridDim.x * (256 / L);
     for (int64_t t0 = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / kWarp * (kWarp / L); t0 < tokens; t0 += step) {
         const int64_t t = t0 + lane / L;
+        T* row = grad + t * ldgl;
         int id = -1;
         float p = 0.f, g = 0.f;
         if (t < tokens && l < k) {
             id = __ldg(ids + t * k + l);
             p = __ldg(probs + t * k + l);
             g = __ldg(grad_probs + t * k + l);
+        }
+        if (t < tokens) {
+            if constexpr (VEC) {
+                for (int c = l * (16 / (int)sizeof(T)); c < E; c += L * (16 / (int)sizeof(T)))
+                    *reinterpret_cast<uint4*>(row + c) = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int c = l; c < E; c += L) row[c] = from_f32<T>(0.f);
+            }
         }
         if (id < 0 || id >= E) {
             id = -1;
@@ -146,15 +173,10 @@ route_bwd_kernel(const float* __restrict__ grad_probs, const int32_t* __restrict
 #pragma unroll
         for (int m = 4; m; m /= 2) dot += __shfl_xor_sync(~0u, dot, m);
         const float d = p * (g - __shfl_sync(~0u, dot, 0, L));
-        float f[8] = {};
-        for (int j = 0; j < k; ++j) {
-            const int at = __shfl_sync(~0u, id, j, L) - l * 8;
-            const float dj = __shfl_sync(~0u, d, j, L);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (at == i) f[i] = dj;
-        }
-        if (t < tokens && n > 0) store8<T, VEC>(grad + t * ldgl + l * 8, n, f);
+        // of a token's equal ids the last one's lane; the zeros are in place for all lanes
+        const uint32_t same = __match_any_sync(~0u, lane / L << 16 | (id & 0xffff));
+        __syncwarp();
+        if (id >= 0 && same >> lane == 1) row[id] = from_f32<T>(d);
     }
 }
 
@@ -197,43 +219,58 @@ inline SortShape sort_shape(int64_t n)
     return {(int)((n + chunk - 1) / chunk), chunk};
 }
 
-// Choices [from, to) of a warp's part: each(choice, id, bin, rank among the 32 of its bin, how many of them).
-// Bin kBins: past the part's end.
-template <typename Each>
-__device__ __forceinline__ void walk(const int32_t* ids, int64_t from, int64_t to, int E, Each each)
-{
-    const int lane = threadIdx.x % kWarp;
-    for (int64_t c0 = from; c0 < to; c0 += kBatch * kWarp) {
-        int id[kBatch];
+// A warp's part [from, to) of the choices, the first kBatch rounds of it in registers.
+struct Part {
+    const int32_t* ids;
+    int64_t from, to;
+    int id[kBatch];
+    __device__ Part(const int32_t* p, int64_t n, int64_t chunk) : ids(p)
+    {
+        const int64_t part = chunk / kSortWarps, first = blockIdx.x * chunk;
+        from = min(n, first + threadIdx.x / kWarp * part);
+        to = min(n, from + part);
+        load(from, id);
+    }
+    __device__ __forceinline__ void load(int64_t c0, int (&v)[kBatch]) const
+    {
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int64_t c = c0 + b * kWarp + lane;
-            id[b] = c < to ? __ldg(ids + c) : 0;
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int64_t c = c0 + b * kWarp + lane;
-            if (c0 + b * kWarp >= to) break;
-            const int bin = c >= to ? kBins : id[b] >= 0 && id[b] < E ? id[b] : E;
-            const uint32_t same = __match_any_sync(~0u, bin);
-            each(c, id[b], bin, __popc(same & ((1u << lane) - 1)), __popc(same));
-            __syncwarp();
+            const int64_t c = c0 + b * kWarp + threadIdx.x % kWarp;
+            v[b] = c < to ? __ldg(ids + c) : 0;
         }
     }
-}
+    // each(choice, id, bin, rank among the 32 of its bin, how many of them); bin kBins: past the part's end
+    template <typename Each>
+    __device__ __forceinline__ void walk(int E, Each each) const
+    {
+        const int lane = threadIdx.x % kWarp;
+        auto rounds = [&](int64_t c0, const int (&v)[kBatch]) {
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int64_t c = c0 + b * kWarp + lane;
+                if (c0 + b * kWarp >= to) break;
+                const int bin = c >= to ? kBins : v[b] >= 0 && v[b] < E ? v[b] : E;
+                const uint32_t same = __match_any_sync(~0u, bin);
+                each(c, v[b], bin, __popc(same & ((1u << lane) - 1)), __popc(same));
+                __syncwarp();
+            }
+        };
+        rounds(from, id);
+        for (int64_t c0 = from + kBatch * kWarp; c0 < to; c0 += kBatch * kWarp) {
+            int v[kBatch];
+            load(c0, v);
+            rounds(c0, v);
+        }
+    }
+};
 
 // Counts the warps' parts of the block's chunk into warps[warp][bin].
-__device__ __forceinline__ void count_parts(const int32_t* ids, int64_t n, int64_t chunk, int E, int (*warps)[kBins],
-                                            int64_t& from, int64_t& to)
+__device__ __forceinline__ void count_parts(const Part& part, int E, int (*warps)[kBins])
 {
-    const int warp = threadIdx.x / kWarp;
-    int* mine = warps[warp];
+    int* mine = warps[threadIdx.x / kWarp];
     for (int e = threadIdx.x % kWarp; e <= E; e += kWarp) mine[e] = 0;
     __syncwarp();
-    const int64_t part = chunk / kSortWarps, first = blockIdx.x * chunk;
-    from = min(n, first + warp * part);
-    to = min(n, from + part);
-    walk(ids, from, to, E, [&](int64_t, int, int bin, int rank, int many) {
+    part.walk(E, [&](int64_t, int, int bin, int rank, int many) {
         if (rank == 0 && bin < kBins) mine[bin] += many;
     });
     __syncthreads();
@@ -244,8 +281,8 @@ expert_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
 {
     pdl_wait();
     __shared__ int warps[kSortWarps][kBins];
-    int64_t from, to;
-    count_parts(ids, n, chunk, E, warps, from, to);
+    const Part part(ids, n, chunk);
+    count_parts(part, E, warps);
     for (int e = threadIdx.x; e <= E; e += kSortThreads) {
         int s = 0;
 #pragma unroll
@@ -263,6 +300,7 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
     __shared__ int warps[kSortWarps][kBins];
     __shared__ int total[kBins], before[kBins], scan[kSortWarps];
     const int bins = E + 1, tid = threadIdx.x;
+    const Part part(ids, n, chunk);
     if (gridDim.x > 1) {
         for (int e = tid; e < bins; e += kSortThreads) total[e] = before[e] = 0;
         __syncthreads();
@@ -280,8 +318,7 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
             atomicAdd(&before[e], ahead);
         }
     }
-    int64_t from, to;
-    count_parts(ids, n, chunk, E, warps, from, to);
+    count_parts(part, E, warps);
     // where each expert's places begin: an exclusive scan of the totals over the bins
     {
         const int e = tid, lane = e % kWarp;
@@ -319,11 +356,11 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
     __syncthreads();
     int* mine = warps[tid / kWarp];
     bool bad = false;
-    walk(ids, from, to, E, [&](int64_t c, int id, int bin, int rank, int many) {
+    part.walk(E, [&](int64_t c, int id, int bin, int rank, int many) {
         const int at = bin < kBins ? mine[bin] + rank : 0;
         __syncwarp();
         if (rank == 0 && bin < kBins) mine[bin] += many;
-        if (c < to) {
+        if (c < part.to) {
             slots[c] = bin < E ? at : -1;
             if (order) order[at] = bin < E ? (int32_t)c : -1;
             bad = bad || id >= E;
@@ -451,19 +488,38 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant_
     const Unit unit(W > 1 ? kWarp : a.lanes);
     const int lanes = unit.lanes;
     bool bad = false;
+    // a token's slots and shares, on the grid loaded a token ahead (40000 x 515 bf16, off it: 82 us so, 62
+    // without: the registers)
+    int next[K];
+    float next_p[K];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const bool has = j < a.k && t < a.tokens;
+            next[j] = has ? __ldg(a.slots + t * a.k + j) : -1;
+            next_p[j] = has && a.gys ? __ldg(a.probs + t * a.k + j) : 0.f;
+        }
+    };
+    const int64_t first = W > 1 ? blockIdx.x : unit.unit - lane / lanes, step = W > 1 ? gridDim.x : unit.units;
+    if (VEC) fetch(W > 1 ? first : first + lane / lanes);
     // all units of a warp go through the loop together
-    for (int64_t t0 = W > 1 ? blockIdx.x : unit.unit - lane / lanes; t0 < a.tokens; t0 += W > 1 ? gridDim.x : unit.units) {
+    for (int64_t t0 = first; t0 < a.tokens; t0 += step) {
         const int64_t t = W > 1 ? t0 : t0 + lane / lanes;
         const bool here = t < a.tokens;
         int s[K];
         float p[K], dot[K];
-        if (here) load_slots(a.slots, t, a.k, a.R, s, bad);
+        if (!VEC) fetch(t);
 #pragma unroll
         for (int j = 0; j < K; ++j) {
-            if (!here) s[j] = -1;
-            p[j] = s[j] >= 0 && a.gys ? __ldg(a.probs + t * a.k + j) : 0.f;
+            s[j] = next[j];
+            if (s[j] >= a.R) {
+                bad = true;
+                s[j] = -1;
+            }
+            p[j] = next_p[j];
             dot[j] = 0.f;
         }
+        if (VEC) fetch(t + step);
         for (int run = W > 1 ? warp * U : 0; here && run * lanes * 8 < H; run += W * U) {
             Raw8<T> vg[U], v[U][K];
 #pragma unroll

@@ -1,7 +1,7 @@
 // packed8.cu -- matrices to 8 bits and back: 8-bit floats with a power of two for
 // every 32 columns, so that scaling is exact and the only rounding is the one to four bits.
 // Bound by memory: rows by units of lanes (row_units.cuh), several runs' loads in flight.  Four
-// lanes have a block of 32 columns, eight neighbours each.
+// lanes have a block of 32 columns, or eight of fp32, a 16-byte word each.
 #include "packed8.cuh"
 #include "dlrm_block.h"
 #include "row_units.cuh"
@@ -13,15 +13,6 @@ constexpr int kThreads8 = 256;
 
 template <typename T>
 constexpr int kRuns8 = kRuns<T, true, 2>;
-
-// A value's size as it counts for its block: infinities and NaN, which become NaN, do not.
-__device__ __forceinline__ uint32_t size_bits(float& f)
-{
-    const uint32_t b = __float_as_uint(f) & 0x7fffffffu;
-    if (b < 0x7f800000u) return b;
-    f = __uint_as_float(0x7fc00000u);
-    return 0;
-}
 
 // The exponent byte for the largest size 1.m 2^(E - 127): that is at most 448 2^(e - 127) from
 // e = E - 8 on, or E - 7 where 1.m > 1.75.
@@ -39,20 +30,38 @@ __device__ __forceinline__ uint16_t round8(float lo, float hi)
     return h;
 }
 
-// The exponent of a quad's block, and the lane's values in its scale as bytes.
-__device__ __forceinline__ int quad8(float (&f)[8], uint32_t (&w)[2])
+// The exponent of a block, which LANES neighbouring lanes have 32 / LANES values each of, and the
+// lane's values in its scale as bytes.  Infinities and NaN become NaN and do not count for the block.
+template <int LANES>
+__device__ __forceinline__ int block8(float (&f)[32 / LANES], uint32_t (&w)[8 / LANES])
 {
-    const uint32_t quad = 0xfu << (threadIdx.x % kWarp & ~3);
-    uint32_t top = 0;
+    constexpr int V = 32 / LANES;
+    const uint32_t those = (LANES == 32 ? ~0u : (1u << LANES % 32) - 1) << (threadIdx.x % kWarp / LANES * LANES);
+    auto largest = [&] {
+        uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, size_bits(f[i]));
-    top = max(top, __shfl_xor_sync(quad, top, 1));
-    top = max(top, __shfl_xor_sync(quad, top, 2));
+        for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int m = 1; m < LANES; m *= 2) top = max(top, __shfl_xor_sync(those, top, m));
+        return top;
+    };
+    uint32_t top = largest(), gone = 0;
+    if (top >= 0x7f800000u) {   // the same in all of the block's lanes
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if ((__float_as_uint(f[i]) & 0x7fffffffu) >= 0x7f800000u) {
+                f[i] = 0.f;
+                gone |= 1u << i;
+            }
+        top = largest();
+    }
     const int e = exponent8(top);
     const float up = scale_up(e);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        w[i] = round8(f[4 * i] * up, f[4 * i + 1] * up) | (uint32_t)round8(f[4 * i + 2] * up, f[4 * i + 3] * up) << 16;
+    for (int i = 0; i < V; ++i) f[i] = gone >> i & 1 ? __uint_as_float(0x7fc00000u) : f[i] * up;
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+        w[i] = round8(f[4 * i], f[4 * i + 1]) | (uint32_t)round8(f[4 * i + 2], f[4 * i + 3]) << 16;
     return e;
 }
 
@@ -69,18 +78,30 @@ pack8_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, int lanes, uint
         Raw8<T> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (const int c = unit.eight((int)it.part * U + u); c < N) v[u] = load8<T, true>(x + it.row * ldx + c, 8);
-            else v[u] = Raw8<T>{};
+            v[u] = load_cols<T, true>(x + it.row * ldx, unit.first<true, sizeof(T)>((int)it.part * U + u), N, lanes);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = unit.eight((int)it.part * U + u);
+            const int c = unit.first<true, sizeof(T)>((int)it.part * U + u);
             float f[8];
-            uint32_t w[2];
             widen8<T>(v[u], f);
-            const int e = quad8(f, w);
-            if (c < N) {
-                *reinterpret_cast<uint2*>(q + it.row * ldq + c) = make_uint2(w[0], w[1]);
-                if (unit.l % 4 == 0) exps[it.row * blocks + c / kBlock8] = (uint8_t)e;
+            if constexpr (sizeof(T) == 2) {
+                uint32_t w[2];
+                const int e = block8<4>(f, w);
+                if (c < N) {
+                    *reinterpret_cast<uint2*>(q + it.row * ldq + c) = make_uint2(w[0], w[1]);
+                    if (unit.l % 4 == 0) exps[it.row * blocks + c / kBlock8] = (uint8_t)e;
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float g[4] = {f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]};
+                    uint32_t w[1];
+                    const int e = block8<8>(g, w), at = c + h * 4 * lanes;
+                    if (at < N) {
+                        *reinterpret_cast<uint32_t*>(q + it.row * ldq + at) = w[0];
+                        if (unit.l % 8 == 0) exps[it.row * blocks + at / kBlock8] = (uint8_t)e;
+                    }
+                }
             }
         }
     }
@@ -108,7 +129,7 @@ pack8_any_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, uint8_t* __
                 if (i >= n) f[i] = 0.f;
         }
         uint32_t w[2];
-        const int e = quad8(f, w);
+        const int e = block8<4>(f, w);
         uint8_t* p = q + it.row * ldq + c;
         const uint32_t off = (uint32_t)(uintptr_t)p & 7u;
         if (n == 8 && off == 0) {
@@ -141,9 +162,22 @@ unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!unit.has<VEC>((int)it.part * U + u, N)) break;
-            const int c = VEC ? unit.eight((int)it.part * U + u) : unit.first<VEC, sizeof(T)>((int)it.part * U + u);
+            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
             if constexpr (VEC) {
-                if (c < N) v[u] = load_run8<true>(m, it.row, c, 8);
+                if constexpr (sizeof(T) == 2) {
+                    if (c < N) v[u] = load_run8<true>(m, it.row, c, 8);
+                } else {   // two words of four columns, the exponents in the lower bytes of e
+                    const int d = c + 4 * lanes;
+                    v[u] = {};
+                    if (c < N) {
+                        v[u].q.x = __ldg(reinterpret_cast<const uint32_t*>(m.q + it.row * m.ld + c));
+                        v[u].e = __ldg(m.exps + it.row * m.blocks + c / kBlock8);
+                    }
+                    if (d < N) {
+                        v[u].q.y = __ldg(reinterpret_cast<const uint32_t*>(m.q + it.row * m.ld + d));
+                        v[u].e |= (uint32_t)__ldg(m.exps + it.row * m.blocks + d / kBlock8) << 8;
+                    }
+                }
             } else {
                 const uint8_t* row = m.q + it.row * m.ld;
                 const bool words = sizeof(T) == 2 && ((uintptr_t)row & 1u) == 0;
@@ -168,10 +202,15 @@ unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!unit.has<VEC>((int)it.part * U + u, N)) break;
-            const int c = VEC ? unit.eight((int)it.part * U + u) : unit.first<VEC, sizeof(T)>((int)it.part * U + u);
+            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
             float f[8];
             if constexpr (VEC) {
-                widen_run8<T>(v[u], f);
+                if constexpr (sizeof(T) == 2) {
+                    widen_run8<T>(v[u], f);
+                } else {
+                    const float a = scale8(v[u].e & 0xffu), b = scale8(v[u].e >> 8), scale[4] = {a, a, b, b};
+                    widen_codes8<T>(v[u].q, scale, f);
+                }
             } else {
                 const float own = scale8(v[u].e);
                 if constexpr (sizeof(T) == 2) {
@@ -189,8 +228,7 @@ unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __
                     }
                 }
             }
-            if constexpr (!VEC) store_cols<T, VEC>(y + it.row * ldy, c, N, lanes, f);
-            else if (c < N) store8<T, true>(y + it.row * ldy + c, 8, f);
+            store_cols<T, VEC>(y + it.row * ldy, c, N, lanes, f);
         }
     }
 }
@@ -222,7 +260,7 @@ extern "C" dlrm_status dlrm_pack8(const void* d_x, int64_t ldx, dlrm_dtype dtype
     const bool vec = N % 8 == 0 && rows_aligned16(d_x, ldx, M, es) && rows_aligned8(d_q, ldq, M);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        const int lanes = unit_lanes(N, true, 4), blocks = blocks8(N);   // a block's four lanes at least
+        const int lanes = unit_lanes(N, true, sizeof(T) == 2 ? 4 : 8), blocks = blocks8(N);   // a block's lanes at least
         if (vec)
             return check_launch_pdl(launch_pdl(pack8_kernel<T>, dim3(item_blocks(M, N, lanes, kRuns8<T>)), dim3(kThreads8), 0,
                                                as_stream(stream), (const T*)d_x, ldx, M, N, lanes, d_q, ldq, d_exps, blocks),
@@ -245,7 +283,7 @@ extern "C" dlrm_status dlrm_unpack8(const uint8_t* d_q, int64_t ldq, const uint8
     if ((s = check_packed(fn, "d_q", d_q, ldq, d_exps, M, N)) != DLRM_OK) return s;
     if ((s = check_matrix(fn, "d_y", d_y, ldy, M, N, es)) != DLRM_OK) return s;
     const bool vec = N % 8 == 0 && rows_aligned16(d_y, ldy, M, es) && rows_aligned8(d_q, ldq, M);
-    const Packed8 m = {d_q, ldq, d_exps, blocks8(N)};
+    const Packed8 m = packed8(d_q, ldq, d_exps, M, N);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
         auto kern = vec ? unpack8_kernel<T, true> : unpack8_kernel<T, false>;

@@ -12,9 +12,15 @@ struct Packed8 {
     int64_t ld;
     const uint8_t* exps;      // [rows][blocks]
     int blocks;
+    const uint8_t* end;       // behind the last row
 };
 
 inline int blocks8(int cols) { return (cols - 1) / kBlock8 + 1; }
+
+inline Packed8 packed8(const uint8_t* q, int64_t ld, const uint8_t* exps, int rows, int cols)
+{
+    return {q, ld, exps, blocks8(cols), q + (rows > 0 ? (rows - 1) * (rows > 1 ? ld : 0) + cols : 0)};
+}
 
 // Eight columns as they lie in memory, and their block's exponent byte.
 struct Run8 {
@@ -32,10 +38,17 @@ __device__ __forceinline__ Run8 load_run8(const Packed8& m, int64_t row, int col
     if constexpr (VEC) {
         r.q = __ldg(reinterpret_cast<const uint2*>(p));
     } else {
-        uint8_t b[8];
+        const uint32_t off = (uint32_t)(uintptr_t)p & 3u;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(p - off);
+        if (n >= 8 && (uintptr_t)w >= (uintptr_t)m.q && (uintptr_t)(w + 3) <= (uintptr_t)m.end) {
+            const uint32_t a = __ldg(w), b = __ldg(w + 1), c = __ldg(w + 2);   // the words that it lies in
+            r.q = make_uint2(__funnelshift_r(a, b, off * 8), __funnelshift_r(b, c, off * 8));
+        } else {
+            uint8_t b[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = i < n ? __ldg(p + i) : 0;
-        memcpy(&r.q, b, 8);
+            for (int i = 0; i < 8; ++i) b[i] = i < n ? __ldg(p + i) : 0;
+            memcpy(&r.q, b, 8);
+        }
     }
     r.e = scaled ? __ldg(m.exps + row * m.blocks + col / kBlock8) : 0;
     return r;

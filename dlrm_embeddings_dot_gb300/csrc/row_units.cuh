@@ -8,7 +8,7 @@ namespace dlrm {
 
 // A lane's run of eight columns of a row, ES the element's size: on the 16-byte grid (VEC) 16-byte
 // words, a warp's words one after another so that each access is of whole sectors (two words side by side
-// in a lane cost fp32 every sector twice: norms 16384 x 1024 75 us, 64 so); off it every 32nd column
+// in a lane cost fp32 every sector twice: norms of 16384 x 1024 80 us, 51 so); off it every 32nd column
 // of 256, or pair of them.
 template <bool VEC, int ES>
 __device__ __forceinline__ int run_col(int first, int i)
@@ -33,8 +33,6 @@ struct Unit {
     {
         return VEC ? run * lanes * 8 + l * (ES == 2 ? 8 : 4) : run * 256 + l * (ES == 2 ? 2 : 1);
     }
-    // the first of eight neighbouring columns
-    __device__ __forceinline__ int eight(int run) const { return (run * lanes + l) * 8; }
     // whether the run-th run of any of the unit's lanes has columns of a row
     template <bool VEC>
     __device__ __forceinline__ bool has(int run, int H) const { return VEC || run * 256 < H; }

@@ -127,7 +127,7 @@ dlrm_status dlrm_route_fwd(const void* d_logits, int64_t ldl, dlrm_dtype dtype, 
  *   grad_logits[t][ids[t][j]] = probs[t][j] (grad_probs[t][j] - sum over i of grad_probs[t][i] probs[t][i])
  * and 0 for experts that were not chosen.  The choice itself has no gradient.
  *   d_grad_probs fp32 [T][k];  d_ids, d_probs: the forward's;  d_grad_logits [T][E] (output)
- * ids outside [0, E) (-1) take no part.  ids of one token are distinct; of equal ones the last counts.
+ * ids outside [0, E) (-1) take no part.  Of equal ids of a token the last one counts.
  */
 dlrm_status dlrm_route_bwd(const float* d_grad_probs, const int32_t* d_ids, const float* d_probs, dlrm_dtype dtype,
                            int T, int E, int k, void* d_grad_logits, int64_t ldgl, void* stream);

@@ -145,6 +145,27 @@ def test_norm_backward(cuda_lib, dtype, option, M, N, pad, lead, paths):
         assert torch.equal(alone[k], out[k]), k
 
 
+@pytest.mark.parametrize("N", [300, 515, 1024])
+def test_norm_backward_of_rows_that_share_a_block(cuda_lib, N):
+    """Rows of one block go their own pace, with sums of one value and of two: every row right, every run the same."""
+    M, option = 6000, OPTIONS[2]
+    a = _norm_case(5, M, N, 0, 0, "f32", option)
+    r, h, st = _forward(cuda_lib, a, option, M, N, "f32")
+    g = torch.Generator().manual_seed(6)
+    gh = _rand(g, M, N, std=0.1)
+    want = ref.backward(None, *(_d(t) for t in (gh, a["y"], a["gate"], r, st, a["w_post"], a["b_post"], a["scale"], a["w_pre"])),
+                        True, "sigmoid")
+    first = None
+    for _ in range(6):
+        out = {"y": torch.empty_like(r), "gate": torch.empty_like(a["gate"]), "residual": torch.empty_like(r)}
+        cuda_lib.dlrm_block_norm_bwd(None, gh, a["y"], a["gate"], r, st, a["w_post"], a["b_post"], a["scale"], a["w_pre"],
+                                     *out.values(), *[None] * 5, **_codes(cuda_lib, option))
+        first = first or out
+        for k in out:
+            dref.assert_close(out[k], *want[k], "f32", k)
+            assert torch.equal(out[k], first[k])
+
+
 def test_norm_rows_of_zeros_constants_and_numbers_that_are_none(cuda_lib):
     """A row of zeros is zeros (eps > 0), a constant row of LAYER its bias, infinities and NaN stay in their rows."""
     for layer in (False, True):
