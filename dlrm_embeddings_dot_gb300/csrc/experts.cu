@@ -396,21 +396,21 @@ dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict_
     pdl_wait();
     bool bad = false;
     const Unit unit(lanes);
-    for (Items it(unit, (H + lanes * 8 * U - 1) / (lanes * 8 * U)); it.row < tokens; it.next()) {
+    for (Items it(unit, H, U); it.row < tokens; it.next()) {
         int s[kMaxK];
         Raw8<T> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (unit.has<VEC>((int)it.part * U + u, H))
-                v[u] = load_cols<T, VEC>(x + it.row * ldx, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, lanes);
+            if (u < it.per)
+                v[u] = load_cols<T, VEC>(x + it.row * ldx, unit.first<VEC, sizeof(T)>(it.run(u)), H, lanes);
         load_slots(slots, it.row, k, R, s, bad);
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j)
             if (s[j] >= 0)
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    if (unit.has<VEC>((int)it.part * U + u, H))
-                        store_raw<T, VEC>(xs + s[j] * ldxs, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, lanes, v[u]);
+                    if (u < it.per)
+                        store_raw<T, VEC>(xs + s[j] * ldxs, unit.first<VEC, sizeof(T)>(it.run(u)), H, lanes, v[u]);
     }
     if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
 }
@@ -426,7 +426,7 @@ combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict
     pdl_wait();
     bool bad = false;
     const Unit unit(lanes);
-    for (Items it(unit, (H + lanes * 8 * U - 1) / (lanes * 8 * U)); it.row < tokens; it.next()) {
+    for (Items it(unit, H, U); it.row < tokens; it.next()) {
         int s[K];
         float p[K];
         load_slots(slots, it.row, k, R, s, bad);
@@ -435,8 +435,8 @@ combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict
         Raw8<T> v[U][K], vr[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!unit.has<VEC>((int)it.part * U + u, H)) break;
-            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
+            if (u >= it.per) break;
+            const int c = unit.first<VEC, sizeof(T)>(it.run(u));
 #pragma unroll
             for (int j = 0; j < K; ++j)
                 if (s[j] >= 0) v[u][j] = load_cols<T, VEC>(ys + s[j] * ldys, c, H, lanes);
@@ -444,7 +444,7 @@ combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!unit.has<VEC>((int)it.part * U + u, H)) break;
+            if (u >= it.per) break;
             float f[8] = {}, w[8];
 #pragma unroll
             for (int j = 0; j < K; ++j)
@@ -458,7 +458,7 @@ combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] += w[i];
             }
-            store_cols<T, VEC>(y + it.row * ldy, unit.first<VEC, sizeof(T)>((int)it.part * U + u), H, lanes, f);
+            store_cols<T, VEC>(y + it.row * ldy, unit.first<VEC, sizeof(T)>(it.run(u)), H, lanes, f);
         }
     }
     if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
@@ -524,7 +524,6 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant_
             Raw8<T> vg[U], v[U][K];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (!unit.has<VEC>(run + u, H)) break;
                 const int c = unit.first<VEC, sizeof(T)>(run + u);
                 vg[u] = load_cols<T, VEC>((const T*)a.gy + t * a.ldgy, c, H, lanes);
                 if (a.gp)
@@ -534,7 +533,6 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant_
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (!unit.has<VEC>(run + u, H)) break;
                 const int c = unit.first<VEC, sizeof(T)>(run + u);
                 float g[8];
                 widen8<T>(vg[u], g);

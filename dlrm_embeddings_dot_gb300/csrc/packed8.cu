@@ -1,7 +1,7 @@
 // packed8.cu -- matrices to 8 bits and back: 8-bit floats with a power of two for
 // every 32 columns, so that scaling is exact and the only rounding is the one to four bits.
-// Bound by memory: rows by units of lanes (row_units.cuh), several runs' loads in flight.  Four
-// lanes have a block of 32 columns, or eight of fp32, a 16-byte word each.
+// Bound by memory, several 16-byte words a lane in flight.  Four lanes have a block of 32 columns,
+// eight of fp32, a word each.
 #include "packed8.cuh"
 #include "dlrm_block.h"
 #include "row_units.cuh"
@@ -11,8 +11,37 @@ namespace {
 
 constexpr int kThreads8 = 256;
 
+constexpr int kWords8 = 4;
+
 template <typename T>
 constexpr int kRuns8 = kRuns<T, true, 2>;
+
+// Walks the words of rows, `groups` of them a row, kWords8 at a time: each(k, row, word) for those
+// there are, in a loop over k that the compiler unrolls.
+struct Words {
+    int64_t i, end, stride, row, g, groups, drow, dg;
+    __device__ Words(int64_t rows, int64_t n) : groups(n)
+    {
+        end = groups * rows;
+        stride = (int64_t)gridDim.x * kThreads8;
+        i = (int64_t)blockIdx.x * kThreads8 + threadIdx.x;
+        row = i / groups;
+        g = i - row * groups;
+        drow = stride / groups;
+        dg = stride - drow * groups;
+    }
+    __device__ __forceinline__ bool more() const { return i < end; }
+    __device__ __forceinline__ void next()
+    {
+        i += stride;
+        row += drow;
+        g += dg;
+        if (g >= groups) {
+            g -= groups;
+            ++row;
+        }
+    }
+};
 
 // The exponent byte for the largest size 1.m 2^(E - 127): that is at most 448 2^(e - 127) from
 // e = E - 8 on, or E - 7 where 1.m > 1.75.
@@ -65,42 +94,40 @@ __device__ __forceinline__ int block8(float (&f)[32 / LANES], uint32_t (&w)[8 / 
     return e;
 }
 
-// blocks: exponent bytes of a row
+// blocks: exponent bytes of a row.  Rows go by units of lanes (row_units.cuh): as one sequence of words,
+// as in unpack8_kernel, the places of four words cost registers (65536 x 1024 bf16 46 us, so 40).
 template <typename T>
 __global__ void __launch_bounds__(kThreads8)
 pack8_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, int lanes, uint8_t* __restrict__ q, int64_t ldq,
              uint8_t* __restrict__ exps, int blocks)
 {
-    constexpr int U = kRuns8<T>;
+    constexpr int U = kRuns8<T>, V = 16 / sizeof(T);
     pdl_wait();
     const Unit unit(lanes);
-    for (Items it(unit, (N + lanes * 8 * U - 1) / (lanes * 8 * U)); it.row < M; it.next()) {
+    for (Items it(unit, N, U); it.row < M; it.next()) {
         Raw8<T> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            v[u] = load_cols<T, true>(x + it.row * ldx, unit.first<true, sizeof(T)>((int)it.part * U + u), N, lanes);
+            if (u < it.per)
+                v[u] = load_cols<T, true>(x + it.row * ldx, unit.first<true, sizeof(T)>(it.run(u)), N, lanes);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = unit.first<true, sizeof(T)>((int)it.part * U + u);
+            if (u >= it.per) break;
+            const int c = unit.first<true, sizeof(T)>(it.run(u));
             float f[8];
             widen8<T>(v[u], f);
-            if constexpr (sizeof(T) == 2) {
-                uint32_t w[2];
-                const int e = block8<4>(f, w);
-                if (c < N) {
-                    *reinterpret_cast<uint2*>(q + it.row * ldq + c) = make_uint2(w[0], w[1]);
-                    if (unit.l % 4 == 0) exps[it.row * blocks + c / kBlock8] = (uint8_t)e;
-                }
-            } else {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float g[4] = {f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]};
-                    uint32_t w[1];
-                    const int e = block8<8>(g, w), at = c + h * 4 * lanes;
-                    if (at < N) {
-                        *reinterpret_cast<uint32_t*>(q + it.row * ldq + at) = w[0];
-                        if (unit.l % 8 == 0) exps[it.row * blocks + at / kBlock8] = (uint8_t)e;
-                    }
+            for (int h = 0; h < 8 / V; ++h) {   // the run's 16-byte words
+                float g[V];
+                uint32_t w[V / 4];
+#pragma unroll
+                for (int i = 0; i < V; ++i) g[i] = f[h * V + i];
+                const int e = block8<kBlock8 / V>(g, w), at = c + h * 4 * lanes;
+                if (at < N) {
+                    uint8_t* p = q + it.row * ldq + at;
+                    if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+                    else *reinterpret_cast<uint32_t*>(p) = w[0];
+                    if (at % kBlock8 == 0) exps[it.row * blocks + at / kBlock8] = (uint8_t)e;
                 }
             }
         }
@@ -117,20 +144,19 @@ pack8_any_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, uint8_t* __
 {
     pdl_wait();
     const T* const end = x + (M - 1) * ldx + N;
-    const Unit unit(1);
-    for (Items it(unit, (int64_t)blocks * 4); it.row < M; it.next()) {   // a quad's lanes leave together
-        const int64_t c = it.part * 8;
+    for (Words w8(M, (int64_t)blocks * 4); w8.more(); w8.next()) {   // a quad's lanes leave together
+        const int64_t row = w8.row, c = w8.g * 8;
         const int n = (int)min((int64_t)8, N - c);    // 0 or less: past the row's end
         float f[8] = {};
         if (n > 0) {
-            widen8<T>(load8_shifted<T>(x + it.row * ldx + c, n, x, end), f);
+            widen8<T>(load8_shifted<T>(x + row * ldx + c, n, x, end), f);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (i >= n) f[i] = 0.f;
         }
         uint32_t w[2];
         const int e = block8<4>(f, w);
-        uint8_t* p = q + it.row * ldq + c;
+        uint8_t* p = q + row * ldq + c;
         const uint32_t off = (uint32_t)(uintptr_t)p & 7u;
         if (n == 8 && off == 0) {
             *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
@@ -145,91 +171,88 @@ pack8_any_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, uint8_t* __
             for (int i = 0; i < 8; ++i)
                 if (i < n) p[i] = (uint8_t)(w[i / 4] >> 8 * (i % 4));
         }
-        if (it.part % 4 == 0) exps[it.row * blocks + it.part / 4] = (uint8_t)e;
+        if (w8.g % 4 == 0) exps[row * blocks + w8.g / 4] = (uint8_t)e;
     }
 }
 
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(kThreads8)
-unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __restrict__ y, int64_t ldy)
+unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, T* __restrict__ y, int64_t ldy)
 {
-    constexpr int U = VEC ? 4 : 1;
+    constexpr int V = 16 / sizeof(T);
     pdl_wait();
-    const Unit unit(lanes);
-    const int lane = threadIdx.x % kWarp;
-    for (Items it(unit, (N + lanes * 8 * U - 1) / (lanes * 8 * U)); it.row < M; it.next()) {
-        Run8 v[U];
+    Words w(M, N / V);
+    while (w.more()) {
+        uint2 v[kWords8];
+        uint32_t e[kWords8];
+        T* to[kWords8];
+        int live = 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (!unit.has<VEC>((int)it.part * U + u, N)) break;
-            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
-            if constexpr (VEC) {
-                if constexpr (sizeof(T) == 2) {
-                    if (c < N) v[u] = load_run8<true>(m, it.row, c, 8);
-                } else {   // two words of four columns, the exponents in the lower bytes of e
-                    const int d = c + 4 * lanes;
-                    v[u] = {};
-                    if (c < N) {
-                        v[u].q.x = __ldg(reinterpret_cast<const uint32_t*>(m.q + it.row * m.ld + c));
-                        v[u].e = __ldg(m.exps + it.row * m.blocks + c / kBlock8);
-                    }
-                    if (d < N) {
-                        v[u].q.y = __ldg(reinterpret_cast<const uint32_t*>(m.q + it.row * m.ld + d));
-                        v[u].e |= (uint32_t)__ldg(m.exps + it.row * m.blocks + d / kBlock8) << 8;
-                    }
-                }
-            } else {
-                const uint8_t* row = m.q + it.row * m.ld;
-                const bool words = sizeof(T) == 2 && ((uintptr_t)row & 1u) == 0;
-                uint32_t w[2] = {0, 0};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int x = run_col<VEC, sizeof(T)>(c, 2 * i), z = run_col<VEC, sizeof(T)>(c, 2 * i + 1);
-                    uint32_t h = 0;
-                    if (words && z < N) {
-                        h = __ldg(reinterpret_cast<const uint16_t*>(row + x));
-                    } else {
-                        if (x < N) h = __ldg(row + x);
-                        if (z < N) h |= (uint32_t)__ldg(row + z) << 8;
-                    }
-                    w[i / 2] |= h << 16 * (i % 2);
-                }
-                v[u].q = make_uint2(w[0], w[1]);
-                const int64_t b = (it.part * U + u) * 8 + lane;   // lane i has the run's i-th block's exponent
-                v[u].e = lane < 8 && b < m.blocks ? __ldg(m.exps + it.row * m.blocks + b) : 0;
+        for (int k = 0; k < kWords8; ++k)
+            if (w.more()) {
+                const int col = (int)w.g * V;
+                const uint8_t* p = m.q + w.row * m.ld + col;
+                if constexpr (V == 8) v[k] = __ldg(reinterpret_cast<const uint2*>(p));
+                else v[k] = make_uint2(__ldg(reinterpret_cast<const uint32_t*>(p)), 0);
+                e[k] = __ldg(m.exps + w.row * m.blocks + col / kBlock8);
+                to[k] = y + w.row * ldy + col;
+                live = k + 1;
+                w.next();
             }
-        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (!unit.has<VEC>((int)it.part * U + u, N)) break;
-            const int c = unit.first<VEC, sizeof(T)>((int)it.part * U + u);
+        for (int k = 0; k < kWords8; ++k) {
+            if (k >= live) break;
             float f[8];
-            if constexpr (VEC) {
-                if constexpr (sizeof(T) == 2) {
-                    widen_run8<T>(v[u], f);
-                } else {
-                    const float a = scale8(v[u].e & 0xffu), b = scale8(v[u].e >> 8), scale[4] = {a, a, b, b};
-                    widen_codes8<T>(v[u].q, scale, f);
-                }
-            } else {
-                const float own = scale8(v[u].e);
-                if constexpr (sizeof(T) == 2) {
-                    float scale[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) scale[i] = __shfl_sync(~0u, own, 2 * i + lane / 16);
-                    widen_codes8<T>(v[u].q, scale, f);
-                } else {   // a scale each: the values without it, then it
-                    const float one[4] = {1.f, 1.f, 1.f, 1.f};
-                    widen_codes8<T>(v[u].q, one, f);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        f[i] *= __shfl_sync(~0u, own, i);
-                        if (fabsf(f[i]) > kMost8<T>) f[i] = copysignf(kMost8<T>, f[i]);
-                    }
-                }
-            }
-            store_cols<T, VEC>(y + it.row * ldy, c, N, lanes, f);
+            widen_run8<T>({v[k], e[k]}, f);
+            if constexpr (V == 8) store8<T, true>(to[k], 8, f);
+            else *reinterpret_cast<float4*>(to[k]) = make_float4(f[0], f[1], f[2], f[3]);
         }
+    }
+}
+
+// Off the grid: rows by warps (row_units.cuh), every 32nd column a lane or pair of them.
+template <typename T>
+__global__ void __launch_bounds__(kThreads8)
+unpack8_any_kernel(const __grid_constant__ Packed8 m, int M, int N, T* __restrict__ y, int64_t ldy)
+{
+    pdl_wait();
+    const Unit unit(kWarp);
+    const int lane = threadIdx.x % kWarp;
+    for (Items it(unit, N, 1); it.row < M; it.next()) {
+        const int c = unit.first<false, sizeof(T)>((int)it.part);
+        const uint8_t* row = m.q + it.row * m.ld;
+        const bool words = sizeof(T) == 2 && ((uintptr_t)row & 1u) == 0;
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int x = run_col<false, sizeof(T)>(c, 2 * i), z = run_col<false, sizeof(T)>(c, 2 * i + 1);
+            uint32_t h = 0;
+            if (words && z < N) {
+                h = __ldg(reinterpret_cast<const uint16_t*>(row + x));
+            } else {
+                if (x < N) h = __ldg(row + x);
+                if (z < N) h |= (uint32_t)__ldg(row + z) << 8;
+            }
+            w[i / 2] |= h << 16 * (i % 2);
+        }
+        const int64_t b = it.part * 8 + lane;   // lane i has the part's i-th block's exponent
+        const float own = scale8(lane < 8 && b < m.blocks ? __ldg(m.exps + it.row * m.blocks + b) : 0);
+        float f[8];
+        if constexpr (sizeof(T) == 2) {
+            float scale[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) scale[i] = __shfl_sync(~0u, own, 2 * i + lane / 16);
+            widen_codes8<T>(make_uint2(w[0], w[1]), scale, f);
+        } else {   // a scale each: the values without it, then it
+            const float one[4] = {1.f, 1.f, 1.f, 1.f};
+            widen_codes8<T>(make_uint2(w[0], w[1]), one, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                f[i] *= __shfl_sync(~0u, own, i);
+                if (fabsf(f[i]) > kMost8<T>) f[i] = copysignf(kMost8<T>, f[i]);
+            }
+        }
+        store_cols<T, false>(y + it.row * ldy, c, N, kWarp, f);
     }
 }
 
@@ -239,6 +262,13 @@ dlrm_status check_sizes8(const char* fn, dlrm_dtype dtype, int M, int N)
     if (M < 0 || N < 1) return fail(DLRM_ERR_INVALID_ARG, "%s: need M >= 0 and N >= 1", fn);
     if (M > kMaxSize || N > kMaxSize) return fail(DLRM_ERR_UNSUPPORTED, "%s: sizes up to %d", fn, kMaxSize);
     return DLRM_OK;
+}
+
+// Blocks for lanes that take `each` words at a time.
+unsigned word_blocks(int64_t words, int each)
+{
+    const int64_t want = (words + kThreads8 * each - 1) / (kThreads8 * each), most = (int64_t)num_sms() * 8;
+    return (unsigned)(want < most ? want : most);
 }
 
 }  // namespace
@@ -265,7 +295,7 @@ extern "C" dlrm_status dlrm_pack8(const void* d_x, int64_t ldx, dlrm_dtype dtype
             return check_launch_pdl(launch_pdl(pack8_kernel<T>, dim3(item_blocks(M, N, lanes, kRuns8<T>)), dim3(kThreads8), 0,
                                                as_stream(stream), (const T*)d_x, ldx, M, N, lanes, d_q, ldq, d_exps, blocks),
                                     "pack8_kernel");
-        return check_launch_pdl(launch_pdl(pack8_any_kernel<T>, dim3(item_blocks(M, blocks * kBlock8, 1, 1)), dim3(kThreads8),
+        return check_launch_pdl(launch_pdl(pack8_any_kernel<T>, dim3(word_blocks((int64_t)M * blocks * 4, 1)), dim3(kThreads8),
                                            0, as_stream(stream), (const T*)d_x, ldx, M, N, d_q, ldq, d_exps, blocks),
                                 "pack8_any_kernel");
     });
@@ -286,10 +316,9 @@ extern "C" dlrm_status dlrm_unpack8(const uint8_t* d_q, int64_t ldq, const uint8
     const Packed8 m = packed8(d_q, ldq, d_exps, M, N);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        auto kern = vec ? unpack8_kernel<T, true> : unpack8_kernel<T, false>;
-        const int lanes = unit_lanes(N, vec);
-        return check_launch_pdl(launch_pdl(kern, dim3(item_blocks(M, N, lanes, vec ? 4 : 1)), dim3(kThreads8), 0, as_stream(stream), m, M,
-                                           N, lanes, (T*)d_y, ldy),
+        auto kern = vec ? unpack8_kernel<T> : unpack8_any_kernel<T>;
+        const unsigned blocks = vec ? word_blocks((int64_t)M * N * (int)sizeof(T) / 16, kWords8) : item_blocks(M, N, kWarp, 1);
+        return check_launch_pdl(launch_pdl(kern, dim3(blocks), dim3(kThreads8), 0, as_stream(stream), m, M, N, (T*)d_y, ldy),
                                 "unpack8_kernel");
     });
 }

@@ -33,9 +33,6 @@ struct Unit {
     {
         return VEC ? run * lanes * 8 + l * (ES == 2 ? 8 : 4) : run * 256 + l * (ES == 2 ? 2 : 1);
     }
-    // whether the run-th run of any of the unit's lanes has columns of a row
-    template <bool VEC>
-    __device__ __forceinline__ bool has(int run, int H) const { return VEC || run * 256 < H; }
 };
 
 // Runs a lane takes at once: as many as eight 16-byte words hold for K rows; off the grid one, whose
@@ -120,16 +117,22 @@ __device__ __forceinline__ void store_cols(T* row, int first, int H, int lanes, 
     store_raw<T, VEC>(row, first, H, lanes, r);
 }
 
-// Walks (row, part of the row) pairs, a unit at a time, without a division after the first.
+// Walks (row, part of the row) pairs, a unit at a time, without a division after the first.  The runs of a row
+// are shared out over its parts, `most` runs a lane at most: part * per + u for u < per.
 struct Items {
     int64_t row, part, parts, drow, dpart;
-    __device__ Items(const Unit& u, int64_t p) : parts(p)
+    int per;
+    __device__ Items(const Unit& u, int H, int most)
     {
+        const int runs = (H - 1) / (u.lanes * 8) + 1, p = (runs - 1) / most + 1;
+        parts = p;
+        per = (runs - 1) / p + 1;
         row = u.unit / p;
         part = u.unit - row * p;
         drow = u.units / p;
         dpart = u.units - drow * p;
     }
+    __device__ __forceinline__ int run(int u) const { return (int)part * per + u; }
     __device__ void next()
     {
         row += drow;
