@@ -387,12 +387,12 @@ __device__ __forceinline__ void load_slots(const int32_t* slots, int64_t t, int 
 }
 
 // xs[slots[t][j]] = x[t]: a row is read once and written k times.
-template <typename T, bool VEC>
+template <typename T, int LAY>
 __global__ void __launch_bounds__(256)
 dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slots, int tokens, int k, int H, int R,
                 int lanes, T* __restrict__ xs, int64_t ldxs, uint32_t* __restrict__ status)
 {
-    constexpr int U = kRuns<T, VEC, 2>;
+    constexpr int U = kRuns<T, LAY, 2>;
     pdl_wait();
     bool bad = false;
     const Unit unit(lanes);
@@ -402,7 +402,7 @@ dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict_
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (u < it.per)
-                v[u] = load_cols<T, VEC>(x + it.row * ldx, unit.first<VEC, sizeof(T)>(it.run(u)), H, lanes);
+                v[u] = load_cols<T, LAY>(x + it.row * ldx, unit.first<LAY, sizeof(T)>(it.run(u)), H, lanes);
         load_slots(slots, it.row, k, R, s, bad);
 #pragma unroll
         for (int j = 0; j < kMaxK; ++j)
@@ -410,19 +410,19 @@ dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict_
 #pragma unroll
                 for (int u = 0; u < U; ++u)
                     if (u < it.per)
-                        store_raw<T, VEC>(xs + s[j] * ldxs, unit.first<VEC, sizeof(T)>(it.run(u)), H, lanes, v[u]);
+                        store_raw<T, LAY>(xs + s[j] * ldxs, unit.first<LAY, sizeof(T)>(it.run(u)), H, lanes, v[u]);
     }
     if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
 }
 
 // y[t] = residual[t] + sum over j of probs[t][j] ys[slots[t][j]]; probs NULL: the plain sum.  k <= K.
-template <typename T, bool VEC, int K>
+template <typename T, int LAY, int K>
 __global__ void __launch_bounds__(256)
 combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict__ slots, const float* __restrict__ probs,
                const T* __restrict__ res, int64_t ldres, int tokens, int k, int H, int R, int lanes, T* __restrict__ y,
                int64_t ldy, uint32_t* __restrict__ status)
 {
-    constexpr int U = kRuns<T, VEC, K>;
+    constexpr int U = kRuns<T, LAY, K>;
     pdl_wait();
     bool bad = false;
     const Unit unit(lanes);
@@ -436,11 +436,11 @@ combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (u >= it.per) break;
-            const int c = unit.first<VEC, sizeof(T)>(it.run(u));
+            const int c = unit.first<LAY, sizeof(T)>(it.run(u));
 #pragma unroll
             for (int j = 0; j < K; ++j)
-                if (s[j] >= 0) v[u][j] = load_cols<T, VEC>(ys + s[j] * ldys, c, H, lanes);
-            if (res) vr[u] = load_cols<T, VEC>(res + it.row * ldres, c, H, lanes);
+                if (s[j] >= 0) v[u][j] = load_cols<T, LAY>(ys + s[j] * ldys, c, H, lanes);
+            if (res) vr[u] = load_cols<T, LAY>(res + it.row * ldres, c, H, lanes);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -458,7 +458,7 @@ combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[i] += w[i];
             }
-            store_cols<T, VEC>(y + it.row * ldy, unit.first<VEC, sizeof(T)>(it.run(u)), H, lanes, f);
+            store_cols<T, LAY>(y + it.row * ldy, unit.first<LAY, sizeof(T)>(it.run(u)), H, lanes, f);
         }
     }
     if (bad) set_status(status, DLRM_STATUS_OOB_INDEX);
@@ -478,10 +478,10 @@ struct CombineBwd {
 
 // A unit takes a token, or with W = 8 warps a whole block does: grad_y once, and for each choice its
 // row of ys in and of grad_ys out.  k <= K.
-template <typename T, bool VEC, int K, int W>
+template <typename T, int LAY, int K, int W>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant__ CombineBwd a)
 {
-    constexpr int U = kRuns<T, VEC, K>;
+    constexpr int U = kRuns<T, LAY, K>;
     __shared__ float red[W > 1 ? 8 * K : 1];
     pdl_wait();
     const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp, H = a.H;
@@ -501,14 +501,14 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant_
         }
     };
     const int64_t first = W > 1 ? blockIdx.x : unit.unit - lane / lanes, step = W > 1 ? gridDim.x : unit.units;
-    if (VEC) fetch(W > 1 ? first : first + lane / lanes);
+    if (LAY == kOnGrid) fetch(W > 1 ? first : first + lane / lanes);
     // all units of a warp go through the loop together
     for (int64_t t0 = first; t0 < a.tokens; t0 += step) {
         const int64_t t = W > 1 ? t0 : t0 + lane / lanes;
         const bool here = t < a.tokens;
         int s[K];
         float p[K], dot[K];
-        if (!VEC) fetch(t);
+        if (LAY != kOnGrid) fetch(t);
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             s[j] = next[j];
@@ -519,21 +519,21 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant_
             p[j] = next_p[j];
             dot[j] = 0.f;
         }
-        if (VEC) fetch(t + step);
+        if (LAY == kOnGrid) fetch(t + step);
         for (int run = W > 1 ? warp * U : 0; here && run * lanes * 8 < H; run += W * U) {
             Raw8<T> vg[U], v[U][K];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = unit.first<VEC, sizeof(T)>(run + u);
-                vg[u] = load_cols<T, VEC>((const T*)a.gy + t * a.ldgy, c, H, lanes);
+                const int c = unit.first<LAY, sizeof(T)>(run + u);
+                vg[u] = load_cols<T, LAY>((const T*)a.gy + t * a.ldgy, c, H, lanes);
                 if (a.gp)
 #pragma unroll
                     for (int j = 0; j < K; ++j)
-                        if (s[j] >= 0) v[u][j] = load_cols<T, VEC>((const T*)a.ys + s[j] * a.ldys, c, H, lanes);
+                        if (s[j] >= 0) v[u][j] = load_cols<T, LAY>((const T*)a.ys + s[j] * a.ldys, c, H, lanes);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = unit.first<VEC, sizeof(T)>(run + u);
+                const int c = unit.first<LAY, sizeof(T)>(run + u);
                 float g[8];
                 widen8<T>(vg[u], g);
 #pragma unroll
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const __grid_constant_
                             float o[8];
 #pragma unroll
                             for (int i = 0; i < 8; ++i) o[i] = p[j] * g[i];
-                            store_cols<T, VEC>((T*)a.gys + s[j] * a.ldgys, c, H, lanes, o);
+                            store_cols<T, LAY>((T*)a.gys + s[j] * a.ldgys, c, H, lanes, o);
                         }
                     }
             }
@@ -612,6 +612,15 @@ dlrm_status check_rows(const char* fn, dlrm_dtype dtype, int T, int k, int H, in
     return DLRM_OK;
 }
 
+// fn(the layout as a constant)
+template <typename Fn>
+dlrm_status with_layout(int lay, Fn&& fn)
+{
+    if (lay == kOnGrid) return fn(std::integral_constant<int, kOnGrid>());
+    if (lay == kFewLanes) return fn(std::integral_constant<int, kFewLanes>());
+    return fn(std::integral_constant<int, kOffGrid>());
+}
+
 // fn(k rounded up to 2, 4 or 8 as a constant)
 template <typename Fn>
 dlrm_status with_choices(int k, Fn&& fn)
@@ -637,14 +646,16 @@ dlrm_status run_combine(const char* fn, const void* ys, int64_t ldys, const int3
                      rows_aligned16(y, ldy, T, es);
     return with_type(dtype, [&](auto t) {
         using E = decltype(t);
-        return with_choices(k, [&](auto kk) {
-            constexpr int K = decltype(kk)::value;
-            auto kern = vec ? combine_kernel<E, true, K> : combine_kernel<E, false, K>;
-            const int lanes = unit_lanes(H, vec);
-            return check_launch_pdl(launch_pdl(kern, dim3(item_blocks(T, H, lanes, vec ? kRuns<E, true, K> : kRuns<E, false, K>)), dim3(256), 0,
-                                               as_stream(stream), (const E*)ys, ldys, slots, probs, (const E*)res, ldres, T, k,
-                                               H, R, lanes, (E*)y, ldy, status),
-                                    fn);
+        return with_layout(row_layout(vec, H), [&](auto l) {
+            constexpr int LAY = decltype(l)::value;
+            return with_choices(k, [&](auto kk) {
+                constexpr int K = decltype(kk)::value;
+                const int lanes = unit_lanes(H, LAY);
+                return check_launch_pdl(launch_pdl(combine_kernel<E, LAY, K>, dim3(item_blocks(T, H, lanes, kRuns<E, LAY, K>)),
+                                                   dim3(256), 0, as_stream(stream), (const E*)ys, ldys, slots, probs,
+                                                   (const E*)res, ldres, T, k, H, R, lanes, (E*)y, ldy, status),
+                                        fn);
+            });
         });
     });
 }
@@ -768,11 +779,14 @@ extern "C" dlrm_status dlrm_dispatch_fwd(const void* d_x, int64_t ldx, const int
     const bool vec = H % 8 == 0 && rows_aligned16(d_x, ldx, T, es) && rows_aligned16(d_xs, ldxs, R, es);
     return with_type(dtype, [&](auto t) {
         using X = decltype(t);
-        auto kern = vec ? dispatch_kernel<X, true> : dispatch_kernel<X, false>;
-        const int lanes = unit_lanes(H, vec);
-        return check_launch_pdl(launch_pdl(kern, dim3(item_blocks(T, H, lanes, vec ? kRuns<X, true, 2> : kRuns<X, false, 2>)), dim3(256), 0, as_stream(stream),
-                                           (const X*)d_x, ldx, d_slots, T, k, H, R, lanes, (X*)d_xs, ldxs, d_status),
-                                "dispatch_kernel");
+        return with_layout(row_layout(vec, H), [&](auto l) {
+            constexpr int LAY = decltype(l)::value;
+            const int lanes = unit_lanes(H, LAY);
+            return check_launch_pdl(launch_pdl(dispatch_kernel<X, LAY>, dim3(item_blocks(T, H, lanes, kRuns<X, LAY, 2>)),
+                                               dim3(256), 0, as_stream(stream), (const X*)d_x, ldx, d_slots, T, k, H, R, lanes,
+                                               (X*)d_xs, ldxs, d_status),
+                                    "dispatch_kernel");
+        });
     });
 }
 
@@ -835,19 +849,23 @@ extern "C" dlrm_status dlrm_combine_bwd(const void* d_grad_y, int64_t ldgy, cons
                      (!d_grad_ys || rows_aligned16(d_grad_ys, ldgys, R, es));
     // a block a token where those would leave SMs idle (16 tokens of 4096 columns, 4 each, fp16)
     const bool wide = T < num_sms() * 4 && H > 512;
-    const int lanes = unit_lanes(H, vec);
+    const int lay = row_layout(vec, H), lanes = unit_lanes(H, lay);
     const CombineBwd a = {d_grad_y, d_ys, ldgy, ldys, d_slots, d_probs, T, k, H, R, lanes, d_grad_ys, ldgys, d_grad_probs,
                           d_status};
     const int64_t blocks = wide ? T : ((int64_t)T * lanes + 255) / 256, most = (int64_t)num_sms() * 8;
     return with_type(dtype, [&](auto t) {
         using X = decltype(t);
-        return with_choices(k, [&](auto kk) {
-            constexpr int K = decltype(kk)::value;
-            auto kern = wide ? (vec ? combine_bwd_kernel<X, true, K, 8> : combine_bwd_kernel<X, false, K, 8>)
-                             : (vec ? combine_bwd_kernel<X, true, K, 1> : combine_bwd_kernel<X, false, K, 1>);
-            return check_launch_pdl(launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
-                                               as_stream(stream), a),
-                                    "combine_bwd_kernel");
+        return with_layout(lay, [&](auto l) {
+            constexpr int LAY = decltype(l)::value;
+            return with_choices(k, [&](auto kk) {
+                constexpr int K = decltype(kk)::value;
+                auto kern = combine_bwd_kernel<X, LAY, K, 1>;
+                if constexpr (LAY != kFewLanes)
+                    if (wide) kern = combine_bwd_kernel<X, LAY, K, 8>;
+                return check_launch_pdl(launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
+                                                   as_stream(stream), a),
+                                        "combine_bwd_kernel");
+            });
         });
     });
 }

@@ -14,7 +14,7 @@ constexpr int kThreads8 = 256;
 constexpr int kWords8 = 4;
 
 template <typename T>
-constexpr int kRuns8 = kRuns<T, true, 2>;
+constexpr int kRuns8 = kRuns<T, kOnGrid, 2>;
 
 // Walks the words of rows, `groups` of them a row, kWords8 at a time: each(k, row, word) for those
 // there are, in a loop over k that the compiler unrolls.
@@ -109,11 +109,11 @@ pack8_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, int lanes, uint
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (u < it.per)
-                v[u] = load_cols<T, true>(x + it.row * ldx, unit.first<true, sizeof(T)>(it.run(u)), N, lanes);
+                v[u] = load_cols<T, kOnGrid>(x + it.row * ldx, unit.first<kOnGrid, sizeof(T)>(it.run(u)), N, lanes);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (u >= it.per) break;
-            const int c = unit.first<true, sizeof(T)>(it.run(u));
+            const int c = unit.first<kOnGrid, sizeof(T)>(it.run(u));
             float f[8];
             widen8<T>(v[u], f);
 #pragma unroll
@@ -219,7 +219,7 @@ unpack8_any_kernel(const __grid_constant__ Packed8 m, int M, int N, T* __restric
     const Unit unit(kWarp);
     const int lane = threadIdx.x % kWarp;
     for (Items it(unit, N, 1); it.row < M; it.next()) {
-        const int c = unit.first<false, sizeof(T)>((int)it.part);
+        const int c = unit.first<kOffGrid, sizeof(T)>((int)it.part);
         const uint8_t* row = m.q + it.row * m.ld;
         const bool words = sizeof(T) == 2 && ((uintptr_t)row & 1u) == 0;
         uint32_t w[2] = {0, 0};
@@ -252,7 +252,7 @@ unpack8_any_kernel(const __grid_constant__ Packed8 m, int M, int N, T* __restric
                 if (fabsf(f[i]) > kMost8<T>) f[i] = copysignf(kMost8<T>, f[i]);
             }
         }
-        store_cols<T, false>(y + it.row * ldy, c, N, kWarp, f);
+        store_cols<T, kOffGrid>(y + it.row * ldy, c, N, kWarp, f);
     }
 }
 
@@ -290,7 +290,7 @@ extern "C" dlrm_status dlrm_pack8(const void* d_x, int64_t ldx, dlrm_dtype dtype
     const bool vec = N % 8 == 0 && rows_aligned16(d_x, ldx, M, es) && rows_aligned8(d_q, ldq, M);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        const int lanes = unit_lanes(N, true, sizeof(T) == 2 ? 4 : 8), blocks = blocks8(N);   // a block's lanes at least
+        const int lanes = unit_lanes(N, kOnGrid, sizeof(T) == 2 ? 4 : 8), blocks = blocks8(N);   // a block's lanes at least
         if (vec)
             return check_launch_pdl(launch_pdl(pack8_kernel<T>, dim3(item_blocks(M, N, lanes, kRuns8<T>)), dim3(kThreads8), 0,
                                                as_stream(stream), (const T*)d_x, ldx, M, N, lanes, d_q, ldq, d_exps, blocks),

@@ -16,8 +16,11 @@ __device__ __forceinline__ int run_col(int first, int i)
     return first + (VEC ? ES == 2 ? i : i / 4 * 128 + i % 4 : ES == 2 ? i / 2 * 64 + i % 2 : i * 32);
 }
 
-// A unit of `lanes` threads (on the grid a power of two up to a warp, as many as a row has runs; else
-// a warp) takes U runs a lane of one row at a time, whose loads are in flight together.
+// How units read rows: on the 16-byte grid, off it, or off it by a few lanes, every lanes-th column each.
+enum { kOffGrid = 0, kOnGrid = 1, kFewLanes = 2 };
+
+// A unit of `lanes` threads (a power of two; off the grid a warp) takes U runs a lane of one row at a
+// time, whose loads are in flight together.
 struct Unit {
     int lanes, l;                 // the unit's threads, and which of them this is
     int64_t units, unit;          // in the grid
@@ -28,28 +31,33 @@ struct Unit {
         unit = (int64_t)blockIdx.x * per + threadIdx.x / n;
     }
     // the first column of the lane's run-th run of a row
-    template <bool VEC, int ES>
+    template <int LAY, int ES>
     __device__ __forceinline__ int first(int run) const
     {
-        return VEC ? run * lanes * 8 + l * (ES == 2 ? 8 : 4) : run * 256 + l * (ES == 2 ? 2 : 1);
+        return run * lanes * 8 + l * (LAY == kOnGrid ? 16 / ES : LAY == kOffGrid && ES == 2 ? 2 : 1);
     }
 };
 
 // Runs a lane takes at once: as many as eight 16-byte words hold for K rows; off the grid one, whose
 // single loads are as many (sums of two rows 40000 x 515 fp16: one run 41 us, four 62).
-template <typename T, bool VEC, int K>
-constexpr int kRuns = VEC && 16 / (K * (int)sizeof(T)) > 1 ? 16 / (K * (int)sizeof(T)) : 1;
+template <typename T, int LAY, int K>
+constexpr int kRuns = LAY == kOnGrid && 16 / (K * (int)sizeof(T)) > 1 ? 16 / (K * (int)sizeof(T)) : 1;
 
 // Whether two neighbouring 2-byte elements of a row are one 4-byte word.
 __device__ __forceinline__ bool row_of_words(const void* row) { return ((uintptr_t)row & 3u) == 0; }
 
-// The run's columns of a row; columns past its end read as 0 and are not stored.  VEC: a lane's second
+// The run's columns of a row; columns past its end read as 0 and are not stored.  On the grid a lane's second
 // 16-byte word is `lanes` words behind its first.
-template <typename T, bool VEC>
+template <typename T, int LAY>
 __device__ __forceinline__ Raw8<T> load_cols(const T* row, int first, int H, int lanes)
 {
     Raw8<T> r = {};
-    if constexpr (VEC) {
+    if constexpr (LAY == kFewLanes) {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = first + i * lanes < H ? __ldg(row + first + i * lanes) : from_f32<T>(0.f);
+        memcpy(&r, e, sizeof(e));
+    } else if constexpr (LAY == kOnGrid) {
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
             if (first + i * 4 * lanes < H) r.w[i] = ldg_nc_v4(row + first + i * 4 * lanes);
@@ -78,11 +86,17 @@ __device__ __forceinline__ Raw8<T> load_cols(const T* row, int first, int H, int
     return r;
 }
 
-template <typename T, bool VEC>
+template <typename T, int LAY>
 __device__ __forceinline__ void store_raw(T* row, int first, int H, int lanes, const Raw8<T>& r)
 {
     T* p = row + first;
-    if constexpr (VEC) {
+    if constexpr (LAY == kFewLanes) {
+        T e[8];
+        memcpy(e, &r, sizeof(e));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (first + i * lanes < H) p[i * lanes] = e[i];
+    } else if constexpr (LAY == kOnGrid) {
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
             if (first + i * 4 * lanes < H) *reinterpret_cast<uint4*>(p + i * 4 * lanes) = r.w[i];
@@ -108,13 +122,13 @@ __device__ __forceinline__ void store_raw(T* row, int first, int H, int lanes, c
     }
 }
 
-template <typename T, bool VEC>
+template <typename T, int LAY>
 __device__ __forceinline__ void store_cols(T* row, int first, int H, int lanes, const float (&f)[8])
 {
     Raw8<T> r;
     if constexpr (sizeof(T) == 2) r.w[0] = pack8<T>(f);
     else memcpy(&r, f, 32);
-    store_raw<T, VEC>(row, first, H, lanes, r);
+    store_raw<T, LAY>(row, first, H, lanes, r);
 }
 
 // Walks (row, part of the row) pairs, a unit at a time, without a division after the first.  The runs of a row
@@ -146,12 +160,19 @@ struct Items {
 
 // ---------------------------------------------------------------- host side
 // The lanes of a unit, and the blocks of 256 threads for rows taken in parts of `runs` runs a lane.
-inline int unit_lanes(int H, bool vec, int least = 1)
+// On the grid the most lanes of which four fifths have columns (160 fp32 columns of 5 rows: 8 lanes, not 32).
+inline int unit_lanes(int H, int lay, int least = 1)
 {
-    int n = vec ? least : kWarp;
-    while (n < kWarp && n * 8 < H) n *= 2;
-    return n;
+    if (lay == kOffGrid) return kWarp;
+    const int64_t runs = ((int64_t)H + 7) / 8;
+    int n = 1;
+    while (n < kWarp && n < runs) n *= 2;
+    while (lay == kOnGrid && n > 4 && 5 * runs < 4 * ((runs + n - 1) / n * n)) n /= 2;
+    return n < least ? least : n;
 }
+
+// Rows off the grid of up to 128 columns are a few lanes' each.
+inline int row_layout(bool vec, int H) { return vec ? kOnGrid : H <= 128 ? kFewLanes : kOffGrid; }
 
 inline unsigned item_blocks(int64_t rows, int H, int lanes, int runs)
 {
