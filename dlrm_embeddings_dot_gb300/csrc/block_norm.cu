@@ -17,39 +17,40 @@ struct NormSum {
     float *gw_post, *gb_post, *gscale, *gw_pre, *gb_pre;
 };
 
-// The vectors' gradients: kSumCols columns a block, a sector of each block's sums, 128 threads a column;
-// blockIdx.y 0 the side of the norm after the block, 1 that of the norm before the next.
-constexpr int kSumCols = 8, kSumRows = 128;
-
-__global__ void __launch_bounds__(kSumCols * kSumRows) block_norm_sum_kernel(const __grid_constant__ NormSum a)
+// The vectors' gradients: COLS columns a block, 1024 / COLS threads a column; blockIdx.y 0 the side of the
+// norm after the block, 1 that of the norm before the next.  Eight columns are a sector of each block's
+// sums; 32 are four, where there are columns for as many blocks (us, 8 / 32: 771 columns 4.7 / 5.2, 8192 18 / 7).
+template <int COLS>
+__global__ void __launch_bounds__(1024) block_norm_sum_kernel(const __grid_constant__ NormSum a)
 {
+    constexpr int kRows = 1024 / COLS, kEach = kWarp / COLS;   // threads a column; of them in a warp
     pdl_wait();
-    __shared__ float red[2][kSumRows / 4][kSumCols];
-    const int tx = threadIdx.x % kSumCols, ty = threadIdx.x / kSumCols, n = blockIdx.x * kSumCols + tx;
+    __shared__ float red[2][kRows / kEach][COLS];
+    const int tx = threadIdx.x % COLS, ty = threadIdx.x / COLS, n = blockIdx.x * COLS + tx;
     const bool pre = blockIdx.y == 1;
     if (pre ? !a.gw_pre && !a.gb_pre : !a.gw_post && !a.gb_post && !a.gscale) return;
     float s = 0.f, t = 0.f;
     if (n < a.N) {
         const float* p = a.partial + (pre ? 2 * a.Np : 0) + n;
 #pragma unroll 4
-        for (int b = ty; b < a.blocks; b += kSumRows) {
+        for (int b = ty; b < a.blocks; b += kRows) {
             s += p[(int64_t)b * 4 * a.Np];
             t += p[(int64_t)b * 4 * a.Np + a.Np];
         }
     }
 #pragma unroll
-    for (int m = 16; m >= kSumCols; m /= 2) {   // a warp's four rows
+    for (int m = 16; m >= COLS; m /= 2) {   // a warp's rows
         s += __shfl_xor_sync(~0u, s, m);
         t += __shfl_xor_sync(~0u, t, m);
     }
-    if (ty % 4 == 0) {
-        red[0][ty / 4][tx] = s;
-        red[1][ty / 4][tx] = t;
+    if (ty % kEach == 0) {
+        red[0][ty / kEach][tx] = s;
+        red[1][ty / kEach][tx] = t;
     }
     __syncthreads();
     if (ty || n >= a.N) return;
 #pragma unroll
-    for (int y = 1; y < kSumRows / 4; ++y) {
+    for (int y = 1; y < kRows / kEach; ++y) {
         s += red[0][y][tx];
         t += red[1][y][tx];
     }
@@ -210,7 +211,8 @@ extern "C" dlrm_status dlrm_block_norm_bwd(
           (!d_grad_residual || rows_aligned16(d_grad_residual, ldgres, M, es));
     const int64_t Np = (N + 7) / 8 * 8;
     const NormBwd a = {d_grad_r, d_grad_h, d_y, d_gate, d_r, ldgr, ldgh, ldy, ldg, ldr, !d_gate ? 0 : wide_gate ? N : 1,
-                       (const float4*)d_stats, d_w_post, d_b_post, d_scale, d_w_pre, M, N, end_rows(N, es), norm == DLRM_NORM_LAYER,
+                       (const float4*)d_stats, d_w_post, d_b_post, d_scale, d_w_pre, M, N, end_rows(N, es),
+                       norm == DLRM_NORM_LAYER,
                        (int)gate_act, (float)(1.0 / N), d_grad_y, d_grad_gate, d_grad_residual, ldgy, ldgg, ldgres,
                        sums ? (float*)d_workspace : nullptr, Np};
     s = with_type(dtype, [&](auto t) {
@@ -220,6 +222,8 @@ extern "C" dlrm_status dlrm_block_norm_bwd(
     if (s != DLRM_OK || !sums) return s;
     const NormSum q = {a.partial, Np, norm_blocks(M, N), N, d_w_post, d_b_post, d_scale,
                        d_grad_w_post, d_grad_b_post, d_grad_scale, d_grad_w_pre, d_grad_b_pre};
-    return check_launch_pdl(launch_pdl(block_norm_sum_kernel, dim3((N + kSumCols - 1) / kSumCols, 2), dim3(kSumCols * kSumRows), 0, st, q),
+    const int cols = N > 1024 ? 32 : 8;
+    return check_launch_pdl(launch_pdl(cols == 32 ? block_norm_sum_kernel<32> : block_norm_sum_kernel<8>,
+                                       dim3((N + cols - 1) / cols, 2), dim3(1024), 0, st, q),
                             "block_norm_sum_kernel");
 }

@@ -80,7 +80,9 @@ struct Cursor {
 // The rows to come: kAhead rows of NT tensors, three where the blocks that share an SM (two of
 // 256 threads, one of more) have the memory.  Columns past the row's end are 0.
 template <int STAGE, int THREADS>
-constexpr int kRowsAhead = (THREADS > 256 ? 224 << 10 : 110 << 10) / STAGE < 3 ? (THREADS > 256 ? 224 << 10 : 110 << 10) / STAGE : 3;
+constexpr int kRowsThatFit = (THREADS > 256 ? 224 << 10 : 110 << 10) / STAGE;
+template <int STAGE, int THREADS>
+constexpr int kRowsAhead = kRowsThatFit<STAGE, THREADS> < 3 ? kRowsThatFit<STAGE, THREADS> : 3;
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, uint32_t bytes)   // the rest of the word becomes 0
 {
@@ -167,7 +169,8 @@ struct Ring<T, kAny, NT, THREADS> {
             for (int w = lane; w * 16 < end; w += kWarp)
                 if (w > 0 || !cut) copy16(to + (w - lane) * 16, p - off + w * 16, min(16, end - w * 16));
             if (cut && lane >= off / kES && lane < min(16, end) / kES)
-                reinterpret_cast<T*>(mine + stage * kStage + slot * kSlot)[lane] = __ldg(reinterpret_cast<const T*>(p) + lane - off / kES);
+                reinterpret_cast<T*>(mine + stage * kStage + slot * kSlot)[lane] =
+                    __ldg(reinterpret_cast<const T*>(p) + lane - off / kES);
         }
     }
     static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -253,7 +256,8 @@ __device__ __forceinline__ void store_run(T* row, int first, int N, bool full, c
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int c = norm_col<LAY, 4>(first, 4 * i);
-                if (c < N) *reinterpret_cast<float4*>(row + c) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                if (c < N)
+                    *reinterpret_cast<float4*>(row + c) = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
             }
         }
     } else if constexpr (LAY < 0) {
@@ -323,7 +327,8 @@ __device__ __forceinline__ void store_vector(float* p, int first, int N, const f
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (norm_col<LAY, ES>(first, 4 * i) < N)
-                *reinterpret_cast<float4*>(p + norm_col<LAY, ES>(first, 4 * i)) = make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+                *reinterpret_cast<float4*>(p + norm_col<LAY, ES>(first, 4 * i)) =
+                    make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -425,7 +430,8 @@ struct Group {
 // ------------------------------------------------------------------- forward
 // (mean, 1 / sqrt(mean square + eps)) of a row; f becomes what is left without the mean, 0 past the end
 template <int LAY, int ES, int W>
-__device__ __forceinline__ float2 centre(float2 (&f)[4], int first, bool full, const NormFwd& a, float* red, int& turn, int warp)
+__device__ __forceinline__ float2 centre(float2 (&f)[4], int first, bool full, const NormFwd& a, float* red, int& turn,
+                                         int warp)
 {
     float s[1], mean = 0.f;
     if (a.layer) {
@@ -793,7 +799,8 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
                     for (int i = 0; i < 4; ++i) sum[s][i] = __fadd2_rn(sum[s][i], tile[i * 256 + g * W * 32 + threadIdx.x]);
             }
         }
-        if (warp < W && lane < kRowLanes<LAY>) store_vector<LAY, sizeof(T)>(a.partial + ((int64_t)blockIdx.x * 4 + s) * a.Np, first, N, sum[s]);
+        if (warp < W && lane < kRowLanes<LAY>)
+            store_vector<LAY, sizeof(T)>(a.partial + ((int64_t)blockIdx.x * 4 + s) * a.Np, first, N, sum[s]);
     }
 }
 

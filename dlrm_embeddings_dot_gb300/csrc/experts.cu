@@ -631,10 +631,9 @@ dlrm_status with_choices(int k, Fn&& fn)
 }
 
 // Blocks of 256 threads where `lanes` take a token.
-inline unsigned token_blocks(int64_t tokens, int lanes)
+inline unsigned token_blocks(int64_t tokens, int lanes, const void* kern)
 {
-    const int64_t want = (tokens * lanes + 255) / 256, most = (int64_t)num_sms() * 8;
-    return (unsigned)(want < most ? want : most);
+    return grid_blocks((tokens * lanes + 255) / 256, kern);
 }
 
 dlrm_status run_combine(const char* fn, const void* ys, int64_t ldys, const int32_t* slots, const float* probs,
@@ -651,9 +650,10 @@ dlrm_status run_combine(const char* fn, const void* ys, int64_t ldys, const int3
             return with_choices(k, [&](auto kk) {
                 constexpr int K = decltype(kk)::value;
                 const int lanes = unit_lanes(H, LAY);
-                return check_launch_pdl(launch_pdl(combine_kernel<E, LAY, K>, dim3(item_blocks(T, H, lanes, kRuns<E, LAY, K>)),
-                                                   dim3(256), 0, as_stream(stream), (const E*)ys, ldys, slots, probs,
-                                                   (const E*)res, ldres, T, k, H, R, lanes, (E*)y, ldy, status),
+                auto kern = combine_kernel<E, LAY, K>;
+                const unsigned blocks = item_blocks(T, H, lanes, kRuns<E, LAY, K>, (const void*)kern);
+                return check_launch_pdl(launch_pdl(kern, dim3(blocks), dim3(256), 0, as_stream(stream), (const E*)ys, ldys, slots,
+                                                   probs, (const E*)res, ldres, T, k, H, R, lanes, (E*)y, ldy, status),
                                         fn);
             });
         });
@@ -682,7 +682,7 @@ extern "C" dlrm_status dlrm_route_fwd(const void* d_logits, int64_t ldl, dlrm_dt
             constexpr int L = decltype(l)::value;
             auto kern = E % 8 == 0 && rows_aligned16(d_logits, ldl, T, sizeof(X)) ? route_fwd_kernel<X, true, L>
                                                                                   : route_fwd_kernel<X, false, L>;
-            return check_launch_pdl(launch_pdl(kern, dim3(token_blocks(T, L)), dim3(256), 0, as_stream(stream),
+            return check_launch_pdl(launch_pdl(kern, dim3(token_blocks(T, L, (const void*)kern)), dim3(256), 0, as_stream(stream),
                                                (const X*)d_logits, ldl, T, E, k, d_ids, d_probs),
                                     "route_fwd_kernel");
         });
@@ -708,8 +708,8 @@ extern "C" dlrm_status dlrm_route_bwd(const float* d_grad_probs, const int32_t* 
             constexpr int L = decltype(l)::value;
             auto kern = E % 8 == 0 && rows_aligned16(d_grad_logits, ldgl, T, sizeof(X)) ? route_bwd_kernel<X, true, L>
                                                                                         : route_bwd_kernel<X, false, L>;
-            return check_launch_pdl(launch_pdl(kern, dim3(token_blocks(T, L)), dim3(256), 0, as_stream(stream), d_grad_probs,
-                                               d_ids, d_probs, T, E, k, (X*)d_grad_logits, ldgl),
+            return check_launch_pdl(launch_pdl(kern, dim3(token_blocks(T, L, (const void*)kern)), dim3(256), 0, as_stream(stream),
+                                               d_grad_probs, d_ids, d_probs, T, E, k, (X*)d_grad_logits, ldgl),
                                     "route_bwd_kernel");
         });
     });
@@ -782,7 +782,7 @@ extern "C" dlrm_status dlrm_dispatch_fwd(const void* d_x, int64_t ldx, const int
         return with_layout(row_layout(vec, H), [&](auto l) {
             constexpr int LAY = decltype(l)::value;
             const int lanes = unit_lanes(H, LAY);
-            return check_launch_pdl(launch_pdl(dispatch_kernel<X, LAY>, dim3(item_blocks(T, H, lanes, kRuns<X, LAY, 2>)),
+            return check_launch_pdl(launch_pdl(dispatch_kernel<X, LAY>, dim3(item_blocks(T, H, lanes, kRuns<X, LAY, 2>, nullptr)),
                                                dim3(256), 0, as_stream(stream), (const X*)d_x, ldx, d_slots, T, k, H, R, lanes,
                                                (X*)d_xs, ldxs, d_status),
                                     "dispatch_kernel");
@@ -852,7 +852,7 @@ extern "C" dlrm_status dlrm_combine_bwd(const void* d_grad_y, int64_t ldgy, cons
     const int lay = row_layout(vec, H), lanes = unit_lanes(H, lay);
     const CombineBwd a = {d_grad_y, d_ys, ldgy, ldys, d_slots, d_probs, T, k, H, R, lanes, d_grad_ys, ldgys, d_grad_probs,
                           d_status};
-    const int64_t blocks = wide ? T : ((int64_t)T * lanes + 255) / 256, most = (int64_t)num_sms() * 8;
+    const int64_t blocks = wide ? T : ((int64_t)T * lanes + 255) / 256;
     return with_type(dtype, [&](auto t) {
         using X = decltype(t);
         return with_layout(lay, [&](auto l) {
@@ -862,7 +862,7 @@ extern "C" dlrm_status dlrm_combine_bwd(const void* d_grad_y, int64_t ldgy, cons
                 auto kern = combine_bwd_kernel<X, LAY, K, 1>;
                 if constexpr (LAY != kFewLanes)
                     if (wide) kern = combine_bwd_kernel<X, LAY, K, 8>;
-                return check_launch_pdl(launch_pdl(kern, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0,
+                return check_launch_pdl(launch_pdl(kern, dim3(grid_blocks(blocks, (const void*)kern)), dim3(256), 0,
                                                    as_stream(stream), a),
                                         "combine_bwd_kernel");
             });

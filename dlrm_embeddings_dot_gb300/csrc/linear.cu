@@ -13,6 +13,7 @@
 #include "few_rows.cuh"
 #include "gemm_tc.cuh"
 #include "packed8.cuh"
+#include "row_units.cuh"
 #include "thin_grad.cuh"
 
 namespace dlrm {
@@ -142,13 +143,15 @@ __global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ Unp
         while (i < n) {   // kUnpack runs at a time, whose loads are in flight together
             constexpr int kUnpack = 4;
             Run8 r[kUnpack];
-            int64_t at[kUnpack];
+            X* to[kUnpack];
+            int live = 0;
 #pragma unroll
-            for (int k = 0; k < kUnpack; ++k) {
-                at[k] = i;
+            for (int k = 0; k < kUnpack; ++k)
                 if (i < n) {
                     const int col = (int)g * 8, left = j0.cols - col;
                     r[k] = j0.vec && left >= 8 ? load_run8<true>(j0.src, row, col, 8) : load_run8<false>(j0.src, row, col, left);
+                    to[k] = (X*)j0.dst + i * 8;
+                    live = k + 1;
                     i += stride;
                     row += drow;
                     g += dg;
@@ -156,17 +159,14 @@ __global__ void __launch_bounds__(256) unpack_kernel(const __grid_constant__ Unp
                         g -= groups;
                         ++row;
                     }
-                } else {
-                    at[k] = n;
                 }
-            }
 #pragma unroll
-            for (int k = 0; k < kUnpack; ++k)
-                if (at[k] < n) {
-                    float f[8];
-                    widen_run8<T>(r[k], f);
-                    *reinterpret_cast<uint4*>((X*)j0.dst + at[k] * 8) = pack8<X>(f);
-                }
+            for (int k = 0; k < kUnpack; ++k) {
+                if (k >= live) break;
+                float f[8];
+                widen_run8<T>(r[k], f);
+                *reinterpret_cast<uint4*>(to[k]) = pack8<X>(f);
+            }
         }
         return;
     }
@@ -187,8 +187,9 @@ template <typename T>
 dlrm_status launch_unpack(Unpack8Job a, const PackJob& b, cudaStream_t st, Overlap overlap)
 {
     // (two blocks an SM, so that dZ's run beside them: 65536 x 1024 x 1024 fp16 333 us in all, eight 313)
-    auto blocks = [](int64_t runs, int each) {
-        const int64_t want = (runs + each - 1) / each, most = (int64_t)num_sms() * 8;
+    const int64_t most = blocks_at_once((const void*)unpack_kernel<T>);
+    auto blocks = [&](int64_t runs, int each) {
+        const int64_t want = (runs + each - 1) / each;
         return (int)(want < most ? want : most);
     };
     a.blocks = blocks((int64_t)a.rows * ((a.cols + 7) / 8), 1024);

@@ -59,35 +59,71 @@ __device__ __forceinline__ uint16_t round8(float lo, float hi)
     return h;
 }
 
-// The exponent of a block, which LANES neighbouring lanes have 32 / LANES values each of, and the
-// lane's values in its scale as bytes.  Infinities and NaN become NaN and do not count for the block.
-template <int LANES>
-__device__ __forceinline__ int block8(float (&f)[32 / LANES], uint32_t (&w)[8 / LANES])
+// The largest size in a block, which LANES neighbouring lanes have a 16-byte word each of, as fp32's bits.
+template <typename T, int LANES>
+__device__ __forceinline__ uint32_t block_size8(const uint4& v)
 {
-    constexpr int V = 32 / LANES;
     const uint32_t those = (LANES == 32 ? ~0u : (1u << LANES % 32) - 1) << (threadIdx.x % kWarp / LANES * LANES);
-    auto largest = [&] {
-        uint32_t top = 0;
+    if constexpr (sizeof(T) == 2) {   // sizes of numbers order as their bits do: two at a time
+        uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
 #pragma unroll
-        for (int i = 0; i < V; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+        for (int m = 1; m < LANES; m *= 2) top = __vmaxu2(top, __shfl_xor_sync(those, top, m));
+        const uint16_t h = (uint16_t)max(top & 0xffffu, top >> 16);
+        T t;
+        memcpy(&t, &h, 2);
+        return __float_as_uint(to_f32(t));
+    } else {
+        uint32_t top = max(max(v.x & 0x7fffffffu, v.y & 0x7fffffffu), max(v.z & 0x7fffffffu, v.w & 0x7fffffffu));
 #pragma unroll
         for (int m = 1; m < LANES; m *= 2) top = max(top, __shfl_xor_sync(those, top, m));
         return top;
-    };
-    uint32_t top = largest(), gone = 0;
-    if (top >= 0x7f800000u) {   // the same in all of the block's lanes
+    }
+}
+
+// A word with its infinities and NaN as zeros, and which they were.
+template <typename T>
+__device__ __forceinline__ uint32_t drop_wild(uint4& v)
+{
+    constexpr int V = 16 / sizeof(T);
+    T e[V];
+    memcpy(e, &v, 16);
+    uint32_t gone = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if ((__float_as_uint(f[i]) & 0x7fffffffu) >= 0x7f800000u) {
-                f[i] = 0.f;
-                gone |= 1u << i;
-            }
-        top = largest();
+    for (int i = 0; i < V; ++i)
+        if ((__float_as_uint(to_f32(e[i])) & 0x7fffffffu) >= 0x7f800000u) {
+            e[i] = from_f32<T>(0.f);
+            gone |= 1u << i;
+        }
+    memcpy(&v, e, 16);
+    return gone;
+}
+
+// The exponent of a block, and the lane's word of it in its scale as bytes.  Infinities and NaN become NaN
+// and do not count for the block.
+template <typename T>
+__device__ __forceinline__ int block8(uint4 v, uint32_t (&w)[4 / sizeof(T)])
+{
+    constexpr int V = 16 / sizeof(T), kLanes = kBlock8 / V;
+    uint32_t top = block_size8<T, kLanes>(v), gone = 0;
+    if (top >= 0x7f800000u) {   // the same in all of the block's lanes
+        gone = drop_wild<T>(v);
+        top = block_size8<T, kLanes>(v);
     }
     const int e = exponent8(top);
     const float up = scale_up(e);
+    float f[8];
+    if constexpr (sizeof(T) == 2) {
+        unpack8<T>(v, f);
+    } else {
+        const float4 g = u4_as_f4(v);
+        f[0] = g.x; f[1] = g.y; f[2] = g.z; f[3] = g.w;
+    }
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = gone >> i & 1 ? __uint_as_float(0x7fc00000u) : f[i] * up;
+    for (int i = 0; i < V; ++i) f[i] *= up;
+    if (gone)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (gone >> i & 1) f[i] = __uint_as_float(0x7fc00000u);
 #pragma unroll
     for (int i = 0; i < V / 4; ++i)
         w[i] = round8(f[4 * i], f[4 * i + 1]) | (uint32_t)round8(f[4 * i + 2], f[4 * i + 3]) << 16;
@@ -114,15 +150,10 @@ pack8_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, int lanes, uint
         for (int u = 0; u < U; ++u) {
             if (u >= it.per) break;
             const int c = unit.first<kOnGrid, sizeof(T)>(it.run(u));
-            float f[8];
-            widen8<T>(v[u], f);
 #pragma unroll
             for (int h = 0; h < 8 / V; ++h) {   // the run's 16-byte words
-                float g[V];
                 uint32_t w[V / 4];
-#pragma unroll
-                for (int i = 0; i < V; ++i) g[i] = f[h * V + i];
-                const int e = block8<kBlock8 / V>(g, w), at = c + h * 4 * lanes;
+                const int e = block8<T>(v[u].w[h], w), at = c + h * 4 * lanes;
                 if (at < N) {
                     uint8_t* p = q + it.row * ldq + at;
                     if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
@@ -131,6 +162,31 @@ pack8_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, int lanes, uint
                 }
             }
         }
+    }
+}
+
+// The same of eight neighbours a lane, four lanes a block.
+template <typename T>
+__device__ __forceinline__ int run8(Raw8<T> v, uint32_t (&w)[2])
+{
+    if constexpr (sizeof(T) == 2) {
+        return block8<T>(v.w[0], w);
+    } else {
+        uint32_t gone = 0, top = max(block_size8<T, 4>(v.w[0]), block_size8<T, 4>(v.w[1]));
+        if (top >= 0x7f800000u) {
+            gone = drop_wild<T>(v.w[0]) | drop_wild<T>(v.w[1]) << 4;
+            top = max(block_size8<T, 4>(v.w[0]), block_size8<T, 4>(v.w[1]));
+        }
+        const int e = exponent8(top);
+        const float up = scale_up(e);
+        float f[8];
+        widen8<T>(v, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = gone >> i & 1 ? __uint_as_float(0x7fc00000u) : f[i] * up;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = round8(f[4 * i], f[4 * i + 1]) | (uint32_t)round8(f[4 * i + 2], f[4 * i + 3]) << 16;
+        return e;
     }
 }
 
@@ -147,15 +203,20 @@ pack8_any_kernel(const T* __restrict__ x, int64_t ldx, int M, int N, uint8_t* __
     for (Words w8(M, (int64_t)blocks * 4); w8.more(); w8.next()) {   // a quad's lanes leave together
         const int64_t row = w8.row, c = w8.g * 8;
         const int n = (int)min((int64_t)8, N - c);    // 0 or less: past the row's end
-        float f[8] = {};
+        Raw8<T> v = {};
         if (n > 0) {
-            widen8<T>(load8_shifted<T>(x + row * ldx + c, n, x, end), f);
+            v = load8_shifted<T>(x + row * ldx + c, n, x, end);
+            if (n < 8) {
+                T e[8];
+                memcpy(e, &v, sizeof(e));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i >= n) f[i] = 0.f;
+                for (int i = 0; i < 8; ++i)
+                    if (i >= n) e[i] = from_f32<T>(0.f);
+                memcpy(&v, e, sizeof(e));
+            }
         }
         uint32_t w[2];
-        const int e = block8<4>(f, w);
+        const int e = run8<T>(v, w);
         uint8_t* p = q + row * ldq + c;
         const uint32_t off = (uint32_t)(uintptr_t)p & 7u;
         if (n == 8 && off == 0) {
@@ -265,10 +326,9 @@ dlrm_status check_sizes8(const char* fn, dlrm_dtype dtype, int M, int N)
 }
 
 // Blocks for lanes that take `each` words at a time.
-unsigned word_blocks(int64_t words, int each)
+unsigned word_blocks(int64_t words, int each, const void* kern)
 {
-    const int64_t want = (words + kThreads8 * each - 1) / (kThreads8 * each), most = (int64_t)num_sms() * 8;
-    return (unsigned)(want < most ? want : most);
+    return grid_blocks((words + kThreads8 * each - 1) / (kThreads8 * each), kern);
 }
 
 }  // namespace
@@ -291,12 +351,17 @@ extern "C" dlrm_status dlrm_pack8(const void* d_x, int64_t ldx, dlrm_dtype dtype
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
         const int lanes = unit_lanes(N, kOnGrid, sizeof(T) == 2 ? 4 : 8), blocks = blocks8(N);   // a block's lanes at least
-        if (vec)
-            return check_launch_pdl(launch_pdl(pack8_kernel<T>, dim3(item_blocks(M, N, lanes, kRuns8<T>)), dim3(kThreads8), 0,
-                                               as_stream(stream), (const T*)d_x, ldx, M, N, lanes, d_q, ldq, d_exps, blocks),
+        if (vec) {
+            auto kern = pack8_kernel<T>;
+            const unsigned grid = item_blocks(M, N, lanes, kRuns8<T>, (const void*)kern);
+            return check_launch_pdl(launch_pdl(kern, dim3(grid), dim3(kThreads8), 0, as_stream(stream), (const T*)d_x, ldx, M, N,
+                                               lanes, d_q, ldq, d_exps, blocks),
                                     "pack8_kernel");
-        return check_launch_pdl(launch_pdl(pack8_any_kernel<T>, dim3(word_blocks((int64_t)M * blocks * 4, 1)), dim3(kThreads8),
-                                           0, as_stream(stream), (const T*)d_x, ldx, M, N, d_q, ldq, d_exps, blocks),
+        }
+        auto kern = pack8_any_kernel<T>;
+        const unsigned grid = word_blocks((int64_t)M * blocks * 4, 1, (const void*)kern);
+        return check_launch_pdl(launch_pdl(kern, dim3(grid), dim3(kThreads8), 0, as_stream(stream), (const T*)d_x, ldx, M, N, d_q,
+                                           ldq, d_exps, blocks),
                                 "pack8_any_kernel");
     });
 }
@@ -317,7 +382,9 @@ extern "C" dlrm_status dlrm_unpack8(const uint8_t* d_q, int64_t ldq, const uint8
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
         auto kern = vec ? unpack8_kernel<T> : unpack8_any_kernel<T>;
-        const unsigned blocks = vec ? word_blocks((int64_t)M * N * (int)sizeof(T) / 16, kWords8) : item_blocks(M, N, kWarp, 1);
+        const void* const k = (const void*)kern;
+        const unsigned blocks = vec ? word_blocks((int64_t)M * N * (int)sizeof(T) / 16, kWords8, k)
+                                    : item_blocks(M, N, kWarp, 1, k);
         return check_launch_pdl(launch_pdl(kern, dim3(blocks), dim3(kThreads8), 0, as_stream(stream), m, M, N, (T*)d_y, ldy),
                                 "unpack8_kernel");
     });
