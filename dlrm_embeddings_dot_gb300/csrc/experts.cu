@@ -197,7 +197,7 @@ dlrm_status with_lanes(int E, Fn&& fn)
 // the chunks' counts first, and a block adds up those of the blocks before it (and all of
 // them: where an expert begins).  The steps are chains of latencies: a warp's choices are
 // loaded kBatch rounds at a time, and the counts' sums are shared out over all threads.
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / kWarp;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / kWarp;
 constexpr int kSortChunk = 2048;        // choices of a block, while there are no more than kSortBlocks blocks
 constexpr int kSortOne = 4096;          // so many choices are one block's
 constexpr int kSortBlocks = 128;    // each of which reads all counts
@@ -279,7 +279,7 @@ __device__ __forceinline__ void count_parts(const Part& part, int E, int (*warps
 __global__ void __launch_bounds__(kSortThreads)
 expert_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int E, int32_t* __restrict__ counts)
 {
-    pdl_wait();
+    pdl_begin({0, 1});   // the places' kernel counts its choices meanwhile
     __shared__ int warps[kSortWarps][kBins];
     const Part part(ids, n, chunk);
     count_parts(part, E, warps);
@@ -296,29 +296,33 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
                     int32_t* __restrict__ offsets, int32_t* __restrict__ slots, int32_t* __restrict__ order,
                     uint32_t* __restrict__ status)
 {
-    pdl_wait();
     __shared__ int warps[kSortWarps][kBins];
     __shared__ int total[kBins], before[kBins], scan[kSortWarps];
     const int bins = E + 1, tid = threadIdx.x;
+    if (gridDim.x == 1) pdl_wait();   // else the counts' kernel has waited for the choices
     const Part part(ids, n, chunk);
+    for (int e = tid; e < bins; e += kSortThreads) total[e] = before[e] = 0;
+    count_parts(part, E, warps);
     if (gridDim.x > 1) {
-        for (int e = tid; e < bins; e += kSortThreads) total[e] = before[e] = 0;
-        __syncthreads();
+        pdl_wait();
         // a thread has one bin of every (kSortThreads / bins)-th block
         const int parts = kSortThreads / bins, e = tid % bins, p = tid / bins;
         if (p < parts) {
             int all = 0, ahead = 0;
+            // a block begins with its own row, so that they do not all ask for the same one
+            const int rows = ((int)gridDim.x - p + parts - 1) / parts, from = (int)(blockIdx.x % rows);
 #pragma unroll 8
-            for (int b = p; b < (int)gridDim.x; b += parts) {
-                const int v = __ldg(counts + b * bins + e);
+            for (int i = 0; i < rows; ++i) {
+                const int b = p + (i + from < rows ? i + from : i + from - rows) * parts;
+                const int v = __ldcg(counts + b * bins + e);
                 all += v;
                 ahead += b < (int)blockIdx.x ? v : 0;
             }
             atomicAdd(&total[e], all);      // whole numbers: the same in any order
             atomicAdd(&before[e], ahead);
         }
+        __syncthreads();
     }
-    count_parts(part, E, warps);
     // where each expert's places begin: an exclusive scan of the totals over the bins
     {
         const int e = tid, lane = e % kWarp;
