@@ -195,7 +195,7 @@ dlrm_status dlrm_combine_bwd(const void* d_grad_y, int64_t ldgy, const void* d_y
  * 448 or less, so that all but the smallest values keep 4 significant bits; values are
  * rounded to nearest, ties to even.  Infinities and NaN become NaN.
  * A value read back is at most dtype's largest in size (fp32: bf16's), where rounding
- * took it past that.
+ * took it past that.  (dlrm_pack8 makes no byte e past 247; 255 is not a power of two.)
  *
  *   dlrm_pack8     q, exps = x
  *   dlrm_unpack8   y = q 2^(e - 127)

@@ -44,7 +44,8 @@ def _d(t):
 # ------------------------------------------------------------------------------------------- norms
 SHAPES = [(1, 1, 0, 0), (1, 8, 0, 0), (3, 7, 0, 0), (2, 33, 3, 1), (5, 256, 0, 0), (2, 257, 0, 0), (37, 480, 8, 0),
           (300, 1024, 0, 0), (3, 1032, 8, 0), (9, 2048, 0, 1), (2, 2500, 0, 0), (4, 4100, 0, 0), (3, 8192, 0, 0),
-          (2, 8191, 0, 0), (2600, 96, 0, 0), (700, 515, 0, 0)]
+          (2, 8191, 0, 0), (2600, 96, 0, 0), (700, 515, 0, 0), (5000, 16, 0, 0), (333, 32, 8, 0), (77, 64, 0, 1),
+          (65, 128, 8, 0), (513, 128, 0, 0), (19, 200, 0, 0), (9, 1999, 1, 0)]
 OPTIONS = [   # layer, gate, per row, block, next norm, vectors, residual
     (False, None, False, True, True, False, True), (False, "silu", False, True, True, True, True),
     (True, "sigmoid", True, True, True, True, True), (True, "raw", False, True, False, True, False),
@@ -251,6 +252,21 @@ def test_route(cuda_lib, dtype, T, E, k, pad, closed):
     put = lambda t: torch.zeros(T, E + 1, dtype=torch.float64).scatter_(1, torch.where(rid < 0, E, rid), t)[:, :E]
     dref.assert_close(grad, put(v), put(e), dtype)
     assert _guard_ok(grad)
+
+
+def test_route_gradient_of_the_same_expert_twice(cuda_lib):
+    """Not what the choice gives, but what a call may hold: the last of equal ids counts, ids outside none."""
+    ids = torch.tensor([[3, 3, 1], [7, -1, 7], [0, 8, 9]], dtype=torch.int32, device=dev())
+    probs, gp = torch.rand(3, 3, device=dev()), torch.rand(3, 3, device=dev())
+    inside = (ids >= 0) & (ids < 8)
+    p, g = torch.where(inside, probs, 0.0).double().cpu(), torch.where(inside, gp, 0.0).double().cpu()
+    d = p * (g - (p * g).sum(1, keepdim=True))
+    for pad in (0, 1):
+        grad = _empty(3, 8, "f32", pad)
+        cuda_lib.dlrm_route_bwd(gp, ids, probs, grad)
+        want = torch.zeros(3, 8, dtype=torch.float64)
+        want[0, 3], want[0, 1], want[1, 7], want[2, 0] = d[0, 1], d[0, 2], d[1, 2], d[2, 0]
+        assert ((grad.double().cpu() - want).abs() <= 2.0**-20).all() and _guard_ok(grad)
 
 
 def test_route_where_logits_are_not_numbers(cuda_lib):
