@@ -25,7 +25,7 @@
 // Nothing here depends on which columns a lane has.  On the 16-byte grid they are 16-byte words.
 // Off it a warp copies the aligned 16-byte words that hold its 256 columns and a lane has every
 // 32nd column, or pair of them, which shared memory gives without conflicts; the instructions for that
-// bound it (40000 x 771 bf16, centred: 136 and 186 us, 0.34 and 0.40).
+// bound it (40000 x 771 bf16, centred: 140 and 191 us, 0.33 and 0.39).
 #pragma once
 
 #include "block_norm.h"
@@ -663,6 +663,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
         const float4 st = st_next;
         float g1 = g_next, slope1 = 1.f;
         st_next = make_float4(0, 0, 0, 0);
+        g_next = 1.f;   // lanes without a next row: not this row's gate, which may be infinite
         if (row + step < a.M) {
             st_next = __ldg(a.stats + row + step);
             if (a.gate_cols == 1) g_next = to_f32(__ldg(cg.ahead(1)));

@@ -167,6 +167,21 @@ def test_norm_backward_of_rows_that_share_a_block(cuda_lib, N):
             assert torch.equal(out[k], first[k])
 
 
+@pytest.mark.parametrize("N", [16, 40, 100])
+def test_norm_gradient_of_infinite_gates(cuda_lib, N):
+    """Gates of infinity by row and gradients of 1: the bias's gradient is infinite, also where the last rows
+    are fewer than a warp's."""
+    M = 20001
+    y, ones = torch.randn(M, N, device=dev()), torch.ones(M, N, device=dev())
+    gate = torch.full((M, 1), INF, device=dev())
+    st = torch.zeros(M, 4, device=dev())
+    gb = torch.zeros(N, device=dev())
+    ws = torch.empty(cuda_lib.dlrm_block_norm_bwd_workspace_size(y), dtype=torch.uint8, device=dev())
+    cuda_lib.dlrm_block_norm_bwd(ones, None, y, gate, None, st, None, None, None, None, None, None, None, None, gb, None, None,
+                                 None, workspace=ws)
+    assert torch.equal(gb, torch.full_like(gb, INF))
+
+
 def test_norm_rows_of_zeros_constants_and_numbers_that_are_none(cuda_lib):
     """A row of zeros is zeros (eps > 0), a constant row of LAYER its bias, infinities and NaN stay in their rows."""
     for layer in (False, True):
