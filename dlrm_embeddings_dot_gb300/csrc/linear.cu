@@ -596,13 +596,7 @@ BwdLayout bwd_layout(const void* dy, int64_t ldg, const Kept& in, const void* w,
 {
     BwdLayout l = {};
     if (few_outputs(N)) {
-        if (in.bits8) {   // read back first
-            const int es = dense_dtype_size(dt);
-            l.x = dlrm_ws_align((size_t)M * padded(K) * es);
-            l.dz = act != DLRM_ACT_NONE ? dlrm_ws_align((size_t)M * padded(N) * es) : 0;
-        }
-        l.sums = thin::workspace_bytes(dt, M, N, K);
-        l.total = l.dz + l.x + l.sums;
+        l.total = l.sums = thin::workspace_bytes(dt, M, N, K);
         return l;
     }
     l.dz = act != DLRM_ACT_NONE || p > 0 || needs_pack(dy, ldg, M, dt) ? operand_bytes(M, N, z_planes(dt, act)) : 0;
@@ -660,28 +654,16 @@ dlrm_status run_bwd(const char* fn, const void* d_grad_y, int64_t ldg, const Kep
         const float z_scale = zp == 2 ? scale / kFit<T> : scale;
         if (few_outputs(N)) {
             if (!d_grad_x && !d_grad_w && !d_grad_bias) return DLRM_OK;
-            uint8_t* ws = (uint8_t*)d_workspace;
-            Kept at = in;
-            if (in.bits8) {
-                dlrm_status r = DLRM_OK;
-                at.pre = ws;
-                at.x = ws + l.dz;
-                at.ldp = padded(N);
-                at.ldx = padded(K);
-                if (act != DLRM_ACT_NONE)
-                    r = dlrm_unpack8(in.pre8.q, in.pre8.ld, in.pre8.exps, dtype, M, N, ws, at.ldp, st);
-                if (r == DLRM_OK && d_grad_w)
-                    r = dlrm_unpack8(in.x8.q, in.x8.ld, in.x8.exps, dtype, M, K, ws + l.dz, at.ldx, st);
-                if (r != DLRM_OK) return r;
-                ws += l.dz + l.x;
-            }
-            thin::Grad a = {d_grad_y, at.pre, at.x, d_w, ldg, at.ldp, at.ldx, ldw, M, N, K, (int)act, drop, z_scale, scale};
+            thin::Grad a = {d_grad_y, in.pre, in.x, d_w, ldg, in.ldp, in.ldx, ldw, M, N, K, (int)act, drop, z_scale, scale};
+            a.x8 = in.x8;
+            a.pre8 = in.pre8;
             a.dx = d_grad_x;
             a.dw = d_grad_w;
             a.lddx = lddx;
             a.lddw = lddw;
             a.db = d_grad_bias;
-            return thin::run<T>(dtype, a, (float*)ws, st);
+            float* const sums = (float*)d_workspace;
+            return in.bits8 ? thin::run8(dtype, a, sums, st) : thin::run<T, false>(dtype, a, sums, st);
         }
         const bool bf = dtype != DLRM_F16;
         uint8_t* ws = (uint8_t*)d_workspace;
@@ -714,7 +696,7 @@ dlrm_status run_bwd(const char* fn, const void* d_grad_y, int64_t ldg, const Kep
         }
         Epilogue ex = {}, ew = {};
         ex.scale = ew.scale = z_scale;
-        const Shape sx = grad_shape(dtype, act, M, K, N), 
+        const Shape sx = grad_shape(dtype, act, M, K, N),
                     sw = in.bits8 ? grad_shape8(dtype, act, N, K, M) : grad_shape(dtype, act, N, K, M);
         if (r == DLRM_OK && d_grad_x) {
             ex.out = d_grad_x;

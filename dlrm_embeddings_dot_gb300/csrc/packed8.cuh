@@ -93,6 +93,16 @@ __device__ __forceinline__ void widen_run8(const Run8& r, float (&f)[8])
     widen_codes8<T>(r.q, scale, f);
 }
 
+// One column: a code and its block's exponent byte.
+template <typename T>
+__device__ __forceinline__ float value8(uint32_t code, uint32_t e)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
+    const float f = __half2float(__ushort_as_half((uint16_t)h)) * scale8(e);
+    return fabsf(f) > kMost8<T> ? copysignf(kMost8<T>, f) : f;
+}
+
 // Whether runs of eight columns start on 8-byte boundaries in every row.
 inline bool rows_aligned8(const void* p, int64_t ld, int rows)
 {

@@ -17,10 +17,15 @@
 // HBM bounds few outputs, the instructions of a row many: 65536 x 1024, us, for 1, 8 and 16
 // outputs: fp16 63, 65, 74 (two passes over x at the measured copy rate: 40), fp32 99, 114,
 // 172 (79).  One launch and the sum of the chunks is all that a small batch pays (300 x 64: 6.4).
+//
+// P8: x and the pre-activation come in 8 bits (packed8.cuh) and are widened in registers; the sums are
+// the same.  46101 x 574 to 16, fp16, GELU: 148 us with both read back to copies first, 81 so;
+// 65536 x 1024 to 1 and 16 outputs bf16 61, 72 (31 of them the floor).
 #pragma once
 
 #include "dense_epilogue.cuh"
 #include "few_rows.cuh"
+#include "packed8.cuh"
 
 namespace dlrm {
 namespace thin {
@@ -39,11 +44,12 @@ struct Grad {
     int64_t lddx, lddw;
     float* db;          // may be NULL
     float* partial;     // [chunks][N * K + N], NULL for one chunk
+    Packed8 x8, pre8;   // x and pre of the kernels that take them in 8 bits (P8)
 };
 
 // dZ of the rows t0 .. t0 + rows - 1 (256 at most, one a thread), eight outputs at a time:
 // store(group, values).  Where bias is summed, lane n of a warp adds the warp's rows of output n to b.
-template <typename T, typename Store>
+template <typename T, bool P8, typename Store>
 __device__ __forceinline__ void tile_of_dz(const Grad& a, const DropKey& key, int t0, int rows, float& b, Store store)
 {
     const int tid = threadIdx.x, row = t0 + tid;
@@ -56,7 +62,8 @@ __device__ __forceinline__ void tile_of_dz(const Grad& a, const DropKey& key, in
             widen8<T>(load8<T, false>((const T*)a.dy + row * a.ldg + g * 8, n), f);
             if (a.act != DLRM_ACT_NONE) {
                 float z[8];
-                widen8<T>(load8<T, false>((const T*)a.pre + row * a.ldp + g * 8, n), z);
+                if constexpr (P8) widen_run8<T>(load_run8<false>(a.pre8, row, g * 8, n), z);
+                else widen8<T>(load8<T, false>((const T*)a.pre + row * a.ldp + g * 8, n), z);
                 slope8<T>(f, z, a.act);
             }
             if (a.drop.thr) drop8(f, a.drop, key, (uint32_t)row, (uint32_t)g);
@@ -136,7 +143,7 @@ __device__ __forceinline__ uint32_t pack2(T lo, T hi)
 // for 8, 30 / 70 for 16.
 // TERMS: dZ as one value of the type, or as the sum of two (GELU and SILU, whose slopes it does not
 // hold): the products of the second are added first.
-template <typename T, bool VEC, int TERMS>
+template <typename T, bool VEC, int TERMS, bool P8>
 __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_constant__ Grad a)
 {
     pdl_wait();
@@ -182,15 +189,20 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
 
     const T* const xend = (const T*)a.x + (a.M - 1) * a.ldx + a.K;
     // rows s + 2 q, + 1, + 8, + 9 of a tile; element j of a row is step j's
-    auto fetch = [&](int t0, int rows, int s, uint4 (&v)[4]) {
+    using Run = std::conditional_t<P8, Run8, uint4>;
+    auto fetch = [&](int t0, int rows, int s, Run (&v)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = s + 2 * q + i % 2 + i / 2 * 8;
-            const T* p = (const T*)a.x + (t0 + r) * a.ldx + c0;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (r < rows && g * 8 < left) {
+            const int n = (int)min((int64_t)8, left - g * 8);
+            v[i] = {};
+            if (r >= rows || n <= 0) continue;
+            if constexpr (P8) {
+                v[i] = load_run8<VEC>(a.x8, t0 + r, (int)c0 + g * 8, n);
+            } else {
+                const T* p = (const T*)a.x + (t0 + r) * a.ldx + c0;
                 if constexpr (VEC) v[i] = ldg_nc_v4(reinterpret_cast<const uint4*>(p) + g);
-                else v[i] = load8_shifted<T>(p + g * 8, (int)min((int64_t)8, left - g * 8), (const T*)a.x, xend).w[0];
+                else v[i] = load8_shifted<T>(p + g * 8, n, (const T*)a.x, xend).w[0];
             }
         }
     };
@@ -198,10 +210,10 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
     const int r0 = blockIdx.y * a.rows, r1 = min(a.M, r0 + a.rows);
     for (int t0 = r0; t0 < r1; t0 += kTile) {
         const int rows = min(kTile, r1 - t0);
-        uint4 xn[4];
+        Run xn[4];
         if (a.dw) fetch(t0, rows, rw * 16, xn);
         __syncthreads();
-        tile_of_dz<T>(a, key, t0, rows, bsum, [&](int h, const float (&f)[8]) {
+        tile_of_dz<T, P8>(a, key, t0, rows, bsum, [&](int h, const float (&f)[8]) {
             if constexpr (TERMS == 2) {
                 float hi[8], lo[8];
 #pragma unroll
@@ -218,7 +230,15 @@ __global__ void __launch_bounds__(256, 2) thin_grad_mma_kernel(const __grid_cons
             uint4 xv[4];
             if (a.dw) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) xv[i] = xn[i];
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (P8) {
+                        float f[8];
+                        widen_run8<T>(xn[i], f);
+                        xv[i] = pack8<T>(f);
+                    } else {
+                        xv[i] = xn[i];
+                    }
+                }
                 fetch(t0, rows, s + step * 16, xn);
             }
             const uint32_t at = (uint32_t)__cvta_generic_to_shared(dzs[0]) + (s * kPitch) * 2;
@@ -362,7 +382,7 @@ __device__ __forceinline__ void store_run(float* p, const float (&v)[C])
 // values are 32 each at most.  VEC: rows of x, W and dX are on the 16-byte grid and K is
 // a multiple of C; a thread's columns lie cg apart without it, which keeps a warp's
 // accesses on consecutive elements.
-template <int NT, int C, bool VEC>
+template <int NT, int C, bool VEC, bool P8>
 __global__ void __launch_bounds__(256, 2) thin_grad_f32_kernel(const __grid_constant__ Grad a)
 {
     pdl_wait();
@@ -385,6 +405,30 @@ __global__ void __launch_bounds__(256, 2) thin_grad_f32_kernel(const __grid_cons
         }
     };
 
+    // a row of x in 8 bits; columns past its end are some others'
+    auto load8bits = [&](int row, float (&v)[C]) {
+        const uint8_t* q = a.x8.q + row * a.x8.ld;
+        const uint8_t* e = a.x8.exps + (int64_t)row * a.x8.blocks;
+        if constexpr (VEC) {
+            const int c = in(0) ? (int)c0 + at(0, tx) : 0;
+            Run8 r = {};
+            if constexpr (C == 8) r.q = __ldg(reinterpret_cast<const uint2*>(q + c));
+            else if constexpr (C == 4) r.q.x = __ldg(reinterpret_cast<const uint32_t*>(q + c));
+            else r.q.x = __ldg(reinterpret_cast<const uint16_t*>(q + c));
+            r.e = __ldg(e + c / kBlock8);
+            float f[8];
+            widen_run8<float>(r, f);
+#pragma unroll
+            for (int i = 0; i < C; ++i) v[i] = f[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int c = in(i) ? (int)c0 + at(i, tx) : 0;
+                v[i] = value8<float>(__ldg(q + c), __ldg(e + c / kBlock8));
+            }
+        }
+    };
+
     float wv[NT][C], acc[NT][C], bsum = 0.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -397,7 +441,7 @@ __global__ void __launch_bounds__(256, 2) thin_grad_f32_kernel(const __grid_cons
     for (int t0 = r0; t0 < r1; t0 += kTile) {
         const int rows = min(kTile, r1 - t0);
         __syncthreads();
-        tile_of_dz<float>(a, key, t0, rows, bsum, [&](int h, const float (&f)[8]) {
+        tile_of_dz<float, P8>(a, key, t0, rows, bsum, [&](int h, const float (&f)[8]) {
 #pragma unroll
             for (int i = 0; i < (NT < 8 ? NT : 8); ++i) dzs[tid][h * 8 + i] = f[i];
         });
@@ -406,8 +450,10 @@ __global__ void __launch_bounds__(256, 2) thin_grad_f32_kernel(const __grid_cons
             float xv[kAhead][C] = {};
             if (a.dw)
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (r + k * step < rows) load((const float*)a.x + (t0 + r + k * step) * a.ldx, xv[k]);
+                for (int k = 0; k < kAhead; ++k) {
+                    if constexpr (P8) load8bits(t0 + min(r + k * step, rows - 1), xv[k]);   // no branches: loads, then conversions
+                    else if (r + k * step < rows) load((const float*)a.x + (t0 + r + k * step) * a.ldx, xv[k]);
+                }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int rr = r + k * step;
@@ -535,7 +581,7 @@ inline size_t workspace_bytes(dlrm_dtype dt, int M, int N, int K)
 }
 
 // a.cg, a.rows and a.partial are set here.
-template <typename T>
+template <typename T, bool P8>
 dlrm_status run(dlrm_dtype dt, Grad a, float* ws, cudaStream_t st)
 {
     const Shape s = shape(dt, a.M, a.N, a.K);
@@ -544,13 +590,14 @@ dlrm_status run(dlrm_dtype dt, Grad a, float* ws, cudaStream_t st)
     a.partial = s.chunks > 1 ? ws : nullptr;
     const dim3 grid(a.dx || a.dw ? s.blocks_x : 1, s.chunks);
     const int es = sizeof(T);
-    const bool vec = (!a.dw || rows_aligned16(a.x, a.ldx, a.M, es)) && (!a.dx || rows_aligned16(a.dx, a.lddx, a.M, es));
+    const bool vec = (!a.dw || (P8 ? rows_aligned8(a.x8.q, a.x8.ld, a.M) : rows_aligned16(a.x, a.ldx, a.M, es))) &&
+                     (!a.dx || rows_aligned16(a.dx, a.lddx, a.M, es));
     dlrm_status r;
     if constexpr (std::is_same_v<T, float>) {
         const bool v = vec && a.K % columns(a.N) == 0 && (!a.dx || rows_aligned16(a.w, a.ldw, a.N, es));
         auto go = [&](auto n) {
             constexpr int NT = decltype(n)::value, C = NT <= 4 ? 8 : NT <= 8 ? 4 : 2;
-            auto kern = v ? thin_grad_f32_kernel<NT, C, true> : thin_grad_f32_kernel<NT, C, false>;
+            auto kern = v ? thin_grad_f32_kernel<NT, C, true, P8> : thin_grad_f32_kernel<NT, C, false, P8>;
             return check_launch_pdl(launch_pdl(kern, grid, dim3(256), 0, st, a), "thin_grad_f32_kernel");
         };
         r = a.N == 1   ? go(std::integral_constant<int, 1>{})
@@ -559,8 +606,8 @@ dlrm_status run(dlrm_dtype dt, Grad a, float* ws, cudaStream_t st)
                        : go(std::integral_constant<int, 16>{});
     } else {
         const bool v = vec && a.K % 8 == 0, two = a.act == DLRM_ACT_GELU || a.act == DLRM_ACT_SILU;
-        auto kern = two ? (v ? thin_grad_mma_kernel<T, true, 2> : thin_grad_mma_kernel<T, false, 2>)
-                        : (v ? thin_grad_mma_kernel<T, true, 1> : thin_grad_mma_kernel<T, false, 1>);
+        auto kern = two ? (v ? thin_grad_mma_kernel<T, true, 2, P8> : thin_grad_mma_kernel<T, false, 2, P8>)
+                        : (v ? thin_grad_mma_kernel<T, true, 1, P8> : thin_grad_mma_kernel<T, false, 1, P8>);
         r = check_launch_pdl(launch_pdl(kern, grid, dim3(256), 0, st, a), "thin_grad_mma_kernel");
     }
     if (r != DLRM_OK || s.chunks == 1 || !(a.dw || a.db)) return r;
@@ -574,6 +621,9 @@ dlrm_status run(dlrm_dtype dt, Grad a, float* ws, cudaStream_t st)
     };
     return s.chunks <= 8 ? sum(std::integral_constant<int, 4>{}) : sum(std::integral_constant<int, 32>{});
 }
+
+// The same with x and pre in 8 bits (thin_grad8.cu).
+dlrm_status run8(dlrm_dtype dt, const Grad& a, float* ws, cudaStream_t st);
 
 }  // namespace thin
 }  // namespace dlrm
