@@ -25,7 +25,7 @@
 // Nothing here depends on which columns a lane has.  On the 16-byte grid they are 16-byte words.
 // Off it a warp copies the aligned 16-byte words that hold its 256 columns and a lane has every
 // 32nd column, or pair of them, which shared memory gives without conflicts; the instructions for that
-// bound it (40000 x 771 bf16, centred: 140 and 191 us, 0.33 and 0.39).
+// bound it (40000 x 771 bf16, centred, a gate value a row: 121 and 186 us, 0.31 and 0.30).
 #pragma once
 
 #include "block_norm.h"
@@ -77,12 +77,22 @@ struct Cursor {
     __device__ __forceinline__ void next() { row += inc; }
 };
 
-// The rows to come: kAhead rows of NT tensors, three where the blocks that share an SM (two of
-// 256 threads, one of more) have the memory.  Columns past the row's end are 0.
-template <int STAGE, int THREADS>
-constexpr int kRowsThatFit = (THREADS > 256 ? 224 << 10 : 110 << 10) / STAGE;
-template <int STAGE, int THREADS>
-constexpr int kRowsAhead = kRowsThatFit<STAGE, THREADS> < 3 ? kRowsThatFit<STAGE, THREADS> : 3;
+// A block's warps in groups of W, WARPS an SM at most: a row each, or several where a few lanes take one.
+template <int W, int WARPS, int LAY>
+struct Group {
+    static constexpr int kGroups = norm_groups(W, WARPS), kWarps = kGroups * W, kThreads = kWarps * 32,
+                         kPerSM = norm_per_sm(W, WARPS);
+    static constexpr int kEach = kWarp / kRowLanes<LAY>, kRows = kGroups * kEach;
+    // the places of a row's sums in shared memory, and an area's floats
+    static constexpr int kPitch = W == 2 ? 2 : (W + 3) / 4 * 4, kArea = kGroups * 2 * kPitch;
+};
+
+// The rows to come: kAhead rows of NT tensors, three where the blocks that share an SM have the memory.
+// Columns past the row's end are 0.
+template <int STAGE, typename G>
+constexpr int kRowsThatFit = (224 << 10) / G::kPerSM / STAGE;
+template <int STAGE, typename G>
+constexpr int kRowsAhead = kRowsThatFit<STAGE, G> < 3 ? kRowsThatFit<STAGE, G> : 3;
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, uint32_t bytes)   // the rest of the word becomes 0
 {
@@ -90,10 +100,11 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, uint32_t b
 }
 
 // On the grid: each thread copies and reads its own eight columns.
-template <typename T, int LAY, int NT, int THREADS>
+template <typename T, int LAY, int NT, typename G>
 struct Ring {
+    static constexpr int THREADS = G::kThreads;
     static constexpr int kWords = sizeof(T) / 2, kSlot = kWords * THREADS * 16, kStage = NT * kSlot;
-    static constexpr int kAhead = kRowsAhead<kStage, THREADS>;
+    static constexpr int kAhead = kRowsAhead<kStage, G>;
     static_assert(kAhead >= 1, "a row fits");
     static constexpr size_t kBytes = (size_t)kAhead * kStage;
     uint8_t* mine;    // word 0 of slot 0 of stage 0
@@ -136,10 +147,11 @@ struct Ring {
 // Off the grid: a warp's 256 columns lie in 16 ES + 1 aligned words at most, which its lanes copy.
 // Near the matrix's ends the last word is cut there, and one that begins before the matrix is put
 // together from its elements.
-template <typename T, int NT, int THREADS>
-struct Ring<T, kAny, NT, THREADS> {
+template <typename T, int NT, typename G>
+struct Ring<T, kAny, NT, G> {
+    static constexpr int THREADS = G::kThreads;
     static constexpr int kES = sizeof(T), kWords = 16 * kES + 1, kSlot = THREADS / kWarp * kWords * 16, kStage = NT * kSlot;
-    static constexpr int kAhead = kRowsAhead<kStage, THREADS>;
+    static constexpr int kAhead = kRowsAhead<kStage, G>;
     static_assert(kAhead >= 1, "a row fits");
     static constexpr size_t kBytes = (size_t)kAhead * kStage;
     uint8_t* mine;    // the warp's word 0
@@ -198,10 +210,10 @@ struct Ring<T, kAny, NT, THREADS> {
 };
 
 // A few lanes a row: its columns straight to registers, all tensors' loads in flight together.
-template <typename T, int LAY, int NT, int THREADS>
+template <typename T, int LAY, int NT, typename G>
 struct Few {
     static constexpr int kAhead = 1;
-    static constexpr size_t kBytes = THREADS * 32;   // the backward adds up its blocks' sums there
+    static constexpr size_t kBytes = G::kThreads * 32;   // the backward adds up its blocks' sums there
     int N, first;
     Raw8<T> v[NT];
     __device__ Few(uint8_t*, int n, int f, int) : N(n), first(f) {}
@@ -235,8 +247,8 @@ struct Few {
     }
 };
 
-template <typename T, int LAY, int NT, int THREADS>
-using Rows = std::conditional_t<(LAY < 0), Few<T, LAY, NT, THREADS>, Ring<T, LAY < 0 ? kGrid : LAY, NT, THREADS>>;
+template <typename T, int LAY, int NT, typename G>
+using Rows = std::conditional_t<(LAY < 0), Few<T, LAY, NT, G>, Ring<T, LAY < 0 ? kGrid : LAY, NT, G>>;
 
 // full: all columns are in the row; of a few lanes: there is a row.
 template <typename T, int LAY>
@@ -341,7 +353,7 @@ __device__ __forceinline__ void store_vector(float* p, int first, int N, const f
 
 // Sums of V (1 or 2) values over the W warps of a row, the same in all of them.  red: two areas
 // that take turns, so that one barrier a sum is enough.
-template <int W, int LANES, int V>
+template <typename G, int W, int LANES, int V>
 __device__ __forceinline__ void row_sum(float (&v)[V], float* red, int& turn, int warp)
 {
     const int lane = threadIdx.x % kWarp;
@@ -370,25 +382,27 @@ __device__ __forceinline__ void row_sum(float (&v)[V], float* red, int& turn, in
             v[0] = s;
         }
     } else {
-        constexpr int kWarps = W > 8 ? W : 8;
-        float* area = red + turn * kWarps * 2;   // [row][2 values][warp]: rows' sums of one and two values may meet
+        constexpr int P = G::kPitch;
+        float* area = red + turn * G::kArea;   // [row][2 values][warp]: rows' sums of one and two values may meet
         turn ^= 1;
-        if (V == 2 ? lane % 16 == 0 : lane == 0) area[(warp / W * 2 + lane / 16) * W + warp % W] = s;
-        if constexpr (W >= 8) __syncthreads();
+        if (V == 2 ? lane % 16 == 0 : lane == 0) area[(warp / W * 2 + lane / 16) * P + warp % W] = s;
+        if constexpr (G::kGroups == 1) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / W), "r"(W * 32) : "memory");
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float* p = area + (warp / W * 2 + i) * W;
+            const float* p = area + (warp / W * 2 + i) * P;
             if constexpr (W == 2) {
                 const float2 q = *reinterpret_cast<const float2*>(p);
                 v[i] = q.x + q.y;
             } else {
                 v[i] = 0.f;
 #pragma unroll
-                for (int w = 0; w < W; w += 4) {
+                for (int w = 0; w < W / 4 * 4; w += 4) {
                     const float4 q = *reinterpret_cast<const float4*>(p + w);
                     v[i] += (q.x + q.y) + (q.z + q.w);
                 }
+#pragma unroll
+                for (int w = W / 4 * 4; w < W; ++w) v[i] += p[w];
             }
         }
     }
@@ -420,23 +434,19 @@ __device__ __forceinline__ void gate_both(float& g, int act, float& slope)
     slope = s * fmaf(m, 1.f - s, act == DLRM_GATE_SIGMOID ? 0.f : 1.f);
 }
 
-// Blocks of at least 256 threads, in groups of W warps: a row each, or several where a few lanes take one.
-template <int W, int LAY = kGrid>
-struct Group {
-    static constexpr int kWarps = W > 8 ? W : 8, kThreads = kWarps * 32, kGroups = kWarps / W;
-    static constexpr int kEach = kWarp / kRowLanes<LAY>, kRows = kGroups * kEach;
-};
-
 // ------------------------------------------------------------------- forward
+template <int W, int LAY>
+using FwdGroup = Group<W, fwd_warps(W, LAY == kAny), LAY>;
+
 // (mean, 1 / sqrt(mean square + eps)) of a row; f becomes what is left without the mean, 0 past the end
-template <int LAY, int ES, int W>
+template <typename G, int LAY, int ES, int W>
 __device__ __forceinline__ float2 centre(float2 (&f)[4], int first, bool full, const NormFwd& a, float* red, int& turn,
                                          int warp)
 {
     float s[1], mean = 0.f;
     if (a.layer) {
         s[0] = add_up(f);
-        row_sum<W, kRowLanes<LAY>>(s, red, turn, warp);
+        row_sum<G, W, kRowLanes<LAY>>(s, red, turn, warp);
         mean = s[0] * a.inv_n;
         if (full && LAY >= 0) {
 #pragma unroll
@@ -453,19 +463,19 @@ __device__ __forceinline__ float2 centre(float2 (&f)[4], int first, bool full, c
 #pragma unroll
     for (int i = 1; i < 4; ++i) q = __ffma2_rn(f[i], f[i], q);
     s[0] = q.x + q.y;
-    row_sum<W, kRowLanes<LAY>>(s, red, turn, warp);
+    row_sum<G, W, kRowLanes<LAY>>(s, red, turn, warp);
     return make_float2(mean, 1.f / sqrtf(fmaf(s[0], a.inv_n, a.eps)));
 }
 
 template <typename T, int LAY, int W>
-__global__ void __launch_bounds__(Group<W>::kThreads, W > 8 ? 1 : 2)
+__global__ void __launch_bounds__(FwdGroup<W, LAY>::kThreads, FwdGroup<W, LAY>::kPerSM)
 block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
 {
-    constexpr int kWarps = Group<W>::kWarps, G = Group<W, LAY>::kRows, kEach = Group<W, LAY>::kEach;
-    using R = Rows<T, LAY, 3, Group<W>::kThreads>;
+    using G = FwdGroup<W, LAY>;
+    using R = Rows<T, LAY, 3, G>;
     constexpr int kAhead = R::kAhead;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
+    __shared__ __align__(16) float red[W > 1 ? 2 * G::kArea : 1];
     // the same in all lanes, so that what depends on the row alone takes the uniform datapath
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp, N = a.N;
     const bool whole = warp % W * 256 + 256 <= N;   // all columns of the warp are in the row
@@ -474,8 +484,8 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
     int turn = 0;
     R ring(smem, N, first, warp % W * 256);
     pdl_wait();
-    const int64_t step = (int64_t)gridDim.x * G;
-    const int64_t row0 = (int64_t)blockIdx.x * G + warp / W * kEach + sub;
+    const int64_t step = (int64_t)gridDim.x * G::kRows;
+    const int64_t row0 = (int64_t)blockIdx.x * G::kRows + warp / W * G::kEach + sub;
     Cursor<T> cy(a.y, a.ldy, row0, step), cg(a.gate, a.ldg, row0, step), cres(a.res, a.ldres, row0, step),
         cr(a.r, a.ldr, row0, step), ch(a.h, a.ldh, row0, step);
     auto fetch = [&](int stage, int64_t row, int rows) {
@@ -528,7 +538,7 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) g[i] = both(g1);
             }
-            const float2 s = centre<LAY, sizeof(T), W>(f, first, full, a, red, turn, warp);
+            const float2 s = centre<G, LAY, sizeof(T), W>(f, first, full, a, red, turn, warp);
             st.x = s.x;
             st.y = s.y;
 #pragma unroll
@@ -539,7 +549,7 @@ block_norm_fwd_kernel(const __grid_constant__ NormFwd a)
             store_run<T, LAY>(cr.out(), first, N, full, r);
         }
         if (a.h) {
-            const float2 s = centre<LAY, sizeof(T), W>(r, first, full, a, red, turn, warp);
+            const float2 s = centre<G, LAY, sizeof(T), W>(r, first, full, a, red, turn, warp);
             st.z = s.x;
             st.w = s.y;
 #pragma unroll
@@ -573,9 +583,17 @@ dlrm_status with_rows(int N, bool vec, Fn&& fn)
         switch (norm_warps(N)) {
         case 1: return fn(lay, one);
         case 2: return fn(lay, integral_constant<int, 2>());
+        case 3: return fn(lay, integral_constant<int, 3>());
         case 4: return fn(lay, integral_constant<int, 4>());
+        case 5: return fn(lay, integral_constant<int, 5>());
+        case 6: return fn(lay, integral_constant<int, 6>());
+        case 7: return fn(lay, integral_constant<int, 7>());
         case 8: return fn(lay, integral_constant<int, 8>());
+        case 10: return fn(lay, integral_constant<int, 10>());
+        case 12: return fn(lay, integral_constant<int, 12>());
         case 16: return fn(lay, integral_constant<int, 16>());
+        case 20: return fn(lay, integral_constant<int, 20>());
+        case 24: return fn(lay, integral_constant<int, 24>());
         default: return fn(lay, integral_constant<int, 32>());
         }
     };
@@ -583,35 +601,39 @@ dlrm_status with_rows(int N, bool vec, Fn&& fn)
 }
 
 template <typename K, typename A>
-dlrm_status launch_norm(const char* what, K kern, const A& a, int threads, size_t smem, cudaStream_t st)
+dlrm_status launch_norm(const char* what, K kern, const A& a, int warps, int threads, size_t smem, cudaStream_t st)
 {
     const cudaError_t e =   // the first 48 KB need no leave
         smem > 46 << 10 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) : cudaSuccess;
     if (e != cudaSuccess) return fail(DLRM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    return check_launch_pdl(launch_pdl(kern, dim3(norm_blocks(a.M, a.N)), dim3(threads), smem, st, a), what);
+    return check_launch_pdl(launch_pdl(kern, dim3(norm_blocks(a.M, a.N, warps)), dim3(threads), smem, st, a), what);
 }
 
 template <typename T>
 dlrm_status launch_fwd(const NormFwd& a, bool vec, cudaStream_t st)
 {
     return with_rows(a.N, vec, [&](auto l, auto w) {
-        constexpr int LAY = decltype(l)::value, W = decltype(w)::value, kThreads = Group<W, LAY>::kThreads;
-        return launch_norm("block_norm_fwd_kernel", block_norm_fwd_kernel<T, LAY, W>, a, kThreads,
-                           Rows<T, LAY, 3, kThreads>::kBytes, st);
+        constexpr int LAY = decltype(l)::value, W = decltype(w)::value;
+        using G = FwdGroup<W, LAY>;
+        return launch_norm("block_norm_fwd_kernel", block_norm_fwd_kernel<T, LAY, W>, a, fwd_warps(W, LAY == kAny), G::kThreads,
+                           Rows<T, LAY, 3, G>::kBytes, st);
     });
 }
 
 // ------------------------------------------------------------------ backward
+template <int W, int LAY, bool POST, bool PRE>
+using BwdGroup = Group<W, bwd_warps(POST, PRE, LAY == kGrid), LAY>;
+
 template <typename T, int LAY, int W, bool POST, bool PRE>
-__global__ void __launch_bounds__(Group<W>::kThreads, W > 8 ? 1 : 2)
+__global__ void __launch_bounds__(BwdGroup<W, LAY, POST, PRE>::kThreads, BwdGroup<W, LAY, POST, PRE>::kPerSM)
 block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
 {
-    constexpr int kWarps = Group<W>::kWarps, G = Group<W, LAY>::kRows, kEach = Group<W, LAY>::kEach;
+    using G = BwdGroup<W, LAY, POST, PRE>;
     constexpr int kGr = 0, kGh = 1, kR = 2, kY = PRE ? 3 : 1, kGate = kY + 1;   // slots
-    using Rg = Rows<T, LAY, POST && PRE ? 5 : 3, Group<W>::kThreads>;
+    using Rg = Rows<T, LAY, POST && PRE ? 5 : 3, G>;
     constexpr int kAhead = Rg::kAhead;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) float red[W > 1 ? 4 * kWarps : 1];
+    __shared__ __align__(16) float red[W > 1 ? 2 * G::kArea : 1];
     // the same in all lanes, so that what depends on the row alone takes the uniform datapath
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / kWarp, 0), lane = threadIdx.x % kWarp, N = a.N;
     const bool whole = warp % W * 256 + 256 <= N;   // all columns of the warp are in the row
@@ -620,7 +642,7 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
     int turn = 0;
     Rg ring(smem, N, first, warp % W * 256);
     pdl_wait();
-    const int64_t step = (int64_t)gridDim.x * G, row0 = (int64_t)blockIdx.x * G + warp / W * kEach + sub;
+    const int64_t step = (int64_t)gridDim.x * G::kRows, row0 = (int64_t)blockIdx.x * G::kRows + warp / W * G::kEach + sub;
     Cursor<T> cgr(a.gr, a.ldgr, row0, step), cgh(a.gh, a.ldgh, row0, step), cr(a.r, a.ldr, row0, step),
         cy(a.y, a.ldy, row0, step), cg(a.gate, a.ldg, row0, step), cgy(a.gy, a.ldgy, row0, step), cgg(a.gg, a.ldgg, row0, step),
         cgres(a.gres, a.ldgres, row0, step);
@@ -690,12 +712,12 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
             float c0, c1 = 0.f;
             if (a.layer) {
                 float c[2] = {p.x + p.y, q.x + q.y};
-                row_sum<W, kRowLanes<LAY>>(c, red, turn, warp);
+                row_sum<G, W, kRowLanes<LAY>>(c, red, turn, warp);
                 c0 = c[0] * -a.inv_n;
                 c1 = c[1] * -a.inv_n;
             } else {
                 float c[1] = {p.x + p.y};
-                row_sum<W, kRowLanes<LAY>>(c, red, turn, warp);
+                row_sum<G, W, kRowLanes<LAY>>(c, red, turn, warp);
                 c0 = c[0] * -a.inv_n;
             }
 #pragma unroll
@@ -742,17 +764,17 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
             float c0, c1 = 0.f;
             if (a.layer) {
                 float c[2] = {p.x + p.y, q.x + q.y};
-                row_sum<W, kRowLanes<LAY>>(c, red, turn, warp);
+                row_sum<G, W, kRowLanes<LAY>>(c, red, turn, warp);
                 c0 = c[0] * -a.inv_n;
                 c1 = c[1] * -a.inv_n;
             } else {
                 float c[1] = {p.x + p.y};
-                row_sum<W, kRowLanes<LAY>>(c, red, turn, warp);
+                row_sum<G, W, kRowLanes<LAY>>(c, red, turn, warp);
                 c0 = c[0] * -a.inv_n;
             }
             if (a.gg && a.gate_cols == 1) {
                 float c[1] = {t.x + t.y};
-                row_sum<W, kRowLanes<LAY>>(c, red, turn, warp);
+                row_sum<G, W, kRowLanes<LAY>>(c, red, turn, warp);
                 if (here && warp % W == 0 && lane % kRowLanes<LAY> == 0) *cgg.out() = from_f32<T>(c[0] * slope1);
             }
             if (a.gy) {
@@ -777,7 +799,8 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
     // the rows' sums of a block: its groups one after another, by way of the ring's memory
     float2* const tile = reinterpret_cast<float2*>(smem);
     asm volatile("cp.async.wait_all;" ::: "memory");
-    constexpr int kGroups = Group<W>::kGroups;
+    constexpr int kGroups = G::kGroups, kThreads = G::kThreads;
+    static_assert(Rg::kBytes >= kThreads * 32, "a tile fits");
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         if (s < 2 ? !POST : !PRE) continue;
@@ -791,13 +814,13 @@ block_norm_bwd_kernel(const __grid_constant__ NormBwd a)
         if constexpr (kGroups > 1) {
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tile[i * 256 + threadIdx.x] = sum[s][i];
+            for (int i = 0; i < 4; ++i) tile[i * kThreads + threadIdx.x] = sum[s][i];
             __syncthreads();
             if (warp < W) {
 #pragma unroll
                 for (int g = 1; g < kGroups; ++g)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sum[s][i] = __fadd2_rn(sum[s][i], tile[i * 256 + g * W * 32 + threadIdx.x]);
+                    for (int i = 0; i < 4; ++i) sum[s][i] = __fadd2_rn(sum[s][i], tile[i * kThreads + g * W * 32 + threadIdx.x]);
             }
         }
         if (warp < W && lane < kRowLanes<LAY>)
@@ -809,9 +832,10 @@ template <typename T, bool POST, bool PRE>
 dlrm_status launch_bwd(const NormBwd& a, bool vec, cudaStream_t st)
 {
     return with_rows(a.N, vec, [&](auto l, auto w) {
-        constexpr int LAY = decltype(l)::value, W = decltype(w)::value, kThreads = Group<W, LAY>::kThreads;
-        return launch_norm("block_norm_bwd_kernel", block_norm_bwd_kernel<T, LAY, W, POST, PRE>, a, kThreads,
-                           Rows<T, LAY, POST && PRE ? 5 : 3, kThreads>::kBytes, st);
+        constexpr int LAY = decltype(l)::value, W = decltype(w)::value, kWarps = bwd_warps(POST, PRE, LAY == kGrid);
+        using G = BwdGroup<W, LAY, POST, PRE>;
+        return launch_norm("block_norm_bwd_kernel", block_norm_bwd_kernel<T, LAY, W, POST, PRE>, a, kWarps, G::kThreads,
+                           Rows<T, LAY, POST && PRE ? 5 : 3, G>::kBytes, st);
     });
 }
 

@@ -39,17 +39,34 @@ struct NormBwd {
 // gradient 17 / 41, 24 / 41, 37 / 42, 52 / 74.
 inline int norm_lanes(int N) { return N <= 32 ? 4 : N <= 64 ? 8 : N <= 128 ? 16 : 32; }
 
+// Warps of a row, 256 columns each: every number to 8, then in steps that leave a fifth idle at most up to 24.  (Powers of two
+// only, us: 40000 x 1280 fp16 forward 135, so 98 and gradient 209, 143; 10000 x 4500 bf16 gradient 522, 297.)
 inline int norm_warps(int N)
 {
-    int w = 1;
-    while (w * 256 < N) w *= 2;
-    return w;
+    const int w = (N + 255) / 256;
+    return w <= 8 ? w : w <= 12 ? (w + 1) / 2 * 2 : w <= 24 ? (w + 3) / 4 * 4 : 32;
 }
 
-inline int norm_blocks(int M, int N)
+// Blocks of an SM and rows of a block where W warps take a row: blocks of eight warps, or of one group where W is more,
+// or one block of as many groups as fit where eight are no whole number of groups.
+constexpr bool norm_eights(int W) { return W <= 8 && 8 % W == 0; }
+constexpr int norm_per_sm(int W, int warps) { return norm_eights(W) ? warps / 8 : W > 8 && warps >= 2 * W ? warps / W : 1; }
+constexpr int norm_groups(int W, int warps) { return W > 8 ? 1 : norm_eights(W) ? 8 / W : warps / W; }
+
+// Warps an SM at most.  More hide more of a row's chain of sums, at fewer registers each.  Measured, us, 16 / 24 warps:
+// forward 22924 x 2272 fp16 201 / 141, 40000 x 1536 bf16 125 / 107; in blocks of eight warps on the grid 65536 x 1024 bf16
+// 111 / 117, off it (any) 40000 x 771 bf16 141 / 123, 40000 x 201 37 / 41.  Gradient on the grid of the norm before the
+// next block alone 16000 x 2904 bf16 145 / 90, 65536 x 1024 117 / 98; of that after the block 22924 x 2272 149 / 121 and
+// the same with 20; of both 219 / 244; off the grid 30000 x 1700 109 / 115, a few lanes a row 12 / 14.
+constexpr int fwd_warps(int W, bool any) { return norm_eights(W) && (W == 1 || !any) ? 16 : 24; }
+constexpr int bwd_warps(bool post, bool pre, bool grid) { return !grid || (post && pre) ? 16 : pre ? 24 : 20; }
+
+inline bool on_grid(bool vec, int N) { return vec && norm_lanes(N) == kWarp; }
+
+inline int norm_blocks(int M, int N, int warps)
 {
-    const int w = norm_warps(N), rows = w > 8 ? 1 : 8 / w * (kWarp / norm_lanes(N));
-    const int64_t want = ((int64_t)M + rows - 1) / rows, most = (int64_t)num_sms() * (w > 8 ? 1 : 2);
+    const int w = norm_warps(N), rows = norm_groups(w, warps) * (kWarp / norm_lanes(N));
+    const int64_t want = ((int64_t)M + rows - 1) / rows, most = (int64_t)num_sms() * norm_per_sm(w, warps);
     return (int)(want < most ? want : most);
 }
 

@@ -45,7 +45,9 @@ def _d(t):
 SHAPES = [(1, 1, 0, 0), (1, 8, 0, 0), (3, 7, 0, 0), (2, 33, 3, 1), (5, 256, 0, 0), (2, 257, 0, 0), (37, 480, 8, 0),
           (300, 1024, 0, 0), (3, 1032, 8, 0), (9, 2048, 0, 1), (2, 2500, 0, 0), (4, 4100, 0, 0), (3, 8192, 0, 0),
           (2, 8191, 0, 0), (2600, 96, 0, 0), (700, 515, 0, 0), (5000, 16, 0, 0), (333, 32, 8, 0), (77, 64, 0, 1),
-          (65, 128, 8, 0), (513, 128, 0, 0), (19, 200, 0, 0), (9, 1999, 1, 0)]
+          (65, 128, 8, 0), (513, 128, 0, 0), (19, 200, 0, 0), (9, 1999, 1, 0),
+          (2000, 700, 0, 0), (1300, 1200, 8, 0), (900, 1501, 0, 0), (700, 1720, 0, 1), (600, 2304, 0, 0), (500, 2903, 0, 0),
+          (400, 4800, 0, 0), (333, 6001, 0, 0)]
 OPTIONS = [   # layer, gate, per row, block, next norm, vectors, residual
     (False, None, False, True, True, False, True), (False, "silu", False, True, True, True, True),
     (True, "sigmoid", True, True, True, True, True), (True, "raw", False, True, False, True, False),
@@ -146,7 +148,7 @@ def test_norm_backward(cuda_lib, dtype, option, M, N, pad, lead, paths):
         assert torch.equal(alone[k], out[k]), k
 
 
-@pytest.mark.parametrize("N", [300, 515, 1024])
+@pytest.mark.parametrize("N", [300, 515, 700, 1024, 1200, 1500, 1720])
 def test_norm_backward_of_rows_that_share_a_block(cuda_lib, N):
     """Rows of one block go their own pace, with sums of one value and of two: every row right, every run the same."""
     M, option = 6000, OPTIONS[2]
