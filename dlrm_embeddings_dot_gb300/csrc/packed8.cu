@@ -271,13 +271,27 @@ unpack8_kernel(const __grid_constant__ Packed8 m, int M, int N, T* __restrict__ 
     }
 }
 
-// Off the grid: rows by warps (row_units.cuh), every 32nd column a lane or pair of them.
-template <typename T>
+// Off the grid: rows by warps (row_units.cuh), every 32nd column a lane or pair of them; FEW: by a few lanes
+// (to 8 bits and back, us, a warp a row / so: 56414 x 44 bf16 25 / 16, 65536 x 7 fp16 25 / 10).
+template <typename T, bool FEW>
 __global__ void __launch_bounds__(kThreads8)
-unpack8_any_kernel(const __grid_constant__ Packed8 m, int M, int N, T* __restrict__ y, int64_t ldy)
+unpack8_any_kernel(const __grid_constant__ Packed8 m, int M, int N, int lanes, T* __restrict__ y, int64_t ldy)
 {
     pdl_wait();
-    const Unit unit(kWarp);
+    const Unit unit(FEW ? lanes : kWarp);
+    if constexpr (FEW) {
+        for (int64_t row = unit.unit; row < M; row += unit.units) {
+            const uint8_t *q = m.q + row * m.ld, *e = m.exps + row * m.blocks;
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = min(unit.l + i * lanes, N - 1);
+                f[i] = value8<T>(__ldg(q + c), __ldg(e + c / kBlock8));
+            }
+            store_cols<T, kFewLanes>(y + row * ldy, unit.l, N, lanes, f);
+        }
+        return;
+    }
     const int lane = threadIdx.x % kWarp;
     for (Items it(unit, N, 1); it.row < M; it.next()) {
         const int c = unit.first<kOffGrid, sizeof(T)>((int)it.part);
@@ -381,11 +395,16 @@ extern "C" dlrm_status dlrm_unpack8(const uint8_t* d_q, int64_t ldq, const uint8
     const Packed8 m = packed8(d_q, ldq, d_exps, M, N);
     return with_type(dtype, [&](auto t) {
         using T = decltype(t);
-        auto kern = vec ? unpack8_kernel<T> : unpack8_any_kernel<T>;
-        const void* const k = (const void*)kern;
-        const unsigned blocks = vec ? word_blocks((int64_t)M * N * (int)sizeof(T) / 16, kWords8, k)
-                                    : item_blocks(M, N, kWarp, 1, k);
-        return check_launch_pdl(launch_pdl(kern, dim3(blocks), dim3(kThreads8), 0, as_stream(stream), m, M, N, (T*)d_y, ldy),
-                                "unpack8_kernel");
+        if (vec) {
+            auto kern = unpack8_kernel<T>;
+            const unsigned blocks = word_blocks((int64_t)M * N * (int)sizeof(T) / 16, kWords8, (const void*)kern);
+            return check_launch_pdl(launch_pdl(kern, dim3(blocks), dim3(kThreads8), 0, as_stream(stream), m, M, N, (T*)d_y, ldy),
+                                    "unpack8_kernel");
+        }
+        const int lay = row_layout(false, N), lanes = unit_lanes(N, lay);
+        auto kern = lay == kFewLanes ? unpack8_any_kernel<T, true> : unpack8_any_kernel<T, false>;
+        return check_launch_pdl(launch_pdl(kern, dim3(item_blocks(M, N, lanes, 1, (const void*)kern)), dim3(kThreads8), 0,
+                                           as_stream(stream), m, M, N, lanes, (T*)d_y, ldy),
+                                "unpack8_any_kernel");
     });
 }
