@@ -147,10 +147,10 @@ extern "C" dlrm_status dlrm_block_norm_fwd(const void* d_y, int64_t ldy, const v
 extern "C" size_t dlrm_block_norm_bwd_workspace_size(int M, int N)
 {
     if (M < 1 || N < 1 || M > kMaxSize || N > DLRM_BLOCK_MAX_WIDTH) return 0;
-    int most = 0;   // whichever norms are asked for, on the grid or off it
-    for (const int warps : {norms::bwd_warps(true, true, true), norms::bwd_warps(false, true, true),
-                            norms::bwd_warps(true, false, true), norms::bwd_warps(true, true, false)})
-        most = std::max(most, norm_blocks(M, N, warps));
+    int most = norm_blocks(M, N, norms::bwd_warps(true, true, true));
+    if (norms::on_grid(N % 8 == 0, N))   // the rows may be: whichever norms are asked for, on the grid or off it
+        for (const bool post : {false, true})
+            most = std::max(most, norm_blocks(M, N, norms::bwd_warps(post, !post, true)));
     return dlrm_ws_align((size_t)most * 4 * ((N + 7) / 8 * 8) * 4);
 }
 
@@ -226,7 +226,8 @@ extern "C" dlrm_status dlrm_block_norm_bwd(
         return norms::backward<T>(a, vec, st);
     });
     if (s != DLRM_OK || !sums) return s;
-    const NormSum q = {a.partial, Np, norm_blocks(M, N, norms::bwd_warps(d_y, d_grad_h, norms::on_grid(vec, N))), N, d_w_post, d_b_post, d_scale,
+    const int blocks = norm_blocks(M, N, norms::bwd_warps(d_y, d_grad_h, norms::on_grid(vec, N)));
+    const NormSum q = {a.partial, Np, blocks, N, d_w_post, d_b_post, d_scale,
                        d_grad_w_post, d_grad_b_post, d_grad_scale, d_grad_w_pre, d_grad_b_pre};
     const int cols = N > 1024 ? 32 : 8;
     return check_launch_pdl(launch_pdl(cols == 32 ? block_norm_sum_kernel<32> : block_norm_sum_kernel<8>,
