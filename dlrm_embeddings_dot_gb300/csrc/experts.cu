@@ -3,6 +3,7 @@
 // experts and back.  Each is bound by memory, or by latency where there are few tokens.
 #include "dlrm_block.h"
 #include "row_units.cuh"
+#include "sort_layout.h"
 
 namespace dlrm {
 namespace {
@@ -196,28 +197,11 @@ dlrm_status with_lanes(int E, Fn&& fn)
 // expert count as expert E.  With one block that is all; with more, expert_count_kernel writes
 // the chunks' counts first, and a block adds up those of the blocks before it (and all of
 // them: where an expert begins).  The steps are chains of latencies: a warp's choices are
-// loaded kBatch rounds at a time, and the counts' sums are shared out over all threads.
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / kWarp;
-constexpr int kSortChunk = 2048;        // choices of a block, while there are no more than kSortBlocks blocks
-constexpr int kSortOne = 4096;          // so many choices are one block's
-constexpr int kSortBlocks = 128;    // each of which reads all counts
+// loaded kBatch rounds at a time, and the counts' sums are shared out over all threads
+// (sort_layout.h).
 constexpr int kBatch = 8;
 constexpr int kBins = DLRM_ROUTE_MAX_EXPERTS + 1;
 static_assert(kBins <= kSortThreads, "a thread for each bin");
-
-struct SortShape {
-    int blocks;
-    int64_t chunk;
-};
-
-inline SortShape sort_shape(int64_t n)
-{
-    if (n <= kSortOne) return {1, (n + kSortThreads - 1) / kSortThreads * kSortThreads};
-    int64_t chunk = kSortChunk;
-    if ((n + chunk - 1) / chunk > kSortBlocks)
-        chunk = ((n + kSortBlocks - 1) / kSortBlocks + kSortThreads - 1) / kSortThreads * kSortThreads;
-    return {(int)((n + chunk - 1) / chunk), chunk};
-}
 
 // A warp's part [from, to) of the choices, the first kBatch rounds of it in registers.
 struct Part {
@@ -305,21 +289,17 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
     count_parts(part, E, warps);
     if (gridDim.x > 1) {
         pdl_wait();
-        // a thread has one bin of every (kSortThreads / bins)-th block
-        const int parts = kSortThreads / bins, e = tid % bins, p = tid / bins;
-        if (p < parts) {
+        const CountShare share = count_share(tid, bins, (int)gridDim.x, (int)blockIdx.x);
+        if (share.rows > 0) {
             int all = 0, ahead = 0;
-            // a block begins with its own row, so that they do not all ask for the same one
-            const int rows = ((int)gridDim.x - p + parts - 1) / parts, from = (int)(blockIdx.x % rows);
 #pragma unroll 8
-            for (int i = 0; i < rows; ++i) {
-                const int b = p + (i + from < rows ? i + from : i + from - rows) * parts;
-                const int v = __ldcg(counts + b * bins + e);
+            for (int i = 0; i < share.rows; ++i) {
+                const int b = share.block(i), v = __ldcg(counts + b * bins + share.bin);
                 all += v;
                 ahead += b < (int)blockIdx.x ? v : 0;
             }
-            atomicAdd(&total[e], all);      // whole numbers: the same in any order
-            atomicAdd(&before[e], ahead);
+            atomicAdd(&total[share.bin], all);      // whole numbers: the same in any order
+            atomicAdd(&before[share.bin], ahead);
         }
         __syncthreads();
     }
