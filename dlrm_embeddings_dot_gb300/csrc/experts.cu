@@ -195,10 +195,13 @@ dlrm_status with_lanes(int E, Fn&& fn)
 // its warps contiguous parts of it; a warp counts and places 32 choices at a time, those of
 // one expert found by match.any, in counters of its own in shared memory.  Choices without
 // expert count as expert E.  With one block that is all; with more, expert_count_kernel writes
-// the chunks' counts first, and a block adds up those of the blocks before it (and all of
-// them: where an expert begins).  The steps are chains of latencies: a warp's choices are
+// the chunks' counts and their warps' first, and a block of expert_place_kernel adds up those of the
+// blocks before it (and all of them: where an expert begins).  Both wait for what is before them on the stream
+// before they read a choice.  The steps are chains of latencies: a warp's choices are
 // loaded kBatch rounds at a time, and the counts' sums are shared out over all threads
-// (sort_layout.h).
+// (sort_layout.h).  (us in a graph; the warps counted a second time while the counts were written / counts
+// read back: 9000 choices of 16 4.7 / 5.6, 65536 x 4 of 64 8.9 / 9.4, 65536 x 8 of 256 19.8 / 19.0, 300000 x 8 of 33
+// 41.9 / 31.9.  The former read choices ahead of its own wait.)
 constexpr int kBatch = 8;
 constexpr int kBins = DLRM_ROUTE_MAX_EXPERTS + 1;
 static_assert(kBins <= kSortThreads, "a thread for each bin");
@@ -261,12 +264,15 @@ __device__ __forceinline__ void count_parts(const Part& part, int E, int (*warps
 }
 
 __global__ void __launch_bounds__(kSortThreads)
-expert_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int E, int32_t* __restrict__ counts)
+expert_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int E, int32_t* __restrict__ counts,
+                    int32_t* __restrict__ parts)
 {
-    pdl_begin({0, 1});   // the places' kernel counts its choices meanwhile
+    pdl_wait();
     __shared__ int warps[kSortWarps][kBins];
     const Part part(ids, n, chunk);
     count_parts(part, E, warps);
+    int32_t* own = parts + ((int)blockIdx.x * kSortWarps + (int)threadIdx.x / kWarp) * (E + 1);
+    for (int e = threadIdx.x % kWarp; e <= E; e += kWarp) own[e] = warps[threadIdx.x / kWarp][e];
     for (int e = threadIdx.x; e <= E; e += kSortThreads) {
         int s = 0;
 #pragma unroll
@@ -277,18 +283,23 @@ expert_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
 
 __global__ void __launch_bounds__(kSortThreads)
 expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int E, const int32_t* __restrict__ counts,
-                    int32_t* __restrict__ offsets, int32_t* __restrict__ slots, int32_t* __restrict__ order,
-                    uint32_t* __restrict__ status)
+                    const int32_t* __restrict__ parts, int32_t* __restrict__ offsets, int32_t* __restrict__ slots,
+                    int32_t* __restrict__ order, uint32_t* __restrict__ status)
 {
     __shared__ int warps[kSortWarps][kBins];
     __shared__ int total[kBins], before[kBins], scan[kSortWarps];
     const int bins = E + 1, tid = threadIdx.x;
-    if (gridDim.x == 1) pdl_wait();   // else the counts' kernel has waited for the choices
+    pdl_wait();
     const Part part(ids, n, chunk);
-    for (int e = tid; e < bins; e += kSortThreads) total[e] = before[e] = 0;
-    count_parts(part, E, warps);
-    if (gridDim.x > 1) {
-        pdl_wait();
+    if (gridDim.x == 1) {
+        count_parts(part, E, warps);
+    } else {
+        const int w = tid / kWarp;
+        const int32_t* own = parts + ((int)blockIdx.x * kSortWarps + w) * bins;
+#pragma unroll 4
+        for (int e = tid % kWarp; e < bins; e += kWarp) warps[w][e] = __ldcg(own + e);
+        for (int e = tid; e < bins; e += kSortThreads) total[e] = before[e] = 0;
+        __syncthreads();
         const CountShare share = count_share(tid, bins, (int)gridDim.x, (int)blockIdx.x);
         if (share.rows > 0) {
             int all = 0, ahead = 0;
@@ -709,7 +720,7 @@ extern "C" size_t dlrm_expert_sort_workspace_size(int T, int k, int E)
 {
     if (!sort_sizes_ok(T, k, E)) return 0;
     const SortShape z = sort_shape((int64_t)T * k);
-    return z.blocks > 1 ? dlrm_ws_align((size_t)z.blocks * (E + 1) * 4) : 0;
+    return z.blocks > 1 ? dlrm_ws_align((size_t)z.blocks * (1 + kSortWarps) * (E + 1) * 4) : 0;
 }
 
 extern "C" dlrm_status dlrm_expert_sort(const int32_t* d_ids, int T, int k, int E, int32_t* d_offsets, int32_t* d_slots,
@@ -736,15 +747,15 @@ extern "C" dlrm_status dlrm_expert_sort(const int32_t* d_ids, int T, int k, int 
     const int64_t n = (int64_t)T * k;
     const SortShape z = sort_shape(n);
     const cudaStream_t st = as_stream(stream);
-    int32_t* counts = (int32_t*)d_workspace;
+    int32_t *const counts = (int32_t*)d_workspace, *const parts = counts + (z.blocks > 1 ? z.blocks * (E + 1) : 0);
     if (z.blocks > 1) {
         s = check_launch_pdl(launch_pdl(expert_count_kernel, dim3(z.blocks), dim3(kSortThreads), 0, st, d_ids, n, z.chunk, E,
-                                        counts),
+                                        counts, parts),
                              "expert_count_kernel");
         if (s != DLRM_OK) return s;
     }
     return check_launch_pdl(launch_pdl(expert_place_kernel, dim3(z.blocks), dim3(kSortThreads), 0, st, d_ids, n, z.chunk, E,
-                                       (const int32_t*)counts, d_offsets, d_slots, d_order, d_status),
+                                       (const int32_t*)counts, (const int32_t*)parts, d_offsets, d_slots, d_order, d_status),
                             "expert_place_kernel");
 }
 
