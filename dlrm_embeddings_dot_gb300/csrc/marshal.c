@@ -376,6 +376,14 @@ static struct {
 } block;
 #define N_BLOCK 12
 
+/* The count of arguments, and that bind_block has been called: a library of before these entry points has none. */
+static int ready(Py_ssize_t got, Py_ssize_t want)
+{
+    if (types[U8]) return count(got, want);
+    PyErr_SetString(PyExc_RuntimeError, "the library was built before the residual blocks' entry points: build it again");
+    return 0;
+}
+
 /* The first of n arguments that is a tensor; NULL with an exception set where none is. */
 static PyObject* some(PyObject* const* t, int n, const char* names)
 {
@@ -426,7 +434,7 @@ static PyObject* block_norm_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n
     int c, norm, act;
     static const char* const names[] = {"y",     "gate",  "residual", "w_post", "b_post", "scale",
                                         "w_pre", "b_pre", "r",        "h",      "stats"};
-    if (!count(n, 15)) return NULL;
+    if (!ready(n, 15)) return NULL;
     PyObject *x = a[0] != Py_None ? a[0] : a[2], *t;
     if (!given(x, "residual") || (c = type_code(x)) < 0 || !sizes(x, x == a[0] ? "y" : "residual", 2, mn)) return NULL;
     t = types[c];
@@ -458,7 +466,7 @@ static PyObject* block_norm_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n
                                         "grad_y",      "grad_gate",  "grad_residual", "grad_w_post", "grad_b_post",
                                         "grad_scale",  "grad_w_pre", "grad_b_pre", NULL,        NULL,
                                         "workspace"};
-    if (!count(n, 22)) return NULL;
+    if (!ready(n, 22)) return NULL;
     PyObject* x = some(a, 2, "grad_r and grad_h");
     if (!x || (c = type_code(x)) < 0 || !sizes(x, x == a[0] ? "grad_r" : "grad_h", 2, mn)) return NULL;
     PyObject* t = types[c];
@@ -491,7 +499,7 @@ static PyObject* route_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *l, *ids, *probs, *st;
     int c;
     static const char* const names[] = {"logits", "ids", "probs"};
-    if (!count(n, 4) || (c = type_code(a[0])) < 0 || !sizes(a[0], "logits", 2, te) || !sizes(a[1], "ids", 2, tk)) return NULL;
+    if (!ready(n, 4) || (c = type_code(a[0])) < 0 || !sizes(a[0], "logits", 2, te) || !sizes(a[1], "ids", 2, tk)) return NULL;
     const int64_t choice[2] = {te[0], tk[1]};
     if (!matrix(a[0], "logits", types[c], te[0], te[1], &l, &ldl) || !argument(a[1], "ids", types[I32], 2, choice, &ids, NULL) ||
         !argument(a[2], "probs", types[F32], 2, choice, &probs, NULL) || !where(a, names, 3, a[3], &st))
@@ -506,7 +514,7 @@ static PyObject* route_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *gp, *ids, *probs, *l, *st;
     int c;
     static const char* const names[] = {"grad_probs", "ids", "probs", "grad_logits"};
-    if (!count(n, 5) || (c = type_code(a[3])) < 0 || !sizes(a[3], "grad_logits", 2, te) || !sizes(a[1], "ids", 2, tk))
+    if (!ready(n, 5) || (c = type_code(a[3])) < 0 || !sizes(a[3], "grad_logits", 2, te) || !sizes(a[1], "ids", 2, tk))
         return NULL;
     const int64_t choice[2] = {te[0], tk[1]};
     if (!argument(a[0], "grad_probs", types[F32], 2, choice, &gp, NULL) ||
@@ -525,7 +533,7 @@ static PyObject* expert_sort(PyObject* self, PyObject* const* a, Py_ssize_t n)
     size_t bytes;
     int E;
     static const char* const names[] = {"ids", NULL, "offsets", "slots", "order", "workspace", "status"};
-    if (!count(n, 8) || !sizes(a[0], "ids", 2, tk) || !code(a[1], "E", &E)) return NULL;
+    if (!ready(n, 8) || !sizes(a[0], "ids", 2, tk) || !code(a[1], "E", &E)) return NULL;
     if (!argument(a[0], "ids", types[I32], 2, tk, &ids, NULL) || !vector(a[2], "offsets", types[I32], (int64_t)E + 1, &offsets) ||
         !argument(a[3], "slots", types[I32], 2, tk, &slots, NULL) ||
         !vector(a[4], "order", types[I32], tk[0] * tk[1], &order) || !workspace(a[5], &ws, &bytes) ||
@@ -541,7 +549,7 @@ static PyObject* dispatch_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *x, *slots, *xs, *status, *st;
     int c;
     static const char* const names[] = {"x", "slots", "xs", "status"};
-    if (!count(n, 5) || (c = type_code(a[0])) < 0 || !sizes(a[0], "x", 2, th) || !sizes(a[1], "slots", 2, tk) ||
+    if (!ready(n, 5) || (c = type_code(a[0])) < 0 || !sizes(a[0], "x", 2, th) || !sizes(a[1], "slots", 2, tk) ||
         !sizes(a[2], "xs", 2, rh))
         return NULL;
     const int64_t choice[2] = {th[0], tk[1]};
@@ -559,7 +567,7 @@ static PyObject* dispatch_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *x, *slots, *xs, *status, *st;
     int c;
     static const char* const names[] = {"grad_xs", "slots", "grad_x", "status"};
-    if (!count(n, 5) || (c = type_code(a[2])) < 0 || !sizes(a[2], "grad_x", 2, th) || !sizes(a[1], "slots", 2, tk) ||
+    if (!ready(n, 5) || (c = type_code(a[2])) < 0 || !sizes(a[2], "grad_x", 2, th) || !sizes(a[1], "slots", 2, tk) ||
         !sizes(a[0], "grad_xs", 2, rh))
         return NULL;
     const int64_t choice[2] = {th[0], tk[1]};
@@ -579,7 +587,7 @@ static PyObject* combine_fwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *ys, *slots, *probs, *r, *y, *status, *st;
     int c;
     static const char* const names[] = {"ys", "slots", "probs", "residual", "y", "status"};
-    if (!count(n, 7) || (c = type_code(a[4])) < 0 || !sizes(a[4], "y", 2, th) || !sizes(a[1], "slots", 2, tk) ||
+    if (!ready(n, 7) || (c = type_code(a[4])) < 0 || !sizes(a[4], "y", 2, th) || !sizes(a[1], "slots", 2, tk) ||
         !sizes(a[0], "ys", 2, rh))
         return NULL;
     const int64_t choice[2] = {th[0], tk[1]};
@@ -600,7 +608,7 @@ static PyObject* combine_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *gy, *ys, *slots, *probs, *gys, *gp, *status, *st;
     int c;
     static const char* const names[] = {"grad_y", "ys", "slots", "probs", "grad_ys", "grad_probs", "status"};
-    if (!count(n, 8) || (c = type_code(a[0])) < 0 || !sizes(a[0], "grad_y", 2, th) || !sizes(a[2], "slots", 2, tk)) return NULL;
+    if (!ready(n, 8) || (c = type_code(a[0])) < 0 || !sizes(a[0], "grad_y", 2, th) || !sizes(a[2], "slots", 2, tk)) return NULL;
     PyObject* const rows[2] = {a[1], a[4]};
     PyObject* any = some(rows, 2, "ys and grad_ys");
     if (!any || !sizes(any, any == a[1] ? "ys" : "grad_ys", 2, rh)) return NULL;
@@ -631,7 +639,7 @@ static PyObject* pack8(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *x, *q, *e, *st;
     int c;
     static const char* const names[] = {"x", "q", "exps"};
-    if (!count(n, 4) || (c = type_code(a[0])) < 0 || !sizes(a[0], "x", 2, mn) ||
+    if (!ready(n, 4) || (c = type_code(a[0])) < 0 || !sizes(a[0], "x", 2, mn) ||
         !matrix(a[0], "x", types[c], mn[0], mn[1], &x, &ldx) || !packed(a[1], a[2], "q", "exps", mn[0], mn[1], &q, &ldq, &e) ||
         !where(a, names, 3, a[3], &st))
         return NULL;
@@ -645,7 +653,7 @@ static PyObject* unpack8(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *y, *q, *e, *st;
     int c;
     static const char* const names[] = {"q", "exps", "y"};
-    if (!count(n, 4) || (c = type_code(a[2])) < 0 || !sizes(a[2], "y", 2, mn) ||
+    if (!ready(n, 4) || (c = type_code(a[2])) < 0 || !sizes(a[2], "y", 2, mn) ||
         !packed(a[0], a[1], "q", "exps", mn[0], mn[1], &q, &ldq, &e) || !matrix(a[2], "y", types[c], mn[0], mn[1], &y, &ldy) ||
         !where(a, names, 3, a[3], &st))
         return NULL;
@@ -662,7 +670,7 @@ static PyObject* linear_bwd8(PyObject* self, PyObject* const* a, Py_ssize_t n)
     int c, act;
     static const char* const names[] = {"grad_y", "x_q",    "x_exps",    "w",  "pre_q", "pre_exps", "grad_x",
                                         "grad_w", "grad_bias", NULL,     NULL, "rng",   "workspace", "status"};
-    if (!count(n, 15) || (c = type_code(a[0])) < 0 || !sizes(a[0], "grad_y", 2, mn) || !sizes(a[3], "w", 2, nk)) return NULL;
+    if (!ready(n, 15) || (c = type_code(a[0])) < 0 || !sizes(a[0], "grad_y", 2, mn) || !sizes(a[3], "w", 2, nk)) return NULL;
     PyObject* t = types[c];
     const int64_t M = mn[0], N = nk[0], K = nk[1];
     if (!matrix(a[0], "grad_y", t, M, N, &g, &ldg) || !packed(a[1], a[2], "x_q", "x_exps", M, K, &x, &ldx, &xe) ||

@@ -41,7 +41,8 @@ def _load():
                torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream")
                else lambda d: torch.cuda.current_stream(d).cuda_stream,
                tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
-        m.bind_block(torch.uint8, tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in block_abi.ENTRY_POINTS))
+        if hasattr(m, "bind_block") and all(hasattr(lib, n) for n in block_abi.ENTRY_POINTS):   # a build without the blocks has neither
+            m.bind_block(torch.uint8, tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in block_abi.ENTRY_POINTS))
         _marshal = m
     return _marshal
 
