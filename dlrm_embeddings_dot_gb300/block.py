@@ -43,8 +43,8 @@ def dlrm_block_norm_fwd(y, gate, residual, w_post, b_post, scale, w_pre, b_pre, 
     """r = residual + scale * gate(g) * (norm(y) * w_post + b_post); h = norm(r) * w_pre + b_pre.  Without
     y (None) r is the residual, without h no norm of r is taken; gate is [M][N] or [M][1].  stats [M][4]
     keeps the rows' statistics for the backward.  See ``include/dlrm_block.h``."""
-    rc = _entry("block_norm_fwd")(y, gate, residual, w_post, b_post, scale, w_pre, b_pre, r, h, stats,
-                                                            norm, gate_act, eps, _handle(stream))
+    rc = _entry("block_norm_fwd")(y, gate, residual, w_post, b_post, scale, w_pre, b_pre, r, h, stats, norm,
+                                  gate_act, eps, _handle(stream))
     if rc:
         _fail("dlrm_block_norm_fwd", rc)
 
@@ -139,14 +139,15 @@ def dlrm_unpack8(q, exps, y, stream=None):
 
 
 def dlrm_linear_bwd8_workspace_size(grad_y, x_q, w, act=DLRM_ACT_NONE, p=0.0) -> int:
-    (M, K), N = x_q.shape, w.shape[0]
+    """Bytes for all three gradients; x_q may be None, as for a call without grad_w."""
+    M, (N, K) = grad_y.shape[0], w.shape
     return _size("dlrm_linear_bwd8_workspace_size", *_at(grad_y), *_at(w), _code(w.dtype), M, N, K, act, p)
 
 
 def dlrm_linear_bwd8(grad_y, x_q, x_exps, w, pre_q, pre_exps, grad_x, grad_w, grad_bias, act=DLRM_ACT_NONE, p=0.0, rng=None,
                      workspace=None, status=None, stream=None):
     """``dlrm_linear_bwd`` with the layer's input and pre-activation in 8 bits (``dlrm_pack8``)."""
-    rc = _entry("linear_bwd8")(grad_y, x_q, x_exps, w, pre_q, pre_exps, grad_x, grad_w, grad_bias,
-                                                         act, p, rng, workspace, status, _handle(stream))
+    rc = _entry("linear_bwd8")(grad_y, x_q, x_exps, w, pre_q, pre_exps, grad_x, grad_w, grad_bias, act, p, rng,
+                               workspace, status, _handle(stream))
     if rc:
         _fail("dlrm_linear_bwd8", rc)
