@@ -429,9 +429,10 @@ __device__ __forceinline__ void gate_both(float& g, int act, float& slope)
 {
     slope = 1.f;
     if (act == DLRM_GATE_NONE) return;
-    const float s = sigmoid<T>(g), m = act == DLRM_GATE_SIGMOID ? 1.f : g;
+    float rest;
+    const float s = sigmoid<T>(g, rest), m = act == DLRM_GATE_SIGMOID ? 1.f : g;
     g = s * m;
-    slope = s * fmaf(m, 1.f - s, act == DLRM_GATE_SIGMOID ? 0.f : 1.f);
+    slope = s * fmaf(m, rest, act == DLRM_GATE_SIGMOID ? 0.f : 1.f);
 }
 
 // ------------------------------------------------------------------- forward

@@ -202,13 +202,22 @@ __device__ __forceinline__ float rcp_fast(float x)
     return r;
 }
 
-// 1 / (1 + e^-z)
+// 1 / (1 + e^-z), and 1 less that: near 1 the difference has none of its digits left, so above 0 it is a product
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z, float& rest)
+{
+    const float e = exp2_fast(z * -1.44269504f), d = 1.f + e, r = rcp_fast(d);
+    float s = r;
+    if constexpr (std::is_same_v<T, float>) s = d < 0x1p126f ? fmaf(fmaf(-d, r, 1.f), r, r) : r;
+    rest = z > 0.f ? e * s : 1.f - s;
+    return s;
+}
+
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z)
 {
-    const float d = 1.f + exp2_fast(z * -1.44269504f), r = rcp_fast(d);
-    if constexpr (std::is_same_v<T, float>) return d < 0x1p126f ? fmaf(fmaf(-d, r, 1.f), r, r) : r;
-    else return r;
+    float rest;
+    return sigmoid<T>(z, rest);
 }
 
 // exp(-z^2 / 2)
