@@ -124,7 +124,7 @@ dlrm_status launch_pack(const PackJob& a, const PackJob& b, cudaStream_t st, Ove
 struct Unpack8Job {
     Packed8 src;
     int rows, cols, vec;
-    void* dst;          // [rows][padded(cols)], T; for fp32 bf16, which holds every value of 8 bits
+    void* dst;          // [rows][padded(cols)], T; for fp32 bf16, which holds every value of 8 bits from exponent 3 on
     int blocks;
 };
 

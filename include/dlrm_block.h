@@ -161,7 +161,7 @@ size_t dlrm_expert_sort_workspace_size(int T, int k, int E);
  * is token t's j-th (dlrm_expert_sort).  Slots below 0 have no row and take no part;
  * slots of R or more neither, and set DLRM_STATUS_OOB_INDEX in *d_status (may be NULL).
  * Rows of outputs [R][H] that no slot names stay as they were.  Slots of one output
- * [R][H] are distinct (of equal ones any one's row is written).  1 <= k <= DLRM_ROUTE_MAX_TOP_K,
+ * [R][H] are distinct (of equal ones each column is any one's).  1 <= k <= DLRM_ROUTE_MAX_TOP_K,
  * 0 <= R; sizes up to 2^31 - 2^20 - 1.
  *
  *   dlrm_dispatch_fwd   xs[slots[t][j]] = x[t]
@@ -214,7 +214,9 @@ dlrm_status dlrm_unpack8(const uint8_t* d_q, int64_t ldq, const uint8_t* d_exps,
  *     the output (NULL for DLRM_ACT_NONE).  RELU passes no gradient where the value
  *     kept in 8 bits is 0.
  * Everything else is as in dlrm_linear_bwd: the same gradients for the values that
- * the 8 bits stand for.
+ * the 8 bits stand for, as dlrm_unpack8 reads them.  fp32 layers of more than 16 outputs
+ * multiply the input's values as bf16 numbers, which are multiples of 2^-133: values of
+ * blocks with e of 0 to 2 are rounded to those.
  */
 dlrm_status dlrm_linear_bwd8(const void* d_grad_y, int64_t ldg, const uint8_t* d_x_q, int64_t ldx,
                              const uint8_t* d_x_exps, const void* d_w, int64_t ldw, const uint8_t* d_pre_q, int64_t ldp,
