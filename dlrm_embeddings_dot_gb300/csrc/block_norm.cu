@@ -79,13 +79,13 @@ dlrm_status check_norm(const char* fn, dlrm_dtype dtype, int M, int N, int norm,
     return DLRM_OK;
 }
 
-// Checks fp32 vectors of N elements, each of which may be NULL; *vec: whether all start on 16-byte boundaries.
+// Checks fp32 vectors of N elements, each of which may be NULL; *vec (may be NULL): whether all start on 16-byte boundaries.
 dlrm_status check_vectors(const char* fn, std::initializer_list<const void*> v, bool* vec)
 {
     for (const void* p : v) {
         if (reinterpret_cast<uintptr_t>(p) & 3u)
             return fail(DLRM_ERR_INVALID_ARG, "%s: a vector is not aligned to its element size", fn);
-        *vec = *vec && aligned16(p);
+        if (vec) *vec = *vec && aligned16(p);
     }
     return DLRM_OK;
 }
@@ -168,10 +168,10 @@ extern "C" dlrm_status dlrm_block_norm_bwd(
     dlrm_status s = check_norm(fn, dtype, M, N, norm, gate_act);
     if (s != DLRM_OK) return s;
     const int es = dense_dtype_size(dtype);
-    bool vec = N % 8 == 0, grads_vec = true;
+    bool vec = N % 8 == 0;
     float* const grads[5] = {d_grad_w_post, d_grad_b_post, d_grad_scale, d_grad_w_pre, d_grad_b_pre};
     if ((s = check_vectors(fn, {d_w_post, d_b_post, d_scale, d_w_pre}, &vec)) != DLRM_OK) return s;
-    if ((s = check_vectors(fn, {grads[0], grads[1], grads[2], grads[3], grads[4]}, &grads_vec)) != DLRM_OK) return s;
+    if ((s = check_vectors(fn, {grads[0], grads[1], grads[2], grads[3], grads[4]}, nullptr)) != DLRM_OK) return s;
     const cudaStream_t st = as_stream(stream);
     if (M == 0) {
         for (float* g : grads)   // no rows: the sums over them are zero

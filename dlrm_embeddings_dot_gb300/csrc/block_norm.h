@@ -34,8 +34,8 @@ struct NormBwd {
     int64_t Np;
 };
 
-// Rows of up to 128 columns are a few lanes' each, longer ones take warps, a power of two.  Measured, us, few lanes / a
-// warp a row, 65536 rows, bf16: forward of 16 columns 10 / 26, 64 14 / 26, 128 24 / 27, 99 (off the grid) 31 / 41;
+// Rows of up to 128 columns are a few lanes' each, a power of two; longer ones take warps (norm_warps).  Measured, us, few
+// lanes / a warp a row, 65536 rows, bf16: forward of 16 columns 10 / 26, 64 14 / 26, 128 24 / 27, 99 (off the grid) 31 / 41;
 // gradient 17 / 41, 24 / 41, 37 / 42, 52 / 74.
 inline int norm_lanes(int N) { return N <= 32 ? 4 : N <= 64 ? 8 : N <= 128 ? 16 : 32; }
 
@@ -48,7 +48,8 @@ inline int norm_warps(int N)
 }
 
 // Blocks of an SM and rows of a block where W warps take a row: blocks of eight warps, or of one group where W is more,
-// or one block of as many groups as fit where eight are no whole number of groups.
+// or one block of as many groups as fit where eight are no whole number of groups.  From 16 warps on an SM has one
+// row at a time, in the gradient of both norms from 10 on (bwd_warps).
 constexpr bool norm_eights(int W) { return W <= 8 && 8 % W == 0; }
 constexpr int norm_per_sm(int W, int warps) { return norm_eights(W) ? warps / 8 : W > 8 && warps >= 2 * W ? warps / W : 1; }
 constexpr int norm_groups(int W, int warps) { return W > 8 ? 1 : norm_eights(W) ? 8 / W : warps / W; }

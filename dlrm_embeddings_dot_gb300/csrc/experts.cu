@@ -842,7 +842,10 @@ extern "C" dlrm_status dlrm_combine_bwd(const void* d_grad_y, int64_t ldgy, cons
     const bool vec = H % 8 == 0 && rows_aligned16(d_grad_y, ldgy, T, es) &&
                      (!d_grad_probs || rows_aligned16(d_ys, ldys, R, es)) &&
                      (!d_grad_ys || rows_aligned16(d_grad_ys, ldgys, R, es));
-    // a block a token where those would leave SMs idle (16 tokens of 4096 columns, 4 each, fp16)
+    // a block a token where those would leave SMs idle.  In a graph, us, a warp / a block a token, fp16 of 2 and 8:
+    // 16 tokens x 768 2.7 / 2.2 and 6.3 / 2.9, x 4096 6.5 / 2.3 and 21 / 4.0; 600 x 768 2.8 / 3.7 and 6.6 / 5.7, x 4096
+    // 6.7 / 4.2 and 24 / 10; 1200 x 768 2.8 / 6.3 and 6.5 / 9.9, x 4096 6.9 / 7.3 and 37 / 28; fp32 16 x 768 of 8
+    // 8.0 / 3.7, 1200 8.9 / 14
     const bool wide = T < num_sms() * 4 && H > 512;
     const int lay = row_layout(vec, H), lanes = unit_lanes(H, lay);
     const CombineBwd a = {d_grad_y, d_ys, ldgy, ldys, d_slots, d_probs, T, k, H, R, lanes, d_grad_ys, ldgys, d_grad_probs,
