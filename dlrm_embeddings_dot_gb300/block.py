@@ -20,21 +20,9 @@ from .dense import _size as _dense_size
 from .dense_abi import DLRM_ACT_NONE
 
 
-def _missing(name):
-    return RuntimeError(f"the library was built before {name}: build it again")
-
-
-def _entry(name):
-    """The checking extension's function for an entry point; an extension or a library without it is told of."""
-    f = getattr(_dense._marshal or _dense._load(), name, None)
-    if f is None:
-        raise _missing("dlrm_" + name)
-    return f
-
-
 def _size(name, *args) -> int:
     if not hasattr(_dl.load(), name):
-        raise _missing(name)
+        raise RuntimeError(f"the library was built before {name}: build it again")
     return _dense_size(name, *args)
 
 
@@ -43,8 +31,8 @@ def dlrm_block_norm_fwd(y, gate, residual, w_post, b_post, scale, w_pre, b_pre, 
     """r = residual + scale * gate(g) * (norm(y) * w_post + b_post); h = norm(r) * w_pre + b_pre.  Without
     y (None) r is the residual, without h no norm of r is taken; gate is [M][N] or [M][1].  stats [M][4]
     keeps the rows' statistics for the backward.  See ``include/dlrm_block.h``."""
-    rc = _entry("block_norm_fwd")(y, gate, residual, w_post, b_post, scale, w_pre, b_pre, r, h, stats, norm,
-                                  gate_act, eps, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).block_norm_fwd(y, gate, residual, w_post, b_post, scale, w_pre, b_pre, r, h, stats,
+                                                            norm, gate_act, eps, _handle(stream))
     if rc:
         _fail("dlrm_block_norm_fwd", rc)
 
@@ -60,7 +48,7 @@ def dlrm_block_norm_bwd(grad_r, grad_h, y, gate, r, stats, w_post, b_post, scale
                         gate_act=DLRM_GATE_NONE, workspace=None, stream=None):
     """Gradients of ``dlrm_block_norm_fwd``; each output may be None.  r is the forward's r (its residual
     where it had no y), None without grad_h.  See ``include/dlrm_block.h``."""
-    rc = _entry("block_norm_bwd")(
+    rc = (_dense._marshal or _dense._load()).block_norm_bwd(
         grad_r, grad_h, y, gate, r, stats, w_post, b_post, scale, w_pre, grad_y, grad_gate, grad_residual, grad_w_post,
         grad_b_post, grad_scale, grad_w_pre, grad_b_pre, norm, gate_act, workspace, _handle(stream))
     if rc:
@@ -70,14 +58,14 @@ def dlrm_block_norm_bwd(grad_r, grad_h, y, gate, r, stats, w_post, b_post, scale
 def dlrm_route_fwd(logits, ids, probs, stream=None):
     """The k experts of the largest logits of each token (k from ids [T][k]) and their shares; experts
     with a logit of -infinity are closed, ids of choices that stay empty -1."""
-    rc = _entry("route_fwd")(logits, ids, probs, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).route_fwd(logits, ids, probs, _handle(stream))
     if rc:
         _fail("dlrm_route_fwd", rc)
 
 
 def dlrm_route_bwd(grad_probs, ids, probs, grad_logits, stream=None):
     """Gradient of the logits of ``dlrm_route_fwd``, 0 for experts that were not chosen."""
-    rc = _entry("route_bwd")(grad_probs, ids, probs, grad_logits, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).route_bwd(grad_probs, ids, probs, grad_logits, _handle(stream))
     if rc:
         _fail("dlrm_route_bwd", rc)
 
@@ -90,28 +78,28 @@ def dlrm_expert_sort_workspace_size(ids, E) -> int:
 def dlrm_expert_sort(ids, E, offsets, slots, order=None, workspace=None, status=None, stream=None):
     """Places of the tokens' choices sorted by expert: slots [T][k], offsets [E + 1] where each expert's
     places begin, order [T k] the choice at each place (may be None)."""
-    rc = _entry("expert_sort")(ids, E, offsets, slots, order, workspace, status, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).expert_sort(ids, E, offsets, slots, order, workspace, status, _handle(stream))
     if rc:
         _fail("dlrm_expert_sort", rc)
 
 
 def dlrm_dispatch_fwd(x, slots, xs, status=None, stream=None):
     """xs[slots[t][j]] = x[t]; rows of xs that no slot names stay as they were."""
-    rc = _entry("dispatch_fwd")(x, slots, xs, status, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).dispatch_fwd(x, slots, xs, status, _handle(stream))
     if rc:
         _fail("dlrm_dispatch_fwd", rc)
 
 
 def dlrm_dispatch_bwd(grad_xs, slots, grad_x, status=None, stream=None):
     """grad_x[t] = sum over j of grad_xs[slots[t][j]]."""
-    rc = _entry("dispatch_bwd")(grad_xs, slots, grad_x, status, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).dispatch_bwd(grad_xs, slots, grad_x, status, _handle(stream))
     if rc:
         _fail("dlrm_dispatch_bwd", rc)
 
 
 def dlrm_combine_fwd(ys, slots, probs, residual, y, status=None, stream=None):
     """y[t] = residual[t] + sum over j of probs[t][j] * ys[slots[t][j]]; residual may be None."""
-    rc = _entry("combine_fwd")(ys, slots, probs, residual, y, status, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).combine_fwd(ys, slots, probs, residual, y, status, _handle(stream))
     if rc:
         _fail("dlrm_combine_fwd", rc)
 
@@ -119,21 +107,21 @@ def dlrm_combine_fwd(ys, slots, probs, residual, y, status=None, stream=None):
 def dlrm_combine_bwd(grad_y, ys, slots, probs, grad_ys, grad_probs, status=None, stream=None):
     """Gradients of ``dlrm_combine_fwd``; grad_ys or grad_probs may be None.  The residual's gradient is
     grad_y itself."""
-    rc = _entry("combine_bwd")(grad_y, ys, slots, probs, grad_ys, grad_probs, status, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).combine_bwd(grad_y, ys, slots, probs, grad_ys, grad_probs, status, _handle(stream))
     if rc:
         _fail("dlrm_combine_bwd", rc)
 
 
 def dlrm_pack8(x, q, exps, stream=None):
     """x in 8 bits: q [M][N] bytes, exps [M][ceil(N / 32)] the blocks' powers of two."""
-    rc = _entry("pack8")(x, q, exps, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).pack8(x, q, exps, _handle(stream))
     if rc:
         _fail("dlrm_pack8", rc)
 
 
 def dlrm_unpack8(q, exps, y, stream=None):
     """The values that q and exps stand for."""
-    rc = _entry("unpack8")(q, exps, y, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).unpack8(q, exps, y, _handle(stream))
     if rc:
         _fail("dlrm_unpack8", rc)
 
@@ -147,7 +135,7 @@ def dlrm_linear_bwd8_workspace_size(grad_y, x_q, w, act=DLRM_ACT_NONE, p=0.0) ->
 def dlrm_linear_bwd8(grad_y, x_q, x_exps, w, pre_q, pre_exps, grad_x, grad_w, grad_bias, act=DLRM_ACT_NONE, p=0.0, rng=None,
                      workspace=None, status=None, stream=None):
     """``dlrm_linear_bwd`` with the layer's input and pre-activation in 8 bits (``dlrm_pack8``)."""
-    rc = _entry("linear_bwd8")(grad_y, x_q, x_exps, w, pre_q, pre_exps, grad_x, grad_w, grad_bias, act, p, rng,
-                               workspace, status, _handle(stream))
+    rc = (_dense._marshal or _dense._load()).linear_bwd8(grad_y, x_q, x_exps, w, pre_q, pre_exps, grad_x, grad_w, grad_bias,
+                                                         act, p, rng, workspace, status, _handle(stream))
     if rc:
         _fail("dlrm_linear_bwd8", rc)

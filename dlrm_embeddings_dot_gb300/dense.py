@@ -25,6 +25,21 @@ _TYPES = (torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.int64
 _marshal = None
 
 
+def _bind_block(m, lib):
+    """The residual blocks' entry points (block.py), where the library and the extension have them: a build of
+    before them has the dense network's alone."""
+    if hasattr(m, "bind_block"):
+        if all(hasattr(lib, n) for n in block_abi.ENTRY_POINTS):
+            m.bind_block(torch.uint8, tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in block_abi.ENTRY_POINTS))
+        return      # its functions say so themselves
+
+    def missing(*_):
+        raise RuntimeError("the _marshal extension was built before the residual blocks' entry points: build it again")
+
+    for n in block_abi.ENTRY_POINTS:
+        setattr(m, n.removeprefix("dlrm_"), missing)
+
+
 def _load():
     """The checking extension (csrc/marshal.c), bound to the library's entry points."""
     global _marshal
@@ -41,8 +56,7 @@ def _load():
                torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream")
                else lambda d: torch.cuda.current_stream(d).cuda_stream,
                tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
-        if hasattr(m, "bind_block") and all(hasattr(lib, n) for n in block_abi.ENTRY_POINTS):   # a build without the blocks has neither
-            m.bind_block(torch.uint8, tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in block_abi.ENTRY_POINTS))
+        _bind_block(m, lib)
         _marshal = m
     return _marshal
 
