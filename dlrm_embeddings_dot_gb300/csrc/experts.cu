@@ -200,8 +200,8 @@ dlrm_status with_lanes(int E, Fn&& fn)
 // before they read a choice.  The steps are chains of latencies: a warp's choices are
 // loaded kBatch rounds at a time, and the counts' sums are shared out over all threads
 // (sort_layout.h).  (us in a graph; the warps counted a second time while the counts were written / counts
-// read back: 9000 choices of 16 4.7 / 5.6, 65536 x 4 of 64 8.9 / 9.4, 65536 x 8 of 256 19.8 / 19.0, 300000 x 8 of 33
-// 41.9 / 31.9.  The former read choices ahead of its own wait.)
+// read back: 9000 choices of 16 4.9 / 5.6, 65536 x 4 of 64 8.9 / 9.3, 65536 x 8 of 256 19.8 / 19.4, 300000 x 8 of 33
+// 42.0 / 31.8.  The former read choices ahead of its own wait.)
 constexpr int kBatch = 8;
 constexpr int kBins = DLRM_ROUTE_MAX_EXPERTS + 1;
 static_assert(kBins <= kSortThreads, "a thread for each bin");
@@ -271,27 +271,30 @@ expert_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
     __shared__ int warps[kSortWarps][kBins];
     const Part part(ids, n, chunk);
     count_parts(part, E, warps);
-    int32_t* own = parts + ((int)blockIdx.x * kSortWarps + (int)threadIdx.x / kWarp) * (E + 1);
-    for (int e = threadIdx.x % kWarp; e <= E; e += kWarp) own[e] = warps[threadIdx.x / kWarp][e];
     for (int e = threadIdx.x; e <= E; e += kSortThreads) {
         int s = 0;
 #pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) s += warps[w][e];
+        for (int w = 0; w < kSortWarps; ++w) {
+            s += warps[w][e];
+            parts[((int)blockIdx.x * kSortWarps + w) * (E + 1) + e] = warps[w][e];
+        }
         counts[blockIdx.x * (E + 1) + e] = s;
     }
 }
 
+// MANY: more than one block, whose counts expert_count_kernel has written.
+template <bool MANY>
 __global__ void __launch_bounds__(kSortThreads)
 expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, int E, const int32_t* __restrict__ counts,
                     const int32_t* __restrict__ parts, int32_t* __restrict__ offsets, int32_t* __restrict__ slots,
                     int32_t* __restrict__ order, uint32_t* __restrict__ status)
 {
     __shared__ int warps[kSortWarps][kBins];
-    __shared__ int total[kBins], before[kBins], scan[kSortWarps];
+    __shared__ int total[MANY ? kBins : 1], before[MANY ? kBins : 1], scan[kSortWarps];
     const int bins = E + 1, tid = threadIdx.x;
     pdl_wait();
     const Part part(ids, n, chunk);
-    if (gridDim.x == 1) {
+    if constexpr (!MANY) {
         count_parts(part, E, warps);
     } else {
         const int w = tid / kWarp;
@@ -321,7 +324,7 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
         if (e < bins) {
 #pragma unroll
             for (int w = 0; w < kSortWarps; ++w) mine[w] = warps[w][e];
-            if (gridDim.x > 1) {
+            if constexpr (MANY) {
                 v = total[e];
             } else {
 #pragma unroll
@@ -340,7 +343,7 @@ expert_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t chunk, i
             for (int w = 0; w < e / kWarp; ++w) s += scan[w];
             int at = s - v;
             if (blockIdx.x == 0) offsets[e] = at;   // offsets[E]: how many have a place
-            if (gridDim.x > 1) at += before[e];
+            if constexpr (MANY) at += before[e];
 #pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
                 warps[w][e] = at;
@@ -754,7 +757,8 @@ extern "C" dlrm_status dlrm_expert_sort(const int32_t* d_ids, int T, int k, int 
                              "expert_count_kernel");
         if (s != DLRM_OK) return s;
     }
-    return check_launch_pdl(launch_pdl(expert_place_kernel, dim3(z.blocks), dim3(kSortThreads), 0, st, d_ids, n, z.chunk, E,
+    auto place = z.blocks > 1 ? expert_place_kernel<true> : expert_place_kernel<false>;
+    return check_launch_pdl(launch_pdl(place, dim3(z.blocks), dim3(kSortThreads), 0, st, d_ids, n, z.chunk, E,
                                        (const int32_t*)counts, (const int32_t*)parts, d_offsets, d_slots, d_order, d_status),
                             "expert_place_kernel");
 }
