@@ -18,7 +18,7 @@
 //              and block_norm_sum_kernel adds them in order
 //
 // Measured (us, share of the copy rate; 65536 x 1024 unless said): forward bf16 with a gate 106,
-// 0.95; gradient fp16 with a gate 169, 0.95; 16384 x 1024 fp32 49 and 82, 0.98.  Pairs of fp32 values go
+// 0.95; gradient fp16 with a gate 170, 0.94; 16384 x 1024 fp32 49 and 82, 0.98.  Pairs of fp32 values go
 // through one instruction (fma.f32x2 and the like), and what depends on the row alone through the
 // uniform datapath: the warp's number has to be read from one lane for that (gradient 236 us without).
 //

@@ -61,7 +61,8 @@ typedef enum {
  *     means of RMS and for norms that are not taken
  *   eps >= 0 and finite
  * h and r's statistics are taken from r before its rounding to dtype.  A row of
- * zeros with eps = 0 is a row of NaN, as the formula says.
+ * zeros with eps = 0 is a row of NaN, as the formula says.  Squares are summed in
+ * fp32: where their sum passes its range (values of some 2^63) 1 / sqrt is 0.
  * Requires 1 <= N <= DLRM_BLOCK_MAX_WIDTH (more: DLRM_ERR_UNSUPPORTED).
  */
 dlrm_status dlrm_block_norm_fwd(const void* d_y, int64_t ldy, const void* d_gate, int64_t ldg, int gate_cols,
@@ -113,7 +114,7 @@ size_t dlrm_block_norm_bwd_workspace_size(int M, int N);
  *   probs[t][j] = exp(logits[t][ids[t][j]]) / sum over j of the same
  * A logit of -infinity closes its expert to the token: it is never chosen.  Where
  * fewer than k are open the last ids are -1 with probs 0 (all of them, where none
- * is).
+ * is).  Where the largest is a NaN or +infinity the probs of the chosen are NaN.
  *   d_logits [T][E];  d_ids int32 [T][k], d_probs fp32 [T][k] (outputs)
  * Requires 1 <= E <= DLRM_ROUTE_MAX_EXPERTS, 1 <= k <= min(E, DLRM_ROUTE_MAX_TOP_K)
  * (larger E or k: DLRM_ERR_UNSUPPORTED).
